@@ -1,8 +1,9 @@
 """Euler characteristic curves of dense 2D/3D grids on AMD Instinct MI355X.
 
 The compute path is libecc_mi355.so (hand-written HIP for gfx950, C ABI in
-include/ecc.h); ``euler_characteristic_curves_amd.ecc`` is its thin PyTorch
-binding.  The binding is imported lazily so that ``workloads`` (seeded
+include/ecc.h and include/ecc_train.h); ``euler_characteristic_curves_amd.ecc``
+(the curves) and ``euler_characteristic_curves_amd.train`` (operators that train
+a network through them) are its thin PyTorch binding.  The binding is imported lazily so that ``workloads`` (seeded
 synthetic inputs) can be used without the built library; any attempt to use
 an ECC entry point without the library raises ImportError.
 """
@@ -18,11 +19,16 @@ _API = (
     "ecc_hard_directional", "soft_ecc_directional",
 )
 
-__all__ = list(_API)
+_TRAIN_API = ("group_norm_act", "group_norm_readout", "GroupNormAct", "GroupNormReadout")
+
+__all__ = list(_API + _TRAIN_API)
 
 
 def __getattr__(name):
     if name in _API:
         from . import ecc as _ecc
         return getattr(_ecc, name)
+    if name in _TRAIN_API:
+        from . import train as _train
+        return getattr(_train, name)
     raise AttributeError(name)

@@ -36,6 +36,28 @@ EXPORTS = (
 )
 
 
+# mirrored from include/ecc_train.h
+ECC_E_GROUPS = 9
+ECC_E_ACT = 10
+ECC_E_VALUE = 11
+ECC_T_F32 = 0
+ECC_T_F16 = 1
+ECC_T_BF16 = 2
+ECC_ACT_NONE = 0
+ECC_ACT_RELU = 1
+ECC_ACT_SILU = 2
+ECC_ACT_GELU = 3
+ECC_MAX_CHANNELS = 8192
+ECC_MAX_READOUT_CHANNELS = 1024
+ECC_MAX_NORM_BATCH = 32768
+ECC_MAX_MATRIX = 32768
+ECC_MAX_NS_STEPS = 64
+
+TRAIN_EXPORTS = (
+    "ecc_norm_fwd", "ecc_norm_bwd", "ecc_norm_readout_fwd", "ecc_norm_readout_bwd", "ecc_norm_workspace_bytes",
+)
+
+
 class EccError(RuntimeError):
     """A libecc_mi355 entry point returned a non-zero status."""
 
@@ -86,6 +108,16 @@ def _load():
     lib.ecc_workspace_bytes.restype = SZ
     lib.ecc_workspace_bytes_batched.argtypes = [I, I64, I32]
     lib.ecc_workspace_bytes_batched.restype = SZ
+    lib.ecc_norm_fwd.argtypes = [P, I, I64, I64, I64, I64, P, P, I, I, F, P, P, P, SZ, P]
+    lib.ecc_norm_fwd.restype = I
+    lib.ecc_norm_bwd.argtypes = [P, I, I64, I64, I64, I64, P, P, I, I, P, P, P, P, P, P, SZ, P]
+    lib.ecc_norm_bwd.restype = I
+    lib.ecc_norm_readout_fwd.argtypes = [P, I, I64, I64, I64, I64, P, P, P, P, I, I, F, P, P, P, SZ, P]
+    lib.ecc_norm_readout_fwd.restype = I
+    lib.ecc_norm_readout_bwd.argtypes = [P, I, I64, I64, I64, I64, P, P, P, I, I, P, P, P, P, P, P, P, P, SZ, P]
+    lib.ecc_norm_readout_bwd.restype = I
+    lib.ecc_norm_workspace_bytes.argtypes = [I64, I64, I64, I64]
+    lib.ecc_norm_workspace_bytes.restype = SZ
     lib.ecc_status_string.argtypes = [I]
     lib.ecc_status_string.restype = ctypes.c_char_p
     lib.ecc_last_error.argtypes = []

@@ -20,7 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libecc_mi355.so")
 
-SOURCES = ["ecc_api.cpp", "ecc_hard.hip", "ecc_soft.hip", "ecc_soft_grad.hip", "ecc_height.hip", "ecc_static.hip"]
+SOURCES = ["ecc_api.cpp", "ecc_hard.hip", "ecc_soft.hip", "ecc_soft_grad.hip", "ecc_height.hip", "ecc_static.hip",
+           "ecc_train_api.cpp", "ecc_norm_f32.hip", "ecc_norm_f16.hip", "ecc_norm_bf16.hip"]
 RATE_SOURCE = "ecc_sigmoid_rate.hip"
 RATE_LIB = os.path.join(PKG, "libecc_sigmoid_rate.so")
 ARCH = os.environ.get("ECC_OFFLOAD_ARCH", "gfx950")
@@ -54,7 +55,7 @@ def _compile(src):
 def build(verbose=False):
     """Compile every source and link the shared library; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+    with cf.ThreadPoolExecutor(max_workers=8) as ex:
         results = list(ex.map(_compile, SOURCES + [RATE_SOURCE]))
     rate_obj = results.pop()[0]
     objs = [o for o, _ in results]

@@ -1,0 +1,116 @@
+// Element types, activations and their slopes for the training operators.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ecc {
+
+typedef _Float16 f16;
+typedef __bf16 bf16;
+
+template <class T>
+__device__ __forceinline__ float to_f32(T v) {
+  return (float)v;
+}
+
+// V elements from memory aligned to one element only: the target's global
+// loads and stores take any alignment, so one 16-byte access serves rows that
+// are not a multiple of 16 bytes too.
+template <class T, int V>
+struct Vec {
+  T v[V];
+};
+template <class T, int V>
+__device__ __forceinline__ void load_vec(const T* p, Vec<T, V>& r) {
+  __builtin_memcpy(&r, p, sizeof(T) * V);
+}
+template <class T, int V>
+__device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& r) {
+  __builtin_memcpy(p, &r, sizeof(T) * V);
+}
+
+// One parameter as float32; null stands for `dflt`.
+__device__ __forceinline__ float load_param(const void* p, int pdtype, int64_t i, float dflt) {
+  if (!p) return dflt;
+  if (pdtype == 0) return reinterpret_cast<const float*>(p)[i];
+  if (pdtype == 1) return (float)reinterpret_cast<const f16*>(p)[i];
+  return (float)reinterpret_cast<const bf16*>(p)[i];
+}
+__device__ __forceinline__ void store_param(void* p, int pdtype, int64_t i, float v) {
+  if (pdtype == 0)
+    reinterpret_cast<float*>(p)[i] = v;
+  else if (pdtype == 1)
+    reinterpret_cast<f16*>(p)[i] = (f16)v;
+  else
+    reinterpret_cast<bf16*>(p)[i] = (bf16)v;
+}
+
+// exp(x) through the hardware's 2^y, relative error below 2^-22: the part of
+// x log2(e) that one float32 product rounds away is put back to first order.
+// x is clamped to where the result is a normal float (a NaN becomes finite
+// here; every caller multiplies by its own argument, which carries it).
+__device__ __forceinline__ float exp_f32(float x) {
+  x = __builtin_amdgcn_fmed3f(x, -87.0f, 88.0f);
+  const float hi = x * 1.44269502f;
+  const float lo = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -hi));
+  const float r = __builtin_amdgcn_exp2f(hi);
+  return fmaf(r, lo * 0.693147182f, r);
+}
+
+constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3;
+
+// Normal distribution function of u and e = exp(-u^2/2).  The upper tail at
+// z = |u| is e * t * p(t) with t = 1 / (1 + 0.3 z): t p(t) is erfcx(z /
+// sqrt 2) / 2, a polynomial in t fitted to it over z in [0, 14] (relative
+// error 1.5e-7, 4.2e-7 with float32 arithmetic), so both tails keep their
+// relative accuracy, where 1 + erf(u / sqrt 2) cancels.
+__device__ __forceinline__ float normal_cdf(float u, float& e) {
+  e = exp_f32(-0.5f * u * u);
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, fabsf(u), 1.0f));
+  float p = 0.0356748769f;
+  p = fmaf(p, t, -0.1572034993f);
+  p = fmaf(p, t, 0.2063541957f);
+  p = fmaf(p, t, -0.0536842455f);
+  p = fmaf(p, t, 0.1285619242f);
+  p = fmaf(p, t, 0.0999134088f);
+  p = fmaf(p, t, 0.1207539682f);
+  p = fmaf(p, t, 0.1196292981f);
+  const float q = e * (t * p);
+  return u >= 0.0f ? 1.0f - q : q;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float u) {
+  if constexpr (ACT == kActRelu) return u <= 0.0f ? 0.0f : u;
+  if constexpr (ACT == kActSilu) return u * __builtin_amdgcn_rcpf(1.0f + exp_f32(-u));
+  if constexpr (ACT == kActGelu) {
+    float e;
+    return u * normal_cdf(u, e);
+  }
+  return u;
+}
+
+// Slope; y receives the value.
+template <int ACT>
+__device__ __forceinline__ float act_slope(float u, float& y) {
+  if constexpr (ACT == kActRelu) {
+    y = u <= 0.0f ? 0.0f : u;
+    return u > 0.0f ? 1.0f : (u <= 0.0f ? 0.0f : u);
+  }
+  if constexpr (ACT == kActSilu) {
+    const float s = __builtin_amdgcn_rcpf(1.0f + exp_f32(-u));
+    y = u * s;
+    return fmaf(y, 1.0f - s, s);
+  }
+  if constexpr (ACT == kActGelu) {
+    float e;
+    const float c = normal_cdf(u, e);
+    y = u * c;
+    return fmaf(u * 0.398942280f, e, c);
+  }
+  y = u;
+  return 1.0f;
+}
+
+}  // namespace ecc

@@ -4,6 +4,7 @@
 // include/ecc.h for the contract of every entry point.
 
 #include "../../include/ecc.h"
+#include "../../include/ecc_train.h"
 
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -13,6 +14,7 @@
 #include <atomic>
 
 #include "ecc_internal.hpp"
+#include "ecc_train_internal.hpp"
 
 namespace {
 
@@ -130,6 +132,8 @@ int hip_status(hipError_t e) {
 }  // namespace
 
 namespace ecc {
+
+void set_error(const char* message) { snprintf(g_err, sizeof(g_err), "%s", message); }
 
 hipError_t device_info(DeviceInfo* info) {
   int dev = 0;
@@ -379,6 +383,9 @@ const char* ecc_status_string(int status) {
     case ECC_E_WORKSPACE: return "workspace missing or too small";
     case ECC_E_HIP: return "HIP runtime error";
     case ECC_E_NDIRS: return "number of directions out of range";
+    case ECC_E_GROUPS: return "groups must divide the channels";
+    case ECC_E_ACT: return "unknown activation";
+    case ECC_E_VALUE: return "scalar argument out of range";
     default: return "unknown status";
   }
 }

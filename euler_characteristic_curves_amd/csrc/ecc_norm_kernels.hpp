@@ -1,0 +1,630 @@
+// Group norm with an activation over channels-last features, its read-out to
+// a scalar grid, and the backward passes of both (contract: include/ecc_train.h).
+//
+// For sample b, group g of D = C/G channels and N = S D elements:
+//   mean = sum x / N,  var = sum (x - mean)^2 / N,  rstd = 1/sqrt(var + eps)
+//   u_c = (x_c - mean) a_c + bias_c,  a_c = rstd weight_c
+//   y_c = act(u_c);   field = offset + sum_c r_c y_c
+// and backwards, with q_c = dL/dy_c act'(u_c) (dL/dy_c = df r_c for the grid):
+//   A1_c = sum q_c,  A2_c = sum q_c (x_c - mean)          per sample
+//   dbias_c = sum_b A1,  dweight_c = sum_b rstd A2
+//   m1 = sum_{c in g} weight_c A1_c / N,  m2 = sum_{c in g} weight_c rstd A2_c / N
+//   dx_c = a_c q_c - rstd m1 - (x_c - mean) rstd^2 m2
+//
+// Every pass is a stream over the features and bound by HBM (or by the memory
+// side cache when the features fit it); the statistics force two passes each
+// way, so forward reads x twice and backward reads x and dy twice.  Mapping:
+// a row of C channels is taken by L lanes of one wave, K vectors of V = 16
+// bytes each, so a lane keeps its V K channels for the whole pass and holds
+// their scale, shift and sums in registers; a wave has floor(64 / L) rows in
+// flight per step.  A row that is not a multiple of V ends in a vector that
+// overlaps the one before it; the overlap is left out of every sum (and
+// stored twice with the same value).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "ecc_act.hpp"
+#include "ecc_train_internal.hpp"
+
+namespace ecc {
+namespace {
+
+constexpr int kNT = 256;
+constexpr int kNW = kNT / 64;
+
+// How a pass is laid out; filled by norm_geom on the host.
+struct NormGeom {
+  int64_t S, C;
+  int NB;      // workgroups per sample
+  int L;       // lanes per row
+  int nv;      // vectors per row
+  int chunks;  // column chunks of 64 vectors (rows of more than 4 x 64 vectors)
+};
+
+// A lane's columns.
+template <int V, int K>
+struct Cols {
+  int c[K];      // first channel of vector k
+  int dup[K];    // leading elements that belong to another vector (V: none is its own)
+  int64_t first, stride;
+  int l;
+  __device__ Cols(const NormGeom& g) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int sub = lane / g.L, rows = 64 / g.L;
+    l = lane - sub * g.L;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int v = (int)blockIdx.z * 64 + l + k * g.L;
+      const int at = v * V, last = (int)g.C - V;
+      if (v < g.nv) {
+        c[k] = at < last ? at : last;
+        dup[k] = at - c[k];
+      } else {
+        c[k] = last;
+        dup[k] = V;
+      }
+    }
+    const int64_t w = (int64_t)blockIdx.x * kNW + wave;
+    stride = (int64_t)g.NB * kNW * rows;
+    first = sub < rows ? w * rows + sub : g.S;
+  }
+};
+
+template <int K>
+constexpr int kUnroll = K == 1 ? 4 : (K == 2 ? 2 : 1);
+
+// Calls body(row...) for the rows of this lane: U at a time, then one by one.
+// body<N> gets an array of N row indexes.
+template <int U, class Body>
+__device__ __forceinline__ void for_rows(int64_t first, int64_t stride, int64_t S, Body body) {
+  int64_t r = first;
+  for (; r + (U - 1) * stride < S; r += U * stride) {
+    int64_t rows[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) rows[i] = r + i * stride;
+    body(rows, std::integral_constant<int, U>());
+  }
+  if constexpr (U > 1) {
+    for (; r < S; r += stride) {
+      int64_t rows[1] = {r};
+      body(rows, std::integral_constant<int, 1>());
+    }
+  }
+}
+
+// Elements of a vector whose sums are joined at a time: few, so that the
+// buffer does not limit how many workgroups a CU holds during the pass.
+template <int V>
+constexpr int kSumElems = V < 2 ? V : 2;
+
+// Sums over the workgroup's rows of NV values per channel, in a fixed order
+// and in float64, written to out[channel * NV + i].  lds: kSumElems<V> NV kNT
+// doubles.  P threads share one output and join by shuffles, P the largest
+// power of two with P L kSumElems NV <= kNT (and at most 64).
+template <int V, int K, int NV, class Value>
+__device__ __forceinline__ void column_sums(const NormGeom& g, const Cols<V, K>& col, double* lds, double* out,
+                                            Value value) {
+  constexpr int E = kSumElems<V>;
+  const int rows = 64 / g.L, L = g.L;
+  const int nout = L * E * NV;
+  int P = 1;
+  while (P < 64 && 2 * P * nout <= kNT) P *= 2;
+  const int p = threadIdx.x % P;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j0 = 0; j0 < V; j0 += E) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) lds[(j * NV + i) * kNT + threadIdx.x] = value(k, j0 + j, i);
+      __syncthreads();
+      // every thread of a wave takes the same number of turns: the shuffles see whole waves
+      for (int o0 = 0; o0 < nout; o0 += kNT / P) {
+        const int o = o0 + threadIdx.x / P;
+        const int l = o % L, ji = o / L;
+        double s = 0.0;
+        if (o < nout)
+          for (int e = p; e < kNW * rows; e += P) s += lds[ji * kNT + (e / rows) * 64 + (e % rows) * L + l];
+        for (int d = 1; d < P; d *= 2) s += __shfl_xor(s, d);
+        const int v = (int)blockIdx.z * 64 + l + k * L;
+        if (o < nout && p == 0 && v < g.nv) {
+          const int at = v * V, last = (int)g.C - V, c = at < last ? at : last;
+          const int j = j0 + ji / NV;
+          if (j >= at - c) out[(int64_t)(c + j) * NV + ji % NV] = s;
+        }
+      }
+    }
+}
+
+// Moments about zero per channel.  A thread sums x - k and (x - k)^2 in
+// float32, k the first value it meets in that channel, so neither an offset of
+// the channel nor a few far values cost it digits; float64 from there on.
+template <class T, int V, int K>
+__global__ __launch_bounds__(kNT) void norm_stats_kernel(NormGeom g, const T* x, double* part, int64_t row) {
+  __shared__ double lds[kSumElems<V> * 2 * kNT];
+  Cols<V, K> col(g);
+  const T* xs = x + (int64_t)blockIdx.y * g.S * g.C;
+  float piv[K][V], s1[K][V], s2[K][V];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    Vec<T, V> v = {};
+    if (col.first < g.S) load_vec(xs + col.first * g.C + col.c[k], v);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      piv[k][j] = (float)v.v[j];
+      s1[k][j] = s2[k][j] = 0.0f;
+    }
+  }
+  int64_t n = 0;
+  for_rows<kUnroll<K>>(col.first, col.stride, g.S, [&](const int64_t* rows, auto U) {
+    Vec<T, V> v[U.value][K];
+#pragma unroll
+    for (int i = 0; i < U.value; ++i)
+#pragma unroll
+      for (int k = 0; k < K; ++k) load_vec(xs + rows[i] * g.C + col.c[k], v[i][k]);
+#pragma unroll
+    for (int i = 0; i < U.value; ++i)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float d = (float)v[i][k].v[j] - piv[k][j];
+          s1[k][j] += d;
+          s2[k][j] = fmaf(d, d, s2[k][j]);
+        }
+    n += U.value;
+  });
+  column_sums<V, K, 2>(g, col, lds, part + ((int64_t)blockIdx.y * g.NB + blockIdx.x) * row, [&](int k, int j, int i) {
+    const double p = (double)piv[k][j], a = (double)s1[k][j], m = (double)n;
+    return i == 0 ? fma(m, p, a) : (double)s2[k][j] + p * (2.0 * a + m * p);
+  });
+}
+
+// What the passes after the statistics keep per channel.
+template <int V, int K>
+struct Affine {
+  float mean[K][V], a[K][V], b[K][V];
+  __device__ void load(const NormArgs& p, const Cols<V, K>& col, int D) {
+    const float* st = p.stats + (int64_t)blockIdx.y * p.G * 2;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = col.c[k] + j, gr = (unsigned)c / (unsigned)D;
+        mean[k][j] = st[2 * gr];
+        a[k][j] = st[2 * gr + 1] * load_param(p.weight, p.pdtype, c, 1.0f);
+        b[k][j] = load_param(p.bias, p.pdtype, c, 0.0f);
+      }
+  }
+  __device__ __forceinline__ float u(int k, int j, float x) const { return fmaf(x - mean[k][j], a[k][j], b[k][j]); }
+};
+
+template <class T, int V, int K, int ACT>
+__global__ __launch_bounds__(kNT) void norm_apply_kernel(NormGeom g, NormArgs p, int D) {
+  Cols<V, K> col(g);
+  Affine<V, K> af;
+  af.load(p, col, D);
+  const int64_t base = (int64_t)blockIdx.y * g.S * g.C;
+  const T* xs = reinterpret_cast<const T*>(p.x) + base;
+  T* ys = reinterpret_cast<T*>(p.y) + base;
+  for_rows<kUnroll<K>>(col.first, col.stride, g.S, [&](int64_t* rows, auto U) {
+    Vec<T, V> v[U.value][K];
+#pragma unroll
+    for (int i = 0; i < U.value; ++i) {
+      rows[i] = g.S - 1 - rows[i];  // what the statistics read last is read first
+#pragma unroll
+      for (int k = 0; k < K; ++k) load_vec(xs + rows[i] * g.C + col.c[k], v[i][k]);
+    }
+#pragma unroll
+    for (int i = 0; i < U.value; ++i)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        Vec<T, V> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) o.v[j] = (T)act_value<ACT>(af.u(k, j, (float)v[i][k].v[j]));
+        if (col.dup[k] < V) store_vec(ys + rows[i] * g.C + col.c[k], o);
+      }
+  });
+}
+
+// Sum over the L lanes of a row, valid in its lane 0.
+__device__ __forceinline__ float row_sum(float s, int l, int L) {
+  for (int d = 1; d < L; d *= 2) {
+    const float o = __shfl_down(s, d);
+    s += l + d < L ? o : 0.0f;
+  }
+  return s;
+}
+
+template <class T, int V, int K, int ACT>
+__global__ __launch_bounds__(kNT) void readout_apply_kernel(NormGeom g, NormArgs p, int D) {
+  Cols<V, K> col(g);
+  Affine<V, K> af;
+  af.load(p, col, D);
+  float r[K][V];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j) r[k][j] = j < col.dup[k] ? 0.0f : load_param(p.readout, p.pdtype, col.c[k] + j, 0.0f);
+  const float off = load_param(p.offset, p.pdtype, 0, 0.0f);
+  const T* xs = reinterpret_cast<const T*>(p.x) + (int64_t)blockIdx.y * g.S * g.C;
+  float* fs = p.field + (int64_t)blockIdx.y * g.S;
+  // the lanes of a wave stay together for the shuffles: rows past the end are
+  // computed from the first row and not stored
+  const int rows_wave = 64 / g.L;
+  constexpr int U = kUnroll<K>;
+  const int64_t wfirst = ((int64_t)blockIdx.x * kNW + (threadIdx.x >> 6)) * rows_wave;
+  for (int64_t w = wfirst; w < g.S; w += U * col.stride) {
+    Vec<T, V> v[U][K];
+    int64_t row[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t at = col.first + (w - wfirst) + i * col.stride;
+      row[i] = at < g.S ? g.S - 1 - at : -1;
+      const int64_t from = row[i] < 0 ? 0 : row[i];
+#pragma unroll
+      for (int k = 0; k < K; ++k) load_vec(xs + from * g.C + col.c[k], v[i][k]);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      float s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) s = fmaf(act_value<ACT>(af.u(k, j, (float)v[i][k].v[j])), r[k][j], s);
+      s = row_sum(s, col.l, g.L);
+      if (col.l == 0 && row[i] >= 0) fs[row[i]] = s + off;
+    }
+  }
+}
+
+// Backward sums: A1, A2 (and, for the grid, A3 = sum df y) per channel, and
+// the sum of df behind them.  READ: the gradient is one float32 per voxel.
+template <class T, int V, int K, int ACT, bool READ>
+__global__ __launch_bounds__(kNT) void norm_sums_kernel(NormGeom g, NormArgs p, int D, double* part, int64_t prow) {
+  constexpr int NV = READ ? 3 : 2;
+  __shared__ double lds[kSumElems<V> * NV * kNT];
+  Cols<V, K> col(g);
+  Affine<V, K> af;
+  af.load(p, col, D);
+  const int64_t base = (int64_t)blockIdx.y * g.S * g.C;
+  const T* xs = reinterpret_cast<const T*>(p.x) + base;
+  const T* gs = READ ? nullptr : reinterpret_cast<const T*>(p.gy) + base;
+  const float* fs = READ ? reinterpret_cast<const float*>(p.gy) + (int64_t)blockIdx.y * g.S : nullptr;
+  float s[K][V][NV];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) s[k][j][i] = 0.0f;
+  float sdf = 0.0f;
+  constexpr int U = READ ? kUnroll<K> : (kUnroll<K> + 1) / 2;
+  for_rows<U>(col.first, col.stride, g.S, [&](const int64_t* rows, auto N) {
+    Vec<T, V> v[N.value][K], q[N.value][K];
+    float df[N.value];
+#pragma unroll
+    for (int i = 0; i < N.value; ++i) {
+      if constexpr (READ) df[i] = fs[rows[i]];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        load_vec(xs + rows[i] * g.C + col.c[k], v[i][k]);
+        if constexpr (!READ) load_vec(gs + rows[i] * g.C + col.c[k], q[i][k]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N.value; ++i) {
+      if constexpr (READ) sdf += df[i];
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float d = (float)v[i][k].v[j] - af.mean[k][j];
+          float y;
+          const float sl = act_slope<ACT>(fmaf(d, af.a[k][j], af.b[k][j]), y);
+          float dy;
+          if constexpr (READ) dy = df[i]; else dy = (float)q[i][k].v[j];
+          const float du = dy * sl;
+          s[k][j][0] += du;
+          s[k][j][1] = fmaf(du, d, s[k][j][1]);
+          if constexpr (READ) s[k][j][2] = fmaf(dy, y, s[k][j][2]);
+        }
+    }
+  });
+  double* out = part + ((int64_t)blockIdx.y * g.NB + blockIdx.x) * prow;
+  column_sums<V, K, NV>(g, col, lds, out, [&](int k, int j, int i) { return (double)s[k][j][i]; });
+  if constexpr (READ) {
+    __syncthreads();
+    lds[threadIdx.x] = col.l == 0 ? (double)sdf : 0.0;
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      double t = 0.0;
+      for (int w = 0; w < kNW; ++w) t += lds[w * 64 + threadIdx.x];
+      for (int d = 1; d < 64; d *= 2) t += __shfl_xor(t, d);
+      if (threadIdx.x == 0) out[g.C * NV] = t;
+    }
+  }
+}
+
+// dx.  Workgroup rows past the samples (blockIdx.y == B) sum the parameter
+// gradients over the samples instead; without dx they are the whole launch.
+template <class T, int V, int K, int ACT, bool READ>
+__global__ __launch_bounds__(kNT) void norm_grad_kernel(NormGeom g, NormArgs p, int D, const double* chan,
+                                                        int64_t prow, const float* coef) {
+  constexpr int NV = READ ? 3 : 2;
+  if (!p.gx || blockIdx.y == p.B) {
+    if (blockIdx.z) return;
+    for (int64_t c = (int64_t)blockIdx.x * kNT + threadIdx.x; c < g.C + (READ ? 1 : 0); c += (int64_t)g.NB * kNT) {
+      double t[3] = {0.0, 0.0, 0.0};
+      for (int64_t b = 0; b < p.B; ++b)
+        for (int i = 0; i < (c < g.C ? NV : 1); ++i) t[i] += chan[b * prow + c * NV + i];
+      if (c == g.C) {
+        if (p.go) store_param(p.go, p.pdtype, 0, (float)t[0]);
+        continue;
+      }
+      const double r = READ ? (double)load_param(p.readout, p.pdtype, c, 0.0f) : 1.0;
+      if (p.gb) store_param(p.gb, p.pdtype, c, (float)(r * t[0]));
+      if (p.gw) store_param(p.gw, p.pdtype, c, (float)(r * t[1]));
+      if (READ && p.gr) store_param(p.gr, p.pdtype, c, (float)t[2]);
+    }
+    return;
+  }
+  Cols<V, K> col(g);
+  Affine<V, K> af;
+  af.load(p, col, D);
+  float c0[K][V], c1[K][V], ar[K][V];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = col.c[k] + j;
+      const int64_t gr = (int64_t)blockIdx.y * p.G + (unsigned)c / (unsigned)D;
+      c0[k][j] = coef[2 * gr];
+      c1[k][j] = coef[2 * gr + 1];
+      ar[k][j] = READ ? af.a[k][j] * load_param(p.readout, p.pdtype, c, 0.0f) : af.a[k][j];
+    }
+  const int64_t base = (int64_t)blockIdx.y * g.S * g.C;
+  const T* xs = reinterpret_cast<const T*>(p.x) + base;
+  const T* gs = READ ? nullptr : reinterpret_cast<const T*>(p.gy) + base;
+  const float* fs = READ ? reinterpret_cast<const float*>(p.gy) + (int64_t)blockIdx.y * g.S : nullptr;
+  T* os = reinterpret_cast<T*>(p.gx) + base;
+  constexpr int U = READ ? kUnroll<K> : (kUnroll<K> + 1) / 2;
+  for_rows<U>(col.first, col.stride, g.S, [&](int64_t* rows, auto N) {
+    Vec<T, V> v[N.value][K], q[N.value][K];
+    float df[N.value];
+#pragma unroll
+    for (int i = 0; i < N.value; ++i) {
+      rows[i] = g.S - 1 - rows[i];  // what the sums read last is read first
+      if constexpr (READ) df[i] = fs[rows[i]];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        load_vec(xs + rows[i] * g.C + col.c[k], v[i][k]);
+        if constexpr (!READ) load_vec(gs + rows[i] * g.C + col.c[k], q[i][k]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N.value; ++i)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        Vec<T, V> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float d = (float)v[i][k].v[j] - af.mean[k][j];
+          float y;
+          const float sl = act_slope<ACT>(fmaf(d, af.a[k][j], af.b[k][j]), y);
+          float dy;
+          if constexpr (READ) dy = df[i]; else dy = (float)q[i][k].v[j];
+          o.v[j] = (T)fmaf(ar[k][j], dy * sl, fmaf(-d, c1[k][j], -c0[k][j]));
+        }
+        if (col.dup[k] < V) store_vec(os + rows[i] * g.C + col.c[k], o);
+      }
+  });
+}
+
+__device__ __forceinline__ double block_sum(double v, double* lds) {
+  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double t = 0.0;
+  for (int w = 0; w < kNW; ++w) t += lds[w];
+  return t;
+}
+
+// Joins the partial rows of one sample and group: statistics (forward).
+__global__ __launch_bounds__(kNT) void norm_join_kernel(NormArgs p, const double* part, int NB, int D, int64_t prow) {
+  __shared__ double lds[kNW];
+  const int64_t b = blockIdx.y, gr = blockIdx.x;
+  const int W = D < kNT ? D : kNT, parts = kNT / W;
+  const int at = threadIdx.x % W, pt = threadIdx.x / W;
+  double s1 = 0.0, s2 = 0.0;
+  if (pt < parts)
+    for (int blk = pt; blk < NB; blk += parts)
+      for (int64_t c = at; c < D; c += W) {
+        const double* q = part + (b * NB + blk) * prow + (gr * D + c) * 2;
+        s1 += q[0];
+        s2 += q[1];
+      }
+  s1 = block_sum(s1, lds);
+  s2 = block_sum(s2, lds);
+  if (threadIdx.x == 0) {
+    const double n = (double)p.S * (double)D, mean = s1 / n;
+    double var = s2 / n - mean * mean;
+    var = var < 0.0 ? 0.0 : var;
+    p.stats[(b * p.G + gr) * 2] = (float)mean;
+    p.stats[(b * p.G + gr) * 2 + 1] = (float)(1.0 / sqrt(var + (double)p.eps));
+  }
+}
+
+// Joins the partial rows of one sample and group: channel sums with A2 scaled
+// by rstd, and the group's coefficients rstd m1 and rstd^2 m2 (backward).
+template <bool READ>
+__global__ __launch_bounds__(kNT) void norm_join_bwd_kernel(NormArgs p, const double* part, int NB, int D,
+                                                            int64_t prow, double* chan, float* coef) {
+  constexpr int NV = READ ? 3 : 2;
+  __shared__ double lds[NV * kNT];
+  const int64_t b = blockIdx.y, gr = blockIdx.x;
+  const int W = D < kNT ? D : kNT, parts = kNT / W;
+  const int at = threadIdx.x % W, pt = threadIdx.x / W;
+  const double rstd = (double)p.stats[(b * p.G + gr) * 2 + 1];
+  double m1 = 0.0, m2 = 0.0;
+  for (int64_t c0 = 0; c0 < D; c0 += W) {
+    const int64_t c = gr * D + c0 + at;
+    double s[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] = 0.0;
+    if (pt < parts && c0 + at < D)
+      for (int blk = pt; blk < NB; blk += parts) {
+        const double* q = part + (b * NB + blk) * prow + c * NV;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s[i] += q[i];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) lds[i * kNT + threadIdx.x] = s[i];
+    __syncthreads();
+    if (threadIdx.x < W && c0 + at < D) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        s[i] = 0.0;
+        for (int q = 0; q < parts; ++q) s[i] += lds[i * kNT + q * W + at];
+      }
+      s[1] *= rstd;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) chan[b * prow + c * NV + i] = s[i];
+      double w = (double)load_param(p.weight, p.pdtype, c, 1.0f);
+      if (READ) w *= (double)load_param(p.readout, p.pdtype, c, 0.0f);
+      m1 += w * s[0];
+      m2 += w * s[1];
+    }
+  }
+  __syncthreads();
+  m1 = block_sum(m1, lds);
+  m2 = block_sum(m2, lds);
+  if (threadIdx.x == 0) {
+    const double n = (double)p.S * (double)D;
+    coef[2 * (b * p.G + gr)] = (float)(rstd * (m1 / n));
+    coef[2 * (b * p.G + gr) + 1] = (float)(rstd * rstd * (m2 / n));
+  }
+  if (READ && gr == 0) {
+    double t = 0.0;
+    for (int blk = threadIdx.x; blk < NB; blk += kNT) t += part[(b * NB + blk) * prow + p.C * NV];
+    t = block_sum(t, lds);
+    if (threadIdx.x == 0) chan[b * prow + p.C * NV] = t;
+  }
+}
+
+// Lanes and vectors per row: the fewest vectors per lane that keep within 5 %
+// of the best use of the lanes (rows of nv vectors on floor(64 / L) L lanes).
+template <class T>
+NormGeom norm_geom(const NormArgs& a, int& V, int& K) {
+  constexpr int VF = 16 / sizeof(T);
+  V = a.C >= VF ? VF : 1;
+  NormGeom g{};
+  g.S = a.S;
+  g.C = a.C;
+  g.NB = (int)norm_blocks(a.B, a.S, a.C);
+  g.nv = (int)((a.C + V - 1) / V);
+  g.chunks = 1;
+  K = 1;
+  g.L = 64;
+  if (g.nv > 4 * 64) {
+    g.chunks = (g.nv + 63) / 64;
+    return g;
+  }
+  double best = 0.0;
+  for (int k = 1; k <= (V == 1 ? 1 : 4); k *= 2) {
+    const int L = (g.nv + k - 1) / k;
+    if (L > 64) continue;
+    const double use = (double)(g.nv * (64 / L)) / (64.0 * k);
+    if (use > 1.05 * best) {
+      best = use;
+      K = k;
+      g.L = L;
+    }
+  }
+  return g;
+}
+
+template <class F>
+hipError_t with_act(int act, F f) {
+  switch (act) {
+    case kActRelu: return f(std::integral_constant<int, kActRelu>());
+    case kActSilu: return f(std::integral_constant<int, kActSilu>());
+    case kActGelu: return f(std::integral_constant<int, kActGelu>());
+    default: return f(std::integral_constant<int, kActNone>());
+  }
+}
+
+// f(V, K) with the pair as compile-time constants
+template <class T, class F>
+hipError_t with_cols(int V, int K, F f) {
+  constexpr int VF = 16 / sizeof(T);
+  using std::integral_constant;
+  if (V == 1) return f(integral_constant<int, 1>(), integral_constant<int, 1>());
+  if (K == 1) return f(integral_constant<int, VF>(), integral_constant<int, 1>());
+  if (K == 2) return f(integral_constant<int, VF>(), integral_constant<int, 2>());
+  return f(integral_constant<int, VF>(), integral_constant<int, 4>());
+}
+
+}  // namespace
+
+template <class T>
+hipError_t norm_launch_fwd(const NormArgs& a, hipStream_t stream) {
+  int V, K;
+  const NormGeom g = norm_geom<T>(a, V, K);
+  const int D = (int)(a.C / a.G);
+  const int64_t prow = (int64_t)norm_row(a.C);
+  double* part = reinterpret_cast<double*>(a.ws);
+  const dim3 grid((unsigned)g.NB, (unsigned)a.B, (unsigned)g.chunks), block(kNT);
+  return with_cols<T>(V, K, [&](auto v, auto k) {
+    constexpr int VV = v.value, KK = k.value;
+    hipLaunchKernelGGL((norm_stats_kernel<T, VV, KK>), grid, block, 0, stream, g, reinterpret_cast<const T*>(a.x), part,
+                       prow);
+    hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)a.G, (unsigned)a.B), block, 0, stream, a, part, g.NB, D, prow);
+    return with_act(a.act, [&](auto act) {
+      if (a.field)
+        hipLaunchKernelGGL((readout_apply_kernel<T, VV, KK, act.value>), grid, block, 0, stream, g, a, D);
+      else
+        hipLaunchKernelGGL((norm_apply_kernel<T, VV, KK, act.value>), grid, block, 0, stream, g, a, D);
+      return hipGetLastError();
+    });
+  });
+}
+
+template <class T>
+hipError_t norm_launch_bwd(const NormArgs& a, hipStream_t stream) {
+  int V, K;
+  const NormGeom g = norm_geom<T>(a, V, K);
+  const int D = (int)(a.C / a.G);
+  const int64_t prow = (int64_t)norm_row(a.C);
+  double* part = reinterpret_cast<double*>(a.ws);
+  double* chan = part + (int64_t)a.B * g.NB * prow;
+  float* coef = reinterpret_cast<float*>(chan + a.B * prow);
+  const dim3 grid((unsigned)g.NB, (unsigned)a.B, (unsigned)g.chunks), block(kNT), join((unsigned)a.G, (unsigned)a.B);
+  const dim3 last((unsigned)g.NB, a.gx ? (unsigned)a.B + 1 : 1u, a.gx ? (unsigned)g.chunks : 1u);
+  return with_cols<T>(V, K, [&](auto v, auto k) {
+    constexpr int VV = v.value, KK = k.value;
+    return with_act(a.act, [&](auto act) {
+      constexpr int A = act.value;
+      if (a.readout) {
+        hipLaunchKernelGGL((norm_sums_kernel<T, VV, KK, A, true>), grid, block, 0, stream, g, a, D, part, prow);
+        hipLaunchKernelGGL((norm_join_bwd_kernel<true>), join, block, 0, stream, a, part, g.NB, D, prow, chan, coef);
+        hipLaunchKernelGGL((norm_grad_kernel<T, VV, KK, A, true>), last, block, 0, stream, g, a, D, chan, prow, coef);
+      } else {
+        hipLaunchKernelGGL((norm_sums_kernel<T, VV, KK, A, false>), grid, block, 0, stream, g, a, D, part, prow);
+        hipLaunchKernelGGL((norm_join_bwd_kernel<false>), join, block, 0, stream, a, part, g.NB, D, prow, chan, coef);
+        hipLaunchKernelGGL((norm_grad_kernel<T, VV, KK, A, false>), last, block, 0, stream, g, a, D, chan, prow, coef);
+      }
+      return hipGetLastError();
+    });
+  });
+}
+
+}  // namespace ecc

@@ -1,0 +1,201 @@
+"""Thin PyTorch binding of the training operators (include/ecc_train.h).
+
+Features are channels last, ``[batch, *space, channels]``; every function takes
+tensors that live on a ROCm device, checks them, and calls the C entry points
+on the current torch stream.  All arithmetic happens in the HIP kernels.
+Scratch comes from torch's allocator per call, so calls may run on any stream
+and be captured into a graph.
+"""
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _lib
+from ._lib import EccError, check, lib
+from .ecc import _dev_tensor, _ptr, _stream
+
+__all__ = ["group_norm_act", "group_norm_readout", "GroupNormAct", "GroupNormReadout", "EccError"]
+
+_DTYPES = {torch.float32: _lib.ECC_T_F32, torch.float16: _lib.ECC_T_F16, torch.bfloat16: _lib.ECC_T_BF16}
+_ACTS = {"none": _lib.ECC_ACT_NONE, "relu": _lib.ECC_ACT_RELU, "silu": _lib.ECC_ACT_SILU, "gelu": _lib.ECC_ACT_GELU}
+
+
+def _on_device(t):
+    """Runs the call on the tensor's GPU (a no-op where that is the current one)."""
+    return torch.cuda.device(t.device) if t.get_device() != torch.cuda.current_device() else _NULL_CONTEXT
+
+
+class _NullContext:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NULL_CONTEXT = _NullContext()
+
+
+def _param_ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _NormCall:
+    """Checked arguments of one norm: sizes, types and the C argument block."""
+
+    __slots__ = ("x", "weight", "bias", "readout", "offset", "sizes", "dtype", "pdtype", "act", "nbytes")
+
+    def __init__(self, x, groups, weight, bias, act, readout=None, offset=None, with_readout=False):
+        _dev_tensor(x, "x")
+        if x.dtype not in _DTYPES:
+            raise TypeError(f"x dtype {x.dtype} not supported (float32, float16 or bfloat16)")
+        if x.dim() < 3:
+            raise ValueError("x must be [batch, *space, channels]")
+        if act not in _ACTS:
+            raise ValueError(f"act must be one of {sorted(_ACTS)} (got {act!r})")
+        C = x.shape[-1]
+        if isinstance(groups, bool) or not isinstance(groups, int):
+            raise TypeError(f"groups must be an int (got {type(groups).__name__})")
+        if groups < 1 or C < 1 or C % groups:
+            raise ValueError(f"groups={groups} does not divide channels={C}")
+        if with_readout and readout is None:
+            raise TypeError("readout must be a torch.Tensor")
+        pdtype = None
+        for t, name, n in ((weight, "weight", C), (bias, "bias", C), (readout, "readout", C), (offset, "offset", 1)):
+            if t is None:
+                continue
+            _dev_tensor(t, name, None, x.device)
+            if tuple(t.shape) != (n,):
+                raise ValueError(f"{name} must be [{n}] (got {list(t.shape)})")
+            if t.dtype != torch.float32 and t.dtype != x.dtype:
+                raise TypeError(f"{name} must be torch.float32 or x's {x.dtype} (got {t.dtype})")
+            if pdtype is not None and t.dtype != pdtype:
+                raise TypeError(f"{name} is {t.dtype}, the parameters before it {pdtype}")
+            pdtype = t.dtype
+        self.x, self.weight, self.bias, self.readout, self.offset = x, weight, bias, readout, offset
+        B = x.shape[0]
+        self.sizes = (B, x.numel() // (B * C) if B else 0, C, groups)
+        self.dtype, self.act = _DTYPES[x.dtype], _ACTS[act]
+        self.pdtype = _DTYPES[pdtype or torch.float32]
+        self.nbytes = 0
+        if x.numel():
+            self.nbytes = lib.ecc_norm_workspace_bytes(*self.sizes)
+            if not self.nbytes:
+                raise EccError(_lib.ECC_E_SHAPE, "group norm: " + lib.ecc_last_error().decode(errors="replace"))
+
+    def forward(self, eps):
+        """(y or field, stats)."""
+        x, (B, S, C, G) = self.x, self.sizes
+        stats = torch.empty((B, G, 2), dtype=torch.float32, device=x.device)
+        if self.readout is None:
+            out = torch.empty_like(x)
+        else:
+            out = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        if not x.numel():
+            return out, stats
+        with _on_device(x):
+            ws = torch.empty(self.nbytes, dtype=torch.uint8, device=x.device)
+            stream = _stream(x).cuda_stream
+            if self.readout is None:
+                check(lib.ecc_norm_fwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(self.weight), _param_ptr(self.bias),
+                                       self.pdtype, self.act, float(eps), _ptr(out), _ptr(stats), _ptr(ws), self.nbytes,
+                                       stream), "ecc_norm_fwd")
+            else:
+                check(lib.ecc_norm_readout_fwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(self.weight),
+                                               _param_ptr(self.bias), _ptr(self.readout), _param_ptr(self.offset),
+                                               self.pdtype, self.act, float(eps), _ptr(out), _ptr(stats), _ptr(ws),
+                                               self.nbytes, stream), "ecc_norm_readout_fwd")
+        return out, stats
+
+    def backward(self, stats, grad, needs):
+        """Gradients of (x, weight, bias, readout, offset), None where not needed."""
+        x, (B, S, C, G) = self.x, self.sizes
+        inputs = (x, self.weight, self.bias, self.readout, self.offset)
+        grads = [torch.empty_like(t) if need and t is not None else None for t, need in zip(inputs, needs)]
+        if not x.numel():
+            return [None if g is None else g.zero_() for g in grads]
+        if all(g is None for g in grads):
+            return grads
+        ptrs = [_param_ptr(g) for g in grads]
+        with _on_device(x):
+            ws = torch.empty(self.nbytes, dtype=torch.uint8, device=x.device)
+            stream = _stream(x).cuda_stream
+            if self.readout is None:
+                check(lib.ecc_norm_bwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(self.weight), _param_ptr(self.bias),
+                                       self.pdtype, self.act, _ptr(stats), _ptr(grad), *ptrs[:3], _ptr(ws), self.nbytes,
+                                       stream), "ecc_norm_bwd")
+            else:
+                check(lib.ecc_norm_readout_bwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(self.weight),
+                                               _param_ptr(self.bias), _ptr(self.readout), self.pdtype, self.act,
+                                               _ptr(stats), _ptr(grad), *ptrs, _ptr(ws), self.nbytes, stream),
+                      "ecc_norm_readout_bwd")
+        return grads
+
+
+def _contiguous(t):
+    return None if t is None else t.detach().contiguous()
+
+
+def _needs_grad(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+class GroupNormAct(torch.autograd.Function):
+    """Autograd wrapper of ecc_norm_fwd / ecc_norm_bwd."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, groups, act, eps):
+        call = _NormCall(_contiguous(x), groups, _contiguous(weight), _contiguous(bias), act)
+        y, stats = call.forward(eps)
+        ctx.save_for_backward(x, weight, bias, stats)
+        ctx.groups, ctx.act = groups, act
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        x, weight, bias, stats = ctx.saved_tensors
+        call = _NormCall(_contiguous(x), ctx.groups, _contiguous(weight), _contiguous(bias), ctx.act)
+        grads = call.backward(stats, grad.contiguous(), ctx.needs_input_grad[:3])
+        return (*grads[:3], None, None, None)
+
+
+class GroupNormReadout(torch.autograd.Function):
+    """Autograd wrapper of ecc_norm_readout_fwd / ecc_norm_readout_bwd."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, readout, offset, groups, act, eps):
+        call = _NormCall(_contiguous(x), groups, _contiguous(weight), _contiguous(bias), act, _contiguous(readout),
+                         _contiguous(offset), with_readout=True)
+        field, stats = call.forward(eps)
+        ctx.save_for_backward(x, weight, bias, readout, offset, stats)
+        ctx.groups, ctx.act = groups, act
+        return field
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        x, weight, bias, readout, offset, stats = ctx.saved_tensors
+        call = _NormCall(_contiguous(x), ctx.groups, _contiguous(weight), _contiguous(bias), ctx.act,
+                         _contiguous(readout), _contiguous(offset), with_readout=True)
+        return (*call.backward(stats, grad.contiguous(), ctx.needs_input_grad[:5]), None, None, None)
+
+
+def group_norm_act(x, groups, weight=None, bias=None, act="none", eps=1e-5):
+    """act(group_norm(x) * weight + bias) over channels-last features, differentiable in x, weight and bias.
+
+    x: float32, float16 or bfloat16 [batch, *space, channels]; weight and bias: [channels], float32 or x's dtype, or
+    None (1 and 0); act: "none", "relu", "silu" or "gelu".  Returns a tensor like x (see include/ecc_train.h).
+    """
+    if _needs_grad(x, weight, bias):
+        return GroupNormAct.apply(x, weight, bias, groups, act, eps)
+    return _NormCall(x.contiguous(), groups, _contiguous(weight), _contiguous(bias), act).forward(eps)[0]
+
+
+def group_norm_readout(x, groups, weight, bias, readout, offset=None, act="none", eps=1e-5):
+    """The features group_norm_act gives, contracted with ``readout`` [channels] plus ``offset`` [1] to the float32 grid
+    [batch, *space] that a curve takes.  Differentiable in x and all four parameters; the features are not stored."""
+    if _needs_grad(x, weight, bias, readout, offset):
+        return GroupNormReadout.apply(x, weight, bias, readout, offset, groups, act, eps)
+    return _NormCall(x.contiguous(), groups, _contiguous(weight), _contiguous(bias), act, _contiguous(readout),
+                     _contiguous(offset), with_readout=True).forward(eps)[0]

@@ -1,0 +1,114 @@
+/*
+ * ecc_train.h -- C ABI of the operators in libecc_mi355.so that train a
+ * network through the curves: group norm with an activation over
+ * channels-last features, the same norm read out to the scalar grid a curve
+ * takes, Newton-Schulz orthogonalisation, and the momentum update built on it.
+ *
+ * Conventions are those of ecc.h (device pointers owned by the caller, work
+ * enqueued on `stream`, status codes, ecc_last_error), except the workspace:
+ *   - `ws` is scratch of at least the bytes its size function gives, 256-byte
+ *     aligned.  It need not be cleared before a call and holds nothing after
+ *     it; calls that overlap in time must not share one.
+ *   - The library allocates nothing and clears nothing with a memset, so every
+ *     call may be captured into a graph.
+ * Every output is written in full, and its value does not depend on
+ * scheduling: sums are formed in a fixed order and no floating-point atomics
+ * are used.
+ */
+#ifndef ECC_TRAIN_MI355_H
+#define ECC_TRAIN_MI355_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* status codes beyond those of ecc.h */
+#define ECC_E_GROUPS 9 /* groups < 1 or channels not a multiple of groups     */
+#define ECC_E_ACT 10   /* act is not one of ECC_ACT_*                         */
+#define ECC_E_VALUE 11 /* a scalar argument is out of range or not finite     */
+
+/* element types of features, parameters and matrices */
+#define ECC_T_F32 0
+#define ECC_T_F16 1
+#define ECC_T_BF16 2
+
+/* activations */
+#define ECC_ACT_NONE 0
+#define ECC_ACT_RELU 1
+#define ECC_ACT_SILU 2 /* u / (1 + exp(-u))                                   */
+#define ECC_ACT_GELU 3 /* u Phi(u), Phi the normal distribution function      */
+
+#define ECC_MAX_CHANNELS 8192          /* of the norm                         */
+#define ECC_MAX_READOUT_CHANNELS 1024  /* of the norm read out to a grid      */
+#define ECC_MAX_NORM_BATCH 32768
+#define ECC_MAX_MATRIX 32768           /* rows and columns of one matrix      */
+#define ECC_MAX_NS_STEPS 64
+
+/*
+ * Group norm with an activation, channels last.
+ *   x       device, dtype elements, [batch][voxels][channels]
+ *   weight, bias  device, pdtype elements, [channels]; NULL stands for 1 / 0
+ *   y       device, dtype elements, x's shape (must not overlap x):
+ *           xhat = (x - mean) / sqrt(var + eps) over the voxels and the
+ *           channels / groups channels of one group of one sample (var with
+ *           the divisor voxels * channels / groups), u = xhat * weight + bias,
+ *           y = act(u)
+ *   stats   device float32 [batch][groups][2]: mean and 1/sqrt(var + eps),
+ *           written by the forward call and read by the backward one
+ *   pdtype  ECC_T_F32 or dtype
+ * Moments are accumulated in float32 about a pivot per thread and joined in
+ * float64; everything else is float32, rounded once to dtype.  x and y need
+ * only the alignment of their elements.  Three kernel launches.
+ */
+int ecc_norm_fwd(const void* x, int dtype, int64_t batch, int64_t voxels, int64_t channels, int64_t groups,
+                 const void* weight, const void* bias, int pdtype, int act, float eps, void* y, float* stats,
+                 void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Its backward pass.  grad_y: dL/dy, dtype elements.  grad_x (dtype),
+ * grad_weight and grad_bias (pdtype) are OVERWRITTEN; each may be NULL (not
+ * wanted), but not all of them.  With
+ * du = grad_y act'(u) (act'(0) = 0 for relu),
+ *   grad_bias = sum du, grad_weight = sum du xhat   over samples and voxels,
+ *   grad_x = rstd (du weight - m1 - xhat m2), m1 and m2 the means over the
+ *   group of du weight and of du weight xhat.
+ * Three kernel launches.
+ */
+int ecc_norm_bwd(const void* x, int dtype, int64_t batch, int64_t voxels, int64_t channels, int64_t groups,
+                 const void* weight, const void* bias, int pdtype, int act, const float* stats, const void* grad_y,
+                 void* grad_x, void* grad_weight, void* grad_bias, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The same norm contracted to a scalar grid:
+ *   field[b][v] = offset + sum over c of readout[c] act(u[b][v][c]),
+ * float32 [batch][voxels], ready for a curve.  readout: [channels], offset:
+ * [1] or NULL (0), both pdtype.  channels <= ECC_MAX_READOUT_CHANNELS.  The
+ * activated features are never written.
+ */
+int ecc_norm_readout_fwd(const void* x, int dtype, int64_t batch, int64_t voxels, int64_t channels, int64_t groups,
+                         const void* weight, const void* bias, const void* readout, const void* offset, int pdtype,
+                         int act, float eps, float* field, float* stats, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Its backward pass from grad_field = dL/dfield, float32 [batch][voxels]:
+ * grad_readout = sum grad_field act(u), grad_offset = sum grad_field, and the
+ * gradients of ecc_norm_bwd for grad_y = grad_field readout.  Gradients that
+ * are not wanted are NULL.
+ */
+int ecc_norm_readout_bwd(const void* x, int dtype, int64_t batch, int64_t voxels, int64_t channels, int64_t groups,
+                         const void* weight, const void* bias, const void* readout, int pdtype, int act,
+                         const float* stats, const float* grad_field, void* grad_x, void* grad_weight,
+                         void* grad_bias, void* grad_readout, void* grad_offset, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* Workspace bytes of the four calls above (0 for invalid sizes). */
+size_t ecc_norm_workspace_bytes(int64_t batch, int64_t voxels, int64_t channels, int64_t groups);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* ECC_TRAIN_MI355_H */
