@@ -19,7 +19,8 @@ _API = (
     "ecc_hard_directional", "soft_ecc_directional",
 )
 
-_TRAIN_API = ("group_norm_act", "group_norm_readout", "GroupNormAct", "GroupNormReadout")
+_TRAIN_API = ("group_norm_act", "group_norm_readout", "GroupNormAct", "GroupNormReadout", "orthogonalize",
+              "muon_step")
 
 __all__ = list(_API + _TRAIN_API)
 

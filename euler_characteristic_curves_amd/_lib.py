@@ -55,6 +55,7 @@ ECC_MAX_NS_STEPS = 64
 
 TRAIN_EXPORTS = (
     "ecc_norm_fwd", "ecc_norm_bwd", "ecc_norm_readout_fwd", "ecc_norm_readout_bwd", "ecc_norm_workspace_bytes",
+    "ecc_orthogonalize", "ecc_muon_step", "ecc_orth_workspace_bytes",
 )
 
 
@@ -73,7 +74,7 @@ def _load():
             "(ROCm hipcc, gfx950). There is no CPU fallback.")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-    F = ctypes.c_float
+    F, D = ctypes.c_float, ctypes.c_double
     lib.ecc_hard_2d.argtypes = [P, I, I64, I64, P, I32, P, P, SZ, P]
     lib.ecc_hard_2d.restype = I
     lib.ecc_hard_3d.argtypes = [P, I, I64, I64, I64, P, I32, P, P, SZ, P]
@@ -118,6 +119,12 @@ def _load():
     lib.ecc_norm_readout_bwd.restype = I
     lib.ecc_norm_workspace_bytes.argtypes = [I64, I64, I64, I64]
     lib.ecc_norm_workspace_bytes.restype = SZ
+    lib.ecc_orthogonalize.argtypes = [P, I, I64, I64, I64, I32, F, F, F, F, P, P, SZ, P]
+    lib.ecc_orthogonalize.restype = I
+    lib.ecc_muon_step.argtypes = [P, I, P, I, P, I64, I64, I64, D, D, I, D, D, I32, F, F, F, F, P, SZ, P]
+    lib.ecc_muon_step.restype = I
+    lib.ecc_orth_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.ecc_orth_workspace_bytes.restype = SZ
     lib.ecc_status_string.argtypes = [I]
     lib.ecc_status_string.restype = ctypes.c_char_p
     lib.ecc_last_error.argtypes = []

@@ -1,0 +1,515 @@
+// Newton-Schulz orthogonalisation and the momentum update built on it
+// (contract: include/ecc_train.h).
+//
+// With X (m x n, m <= n; a tall matrix is transposed on the way in and out)
+// scaled to Frobenius norm below 1, a step is
+//   A = X X^T,   P = a I + b A + c A A,   X <- P X,
+// an odd polynomial of the singular values.  A and P are symmetric: only their
+// lower triangle of tiles is computed, and written twice.
+//
+// Arithmetic.  gfx950's float32 matrix instructions run at a sixteenth of the
+// float16 ones, so every operand is held as a pair of float16 numbers, x 2^s =
+// hi + lo, 22 bits and a sign together, and a product is three float16 matrix
+// products, hi hi' + hi lo' + lo hi', summed in float32 (the dropped lo lo' is
+// below 2^-24).  The exponent s comes from a bound of the matrix's entries, so
+// that nothing overflows and lo stays above float16's smallest number: per
+// matrix and step for X, per call for A and P.  What bounds the products is
+// the matrix unit; the pair is three times cheaper for LDS and L2 than for it.
+//
+// Layout.  A pair matrix keeps, per row, blocks of 32 columns as 32 hi then 32
+// lo: 128 bytes, the unit a tile's row loads per step of the long axis.  Both
+// operands of a product lie along the summed axis, so X is kept twice, as X
+// and as X^T.  Rows and columns are padded with zeros to the tile, and stay
+// zero, so no product checks a bound.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "ecc_act.hpp"
+#include "ecc_internal.hpp"
+#include "ecc_train_internal.hpp"
+
+namespace ecc {
+namespace {
+
+constexpr int kNT = 256;
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// Offset of element (row, col) of a pair matrix whose rows have `kpad` columns.
+__device__ __forceinline__ int64_t pair_at(int64_t row, int64_t col, int64_t kpad) {
+  return row * 2 * kpad + (col >> 5) * 64 + (col & 31);
+}
+
+// ------------------------------------------------------------- preparation
+// The matrix to be orthogonalised, element i of one matrix: the gradient, or
+// the momentum buffer after its update, or both mixed (Nesterov).
+template <class GT>
+__device__ __forceinline__ float momentum_next(const OrthArgs& p, const GT* g, const float* buf, int64_t i) {
+  return fmaf(p.momentum, buf[i], p.blend * (float)g[i]);
+}
+template <class GT>
+__device__ __forceinline__ float update_value(const OrthArgs& p, const GT* g, const float* buf, int64_t i) {
+  if (!buf) return (float)g[i];
+  const float b = buf[i];  // already the new buffer
+  return p.nesterov ? fmaf(p.momentum, b, p.blend * (float)g[i]) : b;
+}
+
+// Sums of squares, float64, one slot per workgroup; the momentum buffer is
+// updated on the way.
+template <class GT>
+__global__ __launch_bounds__(kNT) void orth_square_kernel(OrthArgs p) {
+  __shared__ double lds[kNT / 64];
+  const int64_t n = p.rows * p.cols, off = (int64_t)blockIdx.y * n;
+  const GT* g = reinterpret_cast<const GT*>(p.g) + off;
+  float* buf = p.buffer ? p.buffer + off : nullptr;
+  double s = 0.0;
+  const int64_t stride = (int64_t)gridDim.x * kNT;
+#pragma unroll 4
+  for (int64_t i = (int64_t)blockIdx.x * kNT + threadIdx.x; i < n; i += stride) {
+    if (buf) buf[i] = momentum_next(p, g, buf, i);
+    const double v = (double)update_value(p, g, buf, i);
+    s = fma(v, v, s);
+  }
+  for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) p.squares[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+// 1 / (norm + eps) of this workgroup's matrix, and the bound of ||X|| that
+// follows, from the slots above (every thread gets both).
+__device__ __forceinline__ double inverse_norm(const OrthArgs& p, int batch, double* lds, double& bound) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < p.square_blocks; i += kNT) s += p.squares[(int64_t)batch * p.square_blocks + i];
+  for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
+  __syncthreads();
+  const double norm = sqrt((lds[0] + lds[1]) + (lds[2] + lds[3]));
+  const double inv = 1.0 / (norm + (double)p.eps);
+  bound = norm * inv;
+  return inv;
+}
+
+// 2^s for a matrix of entries up to `bound`: the largest entry lands in (2^13, 2^14].
+__device__ __forceinline__ float pair_scale(float bound) {
+  int e;
+  frexpf(fmaxf(bound, 1e-30f), &e);  // bound <= 2^e
+  return ldexpf(1.0f, 14 - e);
+}
+
+__device__ __forceinline__ void split(float v, f16& hi, f16& lo) {
+  hi = (f16)v;
+  lo = (f16)(v - (float)hi);
+}
+
+// X and X^T as pairs from a 64 x 64 tile of the input, and the scales of the
+// steps.  P1 has the input's orientation, P2 the other.
+template <class GT>
+__global__ __launch_bounds__(kNT) void orth_prepare_kernel(OrthArgs p, f16* P1, f16* P2, int64_t rpad, int64_t cpad) {
+  __shared__ float tile[64][65];
+  __shared__ double lds[kNT / 64];
+  const int batch = blockIdx.z;
+  double bound;
+  const double inv = inverse_norm(p, batch, lds, bound);
+  const float sc = pair_scale((float)bound);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    float r = (float)bound;
+    for (int k = 0; k <= p.steps; ++k) {
+      p.scales[(int64_t)batch * (p.steps + 1) + k] = pair_scale(r);
+      r = fminf(r * p.growth, p.cap);
+    }
+  }
+  const int64_t n = p.rows * p.cols, off = (int64_t)batch * n;
+  const GT* g = reinterpret_cast<const GT*>(p.g) + off;
+  const float* buf = p.buffer ? p.buffer + off : nullptr;
+  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+#pragma unroll 4
+  for (int i = ty; i < 64; i += 4) {
+    const int64_t r = r0 + i, c = c0 + tx;
+    float v = 0.0f;
+    if (r < p.rows && c < p.cols) v = (float)((double)update_value(p, g, buf, r * p.cols + c) * inv) * sc;
+    tile[i][tx] = v;
+  }
+  __syncthreads();
+  f16* out1 = P1 + (int64_t)batch * rpad * 2 * cpad;
+  f16* out2 = P2 + (int64_t)batch * rpad * 2 * cpad;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int at = q * kNT + threadIdx.x, row = at >> 4, ch = at & 15;
+    const int k = (ch >> 3) * 32 + (ch & 3) * 8;
+    const bool low = (ch >> 2) & 1;
+    f16x8 a, b;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f16 hi, lo;
+      split(tile[row][k + j], hi, lo);
+      a[j] = low ? lo : hi;
+      split(tile[k + j][row], hi, lo);
+      b[j] = low ? lo : hi;
+    }
+    *reinterpret_cast<f16x8*>(out1 + (r0 + row) * 2 * cpad + c0 * 2 + ch * 8) = a;
+    *reinterpret_cast<f16x8*>(out2 + (c0 + row) * 2 * rpad + r0 * 2 + ch * 8) = b;
+  }
+}
+
+// ----------------------------------------------------------------- products
+enum Kind { kGram, kPoly, kUpdate, kLast };
+
+// One product, out = A B^T over pair matrices, and what becomes of it.
+struct Product {
+  const f16 *A, *B;    // [batch][rows][2 kpad]
+  int64_t sA, sB;      // batch strides, elements
+  int64_t kpad;        // columns of both operands
+  int ksteps;          // steps of 32 columns that are not all padding
+  int tiles_m, tiles_n;
+  int splits;          // workgroups that share one tile's columns
+  float* part;         // their float32 sums, when splits > 1
+  int step;
+  float sa, sp;        // scales of A and of P
+  f16 *out, *outT;     // pair matrices written (outT: the transpose, of kUpdate)
+  int64_t sOut, out_pad, outT_pad;
+  const f16* gram;     // kPoly: the matrix A itself
+  OrthArgs o;
+};
+
+template <int T>
+constexpr int kFrag = T / 64;  // 32 x 32 fragments per wave and axis (4 waves, 2 x 2)
+
+// Row and column tile of workgroup `t`.  Symmetric products enumerate the
+// lower triangle, row by row.
+__device__ __forceinline__ void tile_of(bool sym, int t, int tiles_n, int& ti, int& tj) {
+  if (sym) {
+    int i = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+    while ((i + 1) * (i + 2) / 2 <= t) ++i;
+    while (i * (i + 1) / 2 > t) --i;
+    ti = i;
+    tj = t - i * (i + 1) / 2;
+  } else {
+    ti = t / tiles_n;
+    tj = t - ti * tiles_n;
+  }
+}
+
+// Stores 4 values v of rows r..r+3, column c of a tile: transposed, they are 4
+// consecutive columns of row c.
+__device__ __forceinline__ void store_pair4(f16* out, int64_t row, int64_t col, int64_t kpad, const float* v) {
+  f16x4 hi, lo;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f16 h, l;
+    split(v[j], h, l);
+    hi[j] = h;
+    lo[j] = l;
+  }
+  f16* p = out + pair_at(row, col, kpad);
+  *reinterpret_cast<f16x4*>(p) = hi;
+  *reinterpret_cast<f16x4*>(p + 32) = lo;
+}
+__device__ __forceinline__ void store_pair1(f16* out, int64_t row, int64_t col, int64_t kpad, float v) {
+  f16 h, l;
+  split(v, h, l);
+  f16* p = out + pair_at(row, col, kpad);
+  p[0] = h;
+  p[32] = l;
+}
+
+// One result element of the last step, in the caller's orientation.
+template <class PT>
+__device__ __forceinline__ void store_result(const OrthArgs& o, int64_t batch, int64_t i, int64_t j, float v) {
+  if (o.rows > o.cols) {
+    const int64_t t = i;
+    i = j;
+    j = t;
+  }
+  if (i >= o.rows || j >= o.cols) return;
+  PT* out = reinterpret_cast<PT*>(o.out) + (batch * o.rows + i) * o.cols + j;
+  if (o.buffer)
+    *out = (PT)fmaf((float)*out, o.keep, -o.rate * v);
+  else
+    *out = (PT)v;
+}
+
+template <int T, int KIND, class PT>
+__device__ __forceinline__ void epilogue(const Product& p, int batch, int ti, int tj, f32x16 (&acc)[kFrag<T>][kFrag<T>]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const float* xs = p.o.scales + (int64_t)batch * (p.o.steps + 1) + p.step;
+  float f;
+  if constexpr (KIND == kGram)
+    f = p.sa / (xs[0] * xs[0]);
+  else if constexpr (KIND == kPoly)
+    f = p.o.c * p.sp / (p.sa * p.sa);
+  else if constexpr (KIND == kUpdate)
+    f = xs[1] / (p.sp * xs[0]);
+  else
+    f = 1.0f / (p.sp * xs[0]);
+  f16* out = p.out + (int64_t)batch * p.sOut;
+#pragma unroll
+  for (int fi = 0; fi < kFrag<T>; ++fi)
+#pragma unroll
+    for (int fj = 0; fj < kFrag<T>; ++fj) {
+      const int64_t j = (int64_t)tj * T + (wave & 1) * (T / 2) + fj * 32 + (lane & 31);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t i = (int64_t)ti * T + (wave >> 1) * (T / 2) + fi * 32 + q * 8 + (lane >> 5) * 4;
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = acc[fi][fj][q * 4 + r] * f;
+        if constexpr (KIND == kPoly) {
+          const f16* gp = p.gram + (int64_t)batch * p.sOut + pair_at(j, i, p.out_pad);
+          const f16x4 gh = *reinterpret_cast<const f16x4*>(gp), gl = *reinterpret_cast<const f16x4*>(gp + 32);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            v[r] = fmaf(p.o.b * p.sp / p.sa, (float)gh[r] + (float)gl[r], v[r]);
+            if (i + r == j) v[r] += p.o.a * p.sp;
+          }
+        }
+        if constexpr (KIND == kGram || KIND == kPoly) {
+          store_pair4(out, j, i, p.out_pad, v);
+          if (ti != tj)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) store_pair1(out, i + r, j, p.out_pad, v[r]);
+        } else if constexpr (KIND == kUpdate) {
+          store_pair4(p.outT + (int64_t)batch * p.sOut, j, i, p.outT_pad, v);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) store_pair1(out, i + r, j, p.out_pad, v[r]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) store_result<PT>(p.o, batch, i + r, j, v[r]);
+        }
+      }
+    }
+}
+
+// Loads one step (32 columns, T rows, 128 bytes a row) of an operand to LDS.
+// A wave's load covers 8 rows; the 16-byte chunk a lane fetches is permuted
+// within its row by the row's number, so that the fragment reads below, 8 rows
+// at one chunk, meet 8 different groups of banks.
+template <int T>
+__device__ __forceinline__ void load_step(const f16* base, int64_t pitch, int kstep, f16* lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r = lane >> 3, ch = (lane & 7) ^ r;
+#pragma unroll
+  for (int q = 0; q < T / 32; ++q) {
+    const int row0 = (wave * (T / 32) + q) * 8;
+    const f16* src = base + (int64_t)(row0 + r) * pitch + (int64_t)kstep * 64 + ch * 8;
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                     (__attribute__((address_space(3))) void*)(lds + row0 * 64), 16, 0, 0);
+  }
+}
+
+template <int T>
+__device__ __forceinline__ f16x8 fragment(const f16* lds, int row, int chunk) {
+  return *reinterpret_cast<const f16x8*>(lds + row * 64 + ((chunk ^ (row & 7)) << 3));
+}
+
+template <int T>
+__device__ __forceinline__ void multiply_step(const f16* la, const f16* lb, f32x16 (&acc)[kFrag<T>][kFrag<T>]) {
+  constexpr int F = kFrag<T>;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int ra = (wave >> 1) * (T / 2) + (lane & 31), rb = (wave & 1) * (T / 2) + (lane & 31);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int ch = s * 2 + (lane >> 5);
+    f16x8 ah[F], al[F], bh[F], bl[F];
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+      ah[i] = fragment<T>(la, ra + i * 32, ch);
+      bh[i] = fragment<T>(lb, rb + i * 32, ch);
+      al[i] = fragment<T>(la, ra + i * 32, ch + 4);
+      bl[i] = fragment<T>(lb, rb + i * 32, ch + 4);
+    }
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah[i], bh[j], acc[i][j], 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah[i], bl[j], acc[i][j], 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(al[i], bh[j], acc[i][j], 0, 0, 0);
+  }
+}
+
+// One tile of a product: grid (tiles x splits, batch).
+template <int T, int KIND, class PT>
+__global__ __launch_bounds__(kNT) void product_kernel(Product p) {
+  constexpr int F = kFrag<T>;
+  __shared__ __align__(16) f16 a0[T * 64], b0[T * 64], a1[T * 64], b1[T * 64];
+  const int tiles = gridDim.x / p.splits;
+  const int t = blockIdx.x % tiles, sp = blockIdx.x / tiles, batch = blockIdx.y;
+  int ti, tj;
+  tile_of(KIND == kGram || KIND == kPoly, t, p.tiles_n, ti, tj);
+  const int per = (p.ksteps + p.splits - 1) / p.splits;
+  const int k0 = sp * per, k1 = k0 + per < p.ksteps ? k0 + per : p.ksteps;
+  const int64_t pitch = 2 * p.kpad;
+  const f16* A = p.A + batch * p.sA + (int64_t)ti * T * pitch;
+  const f16* B = p.B + batch * p.sB + (int64_t)tj * T * pitch;
+  f32x16 acc[F][F];
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+#pragma unroll
+    for (int j = 0; j < F; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  if (k0 < k1) {
+    load_step<T>(A, pitch, k0, a0);
+    load_step<T>(B, pitch, k0, b0);
+  }
+  for (int k = k0; k < k1; k += 2) {
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (k + 1 < k1) {
+      load_step<T>(A, pitch, k + 1, a1);
+      load_step<T>(B, pitch, k + 1, b1);
+    }
+    multiply_step<T>(a0, b0, acc);
+    if (k + 1 < k1) {
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      if (k + 2 < k1) {
+        load_step<T>(A, pitch, k + 2, a0);
+        load_step<T>(B, pitch, k + 2, b0);
+      }
+      multiply_step<T>(a1, b1, acc);
+    }
+  }
+  if (p.splits > 1) {
+    float* out = p.part + (((int64_t)batch * tiles + t) * p.splits + sp) * (T * T) + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) out[((i * F + j) * 16 + r) * kNT] = acc[i][j][r];
+    return;
+  }
+  epilogue<T, KIND, PT>(p, batch, ti, tj, acc);
+}
+
+// Joins the shared sums of one tile, in order, and finishes it.
+template <int T, int KIND, class PT>
+__global__ __launch_bounds__(kNT) void finish_kernel(Product p) {
+  constexpr int F = kFrag<T>;
+  const int t = blockIdx.x, batch = blockIdx.y;
+  int ti, tj;
+  tile_of(KIND == kGram || KIND == kPoly, t, p.tiles_n, ti, tj);
+  f32x16 acc[F][F];
+  const float* in = p.part + ((int64_t)batch * gridDim.x + t) * p.splits * (T * T) + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+#pragma unroll
+    for (int j = 0; j < F; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        float s = 0.0f;
+        for (int q = 0; q < p.splits; ++q) s += in[(int64_t)q * (T * T) + ((i * F + j) * 16 + r) * kNT];
+        acc[i][j][r] = s;
+      }
+  epilogue<T, KIND, PT>(p, batch, ti, tj, acc);
+}
+
+int tile_count(bool sym, int tm, int tn) { return sym ? tm * (tm + 1) / 2 : tm * tn; }
+
+template <int T, int KIND, class PT>
+hipError_t launch_product_t(Product p, int64_t rows, int64_t cols, int64_t batch, hipStream_t s) {
+  const bool sym = KIND == kGram || KIND == kPoly;
+  p.tiles_m = (int)(rows / T);
+  p.tiles_n = (int)(cols / T);
+  const int tiles = tile_count(sym, p.tiles_m, p.tiles_n);
+  p.splits = orth_splits((int64_t)tiles * batch, p.ksteps);
+  hipLaunchKernelGGL((product_kernel<T, KIND, PT>), dim3((unsigned)(tiles * p.splits), (unsigned)batch), dim3(kNT), 0, s, p);
+  if (p.splits > 1)
+    hipLaunchKernelGGL((finish_kernel<T, KIND, PT>), dim3((unsigned)tiles, (unsigned)batch), dim3(kNT), 0, s, p);
+  return hipGetLastError();
+}
+
+template <int KIND, class PT>
+hipError_t launch_product(const Product& p, int64_t rows, int64_t cols, int64_t batch, hipStream_t s) {
+  const bool sym = KIND == kGram || KIND == kPoly;
+  if (orth_tile(rows, cols, batch, sym) == 64) return launch_product_t<64, KIND, PT>(p, rows, cols, batch, s);
+  return launch_product_t<128, KIND, PT>(p, rows, cols, batch, s);
+}
+
+template <class GT, class PT>
+hipError_t run(const OrthArgs& o, hipStream_t s) {
+  const OrthPlan w = orth_plan(o.batch, o.rows, o.cols);
+  OrthArgs a = o;
+  char* ws = reinterpret_cast<char*>(o.ws);
+  a.squares = reinterpret_cast<double*>(ws + w.at_squares);
+  a.scales = reinterpret_cast<float*>(ws + w.at_scales);
+  a.square_blocks = w.square_blocks;
+  f16* X[2] = {reinterpret_cast<f16*>(ws + w.at_x0), reinterpret_cast<f16*>(ws + w.at_x1)};
+  f16* XT[2] = {reinterpret_cast<f16*>(ws + w.at_xt0), reinterpret_cast<f16*>(ws + w.at_xt1)};
+  f16* A = reinterpret_cast<f16*>(ws + w.at_a);
+  f16* P = reinterpret_cast<f16*>(ws + w.at_p);
+  float* part = reinterpret_cast<float*>(ws + w.at_part);
+
+  hipLaunchKernelGGL((orth_square_kernel<GT>), dim3((unsigned)w.square_blocks, (unsigned)a.batch), dim3(kNT), 0, s, a);
+  const bool tall = a.rows > a.cols;
+  const int64_t rpad = tall ? w.npad : w.mpad, cpad = tall ? w.mpad : w.npad;
+  hipLaunchKernelGGL((orth_prepare_kernel<GT>), dim3((unsigned)(cpad / 64), (unsigned)(rpad / 64), (unsigned)a.batch),
+                     dim3(kNT), 0, s, a, tall ? XT[0] : X[0], tall ? X[0] : XT[0], rpad, cpad);
+  const int64_t sx = w.mpad * w.npad * 2, sm = w.mpad * w.mpad * 2;
+  for (int k = 0; k < a.steps; ++k) {
+    const int in = k & 1, on = 1 - in;
+    Product p{};
+    p.o = a;
+    p.step = k;
+    p.sa = a.sa;
+    p.sp = a.sp;
+    p.part = part;
+    p.A = p.B = X[in];
+    p.sA = p.sB = sx;
+    p.kpad = w.npad;
+    p.ksteps = (int)((w.n + 31) / 32);
+    p.out = A;
+    p.sOut = sm;
+    p.out_pad = w.mpad;
+    hipError_t e = launch_product<kGram, float>(p, w.mpad, w.mpad, a.batch, s);
+    if (e != hipSuccess) return e;
+    p.A = p.B = p.gram = A;
+    p.sA = p.sB = sm;
+    p.kpad = w.mpad;
+    p.ksteps = (int)((w.m + 31) / 32);
+    p.out = P;
+    e = launch_product<kPoly, float>(p, w.mpad, w.mpad, a.batch, s);
+    if (e != hipSuccess) return e;
+    p.A = P;
+    p.B = XT[in];
+    p.sB = sx;
+    p.out = X[on];
+    p.outT = XT[on];
+    p.sOut = sx;
+    p.out_pad = w.npad;
+    p.outT_pad = w.mpad;
+    e = k + 1 < a.steps ? launch_product<kUpdate, float>(p, w.mpad, w.npad, a.batch, s)
+                        : launch_product<kLast, PT>(p, w.mpad, w.npad, a.batch, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <class GT>
+hipError_t run_out(const OrthArgs& o, int odtype, hipStream_t s) {
+  if (odtype == kTF32) return run<GT, float>(o, s);
+  if (odtype == kTF16) return run<GT, f16>(o, s);
+  return run<GT, bf16>(o, s);
+}
+
+}  // namespace
+
+hipError_t launch_orth(const OrthArgs& o, hipStream_t s) {
+  if (o.gdtype == kTF32) return run_out<float>(o, o.odtype, s);
+  if (o.gdtype == kTF16) return run_out<f16>(o, o.odtype, s);
+  return run_out<bf16>(o, o.odtype, s);
+}
+
+}  // namespace ecc

@@ -98,7 +98,64 @@ int run_bwd(const ecc::NormArgs& a, int dtype, void* stream) {
   return hip_status(ecc::norm_launch_bwd<ecc::bf16>(a, s));
 }
 
+int check_matrix(int64_t B, int64_t rows, int64_t cols) {
+  if (B < 1 || rows < 1 || cols < 1)
+    return fail(ECC_E_SHAPE, "batch, rows and cols must be >= 1 (got rows=%lld cols=%lld)", rows, cols);
+  if (B > ECC_MAX_NORM_BATCH) return fail(ECC_E_SHAPE, "batch=%lld exceeds %lld", B, ECC_MAX_NORM_BATCH);
+  if (rows > ECC_MAX_MATRIX || cols > ECC_MAX_MATRIX)
+    return fail(ECC_E_SHAPE, "a matrix of %lld x %lld exceeds the limit per side", rows, cols);
+  if (B > ECC_MAX_VOXELS / (rows * cols)) return fail(ECC_E_SHAPE, "more than 2^40 elements");
+  return ECC_OK;
+}
+
+// Checks shared by the two matrix calls, once sizes, types and coefficients are in o.
+int check_orth(ecc::OrthArgs& o, size_t ws_bytes) {
+  if (!is_dtype(o.gdtype) || !is_dtype(o.odtype))
+    return fail(ECC_E_DTYPE, "dtypes %lld, %lld are not both of ECC_T_*", o.gdtype, o.odtype);
+  int st = check_matrix(o.batch, o.rows, o.cols);
+  if (st != ECC_OK) return st;
+  if (o.steps < 1 || o.steps > ECC_MAX_NS_STEPS)
+    return fail(ECC_E_VALUE, "steps=%lld outside [1, %lld]", o.steps, ECC_MAX_NS_STEPS);
+  st = check_eps(o.eps);
+  if (st != ECC_OK) return st;
+  if (!isfinite(o.a) || !isfinite(o.b) || !isfinite(o.c)) return fail(ECC_E_VALUE, "coefficients must be finite");
+  if (!ecc::orth_bounds(o))
+    return fail(ECC_E_VALUE, "under these coefficients singular values in [0, 1] leave [-16, 16]");
+  return check_workspace(o.ws, ws_bytes, ecc::orth_plan(o.batch, o.rows, o.cols).bytes);
+}
+
 }  // namespace
+
+namespace ecc {
+
+bool orth_bounds(OrthArgs& o) {
+  // 256 samples of the attained range; 2 % covers what lies between them
+  constexpr int kSamples = 256;
+  double r = 1.0, pmax = 0.0, gram = 0.0, cap = 1.0;
+  for (int k = 0; k < o.steps; ++k) {
+    double f = 0.0, q = 0.0;
+    for (int i = 0; i <= kSamples; ++i) {
+      const double x = r * i / kSamples, p = o.a + x * x * (o.b + x * x * o.c);
+      f = fmax(f, fabs(p * x));
+      q = fmax(q, fabs(p));
+    }
+    gram = fmax(gram, r * r);
+    pmax = fmax(pmax, 1.02 * q);
+    r = 1.02 * f;
+    cap = fmax(cap, r);
+    if (!(cap <= 16.0) || !(pmax <= 4096.0)) return false;
+  }
+  int e;
+  frexp(gram, &e);
+  o.sa = ldexpf(1.0f, 14 - e);
+  frexp(fmax(pmax, 1e-30), &e);
+  o.sp = ldexpf(1.0f, 14 - e);
+  o.growth = (float)pmax;
+  o.cap = (float)cap;
+  return true;
+}
+
+}  // namespace ecc
 
 extern "C" {
 
@@ -179,6 +236,68 @@ int ecc_norm_readout_bwd(const void* x, int dtype, int64_t batch, int64_t voxels
   a.gr = grad_readout;
   a.go = grad_offset;
   return run_bwd(a, dtype, stream);
+}
+
+size_t ecc_orth_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
+  if (check_matrix(batch, rows, cols) != ECC_OK) return 0;
+  return ecc::orth_plan(batch, rows, cols).bytes;
+}
+
+int ecc_orthogonalize(const void* g, int dtype, int64_t batch, int64_t rows, int64_t cols, int32_t steps, float eps,
+                      float a, float b, float c, void* out, void* ws, size_t ws_bytes, void* stream) {
+  ecc::set_error("");
+  if (!g) return fail(ECC_E_NULL, "g is NULL");
+  if (!out) return fail(ECC_E_NULL, "out is NULL");
+  ecc::OrthArgs o{};
+  o.g = g;
+  o.gdtype = o.odtype = dtype;
+  o.batch = batch;
+  o.rows = rows;
+  o.cols = cols;
+  o.out = out;
+  o.steps = steps;
+  o.eps = eps;
+  o.a = a;
+  o.b = b;
+  o.c = c;
+  o.ws = ws;
+  const int st = check_orth(o, ws_bytes);
+  if (st != ECC_OK) return st;
+  return hip_status(ecc::launch_orth(o, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int ecc_muon_step(void* param, int pdtype, const void* grad, int gdtype, float* buffer, int64_t batch, int64_t rows,
+                  int64_t cols, double lr, double momentum, int nesterov, double weight_decay, double scale,
+                  int32_t steps, float eps, float a, float b, float c, void* ws, size_t ws_bytes, void* stream) {
+  ecc::set_error("");
+  if (!param) return fail(ECC_E_NULL, "param is NULL");
+  if (!grad) return fail(ECC_E_NULL, "grad is NULL");
+  if (!buffer) return fail(ECC_E_NULL, "buffer is NULL");
+  if (!isfinite(lr) || !isfinite(momentum) || !isfinite(weight_decay) || !isfinite(scale))
+    return fail(ECC_E_VALUE, "lr, momentum, weight_decay and scale must be finite");
+  ecc::OrthArgs o{};
+  o.g = grad;
+  o.gdtype = gdtype;
+  o.odtype = pdtype;
+  o.batch = batch;
+  o.rows = rows;
+  o.cols = cols;
+  o.out = param;
+  o.buffer = buffer;
+  o.momentum = (float)momentum;
+  o.blend = (float)(1.0 - momentum);
+  o.nesterov = nesterov != 0;
+  o.keep = (float)(1.0 - lr * weight_decay);
+  o.rate = (float)(lr * scale);
+  o.steps = steps;
+  o.eps = eps;
+  o.a = a;
+  o.b = b;
+  o.c = c;
+  o.ws = ws;
+  const int st = check_orth(o, ws_bytes);
+  if (st != ECC_OK) return st;
+  return hip_status(ecc::launch_orth(o, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

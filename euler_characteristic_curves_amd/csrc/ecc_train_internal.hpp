@@ -55,4 +55,93 @@ hipError_t norm_launch_fwd(const NormArgs& a, hipStream_t stream);
 template <class T>
 hipError_t norm_launch_bwd(const NormArgs& a, hipStream_t stream);
 
+// ------------------------------------------------- orthogonalised updates
+struct OrthArgs {
+  const void* g;  // gradient, [batch][rows][cols]
+  int gdtype;
+  int64_t batch, rows, cols;
+  void* out;      // orthogonalised matrix, or the parameter when buffer is set
+  int odtype;
+  float* buffer;  // momentum, or null
+  float momentum, blend;  // blend = 1 - momentum
+  int nesterov;
+  float keep, rate;  // parameter <- keep parameter - rate orthogonal
+  int steps;
+  float eps, a, b, c;
+  // bounds of the iteration (orth_bounds): ||X|| <= min(growth^k, cap), and
+  // the scales of the pairs that hold A = X X^T and P
+  float growth, cap, sa, sp;
+  void* ws;
+  // set by the launcher
+  double* squares;
+  int square_blocks;
+  float* scales;  // [batch][steps + 1]: 2^s of X before each step
+};
+
+// What the coefficients do to singular values in [0, 1]: fills growth, cap,
+// sa, sp.  False where they leave [-16, 16] or are not finite.
+bool orth_bounds(OrthArgs& o);
+
+inline int64_t orth_pad(int64_t n) { return n <= 64 ? 64 : (n + 127) / 128 * 128; }
+
+// Tile of a product with `rows` x `cols` (padded) results.
+inline int orth_tile(int64_t rows, int64_t cols, int64_t batch, bool sym) {
+  if (rows < 128 || cols < 128) return 64;
+  const int64_t tm = rows / 128, tn = cols / 128, tiles = (sym ? tm * (tm + 1) / 2 : tm * tn) * batch;
+  return tiles >= 96 ? 128 : 64;
+}
+// Workgroups that share the summed axis of a tile: enough of them for every
+// CU, each with at least 8 steps of 32 columns.
+inline int orth_splits(int64_t tiles, int ksteps) {
+  int64_t s = 256 / tiles, most = ksteps / 8;
+  s = s < most ? s : most;
+  return s < 1 ? 1 : (int)s;
+}
+inline size_t orth_part_bytes(int64_t rows, int64_t cols, int64_t batch, bool sym, int64_t k) {
+  const int64_t T = orth_tile(rows, cols, batch, sym), tm = rows / T, tn = cols / T;
+  const int64_t tiles = (sym ? tm * (tm + 1) / 2 : tm * tn) * batch;
+  const int s = orth_splits(tiles, (int)((k + 31) / 32));
+  return s > 1 ? (size_t)(tiles * s * T * T) * sizeof(float) : 0;
+}
+
+// Workspace: offsets in bytes.
+struct OrthPlan {
+  int64_t m, n, mpad, npad;
+  int square_blocks;
+  size_t at_squares, at_scales, at_x0, at_x1, at_xt0, at_xt1, at_a, at_p, at_part, bytes;
+};
+inline OrthPlan orth_plan(int64_t batch, int64_t rows, int64_t cols) {
+  OrthPlan w{};
+  w.m = rows < cols ? rows : cols;
+  w.n = rows < cols ? cols : rows;
+  w.mpad = orth_pad(w.m);
+  w.npad = orth_pad(w.n);
+  int64_t sb = (w.m * w.n + 8191) / 8192, most = (1024 + batch - 1) / batch;
+  w.square_blocks = (int)(sb < most ? sb : most);
+  size_t at = 0;
+  auto take = [&at](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) & ~(size_t)255;
+    return here;
+  };
+  const size_t x = (size_t)batch * w.mpad * w.npad * 4, mm = (size_t)batch * w.mpad * w.mpad * 4;
+  w.at_squares = take((size_t)batch * w.square_blocks * sizeof(double));
+  w.at_scales = take((size_t)batch * 65 * sizeof(float));
+  w.at_x0 = take(x);
+  w.at_x1 = take(x);
+  w.at_xt0 = take(x);
+  w.at_xt1 = take(x);
+  w.at_a = take(mm);
+  w.at_p = take(mm);
+  const size_t g = orth_part_bytes(w.mpad, w.mpad, batch, true, w.n);
+  const size_t q = orth_part_bytes(w.mpad, w.mpad, batch, true, w.m);
+  const size_t u = orth_part_bytes(w.mpad, w.npad, batch, false, w.m);
+  const size_t part = g > q ? (g > u ? g : u) : (q > u ? q : u);
+  w.at_part = take(part);
+  w.bytes = at;
+  return w;
+}
+
+hipError_t launch_orth(const OrthArgs& o, hipStream_t stream);
+
 }  // namespace ecc

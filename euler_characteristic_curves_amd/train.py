@@ -14,7 +14,8 @@ from . import _lib
 from ._lib import EccError, check, lib
 from .ecc import _dev_tensor, _ptr, _stream
 
-__all__ = ["group_norm_act", "group_norm_readout", "GroupNormAct", "GroupNormReadout", "EccError"]
+__all__ = ["group_norm_act", "group_norm_readout", "GroupNormAct", "GroupNormReadout", "orthogonalize", "muon_step",
+           "EccError"]
 
 _DTYPES = {torch.float32: _lib.ECC_T_F32, torch.float16: _lib.ECC_T_F16, torch.bfloat16: _lib.ECC_T_BF16}
 _ACTS = {"none": _lib.ECC_ACT_NONE, "relu": _lib.ECC_ACT_RELU, "silu": _lib.ECC_ACT_SILU, "gelu": _lib.ECC_ACT_GELU}
@@ -199,3 +200,95 @@ def group_norm_readout(x, groups, weight, bias, readout, offset=None, act="none"
         return GroupNormReadout.apply(x, weight, bias, readout, offset, groups, act, eps)
     return _NormCall(x.contiguous(), groups, _contiguous(weight), _contiguous(bias), act, _contiguous(readout),
                      _contiguous(offset), with_readout=True).forward(eps)[0]
+
+
+# ------------------------------------------------- orthogonalised updates
+_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _matrix_sizes(t, name):
+    """(batch, rows, cols) of a matrix or a stack of matrices."""
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [rows, cols] or [batch, rows, cols] (got {list(t.shape)})")
+    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+
+
+def _matrix_dtype(t, name):
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} dtype {t.dtype} not supported (float32, float16 or bfloat16)")
+    return _DTYPES[t.dtype]
+
+
+def _orth_bytes(sizes):
+    nbytes = lib.ecc_orth_workspace_bytes(*sizes)
+    if not nbytes:
+        raise EccError(_lib.ECC_E_SHAPE, "orthogonalize: " + lib.ecc_last_error().decode(errors="replace"))
+    return nbytes
+
+
+def _polynomial(coefficients):
+    a, b, c = coefficients
+    return float(a), float(b), float(c)
+
+
+def orthogonalize(g, steps=5, eps=1e-7, coefficients=_COEFFICIENTS, out=None):
+    """The Newton-Schulz iterate of a matrix, or of each matrix of a stack (see ecc_orthogonalize in
+    include/ecc_train.h): g with its singular values driven towards 1.  Not differentiable.
+
+    g: float32, float16 or bfloat16, [rows, cols] or [batch, rows, cols]; out: a tensor like g (g itself allowed).
+    """
+    g = g.detach()
+    if out is None:
+        g = g.contiguous()
+    _dev_tensor(g, "g")
+    dtype, sizes = _matrix_dtype(g, "g"), _matrix_sizes(g, "g")
+    if out is None:
+        out = torch.empty_like(g)
+    _dev_tensor(out, "out", g.dtype, g.device)
+    if out.shape != g.shape:
+        raise ValueError("out must have g's shape")
+    a, b, c = _polynomial(coefficients)
+    if not g.numel():
+        return out
+    with _on_device(g):
+        nbytes = _orth_bytes(sizes)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=g.device)
+        check(lib.ecc_orthogonalize(_ptr(g), dtype, *sizes, int(steps), float(eps), a, b, c, _ptr(out), _ptr(ws), nbytes,
+                                    _stream(g).cuda_stream), "ecc_orthogonalize")
+    return out
+
+
+def muon_step(params, grads, buffers, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=None, steps=5, eps=1e-7,
+              coefficients=_COEFFICIENTS):
+    """One step of momentum with orthogonalised updates, in place on ``params`` and ``buffers`` (see ecc_muon_step in
+    include/ecc_train.h).
+
+    params, grads, buffers: sequences of one length; entry i of each is [rows, cols] or a stack [batch, rows, cols] of
+    matrices (layers of one shape), contiguous; buffers are float32.  scale: factor of the update, by default
+    sqrt(max(1, rows / cols)).  Every argument is checked before anything is changed.
+    """
+    params, grads, buffers = list(params), list(grads), list(buffers)
+    if not len(params) == len(grads) == len(buffers):
+        raise ValueError(f"{len(params)} params, {len(grads)} grads, {len(buffers)} buffers")
+    a, b, c = _polynomial(coefficients)
+    calls = []
+    for p, g, m in zip(params, grads, buffers):
+        _dev_tensor(p, "param")
+        _dev_tensor(g, "grad", None, p.device)
+        _dev_tensor(m, "buffer", torch.float32, p.device)
+        sizes = _matrix_sizes(p, "param")
+        if g.shape != p.shape or m.shape != p.shape:
+            raise ValueError(f"param {list(p.shape)}, grad {list(g.shape)} and buffer {list(m.shape)} must agree")
+        calls.append((p, _matrix_dtype(p, "param"), g, _matrix_dtype(g, "grad"), m, sizes,
+                      _orth_bytes(sizes) if p.numel() else 0))
+    for p, pdtype, g, gdtype, m, sizes, nbytes in calls:
+        if not nbytes:
+            continue
+        s = float(scale) if scale is not None else max(1.0, sizes[1] / sizes[2]) ** 0.5
+        with _on_device(p):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=p.device)
+            check(lib.ecc_muon_step(_ptr(p), pdtype, _ptr(g), gdtype, _ptr(m), *sizes, float(lr), float(momentum),
+                                    1 if nesterov else 0, float(weight_decay), s, int(steps), float(eps), a, b, c,
+                                    _ptr(ws), nbytes, _stream(p).cuda_stream), "ecc_muon_step")
+        torch.autograd.graph.increment_version(p)
+        torch.autograd.graph.increment_version(m)

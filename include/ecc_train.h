@@ -107,6 +107,39 @@ int ecc_norm_readout_bwd(const void* x, int dtype, int64_t batch, int64_t voxels
 /* Workspace bytes of the four calls above (0 for invalid sizes). */
 size_t ecc_norm_workspace_bytes(int64_t batch, int64_t voxels, int64_t channels, int64_t groups);
 
+/*
+ * Newton-Schulz orthogonalisation of a stack of matrices g[batch][rows][cols]
+ * (dtype), each on its own: X = g / (|g|_F + eps), then `steps` times
+ *   A = X X^T,  X <- a X + (b A + c A A) X
+ * (with X^T in place of X where rows > cols), written to out (dtype, g's
+ * shape; may be g itself).  The singular vectors stay, the singular values are
+ * driven towards 1 by the polynomial a s + b s^3 + c s^5.
+ * The norm is summed in float64; products take operands of 22 significant bits
+ * (pairs of float16) and sum in float32, so the result is that of float32
+ * arithmetic, rounded once to dtype.
+ * Refused with ECC_E_VALUE: steps outside [1, ECC_MAX_NS_STEPS], eps < 0, a
+ * coefficient that is not finite, and coefficients under which a singular
+ * value in [0, 1] leaves [-16, 16] within the steps.
+ */
+int ecc_orthogonalize(const void* g, int dtype, int64_t batch, int64_t rows, int64_t cols, int32_t steps, float eps,
+                      float a, float b, float c, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Momentum, orthogonalisation and update of a stack of matrices, in place:
+ *   buffer <- momentum buffer + (1 - momentum) grad               (float32)
+ *   u = nesterov ? momentum buffer + (1 - momentum) grad : buffer
+ *   param <- (1 - lr weight_decay) param - lr scale orthogonalize(u)
+ * param: pdtype, grad: gdtype, buffer: float32, all [batch][rows][cols].
+ * Refused with ECC_E_VALUE besides the above: lr, momentum, weight_decay or
+ * scale not finite.
+ */
+int ecc_muon_step(void* param, int pdtype, const void* grad, int gdtype, float* buffer, int64_t batch, int64_t rows,
+                  int64_t cols, double lr, double momentum, int nesterov, double weight_decay, double scale,
+                  int32_t steps, float eps, float a, float b, float c, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of the two calls above (0 for invalid sizes). */
+size_t ecc_orth_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+
 #ifdef __cplusplus
 }
 #endif

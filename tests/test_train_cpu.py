@@ -133,3 +133,35 @@ def test_reference_gradients_agree_with_differences(act, readout):
         along = float((got[name][0] * d).sum())
         # float64 rounding over the step (1e-16 / 1e-5 a term, some hundred terms) and the step's square
         assert abs(slope - along) <= 1e-7 * (1 + float((got[name][0] * d).abs().sum())), name
+
+
+def orth(L, g=FAKE, dtype=0, B=2, rows=30, cols=40, steps=5, eps=1e-7, co=(3.4445, -4.775, 2.0315), out=FAKE, ws=FAKE,
+         wsb=1 << 40):
+    return L.lib.ecc_orthogonalize(g, dtype, B, rows, cols, steps, eps, *co, out, ws, wsb, None)
+
+
+def muon(L, g=FAKE, dtype=0, B=2, rows=30, cols=40, steps=5, eps=1e-7, co=(3.4445, -4.775, 2.0315), out=FAKE, ws=FAKE,
+         wsb=1 << 40, buffer=FAKE, lr=0.1, momentum=0.9, decay=0.0, scale=1.0):
+    return L.lib.ecc_muon_step(out, 0, g, dtype, buffer, B, rows, cols, lr, momentum, 1, decay, scale, steps, eps, *co,
+                               ws, wsb, None)
+
+
+@pytest.mark.parametrize("call", [orth, muon], ids=["orth", "muon"])
+def test_matrix_argument_errors(L, call):
+    assert call(L, g=None) == L.ECC_E_NULL and call(L, out=None) == L.ECC_E_NULL
+    assert call(L, dtype=3) == L.ECC_E_DTYPE
+    for bad in (dict(B=0), dict(rows=0), dict(cols=-1), dict(rows=32769), dict(cols=32769), dict(B=32769),
+                dict(B=32768, rows=32768, cols=32768)):
+        assert call(L, **bad) == L.ECC_E_SHAPE, bad
+    nan, inf = float("nan"), float("inf")
+    for bad in (dict(steps=0), dict(steps=65), dict(eps=-1.0), dict(eps=nan), dict(co=(nan, 0, 0)), dict(co=(1, inf, 0)),
+                dict(co=(20.0, 0.0, 0.0)), dict(co=(3.0, 0.0, 0.0))):
+        assert call(L, **bad) == L.ECC_E_VALUE, bad
+        assert L.lib.ecc_last_error()
+    assert call(L, ws=None) == L.ECC_E_WORKSPACE
+    assert call(L, wsb=L.lib.ecc_orth_workspace_bytes(2, 30, 40) - 1) == L.ECC_E_WORKSPACE
+    assert L.lib.ecc_orth_workspace_bytes(0, 30, 40) == 0 and L.lib.ecc_orth_workspace_bytes(1, 0, 40) == 0
+    if call is muon:
+        assert call(L, buffer=None) == L.ECC_E_NULL
+        for bad in (dict(lr=nan), dict(momentum=inf), dict(decay=nan), dict(scale=inf)):
+            assert call(L, **bad) == L.ECC_E_VALUE, bad
