@@ -45,16 +45,20 @@ struct NormGeom {
   int chunks;  // column chunks of 64 vectors (rows of more than 4 x 64 vectors)
 };
 
-// A lane's columns.
+// A lane's columns, and its rows: the waves of a launch sweep the rows as one
+// window, in which every wave has U neighbouring steps of floor(64 / L) rows,
+// so that what is in flight lies close together in memory (a read of 1.07 GB
+// took 175 us so, and 202 us with a wave's steps a window apart).
 template <int V, int K>
 struct Cols {
   int c[K];      // first channel of vector k
   int dup[K];    // leading elements that belong to another vector (V: none is its own)
-  int64_t first, stride;
-  int l;
+  int64_t wave_id, waves;
+  int l, sub, rows;
   __device__ Cols(const NormGeom& g) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int sub = lane / g.L, rows = 64 / g.L;
+    sub = lane / g.L;
+    rows = 64 / g.L;
     l = lane - sub * g.L;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -68,28 +72,34 @@ struct Cols {
         dup[k] = V;
       }
     }
-    const int64_t w = (int64_t)blockIdx.x * kNW + wave;
-    stride = (int64_t)g.NB * kNW * rows;
-    first = sub < rows ? w * rows + sub : g.S;
+    wave_id = (int64_t)blockIdx.x * kNW + wave;
+    waves = (int64_t)g.NB * kNW;
+  }
+  // The first of U rows, `rows` apart, of turn t.
+  template <int U>
+  __device__ __forceinline__ int64_t row(int64_t t) const {
+    return (t * waves + wave_id) * (U * rows) + sub;
   }
 };
 
 template <int K>
 constexpr int kUnroll = K == 1 ? 4 : (K == 2 ? 2 : 1);
 
-// Calls body(row...) for the rows of this lane: U at a time, then one by one.
-// body<N> gets an array of N row indexes.
-template <int U, class Body>
-__device__ __forceinline__ void for_rows(int64_t first, int64_t stride, int64_t S, Body body) {
-  int64_t r = first;
-  for (; r + (U - 1) * stride < S; r += U * stride) {
+// Calls body(row...) for the rows of this lane: U at a time, and one by one at
+// the end.  body<N> gets an array of N row indexes.
+template <int U, int V, int K, class Body>
+__device__ __forceinline__ void for_rows(const Cols<V, K>& col, int64_t S, Body body) {
+  if (col.sub >= col.rows) return;
+  int64_t r = col.template row<U>(0);
+  const int64_t step = col.waves * (U * col.rows);
+  for (; r + (U - 1) * col.rows < S; r += step) {
     int64_t rows[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) rows[i] = r + i * stride;
+    for (int i = 0; i < U; ++i) rows[i] = r + i * col.rows;
     body(rows, std::integral_constant<int, U>());
   }
   if constexpr (U > 1) {
-    for (; r < S; r += stride) {
+    for (; r < S; r += col.rows) {
       int64_t rows[1] = {r};
       body(rows, std::integral_constant<int, 1>());
     }
@@ -154,7 +164,8 @@ __global__ __launch_bounds__(kNT) void norm_stats_kernel(NormGeom g, const T* x,
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     Vec<T, V> v = {};
-    if (col.first < g.S) load_vec(xs + col.first * g.C + col.c[k], v);
+    const int64_t r0 = col.template row<kUnroll<K>>(0);
+    if (col.sub < col.rows && r0 < g.S) load_vec(xs + r0 * g.C + col.c[k], v);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       piv[k][j] = (float)v.v[j];
@@ -162,7 +173,7 @@ __global__ __launch_bounds__(kNT) void norm_stats_kernel(NormGeom g, const T* x,
     }
   }
   int64_t n = 0;
-  for_rows<kUnroll<K>>(col.first, col.stride, g.S, [&](const int64_t* rows, auto U) {
+  for_rows<kUnroll<K>>(col, g.S, [&](const int64_t* rows, auto U) {
     Vec<T, V> v[U.value][K];
 #pragma unroll
     for (int i = 0; i < U.value; ++i)
@@ -186,9 +197,14 @@ __global__ __launch_bounds__(kNT) void norm_stats_kernel(NormGeom g, const T* x,
   });
 }
 
-// What the passes after the statistics keep per channel.
-template <int V, int K>
+// What the passes after the statistics keep per channel.  Float32 features are
+// centred before they are scaled, so that a group that is constant, or nearly
+// so, keeps its digits.  16-bit features have far fewer of them, and take u = x
+// a + b with the mean in b: its error, half a step of mean a, is 2^-12 of what
+// their own rounding left of x a, and the passes are bound by issue there.
+template <class T, int V, int K>
 struct Affine {
+  static constexpr bool kFold = sizeof(T) == 2;
   float mean[K][V], a[K][V], b[K][V];
   __device__ void load(const NormArgs& p, const Cols<V, K>& col, int D) {
     const float* st = p.stats + (int64_t)blockIdx.y * p.G * 2;
@@ -200,20 +216,23 @@ struct Affine {
         mean[k][j] = st[2 * gr];
         a[k][j] = st[2 * gr + 1] * load_param(p.weight, p.pdtype, c, 1.0f);
         b[k][j] = load_param(p.bias, p.pdtype, c, 0.0f);
+        if constexpr (kFold) b[k][j] = fmaf(-mean[k][j], a[k][j], b[k][j]);
       }
   }
-  __device__ __forceinline__ float u(int k, int j, float x) const { return fmaf(x - mean[k][j], a[k][j], b[k][j]); }
+  __device__ __forceinline__ float u(int k, int j, float x) const {
+    return fmaf(kFold ? x : x - mean[k][j], a[k][j], b[k][j]);
+  }
 };
 
 template <class T, int V, int K, int ACT>
 __global__ __launch_bounds__(kNT) void norm_apply_kernel(NormGeom g, NormArgs p, int D) {
   Cols<V, K> col(g);
-  Affine<V, K> af;
+  Affine<T, V, K> af;
   af.load(p, col, D);
   const int64_t base = (int64_t)blockIdx.y * g.S * g.C;
   const T* xs = reinterpret_cast<const T*>(p.x) + base;
   T* ys = reinterpret_cast<T*>(p.y) + base;
-  for_rows<kUnroll<K>>(col.first, col.stride, g.S, [&](int64_t* rows, auto U) {
+  for_rows<kUnroll<K>>(col, g.S, [&](int64_t* rows, auto U) {
     Vec<T, V> v[U.value][K];
 #pragma unroll
     for (int i = 0; i < U.value; ++i) {
@@ -245,7 +264,7 @@ __device__ __forceinline__ float row_sum(float s, int l, int L) {
 template <class T, int V, int K, int ACT>
 __global__ __launch_bounds__(kNT) void readout_apply_kernel(NormGeom g, NormArgs p, int D) {
   Cols<V, K> col(g);
-  Affine<V, K> af;
+  Affine<T, V, K> af;
   af.load(p, col, D);
   float r[K][V];
 #pragma unroll
@@ -257,16 +276,15 @@ __global__ __launch_bounds__(kNT) void readout_apply_kernel(NormGeom g, NormArgs
   float* fs = p.field + (int64_t)blockIdx.y * g.S;
   // the lanes of a wave stay together for the shuffles: rows past the end are
   // computed from the first row and not stored
-  const int rows_wave = 64 / g.L;
   constexpr int U = kUnroll<K>;
-  const int64_t wfirst = ((int64_t)blockIdx.x * kNW + (threadIdx.x >> 6)) * rows_wave;
-  for (int64_t w = wfirst; w < g.S; w += U * col.stride) {
+  const int64_t step = col.waves * (U * col.rows);
+  for (int64_t w = col.wave_id * (U * col.rows); w < g.S; w += step) {
     Vec<T, V> v[U][K];
     int64_t row[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t at = col.first + (w - wfirst) + i * col.stride;
-      row[i] = at < g.S ? g.S - 1 - at : -1;
+      const int64_t at = w + i * col.rows + col.sub;
+      row[i] = at < g.S && col.sub < col.rows ? g.S - 1 - at : -1;
       const int64_t from = row[i] < 0 ? 0 : row[i];
 #pragma unroll
       for (int k = 0; k < K; ++k) load_vec(xs + from * g.C + col.c[k], v[i][k]);
@@ -291,7 +309,7 @@ __global__ __launch_bounds__(kNT) void norm_sums_kernel(NormGeom g, NormArgs p, 
   constexpr int NV = READ ? 3 : 2;
   __shared__ double lds[kSumElems<V> * NV * kNT];
   Cols<V, K> col(g);
-  Affine<V, K> af;
+  Affine<T, V, K> af;
   af.load(p, col, D);
   const int64_t base = (int64_t)blockIdx.y * g.S * g.C;
   const T* xs = reinterpret_cast<const T*>(p.x) + base;
@@ -306,7 +324,7 @@ __global__ __launch_bounds__(kNT) void norm_sums_kernel(NormGeom g, NormArgs p, 
       for (int i = 0; i < NV; ++i) s[k][j][i] = 0.0f;
   float sdf = 0.0f;
   constexpr int U = READ ? kUnroll<K> : (kUnroll<K> + 1) / 2;
-  for_rows<U>(col.first, col.stride, g.S, [&](const int64_t* rows, auto N) {
+  for_rows<U>(col, g.S, [&](const int64_t* rows, auto N) {
     Vec<T, V> v[N.value][K], q[N.value][K];
     float df[N.value];
 #pragma unroll
@@ -325,9 +343,9 @@ __global__ __launch_bounds__(kNT) void norm_sums_kernel(NormGeom g, NormArgs p, 
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float d = (float)v[i][k].v[j] - af.mean[k][j];
+          const float x = (float)v[i][k].v[j], d = x - af.mean[k][j];
           float y;
-          const float sl = act_slope<ACT>(fmaf(d, af.a[k][j], af.b[k][j]), y);
+          const float sl = act_slope<ACT>(af.u(k, j, x), y);
           float dy;
           if constexpr (READ) dy = df[i]; else dy = (float)q[i][k].v[j];
           const float du = dy * sl;
@@ -376,7 +394,7 @@ __global__ __launch_bounds__(kNT) void norm_grad_kernel(NormGeom g, NormArgs p, 
     return;
   }
   Cols<V, K> col(g);
-  Affine<V, K> af;
+  Affine<T, V, K> af;
   af.load(p, col, D);
   float c0[K][V], c1[K][V], ar[K][V];
 #pragma unroll
@@ -385,8 +403,8 @@ __global__ __launch_bounds__(kNT) void norm_grad_kernel(NormGeom g, NormArgs p, 
     for (int j = 0; j < V; ++j) {
       const int c = col.c[k] + j;
       const int64_t gr = (int64_t)blockIdx.y * p.G + (unsigned)c / (unsigned)D;
-      c0[k][j] = coef[2 * gr];
       c1[k][j] = coef[2 * gr + 1];
+      c0[k][j] = af.kFold ? fmaf(af.mean[k][j], c1[k][j], -coef[2 * gr]) : -coef[2 * gr];
       ar[k][j] = READ ? af.a[k][j] * load_param(p.readout, p.pdtype, c, 0.0f) : af.a[k][j];
     }
   const int64_t base = (int64_t)blockIdx.y * g.S * g.C;
@@ -395,7 +413,7 @@ __global__ __launch_bounds__(kNT) void norm_grad_kernel(NormGeom g, NormArgs p, 
   const float* fs = READ ? reinterpret_cast<const float*>(p.gy) + (int64_t)blockIdx.y * g.S : nullptr;
   T* os = reinterpret_cast<T*>(p.gx) + base;
   constexpr int U = READ ? kUnroll<K> : (kUnroll<K> + 1) / 2;
-  for_rows<U>(col.first, col.stride, g.S, [&](int64_t* rows, auto N) {
+  for_rows<U>(col, g.S, [&](int64_t* rows, auto N) {
     Vec<T, V> v[N.value][K], q[N.value][K];
     float df[N.value];
 #pragma unroll
@@ -415,17 +433,19 @@ __global__ __launch_bounds__(kNT) void norm_grad_kernel(NormGeom g, NormArgs p, 
         Vec<T, V> o;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float d = (float)v[i][k].v[j] - af.mean[k][j];
+          const float x = (float)v[i][k].v[j];
           float y;
-          const float sl = act_slope<ACT>(fmaf(d, af.a[k][j], af.b[k][j]), y);
+          const float sl = act_slope<ACT>(af.u(k, j, x), y);
           float dy;
           if constexpr (READ) dy = df[i]; else dy = (float)q[i][k].v[j];
-          o.v[j] = (T)fmaf(ar[k][j], dy * sl, fmaf(-d, c1[k][j], -c0[k][j]));
+          o.v[j] = (T)fmaf(ar[k][j], dy * sl, fmaf(af.kFold ? -x : af.mean[k][j] - x, c1[k][j], c0[k][j]));
         }
         if (col.dup[k] < V) store_vec(os + rows[i] * g.C + col.c[k], o);
       }
   });
 }
+
+constexpr int kJT = 1024;  // threads of a join
 
 __device__ __forceinline__ double block_sum(double v, double* lds) {
   for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
@@ -433,26 +453,54 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
   double t = 0.0;
-  for (int w = 0; w < kNW; ++w) t += lds[w];
+  for (int w = 0; w < kJT / 64; ++w) t += lds[w];
   return t;
 }
 
+// Sums NV values of column q of the partial rows at, at + step, ..., below n.
+template <int NV>
+__device__ __forceinline__ void add_rows(const double* q, int64_t prow, int at, int step, int n, double (&s)[NV]) {
+  int r = at;
+  for (; r + 3 * step < n; r += 4 * step) {
+    double v[4][NV];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[u][i] = q[(int64_t)(r + u * step) * prow + i];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] += (v[0][i] + v[1][i]) + (v[2][i] + v[3][i]);
+  }
+  for (; r < n; r += step)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] += q[(int64_t)r * prow + i];
+}
+
+// Partial rows to fewer: row blockIdx.y of `out` is the sum of `per` rows of
+// `in`, 256 columns per workgroup (norm_fold on the host says when).
+__global__ __launch_bounds__(kJT) void norm_fold_kernel(const double* in, double* out, int NB, int per, int64_t cols,
+                                                        int64_t prow) {
+  __shared__ double lds[kJT];
+  const int tx = threadIdx.x & 255, ty = threadIdx.x >> 8;
+  const int64_t b = blockIdx.z, c = (int64_t)blockIdx.x * 256 + tx;
+  const int r0 = (int)blockIdx.y * per, r1 = r0 + per < NB ? r0 + per : NB;
+  double s[1] = {0.0};
+  if (c < cols) add_rows<1>(in + b * NB * prow + c, prow, r0 + ty, 4, r1, s);
+  lds[threadIdx.x] = s[0];
+  __syncthreads();
+  if (ty == 0 && c < cols)
+    out[(b * gridDim.y + blockIdx.y) * prow + c] = (lds[tx] + lds[tx + 256]) + (lds[tx + 512] + lds[tx + 768]);
+}
+
 // Joins the partial rows of one sample and group: statistics (forward).
-__global__ __launch_bounds__(kNT) void norm_join_kernel(NormArgs p, const double* part, int NB, int D, int64_t prow) {
-  __shared__ double lds[kNW];
+__global__ __launch_bounds__(kJT) void norm_join_kernel(NormArgs p, const double* part, int NB, int D, int64_t prow) {
+  __shared__ double lds[kJT / 64];
   const int64_t b = blockIdx.y, gr = blockIdx.x;
-  const int W = D < kNT ? D : kNT, parts = kNT / W;
+  const int W = D < kJT ? D : kJT, parts = kJT / W;
   const int at = threadIdx.x % W, pt = threadIdx.x / W;
-  double s1 = 0.0, s2 = 0.0;
+  double s[2] = {0.0, 0.0};
   if (pt < parts)
-    for (int blk = pt; blk < NB; blk += parts)
-      for (int64_t c = at; c < D; c += W) {
-        const double* q = part + (b * NB + blk) * prow + (gr * D + c) * 2;
-        s1 += q[0];
-        s2 += q[1];
-      }
-  s1 = block_sum(s1, lds);
-  s2 = block_sum(s2, lds);
+    for (int64_t c = at; c < D; c += W) add_rows<2>(part + b * NB * prow + (gr * D + c) * 2, prow, pt, parts, NB, s);
+  const double s1 = block_sum(s[0], lds), s2 = block_sum(s[1], lds);
   if (threadIdx.x == 0) {
     const double n = (double)p.S * (double)D, mean = s1 / n;
     double var = s2 / n - mean * mean;
@@ -465,12 +513,12 @@ __global__ __launch_bounds__(kNT) void norm_join_kernel(NormArgs p, const double
 // Joins the partial rows of one sample and group: channel sums with A2 scaled
 // by rstd, and the group's coefficients rstd m1 and rstd^2 m2 (backward).
 template <bool READ>
-__global__ __launch_bounds__(kNT) void norm_join_bwd_kernel(NormArgs p, const double* part, int NB, int D,
+__global__ __launch_bounds__(kJT) void norm_join_bwd_kernel(NormArgs p, const double* part, int NB, int D,
                                                             int64_t prow, double* chan, float* coef) {
   constexpr int NV = READ ? 3 : 2;
-  __shared__ double lds[NV * kNT];
+  __shared__ double lds[NV * kJT];
   const int64_t b = blockIdx.y, gr = blockIdx.x;
-  const int W = D < kNT ? D : kNT, parts = kNT / W;
+  const int W = D < kJT ? D : kJT, parts = kJT / W;
   const int at = threadIdx.x % W, pt = threadIdx.x / W;
   const double rstd = (double)p.stats[(b * p.G + gr) * 2 + 1];
   double m1 = 0.0, m2 = 0.0;
@@ -479,22 +527,23 @@ __global__ __launch_bounds__(kNT) void norm_join_bwd_kernel(NormArgs p, const do
     double s[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) s[i] = 0.0;
-    if (pt < parts && c0 + at < D)
-      for (int blk = pt; blk < NB; blk += parts) {
-        const double* q = part + (b * NB + blk) * prow + c * NV;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) s[i] += q[i];
-      }
+    if (pt < parts && c0 + at < D) add_rows<NV>(part + b * NB * prow + c * NV, prow, pt, parts, NB, s);
+    // halve the rows of W threads until one is left; `parts` need not be a power of two
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NV; ++i) lds[i * kNT + threadIdx.x] = s[i];
+    for (int i = 0; i < NV; ++i) lds[i * kJT + threadIdx.x] = s[i];
+    for (int n = parts; n > 1;) {
+      const int h = (n + 1) / 2;
+      __syncthreads();
+      if (pt + h < n)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) lds[i * kJT + threadIdx.x] += lds[i * kJT + threadIdx.x + h * W];
+      n = h;
+    }
     __syncthreads();
     if (threadIdx.x < W && c0 + at < D) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        s[i] = 0.0;
-        for (int q = 0; q < parts; ++q) s[i] += lds[i * kNT + q * W + at];
-      }
+      for (int i = 0; i < NV; ++i) s[i] = lds[i * kJT + at];
       s[1] *= rstd;
 #pragma unroll
       for (int i = 0; i < NV; ++i) chan[b * prow + c * NV + i] = s[i];
@@ -504,7 +553,6 @@ __global__ __launch_bounds__(kNT) void norm_join_bwd_kernel(NormArgs p, const do
       m2 += w * s[1];
     }
   }
-  __syncthreads();
   m1 = block_sum(m1, lds);
   m2 = block_sum(m2, lds);
   if (threadIdx.x == 0) {
@@ -514,7 +562,7 @@ __global__ __launch_bounds__(kNT) void norm_join_bwd_kernel(NormArgs p, const do
   }
   if (READ && gr == 0) {
     double t = 0.0;
-    for (int blk = threadIdx.x; blk < NB; blk += kNT) t += part[(b * NB + blk) * prow + p.C * NV];
+    for (int blk = threadIdx.x; blk < NB; blk += kJT) t += part[(b * NB + blk) * prow + p.C * NV];
     t = block_sum(t, lds);
     if (threadIdx.x == 0) chan[b * prow + p.C * NV] = t;
   }
@@ -575,6 +623,20 @@ hipError_t with_cols(int V, int K, F f) {
 
 }  // namespace
 
+// Partial rows of `cols` doubles, folded first where one workgroup per sample
+// and group would read more than 256 KB of them; `part` and `NB` become those
+// that the join reads.
+inline void norm_fold(const NormArgs& a, double*& part, int& NB, int64_t cols, int64_t prow, int64_t NV,
+                      hipStream_t stream) {
+  if (NB <= kNormFolded || (int64_t)NB * (a.C / a.G) * NV * (int64_t)sizeof(double) <= 256 * 1024) return;
+  const int per = (NB + kNormFolded - 1) / kNormFolded, rows = (NB + per - 1) / per;
+  double* out = part + a.B * (NB + 1) * prow;
+  hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)((cols + 255) / 256), (unsigned)rows, (unsigned)a.B), dim3(kJT), 0,
+                     stream, part, out, NB, per, cols, prow);
+  part = out;
+  NB = rows;
+}
+
 template <class T>
 hipError_t norm_launch_fwd(const NormArgs& a, hipStream_t stream) {
   int V, K;
@@ -587,7 +649,10 @@ hipError_t norm_launch_fwd(const NormArgs& a, hipStream_t stream) {
     constexpr int VV = v.value, KK = k.value;
     hipLaunchKernelGGL((norm_stats_kernel<T, VV, KK>), grid, block, 0, stream, g, reinterpret_cast<const T*>(a.x), part,
                        prow);
-    hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)a.G, (unsigned)a.B), block, 0, stream, a, part, g.NB, D, prow);
+    double* from = part;
+    int NB = g.NB;
+    norm_fold(a, from, NB, 2 * a.C, prow, 2, stream);
+    hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)a.G, (unsigned)a.B), dim3(kJT), 0, stream, a, from, NB, D, prow);
     return with_act(a.act, [&](auto act) {
       if (a.field)
         hipLaunchKernelGGL((readout_apply_kernel<T, VV, KK, act.value>), grid, block, 0, stream, g, a, D);
@@ -606,20 +671,24 @@ hipError_t norm_launch_bwd(const NormArgs& a, hipStream_t stream) {
   const int64_t prow = (int64_t)norm_row(a.C);
   double* part = reinterpret_cast<double*>(a.ws);
   double* chan = part + (int64_t)a.B * g.NB * prow;
-  float* coef = reinterpret_cast<float*>(chan + a.B * prow);
+  float* coef = reinterpret_cast<float*>(chan + (1 + kNormFolded) * a.B * prow);
   const dim3 grid((unsigned)g.NB, (unsigned)a.B, (unsigned)g.chunks), block(kNT), join((unsigned)a.G, (unsigned)a.B);
   const dim3 last((unsigned)g.NB, a.gx ? (unsigned)a.B + 1 : 1u, a.gx ? (unsigned)g.chunks : 1u);
   return with_cols<T>(V, K, [&](auto v, auto k) {
     constexpr int VV = v.value, KK = k.value;
     return with_act(a.act, [&](auto act) {
       constexpr int A = act.value;
+      double* from = part;
+      int NB = g.NB;
       if (a.readout) {
         hipLaunchKernelGGL((norm_sums_kernel<T, VV, KK, A, true>), grid, block, 0, stream, g, a, D, part, prow);
-        hipLaunchKernelGGL((norm_join_bwd_kernel<true>), join, block, 0, stream, a, part, g.NB, D, prow, chan, coef);
+        norm_fold(a, from, NB, 3 * a.C + 1, prow, 3, stream);
+        hipLaunchKernelGGL((norm_join_bwd_kernel<true>), join, dim3(kJT), 0, stream, a, from, NB, D, prow, chan, coef);
         hipLaunchKernelGGL((norm_grad_kernel<T, VV, KK, A, true>), last, block, 0, stream, g, a, D, chan, prow, coef);
       } else {
         hipLaunchKernelGGL((norm_sums_kernel<T, VV, KK, A, false>), grid, block, 0, stream, g, a, D, part, prow);
-        hipLaunchKernelGGL((norm_join_bwd_kernel<false>), join, block, 0, stream, a, part, g.NB, D, prow, chan, coef);
+        norm_fold(a, from, NB, 2 * a.C, prow, 2, stream);
+        hipLaunchKernelGGL((norm_join_bwd_kernel<false>), join, dim3(kJT), 0, stream, a, from, NB, D, prow, chan, coef);
         hipLaunchKernelGGL((norm_grad_kernel<T, VV, KK, A, false>), last, block, 0, stream, g, a, D, chan, prow, coef);
       }
       return hipGetLastError();
