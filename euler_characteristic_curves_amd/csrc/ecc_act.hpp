@@ -46,27 +46,16 @@ __device__ __forceinline__ void store_param(void* p, int pdtype, int64_t i, floa
     reinterpret_cast<bf16*>(p)[i] = (bf16)v;
 }
 
-// exp(x) through the hardware's 2^y, relative error below 2^-22: the part of
-// x log2(e) that one float32 product rounds away is put back to first order.
-// x is clamped to where the result is a normal float (a NaN becomes finite
-// here; every caller multiplies by its own argument, which carries it).
-__device__ __forceinline__ float exp_f32(float x) {
-  x = __builtin_amdgcn_fmed3f(x, -87.0f, 88.0f);
-  const float hi = x * 1.44269502f;
-  const float lo = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -hi));
-  const float r = __builtin_amdgcn_exp2f(hi);
-  return fmaf(r, lo * 0.693147182f, r);
-}
-
 constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3;
 
-// Normal distribution function of u and e = exp(-u^2/2).  The upper tail at
-// z = |u| is e * t * p(t) with t = 1 / (1 + 0.3 z): t p(t) is erfcx(z /
-// sqrt 2) / 2, a polynomial in t fitted to it over z in [0, 14] (relative
-// error 1.5e-7, 4.2e-7 with float32 arithmetic), so both tails keep their
-// relative accuracy, where 1 + erf(u / sqrt 2) cancels.
-__device__ __forceinline__ float normal_cdf(float u, float& e) {
-  e = exp_f32(-0.5f * u * u);
+// Upper tail of the normal distribution at z = |u|, and e = exp(-z^2/2).  The
+// tail is e * t * p(t) with t = 1 / (1 + 0.3 z): t p(t) is erfcx(z / sqrt 2) /
+// 2, a polynomial in t fitted to it over z in [0, 14] (relative error 1.5e-7),
+// so it keeps its relative accuracy, where 1 + erf(u / sqrt 2) cancels.  The
+// exponent's rounding adds z^2 2^-25 relative, which is below 2^-25 of 1 after
+// e multiplies it.
+__device__ __forceinline__ float normal_tail(float u, float& e) {
+  e = __builtin_amdgcn_exp2f(u * (-0.721347520f * u));
   const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, fabsf(u), 1.0f));
   float p = 0.0356748769f;
   p = fmaf(p, t, -0.1572034993f);
@@ -76,8 +65,7 @@ __device__ __forceinline__ float normal_cdf(float u, float& e) {
   p = fmaf(p, t, 0.0999134088f);
   p = fmaf(p, t, 0.1207539682f);
   p = fmaf(p, t, 0.1196292981f);
-  const float q = e * (t * p);
-  return u >= 0.0f ? 1.0f - q : q;
+  return e * (t * p);
 }
 
 // 1 / (1 + exp(-u)).  The product that scales the exponent is off by half a
@@ -94,7 +82,7 @@ __device__ __forceinline__ float act_value(float u) {
   if constexpr (ACT == kActSilu) return u * logistic(u);
   if constexpr (ACT == kActGelu) {
     float e;
-    return u * normal_cdf(u, e);
+    return fmaf(-fabsf(u), normal_tail(u, e), fmaxf(u, 0.0f));
   }
   return u;
 }
@@ -112,10 +100,12 @@ __device__ __forceinline__ float act_slope(float u, float& y) {
     return fmaf(y, 1.0f - s, s);
   }
   if constexpr (ACT == kActGelu) {
+    // both from the tail q: y = max(u, 0) - |u| q, y' = q - |u| e / sqrt(2 pi), from 1 where u > 0
     float e;
-    const float c = normal_cdf(u, e);
-    y = u * c;
-    return fmaf(u * 0.398942280f, e, c);
+    const float q = normal_tail(u, e), z = fabsf(u);
+    y = fmaf(-z, q, fmaxf(u, 0.0f));
+    const float w = fmaf(-0.398942280f * z, e, q);
+    return u > 0.0f ? 1.0f - w : w;
   }
   y = u;
   return 1.0f;

@@ -577,7 +577,7 @@ NormGeom norm_geom(const NormArgs& a, int& V, int& K) {
   NormGeom g{};
   g.S = a.S;
   g.C = a.C;
-  g.NB = (int)norm_blocks(a.B, a.S, a.C);
+  g.NB = (int)norm_blocks(a.B, a.S, a.C, kNormSums);
   g.nv = (int)((a.C + V - 1) / V);
   g.chunks = 1;
   K = 1;
@@ -624,11 +624,11 @@ hipError_t with_cols(int V, int K, F f) {
 }  // namespace
 
 // Partial rows of `cols` doubles, folded first where one workgroup per sample
-// and group would read more than 256 KB of them; `part` and `NB` become those
+// and group would read more than 128 KB of them; `part` and `NB` become those
 // that the join reads.
 inline void norm_fold(const NormArgs& a, double*& part, int& NB, int64_t cols, int64_t prow, int64_t NV,
                       hipStream_t stream) {
-  if (NB <= kNormFolded || (int64_t)NB * (a.C / a.G) * NV * (int64_t)sizeof(double) <= 256 * 1024) return;
+  if (NB <= kNormFolded || (int64_t)NB * (a.C / a.G) * NV * (int64_t)sizeof(double) <= 128 * 1024) return;
   const int per = (NB + kNormFolded - 1) / kNormFolded, rows = (NB + per - 1) / per;
   double* out = part + a.B * (NB + 1) * prow;
   hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)((cols + 255) / 256), (unsigned)rows, (unsigned)a.B), dim3(kJT), 0,
@@ -653,11 +653,14 @@ hipError_t norm_launch_fwd(const NormArgs& a, hipStream_t stream) {
     int NB = g.NB;
     norm_fold(a, from, NB, 2 * a.C, prow, 2, stream);
     hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)a.G, (unsigned)a.B), dim3(kJT), 0, stream, a, from, NB, D, prow);
+    NormGeom ga = g;
+    ga.NB = (int)norm_blocks(a.B, a.S, a.C, kNormApply);
+    const dim3 apply((unsigned)ga.NB, (unsigned)a.B, (unsigned)g.chunks);
     return with_act(a.act, [&](auto act) {
       if (a.field)
-        hipLaunchKernelGGL((readout_apply_kernel<T, VV, KK, act.value>), grid, block, 0, stream, g, a, D);
+        hipLaunchKernelGGL((readout_apply_kernel<T, VV, KK, act.value>), apply, block, 0, stream, ga, a, D);
       else
-        hipLaunchKernelGGL((norm_apply_kernel<T, VV, KK, act.value>), grid, block, 0, stream, g, a, D);
+        hipLaunchKernelGGL((norm_apply_kernel<T, VV, KK, act.value>), apply, block, 0, stream, ga, a, D);
       return hipGetLastError();
     });
   });

@@ -33,10 +33,15 @@ struct NormArgs {
   void* ws;
 };
 
-// Workgroups per sample of the passes over the features.  A workgroup has at
-// least 4096 elements, and a launch about 8 workgroups per CU of 256.
-inline int64_t norm_blocks(int64_t B, int64_t S, int64_t C) {
-  int64_t nb = (S * C + 4095) / 4096, most = (2048 + B - 1) / B;
+// Workgroups per sample of a pass over the features, `total` in a launch; each
+// has at least 4096 elements.  Passes that hold sums or both gradients need 80
+// to 127 registers, so that 4 workgroups a CU are resident, and leave a partial
+// row each: 1024 (2 x 128^3 x 64, bfloat16: 803 us a training pass, 838 with
+// 2048).  The forward's second pass fits 8 a CU: 2048 (read-out of 256^3 x 32:
+// 226 us, 250 with 1024).
+constexpr int64_t kNormSums = 1024, kNormApply = 2048;
+inline int64_t norm_blocks(int64_t B, int64_t S, int64_t C, int64_t total) {
+  int64_t nb = (S * C + 4095) / 4096, most = (total + B - 1) / B;
   nb = nb < most ? nb : most;
   nb = nb < S ? nb : S;
   return nb < 1 ? 1 : nb;
@@ -50,7 +55,7 @@ constexpr int kNormFolded = 32;
 // float64 per channel and one more.
 inline size_t norm_row(int64_t C) { return (size_t)(3 * C + 1); }
 inline size_t norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G) {
-  const size_t rows = (size_t)B * (size_t)(norm_blocks(B, S, C) + 1 + kNormFolded);
+  const size_t rows = (size_t)B * (size_t)(norm_blocks(B, S, C, kNormSums) + 1 + kNormFolded);
   return rows * norm_row(C) * sizeof(double) + (size_t)B * (size_t)G * 2 * sizeof(float) + 256;
 }
 
