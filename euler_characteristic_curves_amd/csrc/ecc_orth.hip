@@ -507,6 +507,11 @@ hipError_t run_out(const OrthArgs& o, int odtype, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_orth(const OrthArgs& o, hipStream_t s) {
+  if (orth_is_thin(o)) {
+    if (o.gdtype == kTF32) return launch_orth_thin<float>(o, s);
+    if (o.gdtype == kTF16) return launch_orth_thin<f16>(o, s);
+    return launch_orth_thin<bf16>(o, s);
+  }
   if (o.gdtype == kTF32) return run_out<float>(o, o.odtype, s);
   if (o.gdtype == kTF16) return run_out<f16>(o, o.odtype, s);
   return run_out<bf16>(o, o.odtype, s);

@@ -1,0 +1,6 @@
+// Orthogonalisation of thin f32 matrices (ecc_orth_thin_kernels.hpp).
+#include "ecc_orth_thin_kernels.hpp"
+
+namespace ecc {
+template hipError_t launch_orth_thin<float>(const OrthArgs&, hipStream_t);
+}  // namespace ecc

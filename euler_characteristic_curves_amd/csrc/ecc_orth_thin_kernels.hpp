@@ -1,0 +1,520 @@
+// Newton-Schulz orthogonalisation of matrices with a short side of at most 64
+// (contract: include/ecc_train.h; longer ones: ecc_orth.hip).
+//
+// Every X_k is Q_k X_0 with Q_k symmetric, and X_k X_k^T = A_k follows from A_0
+// alone: with P = a I + b A + c A A,
+//   A <- P A P,   Q <- Q P,
+// all of them polynomials of A_0, so they commute and are symmetric.  The long
+// side n is therefore passed twice only, for A_0 = X_0 X_0^T and for Q X_0,
+// whatever the number of steps: 3 m^2 n products in place of 15 m^2 n.
+//
+// Precision.  A direction of singular value s is one of s^2 in A, and an error
+// d of A grows with it, by p(s)^2 a step, where the direct iteration forms A
+// anew.  In float32 that costs digits (relative error 5e-5 of a 64 x 66
+// matrix, direct iteration 1e-6); in float64 it does not (1.1e-6, all of it
+// the final product's), so A, P and Q are float64 throughout, on the float64
+// matrix instructions; launch_orth leaves the cases whose growth would pass
+// 2^26 to the direct iteration.  The final product is float32.
+//
+// What bounds it: the two passes, HBM; the steps, one workgroup per matrix,
+// the float64 matrix rate of a CU, 1.3 us per 64^3 product (lower triangle of
+// tiles), 14 of them in 5 steps, of which the critical ones depend on each
+// other.
+//
+// Orientation.  m is the short side.  `tall` matrices (rows > cols) keep the
+// short side contiguous; lanes then take MB consecutive short-side elements,
+// so element a of tile I is a MB + I there and 16 I + a otherwise.
+
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "ecc_act.hpp"
+#include "ecc_internal.hpp"
+#include "ecc_train_internal.hpp"
+
+namespace ecc {
+namespace {
+
+constexpr int kNT = 512;
+constexpr int kNW = kNT / 64;
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <int MB>
+constexpr int kTiles = MB * (MB + 1) / 2;
+// Row length of a matrix in LDS: columns are flipped by 16 in odd rows, so
+// that the two rows a half wave reads lie in different banks.
+template <int MB>
+constexpr int kLD = MB <= 2 ? 32 : 64;
+template <int MB>
+__device__ __forceinline__ int at(int row, int col) {
+  return row * kLD<MB> + (col ^ ((row & 1) << 4));
+}
+
+struct Thin {
+  OrthArgs o;
+  int m;
+  int64_t n, per;  // columns of a workgroup
+  int splits;
+  double* part;  // [batch][splits][tiles][256]
+  float* q;      // [batch][64 * 64]: Q / (norm + eps) 2^-t
+  float* pow2;   // [batch]: 2^t
+};
+
+// N elements, of which `valid` lie inside.
+template <int N, class T>
+__device__ __forceinline__ void load_some(const T* p, int64_t valid, float (&v)[N]) {
+  if (valid >= N) {
+    Vec<T, N> r;
+    load_vec(p, r);
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = (float)r.v[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = j < valid ? (float)p[j] : 0.0f;
+  }
+}
+template <int N, class T>
+__device__ __forceinline__ void store_some(T* p, int64_t valid, const float (&v)[N]) {
+  if (valid >= N) {
+    Vec<T, N> r;
+#pragma unroll
+    for (int j = 0; j < N; ++j) r.v[j] = (T)v[j];
+    store_vec(p, r);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j < valid) p[j] = (T)v[j];
+  }
+}
+
+// N elements of the matrix that is orthogonalised, from offset `i` on.  UPDATE:
+// the momentum buffer is brought forward on the way.
+template <int N, class GT, bool UPDATE>
+__device__ __forceinline__ void load_u(const OrthArgs& o, const GT* g, float* buf, int64_t i, int64_t valid,
+                                       float (&u)[N]) {
+  if (valid <= 0) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) u[j] = 0.0f;
+    return;
+  }
+  if (!buf) {
+    load_some<N>(g + i, valid, u);
+    return;
+  }
+  float b[N], gv[N];
+  load_some<N>(buf + i, valid, b);
+  if (UPDATE || o.nesterov) load_some<N>(g + i, valid, gv);
+  if constexpr (UPDATE) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) b[j] = fmaf(o.momentum, b[j], o.blend * gv[j]);
+    store_some<N>(buf + i, valid, b);
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) u[j] = o.nesterov ? fmaf(o.momentum, b[j], o.blend * gv[j]) : b[j];
+}
+
+// ------------------------------------------------------------------- A_0
+// One k-step of the lower triangle of tiles; x[I]: this lane's element of tile I.
+template <int MB>
+__device__ __forceinline__ void gram_step(const float (&x)[MB], f64x4 (&acc)[kTiles<MB>]) {
+  double d[MB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i) d[i] = (double)x[i];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j <= i; ++j)
+      acc[i * (i + 1) / 2 + j] = __builtin_amdgcn_mfma_f64_16x16x4f64(d[i], d[j], acc[i * (i + 1) / 2 + j], 0, 0, 0);
+}
+
+// U U^T over columns [c0, c1) of the workgroup's matrix.  out: tile order,
+// tiles x 256 doubles.  lds: kNW x 5 x 256 doubles.
+template <int MB, bool TALL, class GT>
+__device__ __forceinline__ void gram_part(const Thin& t, int64_t batch, int64_t c0, int64_t c1, double* lds,
+                                          double* out) {
+  const OrthArgs& o = t.o;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+  const int64_t off = batch * o.rows * o.cols;
+  const GT* g = reinterpret_cast<const GT*>(o.g) + off;
+  float* buf = o.buffer ? o.buffer + off : nullptr;
+  f64x4 acc[kTiles<MB>];
+#pragma unroll
+  for (int i = 0; i < kTiles<MB>; ++i) acc[i] = f64x4{0.0, 0.0, 0.0, 0.0};
+  for (int64_t c = c0 + wave * 32; c < c1; c += kNW * 32) {
+    if constexpr (TALL) {
+      float x[8][MB];
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const int64_t j = c + s * 4 + q;
+        load_u<MB, GT, true>(o, g, buf, j * o.cols + r * MB, j < c1 ? t.m - r * MB : 0, x[s]);
+      }
+#pragma unroll
+      for (int s = 0; s < 8; ++s) gram_step<MB>(x[s], acc);
+    } else {
+      float x[MB][2][4];
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = i * 16 + r;
+          const int64_t j = c + q * 8 + h * 4;
+          load_u<4, GT, true>(o, g, buf, row * o.cols + j, row < t.m ? c1 - j : 0, x[i][h]);
+        }
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        float y[MB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) y[i] = x[i][s >> 2][s & 3];
+        gram_step<MB>(y, acc);
+      }
+    }
+  }
+  // the waves' sums, five tiles at a time, in order
+#pragma unroll
+  for (int t0 = 0; t0 < kTiles<MB>; t0 += 5) {
+    const int nt = kTiles<MB> - t0 < 5 ? kTiles<MB> - t0 : 5;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+      if (t0 + i < kTiles<MB>)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) lds[(wave * 5 + i) * 256 + k * 64 + lane] = acc[t0 + i < kTiles<MB> ? t0 + i : 0][k];
+    __syncthreads();
+    for (int e = threadIdx.x; e < nt * 256; e += kNT) {
+      double s = 0.0;
+#pragma unroll
+      for (int w = 0; w < kNW; ++w) s += lds[w * 5 * 256 + e];
+      out[t0 * 256 + e] = s;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ steps
+// Row and column, within the matrix, of element e of tile-ordered storage.
+template <int MB>
+__device__ __forceinline__ void place(int e, bool tall, int& row, int& col) {
+  int tile = e >> 8, i = 0;
+  while ((i + 1) * (i + 2) / 2 <= tile) ++i;
+  const int j = tile - i * (i + 1) / 2, a = 4 * ((e >> 6) & 3) + ((e >> 4) & 3), b = e & 15;
+  row = tall ? a * MB + i : i * 16 + a;
+  col = tall ? b * MB + j : j * 16 + b;
+}
+
+// Tile (i, j) of the product of two commuting symmetric matrices.
+template <int MB>
+__device__ __forceinline__ f64x4 tile_product(const double* x, const double* y, int i, int j) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  f64x4 acc = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+  for (int k = 0; k < MB * 16; k += 4)
+    acc = __builtin_amdgcn_mfma_f64_16x16x4f64(x[at<MB>(k + q, i * 16 + r)], y[at<MB>(k + q, j * 16 + r)], acc, 0, 0, 0);
+  return acc;
+}
+template <int MB>
+__device__ __forceinline__ void tile_store(double* z, int i, int j, f64x4 v) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int row = i * 16 + 4 * k + q, col = j * 16 + r;
+    z[at<MB>(row, col)] = v[k];
+    if (i != j) z[at<MB>(col, row)] = v[k];
+  }
+}
+template <int MB>
+__device__ __forceinline__ void tile_index(int tile, int& i, int& j) {
+  i = 0;
+  while ((i + 1) * (i + 2) / 2 <= tile) ++i;
+  j = tile - i * (i + 1) / 2;
+}
+
+// From G = U U^T (tile order, `splits` partial sums apart by tiles x 256) to Q
+// / (norm + eps) 2^-t in float32, row-major with 16 MB columns, at `q`; returns
+// 2^t.  lds: 4 matrices and one double.
+template <int MB>
+__device__ __forceinline__ float thin_steps(const Thin& t, bool tall, const double* part, int splits, double* lds,
+                                            float* q) {
+  constexpr int N = 16 * MB, T = kTiles<MB>, SZ = N * kLD<MB>;
+  const OrthArgs& o = t.o;
+  double *A = lds, *P = lds + SZ, *W = lds + 2 * SZ, *Q = lds + 3 * SZ, *tr = lds + 4 * SZ;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int e = threadIdx.x; e < T * 256; e += kNT) {
+    double s = 0.0;
+    int k = 0;
+    for (; k + 4 <= splits; k += 4) {
+      double v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = part[(int64_t)(k + u) * (T * 256) + e];
+      s += (v[0] + v[1]) + (v[2] + v[3]);
+    }
+    for (; k < splits; ++k) s += part[(int64_t)k * (T * 256) + e];
+    int row, col;
+    place<MB>(e, tall, row, col);
+    A[at<MB>(row, col)] = s;
+    A[at<MB>(col, row)] = s;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    double s = lane < N ? A[at<MB>(lane, lane)] : 0.0;
+    for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
+    if (lane == 0) *tr = s;
+  }
+  __syncthreads();
+  const double inv = 1.0 / (sqrt(*tr) + (double)o.eps);
+  for (int e = threadIdx.x; e < SZ; e += kNT) A[e] = A[e] * inv * inv;
+  __syncthreads();
+  for (int s = 0; s < o.steps; ++s) {
+    const bool first = s == 0, last = s + 1 == o.steps;
+    for (int tile = wave; tile < T; tile += kNW) {
+      int i, j;
+      tile_index<MB>(tile, i, j);
+      f64x4 v = tile_product<MB>(A, A, i, j);
+      const int r = lane & 15, qq = lane >> 4;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = i * 16 + 4 * k + qq, col = j * 16 + r;
+        v[k] = fma((double)o.c, v[k], (double)o.b * A[at<MB>(row, col)]);
+        if (row == col) v[k] += (double)o.a;
+      }
+      tile_store<MB>(first ? Q : P, i, j, v);
+      if (first) tile_store<MB>(P, i, j, v);
+    }
+    __syncthreads();
+    // W = A P and the new Q side by side: work items 0 .. T - 1 and T .. 2 T - 1
+    constexpr int kMine = (2 * T + kNW - 1) / kNW;
+    f64x4 held[kMine];
+    const int from = last ? T : 0, to = first ? T : 2 * T;
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+      const int item = from + wave + u * kNW;
+      if (item < to) {
+        int i, j;
+        tile_index<MB>(item < T ? item : item - T, i, j);
+        held[u] = tile_product<MB>(item < T ? A : Q, P, i, j);
+        if (item < T) tile_store<MB>(W, i, j, held[u]);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+      const int item = from + wave + u * kNW;
+      if (item < to && item >= T) {
+        int i, j;
+        tile_index<MB>(item - T, i, j);
+        tile_store<MB>(Q, i, j, held[u]);
+      }
+    }
+    if (!last)
+      for (int tile = wave; tile < T; tile += kNW) {
+        int i, j;
+        tile_index<MB>(tile, i, j);
+        tile_store<MB>(A, i, j, tile_product<MB>(W, P, i, j));
+      }
+    __syncthreads();
+  }
+  int e = 0;
+  frexp(inv, &e);
+  e = e < -126 ? -126 : (e > 126 ? 126 : e);
+  if (!(inv < 1e300)) e = 0;
+  const double f = inv * ldexp(1.0, -e);
+  for (int k = threadIdx.x; k < N * N; k += kNT) q[k] = (float)(Q[at<MB>(k / N, k % N)] * f);
+  return ldexpf(1.0f, e);
+}
+
+// ------------------------------------------------------------------ Q X_0
+// N elements of the result, from offset i on (the type is uniform, so one
+// branch in a store costs less than three copies of every kernel).
+template <int N, class PT>
+__device__ __forceinline__ void finish_typed(const OrthArgs& o, int64_t i, int64_t valid, float (&v)[N]) {
+  PT* out = reinterpret_cast<PT*>(o.out) + i;
+  if (o.buffer) {
+    float p[N];
+    load_some<N>(out, valid, p);
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = fmaf(p[j], o.keep, -o.rate * v[j]);
+  }
+  store_some<N>(out, valid, v);
+}
+template <int N>
+__device__ __forceinline__ void finish_some(const OrthArgs& o, int64_t i, int64_t valid, float (&v)[N]) {
+  if (valid <= 0) return;
+  if (o.odtype == kTF32)
+    finish_typed<N, float>(o, i, valid, v);
+  else if (o.odtype == kTF16)
+    finish_typed<N, f16>(o, i, valid, v);
+  else
+    finish_typed<N, bf16>(o, i, valid, v);
+}
+
+// Columns [c0, c1) of the result; a wave takes 64 (wide) or 16 (tall) at a
+// time and has read all of them before it writes, so the result may replace
+// the input.  qm: Q in LDS, N x (N + 4).
+template <int MB, bool TALL, class GT>
+__device__ __forceinline__ void apply_part(const Thin& t, int64_t batch, int64_t c0, int64_t c1, int wave, int waves,
+                                           const float* qm, float pow2) {
+  constexpr int N = 16 * MB, LD = N + 4;
+  const OrthArgs& o = t.o;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int64_t off = batch * o.rows * o.cols;
+  const GT* g = reinterpret_cast<const GT*>(o.g) + off;
+  float* buf = o.buffer ? o.buffer + off : nullptr;
+  if constexpr (TALL) {
+    for (int64_t c = c0 + wave * 16; c < c1; c += waves * 16) {
+      float u[MB][4];
+#pragma unroll
+      for (int k = 0; k < MB; ++k) {
+        load_u<4, GT, false>(o, g, buf, (c + r) * o.cols + k * 16 + q * 4, c + r < c1 ? t.m - (k * 16 + q * 4) : 0, u[k]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[k][j] *= pow2;
+      }
+      f32x4 acc[MB];
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < MB; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(u[k][j], qm[(k * 16 + q * 4 + j) * LD + r * MB + i], acc[i], 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t j = c + q * 4 + k;
+        float v[MB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) v[i] = acc[i][k];
+        finish_some<MB>(o, off + j * o.cols + r * MB, j < c1 ? t.m - r * MB : 0, v);
+      }
+    }
+  } else {
+    for (int64_t c = c0 + wave * 64; c < c1; c += waves * 64) {
+      float u[4 * MB][4];
+#pragma unroll
+      for (int k = 0; k < 4 * MB; ++k) {
+        const int row = k * 4 + q;
+        load_u<4, GT, false>(o, g, buf, row * o.cols + c + r * 4, row < t.m ? c1 - (c + r * 4) : 0, u[k]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[k][j] *= pow2;
+      }
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        f32x4 acc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < 4 * MB; ++k) {
+          const float a = qm[(k * 4 + q) * LD + i * 16 + r];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, u[k][j], acc[j], 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = i * 16 + q * 4 + k;
+          float v[4] = {acc[0][k], acc[1][k], acc[2][k], acc[3][k]};
+          finish_some<4>(o, off + row * o.cols + c + r * 4, row < t.m ? c1 - (c + r * 4) : 0, v);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- kernels
+constexpr int kGramLds = kNW * 5 * 256;  // doubles
+template <int MB>
+constexpr int kStepsLds = 4 * 16 * MB * kLD<MB> + 2;
+template <int MB>
+constexpr int kWholeLds =
+    kStepsLds<MB> > kGramLds + kTiles<MB> * 256 ? kStepsLds<MB> : kGramLds + kTiles<MB> * 256;
+
+template <int MB, bool TALL, class GT>
+__global__ __launch_bounds__(kNT) void thin_gram_kernel(Thin t) {
+  __shared__ double lds[kGramLds];
+  const int64_t c0 = (int64_t)blockIdx.x * t.per, c1 = c0 + t.per < t.n ? c0 + t.per : t.n;
+  gram_part<MB, TALL, GT>(t, blockIdx.y, c0, c1, lds,
+                          t.part + ((int64_t)blockIdx.y * t.splits + blockIdx.x) * (kTiles<MB> * 256));
+}
+
+template <int MB>
+__global__ __launch_bounds__(kNT) void thin_steps_kernel(Thin t) {
+  __shared__ double dyn[kStepsLds<MB>];
+  const float p = thin_steps<MB>(t, t.o.rows > t.o.cols, t.part + (int64_t)blockIdx.x * t.splits * (kTiles<MB> * 256),
+                                 t.splits, dyn, t.q + (int64_t)blockIdx.x * (64 * 64));
+  if (threadIdx.x == 0) t.pow2[blockIdx.x] = p;
+}
+
+template <int MB, bool TALL, class GT>
+__global__ __launch_bounds__(256) void thin_apply_kernel(Thin t) {
+  constexpr int N = 16 * MB, COLS = TALL ? 64 : 256;
+  __shared__ float qm[N * (N + 4)];
+  const float* q = t.q + (int64_t)blockIdx.y * (64 * 64);
+  for (int k = threadIdx.x; k < N * N; k += 256) qm[(k / N) * (N + 4) + k % N] = q[k];
+  const float pow2 = t.pow2[blockIdx.y];
+  __syncthreads();
+  const int64_t c0 = (int64_t)blockIdx.x * COLS, c1 = c0 + COLS < t.n ? c0 + COLS : t.n;
+  apply_part<MB, TALL, GT>(t, blockIdx.y, c0, c1, threadIdx.x >> 6, 4, qm, pow2);
+}
+
+// All of it, where one workgroup takes a whole matrix.
+template <int MB, bool TALL, class GT>
+__global__ __launch_bounds__(kNT) void thin_whole_kernel(Thin t) {
+  constexpr int N = 16 * MB, SZ = N * kLD<MB>;
+  __shared__ double dyn[kWholeLds<MB>];
+  // the tile-ordered sums lie behind the waves' sums, where A is not
+  double* g = dyn + kGramLds;
+  gram_part<MB, TALL, GT>(t, blockIdx.x, 0, t.n, dyn, g);
+  __syncthreads();
+  float* q = reinterpret_cast<float*>(dyn);  // over A and P, free at the end
+  const float pow2 = thin_steps<MB>(t, TALL, g, 1, dyn, q);
+  __syncthreads();
+  float* qm = reinterpret_cast<float*>(dyn + SZ * 2);
+  for (int k = threadIdx.x; k < N * N; k += kNT) qm[(k / N) * (N + 4) + k % N] = q[k];
+  __syncthreads();
+  apply_part<MB, TALL, GT>(t, blockIdx.x, 0, t.n, threadIdx.x >> 6, kNW, qm, pow2);
+}
+
+template <int MB, bool TALL, class GT>
+hipError_t thin_run(const Thin& t, hipStream_t s) {
+  const unsigned batch = (unsigned)t.o.batch;
+  if (t.splits == 1) {
+    hipLaunchKernelGGL((thin_whole_kernel<MB, TALL, GT>), dim3(batch), dim3(kNT), 0, s, t);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((thin_gram_kernel<MB, TALL, GT>), dim3((unsigned)t.splits, batch), dim3(kNT), 0, s, t);
+  hipLaunchKernelGGL((thin_steps_kernel<MB>), dim3(batch), dim3(kNT), 0, s, t);
+  constexpr int64_t cols = TALL ? 64 : 256;
+  hipLaunchKernelGGL((thin_apply_kernel<MB, TALL, GT>), dim3((unsigned)((t.n + cols - 1) / cols), batch), dim3(256), 0, s,
+                     t);
+  return hipGetLastError();
+}
+
+template <int MB, class GT>
+hipError_t thin_side(const Thin& t, hipStream_t s) {
+  return t.o.rows > t.o.cols ? thin_run<MB, true, GT>(t, s) : thin_run<MB, false, GT>(t, s);
+}
+
+}  // namespace
+
+template <class GT>
+hipError_t launch_orth_thin(const OrthArgs& o, hipStream_t s) {
+  const ThinPlan w = thin_plan(o.batch, o.rows, o.cols);
+  char* ws = reinterpret_cast<char*>(o.ws);
+  Thin t{};
+  t.o = o;
+  t.m = (int)(o.rows < o.cols ? o.rows : o.cols);
+  t.n = o.rows < o.cols ? o.cols : o.rows;
+  t.per = w.per;
+  t.splits = w.splits;
+  t.part = reinterpret_cast<double*>(ws + w.at_part);
+  t.q = reinterpret_cast<float*>(ws + w.at_q);
+  t.pow2 = reinterpret_cast<float*>(ws + w.at_pow2);
+  if (t.m <= 16) return thin_side<1, GT>(t, s);
+  if (t.m <= 32) return thin_side<2, GT>(t, s);
+  if (t.m <= 48) return thin_side<3, GT>(t, s);
+  return thin_side<4, GT>(t, s);
+}
+
+}  // namespace ecc

@@ -121,7 +121,7 @@ int check_orth(ecc::OrthArgs& o, size_t ws_bytes) {
   if (!isfinite(o.a) || !isfinite(o.b) || !isfinite(o.c)) return fail(ECC_E_VALUE, "coefficients must be finite");
   if (!ecc::orth_bounds(o))
     return fail(ECC_E_VALUE, "under these coefficients singular values in [0, 1] leave [-16, 16]");
-  return check_workspace(o.ws, ws_bytes, ecc::orth_plan(o.batch, o.rows, o.cols).bytes);
+  return check_workspace(o.ws, ws_bytes, ecc::orth_workspace_bytes(o.batch, o.rows, o.cols));
 }
 
 }  // namespace
@@ -132,6 +132,7 @@ bool orth_bounds(OrthArgs& o) {
   // 256 samples of the attained range; 2 % covers what lies between them
   constexpr int kSamples = 256;
   double r = 1.0, pmax = 0.0, gram = 0.0, cap = 1.0;
+  o.amplify = 1.0;
   for (int k = 0; k < o.steps; ++k) {
     double f = 0.0, q = 0.0;
     for (int i = 0; i <= kSamples; ++i) {
@@ -141,6 +142,7 @@ bool orth_bounds(OrthArgs& o) {
     }
     gram = fmax(gram, r * r);
     pmax = fmax(pmax, 1.02 * q);
+    if (k + 1 < o.steps) o.amplify *= fmax(1.0, q * q);
     r = 1.02 * f;
     cap = fmax(cap, r);
     if (!(cap <= 16.0) || !(pmax <= 4096.0)) return false;
@@ -240,7 +242,7 @@ int ecc_norm_readout_bwd(const void* x, int dtype, int64_t batch, int64_t voxels
 
 size_t ecc_orth_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
   if (check_matrix(batch, rows, cols) != ECC_OK) return 0;
-  return ecc::orth_plan(batch, rows, cols).bytes;
+  return ecc::orth_workspace_bytes(batch, rows, cols);
 }
 
 int ecc_orthogonalize(const void* g, int dtype, int64_t batch, int64_t rows, int64_t cols, int32_t steps, float eps,

@@ -80,6 +80,7 @@ struct OrthArgs {
   // bounds of the iteration (orth_bounds): ||X|| <= min(growth^k, cap), and
   // the scales of the pairs that hold A = X X^T and P
   float growth, cap, sa, sp;
+  double amplify;  // what an error of X_0 X_0^T may grow by when it is not formed anew
   void* ws;
   // set by the launcher
   double* squares;
@@ -151,6 +152,53 @@ inline OrthPlan orth_plan(int64_t batch, int64_t rows, int64_t cols) {
   return w;
 }
 
+// Matrices with a short side of at most kThin that are carried through their
+// steps by the short side's matrix alone (ecc_orth_thin_kernels.hpp).
+constexpr int64_t kThin = 64;
+constexpr double kMaxAmplify = 67108864.0;  // 2^26: leaves float64 2^-27
+struct ThinPlan {
+  int64_t per;  // columns of a workgroup of the first pass, a multiple of 32
+  int splits;
+  size_t at_part, at_q, at_pow2, bytes;
+};
+inline ThinPlan thin_plan(int64_t batch, int64_t rows, int64_t cols) {
+  ThinPlan w{};
+  const int64_t n = rows < cols ? cols : rows;
+  // a column costs a workgroup 17 ns of float64 products, a partial sum the
+  // one that joins them 0.2 us: balanced at sqrt(n / 12) parts, if a workgroup
+  // keeps 256 columns and the launch does not pass 256 workgroups
+  int64_t s = 1;
+  while (12 * (s + 1) * (s + 1) <= n) ++s;
+  const int64_t fill = (256 + batch - 1) / batch, most = (n + 255) / 256;
+  s = s < fill ? s : fill;
+  s = s < most ? s : most;
+  w.per = ((n + s - 1) / s + 31) / 32 * 32;
+  w.splits = (int)((n + w.per - 1) / w.per);
+  size_t at = 0;
+  auto take = [&at](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) & ~(size_t)255;
+    return here;
+  };
+  w.at_part = take((size_t)batch * w.splits * 10 * 256 * sizeof(double));
+  w.at_q = take((size_t)batch * 64 * 64 * sizeof(float));
+  w.at_pow2 = take((size_t)batch * sizeof(float));
+  w.bytes = at;
+  return w;
+}
+inline bool orth_is_thin(const OrthArgs& o) {
+  return (o.rows <= kThin || o.cols <= kThin) && o.amplify <= kMaxAmplify;
+}
+// Workspace of either way (the coefficients, which decide, come with the call).
+inline size_t orth_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
+  const size_t direct = orth_plan(batch, rows, cols).bytes;
+  if (rows > kThin && cols > kThin) return direct;
+  const size_t thin = thin_plan(batch, rows, cols).bytes;
+  return thin > direct ? thin : direct;
+}
+
 hipError_t launch_orth(const OrthArgs& o, hipStream_t stream);
+template <class GT>
+hipError_t launch_orth_thin(const OrthArgs& o, hipStream_t stream);
 
 }  // namespace ecc
