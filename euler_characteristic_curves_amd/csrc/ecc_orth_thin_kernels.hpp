@@ -92,31 +92,45 @@ __device__ __forceinline__ void store_some(T* p, int64_t valid, const float (&v)
   }
 }
 
-// N elements of the matrix that is orthogonalised, from offset `i` on.  UPDATE:
-// the momentum buffer is brought forward on the way.
-template <int N, class GT, bool UPDATE>
-__device__ __forceinline__ void load_u(const OrthArgs& o, const GT* g, float* buf, int64_t i, int64_t valid,
-                                       float (&u)[N]) {
-  if (valid <= 0) {
+// N neighbouring elements of the gradient and the buffer, as stored.  Loads
+// carry no condition, so that a wave has all of a chunk in flight: what lies
+// past the end of a line (`count` elements from `line` on) is read from inside
+// it and zeroed by `value`.  VEC: N divides count, or all N lie inside.
+template <int N, class GT>
+struct Raw {
+  Vec<GT, N> g;
+  Vec<float, N> b;
+  template <bool VEC>
+  __device__ __forceinline__ void load(const GT* gp, const float* buf, int64_t line, int first, int count, bool grad) {
+    if constexpr (VEC) {
+      const int64_t i = line + (first < count ? first : 0);
+      if (grad) load_vec(gp + i, g);
+      if (buf) load_vec(buf + i, b);
+    } else {
 #pragma unroll
-    for (int j = 0; j < N; ++j) u[j] = 0.0f;
-    return;
+      for (int j = 0; j < N; ++j) {
+        const int64_t i = line + (first + j < count ? first + j : count - 1);
+        if (grad) g.v[j] = gp[i];
+        if (buf) b.v[j] = buf[i];
+      }
+    }
   }
-  if (!buf) {
-    load_some<N>(g + i, valid, u);
-    return;
-  }
-  float b[N], gv[N];
-  load_some<N>(buf + i, valid, b);
-  if (UPDATE || o.nesterov) load_some<N>(g + i, valid, gv);
-  if constexpr (UPDATE) {
+  // The matrix that is orthogonalised.  The buffer is the old one where
+  // `update` is set, and is brought forward.
+  __device__ __forceinline__ void value(const OrthArgs& o, bool buf, bool update, int first, int count, float (&u)[N]) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) b[j] = fmaf(o.momentum, b[j], o.blend * gv[j]);
-    store_some<N>(buf + i, valid, b);
+    for (int j = 0; j < N; ++j) {
+      float x;
+      if (buf) {
+        if (update) b.v[j] = fmaf(o.momentum, b.v[j], o.blend * (float)g.v[j]);
+        x = o.nesterov ? fmaf(o.momentum, b.v[j], o.blend * (float)g.v[j]) : b.v[j];
+      } else {
+        x = (float)g.v[j];
+      }
+      u[j] = first + j < count ? x : 0.0f;
+    }
   }
-#pragma unroll
-  for (int j = 0; j < N; ++j) u[j] = o.nesterov ? fmaf(o.momentum, b[j], o.blend * gv[j]) : b[j];
-}
+};
 
 // ------------------------------------------------------------------- A_0
 // One k-step of the lower triangle of tiles; x[I]: this lane's element of tile I.
@@ -145,34 +159,53 @@ __device__ __forceinline__ void gram_part(const Thin& t, int64_t batch, int64_t 
   f64x4 acc[kTiles<MB>];
 #pragma unroll
   for (int i = 0; i < kTiles<MB>; ++i) acc[i] = f64x4{0.0, 0.0, 0.0, 0.0};
-  for (int64_t c = c0 + wave * 32; c < c1; c += kNW * 32) {
+  constexpr int CH = 16;  // columns of a wave's chunk
+  const auto chunk = [&](int64_t c, auto vec) {
+    constexpr bool VEC = decltype(vec)::value;
     if constexpr (TALL) {
-      float x[8][MB];
+      Raw<MB, GT> x[CH / 4];
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
+      for (int s = 0; s < CH / 4; ++s) {
         const int64_t j = c + s * 4 + q;
-        load_u<MB, GT, true>(o, g, buf, j * o.cols + r * MB, j < c1 ? t.m - r * MB : 0, x[s]);
+        x[s].template load<VEC>(g, buf, (j < c1 ? j : c1 - 1) * o.cols, r * MB, t.m, true);
       }
 #pragma unroll
-      for (int s = 0; s < 8; ++s) gram_step<MB>(x[s], acc);
+      for (int s = 0; s < CH / 4; ++s) {
+        const int64_t j = c + s * 4 + q;
+        float u[MB];
+        x[s].value(o, buf, true, r * MB, j < c1 ? t.m : 0, u);
+        if (buf && j < c1 && r * MB < t.m) store_some<MB>(buf + j * o.cols + r * MB, t.m - r * MB, x[s].b.v);
+        gram_step<MB>(u, acc);
+      }
     } else {
-      float x[MB][2][4];
+      Raw<4, GT> x[MB];
+      const int first = (int)(c - c0) + q * 4, count = (int)(c1 - c0);
 #pragma unroll
-      for (int i = 0; i < MB; ++i)
+      for (int i = 0; i < MB; ++i) {
+        const int row = i * 16 + r;
+        x[i].template load<VEC>(g, buf, (row < t.m ? row : 0) * o.cols + c0, first, count, true);
+      }
+      float u[MB][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = i * 16 + r;
-          const int64_t j = c + q * 8 + h * 4;
-          load_u<4, GT, true>(o, g, buf, row * o.cols + j, row < t.m ? c1 - j : 0, x[i][h]);
-        }
+      for (int i = 0; i < MB; ++i) {
+        const int row = i * 16 + r;
+        x[i].value(o, buf, true, first, row < t.m ? count : 0, u[i]);
+        if (buf && row < t.m && first < count) store_some<4>(buf + row * o.cols + c0 + first, count - first, x[i].b.v);
+      }
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
+      for (int s = 0; s < 4; ++s) {
         float y[MB];
 #pragma unroll
-        for (int i = 0; i < MB; ++i) y[i] = x[i][s >> 2][s & 3];
+        for (int i = 0; i < MB; ++i) y[i] = u[i][s];
         gram_step<MB>(y, acc);
       }
     }
+  };
+  for (int64_t c = c0 + wave * CH; c < c1; c += kNW * CH) {
+    if (TALL ? t.m % MB == 0 : c + CH <= c1)
+      chunk(c, std::true_type());
+    else
+      chunk(c, std::false_type());
   }
   // the waves' sums, five tiles at a time, in order
 #pragma unroll
@@ -195,25 +228,42 @@ __device__ __forceinline__ void gram_part(const Thin& t, int64_t batch, int64_t 
 }
 
 // ------------------------------------------------------------------ steps
+// Tile (i, j), j <= i, of the lower triangle, at most four tiles a side.
+__device__ __forceinline__ void tile_index(int tile, int& i, int& j) {
+  i = tile >= 6 ? 3 : (tile >= 3 ? 2 : (tile >= 1 ? 1 : 0));
+  j = tile - i * (i + 1) / 2;
+}
+
 // Row and column, within the matrix, of element e of tile-ordered storage.
 template <int MB>
 __device__ __forceinline__ void place(int e, bool tall, int& row, int& col) {
-  int tile = e >> 8, i = 0;
-  while ((i + 1) * (i + 2) / 2 <= tile) ++i;
-  const int j = tile - i * (i + 1) / 2, a = 4 * ((e >> 6) & 3) + ((e >> 4) & 3), b = e & 15;
+  int i, j;
+  tile_index(e >> 8, i, j);
+  const int a = 4 * ((e >> 6) & 3) + ((e >> 4) & 3), b = e & 15;
   row = tall ? a * MB + i : i * 16 + a;
   col = tall ? b * MB + j : j * 16 + b;
 }
 
-// Tile (i, j) of the product of two commuting symmetric matrices.
+// Tile (i, j) of the product of two commuting symmetric matrices.  Every
+// operand is on its way before the first product waits for one; two chains of
+// products, so that one's latency is the other's issue.
 template <int MB>
 __device__ __forceinline__ f64x4 tile_product(const double* x, const double* y, int i, int j) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  f64x4 acc = {0.0, 0.0, 0.0, 0.0};
+  double xv[4 * MB], yv[4 * MB];
 #pragma unroll
-  for (int k = 0; k < MB * 16; k += 4)
-    acc = __builtin_amdgcn_mfma_f64_16x16x4f64(x[at<MB>(k + q, i * 16 + r)], y[at<MB>(k + q, j * 16 + r)], acc, 0, 0, 0);
-  return acc;
+  for (int k = 0; k < 4 * MB; ++k) {
+    xv[k] = x[at<MB>(4 * k + q, i * 16 + r)];
+    yv[k] = y[at<MB>(4 * k + q, j * 16 + r)];
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  f64x4 a = {0.0, 0.0, 0.0, 0.0}, b = a;
+#pragma unroll
+  for (int k = 0; k < 4 * MB; k += 2) {
+    a = __builtin_amdgcn_mfma_f64_16x16x4f64(xv[k], yv[k], a, 0, 0, 0);
+    b = __builtin_amdgcn_mfma_f64_16x16x4f64(xv[k + 1], yv[k + 1], b, 0, 0, 0);
+  }
+  return a + b;
 }
 template <int MB>
 __device__ __forceinline__ void tile_store(double* z, int i, int j, f64x4 v) {
@@ -225,13 +275,6 @@ __device__ __forceinline__ void tile_store(double* z, int i, int j, f64x4 v) {
     if (i != j) z[at<MB>(col, row)] = v[k];
   }
 }
-template <int MB>
-__device__ __forceinline__ void tile_index(int tile, int& i, int& j) {
-  i = 0;
-  while ((i + 1) * (i + 2) / 2 <= tile) ++i;
-  j = tile - i * (i + 1) / 2;
-}
-
 // From G = U U^T (tile order, `splits` partial sums apart by tiles x 256) to Q
 // / (norm + eps) 2^-t in float32, row-major with 16 MB columns, at `q`; returns
 // 2^t.  lds: 4 matrices and one double.
@@ -241,21 +284,33 @@ __device__ __forceinline__ float thin_steps(const Thin& t, bool tall, const doub
   constexpr int N = 16 * MB, T = kTiles<MB>, SZ = N * kLD<MB>;
   const OrthArgs& o = t.o;
   double *A = lds, *P = lds + SZ, *W = lds + 2 * SZ, *Q = lds + 3 * SZ, *tr = lds + 4 * SZ;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int e = threadIdx.x; e < T * 256; e += kNT) {
-    double s = 0.0;
-    int k = 0;
-    for (; k + 4 <= splits; k += 4) {
-      double v[4];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  // the partial sums in order, every element of a thread's at once
+  constexpr int E = (T * 256 + kNT - 1) / kNT;
+  double sum[E];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = part[(int64_t)(k + u) * (T * 256) + e];
-      s += (v[0] + v[1]) + (v[2] + v[3]);
+  for (int u = 0; u < E; ++u) sum[u] = 0.0;
+  for (int k = 0; k < splits; k += 4) {
+    double v[4][E];
+#pragma unroll
+    for (int l = 0; l < 4; ++l)
+#pragma unroll
+      for (int u = 0; u < E; ++u) {
+        const int e = threadIdx.x + u * kNT;
+        v[l][u] = k + l < splits && e < T * 256 ? part[(int64_t)(k + l) * (T * 256) + e] : 0.0;
+      }
+#pragma unroll
+    for (int u = 0; u < E; ++u) sum[u] += (v[0][u] + v[1][u]) + (v[2][u] + v[3][u]);
+  }
+#pragma unroll
+  for (int u = 0; u < E; ++u) {
+    const int e = threadIdx.x + u * kNT;
+    if (e < T * 256) {
+      int row, col;
+      place<MB>(e, tall, row, col);
+      A[at<MB>(row, col)] = sum[u];
+      A[at<MB>(col, row)] = sum[u];
     }
-    for (; k < splits; ++k) s += part[(int64_t)k * (T * 256) + e];
-    int row, col;
-    place<MB>(e, tall, row, col);
-    A[at<MB>(row, col)] = s;
-    A[at<MB>(col, row)] = s;
   }
   __syncthreads();
   if (wave == 0) {
@@ -271,7 +326,7 @@ __device__ __forceinline__ float thin_steps(const Thin& t, bool tall, const doub
     const bool first = s == 0, last = s + 1 == o.steps;
     for (int tile = wave; tile < T; tile += kNW) {
       int i, j;
-      tile_index<MB>(tile, i, j);
+      tile_index(tile, i, j);
       f64x4 v = tile_product<MB>(A, A, i, j);
       const int r = lane & 15, qq = lane >> 4;
 #pragma unroll
@@ -293,7 +348,7 @@ __device__ __forceinline__ float thin_steps(const Thin& t, bool tall, const doub
       const int item = from + wave + u * kNW;
       if (item < to) {
         int i, j;
-        tile_index<MB>(item < T ? item : item - T, i, j);
+        tile_index(item < T ? item : item - T, i, j);
         held[u] = tile_product<MB>(item < T ? A : Q, P, i, j);
         if (item < T) tile_store<MB>(W, i, j, held[u]);
       }
@@ -304,14 +359,14 @@ __device__ __forceinline__ float thin_steps(const Thin& t, bool tall, const doub
       const int item = from + wave + u * kNW;
       if (item < to && item >= T) {
         int i, j;
-        tile_index<MB>(item - T, i, j);
+        tile_index(item - T, i, j);
         tile_store<MB>(Q, i, j, held[u]);
       }
     }
     if (!last)
       for (int tile = wave; tile < T; tile += kNW) {
         int i, j;
-        tile_index<MB>(tile, i, j);
+        tile_index(tile, i, j);
         tile_store<MB>(A, i, j, tile_product<MB>(W, P, i, j));
       }
     __syncthreads();
@@ -326,99 +381,137 @@ __device__ __forceinline__ float thin_steps(const Thin& t, bool tall, const doub
 }
 
 // ------------------------------------------------------------------ Q X_0
-// N elements of the result, from offset i on (the type is uniform, so one
-// branch in a store costs less than three copies of every kernel).
-template <int N, class PT>
-__device__ __forceinline__ void finish_typed(const OrthArgs& o, int64_t i, int64_t valid, float (&v)[N]) {
-  PT* out = reinterpret_cast<PT*>(o.out) + i;
-  if (o.buffer) {
-    float p[N];
-    load_some<N>(out, valid, p);
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = fmaf(p[j], o.keep, -o.rate * v[j]);
-  }
-  store_some<N>(out, valid, v);
-}
+// N elements of the result or the parameter, as stored; the type is uniform,
+// and one branch in a load or a store costs less than three copies of every
+// kernel.
 template <int N>
-__device__ __forceinline__ void finish_some(const OrthArgs& o, int64_t i, int64_t valid, float (&v)[N]) {
-  if (valid <= 0) return;
-  if (o.odtype == kTF32)
-    finish_typed<N, float>(o, i, valid, v);
-  else if (o.odtype == kTF16)
-    finish_typed<N, f16>(o, i, valid, v);
-  else
-    finish_typed<N, bf16>(o, i, valid, v);
-}
+struct Out {
+  float p[N];
+  __device__ __forceinline__ void load(const OrthArgs& o, int64_t i, int64_t valid) {
+    if (valid <= 0) return;
+    if (o.odtype == kTF32)
+      load_some<N>(reinterpret_cast<const float*>(o.out) + i, valid, p);
+    else if (o.odtype == kTF16)
+      load_some<N>(reinterpret_cast<const f16*>(o.out) + i, valid, p);
+    else
+      load_some<N>(reinterpret_cast<const bf16*>(o.out) + i, valid, p);
+  }
+  __device__ __forceinline__ void store(const OrthArgs& o, int64_t i, int64_t valid, float (&v)[N]) {
+    if (valid <= 0) return;
+    if (o.buffer)
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = fmaf(p[j], o.keep, -o.rate * v[j]);
+    if (o.odtype == kTF32)
+      store_some<N>(reinterpret_cast<float*>(o.out) + i, valid, v);
+    else if (o.odtype == kTF16)
+      store_some<N>(reinterpret_cast<f16*>(o.out) + i, valid, v);
+    else
+      store_some<N>(reinterpret_cast<bf16*>(o.out) + i, valid, v);
+  }
+};
 
-// Columns [c0, c1) of the result; a wave takes 64 (wide) or 16 (tall) at a
+// Columns [c0, c1) of the result; a wave takes 32 (wide) or 16 (tall) at a
 // time and has read all of them before it writes, so the result may replace
-// the input.  qm: Q in LDS, N x (N + 4).
+// the input.  qm: Q in LDS, N x (N + 4); its padding is zero off the diagonal,
+// so that what the loads find past the short side adds nothing.
 template <int MB, bool TALL, class GT>
 __device__ __forceinline__ void apply_part(const Thin& t, int64_t batch, int64_t c0, int64_t c1, int wave, int waves,
                                            const float* qm, float pow2) {
-  constexpr int N = 16 * MB, LD = N + 4;
+  constexpr int N = 16 * MB, LD = N + 4, CW = TALL ? 16 : 32;
   const OrthArgs& o = t.o;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int64_t off = batch * o.rows * o.cols;
   const GT* g = reinterpret_cast<const GT*>(o.g) + off;
-  float* buf = o.buffer ? o.buffer + off : nullptr;
-  if constexpr (TALL) {
-    for (int64_t c = c0 + wave * 16; c < c1; c += waves * 16) {
+  const float* buf = o.buffer ? o.buffer + off : nullptr;
+  const bool grad = !buf || o.nesterov;
+  const auto block = [&](int64_t c, auto vec) {
+    constexpr bool VEC = decltype(vec)::value;
+    if constexpr (TALL) {
+      Raw<4, GT> x[MB];
+      Out<MB> p[4];
+#pragma unroll
+      for (int k = 0; k < MB; ++k)
+        x[k].template load<VEC>(g, buf, (c + r < c1 ? c + r : c1 - 1) * o.cols, k * 16 + q * 4, t.m, grad);
+      if (buf)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t j = c + q * 4 + k;
+          p[k].load(o, off + j * o.cols + r * MB, j < c1 ? t.m - r * MB : 0);
+        }
       float u[MB][4];
 #pragma unroll
       for (int k = 0; k < MB; ++k) {
-        load_u<4, GT, false>(o, g, buf, (c + r) * o.cols + k * 16 + q * 4, c + r < c1 ? t.m - (k * 16 + q * 4) : 0, u[k]);
+        x[k].value(o, buf, false, k * 16 + q * 4, t.m, u[k]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) u[k][j] *= pow2;
       }
       f32x4 acc[MB];
 #pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int i = 0; i < MB; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int k = 0; k < MB; ++k)
+      for (int k = 0; k < MB; ++k)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < MB; ++i)
             acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(u[k][j], qm[(k * 16 + q * 4 + j) * LD + r * MB + i], acc[i], 0, 0, 0);
-      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int64_t j = c + q * 4 + k;
         float v[MB];
 #pragma unroll
         for (int i = 0; i < MB; ++i) v[i] = acc[i][k];
-        finish_some<MB>(o, off + j * o.cols + r * MB, j < c1 ? t.m - r * MB : 0, v);
+        p[k].store(o, off + j * o.cols + r * MB, j < c1 ? t.m - r * MB : 0, v);
       }
-    }
-  } else {
-    for (int64_t c = c0 + wave * 64; c < c1; c += waves * 64) {
-      float u[4 * MB][4];
+    } else {
+      Raw<2, GT> x[4 * MB];
+      Out<2> p[MB][4];
+      const int first = (int)(c - c0) + r * 2, count = (int)(c1 - c0);
 #pragma unroll
       for (int k = 0; k < 4 * MB; ++k) {
         const int row = k * 4 + q;
-        load_u<4, GT, false>(o, g, buf, row * o.cols + c + r * 4, row < t.m ? c1 - (c + r * 4) : 0, u[k]);
+        x[k].template load<VEC>(g, buf, (row < t.m ? row : 0) * o.cols + c0, first, count, grad);
+      }
+      if (buf)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[k][j] *= pow2;
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = i * 16 + q * 4 + k;
+            p[i][k].load(o, off + row * o.cols + c0 + first, row < t.m ? count - first : 0);
+          }
+      float u[4 * MB][2];
+#pragma unroll
+      for (int k = 0; k < 4 * MB; ++k) {
+        x[k].value(o, buf, false, first, count, u[k]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) u[k][j] *= pow2;
       }
 #pragma unroll
       for (int i = 0; i < MB; ++i) {
-        f32x4 acc[4];
+        f32x4 acc[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < 2; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < 4 * MB; ++k) {
           const float a = qm[(k * 4 + q) * LD + i * 16 + r];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, u[k][j], acc[j], 0, 0, 0);
+          for (int j = 0; j < 2; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, u[k][j], acc[j], 0, 0, 0);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int row = i * 16 + q * 4 + k;
-          float v[4] = {acc[0][k], acc[1][k], acc[2][k], acc[3][k]};
-          finish_some<4>(o, off + row * o.cols + c + r * 4, row < t.m ? c1 - (c + r * 4) : 0, v);
+          float v[2] = {acc[0][k], acc[1][k]};
+          p[i][k].store(o, off + row * o.cols + c0 + first, row < t.m ? count - first : 0, v);
         }
       }
     }
+  };
+  for (int64_t c = c0 + wave * CW; c < c1; c += waves * CW) {
+    if (TALL ? t.m % 4 == 0 : c + CW <= c1)
+      block(c, std::true_type());
+    else
+      block(c, std::false_type());
   }
 }
 
@@ -448,7 +541,7 @@ __global__ __launch_bounds__(kNT) void thin_steps_kernel(Thin t) {
 
 template <int MB, bool TALL, class GT>
 __global__ __launch_bounds__(256) void thin_apply_kernel(Thin t) {
-  constexpr int N = 16 * MB, COLS = TALL ? 64 : 256;
+  constexpr int N = 16 * MB, COLS = TALL ? 64 : 128;
   __shared__ float qm[N * (N + 4)];
   const float* q = t.q + (int64_t)blockIdx.y * (64 * 64);
   for (int k = threadIdx.x; k < N * N; k += 256) qm[(k / N) * (N + 4) + k % N] = q[k];
@@ -485,7 +578,7 @@ hipError_t thin_run(const Thin& t, hipStream_t s) {
   }
   hipLaunchKernelGGL((thin_gram_kernel<MB, TALL, GT>), dim3((unsigned)t.splits, batch), dim3(kNT), 0, s, t);
   hipLaunchKernelGGL((thin_steps_kernel<MB>), dim3(batch), dim3(kNT), 0, s, t);
-  constexpr int64_t cols = TALL ? 64 : 256;
+  constexpr int64_t cols = TALL ? 64 : 128;
   hipLaunchKernelGGL((thin_apply_kernel<MB, TALL, GT>), dim3((unsigned)((t.n + cols - 1) / cols), batch), dim3(256), 0, s,
                      t);
   return hipGetLastError();
