@@ -42,17 +42,16 @@ namespace {
 constexpr int kNT = 512;
 constexpr int kNW = kNT / 64;
 typedef double f64x4 __attribute__((ext_vector_type(4)));
+typedef double f64x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 template <int MB>
 constexpr int kTiles = MB * (MB + 1) / 2;
-// Row length of a matrix in LDS: columns are flipped by 16 in odd rows, so
-// that the two rows a half wave reads lie in different banks.
-template <int MB>
-constexpr int kLD = MB <= 2 ? 32 : 64;
+// Place of an element in a matrix in LDS: rows are kept in pairs, so that one
+// 16-byte read gives a lane its elements of two products' rows.
 template <int MB>
 __device__ __forceinline__ int at(int row, int col) {
-  return row * kLD<MB> + (col ^ ((row & 1) << 4));
+  return (row >> 1) * (32 * MB) + col * 2 + (row & 1);
 }
 
 struct Thin {
@@ -244,26 +243,27 @@ __device__ __forceinline__ void place(int e, bool tall, int& row, int& col) {
   col = tall ? b * MB + j : j * 16 + b;
 }
 
-// Tile (i, j) of the product of two commuting symmetric matrices.  Every
-// operand is on its way before the first product waits for one; two chains of
-// products, so that one's latency is the other's issue.
+// One operand of tile row i: elements (row, 16 i + lane & 15) of four pairs of
+// rows a step; the order of the rows is that of the other operand's.
 template <int MB>
-__device__ __forceinline__ f64x4 tile_product(const double* x, const double* y, int i, int j) {
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  double xv[4 * MB], yv[4 * MB];
+struct Strip {
+  f64x2 v[2 * MB];
+  __device__ __forceinline__ void load(const double* x, int i) {
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
 #pragma unroll
-  for (int k = 0; k < 4 * MB; ++k) {
-    xv[k] = x[at<MB>(4 * k + q, i * 16 + r)];
-    yv[k] = y[at<MB>(4 * k + q, j * 16 + r)];
+    for (int k = 0; k < 2 * MB; ++k) v[k] = *reinterpret_cast<const f64x2*>(x + at<MB>(8 * k + 2 * q, i * 16 + r));
   }
-  __builtin_amdgcn_sched_barrier(0);
-  f64x4 a = {0.0, 0.0, 0.0, 0.0}, b = a;
+};
+// Tile of the product of two commuting symmetric matrices.
+template <int MB>
+__device__ __forceinline__ f64x4 tile_product(const Strip<MB>& x, const Strip<MB>& y) {
+  f64x4 a = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-  for (int k = 0; k < 4 * MB; k += 2) {
-    a = __builtin_amdgcn_mfma_f64_16x16x4f64(xv[k], yv[k], a, 0, 0, 0);
-    b = __builtin_amdgcn_mfma_f64_16x16x4f64(xv[k + 1], yv[k + 1], b, 0, 0, 0);
+  for (int k = 0; k < 2 * MB; ++k) {
+    a = __builtin_amdgcn_mfma_f64_16x16x4f64(x.v[k][0], y.v[k][0], a, 0, 0, 0);
+    a = __builtin_amdgcn_mfma_f64_16x16x4f64(x.v[k][1], y.v[k][1], a, 0, 0, 0);
   }
-  return a + b;
+  return a;
 }
 template <int MB>
 __device__ __forceinline__ void tile_store(double* z, int i, int j, f64x4 v) {
@@ -281,7 +281,7 @@ __device__ __forceinline__ void tile_store(double* z, int i, int j, f64x4 v) {
 template <int MB>
 __device__ __forceinline__ float thin_steps(const Thin& t, bool tall, const double* part, int splits, double* lds,
                                             float* q) {
-  constexpr int N = 16 * MB, T = kTiles<MB>, SZ = N * kLD<MB>;
+  constexpr int N = 16 * MB, T = kTiles<MB>, SZ = N * N;
   const OrthArgs& o = t.o;
   double *A = lds, *P = lds + SZ, *W = lds + 2 * SZ, *Q = lds + 3 * SZ, *tr = lds + 4 * SZ;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -324,50 +324,58 @@ __device__ __forceinline__ float thin_steps(const Thin& t, bool tall, const doub
   __syncthreads();
   for (int s = 0; s < o.steps; ++s) {
     const bool first = s == 0, last = s + 1 == o.steps;
+    const int r = lane & 15, q4 = lane >> 4;
+    Strip<MB> x, y, z;
     for (int tile = wave; tile < T; tile += kNW) {
       int i, j;
       tile_index(tile, i, j);
-      f64x4 v = tile_product<MB>(A, A, i, j);
-      const int r = lane & 15, qq = lane >> 4;
+      x.load(A, i);
+      y.load(A, j);
+      f64x4 v = tile_product(x, y);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int row = i * 16 + 4 * k + qq, col = j * 16 + r;
+        const int row = i * 16 + 4 * k + q4, col = j * 16 + r;
         v[k] = fma((double)o.c, v[k], (double)o.b * A[at<MB>(row, col)]);
         if (row == col) v[k] += (double)o.a;
       }
-      tile_store<MB>(first ? Q : P, i, j, v);
-      if (first) tile_store<MB>(P, i, j, v);
+      tile_store<MB>(P, i, j, v);
+      if (first) tile_store<MB>(Q, i, j, v);
     }
     __syncthreads();
-    // W = A P and the new Q side by side: work items 0 .. T - 1 and T .. 2 T - 1
-    constexpr int kMine = (2 * T + kNW - 1) / kNW;
+    // W = A P and the new Q = Q P, tile by tile side by side: they share P's strip
+    constexpr int kMine = (T + kNW - 1) / kNW;
     f64x4 held[kMine];
-    const int from = last ? T : 0, to = first ? T : 2 * T;
 #pragma unroll
     for (int u = 0; u < kMine; ++u) {
-      const int item = from + wave + u * kNW;
-      if (item < to) {
+      const int tile = wave + u * kNW;
+      if (tile < T) {
         int i, j;
-        tile_index(item < T ? item : item - T, i, j);
-        held[u] = tile_product<MB>(item < T ? A : Q, P, i, j);
-        if (item < T) tile_store<MB>(W, i, j, held[u]);
+        tile_index(tile, i, j);
+        y.load(P, j);
+        if (!last) x.load(A, i);
+        if (!first) z.load(Q, i);
+        if (!last) tile_store<MB>(W, i, j, tile_product(x, y));
+        if (!first) held[u] = tile_product(z, y);
       }
     }
     __syncthreads();
+    if (!first)
 #pragma unroll
-    for (int u = 0; u < kMine; ++u) {
-      const int item = from + wave + u * kNW;
-      if (item < to && item >= T) {
-        int i, j;
-        tile_index(item - T, i, j);
-        tile_store<MB>(Q, i, j, held[u]);
+      for (int u = 0; u < kMine; ++u) {
+        const int tile = wave + u * kNW;
+        if (tile < T) {
+          int i, j;
+          tile_index(tile, i, j);
+          tile_store<MB>(Q, i, j, held[u]);
+        }
       }
-    }
     if (!last)
       for (int tile = wave; tile < T; tile += kNW) {
         int i, j;
         tile_index(tile, i, j);
-        tile_store<MB>(A, i, j, tile_product<MB>(W, P, i, j));
+        x.load(W, i);
+        y.load(P, j);
+        tile_store<MB>(A, i, j, tile_product(x, y));
       }
     __syncthreads();
   }
@@ -518,7 +526,7 @@ __device__ __forceinline__ void apply_part(const Thin& t, int64_t batch, int64_t
 // ---------------------------------------------------------------- kernels
 constexpr int kGramLds = kNW * 5 * 256;  // doubles
 template <int MB>
-constexpr int kStepsLds = 4 * 16 * MB * kLD<MB> + 2;
+constexpr int kStepsLds = 4 * 256 * MB * MB + 2;
 template <int MB>
 constexpr int kWholeLds =
     kStepsLds<MB> > kGramLds + kTiles<MB> * 256 ? kStepsLds<MB> : kGramLds + kTiles<MB> * 256;
@@ -554,7 +562,7 @@ __global__ __launch_bounds__(256) void thin_apply_kernel(Thin t) {
 // All of it, where one workgroup takes a whole matrix.
 template <int MB, bool TALL, class GT>
 __global__ __launch_bounds__(kNT) void thin_whole_kernel(Thin t) {
-  constexpr int N = 16 * MB, SZ = N * kLD<MB>;
+  constexpr int N = 16 * MB, SZ = N * N;
   __shared__ double dyn[kWholeLds<MB>];
   // the tile-ordered sums lie behind the waves' sums, where A is not
   double* g = dyn + kGramLds;
