@@ -158,53 +158,63 @@ __device__ __forceinline__ void gram_part(const Thin& t, int64_t batch, int64_t 
   f64x4 acc[kTiles<MB>];
 #pragma unroll
   for (int i = 0; i < kTiles<MB>; ++i) acc[i] = f64x4{0.0, 0.0, 0.0, 0.0};
-  constexpr int CH = 16;  // columns of a wave's chunk
-  const auto chunk = [&](int64_t c, auto vec) {
-    constexpr bool VEC = decltype(vec)::value;
-    if constexpr (TALL) {
-      Raw<MB, GT> x[CH / 4];
+  // a wave's chunk of 16 columns; the next one is on its way while this one is multiplied
+  constexpr int CH = 16, R = TALL ? CH / 4 : MB, E = TALL ? MB : 4;
+  const int count = (int)(c1 - c0);
+  typedef Raw<E, GT> Chunk[R];
+  const auto fetch = [&](int64_t c, Chunk& x) {
+    const auto go = [&](auto vec) {
+      constexpr bool VEC = decltype(vec)::value;
 #pragma unroll
-      for (int s = 0; s < CH / 4; ++s) {
+      for (int s = 0; s < R; ++s) {
+        if constexpr (TALL) {
+          const int64_t j = c + s * 4 + q;
+          x[s].template load<VEC>(g, buf, (j < c1 ? j : c1 - 1) * o.cols, r * MB, t.m, true);
+        } else {
+          const int row = s * 16 + r;
+          x[s].template load<VEC>(g, buf, (row < t.m ? row : 0) * o.cols + c0, (int)(c - c0) + q * 4, count, true);
+        }
+      }
+    };
+    if (TALL ? t.m % MB == 0 : c + CH <= c1)
+      go(std::true_type());
+    else
+      go(std::false_type());
+  };
+  const auto use = [&](int64_t c, Chunk& x) {
+    float u[R][E];
+#pragma unroll
+    for (int s = 0; s < R; ++s) {
+      if constexpr (TALL) {
         const int64_t j = c + s * 4 + q;
-        x[s].template load<VEC>(g, buf, (j < c1 ? j : c1 - 1) * o.cols, r * MB, t.m, true);
-      }
-#pragma unroll
-      for (int s = 0; s < CH / 4; ++s) {
-        const int64_t j = c + s * 4 + q;
-        float u[MB];
-        x[s].value(o, buf, true, r * MB, j < c1 ? t.m : 0, u);
-        if (buf && j < c1 && r * MB < t.m) store_some<MB>(buf + j * o.cols + r * MB, t.m - r * MB, x[s].b.v);
-        gram_step<MB>(u, acc);
-      }
-    } else {
-      Raw<4, GT> x[MB];
-      const int first = (int)(c - c0) + q * 4, count = (int)(c1 - c0);
-#pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        const int row = i * 16 + r;
-        x[i].template load<VEC>(g, buf, (row < t.m ? row : 0) * o.cols + c0, first, count, true);
-      }
-      float u[MB][4];
-#pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        const int row = i * 16 + r;
-        x[i].value(o, buf, true, first, row < t.m ? count : 0, u[i]);
-        if (buf && row < t.m && first < count) store_some<4>(buf + row * o.cols + c0 + first, count - first, x[i].b.v);
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        float y[MB];
-#pragma unroll
-        for (int i = 0; i < MB; ++i) y[i] = u[i][s];
-        gram_step<MB>(y, acc);
+        x[s].value(o, buf, true, r * MB, j < c1 ? t.m : 0, u[s]);
+        if (buf && j < c1 && r * MB < t.m) store_some<E>(buf + j * o.cols + r * MB, t.m - r * MB, x[s].b.v);
+      } else {
+        const int row = s * 16 + r, first = (int)(c - c0) + q * 4;
+        x[s].value(o, buf, true, first, row < t.m ? count : 0, u[s]);
+        if (buf && row < t.m && first < count) store_some<E>(buf + row * o.cols + c0 + first, count - first, x[s].b.v);
       }
     }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      float y[MB];
+#pragma unroll
+      for (int i = 0; i < MB; ++i) y[i] = TALL ? u[s][i] : u[i][s];
+      gram_step<MB>(y, acc);
+    }
   };
-  for (int64_t c = c0 + wave * CH; c < c1; c += kNW * CH) {
-    if (TALL ? t.m % MB == 0 : c + CH <= c1)
-      chunk(c, std::true_type());
-    else
-      chunk(c, std::false_type());
+  int64_t c = c0 + wave * CH;
+  if (c < c1) {
+    Chunk x, next;
+    fetch(c, x);
+    for (; c < c1; c += kNW * CH) {
+      const bool more = c + kNW * CH < c1;
+      if (more) fetch(c + kNW * CH, next);
+      use(c, x);
+      if (more)
+#pragma unroll
+        for (int s = 0; s < R; ++s) x[s] = next[s];
+    }
   }
   // the waves' sums, five tiles at a time, in order
 #pragma unroll
@@ -290,17 +300,17 @@ __device__ __forceinline__ float thin_steps(const Thin& t, bool tall, const doub
   double sum[E];
 #pragma unroll
   for (int u = 0; u < E; ++u) sum[u] = 0.0;
-  for (int k = 0; k < splits; k += 4) {
-    double v[4][E];
+  for (int k = 0; k < splits; k += 8) {
+    double v[8][E];
 #pragma unroll
-    for (int l = 0; l < 4; ++l)
+    for (int l = 0; l < 8; ++l)
 #pragma unroll
       for (int u = 0; u < E; ++u) {
         const int e = threadIdx.x + u * kNT;
         v[l][u] = k + l < splits && e < T * 256 ? part[(int64_t)(k + l) * (T * 256) + e] : 0.0;
       }
 #pragma unroll
-    for (int u = 0; u < E; ++u) sum[u] += (v[0][u] + v[1][u]) + (v[2][u] + v[3][u]);
+    for (int u = 0; u < E; ++u) sum[u] += ((v[0][u] + v[1][u]) + (v[2][u] + v[3][u])) + ((v[4][u] + v[5][u]) + (v[6][u] + v[7][u]));
   }
 #pragma unroll
   for (int u = 0; u < E; ++u) {
@@ -420,7 +430,8 @@ struct Out {
 
 // Columns [c0, c1) of the result; a wave takes 32 (wide) or 16 (tall) at a
 // time and has read all of them before it writes, so the result may replace
-// the input.  qm: Q in LDS, N x (N + 4); its padding is zero off the diagonal,
+// the input.  The summed axis is taken in the order that lets a lane read four
+// of its factors of Q, symmetric, at once.  qm: Q in LDS, N x (N + 4); its padding is zero off the diagonal,
 // so that what the loads find past the short side adds nothing.
 template <int MB, bool TALL, class GT>
 __device__ __forceinline__ void apply_part(const Thin& t, int64_t batch, int64_t c0, int64_t c1, int wave, int waves,
@@ -457,12 +468,15 @@ __device__ __forceinline__ void apply_part(const Thin& t, int64_t batch, int64_t
 #pragma unroll
       for (int i = 0; i < MB; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int k = 0; k < MB; ++k)
+      for (int k = 0; k < MB; ++k) {
+        f32x4 m[MB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) m[i] = *reinterpret_cast<const f32x4*>(qm + (r * MB + i) * LD + k * 16 + q * 4);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int i = 0; i < MB; ++i)
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(u[k][j], qm[(k * 16 + q * 4 + j) * LD + r * MB + i], acc[i], 0, 0, 0);
+          for (int i = 0; i < MB; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(u[k][j], m[i][j], acc[i], 0, 0, 0);
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int64_t j = c + q * 4 + k;
@@ -477,7 +491,7 @@ __device__ __forceinline__ void apply_part(const Thin& t, int64_t batch, int64_t
       const int first = (int)(c - c0) + r * 2, count = (int)(c1 - c0);
 #pragma unroll
       for (int k = 0; k < 4 * MB; ++k) {
-        const int row = k * 4 + q;
+        const int row = (k >> 2) * 16 + q * 4 + (k & 3);
         x[k].template load<VEC>(g, buf, (row < t.m ? row : 0) * o.cols + c0, first, count, grad);
       }
       if (buf)
@@ -500,12 +514,14 @@ __device__ __forceinline__ void apply_part(const Thin& t, int64_t batch, int64_t
         f32x4 acc[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        f32x4 m[MB];
 #pragma unroll
-        for (int k = 0; k < 4 * MB; ++k) {
-          const float a = qm[(k * 4 + q) * LD + i * 16 + r];
+        for (int k = 0; k < MB; ++k) m[k] = *reinterpret_cast<const f32x4*>(qm + (i * 16 + r) * LD + k * 16 + q * 4);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, u[k][j], acc[j], 0, 0, 0);
-        }
+        for (int k = 0; k < 4 * MB; ++k)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(m[k >> 2][k & 3], u[k][j], acc[j], 0, 0, 0);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int row = i * 16 + q * 4 + k;
@@ -541,7 +557,7 @@ __global__ __launch_bounds__(kNT) void thin_gram_kernel(Thin t) {
 
 template <int MB>
 __global__ __launch_bounds__(kNT) void thin_steps_kernel(Thin t) {
-  __shared__ double dyn[kStepsLds<MB>];
+  __shared__ __align__(16) double dyn[kStepsLds<MB>];
   const float p = thin_steps<MB>(t, t.o.rows > t.o.cols, t.part + (int64_t)blockIdx.x * t.splits * (kTiles<MB> * 256),
                                  t.splits, dyn, t.q + (int64_t)blockIdx.x * (64 * 64));
   if (threadIdx.x == 0) t.pow2[blockIdx.x] = p;
@@ -550,9 +566,14 @@ __global__ __launch_bounds__(kNT) void thin_steps_kernel(Thin t) {
 template <int MB, bool TALL, class GT>
 __global__ __launch_bounds__(256) void thin_apply_kernel(Thin t) {
   constexpr int N = 16 * MB, COLS = TALL ? 64 : 128;
-  __shared__ float qm[N * (N + 4)];
+  __shared__ __align__(16) float qm[N * (N + 4)];
   const float* q = t.q + (int64_t)blockIdx.y * (64 * 64);
-  for (int k = threadIdx.x; k < N * N; k += 256) qm[(k / N) * (N + 4) + k % N] = q[k];
+#pragma unroll
+  for (int u = 0; u < (N * N + 1023) / 1024; ++u) {
+    const int k = (u * 256 + threadIdx.x) * 4;
+    if (N * N >= 1024 || k < N * N)
+      *reinterpret_cast<f32x4*>(qm + (k / N) * (N + 4) + k % N) = *reinterpret_cast<const f32x4*>(q + k);
+  }
   const float pow2 = t.pow2[blockIdx.y];
   __syncthreads();
   const int64_t c0 = (int64_t)blockIdx.x * COLS, c1 = c0 + COLS < t.n ? c0 + COLS : t.n;
@@ -563,7 +584,7 @@ __global__ __launch_bounds__(256) void thin_apply_kernel(Thin t) {
 template <int MB, bool TALL, class GT>
 __global__ __launch_bounds__(kNT) void thin_whole_kernel(Thin t) {
   constexpr int N = 16 * MB, SZ = N * N;
-  __shared__ double dyn[kWholeLds<MB>];
+  __shared__ __align__(16) double dyn[kWholeLds<MB>];
   // the tile-ordered sums lie behind the waves' sums, where A is not
   double* g = dyn + kGramLds;
   gram_part<MB, TALL, GT>(t, blockIdx.x, 0, t.n, dyn, g);

@@ -157,7 +157,7 @@ inline OrthPlan orth_plan(int64_t batch, int64_t rows, int64_t cols) {
 constexpr int64_t kThin = 64;
 constexpr double kMaxAmplify = 67108864.0;  // 2^26: leaves float64 2^-27
 struct ThinPlan {
-  int64_t per;  // columns of a workgroup of the first pass, a multiple of 32
+  int64_t per;  // columns of a workgroup of the first pass, a multiple of 16
   int splits;
   size_t at_part, at_q, at_pow2, bytes;
 };
@@ -166,13 +166,14 @@ inline ThinPlan thin_plan(int64_t batch, int64_t rows, int64_t cols) {
   const int64_t n = rows < cols ? cols : rows;
   // a column costs a workgroup 17 ns of float64 products, a partial sum the
   // one that joins them 0.2 us: balanced at sqrt(n / 12) parts, if a workgroup
-  // keeps 256 columns and the launch does not pass 256 workgroups
+  // keeps 128 columns and the launch does not pass the 256 CUs, of which each
+  // holds one
   int64_t s = 1;
   while (12 * (s + 1) * (s + 1) <= n) ++s;
-  const int64_t fill = (256 + batch - 1) / batch, most = (n + 255) / 256;
+  const int64_t fill = batch < 256 ? 256 / batch : 1, most = (n + 127) / 128;
   s = s < fill ? s : fill;
   s = s < most ? s : most;
-  w.per = ((n + s - 1) / s + 31) / 32 * 32;
+  w.per = ((n + s - 1) / s + 15) / 16 * 16;
   w.splits = (int)((n + w.per - 1) / w.per);
   size_t at = 0;
   auto take = [&at](size_t bytes) {
