@@ -37,6 +37,7 @@ namespace {
 constexpr int kNT = 256;
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // Offset of element (row, col) of a pair matrix whose rows have `kpad` columns.
@@ -166,9 +167,10 @@ struct Product {
   int64_t sA, sB;      // batch strides, elements
   int64_t kpad;        // columns of both operands
   int ksteps;          // steps of 32 columns that are not all padding
-  int tiles_m, tiles_n;
-  int splits;          // workgroups that share one tile's columns
-  float* part;         // their float32 sums, when splits > 1
+  int tiles, tiles_n;  // of one matrix
+  int whole;           // tiles, of all matrices, that one workgroup computes
+  int splits;          // workgroups that share the columns of each of the others
+  float* part;         // their float32 sums
   int step;
   float sa, sp;        // scales of A and of P
   f16 *out, *outT;     // pair matrices written (outT: the transpose, of kUpdate)
@@ -234,8 +236,11 @@ __device__ __forceinline__ void store_result(const OrthArgs& o, int64_t batch, i
     *out = (PT)v;
 }
 
+// Four values of a thread: rows r..r+3 (of fragment fi's group q) and one
+// column (of fragment fj) of a tile.
 template <int T, int KIND, class PT>
-__device__ __forceinline__ void epilogue(const Product& p, int batch, int ti, int tj, f32x16 (&acc)[kFrag<T>][kFrag<T>]) {
+__device__ __forceinline__ void epilogue(const Product& p, int batch, int ti, int tj, int fi, int fj, int q,
+                                         float (&v)[4]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float* xs = p.o.scales + (int64_t)batch * (p.o.steps + 1) + p.step;
   float f;
@@ -248,41 +253,32 @@ __device__ __forceinline__ void epilogue(const Product& p, int batch, int ti, in
   else
     f = 1.0f / (p.sp * xs[0]);
   f16* out = p.out + (int64_t)batch * p.sOut;
+  const int64_t j = (int64_t)tj * T + (wave & 1) * (T / 2) + fj * 32 + (lane & 31);
+  const int64_t i = (int64_t)ti * T + (wave >> 1) * (T / 2) + fi * 32 + q * 8 + (lane >> 5) * 4;
 #pragma unroll
-  for (int fi = 0; fi < kFrag<T>; ++fi)
+  for (int r = 0; r < 4; ++r) v[r] *= f;
+  if constexpr (KIND == kPoly) {
+    const f16* gp = p.gram + (int64_t)batch * p.sOut + pair_at(j, i, p.out_pad);
+    const f16x4 gh = *reinterpret_cast<const f16x4*>(gp), gl = *reinterpret_cast<const f16x4*>(gp + 32);
 #pragma unroll
-    for (int fj = 0; fj < kFrag<T>; ++fj) {
-      const int64_t j = (int64_t)tj * T + (wave & 1) * (T / 2) + fj * 32 + (lane & 31);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t i = (int64_t)ti * T + (wave >> 1) * (T / 2) + fi * 32 + q * 8 + (lane >> 5) * 4;
-        float v[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = acc[fi][fj][q * 4 + r] * f;
-        if constexpr (KIND == kPoly) {
-          const f16* gp = p.gram + (int64_t)batch * p.sOut + pair_at(j, i, p.out_pad);
-          const f16x4 gh = *reinterpret_cast<const f16x4*>(gp), gl = *reinterpret_cast<const f16x4*>(gp + 32);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            v[r] = fmaf(p.o.b * p.sp / p.sa, (float)gh[r] + (float)gl[r], v[r]);
-            if (i + r == j) v[r] += p.o.a * p.sp;
-          }
-        }
-        if constexpr (KIND == kGram || KIND == kPoly) {
-          store_pair4(out, j, i, p.out_pad, v);
-          if (ti != tj)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) store_pair1(out, i + r, j, p.out_pad, v[r]);
-        } else if constexpr (KIND == kUpdate) {
-          store_pair4(p.outT + (int64_t)batch * p.sOut, j, i, p.outT_pad, v);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) store_pair1(out, i + r, j, p.out_pad, v[r]);
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) store_result<PT>(p.o, batch, i + r, j, v[r]);
-        }
-      }
+    for (int r = 0; r < 4; ++r) {
+      v[r] = fmaf(p.o.b * p.sp / p.sa, (float)gh[r] + (float)gl[r], v[r]);
+      if (i + r == j) v[r] += p.o.a * p.sp;
     }
+  }
+  if constexpr (KIND == kGram || KIND == kPoly) {
+    store_pair4(out, j, i, p.out_pad, v);
+    if (ti != tj)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) store_pair1(out, i + r, j, p.out_pad, v[r]);
+  } else if constexpr (KIND == kUpdate) {
+    store_pair4(p.outT + (int64_t)batch * p.sOut, j, i, p.outT_pad, v);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) store_pair1(out, i + r, j, p.out_pad, v[r]);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) store_result<PT>(p.o, batch, i + r, j, v[r]);
+  }
 }
 
 // Loads one step (32 columns, T rows, 128 bytes a row) of an operand to LDS.
@@ -307,47 +303,83 @@ __device__ __forceinline__ f16x8 fragment(const f16* lds, int row, int chunk) {
   return *reinterpret_cast<const f16x8*>(lds + row * 64 + ((chunk ^ (row & 7)) << 3));
 }
 
+// The first products' fragments are read, then one more with every product.
 template <int T>
 __device__ __forceinline__ void multiply_step(const f16* la, const f16* lb, f32x16 (&acc)[kFrag<T>][kFrag<T>]) {
   constexpr int F = kFrag<T>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int ra = (wave >> 1) * (T / 2) + (lane & 31), rb = (wave & 1) * (T / 2) + (lane & 31);
+  f16x8 ah[2][F], al[2][F], bh[2][F], bl[2][F];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int ch = s * 2 + (lane >> 5);
-    f16x8 ah[F], al[F], bh[F], bl[F];
 #pragma unroll
     for (int i = 0; i < F; ++i) {
-      ah[i] = fragment<T>(la, ra + i * 32, ch);
-      bh[i] = fragment<T>(lb, rb + i * 32, ch);
-      al[i] = fragment<T>(la, ra + i * 32, ch + 4);
-      bl[i] = fragment<T>(lb, rb + i * 32, ch + 4);
+      ah[s][i] = fragment<T>(la, ra + i * 32, ch);
+      bh[s][i] = fragment<T>(lb, rb + i * 32, ch);
     }
 #pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-      for (int j = 0; j < F; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah[i], bh[j], acc[i][j], 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-      for (int j = 0; j < F; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah[i], bl[j], acc[i][j], 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-      for (int j = 0; j < F; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(al[i], bh[j], acc[i][j], 0, 0, 0);
+    for (int i = 0; i < F; ++i) {
+      bl[s][i] = fragment<T>(lb, rb + i * 32, ch + 4);
+      al[s][i] = fragment<T>(la, ra + i * 32, ch + 4);
+    }
   }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah[s][i], bh[s][j], acc[i][j], 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah[s][i], bl[s][j], acc[i][j], 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(al[s][i], bh[s][j], acc[i][j], 0, 0, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x100, 2 * F, 0);
+#pragma unroll
+  for (int i = 0; i < 6 * F; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, 6 * F * F - 6 * F, 0);
 }
 
-// One tile of a product: grid (tiles x splits, batch).
+// Steps of the long axis that are on their way to LDS at a time, the one in
+// use counted: a small tile is done with a step before the next could arrive.
+template <int T>
+constexpr int kStages = T == 64 ? 4 : 2;
+
+// Waits for all but the newest N steps' loads of this wave and for what it has
+// read of LDS, then for the other waves.  (A workgroup fence would wait for
+// every load; one block, and ordered with memory, so that no read of LDS is
+// still on its way when another wave's loads overwrite it.)
+template <int T, int N>
+__device__ __forceinline__ void wait_step() {
+  constexpr int vm = N * 2 * (T / 32);  // loads a wave issues per step
+  __builtin_amdgcn_s_waitcnt((vm & 15) | 0x0070 | ((vm >> 4) << 14));  // the same, known to the compiler
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(vm) : "memory");
+}
+
+// One tile of a product, or a share of its columns.
 template <int T, int KIND, class PT>
 __global__ __launch_bounds__(kNT) void product_kernel(Product p) {
-  constexpr int F = kFrag<T>;
+  constexpr int F = kFrag<T>, S = kStages<T>;
+  // arrays of their own, so that a read of one is known not to wait for another's loads
   __shared__ __align__(16) f16 a0[T * 64], b0[T * 64], a1[T * 64], b1[T * 64];
-  const int tiles = gridDim.x / p.splits;
-  const int t = blockIdx.x % tiles, sp = blockIdx.x / tiles, batch = blockIdx.y;
+  __shared__ __align__(16) f16 a2[S > 2 ? T * 64 : 8], b2[S > 2 ? T * 64 : 8], a3[S > 2 ? T * 64 : 8], b3[S > 2 ? T * 64 : 8];
+  const int rest = (int)blockIdx.x - p.whole;
+  const int all = rest < 0 ? (int)blockIdx.x : p.whole + rest / p.splits, sp = rest < 0 ? 0 : rest % p.splits;
+  const int batch = all / p.tiles;
   int ti, tj;
-  tile_of(KIND == kGram || KIND == kPoly, t, p.tiles_n, ti, tj);
-  const int per = (p.ksteps + p.splits - 1) / p.splits;
+  tile_of(KIND == kGram || KIND == kPoly, all - batch * p.tiles, p.tiles_n, ti, tj);
+  const int per = rest < 0 ? p.ksteps : (p.ksteps + p.splits - 1) / p.splits;
   const int k0 = sp * per, k1 = k0 + per < p.ksteps ? k0 + per : p.ksteps;
   const int64_t pitch = 2 * p.kpad;
   const f16* A = p.A + batch * p.sA + (int64_t)ti * T * pitch;
@@ -359,83 +391,110 @@ __global__ __launch_bounds__(kNT) void product_kernel(Product p) {
     for (int j = 0; j < F; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-  if (k0 < k1) {
-    load_step<T>(A, pitch, k0, a0);
-    load_step<T>(B, pitch, k0, b0);
-  }
-  for (int k = k0; k < k1; k += 2) {
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    if (k + 1 < k1) {
-      load_step<T>(A, pitch, k + 1, a1);
-      load_step<T>(B, pitch, k + 1, b1);
+  const auto load = [&](int k, f16* la, f16* lb) {
+    if (k < k1) {
+      load_step<T>(A, pitch, k, la);
+      load_step<T>(B, pitch, k, lb);
     }
-    multiply_step<T>(a0, b0, acc);
-    if (k + 1 < k1) {
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
-      if (k + 2 < k1) {
-        load_step<T>(A, pitch, k + 2, a0);
-        load_step<T>(B, pitch, k + 2, b0);
-      }
-      multiply_step<T>(a1, b1, acc);
+  };
+  // step k, whose loads are complete, and the loads of step k + S - 1 into the
+  // buffer that step k - 1 has left
+  const auto step = [&](int k, f16* la, f16* lb, f16* na, f16* nb) {
+    if (k >= k1) return;
+    const int newer = k1 - 1 - k;
+    if (newer >= S - 2)
+      wait_step<T, S - 2>();
+    else if (S > 3 && newer == 1)
+      wait_step<T, 1>();
+    else
+      wait_step<T, 0>();
+    load(k + S - 1, na, nb);
+    multiply_step<T>(la, lb, acc);
+  };
+  load(k0, a0, b0);
+  if constexpr (S == 2) {
+    for (int k = k0; k < k1; k += 2) {
+      step(k, a0, b0, a1, b1);
+      step(k + 1, a1, b1, a0, b0);
+    }
+  } else {
+    load(k0 + 1, a1, b1);
+    load(k0 + 2, a2, b2);
+    for (int k = k0; k < k1; k += 4) {
+      step(k, a0, b0, a3, b3);
+      step(k + 1, a1, b1, a0, b0);
+      step(k + 2, a2, b2, a1, b1);
+      step(k + 3, a3, b3, a2, b2);
     }
   }
-  if (p.splits > 1) {
-    float* out = p.part + (((int64_t)batch * tiles + t) * p.splits + sp) * (T * T) + threadIdx.x;
+  if (rest >= 0 && p.splits > 1) {
+    float* out = p.part + (int64_t)rest * (T * T) + threadIdx.x * 4;
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
       for (int j = 0; j < F; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) out[((i * F + j) * 16 + r) * kNT] = acc[i][j][r];
+        for (int q = 0; q < 4; ++q) {
+          f32x4 v;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = acc[i][j][q * 4 + r];
+          *reinterpret_cast<f32x4*>(out + ((i * F + j) * 4 + q) * (4 * kNT)) = v;
+        }
     return;
   }
-  epilogue<T, KIND, PT>(p, batch, ti, tj, acc);
-}
-
-// Joins the shared sums of one tile, in order, and finishes it.
-template <int T, int KIND, class PT>
-__global__ __launch_bounds__(kNT) void finish_kernel(Product p) {
-  constexpr int F = kFrag<T>;
-  const int t = blockIdx.x, batch = blockIdx.y;
-  int ti, tj;
-  tile_of(KIND == kGram || KIND == kPoly, t, p.tiles_n, ti, tj);
-  f32x16 acc[F][F];
-  const float* in = p.part + ((int64_t)batch * gridDim.x + t) * p.splits * (T * T) + threadIdx.x;
 #pragma unroll
   for (int i = 0; i < F; ++i)
 #pragma unroll
     for (int j = 0; j < F; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        float s = 0.0f;
-        for (int q = 0; q < p.splits; ++q) s += in[(int64_t)q * (T * T) + ((i * F + j) * 16 + r) * kNT];
-        acc[i][j][r] = s;
+      for (int q = 0; q < 4; ++q) {
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = acc[i][j][q * 4 + r];
+        epilogue<T, KIND, PT>(p, batch, ti, tj, i, j, q, v);
       }
-  epilogue<T, KIND, PT>(p, batch, ti, tj, acc);
 }
 
-int tile_count(bool sym, int tm, int tn) { return sym ? tm * (tm + 1) / 2 : tm * tn; }
+// Joins the shares of a tile, in order, and finishes it: blockIdx.y is the
+// part of the accumulators, four values a thread.
+template <int T, int KIND, class PT>
+__global__ __launch_bounds__(kNT) void finish_kernel(Product p) {
+  constexpr int F = kFrag<T>;
+  const int all = p.whole + (int)blockIdx.x, batch = all / p.tiles, unit = blockIdx.y;
+  int ti, tj;
+  tile_of(KIND == kGram || KIND == kPoly, all - batch * p.tiles, p.tiles_n, ti, tj);
+  const float* in = p.part + (int64_t)blockIdx.x * p.splits * (T * T) + unit * (4 * kNT) + threadIdx.x * 4;
+  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+  int k = 0;
+  for (; k + 8 <= p.splits; k += 8) {
+    f32x4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const f32x4*>(in + (int64_t)(k + u) * (T * T));
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s += v[u];
+  }
+  for (; k < p.splits; ++k) s += *reinterpret_cast<const f32x4*>(in + (int64_t)k * (T * T));
+  float v[4] = {s[0], s[1], s[2], s[3]};
+  epilogue<T, KIND, PT>(p, batch, ti, tj, unit / (4 * F), unit / 4 % F, unit % 4, v);
+}
 
 template <int T, int KIND, class PT>
-hipError_t launch_product_t(Product p, int64_t rows, int64_t cols, int64_t batch, hipStream_t s) {
-  const bool sym = KIND == kGram || KIND == kPoly;
-  p.tiles_m = (int)(rows / T);
+hipError_t launch_product_t(Product p, const OrthShare& w, int64_t cols, hipStream_t s) {
+  p.tiles = (int)w.tiles;
   p.tiles_n = (int)(cols / T);
-  const int tiles = tile_count(sym, p.tiles_m, p.tiles_n);
-  p.splits = orth_splits((int64_t)tiles * batch, p.ksteps);
-  hipLaunchKernelGGL((product_kernel<T, KIND, PT>), dim3((unsigned)(tiles * p.splits), (unsigned)batch), dim3(kNT), 0, s, p);
-  if (p.splits > 1)
-    hipLaunchKernelGGL((finish_kernel<T, KIND, PT>), dim3((unsigned)tiles, (unsigned)batch), dim3(kNT), 0, s, p);
+  p.whole = (int)w.whole;
+  p.splits = w.splits;
+  hipLaunchKernelGGL((product_kernel<T, KIND, PT>), dim3((unsigned)(w.whole + w.rest * w.splits)), dim3(kNT), 0, s, p);
+  if (w.splits > 1)
+    hipLaunchKernelGGL((finish_kernel<T, KIND, PT>), dim3((unsigned)w.rest, T == 128 ? 16 : 4), dim3(kNT), 0, s, p);
   return hipGetLastError();
 }
 
 template <int KIND, class PT>
 hipError_t launch_product(const Product& p, int64_t rows, int64_t cols, int64_t batch, hipStream_t s) {
-  const bool sym = KIND == kGram || KIND == kPoly;
-  if (orth_tile(rows, cols, batch, sym) == 64) return launch_product_t<64, KIND, PT>(p, rows, cols, batch, s);
-  return launch_product_t<128, KIND, PT>(p, rows, cols, batch, s);
+  const OrthShare w = orth_share(rows, cols, batch, KIND == kGram || KIND == kPoly, p.ksteps);
+  if (w.tile == 64) return launch_product_t<64, KIND, PT>(p, w, cols, s);
+  return launch_product_t<128, KIND, PT>(p, w, cols, s);
 }
 
 template <class GT, class PT>

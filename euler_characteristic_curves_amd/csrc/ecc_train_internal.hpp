@@ -94,24 +94,40 @@ bool orth_bounds(OrthArgs& o);
 
 inline int64_t orth_pad(int64_t n) { return n <= 64 ? 64 : (n + 127) / 128 * 128; }
 
-// Tile of a product with `rows` x `cols` (padded) results.
-inline int orth_tile(int64_t rows, int64_t cols, int64_t batch, bool sym) {
-  if (rows < 128 || cols < 128) return 64;
-  const int64_t tm = rows / 128, tn = cols / 128, tiles = (sym ? tm * (tm + 1) / 2 : tm * tn) * batch;
-  return tiles >= 96 ? 128 : 64;
-}
-// Workgroups that share the summed axis of a tile: enough of them for every
-// CU, each with at least 8 steps of 32 columns.
-inline int orth_splits(int64_t tiles, int ksteps) {
-  int64_t s = 256 / tiles, most = ksteps / 8;
-  s = s < most ? s : most;
-  return s < 1 ? 1 : (int)s;
+// How a product of `batch` matrices of `rows` x `cols` (padded) results is
+// shared out: `whole` tiles by a workgroup each, the `rest` by `splits` each.
+struct OrthShare {
+  int64_t tile, tiles, whole, rest;
+  int splits;
+};
+inline OrthShare orth_share(int64_t rows, int64_t cols, int64_t batch, bool sym, int ksteps) {
+  OrthShare w{};
+  const auto count = [&](int64_t t) {
+    const int64_t tm = rows / t, tn = cols / t;
+    return sym ? tm * (tm + 1) / 2 : tm * tn;
+  };
+  w.tile = 64;
+  if (rows >= 128 && cols >= 128 && count(128) * batch * (ksteps >= 16 ? ksteps / 8 : 1) >= 192) w.tile = 128;
+  w.tiles = count(w.tile);
+  const int64_t all = w.tiles * batch, slots = w.tile == 128 ? 512 : 1024;
+  w.whole = all / slots * slots;
+  w.rest = all - w.whole;
+  w.splits = 1;
+  // a share keeps 8 steps, and shares cost a launch more, some 4 us, which is 8 to 16 steps
+  if (w.rest && ksteps >= 24) {
+    int64_t s = slots / w.rest;
+    s = s < ksteps / 8 ? s : ksteps / 8;
+    w.splits = s < 1 ? 1 : (int)s;
+  }
+  if (w.splits == 1) {
+    w.whole = all;
+    w.rest = 0;
+  }
+  return w;
 }
 inline size_t orth_part_bytes(int64_t rows, int64_t cols, int64_t batch, bool sym, int64_t k) {
-  const int64_t T = orth_tile(rows, cols, batch, sym), tm = rows / T, tn = cols / T;
-  const int64_t tiles = (sym ? tm * (tm + 1) / 2 : tm * tn) * batch;
-  const int s = orth_splits(tiles, (int)((k + 31) / 32));
-  return s > 1 ? (size_t)(tiles * s * T * T) * sizeof(float) : 0;
+  const OrthShare w = orth_share(rows, cols, batch, sym, (int)((k + 31) / 32));
+  return w.splits > 1 ? (size_t)(w.rest * w.splits * w.tile * w.tile) * sizeof(float) : 0;
 }
 
 // Workspace: offsets in bytes.
