@@ -27,9 +27,10 @@ __all__ = list(_API + _TRAIN_API)
 
 def __getattr__(name):
     if name in _API:
-        from . import ecc as _ecc
-        return getattr(_ecc, name)
-    if name in _TRAIN_API:
-        from . import train as _train
-        return getattr(_train, name)
-    raise AttributeError(name)
+        from . import ecc as _module
+    elif name in _TRAIN_API:
+        from . import train as _module
+    else:
+        raise AttributeError(name)
+    globals()[name] = value = getattr(_module, name)  # found without this call from now on
+    return value

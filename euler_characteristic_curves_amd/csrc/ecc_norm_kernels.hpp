@@ -197,6 +197,77 @@ __global__ __launch_bounds__(kNT) void norm_stats_kernel(NormGeom g, const T* x,
   });
 }
 
+// Sums NV values of column q of the partial rows at, at + step, ..., below n.
+template <int NV>
+__device__ __forceinline__ void add_rows(const double* q, int64_t prow, int at, int step, int n, double (&s)[NV]) {
+  int r = at;
+  for (; r + 3 * step < n; r += 4 * step) {
+    double v[4][NV];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[u][i] = q[(int64_t)(r + u * step) * prow + i];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] += (v[0][i] + v[1][i]) + (v[2][i] + v[3][i]);
+  }
+  for (; r < n; r += step)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] += q[(int64_t)r * prow + i];
+}
+
+__device__ __forceinline__ void group_stats(double s1, double s2, double n, float eps, float* st) {
+  const double mean = s1 / n;
+  double var = s2 / n - mean * mean;
+  var = var < 0.0 ? 0.0 : var;
+  st[0] = (float)mean;
+  st[1] = (float)(1.0 / sqrt(var + (double)eps));
+}
+
+// Where a sample's partial rows are few (at most 64 KB), every
+// workgroup of the second pass joins them itself, which costs less than a
+// launch between the passes (3 to 4 us).  Returns this sample's statistics.
+constexpr int kHereChannels = 512;
+struct JoinLds {
+  double sum[2][kHereChannels];
+  float st[2 * kHereChannels];
+};
+__device__ __forceinline__ const float* join_here(const NormArgs& p, const double* part, int NB, int D, int64_t prow,
+                                                  JoinLds& lds) {
+  const int C = (int)p.C, G = (int)p.G, W = C < kNT ? C : kNT, parts = kNT / W;
+  const int at = threadIdx.x % W, pt = threadIdx.x / W;
+  const double* rows = part + (int64_t)blockIdx.y * NB * prow;
+  if (pt < parts)
+    for (int c = at; c < C; c += W) {
+      double s[2] = {0.0, 0.0};
+      add_rows<2>(rows + (int64_t)c * 2, prow, pt, parts, NB, s);
+      lds.sum[0][pt * C + c] = s[0];  // parts C <= kHereChannels: parts is 1 where C exceeds kNT
+      lds.sum[1][pt * C + c] = s[1];
+    }
+  __syncthreads();
+  int P = 1;  // threads of a group
+  while (P < 64 && 2 * P * G <= kNT) P *= 2;
+  const int q = threadIdx.x % P, n = D * parts;
+  for (int g0 = 0; g0 < G; g0 += kNT / P) {
+    const int g = g0 + threadIdx.x / P;
+    double s1 = 0.0, s2 = 0.0;
+    if (g < G)
+      for (int e = q; e < n; e += P) {
+        const int i = (e / D) * C + g * D + e % D;
+        s1 += lds.sum[0][i];
+        s2 += lds.sum[1][i];
+      }
+    for (int d = 1; d < P; d *= 2) {
+      s1 += __shfl_xor(s1, d);
+      s2 += __shfl_xor(s2, d);
+    }
+    if (g < G && q == 0) group_stats(s1, s2, (double)p.S * (double)D, p.eps, lds.st + 2 * g);
+  }
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < 2 * G; i += kNT) p.stats[(int64_t)blockIdx.y * G * 2 + i] = lds.st[i];
+  return lds.st;
+}
+
 // What the passes after the statistics keep per channel.  Float32 features are
 // centred before they are scaled, so that a group that is constant, or nearly
 // so, keeps its digits.  16-bit features have far fewer of them, and take u = x
@@ -207,7 +278,9 @@ struct Affine {
   static constexpr bool kFold = sizeof(T) == 2;
   float mean[K][V], a[K][V], b[K][V];
   __device__ void load(const NormArgs& p, const Cols<V, K>& col, int D) {
-    const float* st = p.stats + (int64_t)blockIdx.y * p.G * 2;
+    load(p, col, D, p.stats + (int64_t)blockIdx.y * p.G * 2);
+  }
+  __device__ void load(const NormArgs& p, const Cols<V, K>& col, int D, const float* st) {
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -225,10 +298,15 @@ struct Affine {
 };
 
 template <class T, int V, int K, int ACT>
-__global__ __launch_bounds__(kNT) void norm_apply_kernel(NormGeom g, NormArgs p, int D) {
+__global__ __launch_bounds__(kNT) void norm_apply_kernel(NormGeom g, NormArgs p, int D, const double* part, int NB,
+                                                         int64_t prow) {
+  __shared__ JoinLds lds;
   Cols<V, K> col(g);
   Affine<T, V, K> af;
-  af.load(p, col, D);
+  if (part)
+    af.load(p, col, D, join_here(p, part, NB, D, prow, lds));
+  else
+    af.load(p, col, D);
   const int64_t base = (int64_t)blockIdx.y * g.S * g.C;
   const T* xs = reinterpret_cast<const T*>(p.x) + base;
   T* ys = reinterpret_cast<T*>(p.y) + base;
@@ -262,10 +340,15 @@ __device__ __forceinline__ float row_sum(float s, int l, int L) {
 }
 
 template <class T, int V, int K, int ACT>
-__global__ __launch_bounds__(kNT) void readout_apply_kernel(NormGeom g, NormArgs p, int D) {
+__global__ __launch_bounds__(kNT) void readout_apply_kernel(NormGeom g, NormArgs p, int D, const double* part, int NB,
+                                                            int64_t prow) {
+  __shared__ JoinLds lds;
   Cols<V, K> col(g);
   Affine<T, V, K> af;
-  af.load(p, col, D);
+  if (part)
+    af.load(p, col, D, join_here(p, part, NB, D, prow, lds));
+  else
+    af.load(p, col, D);
   float r[K][V];
 #pragma unroll
   for (int k = 0; k < K; ++k)
@@ -457,24 +540,6 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   return t;
 }
 
-// Sums NV values of column q of the partial rows at, at + step, ..., below n.
-template <int NV>
-__device__ __forceinline__ void add_rows(const double* q, int64_t prow, int at, int step, int n, double (&s)[NV]) {
-  int r = at;
-  for (; r + 3 * step < n; r += 4 * step) {
-    double v[4][NV];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[u][i] = q[(int64_t)(r + u * step) * prow + i];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] += (v[0][i] + v[1][i]) + (v[2][i] + v[3][i]);
-  }
-  for (; r < n; r += step)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] += q[(int64_t)r * prow + i];
-}
-
 // Partial rows to fewer: row blockIdx.y of `out` is the sum of `per` rows of
 // `in`, 256 columns per workgroup (norm_fold on the host says when).
 __global__ __launch_bounds__(kJT) void norm_fold_kernel(const double* in, double* out, int NB, int per, int64_t cols,
@@ -501,13 +566,7 @@ __global__ __launch_bounds__(kJT) void norm_join_kernel(NormArgs p, const double
   if (pt < parts)
     for (int64_t c = at; c < D; c += W) add_rows<2>(part + b * NB * prow + (gr * D + c) * 2, prow, pt, parts, NB, s);
   const double s1 = block_sum(s[0], lds), s2 = block_sum(s[1], lds);
-  if (threadIdx.x == 0) {
-    const double n = (double)p.S * (double)D, mean = s1 / n;
-    double var = s2 / n - mean * mean;
-    var = var < 0.0 ? 0.0 : var;
-    p.stats[(b * p.G + gr) * 2] = (float)mean;
-    p.stats[(b * p.G + gr) * 2 + 1] = (float)(1.0 / sqrt(var + (double)p.eps));
-  }
+  if (threadIdx.x == 0) group_stats(s1, s2, (double)p.S * (double)D, p.eps, p.stats + (b * p.G + gr) * 2);
 }
 
 // Joins the partial rows of one sample and group: channel sums with A2 scaled
@@ -649,18 +708,23 @@ hipError_t norm_launch_fwd(const NormArgs& a, hipStream_t stream) {
     constexpr int VV = v.value, KK = k.value;
     hipLaunchKernelGGL((norm_stats_kernel<T, VV, KK>), grid, block, 0, stream, g, reinterpret_cast<const T*>(a.x), part,
                        prow);
-    double* from = part;
-    int NB = g.NB;
-    norm_fold(a, from, NB, 2 * a.C, prow, 2, stream);
-    hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)a.G, (unsigned)a.B), dim3(kJT), 0, stream, a, from, NB, D, prow);
+    // 64 KB of partial rows a workgroup, read from L2, at most
+    const bool here = a.C <= kHereChannels && (int64_t)g.NB * a.C * 2 * (int64_t)sizeof(double) <= 64 * 1024;
+    if (!here) {
+      double* from = part;
+      int NB = g.NB;
+      norm_fold(a, from, NB, 2 * a.C, prow, 2, stream);
+      hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)a.G, (unsigned)a.B), dim3(kJT), 0, stream, a, from, NB, D, prow);
+    }
+    const double* joined = here ? part : nullptr;
     NormGeom ga = g;
     ga.NB = (int)norm_blocks(a.B, a.S, a.C, kNormApply);
     const dim3 apply((unsigned)ga.NB, (unsigned)a.B, (unsigned)g.chunks);
     return with_act(a.act, [&](auto act) {
       if (a.field)
-        hipLaunchKernelGGL((readout_apply_kernel<T, VV, KK, act.value>), apply, block, 0, stream, ga, a, D);
+        hipLaunchKernelGGL((readout_apply_kernel<T, VV, KK, act.value>), apply, block, 0, stream, ga, a, D, joined, g.NB, prow);
       else
-        hipLaunchKernelGGL((norm_apply_kernel<T, VV, KK, act.value>), apply, block, 0, stream, ga, a, D);
+        hipLaunchKernelGGL((norm_apply_kernel<T, VV, KK, act.value>), apply, block, 0, stream, ga, a, D, joined, g.NB, prow);
       return hipGetLastError();
     });
   });

@@ -41,12 +41,12 @@ def _param_ptr(t):
     return None if t is None else t.data_ptr()
 
 
-class _NormCall:
-    """Checked arguments of one norm: sizes, types and the C argument block."""
+class _NormPlan:
+    """What a norm call needs besides its tensors: checked once, kept for the backward pass."""
 
-    __slots__ = ("x", "weight", "bias", "readout", "offset", "sizes", "dtype", "pdtype", "act", "nbytes")
+    __slots__ = ("sizes", "dtype", "pdtype", "act", "nbytes", "read")
 
-    def __init__(self, x, groups, weight, bias, act, readout=None, offset=None, with_readout=False):
+    def __init__(self, x, groups, weight, bias, act, readout=None, offset=None, read=False):
         _dev_tensor(x, "x")
         if x.dtype not in _DTYPES:
             raise TypeError(f"x dtype {x.dtype} not supported (float32, float16 or bfloat16)")
@@ -54,66 +54,64 @@ class _NormCall:
             raise ValueError("x must be [batch, *space, channels]")
         if act not in _ACTS:
             raise ValueError(f"act must be one of {sorted(_ACTS)} (got {act!r})")
-        C = x.shape[-1]
+        shape = x.shape
+        B, C = shape[0], shape[-1]
         if isinstance(groups, bool) or not isinstance(groups, int):
             raise TypeError(f"groups must be an int (got {type(groups).__name__})")
         if groups < 1 or C < 1 or C % groups:
             raise ValueError(f"groups={groups} does not divide channels={C}")
-        if with_readout and readout is None:
+        if read and readout is None:
             raise TypeError("readout must be a torch.Tensor")
         pdtype = None
         for t, name, n in ((weight, "weight", C), (bias, "bias", C), (readout, "readout", C), (offset, "offset", 1)):
             if t is None:
                 continue
             _dev_tensor(t, name, None, x.device)
-            if tuple(t.shape) != (n,):
+            if t.dim() != 1 or t.numel() != n:
                 raise ValueError(f"{name} must be [{n}] (got {list(t.shape)})")
             if t.dtype != torch.float32 and t.dtype != x.dtype:
                 raise TypeError(f"{name} must be torch.float32 or x's {x.dtype} (got {t.dtype})")
             if pdtype is not None and t.dtype != pdtype:
                 raise TypeError(f"{name} is {t.dtype}, the parameters before it {pdtype}")
             pdtype = t.dtype
-        self.x, self.weight, self.bias, self.readout, self.offset = x, weight, bias, readout, offset
-        B = x.shape[0]
-        self.sizes = (B, x.numel() // (B * C) if B else 0, C, groups)
-        self.dtype, self.act = _DTYPES[x.dtype], _ACTS[act]
+        numel = x.numel()
+        self.sizes = (B, numel // (B * C) if B else 0, C, groups)
+        self.dtype, self.act, self.read = _DTYPES[x.dtype], _ACTS[act], read
         self.pdtype = _DTYPES[pdtype or torch.float32]
         self.nbytes = 0
-        if x.numel():
+        if numel:
             self.nbytes = lib.ecc_norm_workspace_bytes(*self.sizes)
             if not self.nbytes:
                 raise EccError(_lib.ECC_E_SHAPE, "group norm: " + lib.ecc_last_error().decode(errors="replace"))
 
-    def forward(self, eps):
-        """(y or field, stats)."""
-        x, (B, S, C, G) = self.x, self.sizes
-        stats = torch.empty((B, G, 2), dtype=torch.float32, device=x.device)
-        if self.readout is None:
-            out = torch.empty_like(x)
-        else:
-            out = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        if not x.numel():
+    def forward(self, x, weight, bias, readout, offset, eps, keep):
+        """(y or field, stats); the statistics are a tensor of their own where they are to be kept."""
+        B, S, C, G = self.sizes
+        out = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if self.read else torch.empty_like(x)
+        stats = torch.empty((B, G, 2), dtype=torch.float32, device=x.device) if keep else None
+        if not self.nbytes:
             return out, stats
         with _on_device(x):
-            ws = torch.empty(self.nbytes, dtype=torch.uint8, device=x.device)
+            ws = torch.empty(self.nbytes + (0 if keep else 8 * B * G), dtype=torch.uint8, device=x.device)
+            at = ws.data_ptr()
+            # the workspace is a multiple of 8 bytes long, so what follows it is aligned for float32
+            at_stats = stats.data_ptr() if keep else at + self.nbytes
             stream = _stream(x).cuda_stream
-            if self.readout is None:
-                check(lib.ecc_norm_fwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(self.weight), _param_ptr(self.bias),
-                                       self.pdtype, self.act, float(eps), _ptr(out), _ptr(stats), _ptr(ws), self.nbytes,
-                                       stream), "ecc_norm_fwd")
+            if self.read:
+                check(lib.ecc_norm_readout_fwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(weight), _param_ptr(bias),
+                                               _ptr(readout), _param_ptr(offset), self.pdtype, self.act, eps, _ptr(out),
+                                               at_stats, at, self.nbytes, stream), "ecc_norm_readout_fwd")
             else:
-                check(lib.ecc_norm_readout_fwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(self.weight),
-                                               _param_ptr(self.bias), _ptr(self.readout), _param_ptr(self.offset),
-                                               self.pdtype, self.act, float(eps), _ptr(out), _ptr(stats), _ptr(ws),
-                                               self.nbytes, stream), "ecc_norm_readout_fwd")
+                check(lib.ecc_norm_fwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(weight), _param_ptr(bias), self.pdtype,
+                                       self.act, eps, _ptr(out), at_stats, at, self.nbytes, stream), "ecc_norm_fwd")
         return out, stats
 
-    def backward(self, stats, grad, needs):
+    def backward(self, inputs, stats, grad, needs):
         """Gradients of (x, weight, bias, readout, offset), None where not needed."""
-        x, (B, S, C, G) = self.x, self.sizes
-        inputs = (x, self.weight, self.bias, self.readout, self.offset)
+        x, weight, bias, readout, _ = inputs
+        B, S, C, G = self.sizes
         grads = [torch.empty_like(t) if need and t is not None else None for t, need in zip(inputs, needs)]
-        if not x.numel():
+        if not self.nbytes:
             return [None if g is None else g.zero_() for g in grads]
         if all(g is None for g in grads):
             return grads
@@ -121,20 +119,19 @@ class _NormCall:
         with _on_device(x):
             ws = torch.empty(self.nbytes, dtype=torch.uint8, device=x.device)
             stream = _stream(x).cuda_stream
-            if self.readout is None:
-                check(lib.ecc_norm_bwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(self.weight), _param_ptr(self.bias),
-                                       self.pdtype, self.act, _ptr(stats), _ptr(grad), *ptrs[:3], _ptr(ws), self.nbytes,
-                                       stream), "ecc_norm_bwd")
+            if self.read:
+                check(lib.ecc_norm_readout_bwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(weight), _param_ptr(bias),
+                                               _ptr(readout), self.pdtype, self.act, _ptr(stats), _ptr(grad), *ptrs,
+                                               _ptr(ws), self.nbytes, stream), "ecc_norm_readout_bwd")
             else:
-                check(lib.ecc_norm_readout_bwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(self.weight),
-                                               _param_ptr(self.bias), _ptr(self.readout), self.pdtype, self.act,
-                                               _ptr(stats), _ptr(grad), *ptrs, _ptr(ws), self.nbytes, stream),
-                      "ecc_norm_readout_bwd")
+                check(lib.ecc_norm_bwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(weight), _param_ptr(bias), self.pdtype,
+                                       self.act, _ptr(stats), _ptr(grad), *ptrs[:3], _ptr(ws), self.nbytes, stream),
+                      "ecc_norm_bwd")
         return grads
 
 
 def _contiguous(t):
-    return None if t is None else t.detach().contiguous()
+    return t if t is None or t.is_contiguous() else t.contiguous()
 
 
 def _needs_grad(*tensors):
@@ -146,18 +143,19 @@ class GroupNormAct(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight, bias, groups, act, eps):
-        call = _NormCall(_contiguous(x), groups, _contiguous(weight), _contiguous(bias), act)
-        y, stats = call.forward(eps)
+        xc, w, b = _contiguous(x), _contiguous(weight), _contiguous(bias)
+        plan = _NormPlan(xc, groups, w, b, act)
+        y, stats = plan.forward(xc, w, b, None, None, float(eps), True)
         ctx.save_for_backward(x, weight, bias, stats)
-        ctx.groups, ctx.act = groups, act
+        ctx.plan = plan
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad):
         x, weight, bias, stats = ctx.saved_tensors
-        call = _NormCall(_contiguous(x), ctx.groups, _contiguous(weight), _contiguous(bias), ctx.act)
-        grads = call.backward(stats, grad.contiguous(), ctx.needs_input_grad[:3])
+        inputs = (_contiguous(x), _contiguous(weight), _contiguous(bias), None, None)
+        grads = ctx.plan.backward(inputs, stats, _contiguous(grad), ctx.needs_input_grad[:3])
         return (*grads[:3], None, None, None)
 
 
@@ -166,20 +164,19 @@ class GroupNormReadout(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight, bias, readout, offset, groups, act, eps):
-        call = _NormCall(_contiguous(x), groups, _contiguous(weight), _contiguous(bias), act, _contiguous(readout),
-                         _contiguous(offset), with_readout=True)
-        field, stats = call.forward(eps)
+        args = [_contiguous(t) for t in (x, weight, bias, readout, offset)]
+        plan = _NormPlan(args[0], groups, args[1], args[2], act, args[3], args[4], read=True)
+        field, stats = plan.forward(*args, float(eps), True)
         ctx.save_for_backward(x, weight, bias, readout, offset, stats)
-        ctx.groups, ctx.act = groups, act
+        ctx.plan = plan
         return field
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad):
-        x, weight, bias, readout, offset, stats = ctx.saved_tensors
-        call = _NormCall(_contiguous(x), ctx.groups, _contiguous(weight), _contiguous(bias), ctx.act,
-                         _contiguous(readout), _contiguous(offset), with_readout=True)
-        return (*call.backward(stats, grad.contiguous(), ctx.needs_input_grad[:5]), None, None, None)
+        *inputs, stats = ctx.saved_tensors
+        inputs = [_contiguous(t) for t in inputs]
+        return (*ctx.plan.backward(inputs, stats, _contiguous(grad), ctx.needs_input_grad[:5]), None, None, None)
 
 
 def group_norm_act(x, groups, weight=None, bias=None, act="none", eps=1e-5):
@@ -190,7 +187,8 @@ def group_norm_act(x, groups, weight=None, bias=None, act="none", eps=1e-5):
     """
     if _needs_grad(x, weight, bias):
         return GroupNormAct.apply(x, weight, bias, groups, act, eps)
-    return _NormCall(x.contiguous(), groups, _contiguous(weight), _contiguous(bias), act).forward(eps)[0]
+    x, weight, bias = _contiguous(x), _contiguous(weight), _contiguous(bias)
+    return _NormPlan(x, groups, weight, bias, act).forward(x, weight, bias, None, None, float(eps), False)[0]
 
 
 def group_norm_readout(x, groups, weight, bias, readout, offset=None, act="none", eps=1e-5):
@@ -198,8 +196,8 @@ def group_norm_readout(x, groups, weight, bias, readout, offset=None, act="none"
     [batch, *space] that a curve takes.  Differentiable in x and all four parameters; the features are not stored."""
     if _needs_grad(x, weight, bias, readout, offset):
         return GroupNormReadout.apply(x, weight, bias, readout, offset, groups, act, eps)
-    return _NormCall(x.contiguous(), groups, _contiguous(weight), _contiguous(bias), act, _contiguous(readout),
-                     _contiguous(offset), with_readout=True).forward(eps)[0]
+    args = [_contiguous(t) for t in (x, weight, bias, readout, offset)]
+    return _NormPlan(args[0], groups, args[1], args[2], act, args[3], args[4], read=True).forward(*args, float(eps), False)[0]
 
 
 # ------------------------------------------------- orthogonalised updates

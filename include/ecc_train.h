@@ -61,7 +61,8 @@ extern "C" {
  *   pdtype  ECC_T_F32 or dtype
  * Moments are accumulated in float32 about a pivot per thread and joined in
  * float64; everything else is float32, rounded once to dtype.  x and y need
- * only the alignment of their elements.  Three kernel launches.
+ * only the alignment of their elements.  Two kernel launches, three or four
+ * where the features are many.
  */
 int ecc_norm_fwd(const void* x, int dtype, int64_t batch, int64_t voxels, int64_t channels, int64_t groups,
                  const void* weight, const void* bias, int pdtype, int act, float eps, void* y, float* stats,
@@ -75,7 +76,7 @@ int ecc_norm_fwd(const void* x, int dtype, int64_t batch, int64_t voxels, int64_
  *   grad_bias = sum du, grad_weight = sum du xhat   over samples and voxels,
  *   grad_x = rstd (du weight - m1 - xhat m2), m1 and m2 the means over the
  *   group of du weight and of du weight xhat.
- * Three kernel launches.
+ * Three or four kernel launches.
  */
 int ecc_norm_bwd(const void* x, int dtype, int64_t batch, int64_t voxels, int64_t channels, int64_t groups,
                  const void* weight, const void* bias, int pdtype, int act, const float* stats, const void* grad_y,
