@@ -108,9 +108,10 @@ __device__ __forceinline__ void split(float v, f16& hi, f16& lo) {
 }
 
 // X and X^T as pairs from a 64 x 64 tile of the input, and the scales of the
-// steps.  P1 has the input's orientation, P2 the other.
+// steps.  P1 has the input's orientation, P2 the other.  D, where given, takes
+// the place of X (which is the other orientation where rows > cols), in float64.
 template <class GT>
-__global__ __launch_bounds__(kNT) void orth_prepare_kernel(OrthArgs p, f16* P1, f16* P2, int64_t rpad, int64_t cpad) {
+__global__ __launch_bounds__(kNT) void orth_prepare_kernel(OrthArgs p, f16* P1, f16* P2, double* D, int64_t rpad, int64_t cpad) {
   __shared__ float tile[64][65];
   __shared__ double lds[kNT / 64];
   const int batch = blockIdx.z;
@@ -139,6 +140,16 @@ __global__ __launch_bounds__(kNT) void orth_prepare_kernel(OrthArgs p, f16* P1, 
   __syncthreads();
   f16* out1 = P1 + (int64_t)batch * rpad * 2 * cpad;
   f16* out2 = P2 + (int64_t)batch * rpad * 2 * cpad;
+  const bool tall = p.rows > p.cols;
+  if (D) {
+    D += (int64_t)batch * rpad * cpad;
+    for (int i = ty; i < 64; i += 4) {
+      if (tall)
+        D[(c0 + i) * rpad + r0 + tx] = (double)tile[tx][i];
+      else
+        D[(r0 + i) * cpad + c0 + tx] = (double)tile[i][tx];
+    }
+  }
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int at = q * kNT + threadIdx.x, row = at >> 4, ch = at & 15;
@@ -153,8 +164,8 @@ __global__ __launch_bounds__(kNT) void orth_prepare_kernel(OrthArgs p, f16* P1, 
       split(tile[k + j][row], hi, lo);
       b[j] = low ? lo : hi;
     }
-    *reinterpret_cast<f16x8*>(out1 + (r0 + row) * 2 * cpad + c0 * 2 + ch * 8) = a;
-    *reinterpret_cast<f16x8*>(out2 + (c0 + row) * 2 * rpad + r0 * 2 + ch * 8) = b;
+    if (!D || tall) *reinterpret_cast<f16x8*>(out1 + (r0 + row) * 2 * cpad + c0 * 2 + ch * 8) = a;
+    if (!D || !tall) *reinterpret_cast<f16x8*>(out2 + (c0 + row) * 2 * rpad + r0 * 2 + ch * 8) = b;
   }
 }
 
@@ -515,8 +526,25 @@ hipError_t run(const OrthArgs& o, hipStream_t s) {
   const bool tall = a.rows > a.cols;
   const int64_t rpad = tall ? w.npad : w.mpad, cpad = tall ? w.mpad : w.npad;
   hipLaunchKernelGGL((orth_prepare_kernel<GT>), dim3((unsigned)(cpad / 64), (unsigned)(rpad / 64), (unsigned)a.batch),
-                     dim3(kNT), 0, s, a, tall ? XT[0] : X[0], tall ? X[0] : XT[0], rpad, cpad);
+                     dim3(kNT), 0, s, a, tall ? XT[0] : X[0], tall ? X[0] : XT[0],
+                     orth_is_long(a) ? reinterpret_cast<double*>(ws + long_plan(a.batch, a.rows, a.cols).at_x) : nullptr,
+                     rpad, cpad);
   const int64_t sx = w.mpad * w.npad * 2, sm = w.mpad * w.mpad * 2;
+  if (orth_is_long(a)) {
+    const hipError_t e = launch_orth_long(a, P, a.ws, s);
+    if (e != hipSuccess) return e;
+    Product p{};
+    p.o = a;
+    p.sp = a.sq;
+    p.part = part;
+    p.A = P;
+    p.sA = sm;
+    p.B = XT[0];
+    p.sB = sx;
+    p.kpad = w.mpad;
+    p.ksteps = (int)((w.m + 31) / 32);
+    return launch_product<kLast, PT>(p, w.mpad, w.npad, a.batch, s);
+  }
   for (int k = 0; k < a.steps; ++k) {
     const int in = k & 1, on = 1 - in;
     Product p{};

@@ -131,7 +131,7 @@ namespace ecc {
 bool orth_bounds(OrthArgs& o) {
   // 256 samples of the attained range; 2 % covers what lies between them
   constexpr int kSamples = 256;
-  double r = 1.0, pmax = 0.0, gram = 0.0, cap = 1.0;
+  double r = 1.0, pmax = 0.0, gram = 0.0, cap = 1.0, all = 1.0;
   o.amplify = 1.0;
   for (int k = 0; k < o.steps; ++k) {
     double f = 0.0, q = 0.0;
@@ -142,6 +142,7 @@ bool orth_bounds(OrthArgs& o) {
     }
     gram = fmax(gram, r * r);
     pmax = fmax(pmax, 1.02 * q);
+    all *= 1.02 * q;
     if (k + 1 < o.steps) o.amplify *= fmax(1.0, q * q);
     r = 1.02 * f;
     cap = fmax(cap, r);
@@ -152,6 +153,9 @@ bool orth_bounds(OrthArgs& o) {
   o.sa = ldexpf(1.0f, 14 - e);
   frexp(fmax(pmax, 1e-30), &e);
   o.sp = ldexpf(1.0f, 14 - e);
+  // (beyond 2^40 the entries are too unlike for a pair; kMaxAmplify is passed long before)
+  frexp(fmin(fmax(all, 1e-30), 1e12), &e);
+  o.sq = ldexpf(1.0f, 14 - e);
   o.growth = (float)pmax;
   o.cap = (float)cap;
   return true;

@@ -81,6 +81,7 @@ struct OrthArgs {
   // the scales of the pairs that hold A = X X^T and P
   float growth, cap, sa, sp;
   double amplify;  // what an error of X_0 X_0^T may grow by when it is not formed anew
+  float sq;        // scale of the pairs that hold the product of all steps' P
   void* ws;
   // set by the launcher
   double* squares;
@@ -206,8 +207,50 @@ inline ThinPlan thin_plan(int64_t batch, int64_t rows, int64_t cols) {
 inline bool orth_is_thin(const OrthArgs& o) {
   return (o.rows <= kThin || o.cols <= kThin) && o.amplify <= kMaxAmplify;
 }
-// Workspace of either way (the coefficients, which decide, come with the call).
+
+// Long matrices: the same for longer short sides (ecc_orth_long.hip), after
+// the direct way's preparation and before its last product, whose pair matrix
+// X^T stays where orth_plan puts it; the rest lies behind.
+struct LongPlan {
+  int64_t m, npad, per;
+  int splits;
+  size_t square_bytes, at_x, at_part, at_square, bytes;
+};
+inline LongPlan long_plan(int64_t batch, int64_t rows, int64_t cols) {
+  LongPlan w{};
+  const OrthPlan d = orth_plan(batch, rows, cols);
+  w.m = d.mpad;
+  w.npad = d.npad;
+  const int64_t b = w.m / 64, tiles = b * (b + 1) / 2 * batch, most = (w.npad + 127) / 128;
+  int64_t s = tiles < 256 ? 256 / tiles : 1;  // a workgroup for every CU
+  s = s < most ? s : most;
+  w.per = ((w.npad + s - 1) / s + 127) / 128 * 128;
+  w.splits = (int)((w.npad + w.per - 1) / w.per);
+  w.square_bytes = (size_t)batch * w.m * w.m * sizeof(double);
+  w.at_x = d.bytes;
+  w.at_part = w.at_x + (size_t)batch * w.m * w.npad * sizeof(double);
+  w.at_square = w.at_part + (size_t)tiles * w.splits * 4096 * sizeof(double);
+  w.bytes = w.at_square + 5 * w.square_bytes;
+  return w;
+}
+// Its float64 products cost some 14 m^3 + m^2 n at a fifth of the direct way's
+// rate for 5 m^3 + 15 m^2 n, and few launches less.  Where launches are most
+// of it, it gains from n = 2 m on (256 x 512: 113 us, direct 127); where the
+// products are, from about 8 m (512 x 4096: 211 and 254; 512 x 1024: 181 and
+// 176) or 24 m (4 x 512 x 16384: 1.2 and 1.4 ms; 1024 x 8192: 0.93 and 0.65).
+// Nearer to square the two are alike, and Q's rounding would show.
+inline bool orth_shape_is_long(int64_t batch, int64_t rows, int64_t cols) {
+  const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows, p = orth_pad(m);
+  const double cube = (double)batch * (double)p * (double)p * (double)p;
+  const int64_t ratio = cube <= 3.4e7 ? 2 : (cube <= 1.4e8 ? 8 : 24);
+  return m > kThin && n >= ratio * m;
+}
+inline bool orth_is_long(const OrthArgs& o) {
+  return orth_shape_is_long(o.batch, o.rows, o.cols) && o.amplify <= kMaxAmplify;
+}
+// Workspace of whichever way (the coefficients, which decide too, come with the call).
 inline size_t orth_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
+  if (orth_shape_is_long(batch, rows, cols)) return long_plan(batch, rows, cols).bytes;
   const size_t direct = orth_plan(batch, rows, cols).bytes;
   if (rows > kThin && cols > kThin) return direct;
   const size_t thin = thin_plan(batch, rows, cols).bytes;
@@ -215,6 +258,9 @@ inline size_t orth_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
 }
 
 hipError_t launch_orth(const OrthArgs& o, hipStream_t stream);
+// From X (float64, in the workspace, scaled by o.scales) to the pair matrix of
+// Q, scaled by o.sq.
+hipError_t launch_orth_long(const OrthArgs& o, _Float16* q, void* ws, hipStream_t stream);
 template <class GT>
 hipError_t launch_orth_thin(const OrthArgs& o, hipStream_t stream);
 
