@@ -19,8 +19,7 @@ _API = (
     "ecc_hard_directional", "soft_ecc_directional",
 )
 
-_TRAIN_API = ("group_norm_act", "group_norm_readout", "GroupNormAct", "GroupNormReadout", "orthogonalize",
-              "muon_step")
+_TRAIN_API = ("group_norm_act", "group_norm_readout", "orthogonalize", "muon_step")
 
 __all__ = list(_API + _TRAIN_API)
 

@@ -230,7 +230,8 @@ __global__ __launch_bounds__(kNT) void long_square_kernel(Square p) {
 
 }  // namespace
 
-hipError_t launch_orth_long(const OrthArgs& o, f16* q, void* ws, hipStream_t s) {
+hipError_t launch_orth_long(const OrthArgs& o, void* q_pairs, void* ws, hipStream_t s) {
+  f16* q = reinterpret_cast<f16*>(q_pairs);
   const LongPlan w = long_plan(o.batch, o.rows, o.cols);
   char* base = reinterpret_cast<char*>(ws);
   double* buf[5];

@@ -260,7 +260,7 @@ inline size_t orth_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
 hipError_t launch_orth(const OrthArgs& o, hipStream_t stream);
 // From X (float64, in the workspace, scaled by o.scales) to the pair matrix of
 // Q, scaled by o.sq.
-hipError_t launch_orth_long(const OrthArgs& o, _Float16* q, void* ws, hipStream_t stream);
+hipError_t launch_orth_long(const OrthArgs& o, void* q, void* ws, hipStream_t stream);
 template <class GT>
 hipError_t launch_orth_thin(const OrthArgs& o, hipStream_t stream);
 

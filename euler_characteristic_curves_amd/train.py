@@ -2,20 +2,19 @@
 
 Features are channels last, ``[batch, *space, channels]``; every function takes
 tensors that live on a ROCm device, checks them, and calls the C entry points
-on the current torch stream.  All arithmetic happens in the HIP kernels.
+on the current torch stream (the norms through their autograd nodes in
+csrc/ecc_torch.cpp).  All arithmetic happens in the HIP kernels.
 Scratch comes from torch's allocator per call, so calls may run on any stream
 and be captured into a graph.
 """
 
 import torch
-from torch.autograd.function import once_differentiable
 
-from . import _lib
+from . import _lib, _torch
 from ._lib import EccError, check, lib
 from .ecc import _dev_tensor, _ptr, _stream
 
-__all__ = ["group_norm_act", "group_norm_readout", "GroupNormAct", "GroupNormReadout", "orthogonalize", "muon_step",
-           "EccError"]
+__all__ = ["group_norm_act", "group_norm_readout", "orthogonalize", "muon_step", "EccError"]
 
 _DTYPES = {torch.float32: _lib.ECC_T_F32, torch.float16: _lib.ECC_T_F16, torch.bfloat16: _lib.ECC_T_BF16}
 _ACTS = {"none": _lib.ECC_ACT_NONE, "relu": _lib.ECC_ACT_RELU, "silu": _lib.ECC_ACT_SILU, "gelu": _lib.ECC_ACT_GELU}
@@ -37,14 +36,10 @@ class _NullContext:
 _NULL_CONTEXT = _NullContext()
 
 
-def _param_ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 class _NormPlan:
-    """What a norm call needs besides its tensors: checked once, kept for the backward pass."""
+    """What a norm call needs besides its tensors, checked."""
 
-    __slots__ = ("sizes", "dtype", "pdtype", "act", "nbytes", "read")
+    __slots__ = ("sizes", "dtype", "pdtype", "act", "nbytes")
 
     def __init__(self, x, groups, weight, bias, act, readout=None, offset=None, read=False):
         _dev_tensor(x, "x")
@@ -76,7 +71,7 @@ class _NormPlan:
             pdtype = t.dtype
         numel = x.numel()
         self.sizes = (B, numel // (B * C) if B else 0, C, groups)
-        self.dtype, self.act, self.read = _DTYPES[x.dtype], _ACTS[act], read
+        self.dtype, self.act = _DTYPES[x.dtype], _ACTS[act]
         self.pdtype = _DTYPES[pdtype or torch.float32]
         self.nbytes = 0
         if numel:
@@ -84,99 +79,17 @@ class _NormPlan:
             if not self.nbytes:
                 raise EccError(_lib.ECC_E_SHAPE, "group norm: " + lib.ecc_last_error().decode(errors="replace"))
 
-    def forward(self, x, weight, bias, readout, offset, eps, keep):
-        """(y or field, stats); the statistics are a tensor of their own where they are to be kept."""
-        B, S, C, G = self.sizes
-        out = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if self.read else torch.empty_like(x)
-        stats = torch.empty((B, G, 2), dtype=torch.float32, device=x.device) if keep else None
-        if not self.nbytes:
-            return out, stats
-        with _on_device(x):
-            ws = torch.empty(self.nbytes + (0 if keep else 8 * B * G), dtype=torch.uint8, device=x.device)
-            at = ws.data_ptr()
-            # the workspace is a multiple of 8 bytes long, so what follows it is aligned for float32
-            at_stats = stats.data_ptr() if keep else at + self.nbytes
-            stream = _stream(x).cuda_stream
-            if self.read:
-                check(lib.ecc_norm_readout_fwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(weight), _param_ptr(bias),
-                                               _ptr(readout), _param_ptr(offset), self.pdtype, self.act, eps, _ptr(out),
-                                               at_stats, at, self.nbytes, stream), "ecc_norm_readout_fwd")
-            else:
-                check(lib.ecc_norm_fwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(weight), _param_ptr(bias), self.pdtype,
-                                       self.act, eps, _ptr(out), at_stats, at, self.nbytes, stream), "ecc_norm_fwd")
-        return out, stats
-
-    def backward(self, inputs, stats, grad, needs):
-        """Gradients of (x, weight, bias, readout, offset), None where not needed."""
-        x, weight, bias, readout, _ = inputs
-        B, S, C, G = self.sizes
-        grads = [torch.empty_like(t) if need and t is not None else None for t, need in zip(inputs, needs)]
-        if not self.nbytes:
-            return [None if g is None else g.zero_() for g in grads]
-        if all(g is None for g in grads):
-            return grads
-        ptrs = [_param_ptr(g) for g in grads]
-        with _on_device(x):
-            ws = torch.empty(self.nbytes, dtype=torch.uint8, device=x.device)
-            stream = _stream(x).cuda_stream
-            if self.read:
-                check(lib.ecc_norm_readout_bwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(weight), _param_ptr(bias),
-                                               _ptr(readout), self.pdtype, self.act, _ptr(stats), _ptr(grad), *ptrs,
-                                               _ptr(ws), self.nbytes, stream), "ecc_norm_readout_bwd")
-            else:
-                check(lib.ecc_norm_bwd(_ptr(x), self.dtype, B, S, C, G, _param_ptr(weight), _param_ptr(bias), self.pdtype,
-                                       self.act, _ptr(stats), _ptr(grad), *ptrs[:3], _ptr(ws), self.nbytes, stream),
-                      "ecc_norm_bwd")
-        return grads
-
 
 def _contiguous(t):
     return t if t is None or t.is_contiguous() else t.contiguous()
 
 
-def _needs_grad(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
-
-
-class GroupNormAct(torch.autograd.Function):
-    """Autograd wrapper of ecc_norm_fwd / ecc_norm_bwd."""
-
-    @staticmethod
-    def forward(ctx, x, weight, bias, groups, act, eps):
-        xc, w, b = _contiguous(x), _contiguous(weight), _contiguous(bias)
-        plan = _NormPlan(xc, groups, w, b, act)
-        y, stats = plan.forward(xc, w, b, None, None, float(eps), True)
-        ctx.save_for_backward(x, weight, bias, stats)
-        ctx.plan = plan
-        return y
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, grad):
-        x, weight, bias, stats = ctx.saved_tensors
-        inputs = (_contiguous(x), _contiguous(weight), _contiguous(bias), None, None)
-        grads = ctx.plan.backward(inputs, stats, _contiguous(grad), ctx.needs_input_grad[:3])
-        return (*grads[:3], None, None, None)
-
-
-class GroupNormReadout(torch.autograd.Function):
-    """Autograd wrapper of ecc_norm_readout_fwd / ecc_norm_readout_bwd."""
-
-    @staticmethod
-    def forward(ctx, x, weight, bias, readout, offset, groups, act, eps):
-        args = [_contiguous(t) for t in (x, weight, bias, readout, offset)]
-        plan = _NormPlan(args[0], groups, args[1], args[2], act, args[3], args[4], read=True)
-        field, stats = plan.forward(*args, float(eps), True)
-        ctx.save_for_backward(x, weight, bias, readout, offset, stats)
-        ctx.plan = plan
-        return field
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, grad):
-        *inputs, stats = ctx.saved_tensors
-        inputs = [_contiguous(t) for t in inputs]
-        return (*ctx.plan.backward(inputs, stats, _contiguous(grad), ctx.needs_input_grad[:5]), None, None, None)
+def _norm(x, groups, weight, bias, readout, offset, act, eps, read):
+    # the checks look at what the kernels will read; the node keeps the caller's own tensors
+    plan = _NormPlan(_contiguous(x), groups, _contiguous(weight), _contiguous(bias), act, _contiguous(readout),
+                     _contiguous(offset), read)
+    return _torch.norm(x, weight, bias, readout, offset, plan.sizes, plan.dtype, plan.pdtype, plan.act, plan.nbytes,
+                       float(eps), read)
 
 
 def group_norm_act(x, groups, weight=None, bias=None, act="none", eps=1e-5):
@@ -185,19 +98,13 @@ def group_norm_act(x, groups, weight=None, bias=None, act="none", eps=1e-5):
     x: float32, float16 or bfloat16 [batch, *space, channels]; weight and bias: [channels], float32 or x's dtype, or
     None (1 and 0); act: "none", "relu", "silu" or "gelu".  Returns a tensor like x (see include/ecc_train.h).
     """
-    if _needs_grad(x, weight, bias):
-        return GroupNormAct.apply(x, weight, bias, groups, act, eps)
-    x, weight, bias = _contiguous(x), _contiguous(weight), _contiguous(bias)
-    return _NormPlan(x, groups, weight, bias, act).forward(x, weight, bias, None, None, float(eps), False)[0]
+    return _norm(x, groups, weight, bias, None, None, act, eps, False)
 
 
 def group_norm_readout(x, groups, weight, bias, readout, offset=None, act="none", eps=1e-5):
     """The features group_norm_act gives, contracted with ``readout`` [channels] plus ``offset`` [1] to the float32 grid
     [batch, *space] that a curve takes.  Differentiable in x and all four parameters; the features are not stored."""
-    if _needs_grad(x, weight, bias, readout, offset):
-        return GroupNormReadout.apply(x, weight, bias, readout, offset, groups, act, eps)
-    args = [_contiguous(t) for t in (x, weight, bias, readout, offset)]
-    return _NormPlan(args[0], groups, args[1], args[2], act, args[3], args[4], read=True).forward(*args, float(eps), False)[0]
+    return _norm(x, groups, weight, bias, readout, offset, act, eps, True)
 
 
 # ------------------------------------------------- orthogonalised updates
