@@ -254,3 +254,80 @@ def test_graph_replays(readout):
         torch.cuda.synchronize()
         for a, b in zip(kept, eager):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("readout", [False, True], ids=["norm", "readout"])
+@pytest.mark.parametrize("groups", [1, 4, 64])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_many_partial_rows(dtype, groups, readout):
+    """Wide groups over many workgroups: partial rows are folded before they are joined."""
+    banner("norm fold", dtype, groups, readout)
+    x, p, grad = make((1, 41, 50, 512), dtype, seed=12, readout=readout)
+    check_all(x, groups, p, grad, "silu")
+
+
+def test_any_subset_of_gradients():
+    """Parameters left out and inputs that need no gradient, in every combination, against the full set."""
+    banner("norm subsets")
+    x, p, grad = make((2, 6, 7, 24), F32, seed=13, readout=True)
+    names = ["x", "weight", "bias", "readout", "offset"]
+    for absent in ((), ("weight",), ("bias",), ("weight", "bias", "offset")):
+        full = {k: v for k, v in {"x": x, **p}.items()}
+        want = norm(x, 4, None if "weight" in absent else p["weight"], None if "bias" in absent else p["bias"], "silu", EPS,
+                    grad, p["readout"], None if "offset" in absent else p["offset"])
+        here = [n for n in names if n not in absent]
+        for mask in range(1, 1 << len(here)):
+            ts = {n: (full[n].cuda() if n in here else None) for n in names}
+            leaves = [n for i, n in enumerate(here) if mask >> i & 1]
+            for n in leaves:
+                ts[n].requires_grad_()
+            out = E.group_norm_readout(ts["x"], 4, ts["weight"], ts["bias"], ts["readout"], ts["offset"], act="silu")
+            grads = torch.autograd.grad(out, [ts[n] for n in leaves], grad.cuda())
+            for n, g in zip(leaves, grads):
+                assert worst(g, want[n]) <= 1, (absent, leaves, n)
+
+
+def test_backward_is_differentiable_once():
+    banner("norm twice")
+    x = torch.randn(2, 5, 6, 8, device="cuda", requires_grad=True)
+    y = E.group_norm_act(x, 2, act="silu")
+    (g,) = torch.autograd.grad(y.sum(), [x], create_graph=True)
+    with pytest.raises(RuntimeError, match="once"):
+        g.sum().backward()
+
+
+def test_changed_input_is_noticed():
+    banner("norm changed")
+    x = torch.randn(2, 5, 6, 8, device="cuda")
+    w = torch.ones(8, device="cuda", requires_grad=True)
+    y = E.group_norm_act(x, 2, w)
+    x.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
+def test_refusals():
+    banner("norm refusals")
+    x = torch.zeros(2, 3, 4, 8, device="cuda")
+    one = torch.ones(8, device="cuda")
+    for kw, exc in ((dict(groups=3), ValueError), (dict(groups=0), ValueError), (dict(groups=2.0), TypeError),
+                    (dict(act="tanh"), ValueError), (dict(weight=one[:4]), ValueError), (dict(weight=one.half()), TypeError),
+                    (dict(weight=one[None]), ValueError), (dict(bias=one.cpu()), ValueError), (dict(eps=-1.0), E.EccError),
+                    (dict(eps=float("nan")), E.EccError), (dict(x=x.double()), TypeError), (dict(x=x[0, 0]), ValueError)):
+        args = {"x": x, "groups": 2, "weight": one, "bias": one, **kw}
+        for grad in (False, True):
+            with pytest.raises(exc):
+                E.group_norm_act(args["x"].detach().clone().requires_grad_(grad), args["groups"], args["weight"], args["bias"],
+                                 act=args.get("act", "none"), eps=args.get("eps", EPS))
+    with pytest.raises(TypeError):
+        E.group_norm_readout(x, 2, None, None, None)
+    with pytest.raises(ValueError):
+        E.group_norm_readout(x, 2, one, None, one, one)
+    half = x.half()
+    with pytest.raises(TypeError):
+        E.group_norm_act(half, 2, one, one.half())
+    wide = torch.zeros(1, 2, 8193, device="cuda")
+    with pytest.raises(E.EccError):
+        E.group_norm_act(wide, 1)
+    with pytest.raises(E.EccError):
+        E.group_norm_readout(wide[..., :1030].contiguous(), 1, None, None, torch.zeros(1030, device="cuda"))

@@ -214,3 +214,75 @@ def test_refusals():
         E.muon_step([p], [g], [b], lr=float("inf"))
     torch.cuda.synchronize()
     assert torch.equal(p, g) and torch.equal(b, g)
+
+
+# short sides of one to four tiles of 16, and longer ones; one workgroup a matrix, and several; both orientations
+CARRIED = [(2, 16, 300), (3, 45, 47), (2, 777, 37), (2, 37, 777), (1, 48, 3001), (1, 3000, 61), (1, 64, 2500), (2, 1500, 64),
+           (1, 5, 9000), (300, 20, 70), (70, 170), (170, 70), (2, 100, 900), (900, 130), (3, 129, 260), (1, 300, 2500)]
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", CARRIED, ids=lambda s: "x".join(map(str, s)))
+def test_short_side_carried_through_the_steps(shape, dtype):
+    banner("orth carried", shape, dtype)
+    g = gradient(shape, dtype, seed=sum(shape))
+    d = g.cuda()
+    out = E.orthogonalize(d)
+    assert E.orthogonalize(d, out=d) is d and torch.equal(d, out)
+    stack, outs = (g, out) if g.dim() == 3 else (g[None], out[None])
+    for i in sorted({0, len(stack) // 2, len(stack) - 1}):
+        check(outs[i], stack[i], dtype)
+
+
+@pytest.mark.parametrize("m,n", [(20, 60), (40, 900), (900, 40), (100, 700)], ids=str)
+def test_short_side_steps_scales_and_broken_values(m, n):
+    """Few and many steps (which turn to the direct iteration), both ends of the range, NaN, zero and rank one."""
+    banner("orth carried steps", m, n)
+    for kw in (dict(steps=1), dict(steps=2), dict(steps=8), dict(steps=9), dict(steps=12, coefficients=(1.5, -0.5, 0.0)),
+               dict(steps=3, coefficients=(0.5, 0.0, 0.0)), dict(eps=0.5)):
+        g = gradient((m, n), seed=2)
+        check(E.orthogonalize(g.cuda(), **kw), g, F32, **kw)
+    for scale in (1e-15, 1e-9, 1e15, 1e30):
+        g = gradient((m, n), seed=3, scale=scale)
+        check(E.orthogonalize(g.cuda()), g, F32)
+    assert torch.equal(E.orthogonalize(torch.zeros(m, n, device="cuda")).cpu(), torch.zeros(m, n))
+    gen = torch.Generator().manual_seed(4)
+    one = torch.randn(m, 1, generator=gen) @ torch.randn(1, n, generator=gen)
+    check(E.orthogonalize(one.cuda()), one, F32)
+    for bad in (float("nan"), float("inf")):
+        g = gradient((3, m, n), seed=5)
+        g[1, 2, 3] = bad
+        out = E.orthogonalize(g.cuda())
+        assert torch.isnan(out[1]).all()
+        check(out[0], g[0], F32)
+        check(out[2], g[2], F32)
+
+
+def test_unaligned_carried():
+    banner("orth carried unaligned")
+    for m, n in ((33, 131), (131, 33), (40, 901), (901, 40)):
+        g = gradient((m, n), BF16, seed=6)
+        flat = torch.zeros(g.numel() + 1, dtype=BF16, device="cuda")
+        flat[1:] = g.cuda().reshape(-1)
+        check(E.orthogonalize(flat[1:].view(m, n)), g, BF16)
+
+
+def test_tiles_beyond_whole_rounds():
+    """More tiles than the card holds at a time: the last ones are shared out."""
+    banner("orth rounds")
+    g = gradient((40, 640, 800), seed=8)
+    out = E.orthogonalize(g.cuda())
+    for i in (0, 20, 38, 39):
+        check(out[i], g[i], F32)
+
+
+@pytest.mark.parametrize("pdtype,gdtype", [(F32, F32), (F32, BF16), (BF16, BF16), (F16, F16)], ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("nesterov", [True, False])
+@pytest.mark.parametrize("shape", [(2, 27, 64), (2, 50, 901), (900, 33), (100, 700)], ids=lambda s: "x".join(map(str, s)))
+def test_muon_carried(shape, nesterov, pdtype, gdtype):
+    test_muon(shape, nesterov, pdtype, gdtype)
+
+
+@pytest.mark.parametrize("shape", [(2, 50, 900), (700, 100)], ids=lambda s: "x".join(map(str, s)))
+def test_graph_replays_carried(shape):
+    test_graph_replays(shape)
