@@ -178,8 +178,8 @@ struct Product {
   int64_t sA, sB;      // batch strides, elements
   int64_t kpad;        // columns of both operands
   int ksteps;          // steps of 32 columns that are not all padding
-  int tiles, tiles_n;  // of one matrix
-  int whole;           // tiles, of all matrices, that one workgroup computes
+  int tiles, tiles_n;  // workgroups of one matrix, column tiles
+  int whole;           // workgroups, of all matrices, that one workgroup computes
   int splits;          // workgroups that share the columns of each of the others
   float* part;         // their float32 sums
   int step;
@@ -191,20 +191,26 @@ struct Product {
 };
 
 template <int T>
-constexpr int kFrag = T / 64;  // 32 x 32 fragments per wave and axis (4 waves, 2 x 2)
+constexpr int kFrag = T / 64;  // 32 x 32 fragments per wave and axis (4 waves, 2 x 2, to T x T results)
 
-// Row and column tile of workgroup `t`.  Symmetric products enumerate the
-// lower triangle, row by row.
+// A workgroup computes R tiles of T x T that share their columns, four waves
+// to each.  Row and column tile of the first one of workgroup `t`.  Symmetric
+// products enumerate the lower triangle, row by row; with R = 2 the last block
+// of a row ends in a tile above the diagonal, which is left out at the end.
+template <int R>
 __device__ __forceinline__ void tile_of(bool sym, int t, int tiles_n, int& ti, int& tj) {
   if (sym) {
-    int i = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-    while ((i + 1) * (i + 2) / 2 <= t) ++i;
-    while (i * (i + 1) / 2 > t) --i;
-    ti = i;
-    tj = t - i * (i + 1) / 2;
+    // rows of i + 1 tiles, or of 2 i + 2
+    int i = R == 1 ? (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f) : (int)((sqrtf(4.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+    const auto before = [](int k) { return R == 1 ? k * (k + 1) / 2 : k * (k + 1); };
+    while (before(i + 1) <= t) ++i;
+    while (before(i) > t) --i;
+    ti = R * i;
+    tj = t - before(i);
   } else {
     ti = t / tiles_n;
     tj = t - ti * tiles_n;
+    ti *= R;
   }
 }
 
@@ -252,7 +258,8 @@ __device__ __forceinline__ void store_result(const OrthArgs& o, int64_t batch, i
 template <int T, int KIND, class PT>
 __device__ __forceinline__ void epilogue(const Product& p, int batch, int ti, int tj, int fi, int fj, int q,
                                          float (&v)[4]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6 & 3;
+  if ((KIND == kGram || KIND == kPoly) && ti < tj) return;
   const float* xs = p.o.scales + (int64_t)batch * (p.o.steps + 1) + p.step;
   float f;
   if constexpr (KIND == kGram)
@@ -296,13 +303,14 @@ __device__ __forceinline__ void epilogue(const Product& p, int batch, int ti, in
 // A wave's load covers 8 rows; the 16-byte chunk a lane fetches is permuted
 // within its row by the row's number, so that the fragment reads below, 8 rows
 // at one chunk, meet 8 different groups of banks.
-template <int T>
+template <int ROWS, int WAVES>
 __device__ __forceinline__ void load_step(const f16* base, int64_t pitch, int kstep, f16* lds) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane >> 3, ch = (lane & 7) ^ r;
+  constexpr int N = ROWS / 8 / WAVES;
 #pragma unroll
-  for (int q = 0; q < T / 32; ++q) {
-    const int row0 = (wave * (T / 32) + q) * 8;
+  for (int q = 0; q < N; ++q) {
+    const int row0 = (wave * N + q) * 8;
     const f16* src = base + (int64_t)(row0 + r) * pitch + (int64_t)kstep * 64 + ch * 8;
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                      (__attribute__((address_space(3))) void*)(lds + row0 * 64), 16, 0, 0);
@@ -319,7 +327,7 @@ template <int T>
 __device__ __forceinline__ void multiply_step(const f16* la, const f16* lb, f32x16 (&acc)[kFrag<T>][kFrag<T>]) {
   constexpr int F = kFrag<T>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int ra = (wave >> 1) * (T / 2) + (lane & 31), rb = (wave & 1) * (T / 2) + (lane & 31);
+  const int ra = (wave >> 2) * T + (wave >> 1 & 1) * (T / 2) + (lane & 31), rb = (wave & 1) * (T / 2) + (lane & 31);
   f16x8 ah[2][F], al[2][F], bh[2][F], bl[2][F];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -362,39 +370,41 @@ __device__ __forceinline__ void multiply_step(const f16* la, const f16* lb, f32x
   __builtin_amdgcn_sched_group_barrier(0x008, 6 * F * F - 6 * F, 0);
 }
 
-// Steps of the long axis that are on their way to LDS at a time, the one in
-// use counted: a small tile is done with a step before the next could arrive.
-template <int T>
-constexpr int kStages = T == 64 ? 4 : 2;
+// Steps of the long axis that are in LDS or on their way to it, the one in use
+// counted.  A small tile is done with a step before the next could arrive; two
+// workgroups of one 128-tile fill the LDS with two stages each, one of two
+// tiles with three stages of 48 KB.
+template <int T, int R>
+constexpr int kStages = T == 64 ? 4 : (R == 2 ? 3 : 2);
 
 // Waits for all but the newest N steps' loads of this wave and for what it has
 // read of LDS, then for the other waves.  (A workgroup fence would wait for
 // every load; one block, and ordered with memory, so that no read of LDS is
 // still on its way when another wave's loads overwrite it.)
-template <int T, int N>
+template <int T, int R, int N>
 __device__ __forceinline__ void wait_step() {
-  constexpr int vm = N * 2 * (T / 32);  // loads a wave issues per step
+  constexpr int vm = N * (T / 32 + T / 32 / R);  // loads a wave issues per step
   __builtin_amdgcn_s_waitcnt((vm & 15) | 0x0070 | ((vm >> 4) << 14));  // the same, known to the compiler
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(vm) : "memory");
 }
 
-// One tile of a product, or a share of its columns.
-template <int T, int KIND, class PT>
-__global__ __launch_bounds__(kNT) void product_kernel(Product p) {
-  constexpr int F = kFrag<T>, S = kStages<T>;
+// R tiles of a product, or a share of their columns.
+template <int T, int R, int KIND, class PT>
+__global__ __launch_bounds__(kNT * R) void product_kernel(Product p) {
+  constexpr int F = kFrag<T>, S = kStages<T, R>, A = T * R * 64, B = T * 64;
   // arrays of their own, so that a read of one is known not to wait for another's loads
-  __shared__ __align__(16) f16 a0[T * 64], b0[T * 64], a1[T * 64], b1[T * 64];
-  __shared__ __align__(16) f16 a2[S > 2 ? T * 64 : 8], b2[S > 2 ? T * 64 : 8], a3[S > 2 ? T * 64 : 8], b3[S > 2 ? T * 64 : 8];
+  __shared__ __align__(16) f16 a0[A], b0[B], a1[A], b1[B];
+  __shared__ __align__(16) f16 a2[S > 2 ? A : 8], b2[S > 2 ? B : 8], a3[S > 3 ? A : 8], b3[S > 3 ? B : 8];
   const int rest = (int)blockIdx.x - p.whole;
   const int all = rest < 0 ? (int)blockIdx.x : p.whole + rest / p.splits, sp = rest < 0 ? 0 : rest % p.splits;
   const int batch = all / p.tiles;
   int ti, tj;
-  tile_of(KIND == kGram || KIND == kPoly, all - batch * p.tiles, p.tiles_n, ti, tj);
+  tile_of<R>(KIND == kGram || KIND == kPoly, all - batch * p.tiles, p.tiles_n, ti, tj);
   const int per = rest < 0 ? p.ksteps : (p.ksteps + p.splits - 1) / p.splits;
   const int k0 = sp * per, k1 = k0 + per < p.ksteps ? k0 + per : p.ksteps;
   const int64_t pitch = 2 * p.kpad;
-  const f16* A = p.A + batch * p.sA + (int64_t)ti * T * pitch;
-  const f16* B = p.B + batch * p.sB + (int64_t)tj * T * pitch;
+  const f16* Ap = p.A + batch * p.sA + (int64_t)ti * T * pitch;
+  const f16* Bp = p.B + batch * p.sB + (int64_t)tj * T * pitch;
   f32x16 acc[F][F];
 #pragma unroll
   for (int i = 0; i < F; ++i)
@@ -404,8 +414,8 @@ __global__ __launch_bounds__(kNT) void product_kernel(Product p) {
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
   const auto load = [&](int k, f16* la, f16* lb) {
     if (k < k1) {
-      load_step<T>(A, pitch, k, la);
-      load_step<T>(B, pitch, k, lb);
+      load_step<T * R, 4 * R>(Ap, pitch, k, la);
+      load_step<T, 4 * R>(Bp, pitch, k, lb);
     }
   };
   // step k, whose loads are complete, and the loads of step k + S - 1 into the
@@ -414,11 +424,11 @@ __global__ __launch_bounds__(kNT) void product_kernel(Product p) {
     if (k >= k1) return;
     const int newer = k1 - 1 - k;
     if (newer >= S - 2)
-      wait_step<T, S - 2>();
+      wait_step<T, R, S - 2>();
     else if (S > 3 && newer == 1)
-      wait_step<T, 1>();
+      wait_step<T, R, 1>();
     else
-      wait_step<T, 0>();
+      wait_step<T, R, 0>();
     load(k + S - 1, na, nb);
     multiply_step<T>(la, lb, acc);
   };
@@ -427,6 +437,13 @@ __global__ __launch_bounds__(kNT) void product_kernel(Product p) {
     for (int k = k0; k < k1; k += 2) {
       step(k, a0, b0, a1, b1);
       step(k + 1, a1, b1, a0, b0);
+    }
+  } else if constexpr (S == 3) {
+    load(k0 + 1, a1, b1);
+    for (int k = k0; k < k1; k += 3) {
+      step(k, a0, b0, a2, b2);
+      step(k + 1, a1, b1, a0, b0);
+      step(k + 2, a2, b2, a1, b1);
     }
   } else {
     load(k0 + 1, a1, b1);
@@ -438,8 +455,9 @@ __global__ __launch_bounds__(kNT) void product_kernel(Product p) {
       step(k + 3, a3, b3, a2, b2);
     }
   }
+  const int half = threadIdx.x / kNT;
   if (rest >= 0 && p.splits > 1) {
-    float* out = p.part + (int64_t)rest * (T * T) + threadIdx.x * 4;
+    float* out = p.part + ((int64_t)rest * R + half) * (T * T) + threadIdx.x % kNT * 4;
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
@@ -462,50 +480,55 @@ __global__ __launch_bounds__(kNT) void product_kernel(Product p) {
         float v[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[r] = acc[i][j][q * 4 + r];
-        epilogue<T, KIND, PT>(p, batch, ti, tj, i, j, q, v);
+        epilogue<T, KIND, PT>(p, batch, ti + half, tj, i, j, q, v);
       }
 }
 
 // Joins the shares of a tile, in order, and finishes it: blockIdx.y is the
 // part of the accumulators, four values a thread.
-template <int T, int KIND, class PT>
+template <int T, int R, int KIND, class PT>
 __global__ __launch_bounds__(kNT) void finish_kernel(Product p) {
   constexpr int F = kFrag<T>;
-  const int all = p.whole + (int)blockIdx.x, batch = all / p.tiles, unit = blockIdx.y;
+  constexpr int64_t next = (int64_t)R * T * T;  // from one share to the next
+  const int block = (int)blockIdx.x / R, half = (int)blockIdx.x % R;
+  const int all = p.whole + block, batch = all / p.tiles, unit = blockIdx.y;
   int ti, tj;
-  tile_of(KIND == kGram || KIND == kPoly, all - batch * p.tiles, p.tiles_n, ti, tj);
-  const float* in = p.part + (int64_t)blockIdx.x * p.splits * (T * T) + unit * (4 * kNT) + threadIdx.x * 4;
+  tile_of<R>(KIND == kGram || KIND == kPoly, all - batch * p.tiles, p.tiles_n, ti, tj);
+  const float* in = p.part + block * p.splits * next + half * (T * T) + unit * (4 * kNT) + threadIdx.x * 4;
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
   int k = 0;
   for (; k + 8 <= p.splits; k += 8) {
     f32x4 v[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const f32x4*>(in + (int64_t)(k + u) * (T * T));
+    for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const f32x4*>(in + (k + u) * next);
 #pragma unroll
     for (int u = 0; u < 8; ++u) s += v[u];
   }
-  for (; k < p.splits; ++k) s += *reinterpret_cast<const f32x4*>(in + (int64_t)k * (T * T));
+  for (; k < p.splits; ++k) s += *reinterpret_cast<const f32x4*>(in + k * next);
   float v[4] = {s[0], s[1], s[2], s[3]};
-  epilogue<T, KIND, PT>(p, batch, ti, tj, unit / (4 * F), unit / 4 % F, unit % 4, v);
+  epilogue<T, KIND, PT>(p, batch, ti + half, tj, unit / (4 * F), unit / 4 % F, unit % 4, v);
 }
 
-template <int T, int KIND, class PT>
+template <int T, int R, int KIND, class PT>
 hipError_t launch_product_t(Product p, const OrthShare& w, int64_t cols, hipStream_t s) {
   p.tiles = (int)w.tiles;
   p.tiles_n = (int)(cols / T);
   p.whole = (int)w.whole;
   p.splits = w.splits;
-  hipLaunchKernelGGL((product_kernel<T, KIND, PT>), dim3((unsigned)(w.whole + w.rest * w.splits)), dim3(kNT), 0, s, p);
+  hipLaunchKernelGGL((product_kernel<T, R, KIND, PT>), dim3((unsigned)(w.whole + w.rest * w.splits)), dim3(kNT * R), 0, s,
+                     p);
   if (w.splits > 1)
-    hipLaunchKernelGGL((finish_kernel<T, KIND, PT>), dim3((unsigned)w.rest, T == 128 ? 16 : 4), dim3(kNT), 0, s, p);
+    hipLaunchKernelGGL((finish_kernel<T, R, KIND, PT>), dim3((unsigned)(w.rest * R), T == 128 ? 16 : 4), dim3(kNT), 0, s,
+                       p);
   return hipGetLastError();
 }
 
 template <int KIND, class PT>
 hipError_t launch_product(const Product& p, int64_t rows, int64_t cols, int64_t batch, hipStream_t s) {
   const OrthShare w = orth_share(rows, cols, batch, KIND == kGram || KIND == kPoly, p.ksteps);
-  if (w.tile == 64) return launch_product_t<64, KIND, PT>(p, w, cols, s);
-  return launch_product_t<128, KIND, PT>(p, w, cols, s);
+  if (w.tile == 64) return launch_product_t<64, 1, KIND, PT>(p, w, cols, s);
+  if (w.pair == 1) return launch_product_t<128, 1, KIND, PT>(p, w, cols, s);
+  return launch_product_t<128, 2, KIND, PT>(p, w, cols, s);
 }
 
 template <class GT, class PT>

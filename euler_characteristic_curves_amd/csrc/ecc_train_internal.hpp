@@ -96,9 +96,10 @@ bool orth_bounds(OrthArgs& o);
 inline int64_t orth_pad(int64_t n) { return n <= 64 ? 64 : (n + 127) / 128 * 128; }
 
 // How a product of `batch` matrices of `rows` x `cols` (padded) results is
-// shared out: `whole` tiles by a workgroup each, the `rest` by `splits` each.
+// shared out: workgroups of `pair` tiles, `tiles` of them a matrix, `whole`
+// of which compute theirs alone and the `rest` with `splits` shares each.
 struct OrthShare {
-  int64_t tile, tiles, whole, rest;
+  int64_t tile, pair, tiles, whole, rest;
   int splits;
 };
 inline OrthShare orth_share(int64_t rows, int64_t cols, int64_t batch, bool sym, int ksteps) {
@@ -108,9 +109,21 @@ inline OrthShare orth_share(int64_t rows, int64_t cols, int64_t batch, bool sym,
     return sym ? tm * (tm + 1) / 2 : tm * tn;
   };
   w.tile = 64;
+  w.pair = 1;
   if (rows >= 128 && cols >= 128 && count(128) * batch * (ksteps >= 16 ? ksteps / 8 : 1) >= 192) w.tile = 128;
   w.tiles = count(w.tile);
-  const int64_t all = w.tiles * batch, slots = w.tile == 128 ? 512 : 1024;
+  int64_t slots = w.tile == 128 ? 512 : 1024;
+  // two tiles a workgroup read fewer columns and have a stage more, but leave
+  // one workgroup a CU: better once the sums are long (3000 x 4000: 2.62 ms,
+  // 2.83 with one; 1500 x 1500: 512 and 521 us), worse before (1024 x 1024: 315
+  // and 298; 12 x 700 x 1000: 956 and 838)
+  if (w.tile == 128 && rows % 256 == 0 && ksteps >= 44) {
+    const int64_t tm = rows / 256;
+    w.pair = 2;
+    w.tiles = sym ? tm * (tm + 1) : tm * (cols / 128);
+    slots = 256;
+  }
+  const int64_t all = w.tiles * batch;
   w.whole = all / slots * slots;
   w.rest = all - w.whole;
   w.splits = 1;
@@ -128,7 +141,7 @@ inline OrthShare orth_share(int64_t rows, int64_t cols, int64_t batch, bool sym,
 }
 inline size_t orth_part_bytes(int64_t rows, int64_t cols, int64_t batch, bool sym, int64_t k) {
   const OrthShare w = orth_share(rows, cols, batch, sym, (int)((k + 31) / 32));
-  return w.splits > 1 ? (size_t)(w.rest * w.splits * w.tile * w.tile) * sizeof(float) : 0;
+  return w.splits > 1 ? (size_t)(w.rest * w.splits * w.pair * w.tile * w.tile) * sizeof(float) : 0;
 }
 
 // Workspace: offsets in bytes.
