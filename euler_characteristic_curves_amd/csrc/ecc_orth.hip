@@ -214,50 +214,80 @@ __device__ __forceinline__ void tile_of(bool sym, int t, int tiles_n, int& ti, i
   }
 }
 
-// Stores 4 values v of rows r..r+3, column c of a tile: transposed, they are 4
-// consecutive columns of row c.
-__device__ __forceinline__ void store_pair4(f16* out, int64_t row, int64_t col, int64_t kpad, const float* v) {
-  f16x4 hi, lo;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    f16 h, l;
-    split(v[j], h, l);
-    hi[j] = h;
-    lo[j] = l;
-  }
-  f16* p = out + pair_at(row, col, kpad);
-  *reinterpret_cast<f16x4*>(p) = hi;
-  *reinterpret_cast<f16x4*>(p + 32) = lo;
-}
-__device__ __forceinline__ void store_pair1(f16* out, int64_t row, int64_t col, int64_t kpad, float v) {
-  f16 h, l;
-  split(v, h, l);
-  f16* p = out + pair_at(row, col, kpad);
-  p[0] = h;
-  p[32] = l;
-}
-
-// One result element of the last step, in the caller's orientation.
+// Four neighbouring results of the last step, columns i..i+3 of row j of the
+// short side's view, in the caller's orientation.
 template <class PT>
-__device__ __forceinline__ void store_result(const OrthArgs& o, int64_t batch, int64_t i, int64_t j, float v) {
-  if (o.rows > o.cols) {
-    const int64_t t = i;
-    i = j;
-    j = t;
+__device__ __forceinline__ void store_result(const OrthArgs& o, int64_t batch, int64_t i, int64_t j, const float* v) {
+  PT* out = reinterpret_cast<PT*>(o.out) + batch * o.rows * o.cols;
+  if (o.rows > o.cols) {  // row j, columns i..i+3: one access
+    if (j >= o.rows) return;
+    out += j * o.cols + i;
+    if (i + 4 <= o.cols) {
+      Vec<PT, 4> r;
+      if (o.buffer) load_vec(out, r);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r.v[k] = (PT)(o.buffer ? fmaf((float)r.v[k], o.keep, -o.rate * v[k]) : v[k]);
+      store_vec(out, r);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k < o.cols) out[k] = (PT)(o.buffer ? fmaf((float)out[k], o.keep, -o.rate * v[k]) : v[k]);
+    }
+    return;
   }
-  if (i >= o.rows || j >= o.cols) return;
-  PT* out = reinterpret_cast<PT*>(o.out) + (batch * o.rows + i) * o.cols + j;
-  if (o.buffer)
-    *out = (PT)fmaf((float)*out, o.keep, -o.rate * v);
-  else
-    *out = (PT)v;
+  if (j >= o.cols) return;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (i + k >= o.rows) return;
+    PT* at = out + (i + k) * o.cols + j;
+    *at = (PT)(o.buffer ? fmaf((float)*at, o.keep, -o.rate * v[k]) : v[k]);
+  }
 }
 
-// Four values of a thread: rows r..r+3 (of fragment fi's group q) and one
-// column (of fragment fj) of a tile.
+// 32 x 32 values of a wave as pairs, through 4 KB of LDS of its own, so that
+// rows of 128 bytes are written whole: a lane holds column lane % 32 of rows
+// 8 q + 4 (lane / 32) + r.  TURN: the rows written are those columns.  `out`:
+// the block's first row.  Chunks of 16 bytes are permuted by the row.
+template <bool TURN>
+__device__ __forceinline__ void store_block(f16* out, int64_t pitch, const f32x16& v, f16* lds) {
+  const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (TURN) {
+      f16x4 hi, lo;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        f16 a, b;
+        split(v[q * 4 + r], a, b);
+        hi[r] = a;
+        lo[r] = b;
+      }
+      *reinterpret_cast<f16x4*>(lds + c * 64 + ((q ^ (c & 7)) << 3) + h * 4) = hi;
+      *reinterpret_cast<f16x4*>(lds + c * 64 + (((q + 4) ^ (c & 7)) << 3) + h * 4) = lo;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = q * 8 + h * 4 + r;
+        f16 a, b;
+        split(v[q * 4 + r], a, b);
+        lds[row * 64 + (((c >> 3) ^ (row & 7)) << 3) + (c & 7)] = a;
+        lds[row * 64 + ((((c >> 3) + 4) ^ (row & 7)) << 3) + (c & 7)] = b;
+      }
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int row = n * 8 + (lane >> 3), ch = lane & 7;
+    *reinterpret_cast<f16x8*>(out + row * pitch + ch * 8) =
+        *reinterpret_cast<const f16x8*>(lds + row * 64 + ((ch ^ (row & 7)) << 3));
+  }
+}
+
+// One fragment of a wave's results; lds: 4 KB of its own.
 template <int T, int KIND, class PT>
-__device__ __forceinline__ void epilogue(const Product& p, int batch, int ti, int tj, int fi, int fj, int q,
-                                         float (&v)[4]) {
+__device__ __forceinline__ void epilogue(const Product& p, int batch, int ti, int tj, int fi, int fj, f32x16 v, f16* lds) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6 & 3;
   if ((KIND == kGram || KIND == kPoly) && ti < tj) return;
   const float* xs = p.o.scales + (int64_t)batch * (p.o.steps + 1) + p.step;
@@ -270,33 +300,33 @@ __device__ __forceinline__ void epilogue(const Product& p, int batch, int ti, in
     f = xs[1] / (p.sp * xs[0]);
   else
     f = 1.0f / (p.sp * xs[0]);
-  f16* out = p.out + (int64_t)batch * p.sOut;
-  const int64_t j = (int64_t)tj * T + (wave & 1) * (T / 2) + fj * 32 + (lane & 31);
-  const int64_t i = (int64_t)ti * T + (wave >> 1) * (T / 2) + fi * 32 + q * 8 + (lane >> 5) * 4;
+  const int64_t j0 = (int64_t)tj * T + (wave & 1) * (T / 2) + fj * 32, i0 = (int64_t)ti * T + (wave >> 1) * (T / 2) + fi * 32;
+  const int64_t j = j0 + (lane & 31);
 #pragma unroll
-  for (int r = 0; r < 4; ++r) v[r] *= f;
-  if constexpr (KIND == kPoly) {
-    const f16* gp = p.gram + (int64_t)batch * p.sOut + pair_at(j, i, p.out_pad);
-    const f16x4 gh = *reinterpret_cast<const f16x4*>(gp), gl = *reinterpret_cast<const f16x4*>(gp + 32);
+  for (int q = 0; q < 4; ++q) {
+    const int64_t i = i0 + q * 8 + (lane >> 5) * 4;
+    float u[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      v[r] = fmaf(p.o.b * p.sp / p.sa, (float)gh[r] + (float)gl[r], v[r]);
-      if (i + r == j) v[r] += p.o.a * p.sp;
+    for (int r = 0; r < 4; ++r) u[r] = v[q * 4 + r] * f;
+    if constexpr (KIND == kPoly) {
+      const f16* gp = p.gram + (int64_t)batch * p.sOut + pair_at(j, i, p.out_pad);
+      const f16x4 gh = *reinterpret_cast<const f16x4*>(gp), gl = *reinterpret_cast<const f16x4*>(gp + 32);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        u[r] = fmaf(p.o.b * p.sp / p.sa, (float)gh[r] + (float)gl[r], u[r]);
+        if (i + r == j) u[r] += p.o.a * p.sp;
+      }
     }
+    if constexpr (KIND == kLast) store_result<PT>(p.o, batch, i, j, u);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[q * 4 + r] = u[r];
   }
-  if constexpr (KIND == kGram || KIND == kPoly) {
-    store_pair4(out, j, i, p.out_pad, v);
-    if (ti != tj)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) store_pair1(out, i + r, j, p.out_pad, v[r]);
-  } else if constexpr (KIND == kUpdate) {
-    store_pair4(p.outT + (int64_t)batch * p.sOut, j, i, p.outT_pad, v);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) store_pair1(out, i + r, j, p.out_pad, v[r]);
-  } else {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) store_result<PT>(p.o, batch, i + r, j, v[r]);
-  }
+  if constexpr (KIND == kLast) return;
+  f16* out = p.out + (int64_t)batch * p.sOut;
+  f16* turned = KIND == kUpdate ? p.outT + (int64_t)batch * p.sOut : out;
+  const int64_t tpad = KIND == kUpdate ? p.outT_pad : p.out_pad;
+  store_block<true>(turned + pair_at(j0, i0, tpad), 2 * tpad, v, lds);
+  if (KIND == kUpdate || ti != tj) store_block<false>(out + pair_at(i0, j0, p.out_pad), 2 * p.out_pad, v, lds);
 }
 
 // Loads one step (32 columns, T rows, 128 bytes a row) of an operand to LDS.
@@ -370,13 +400,6 @@ __device__ __forceinline__ void multiply_step(const f16* la, const f16* lb, f32x
   __builtin_amdgcn_sched_group_barrier(0x008, 6 * F * F - 6 * F, 0);
 }
 
-// Steps of the long axis that are in LDS or on their way to it, the one in use
-// counted.  A small tile is done with a step before the next could arrive; two
-// workgroups of one 128-tile fill the LDS with two stages each, one of two
-// tiles with three stages of 48 KB.
-template <int T, int R>
-constexpr int kStages = T == 64 ? 4 : (R == 2 ? 3 : 2);
-
 // Waits for all but the newest N steps' loads of this wave and for what it has
 // read of LDS, then for the other waves.  (A workgroup fence would wait for
 // every load; one block, and ordered with memory, so that no read of LDS is
@@ -388,10 +411,11 @@ __device__ __forceinline__ void wait_step() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(vm) : "memory");
 }
 
-// R tiles of a product, or a share of their columns.
-template <int T, int R, int KIND, class PT>
+// R tiles of a product, or a share of their columns.  S: steps of the long
+// axis that are in LDS or on their way to it, the one in use counted.
+template <int T, int R, int S, int KIND, class PT>
 __global__ __launch_bounds__(kNT * R) void product_kernel(Product p) {
-  constexpr int F = kFrag<T>, S = kStages<T, R>, A = T * R * 64, B = T * 64;
+  constexpr int F = kFrag<T>, A = T * R * 64, B = T * 64;
   // arrays of their own, so that a read of one is known not to wait for another's loads
   __shared__ __align__(16) f16 a0[A], b0[B], a1[A], b1[B];
   __shared__ __align__(16) f16 a2[S > 2 ? A : 8], b2[S > 2 ? B : 8], a3[S > 3 ? A : 8], b3[S > 3 ? B : 8];
@@ -471,54 +495,62 @@ __global__ __launch_bounds__(kNT * R) void product_kernel(Product p) {
         }
     return;
   }
+  wait_step<T, R, 0>();  // the stages are free: 4 KB of the first ones for each wave
+  f16* mine = R == 1 ? (threadIdx.x < kNT / 2 ? a0 : b0) + (threadIdx.x >> 6 & 1) * 2048 : a0 + (threadIdx.x >> 6) * 2048;
 #pragma unroll
   for (int i = 0; i < F; ++i)
 #pragma unroll
-    for (int j = 0; j < F; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float v[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = acc[i][j][q * 4 + r];
-        epilogue<T, KIND, PT>(p, batch, ti + half, tj, i, j, q, v);
-      }
+    for (int j = 0; j < F; ++j) epilogue<T, KIND, PT>(p, batch, ti + half, tj, i, j, acc[i][j], mine);
 }
 
 // Joins the shares of a tile, in order, and finishes it: blockIdx.y is the
-// part of the accumulators, four values a thread.
+// fragment of each of the four waves.
 template <int T, int R, int KIND, class PT>
 __global__ __launch_bounds__(kNT) void finish_kernel(Product p) {
   constexpr int F = kFrag<T>;
   constexpr int64_t next = (int64_t)R * T * T;  // from one share to the next
+  __shared__ __align__(16) f16 lds[4 * 2048];
   const int block = (int)blockIdx.x / R, half = (int)blockIdx.x % R;
-  const int all = p.whole + block, batch = all / p.tiles, unit = blockIdx.y;
+  const int all = p.whole + block, batch = all / p.tiles;
   int ti, tj;
   tile_of<R>(KIND == kGram || KIND == kPoly, all - batch * p.tiles, p.tiles_n, ti, tj);
-  const float* in = p.part + block * p.splits * next + half * (T * T) + unit * (4 * kNT) + threadIdx.x * 4;
-  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+  const float* in = p.part + block * p.splits * next + half * (T * T) + (int64_t)blockIdx.y * (16 * kNT) + threadIdx.x * 4;
+  f32x4 s[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) s[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   int k = 0;
-  for (; k + 8 <= p.splits; k += 8) {
-    f32x4 v[8];
+  for (; k + 3 <= p.splits; k += 3) {
+    f32x4 v[3][4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const f32x4*>(in + (k + u) * next);
+    for (int u = 0; u < 3; ++u)
 #pragma unroll
-    for (int u = 0; u < 8; ++u) s += v[u];
+      for (int q = 0; q < 4; ++q) v[u][q] = *reinterpret_cast<const f32x4*>(in + (k + u) * next + q * (4 * kNT));
+#pragma unroll
+    for (int u = 0; u < 3; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s[q] += v[u][q];
   }
-  for (; k < p.splits; ++k) s += *reinterpret_cast<const f32x4*>(in + k * next);
-  float v[4] = {s[0], s[1], s[2], s[3]};
-  epilogue<T, KIND, PT>(p, batch, ti + half, tj, unit / (4 * F), unit / 4 % F, unit % 4, v);
+  for (; k < p.splits; ++k)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s[q] += *reinterpret_cast<const f32x4*>(in + k * next + q * (4 * kNT));
+  f32x16 v;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[q * 4 + r] = s[q][r];
+  epilogue<T, KIND, PT>(p, batch, ti + half, tj, (int)blockIdx.y / F, (int)blockIdx.y % F, v, lds + (threadIdx.x >> 6) * 2048);
 }
 
-template <int T, int R, int KIND, class PT>
+template <int T, int R, int S, int KIND, class PT>
 hipError_t launch_product_t(Product p, const OrthShare& w, int64_t cols, hipStream_t s) {
   p.tiles = (int)w.tiles;
   p.tiles_n = (int)(cols / T);
   p.whole = (int)w.whole;
   p.splits = w.splits;
-  hipLaunchKernelGGL((product_kernel<T, R, KIND, PT>), dim3((unsigned)(w.whole + w.rest * w.splits)), dim3(kNT * R), 0, s,
+  hipLaunchKernelGGL((product_kernel<T, R, S, KIND, PT>), dim3((unsigned)(w.whole + w.rest * w.splits)), dim3(kNT * R), 0, s,
                      p);
   if (w.splits > 1)
-    hipLaunchKernelGGL((finish_kernel<T, R, KIND, PT>), dim3((unsigned)(w.rest * R), T == 128 ? 16 : 4), dim3(kNT), 0, s,
+    hipLaunchKernelGGL((finish_kernel<T, R, KIND, PT>), dim3((unsigned)(w.rest * R), kFrag<T> * kFrag<T>), dim3(kNT), 0, s,
                        p);
   return hipGetLastError();
 }
@@ -526,9 +558,10 @@ hipError_t launch_product_t(Product p, const OrthShare& w, int64_t cols, hipStre
 template <int KIND, class PT>
 hipError_t launch_product(const Product& p, int64_t rows, int64_t cols, int64_t batch, hipStream_t s) {
   const OrthShare w = orth_share(rows, cols, batch, KIND == kGram || KIND == kPoly, p.ksteps);
-  if (w.tile == 64) return launch_product_t<64, 1, KIND, PT>(p, w, cols, s);
-  if (w.pair == 1) return launch_product_t<128, 1, KIND, PT>(p, w, cols, s);
-  return launch_product_t<128, 2, KIND, PT>(p, w, cols, s);
+  if (w.tile == 64) return launch_product_t<64, 1, 4, KIND, PT>(p, w, cols, s);
+  if (w.pair == 2) return launch_product_t<128, 2, 3, KIND, PT>(p, w, cols, s);
+  if (w.deep) return launch_product_t<128, 1, 4, KIND, PT>(p, w, cols, s);
+  return launch_product_t<128, 1, 2, KIND, PT>(p, w, cols, s);
 }
 
 template <class GT, class PT>

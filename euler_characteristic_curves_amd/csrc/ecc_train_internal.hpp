@@ -101,6 +101,7 @@ inline int64_t orth_pad(int64_t n) { return n <= 64 ? 64 : (n + 127) / 128 * 128
 struct OrthShare {
   int64_t tile, pair, tiles, whole, rest;
   int splits;
+  bool deep;  // four stages in place of two, one workgroup a CU
 };
 inline OrthShare orth_share(int64_t rows, int64_t cols, int64_t batch, bool sym, int ksteps) {
   OrthShare w{};
@@ -124,6 +125,8 @@ inline OrthShare orth_share(int64_t rows, int64_t cols, int64_t batch, bool sym,
     slots = 256;
   }
   const int64_t all = w.tiles * batch;
+  w.deep = w.tile == 128 && w.pair == 1 && all <= 256;
+  if (w.deep) slots = 256;
   w.whole = all / slots * slots;
   w.rest = all - w.whole;
   w.splits = 1;
