@@ -149,6 +149,8 @@ __global__ __launch_bounds__(256) void long_join_kernel(Long t, double* A) {
 // Products of commuting symmetric matrices [batch][m][m]: C = X Y, or the
 // polynomial c X X + b X + a I (poly), or X Y as a pair matrix times `scale`.
 // blockIdx.x: 32 x 32 tile of the lower triangle; .y: one of up to two products.
+// A tile below the diagonal is written twice; one on it is whole by itself, and
+// its two halves, which differ in their last bits, each have one writer.
 struct Square {
   const double* x[2];
   const double* y[2];
@@ -218,12 +220,14 @@ __global__ __launch_bounds__(kNT) void long_square_kernel(Square p) {
       const int64_t at = row * 2 * p.m + (col >> 5) * 64 + (col & 31), to = col * 2 * p.m + (row >> 5) * 64 + (row & 31);
       out[at] = hi;
       out[at + 32] = lo;
-      out[to] = hi;
-      out[to + 32] = lo;
+      if (bi != bj) {
+        out[to] = hi;
+        out[to + 32] = lo;
+      }
     } else {
       double* out = (second ? p.out[1] : p.out[0]) + off;
       out[row * p.m + col] = s;
-      out[col * p.m + row] = s;
+      if (bi != bj) out[col * p.m + row] = s;
     }
   }
 }

@@ -286,3 +286,14 @@ def test_muon_carried(shape, nesterov, pdtype, gdtype):
 @pytest.mark.parametrize("shape", [(2, 50, 900), (700, 100)], ids=lambda s: "x".join(map(str, s)))
 def test_graph_replays_carried(shape):
     test_graph_replays(shape)
+
+
+@pytest.mark.parametrize("shape", [(2, 140, 300), (2, 45, 700), (1000, 1000), (9, 130, 140)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_repeats_bit_for_bit(shape):
+    """No value depends on which workgroup wrote last."""
+    banner("orth repeats", shape)
+    g = gradient(shape, seed=15).cuda()
+    first = E.orthogonalize(g)
+    for _ in range(20):
+        assert torch.equal(E.orthogonalize(g), first)
