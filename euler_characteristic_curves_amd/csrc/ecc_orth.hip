@@ -16,8 +16,10 @@
 // matrix and step for X, per call for A and P.  What bounds the products is
 // the matrix unit; the pair is three times cheaper for LDS and L2 than for it.
 //
-// Layout.  A pair matrix keeps, per row, blocks of 32 columns as 32 hi then 32
-// lo: 128 bytes, the unit a tile's row loads per step of the long axis.  Both
+// Layout.  A pair matrix keeps blocks of 32 columns one after the other, in
+// each its rows of 32 hi and 32 lo, 128 bytes: what a tile loads per step of
+// the long axis is one piece, and its steps spread over L2's channels, which
+// rows of a length like 16 KB do not (4096 x 4096: 4.2 ms so).  Both
 // operands of a product lie along the summed axis, so X is kept twice, as X
 // and as X^T.  Rows and columns are padded with zeros to the tile, and stay
 // zero, so no product checks a bound.
@@ -40,9 +42,9 @@ typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// Offset of element (row, col) of a pair matrix whose rows have `kpad` columns.
-__device__ __forceinline__ int64_t pair_at(int64_t row, int64_t col, int64_t kpad) {
-  return row * 2 * kpad + (col >> 5) * 64 + (col & 31);
+// Offset of element (row, col) of a pair matrix of `rows` rows.
+__device__ __forceinline__ int64_t pair_at(int64_t row, int64_t col, int64_t rows) {
+  return ((col >> 5) * rows + row) * 64 + (col & 31);
 }
 
 // ------------------------------------------------------------- preparation
@@ -164,8 +166,8 @@ __global__ __launch_bounds__(kNT) void orth_prepare_kernel(OrthArgs p, f16* P1, 
       split(tile[k + j][row], hi, lo);
       b[j] = low ? lo : hi;
     }
-    if (!D || tall) *reinterpret_cast<f16x8*>(out1 + (r0 + row) * 2 * cpad + c0 * 2 + ch * 8) = a;
-    if (!D || !tall) *reinterpret_cast<f16x8*>(out2 + (c0 + row) * 2 * rpad + r0 * 2 + ch * 8) = b;
+    if (!D || tall) *reinterpret_cast<f16x8*>(out1 + pair_at(r0 + row, c0 + (ch >> 3) * 32, rpad) + (ch & 7) * 8) = a;
+    if (!D || !tall) *reinterpret_cast<f16x8*>(out2 + pair_at(c0 + row, r0 + (ch >> 3) * 32, cpad) + (ch & 7) * 8) = b;
   }
 }
 
@@ -176,7 +178,7 @@ enum Kind { kGram, kPoly, kUpdate, kLast };
 struct Product {
   const f16 *A, *B;    // [batch][rows][2 kpad]
   int64_t sA, sB;      // batch strides, elements
-  int64_t kpad;        // columns of both operands
+  int64_t rowsA, rowsB;  // padded
   int ksteps;          // steps of 32 columns that are not all padding
   int tiles, tiles_n;  // workgroups of one matrix, column tiles
   int whole;           // workgroups, of all matrices, that one workgroup computes
@@ -185,7 +187,7 @@ struct Product {
   int step;
   float sa, sp;        // scales of A and of P
   f16 *out, *outT;     // pair matrices written (outT: the transpose, of kUpdate)
-  int64_t sOut, out_pad, outT_pad;
+  int64_t sOut, out_rows, outT_rows;
   const f16* gram;     // kPoly: the matrix A itself
   OrthArgs o;
 };
@@ -245,11 +247,11 @@ __device__ __forceinline__ void store_result(const OrthArgs& o, int64_t batch, i
 }
 
 // 32 x 32 values of a wave as pairs, through 4 KB of LDS of its own, so that
-// rows of 128 bytes are written whole: a lane holds column lane % 32 of rows
+// they are written as one piece: a lane holds column lane % 32 of rows
 // 8 q + 4 (lane / 32) + r.  TURN: the rows written are those columns.  `out`:
-// the block's first row.  Chunks of 16 bytes are permuted by the row.
+// where the block lies.  Chunks of 16 bytes are permuted by the row.
 template <bool TURN>
-__device__ __forceinline__ void store_block(f16* out, int64_t pitch, const f32x16& v, f16* lds) {
+__device__ __forceinline__ void store_block(f16* out, const f32x16& v, f16* lds) {
   const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
   __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -280,7 +282,7 @@ __device__ __forceinline__ void store_block(f16* out, int64_t pitch, const f32x1
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
     const int row = n * 8 + (lane >> 3), ch = lane & 7;
-    *reinterpret_cast<f16x8*>(out + row * pitch + ch * 8) =
+    *reinterpret_cast<f16x8*>(out + row * 64 + ch * 8) =
         *reinterpret_cast<const f16x8*>(lds + row * 64 + ((ch ^ (row & 7)) << 3));
   }
 }
@@ -309,7 +311,7 @@ __device__ __forceinline__ void epilogue(const Product& p, int batch, int ti, in
 #pragma unroll
     for (int r = 0; r < 4; ++r) u[r] = v[q * 4 + r] * f;
     if constexpr (KIND == kPoly) {
-      const f16* gp = p.gram + (int64_t)batch * p.sOut + pair_at(j, i, p.out_pad);
+      const f16* gp = p.gram + (int64_t)batch * p.sOut + pair_at(j, i, p.out_rows);
       const f16x4 gh = *reinterpret_cast<const f16x4*>(gp), gl = *reinterpret_cast<const f16x4*>(gp + 32);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -324,27 +326,32 @@ __device__ __forceinline__ void epilogue(const Product& p, int batch, int ti, in
   if constexpr (KIND == kLast) return;
   f16* out = p.out + (int64_t)batch * p.sOut;
   f16* turned = KIND == kUpdate ? p.outT + (int64_t)batch * p.sOut : out;
-  const int64_t tpad = KIND == kUpdate ? p.outT_pad : p.out_pad;
-  store_block<true>(turned + pair_at(j0, i0, tpad), 2 * tpad, v, lds);
-  if (KIND == kUpdate || ti != tj) store_block<false>(out + pair_at(i0, j0, p.out_pad), 2 * p.out_pad, v, lds);
+  store_block<true>(turned + pair_at(j0, i0, KIND == kUpdate ? p.outT_rows : p.out_rows), v, lds);
+  if (KIND == kUpdate || ti != tj) store_block<false>(out + pair_at(i0, j0, p.out_rows), v, lds);
 }
 
 // Loads one step (32 columns, T rows, 128 bytes a row) of an operand to LDS.
 // A wave's load covers 8 rows; the 16-byte chunk a lane fetches is permuted
 // within its row by the row's number, so that the fragment reads below, 8 rows
 // at one chunk, meet 8 different groups of banks.
+// `step`: where the step's rows begin, the same for every lane, so that a load
+// has a scalar base, one register of offsets (in_step) and a constant, which
+// the hardware adds to both addresses.
 template <int ROWS, int WAVES>
-__device__ __forceinline__ void load_step(const f16* base, int64_t pitch, int kstep, f16* lds) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r = lane >> 3, ch = (lane & 7) ^ r;
-  constexpr int N = ROWS / 8 / WAVES;
-#pragma unroll
-  for (int q = 0; q < N; ++q) {
-    const int row0 = (wave * N + q) * 8;
-    const f16* src = base + (int64_t)(row0 + r) * pitch + (int64_t)kstep * 64 + ch * 8;
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                     (__attribute__((address_space(3))) void*)(lds + row0 * 64), 16, 0, 0);
-  }
+__device__ __forceinline__ uint32_t in_step() {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane >> 3;
+  return (uint32_t)(wave * (ROWS / WAVES) * 128 + r * 128 + ((lane & 7) ^ r) * 16);
+}
+template <int N>
+__device__ __forceinline__ void load_rows(const char* src, f16* dst) {
+  if constexpr (N > 1) load_rows<N - 1>(src, dst);
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)dst, 16, (N - 1) * 1024, 0);
+}
+template <int ROWS, int WAVES>
+__device__ __forceinline__ void load_step(const f16* step, uint32_t offset, f16* lds) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  load_rows<ROWS / 8 / WAVES>(reinterpret_cast<const char*>(step) + offset, lds + wave * (ROWS / WAVES) * 64);
 }
 
 template <int T>
@@ -414,7 +421,7 @@ __device__ __forceinline__ void wait_step() {
 // R tiles of a product, or a share of their columns.  S: steps of the long
 // axis that are in LDS or on their way to it, the one in use counted.
 template <int T, int R, int S, int KIND, class PT>
-__global__ __launch_bounds__(kNT * R) void product_kernel(Product p) {
+__global__ __launch_bounds__(kNT * R, T == 128 && S == 4 ? 1 : 2) void product_kernel(Product p) {
   constexpr int F = kFrag<T>, A = T * R * 64, B = T * 64;
   // arrays of their own, so that a read of one is known not to wait for another's loads
   __shared__ __align__(16) f16 a0[A], b0[B], a1[A], b1[B];
@@ -424,11 +431,13 @@ __global__ __launch_bounds__(kNT * R) void product_kernel(Product p) {
   const int batch = all / p.tiles;
   int ti, tj;
   tile_of<R>(KIND == kGram || KIND == kPoly, all - batch * p.tiles, p.tiles_n, ti, tj);
+  ti = __builtin_amdgcn_readfirstlane(ti);
+  tj = __builtin_amdgcn_readfirstlane(tj);
   const int per = rest < 0 ? p.ksteps : (p.ksteps + p.splits - 1) / p.splits;
   const int k0 = sp * per, k1 = k0 + per < p.ksteps ? k0 + per : p.ksteps;
-  const int64_t pitch = 2 * p.kpad;
-  const f16* Ap = p.A + batch * p.sA + (int64_t)ti * T * pitch;
-  const f16* Bp = p.B + batch * p.sB + (int64_t)tj * T * pitch;
+  const f16* Ap = p.A + batch * p.sA + (int64_t)ti * T * 64;
+  const f16* Bp = p.B + batch * p.sB + (int64_t)tj * T * 64;
+  const uint32_t offA = in_step<T * R, 4 * R>(), offB = in_step<T, 4 * R>();
   f32x16 acc[F][F];
 #pragma unroll
   for (int i = 0; i < F; ++i)
@@ -438,8 +447,8 @@ __global__ __launch_bounds__(kNT * R) void product_kernel(Product p) {
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
   const auto load = [&](int k, f16* la, f16* lb) {
     if (k < k1) {
-      load_step<T * R, 4 * R>(Ap, pitch, k, la);
-      load_step<T, 4 * R>(Bp, pitch, k, lb);
+      load_step<T * R, 4 * R>(Ap + k * p.rowsA * 64, offA, la);
+      load_step<T, 4 * R>(Bp + k * p.rowsB * 64, offB, lb);
     }
   };
   // step k, whose loads are complete, and the loads of step k + S - 1 into the
@@ -597,7 +606,8 @@ hipError_t run(const OrthArgs& o, hipStream_t s) {
     p.sA = sm;
     p.B = XT[0];
     p.sB = sx;
-    p.kpad = w.mpad;
+    p.rowsA = w.mpad;
+    p.rowsB = w.npad;
     p.ksteps = (int)((w.m + 31) / 32);
     return launch_product<kLast, PT>(p, w.mpad, w.npad, a.batch, s);
   }
@@ -611,16 +621,15 @@ hipError_t run(const OrthArgs& o, hipStream_t s) {
     p.part = part;
     p.A = p.B = X[in];
     p.sA = p.sB = sx;
-    p.kpad = w.npad;
+    p.rowsA = p.rowsB = w.mpad;
     p.ksteps = (int)((w.n + 31) / 32);
     p.out = A;
     p.sOut = sm;
-    p.out_pad = w.mpad;
+    p.out_rows = w.mpad;
     hipError_t e = launch_product<kGram, float>(p, w.mpad, w.mpad, a.batch, s);
     if (e != hipSuccess) return e;
     p.A = p.B = p.gram = A;
     p.sA = p.sB = sm;
-    p.kpad = w.mpad;
     p.ksteps = (int)((w.m + 31) / 32);
     p.out = P;
     e = launch_product<kPoly, float>(p, w.mpad, w.mpad, a.batch, s);
@@ -628,11 +637,11 @@ hipError_t run(const OrthArgs& o, hipStream_t s) {
     p.A = P;
     p.B = XT[in];
     p.sB = sx;
+    p.rowsB = w.npad;
     p.out = X[on];
     p.outT = XT[on];
     p.sOut = sx;
-    p.out_pad = w.npad;
-    p.outT_pad = w.mpad;
+    p.outT_rows = w.npad;
     e = k + 1 < a.steps ? launch_product<kUpdate, float>(p, w.mpad, w.npad, a.batch, s)
                         : launch_product<kLast, PT>(p, w.mpad, w.npad, a.batch, s);
     if (e != hipSuccess) return e;

@@ -217,7 +217,7 @@ __global__ __launch_bounds__(kNT) void long_square_kernel(Square p) {
       const float v = (float)(s * p.scale);
       const f16 hi = (f16)v, lo = (f16)(v - (float)hi);
       f16* out = p.pair + off * 2;
-      const int64_t at = row * 2 * p.m + (col >> 5) * 64 + (col & 31), to = col * 2 * p.m + (row >> 5) * 64 + (row & 31);
+      const int64_t at = ((col >> 5) * p.m + row) * 64 + (col & 31), to = ((row >> 5) * p.m + col) * 64 + (row & 31);
       out[at] = hi;
       out[at + 32] = lo;
       if (bi != bj) {
