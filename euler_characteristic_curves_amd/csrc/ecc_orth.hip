@@ -13,13 +13,20 @@
 // products, hi hi' + hi lo' + lo hi', summed in float32 (the dropped lo lo' is
 // below 2^-24).  The exponent s comes from a bound of the matrix's entries, so
 // that nothing overflows and lo stays above float16's smallest number: per
-// matrix and step for X, per call for A and P.  What bounds the products is
-// the matrix unit; the pair is three times cheaper for LDS and L2 than for it.
+// matrix and step for X, per call for A and P.
+//
+// What bounds the products: the matrix unit, whose cycles the clock makes
+// dearer under load.  4096 x 4096 runs at 1.03e15 float16 operations a second
+// (a library's product of that size in float16: 1.16e15), the unit busy half
+// the cycles at 1.9 GHz; short sums, the pipeline's start and the launches.
+// Matrices up to 64 across, and long ones, take other ways (orth_is_thin,
+// orth_is_long).
 //
 // Layout.  A pair matrix keeps blocks of 32 columns one after the other, in
 // each its rows of 32 hi and 32 lo, 128 bytes: what a tile loads per step of
-// the long axis is one piece, and its steps spread over L2's channels, which
-// rows of a length like 16 KB do not (4096 x 4096: 4.2 ms so).  Both
+// the long axis is one piece, as is the 32 x 32 block a wave writes, and a
+// load needs a scalar base and constants only (with rows one after the other,
+// 64-bit addresses per lane: 4096 x 4096 4.19 ms, 4.00 so).  Both
 // operands of a product lie along the summed axis, so X is kept twice, as X
 // and as X^T.  Rows and columns are padded with zeros to the tile, and stay
 // zero, so no product checks a bound.

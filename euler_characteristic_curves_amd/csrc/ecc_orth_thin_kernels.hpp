@@ -16,10 +16,13 @@
 // matrix instructions; launch_orth leaves the cases whose growth would pass
 // 2^26 to the direct iteration.  The final product is float32.
 //
-// What bounds it: the two passes, HBM; the steps, one workgroup per matrix,
-// the float64 matrix rate of a CU, 1.3 us per 64^3 product (lower triangle of
-// tiles), 14 of them in 5 steps, of which the critical ones depend on each
-// other.
+// What bounds it: the two passes, HBM and latency; the steps, one workgroup per
+// matrix, the float64 matrix rate of a CU (64 cycles an instruction), 1.3 us
+// per 64^3 product (lower triangle of tiles), 14 of them in 5 steps, and the
+// strips each phase reads from LDS before it can multiply.  24 matrices of 64 x
+// 1728 in float32, momentum step: 15 us for A_0, 40 for the steps, 19 for the
+// result, 73 in all (three products a step on pairs: 267; floor of the bytes:
+// 11).  27 x 64 in one launch: 13.5 us (17 launches: 64).
 //
 // Orientation.  m is the short side.  `tall` matrices (rows > cols) keep the
 // short side contiguous; lanes then take MB consecutive short-side elements,
