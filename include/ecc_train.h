@@ -115,9 +115,12 @@ size_t ecc_norm_workspace_bytes(int64_t batch, int64_t voxels, int64_t channels,
  * (with X^T in place of X where rows > cols), written to out (dtype, g's
  * shape; may be g itself).  The singular vectors stay, the singular values are
  * driven towards 1 by the polynomial a s + b s^3 + c s^5.
- * The norm is summed in float64; products take operands of 22 significant bits
- * (pairs of float16) and sum in float32, so the result is that of float32
- * arithmetic, rounded once to dtype.
+ * The norm is summed in float64.  Products take operands of 22 significant bits
+ * (pairs of float16) and sum in float32; where the short side is at most 64, or
+ * small beside the long one, and the steps let an error of X X^T grow by less
+ * than 2^26, X X^T is carried through the steps in float64 instead and the long
+ * side passed twice only.  Either way the result is that of float32 arithmetic,
+ * rounded once to dtype.
  * Refused with ECC_E_VALUE: steps outside [1, ECC_MAX_NS_STEPS], eps < 0, a
  * coefficient that is not finite, and coefficients under which a singular
  * value in [0, 1] leaves [-16, 16] within the steps.
