@@ -33,15 +33,18 @@ struct NormArgs {
   void* ws;
 };
 
-// Workgroups per sample of a pass over the features, `total` in a launch; each
-// has at least 4096 elements.  Passes that hold sums or both gradients need 80
+// Workgroups per sample of a pass over the features, `total` in a launch.  Each
+// has at least 4096 elements, or 8192 where it leaves partial sums, which the
+// next pass has to read (256 x 256 x 64 float32 forward: 18.9 us, 20.3 with
+// 4096).  Passes that hold sums or both gradients need 80
 // to 127 registers, so that 4 workgroups a CU are resident, and leave a partial
 // row each: 1024 (2 x 128^3 x 64, bfloat16: 803 us a training pass, 838 with
 // 2048).  The forward's second pass fits 8 a CU: 2048 (read-out of 256^3 x 32:
 // 226 us, 250 with 1024).
 constexpr int64_t kNormSums = 1024, kNormApply = 2048;
 inline int64_t norm_blocks(int64_t B, int64_t S, int64_t C, int64_t total) {
-  int64_t nb = (S * C + 4095) / 4096, most = (total + B - 1) / B;
+  const int64_t least = total == kNormSums ? 8192 : 4096;
+  int64_t nb = (S * C + least - 1) / least, most = (total + B - 1) / B;
   nb = nb < most ? nb : most;
   nb = nb < S ? nb : S;
   return nb < 1 ? 1 : nb;
@@ -113,7 +116,7 @@ inline OrthShare orth_share(int64_t rows, int64_t cols, int64_t batch, bool sym,
   w.pair = 1;
   if (rows >= 128 && cols >= 128 && count(128) * batch * (ksteps >= 16 ? ksteps / 8 : 1) >= 192) w.tile = 128;
   w.tiles = count(w.tile);
-  int64_t slots = w.tile == 128 ? 512 : 1024;
+  int64_t slots = 512;  // two a CU
   // two tiles a workgroup read fewer columns and have a stage more, but leave
   // one workgroup a CU: better once the sums are long (3000 x 4000: 2.62 ms,
   // 2.83 with one; 1500 x 1500: 512 and 521 us), worse before (1024 x 1024: 315
