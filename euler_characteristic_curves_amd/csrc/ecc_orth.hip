@@ -339,31 +339,34 @@ __device__ __forceinline__ void epilogue(const Product& p, int batch, int ti, in
 
 // Loads one step (32 columns, T rows, 128 bytes a row) of an operand to LDS.
 // A wave's load covers 8 rows; the 16-byte chunk a lane fetches is permuted
-// within its row by the row's number, so that the fragment reads below, 8 rows
-// at one chunk, meet 8 different groups of banks.
+// within its row by half the row's number, so that the 16 lanes a fragment's
+// read serves at a time, 16 rows at one chunk, meet every bank once: two rows
+// fill the banks, and eight pairs of rows have eight chunks.
 // `step`: where the step's rows begin, the same for every lane, so that a load
-// has a scalar base, one register of offsets (in_step) and a constant, which
-// the hardware adds to both addresses.
+// has a scalar base, a register of offsets (in_step; its bit 6 turns in every
+// second load) and a constant, which the hardware adds to both addresses.
 template <int ROWS, int WAVES>
 __device__ __forceinline__ uint32_t in_step() {
+  static_assert(ROWS / WAVES % 16 == 0, "the permutation repeats after 16 rows");
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane >> 3;
-  return (uint32_t)(wave * (ROWS / WAVES) * 128 + r * 128 + ((lane & 7) ^ r) * 16);
+  return (uint32_t)(wave * (ROWS / WAVES) * 128 + r * 128 + ((lane & 7) ^ (r >> 1)) * 16);
 }
 template <int N>
-__device__ __forceinline__ void load_rows(const char* src, f16* dst) {
-  if constexpr (N > 1) load_rows<N - 1>(src, dst);
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+__device__ __forceinline__ void load_rows(const char* even, const char* odd, f16* dst) {
+  if constexpr (N > 1) load_rows<N - 1>(even, odd, dst);
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(N % 2 ? even : odd),
                                    (__attribute__((address_space(3))) void*)dst, 16, (N - 1) * 1024, 0);
 }
 template <int ROWS, int WAVES>
 __device__ __forceinline__ void load_step(const f16* step, uint32_t offset, f16* lds) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  load_rows<ROWS / 8 / WAVES>(reinterpret_cast<const char*>(step) + offset, lds + wave * (ROWS / WAVES) * 64);
+  const char* base = reinterpret_cast<const char*>(step);
+  load_rows<ROWS / 8 / WAVES>(base + offset, base + (offset ^ 64), lds + wave * (ROWS / WAVES) * 64);
 }
 
 template <int T>
 __device__ __forceinline__ f16x8 fragment(const f16* lds, int row, int chunk) {
-  return *reinterpret_cast<const f16x8*>(lds + row * 64 + ((chunk ^ (row & 7)) << 3));
+  return *reinterpret_cast<const f16x8*>(lds + row * 64 + ((chunk ^ (row >> 1 & 7)) << 3));
 }
 
 // The first products' fragments are read, then one more with every product.
