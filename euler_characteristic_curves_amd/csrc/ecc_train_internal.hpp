@@ -118,10 +118,12 @@ inline OrthShare orth_share(int64_t rows, int64_t cols, int64_t batch, bool sym,
   w.tiles = count(w.tile);
   int64_t slots = 512;  // two a CU
   // two tiles a workgroup read fewer columns and have a stage more, but leave
-  // one workgroup a CU: better once the sums are long (3000 x 4000: 2.62 ms,
-  // 2.83 with one; 1500 x 1500: 512 and 521 us), worse before (1024 x 1024: 315
-  // and 298; 12 x 700 x 1000: 956 and 838)
-  if (w.tile == 128 && rows % 256 == 0 && ksteps >= 44) {
+  // one workgroup a CU: better once the sums are long (2000 x 8000: 1.81 ms,
+  // 2.22 with one; 1500 x 1500: 475 and 507 us), worse before (12 x 700 x 1000:
+  // 746 and 693), and where single tiles come out in whole rounds (4096 x 4096:
+  // 4.00 and 3.90 ms)
+  const bool even = w.tiles * batch >= 512 && w.tiles * batch % 512 * 16 <= w.tiles * batch;
+  if (w.tile == 128 && rows % 256 == 0 && ksteps >= 44 && !even) {
     const int64_t tm = rows / 256;
     w.pair = 2;
     w.tiles = sym ? tm * (tm + 1) : tm * (cols / 128);
