@@ -16,7 +16,7 @@
 // matrix and step for X, per call for A and P.
 //
 // What bounds the products: the matrix unit, whose cycles the clock makes
-// dearer under load.  4096 x 4096 runs at 1.03e15 float16 operations a second
+// dearer under load.  4096 x 4096 (3.87 ms) runs at 1.06e15 float16 operations a second
 // (a library's product of that size in float16: 1.16e15), the unit busy half
 // the cycles at 1.9 GHz; short sums, the pipeline's start and the launches.
 // Matrices up to 64 across, and long ones, take other ways (orth_is_thin,
@@ -26,7 +26,7 @@
 // each its rows of 32 hi and 32 lo, 128 bytes: what a tile loads per step of
 // the long axis is one piece, as is the 32 x 32 block a wave writes, and a
 // load needs a scalar base and constants only (with rows one after the other,
-// 64-bit addresses per lane: 4096 x 4096 4.19 ms, 4.00 so).  Both
+// 64-bit addresses per lane: 4096 x 4096 4.19 ms, 4.00 then).  Both
 // operands of a product lie along the summed axis, so X is kept twice, as X
 // and as X^T.  Rows and columns are padded with zeros to the tile, and stay
 // zero, so no product checks a bound.
