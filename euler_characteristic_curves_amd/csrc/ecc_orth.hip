@@ -58,10 +58,6 @@ __device__ __forceinline__ int64_t pair_at(int64_t row, int64_t col, int64_t row
 // The matrix to be orthogonalised, element i of one matrix: the gradient, or
 // the momentum buffer after its update, or both mixed (Nesterov).
 template <class GT>
-__device__ __forceinline__ float momentum_next(const OrthArgs& p, const GT* g, const float* buf, int64_t i) {
-  return fmaf(p.momentum, buf[i], p.blend * (float)g[i]);
-}
-template <class GT>
 __device__ __forceinline__ float update_value(const OrthArgs& p, const GT* g, const float* buf, int64_t i) {
   if (!buf) return (float)g[i];
   const float b = buf[i];  // already the new buffer
@@ -78,11 +74,30 @@ __global__ __launch_bounds__(kNT) void orth_square_kernel(OrthArgs p) {
   float* buf = p.buffer ? p.buffer + off : nullptr;
   double s = 0.0;
   const int64_t stride = (int64_t)gridDim.x * kNT;
-#pragma unroll 4
-  for (int64_t i = (int64_t)blockIdx.x * kNT + threadIdx.x; i < n; i += stride) {
-    if (buf) buf[i] = momentum_next(p, g, buf, i);
-    const double v = (double)update_value(p, g, buf, i);
-    s = fma(v, v, s);
+  const auto add = [&](float gv, float& bv) {
+    float u = gv;
+    if (buf) {
+      bv = fmaf(p.momentum, bv, p.blend * gv);
+      u = p.nesterov ? fmaf(p.momentum, bv, p.blend * gv) : bv;
+    }
+    s = fma((double)u, (double)u, s);
+  };
+  const int64_t first = (int64_t)blockIdx.x * kNT + threadIdx.x;
+#pragma unroll 2
+  for (int64_t i = first; i < n / 4; i += stride) {  // four neighbours at a time
+    Vec<GT, 4> gv;
+    Vec<float, 4> bv = {};
+    load_vec(g + i * 4, gv);
+    if (buf) load_vec(buf + i * 4, bv);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) add((float)gv.v[j], bv.v[j]);
+    if (buf) store_vec(buf + i * 4, bv);
+  }
+  if (first < n % 4) {
+    const int64_t i = n / 4 * 4 + first;
+    float bv = buf ? buf[i] : 0.0f;
+    add((float)g[i], bv);
+    if (buf) buf[i] = bv;
   }
   for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
