@@ -9,11 +9,6 @@ namespace ecc {
 typedef _Float16 f16;
 typedef __bf16 bf16;
 
-template <class T>
-__device__ __forceinline__ float to_f32(T v) {
-  return (float)v;
-}
-
 // V elements from memory aligned to one element only: the target's global
 // loads and stores take any alignment, so one 16-byte access serves rows that
 // are not a multiple of 16 bytes too.
