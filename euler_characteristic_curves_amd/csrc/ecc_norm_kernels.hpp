@@ -156,17 +156,21 @@ __device__ __forceinline__ void column_sums(const NormGeom& g, const Cols<V, K>&
     }
 }
 
-// Moments about zero per channel.  A thread sums x - k and (x - k)^2 in
-// float32, k the first value it meets in that channel, so neither an offset of
-// the channel nor a few far values cost it digits; float64 from there on.
+// Moments per channel, about the channel's value in the sample's first row: a
+// value of the group itself, so that nothing cancels where the mean is many
+// deviations off (moments about zero, in float64, lost the variance of values
+// an ulp apart at 10^4).  A thread sums x - k and (x - k)^2 in float32, k the
+// first value it meets in that channel; float64 from there on.
 template <class T, int V, int K>
 __global__ __launch_bounds__(kNT) void norm_stats_kernel(NormGeom g, const T* x, double* part, int64_t row) {
   __shared__ double lds[kSumElems<V> * 2 * kNT];
   Cols<V, K> col(g);
   const T* xs = x + (int64_t)blockIdx.y * g.S * g.C;
   float piv[K][V], s1[K][V], s2[K][V];
+  Vec<T, V> about[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
+    load_vec(xs + col.c[k], about[k]);
     Vec<T, V> v = {};
     const int64_t r0 = col.template row<kUnroll<K>>(0);
     if (col.sub < col.rows && r0 < g.S) load_vec(xs + r0 * g.C + col.c[k], v);
@@ -196,7 +200,7 @@ __global__ __launch_bounds__(kNT) void norm_stats_kernel(NormGeom g, const T* x,
     n += U.value;
   });
   column_sums<V, K, 2>(g, col, lds, part + ((int64_t)blockIdx.y * g.NB + blockIdx.x) * row, [&](int k, int j, int i) {
-    const double p = (double)piv[k][j], a = (double)s1[k][j], m = (double)n;
+    const double p = (double)piv[k][j] - (double)(float)about[k].v[j], a = (double)s1[k][j], m = (double)n;
     return i == 0 ? fma(m, p, a) : (double)s2[k][j] + p * (2.0 * a + m * p);
   });
 }
@@ -219,31 +223,45 @@ __device__ __forceinline__ void add_rows(const double* q, int64_t prow, int at, 
     for (int i = 0; i < NV; ++i) s[i] += q[(int64_t)r * prow + i];
 }
 
-__device__ __forceinline__ void group_stats(double s1, double s2, double n, float eps, float* st) {
-  const double mean = s1 / n;
-  double var = s2 / n - mean * mean;
+// From a channel's sums about its own first value to sums about the group's, `by` below it, of n values more.
+__device__ __forceinline__ void shift_sums(double (&s)[2], double by, double n) {
+  s[1] += by * (2.0 * s[0] + n * by);
+  s[0] += n * by;
+}
+
+// A group's statistics: mean, 1 / sqrt(var + eps), and what float32 leaves of
+// the mean, from sums about `pivot`.
+constexpr int kStat = 3;
+__device__ __forceinline__ void group_stats(double s1, double s2, double n, double pivot, float eps, float* st) {
+  const double off = s1 / n, mean = pivot + off;
+  double var = s2 / n - off * off;
   var = var < 0.0 ? 0.0 : var;
   st[0] = (float)mean;
   st[1] = (float)(1.0 / sqrt(var + (double)eps));
+  st[2] = (float)(off + (pivot - (double)st[0]));
 }
 
 // Where a sample's partial rows are few (at most 64 KB), every
 // workgroup of the second pass joins them itself, which costs less than a
-// launch between the passes (3 to 4 us).  Returns this sample's statistics.
+// launch between the passes (3 to 4 us).  x: this sample's features.  Returns its
+// statistics.
 constexpr int kHereChannels = 512;
 struct JoinLds {
   double sum[2][kHereChannels];
-  float st[2 * kHereChannels];
+  float st[kStat * kHereChannels];
 };
-__device__ __forceinline__ const float* join_here(const NormArgs& p, const double* part, int NB, int D, int64_t prow,
-                                                  JoinLds& lds) {
+template <class T>
+__device__ __forceinline__ const float* join_here(const NormArgs& p, const T* x, const double* part, int NB, int D,
+                                                  int64_t prow, JoinLds& lds) {
   const int C = (int)p.C, G = (int)p.G, W = C < kNT ? C : kNT, parts = kNT / W;
   const int at = threadIdx.x % W, pt = threadIdx.x / W;
   const double* rows = part + (int64_t)blockIdx.y * NB * prow;
   if (pt < parts)
     for (int c = at; c < C; c += W) {
       double s[2] = {0.0, 0.0};
+      const double by = (double)(float)x[c] - (double)(float)x[(unsigned)c / (unsigned)D * D];
       add_rows<2>(rows + (int64_t)c * 2, prow, pt, parts, NB, s);
+      shift_sums(s, by, pt == 0 ? (double)p.S : 0.0);
       lds.sum[0][pt * C + c] = s[0];  // parts C <= kHereChannels: parts is 1 where C exceeds kNT
       lds.sum[1][pt * C + c] = s[1];
     }
@@ -264,11 +282,11 @@ __device__ __forceinline__ const float* join_here(const NormArgs& p, const doubl
       s1 += __shfl_xor(s1, d);
       s2 += __shfl_xor(s2, d);
     }
-    if (g < G && q == 0) group_stats(s1, s2, (double)p.S * (double)D, p.eps, lds.st + 2 * g);
+    if (g < G && q == 0) group_stats(s1, s2, (double)p.S * (double)D, (double)(float)x[g * D], p.eps, lds.st + kStat * g);
   }
   __syncthreads();
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < 2 * G; i += kNT) p.stats[(int64_t)blockIdx.y * G * 2 + i] = lds.st[i];
+    for (int i = threadIdx.x; i < kStat * G; i += kNT) p.stats[(int64_t)blockIdx.y * G * kStat + i] = lds.st[i];
   return lds.st;
 }
 
@@ -277,12 +295,13 @@ __device__ __forceinline__ const float* join_here(const NormArgs& p, const doubl
 // + (bias - mean a), half a step of mean a stays, which is 1e-4 where a group
 // is constant at 100 and the definition gives the bias exactly.  (The subtraction
 // costs 1 to 2 %: 256^3 x 32 read-out, bfloat16, 1108 us a training pass, 1087
-// without.)
+// without.)  x - mean is exact where it is small; what float32 left of the mean,
+// half a step of it at most, is in the offset.
 template <class T, int V, int K>
 struct Affine {
   float mean[K][V], a[K][V], b[K][V];
   __device__ void load(const NormArgs& p, const Cols<V, K>& col, int D) {
-    load(p, col, D, p.stats + (int64_t)blockIdx.y * p.G * 2);
+    load(p, col, D, p.stats + (int64_t)blockIdx.y * p.G * kStat);
   }
   __device__ void load(const NormArgs& p, const Cols<V, K>& col, int D, const float* st) {
 #pragma unroll
@@ -290,12 +309,12 @@ struct Affine {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int c = col.c[k] + j, gr = (unsigned)c / (unsigned)D;
-        mean[k][j] = st[2 * gr];
-        a[k][j] = st[2 * gr + 1] * load_param(p.weight, p.pdtype, c, 1.0f);
-        b[k][j] = load_param(p.bias, p.pdtype, c, 0.0f);
+        mean[k][j] = st[kStat * gr];
+        a[k][j] = st[kStat * gr + 1] * load_param(p.weight, p.pdtype, c, 1.0f);
+        b[k][j] = fmaf(-st[kStat * gr + 2], a[k][j], load_param(p.bias, p.pdtype, c, 0.0f));
       }
   }
-  // from d = x - mean
+  // from d = x - mean, the mean as float32 has it
   __device__ __forceinline__ float u(int k, int j, float d) const { return fmaf(d, a[k][j], b[k][j]); }
 };
 
@@ -305,12 +324,12 @@ __global__ __launch_bounds__(kNT) void norm_apply_kernel(NormGeom g, NormArgs p,
   __shared__ JoinLds lds;
   Cols<V, K> col(g);
   Affine<T, V, K> af;
-  if (part)
-    af.load(p, col, D, join_here(p, part, NB, D, prow, lds));
-  else
-    af.load(p, col, D);
   const int64_t base = (int64_t)blockIdx.y * g.S * g.C;
   const T* xs = reinterpret_cast<const T*>(p.x) + base;
+  if (part)
+    af.load(p, col, D, join_here(p, xs, part, NB, D, prow, lds));
+  else
+    af.load(p, col, D);
   T* ys = reinterpret_cast<T*>(p.y) + base;
   for_rows<kUnroll<K>>(col, g.S, [&](int64_t* rows, auto U) {
     Vec<T, V> v[U.value][K];
@@ -347,8 +366,9 @@ __global__ __launch_bounds__(kNT) void readout_apply_kernel(NormGeom g, NormArgs
   __shared__ JoinLds lds;
   Cols<V, K> col(g);
   Affine<T, V, K> af;
+  const T* xs = reinterpret_cast<const T*>(p.x) + (int64_t)blockIdx.y * g.S * g.C;
   if (part)
-    af.load(p, col, D, join_here(p, part, NB, D, prow, lds));
+    af.load(p, col, D, join_here(p, xs, part, NB, D, prow, lds));
   else
     af.load(p, col, D);
   float r[K][V];
@@ -357,7 +377,6 @@ __global__ __launch_bounds__(kNT) void readout_apply_kernel(NormGeom g, NormArgs
 #pragma unroll
     for (int j = 0; j < V; ++j) r[k][j] = j < col.dup[k] ? 0.0f : load_param(p.readout, p.pdtype, col.c[k] + j, 0.0f);
   const float off = load_param(p.offset, p.pdtype, 0, 0.0f);
-  const T* xs = reinterpret_cast<const T*>(p.x) + (int64_t)blockIdx.y * g.S * g.C;
   float* fs = p.field + (int64_t)blockIdx.y * g.S;
   // the lanes of a wave stay together for the shuffles: rows past the end are
   // computed from the first row and not stored
@@ -489,7 +508,7 @@ __global__ __launch_bounds__(kNT) void norm_grad_kernel(NormGeom g, NormArgs p, 
       const int c = col.c[k] + j;
       const int64_t gr = (int64_t)blockIdx.y * p.G + (unsigned)c / (unsigned)D;
       c1[k][j] = coef[2 * gr + 1];
-      c0[k][j] = -coef[2 * gr];
+      c0[k][j] = fmaf(p.stats[kStat * gr + 2], c1[k][j], -coef[2 * gr]);
       ar[k][j] = READ ? af.a[k][j] * load_param(p.readout, p.pdtype, c, 0.0f) : af.a[k][j];
     }
   const int64_t base = (int64_t)blockIdx.y * g.S * g.C;
@@ -559,16 +578,26 @@ __global__ __launch_bounds__(kJT) void norm_fold_kernel(const double* in, double
 }
 
 // Joins the partial rows of one sample and group: statistics (forward).
+template <class T>
 __global__ __launch_bounds__(kJT) void norm_join_kernel(NormArgs p, const double* part, int NB, int D, int64_t prow) {
   __shared__ double lds[kJT / 64];
   const int64_t b = blockIdx.y, gr = blockIdx.x;
   const int W = D < kJT ? D : kJT, parts = kJT / W;
   const int at = threadIdx.x % W, pt = threadIdx.x / W;
+  const T* x = reinterpret_cast<const T*>(p.x) + b * p.S * p.C + gr * D;
+  const double pivot = (double)(float)x[0];
   double s[2] = {0.0, 0.0};
   if (pt < parts)
-    for (int64_t c = at; c < D; c += W) add_rows<2>(part + b * NB * prow + (gr * D + c) * 2, prow, pt, parts, NB, s);
+    for (int64_t c = at; c < D; c += W) {
+      double t[2] = {0.0, 0.0};
+      const double by = (double)(float)x[c] - pivot;
+      add_rows<2>(part + b * NB * prow + (gr * D + c) * 2, prow, pt, parts, NB, t);
+      shift_sums(t, by, pt == 0 ? (double)p.S : 0.0);
+      s[0] += t[0];
+      s[1] += t[1];
+    }
   const double s1 = block_sum(s[0], lds), s2 = block_sum(s[1], lds);
-  if (threadIdx.x == 0) group_stats(s1, s2, (double)p.S * (double)D, p.eps, p.stats + (b * p.G + gr) * 2);
+  if (threadIdx.x == 0) group_stats(s1, s2, (double)p.S * (double)D, pivot, p.eps, p.stats + (b * p.G + gr) * kStat);
 }
 
 // Joins the partial rows of one sample and group: channel sums with A2 scaled
@@ -581,7 +610,8 @@ __global__ __launch_bounds__(kJT) void norm_join_bwd_kernel(NormArgs p, const do
   const int64_t b = blockIdx.y, gr = blockIdx.x;
   const int W = D < kJT ? D : kJT, parts = kJT / W;
   const int at = threadIdx.x % W, pt = threadIdx.x / W;
-  const double rstd = (double)p.stats[(b * p.G + gr) * 2 + 1];
+  const float* st = p.stats + (b * p.G + gr) * kStat;
+  const double rstd = (double)st[1], rest = (double)st[2];  // A2 was summed about st[0]
   double m1 = 0.0, m2 = 0.0;
   for (int64_t c0 = 0; c0 < D; c0 += W) {
     const int64_t c = gr * D + c0 + at;
@@ -605,7 +635,7 @@ __global__ __launch_bounds__(kJT) void norm_join_bwd_kernel(NormArgs p, const do
     if (threadIdx.x < W && c0 + at < D) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) s[i] = lds[i * kJT + at];
-      s[1] *= rstd;
+      s[1] = (s[1] - rest * s[0]) * rstd;
 #pragma unroll
       for (int i = 0; i < NV; ++i) chan[b * prow + c * NV + i] = s[i];
       double w = (double)load_param(p.weight, p.pdtype, c, 1.0f);
@@ -716,7 +746,7 @@ hipError_t norm_launch_fwd(const NormArgs& a, hipStream_t stream) {
       double* from = part;
       int NB = g.NB;
       norm_fold(a, from, NB, 2 * a.C, prow, 2, stream);
-      hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)a.G, (unsigned)a.B), dim3(kJT), 0, stream, a, from, NB, D, prow);
+      hipLaunchKernelGGL(norm_join_kernel<T>, dim3((unsigned)a.G, (unsigned)a.B), dim3(kJT), 0, stream, a, from, NB, D, prow);
     }
     const double* joined = here ? part : nullptr;
     NormGeom ga = g;

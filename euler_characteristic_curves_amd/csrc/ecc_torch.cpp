@@ -56,10 +56,10 @@ at::Tensor run_forward(const Plan& p, const at::Tensor& x, const at::Tensor& w, 
   const c10::DeviceGuard guard(x.device());
   const auto f32 = x.options().dtype(at::kFloat).requires_grad(false);
   at::Tensor out = p.read ? at::empty(x.sizes().slice(0, x.dim() - 1), f32) : at::empty_like(x);
-  if (keep) *keep = at::empty({p.batch, p.groups, 2}, f32);
+  if (keep) *keep = at::empty({p.batch, p.groups, 3}, f32);
   if (!p.bytes) return out;
   // statistics that nobody keeps lie behind the workspace, whose size is a multiple of 8
-  const int64_t more = keep ? 0 : p.batch * p.groups * 8;
+  const int64_t more = keep ? 0 : p.batch * p.groups * 12;
   at::Tensor ws = at::empty({p.bytes + more}, x.options().dtype(at::kByte).requires_grad(false));
   char* at_ws = static_cast<char*>(ws.data_ptr());
   float* stats = keep ? keep->data_ptr<float>() : reinterpret_cast<float*>(at_ws + p.bytes);

@@ -26,7 +26,7 @@ struct NormArgs {
   float eps;
   void* y;         // features (norm) or null
   float* field;    // grid (readout) or null
-  float* stats;    // [B][G][2]
+  float* stats;    // [B][G][3]
   const void* gy;  // gradient of y, or of the field (float32)
   void* gx;
   void *gw, *gb, *gr, *go;  // parameter gradients, each may be null

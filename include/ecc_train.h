@@ -56,13 +56,16 @@ extern "C" {
  *           channels / groups channels of one group of one sample (var with
  *           the divisor voxels * channels / groups), u = xhat * weight + bias,
  *           y = act(u)
- *   stats   device float32 [batch][groups][2]: mean and 1/sqrt(var + eps),
- *           written by the forward call and read by the backward one
+ *   stats   device float32 [batch][groups][3]: the mean, 1/sqrt(var + eps), and
+ *           what rounding to float32 left of the mean; written by the forward
+ *           call and read by the backward one
  *   pdtype  ECC_T_F32 or dtype
  * Moments are accumulated in float32 about a pivot per thread and joined in
- * float64; everything else is float32, rounded once to dtype.  x and y need
- * only the alignment of their elements.  Two kernel launches, three or four
- * where the features are many.
+ * float64 about a value of the group, and x - mean takes the mean with more
+ * digits than float32 has, so that values a few ulps apart are normalised to
+ * float32's digits too; everything else is float32, rounded once to dtype.
+ * x and y need only the alignment of their elements.  Two kernel launches,
+ * three or four where the features are many.
  */
 int ecc_norm_fwd(const void* x, int dtype, int64_t batch, int64_t voxels, int64_t channels, int64_t groups,
                  const void* weight, const void* bias, int pdtype, int act, float eps, void* y, float* stats,

@@ -40,3 +40,48 @@ def test_constant_group_gives_the_bias(dtype, readout, value):
         # C fused additions in float32, and 2^-20 of an activation's argument
         tol = C * HALF32 * (terms.abs().sum() + o.abs()) + 2.0 ** -20 * (b * r).abs().sum()
         assert ((f - (terms.sum() + o.double())).abs() <= tol).all(), act
+
+
+def near_constant(level, spread, shape=(2, 40, 37, 16), seed=2):
+    """Float32 values about `level` with a deviation of `spread`; channels of a group alike."""
+    gen = torch.Generator().manual_seed(seed)
+    return (level + spread * torch.randn(*shape, generator=gen, dtype=torch.float64)).float()
+
+
+@pytest.mark.parametrize("level,spread", [(1000.0, 1e-3), (1e4, 1e-3), (-3e5, 0.05), (7.7, 1e-5)])
+@pytest.mark.parametrize("shape", [(2, 40, 37, 16), (1, 60, 50, 520)], ids=["joined-here", "joined-apart"])
+def test_mean_that_float32_does_not_hold(level, spread, shape):
+    """A group about its mean by less than the mean's own rounding is normalised to float32's digits of x - mean, and
+    the gradients see the same mean."""
+    banner("norm near constant", level, spread, shape)
+    x = near_constant(level, spread, shape)
+    gen = torch.Generator().manual_seed(3)
+    B, C, G = shape[0], shape[-1], 4
+    w, b = 1 + 0.2 * torch.randn(C, generator=gen), 0.2 * torch.randn(C, generator=gen)
+    grad = torch.randn(*shape, generator=gen)
+    # about the level: 10^5 values of 10^4 cost even float64 the digits that are looked at
+    v = x.double().reshape(B, -1, G, C // G) - level
+    mean = v.mean(dim=(1, 3), keepdim=True)
+    var = (v - mean).square().mean(dim=(1, 3), keepdim=True)
+    rstd = 1 / torch.sqrt(var + EPS)
+    xhat = ((v - mean) * rstd).reshape(shape)
+    u = xhat * w.double() + b.double()
+    leaves = [t.cuda().requires_grad_() for t in (x, w, b)]
+    y = E.group_norm_act(leaves[0], G, leaves[1], leaves[2], eps=EPS)
+    # xhat: roundings of numbers of its size and, through the mean, of its deviation's; and half a step, twice, of what
+    # float32 leaves of the mean, which no later step can give back
+    rest = (mean - ((mean + level).float().double() - level)).abs() * rstd
+    wd, rms = w.double().abs(), torch.sqrt(var) * rstd
+    xb = (64 * HALF32 * (xhat.abs().reshape(v.shape) + rms) + 2 * HALF32 * rest).reshape(shape)
+    assert ((y.detach().double().cpu() - u).abs() / (xb * wd + 4 * HALF32 * (b.double().abs() + u.abs()))).max() <= 1
+    gx, gw, gb = torch.autograd.grad(y, leaves, grad.cuda())
+    q, dims, group = grad.double(), tuple(range(len(shape) - 1)), (1, 3)
+    gwb = q.abs() * xb + 32 * HALF32 * (q * xhat).abs()
+    assert ((gw.double().cpu() - (q * xhat).sum(dim=dims)).abs() / gwb.sum(dim=dims)).max() <= 1
+    t, tb = (q * w.double()).reshape(v.shape), (gwb * wd).reshape(v.shape).mean(dim=group, keepdim=True)
+    h, hb = xhat.reshape(v.shape), xb.reshape(v.shape)
+    m1, m2 = t.mean(dim=group, keepdim=True), (t * h).mean(dim=group, keepdim=True)
+    dx = rstd * (t - m1 - h * m2)
+    dxb = rstd * (32 * HALF32 * t.abs().mean(dim=group, keepdim=True) + h.abs() * tb + hb * m2.abs()
+                  + 64 * HALF32 * (t.abs() + m1.abs() + (h * m2).abs()))
+    assert ((gx.double().cpu().reshape(v.shape) - dx).abs() / dxb).max() <= 1
