@@ -47,6 +47,7 @@ struct NormGeom {
   int L;       // lanes per row
   int nv;      // vectors per row
   int chunks;  // column chunks of 64 vectors (rows of more than 4 x 64 vectors)
+  int runs;    // of kRun turns, of the workgroup that has most (passes that sum)
 };
 
 // A lane's columns, and its rows: the waves of a launch sweep the rows as one
@@ -79,35 +80,57 @@ struct Cols {
     wave_id = (int64_t)blockIdx.x * kNW + wave;
     waves = (int64_t)g.NB * kNW;
   }
-  // The first of U rows, `rows` apart, of turn t.
+  // The first of U rows, `rows` apart, of the first turn; past the end for lanes that have none.
   template <int U>
-  __device__ __forceinline__ int64_t row(int64_t t) const {
-    return (t * waves + wave_id) * (U * rows) + sub;
+  __device__ __forceinline__ int64_t first(int64_t S) const {
+    return sub < rows ? wave_id * (U * rows) + sub : S;
   }
 };
 
+// Rows a turn: of the passes over x and, with as many vectors in flight, of
+// those over x and its gradient.
 template <int K>
 constexpr int kUnroll = K == 1 ? 4 : (K == 2 ? 2 : 1);
+template <int K, bool READ>
+constexpr int kSumsUnroll = READ ? kUnroll<K> : (kUnroll<K> + 1) / 2;
 
-// Calls body(row...) for the rows of this lane: U at a time, and one by one at
-// the end.  body<N> gets an array of N row indexes.
+// Turns whose sums stay in float32.  A thread has as many turns as the features
+// need, and one number added up over all of them is off by half a step of its
+// sum each time, all one way where the terms are alike (1000 turns: 2e-5).  A
+// turn's rows are added to each other first, so a sum is of kRun numbers at
+// most, each of up to 4; then it goes to the workgroup's float64 sums.
+constexpr int kRun = 32;
+
+// Calls body(row...) for the rows of this lane from r on, which is left behind
+// the last: U at a time while r is below `end`, and one by one where the rows
+// end before.  body<N> gets an array of N row indexes.
 template <int U, int V, int K, class Body>
-__device__ __forceinline__ void for_rows(const Cols<V, K>& col, int64_t S, Body body) {
-  if (col.sub >= col.rows) return;
-  int64_t r = col.template row<U>(0);
-  const int64_t step = col.waves * (U * col.rows);
-  for (; r + (U - 1) * col.rows < S; r += step) {
+__device__ __forceinline__ void for_rows(const Cols<V, K>& col, int64_t S, int64_t& r, int64_t end, Body body) {
+  const int64_t step = col.waves * (U * col.rows), full = S - (U - 1) * col.rows, last = end < full ? end : full;
+  for (; r < last; r += step) {
     int64_t rows[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) rows[i] = r + i * col.rows;
     body(rows, std::integral_constant<int, U>());
   }
   if constexpr (U > 1) {
-    for (; r < S; r += col.rows) {
-      int64_t rows[1] = {r};
-      body(rows, std::integral_constant<int, 1>());
-    }
+    if (r < end)
+      for (; r < S; r += col.rows) {
+        int64_t rows[1] = {r};
+        body(rows, std::integral_constant<int, 1>());
+      }
   }
+}
+// All of this lane's rows.
+template <int U, int V, int K, class Body>
+__device__ __forceinline__ void for_rows(const Cols<V, K>& col, int64_t S, Body body) {
+  int64_t r = col.template first<U>(S);
+  for_rows<U>(col, S, r, S, body);
+}
+// The next run of them.
+template <int U, int V, int K, class Body>
+__device__ __forceinline__ void for_run(const Cols<V, K>& col, int64_t S, int64_t& r, Body body) {
+  for_rows<U>(col, S, r, r + kRun * (col.waves * (U * col.rows)), body);
 }
 
 // Elements of a vector whose sums are joined at a time: few, so that the
@@ -116,12 +139,12 @@ template <int V>
 constexpr int kSumElems = V < 2 ? V : 2;
 
 // Sums over the workgroup's rows of NV values per channel, in a fixed order
-// and in float64, written to out[channel * NV + i].  lds: kSumElems<V> NV kNT
-// doubles.  P threads share one output and join by shuffles, P the largest
+// and in float64, written to out[channel * NV + i], or added to it.  lds:
+// kSumElems<V> NV kNT doubles.  P threads share one output and join by shuffles, P the largest
 // power of two with P L kSumElems NV <= kNT (and at most 64).
 template <int V, int K, int NV, class Value>
 __device__ __forceinline__ void column_sums(const NormGeom& g, const Cols<V, K>& col, double* lds, double* out,
-                                            Value value) {
+                                            bool more, Value value) {
   constexpr int E = kSumElems<V>;
   const int rows = 64 / g.L, L = g.L;
   const int nout = L * E * NV;
@@ -150,7 +173,8 @@ __device__ __forceinline__ void column_sums(const NormGeom& g, const Cols<V, K>&
         if (o < nout && p == 0 && v < g.nv) {
           const int at = v * V, last = (int)g.C - V, c = at < last ? at : last;
           const int j = j0 + ji / NV;
-          if (j >= at - c) out[(int64_t)(c + j) * NV + ji % NV] = s;
+          double* to = out + (int64_t)(c + j) * NV + ji % NV;
+          if (j >= at - c) *to = more ? *to + s : s;
         }
       }
     }
@@ -160,49 +184,58 @@ __device__ __forceinline__ void column_sums(const NormGeom& g, const Cols<V, K>&
 // value of the group itself, so that nothing cancels where the mean is many
 // deviations off (moments about zero, in float64, lost the variance of values
 // an ulp apart at 10^4).  A thread sums x - k and (x - k)^2 in float32, k the
-// first value it meets in that channel; float64 from there on.
+// first value it meets of a run in that channel; float64 from there on.
 template <class T, int V, int K>
 __global__ __launch_bounds__(kNT) void norm_stats_kernel(NormGeom g, const T* x, double* part, int64_t row) {
   __shared__ double lds[kSumElems<V> * 2 * kNT];
   Cols<V, K> col(g);
   const T* xs = x + (int64_t)blockIdx.y * g.S * g.C;
-  float piv[K][V], s1[K][V], s2[K][V];
+  constexpr int U = kUnroll<K>;
   Vec<T, V> about[K];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    load_vec(xs + col.c[k], about[k]);
-    Vec<T, V> v = {};
-    const int64_t r0 = col.template row<kUnroll<K>>(0);
-    if (col.sub < col.rows && r0 < g.S) load_vec(xs + r0 * g.C + col.c[k], v);
+  for (int k = 0; k < K; ++k) load_vec(xs + col.c[k], about[k]);
+  int64_t r = col.template first<U>(g.S);
+  for (int run = 0; run < g.runs; ++run) {
+    float piv[K][V], s1[K][V], s2[K][V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      piv[k][j] = (float)v.v[j];
-      s1[k][j] = s2[k][j] = 0.0f;
+    for (int k = 0; k < K; ++k) {
+      Vec<T, V> v = {};
+      if (r < g.S) load_vec(xs + r * g.C + col.c[k], v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        piv[k][j] = (float)v.v[j];
+        s1[k][j] = s2[k][j] = 0.0f;
+      }
     }
-  }
-  int64_t n = 0;
-  for_rows<kUnroll<K>>(col, g.S, [&](const int64_t* rows, auto U) {
-    Vec<T, V> v[U.value][K];
+    int n = 0;
+    for_run<U>(col, g.S, r, [&](const int64_t* rows, auto N) {
+      Vec<T, V> v[N.value][K];
 #pragma unroll
-    for (int i = 0; i < U.value; ++i)
+      for (int i = 0; i < N.value; ++i)
 #pragma unroll
-      for (int k = 0; k < K; ++k) load_vec(xs + rows[i] * g.C + col.c[k], v[i][k]);
-#pragma unroll
-    for (int i = 0; i < U.value; ++i)
+        for (int k = 0; k < K; ++k) load_vec(xs + rows[i] * g.C + col.c[k], v[i][k]);
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float d = (float)v[i][k].v[j] - piv[k][j];
-          s1[k][j] += d;
-          s2[k][j] = fmaf(d, d, s2[k][j]);
+          float t1 = 0.0f, t2 = 0.0f;
+#pragma unroll
+          for (int i = 0; i < N.value; ++i) {
+            const float d = (float)v[i][k].v[j] - piv[k][j];
+            t1 = i ? t1 + d : d;
+            t2 = i ? fmaf(d, d, t2) : d * d;
+          }
+          s1[k][j] += t1;
+          s2[k][j] += t2;
         }
-    n += U.value;
-  });
-  column_sums<V, K, 2>(g, col, lds, part + ((int64_t)blockIdx.y * g.NB + blockIdx.x) * row, [&](int k, int j, int i) {
-    const double p = (double)piv[k][j] - (double)(float)about[k].v[j], a = (double)s1[k][j], m = (double)n;
-    return i == 0 ? fma(m, p, a) : (double)s2[k][j] + p * (2.0 * a + m * p);
-  });
+      n += N.value;
+    });
+    column_sums<V, K, 2>(g, col, lds, part + ((int64_t)blockIdx.y * g.NB + blockIdx.x) * row, run > 0,
+                         [&](int k, int j, int i) {
+      const double p = (double)piv[k][j] - (double)(float)about[k].v[j], a = (double)s1[k][j], m = (double)n;
+      return i == 0 ? fma(m, p, a) : (double)s2[k][j] + p * (2.0 * a + m * p);
+    });
+  }
 }
 
 // Sums NV values of column q of the partial rows at, at + step, ..., below n.
@@ -419,51 +452,64 @@ __global__ __launch_bounds__(kNT) void norm_sums_kernel(NormGeom g, NormArgs p, 
   const T* xs = reinterpret_cast<const T*>(p.x) + base;
   const T* gs = READ ? nullptr : reinterpret_cast<const T*>(p.gy) + base;
   const float* fs = READ ? reinterpret_cast<const float*>(p.gy) + (int64_t)blockIdx.y * g.S : nullptr;
-  float s[K][V][NV];
+  double* out = part + ((int64_t)blockIdx.y * g.NB + blockIdx.x) * prow;
+  double total = 0.0;  // of df
+  constexpr int U = kSumsUnroll<K, READ>;
+  int64_t r = col.template first<U>(g.S);
+  for (int run = 0; run < g.runs; ++run) {
+    float s[K][V][NV];
 #pragma unroll
-  for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int j = 0; j < V; ++j)
+      for (int j = 0; j < V; ++j)
 #pragma unroll
-      for (int i = 0; i < NV; ++i) s[k][j][i] = 0.0f;
-  float sdf = 0.0f;
-  constexpr int U = READ ? kUnroll<K> : (kUnroll<K> + 1) / 2;
-  for_rows<U>(col, g.S, [&](const int64_t* rows, auto N) {
-    Vec<T, V> v[N.value][K], q[N.value][K];
-    float df[N.value];
+        for (int i = 0; i < NV; ++i) s[k][j][i] = 0.0f;
+    float sdf = 0.0f;
+    for_run<U>(col, g.S, r, [&](const int64_t* rows, auto N) {
+      Vec<T, V> v[N.value][K], q[N.value][K];
+      float df[N.value];
 #pragma unroll
-    for (int i = 0; i < N.value; ++i) {
-      if constexpr (READ) df[i] = fs[rows[i]];
+      for (int i = 0; i < N.value; ++i) {
+        if constexpr (READ) df[i] = fs[rows[i]];
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        load_vec(xs + rows[i] * g.C + col.c[k], v[i][k]);
-        if constexpr (!READ) load_vec(gs + rows[i] * g.C + col.c[k], q[i][k]);
+        for (int k = 0; k < K; ++k) {
+          load_vec(xs + rows[i] * g.C + col.c[k], v[i][k]);
+          if constexpr (!READ) load_vec(gs + rows[i] * g.C + col.c[k], q[i][k]);
+        }
       }
-    }
+      if constexpr (READ) {
+        float t = df[0];
 #pragma unroll
-    for (int i = 0; i < N.value; ++i) {
-      if constexpr (READ) sdf += df[i];
+        for (int i = 1; i < N.value; ++i) t += df[i];
+        sdf += t;
+      }
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float d = (float)v[i][k].v[j] - af.mean[k][j];
-          float y;
-          const float sl = act_slope<ACT>(af.u(k, j, d), y);
-          float dy;
-          if constexpr (READ) dy = df[i]; else dy = (float)q[i][k].v[j];
-          const float du = dy * sl;
-          s[k][j][0] += du;
-          s[k][j][1] = fmaf(du, d, s[k][j][1]);
-          if constexpr (READ) s[k][j][2] = fmaf(dy, y, s[k][j][2]);
+          float t[3] = {};
+#pragma unroll
+          for (int i = 0; i < N.value; ++i) {
+            const float d = (float)v[i][k].v[j] - af.mean[k][j];
+            float y;
+            const float sl = act_slope<ACT>(af.u(k, j, d), y);
+            float dy;
+            if constexpr (READ) dy = df[i]; else dy = (float)q[i][k].v[j];
+            const float du = dy * sl;
+            t[0] = i ? t[0] + du : du;
+            t[1] = i ? fmaf(du, d, t[1]) : du * d;
+            if constexpr (READ) t[2] = i ? fmaf(dy, y, t[2]) : dy * y;
+          }
+#pragma unroll
+          for (int i = 0; i < NV; ++i) s[k][j][i] += t[i];
         }
-    }
-  });
-  double* out = part + ((int64_t)blockIdx.y * g.NB + blockIdx.x) * prow;
-  column_sums<V, K, NV>(g, col, lds, out, [&](int k, int j, int i) { return (double)s[k][j][i]; });
+    });
+    column_sums<V, K, NV>(g, col, lds, out, run > 0, [&](int k, int j, int i) { return (double)s[k][j][i]; });
+    total += (double)sdf;
+  }
   if constexpr (READ) {
     __syncthreads();
-    lds[threadIdx.x] = col.l == 0 ? (double)sdf : 0.0;
+    lds[threadIdx.x] = col.l == 0 ? total : 0.0;
     __syncthreads();
     if (threadIdx.x < 64) {
       double t = 0.0;
@@ -516,8 +562,7 @@ __global__ __launch_bounds__(kNT) void norm_grad_kernel(NormGeom g, NormArgs p, 
   const T* gs = READ ? nullptr : reinterpret_cast<const T*>(p.gy) + base;
   const float* fs = READ ? reinterpret_cast<const float*>(p.gy) + (int64_t)blockIdx.y * g.S : nullptr;
   T* os = reinterpret_cast<T*>(p.gx) + base;
-  constexpr int U = READ ? kUnroll<K> : (kUnroll<K> + 1) / 2;
-  for_rows<U>(col, g.S, [&](int64_t* rows, auto N) {
+  for_rows<kSumsUnroll<K, READ>>(col, g.S, [&](int64_t* rows, auto N) {
     Vec<T, V> v[N.value][K], q[N.value][K];
     float df[N.value];
 #pragma unroll
@@ -691,6 +736,12 @@ NormGeom norm_geom(const NormArgs& a, int& V, int& K) {
   return g;
 }
 
+// Runs of the workgroup with most turns, the first, for turns of U rows a lane.
+int norm_runs(const NormGeom& g, int U) {
+  const int64_t span = (int64_t)g.NB * kNW * U * (64 / g.L), turns = (g.S + span - 1) / span;
+  return (int)((turns + kRun - 1) / kRun);
+}
+
 template <class F>
 hipError_t with_act(int act, F f) {
   switch (act) {
@@ -731,13 +782,14 @@ inline void norm_fold(const NormArgs& a, double*& part, int& NB, int64_t cols, i
 template <class T>
 hipError_t norm_launch_fwd(const NormArgs& a, hipStream_t stream) {
   int V, K;
-  const NormGeom g = norm_geom<T>(a, V, K);
+  NormGeom g = norm_geom<T>(a, V, K);
   const int D = (int)(a.C / a.G);
   const int64_t prow = (int64_t)norm_row(a.C);
   double* part = reinterpret_cast<double*>(a.ws);
   const dim3 grid((unsigned)g.NB, (unsigned)a.B, (unsigned)g.chunks), block(kNT);
   return with_cols<T>(V, K, [&](auto v, auto k) {
     constexpr int VV = v.value, KK = k.value;
+    g.runs = norm_runs(g, kUnroll<KK>);
     hipLaunchKernelGGL((norm_stats_kernel<T, VV, KK>), grid, block, 0, stream, g, reinterpret_cast<const T*>(a.x), part,
                        prow);
     // 64 KB of partial rows a workgroup, read from L2, at most
@@ -765,7 +817,7 @@ hipError_t norm_launch_fwd(const NormArgs& a, hipStream_t stream) {
 template <class T>
 hipError_t norm_launch_bwd(const NormArgs& a, hipStream_t stream) {
   int V, K;
-  const NormGeom g = norm_geom<T>(a, V, K);
+  NormGeom g = norm_geom<T>(a, V, K);
   const int D = (int)(a.C / a.G);
   const int64_t prow = (int64_t)norm_row(a.C);
   double* part = reinterpret_cast<double*>(a.ws);
@@ -775,6 +827,7 @@ hipError_t norm_launch_bwd(const NormArgs& a, hipStream_t stream) {
   const dim3 last((unsigned)g.NB, a.gx ? (unsigned)a.B + 1 : 1u, a.gx ? (unsigned)g.chunks : 1u);
   return with_cols<T>(V, K, [&](auto v, auto k) {
     constexpr int VV = v.value, KK = k.value;
+    g.runs = a.readout ? norm_runs(g, kSumsUnroll<KK, true>) : norm_runs(g, kSumsUnroll<KK, false>);
     return with_act(a.act, [&](auto act) {
       constexpr int A = act.value;
       double* from = part;

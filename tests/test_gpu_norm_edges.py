@@ -85,3 +85,33 @@ def test_mean_that_float32_does_not_hold(level, spread, shape):
     dxb = rstd * (32 * HALF32 * t.abs().mean(dim=group, keepdim=True) + h.abs() * tb + hb * m2.abs()
                   + 64 * HALF32 * (t.abs() + m1.abs() + (h * m2).abs()))
     assert ((gx.double().cpu().reshape(v.shape) - dx).abs() / dxb).max() <= 1
+
+
+def test_sums_over_many_rows():
+    """A thousand rows a thread: sums of float32 leave it for float64 on the way, so that neither a constant gradient,
+    whose roundings all go one way, nor an empty border slice, which the first rows of every thread lie in, costs digits."""
+    banner("norm long sums")
+    n, border = 1 << 28, 1 << 20
+    x = torch.randn(1, n, 1, device="cuda", generator=torch.Generator("cuda").manual_seed(4)).add_(1000.0)
+    x[:, :border] = 0.0
+    # float64 moments, chunk by chunk
+    s = torch.zeros(2, dtype=torch.float64)
+    for c in x.view(16, -1):
+        d = c.double() - 1000.0
+        s += torch.stack([d.sum(), (d * d).sum()]).cpu()
+    mean = float(s[0]) / n
+    var = float(s[1]) / n - mean ** 2
+    b, r, o = (torch.full((1,), v, device="cuda", requires_grad=True) for v in (0.0, 1.0, 0.0))
+    f = E.group_norm_readout(x, 1, None, b, r, o)
+    # a thread's first run, an eighth of its rows at most, lies 1000 off its pivot: 40 roundings of that much
+    share = 128 * 2 ** 18 / n
+    tol = 40 * HALF32 * (1 + share * 1e6 / var)
+    at = torch.arange(border, n, 99991, device="cuda")
+    want = (x[0, at, 0].double() - 1000.0 - mean) / (var + EPS) ** 0.5
+    got = f.detach()[0, at].double()
+    assert ((got - want).abs() <= tol * (want.abs() + 1e-2) + 64 * HALF32 * want.abs()).all()
+    step = 0.1
+    grads = torch.autograd.grad(f, [b, r, o], torch.full((), step, device="cuda").expand(f.shape))
+    total = float(torch.tensor(step).double()) * n
+    for name, g in (("bias", grads[0]), ("offset", grads[2])):
+        assert abs(float(g.double()) - total) <= 40 * HALF32 * total, name
