@@ -71,13 +71,18 @@ __device__ __forceinline__ float logistic(float u) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269502f * u));
 }
 
+// Infinite arguments, which finite features and parameters can reach, have the
+// values and slopes that the activations tend to: a factor of the tail or of
+// the logistic function, which are 0 there, is kept finite.
+constexpr float kHuge = 3.40282347e38f;
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float u) {
   if constexpr (ACT == kActRelu) return u <= 0.0f ? 0.0f : u;
-  if constexpr (ACT == kActSilu) return u * logistic(u);
+  if constexpr (ACT == kActSilu) return fmaxf(u, -kHuge) * logistic(u);
   if constexpr (ACT == kActGelu) {
     float e;
-    return fmaf(-fabsf(u), normal_tail(u, e), fmaxf(u, 0.0f));
+    return fmaf(-fminf(fabsf(u), kHuge), normal_tail(u, e), fmaxf(u, 0.0f));
   }
   return u;
 }
@@ -91,13 +96,13 @@ __device__ __forceinline__ float act_slope(float u, float& y) {
   }
   if constexpr (ACT == kActSilu) {
     const float s = logistic(u);
-    y = u * s;
+    y = __builtin_amdgcn_fmed3f(u, -kHuge, kHuge) * s;
     return fmaf(y, 1.0f - s, s);
   }
   if constexpr (ACT == kActGelu) {
     // both from the tail q: y = max(u, 0) - |u| q, y' = q - |u| e / sqrt(2 pi), from 1 where u > 0
     float e;
-    const float q = normal_tail(u, e), z = fabsf(u);
+    const float q = normal_tail(u, e), z = fminf(fabsf(u), kHuge);
     y = fmaf(-z, q, fmaxf(u, 0.0f));
     const float w = fmaf(-0.398942280f * z, e, q);
     return u > 0.0f ? 1.0f - w : w;

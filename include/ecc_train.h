@@ -40,6 +40,7 @@ extern "C" {
 #define ECC_ACT_RELU 1
 #define ECC_ACT_SILU 2 /* u / (1 + exp(-u))                                   */
 #define ECC_ACT_GELU 3 /* u Phi(u), Phi the normal distribution function      */
+/* (at an infinite u, their limits: infinity or 0, with slope 1 or 0)         */
 
 #define ECC_MAX_CHANNELS 8192          /* of the norm                         */
 #define ECC_MAX_READOUT_CHANNELS 1024  /* of the norm read out to a grid      */

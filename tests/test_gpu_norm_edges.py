@@ -115,3 +115,25 @@ def test_sums_over_many_rows():
     total = float(torch.tensor(step).double()) * n
     for name, g in (("bias", grads[0]), ("offset", grads[2])):
         assert abs(float(g.double()) - total) <= 40 * HALF32 * total, name
+
+
+@pytest.mark.parametrize("readout", [False, True], ids=["norm", "readout"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_arguments_beyond_float32(act, readout):
+    """weight * xhat overflows to an infinity: its activation is infinity or 0 and its slope 1 or 0, as for the value
+    that float32 does not hold."""
+    banner("norm overflow", act, readout)
+    x = torch.zeros(1, 2, 25, 1)
+    x[0, 0, 0], x[0, 0, 1] = 5.0, -5.0        # xhat: 5 and -5, the rest 0
+    up, down = torch.tensor([3e38]), torch.tensor([1.0])
+    leaves = [t.cuda().requires_grad_() for t in (x, up, torch.zeros(1))]
+    grad = torch.zeros(1, 2, 25) if readout else torch.zeros(x.shape)
+    grad[0, 0, 0], grad[0, 0, 1] = 1.0, 2.0
+    if readout:
+        out = E.group_norm_readout(*leaves[:1], 1, leaves[1], leaves[2], down.cuda(), act=act)
+    else:
+        out = E.group_norm_act(leaves[0], 1, leaves[1], leaves[2], act=act)
+    flat = out.detach().reshape(50).cpu()
+    assert flat[0] == float("inf") and flat[1] == 0.0 and torch.equal(flat[2:], torch.zeros(48))
+    (gb,) = torch.autograd.grad(out, [leaves[2]], grad.cuda())
+    assert float(gb) == 1.0
