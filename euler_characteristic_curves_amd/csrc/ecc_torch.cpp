@@ -136,6 +136,10 @@ at::Tensor norm(const at::Tensor& x, const Optional& w, const Optional& b, const
                 const std::vector<int64_t>& sizes, int64_t dtype, int64_t pdtype, int64_t act, int64_t bytes, double eps,
                 bool read) {
   const pybind11::gil_scoped_release nogil;
+  // a dual tensor need not require a gradient, and autograd modes do not turn it off
+  const auto dual = [](const Optional& t) { return t && t->_fw_grad(/*level=*/0).defined(); };
+  TORCH_CHECK_NOT_IMPLEMENTED(!dual(x) && !dual(w) && !dual(b) && !dual(r) && !dual(o),
+                              "group norm has no forward-mode derivative");
   const Plan p{sizes[0], sizes[1], sizes[2], sizes[3], dtype, pdtype, act, bytes, eps, read};
   const auto wants = [](const Optional& t) { return t && t->requires_grad(); };
   if (at::GradMode::is_enabled() && (x.requires_grad() || wants(w) || wants(b) || wants(r) || wants(o)))

@@ -96,7 +96,8 @@ def group_norm_act(x, groups, weight=None, bias=None, act="none", eps=1e-5):
     """act(group_norm(x) * weight + bias) over channels-last features, differentiable in x, weight and bias.
 
     x: float32, float16 or bfloat16 [batch, *space, channels]; weight and bias: [channels], float32 or x's dtype, or
-    None (1 and 0); act: "none", "relu", "silu" or "gelu".  Returns a tensor like x (see include/ecc_train.h).
+    None (1 and 0); act: "none", "relu", "silu" or "gelu".  Returns a tensor like x (see include/ecc_train.h).  Forward-mode
+    derivatives are refused.
     """
     return _norm(x, groups, weight, bias, None, None, act, eps, False)
 
