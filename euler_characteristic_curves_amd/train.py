@@ -141,14 +141,15 @@ def orthogonalize(g, steps=5, eps=1e-7, coefficients=_COEFFICIENTS, out=None):
     """The Newton-Schulz iterate of a matrix, or of each matrix of a stack (see ecc_orthogonalize in
     include/ecc_train.h): g with its singular values driven towards 1.  Not differentiable.
 
-    g: float32, float16 or bfloat16, [rows, cols] or [batch, rows, cols]; out: a tensor like g (g itself allowed).
+    g: float32, float16 or bfloat16, [rows, cols] or [batch, rows, cols]; out: a tensor like g (g itself allowed), written
+    in place.
     """
-    g = g.detach()
-    if out is None:
+    g, given = g.detach(), out is not None
+    if not given:
         g = g.contiguous()
     _dev_tensor(g, "g")
     dtype, sizes = _matrix_dtype(g, "g"), _matrix_sizes(g, "g")
-    if out is None:
+    if not given:
         out = torch.empty_like(g)
     _dev_tensor(out, "out", g.dtype, g.device)
     if out.shape != g.shape:
@@ -158,6 +159,8 @@ def orthogonalize(g, steps=5, eps=1e-7, coefficients=_COEFFICIENTS, out=None):
         return out
     with _on_device(g):
         nbytes = _orth_bytes(sizes)
+        if given:  # a backward pass that saved it is to notice
+            torch.autograd.graph.increment_version(out)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=g.device)
         check(lib.ecc_orthogonalize(_ptr(g), dtype, *sizes, int(steps), float(eps), a, b, c, _ptr(out), _ptr(ws), nbytes,
                                     _stream(g).cuda_stream), "ecc_orthogonalize")

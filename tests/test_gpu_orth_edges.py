@@ -1,0 +1,34 @@
+"""Orthogonalisation and the momentum step at the edges of their arguments:
+what autograd sees of tensors written in place, tensors that share memory,
+step counts, graded matrices, and shapes for every way a product is shared
+out."""
+
+import pytest
+import torch
+
+import euler_characteristic_curves_amd as E
+from tests.gpu_util import banner, need_gpu
+from tests.test_gpu_orth import gradient
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def test_out_is_seen_by_autograd():
+    """A tensor that was saved for a backward pass and is then written through `out` is noticed there."""
+    banner("orth version")
+    for shape in ((20, 30), (100, 120)):
+        g = gradient(shape, seed=1).cuda()
+        kept, w = torch.randn(shape, device="cuda"), torch.ones(shape, device="cuda", requires_grad=True)
+        loss = (w * kept).sum()
+        E.orthogonalize(g, out=kept)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+        loss = (w * g).sum()
+        E.orthogonalize(g, out=g)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
