@@ -125,6 +125,12 @@ def _matrix_dtype(t, name):
     return _DTYPES[t.dtype]
 
 
+def _overlap(a, b):
+    """Whether two contiguous tensors share memory."""
+    x, y = a.data_ptr(), b.data_ptr()
+    return x < y + b.numel() * b.element_size() and y < x + a.numel() * a.element_size()
+
+
 def _orth_bytes(sizes):
     nbytes = lib.ecc_orth_workspace_bytes(*sizes)
     if not nbytes:
@@ -141,8 +147,8 @@ def orthogonalize(g, steps=5, eps=1e-7, coefficients=_COEFFICIENTS, out=None):
     """The Newton-Schulz iterate of a matrix, or of each matrix of a stack (see ecc_orthogonalize in
     include/ecc_train.h): g with its singular values driven towards 1.  Not differentiable.
 
-    g: float32, float16 or bfloat16, [rows, cols] or [batch, rows, cols]; out: a tensor like g (g itself allowed), written
-    in place.
+    g: float32, float16 or bfloat16, [rows, cols] or [batch, rows, cols]; out: a tensor like g, written in place; it is
+    g itself or has no memory in common with it.
     """
     g, given = g.detach(), out is not None
     if not given:
@@ -154,6 +160,8 @@ def orthogonalize(g, steps=5, eps=1e-7, coefficients=_COEFFICIENTS, out=None):
     _dev_tensor(out, "out", g.dtype, g.device)
     if out.shape != g.shape:
         raise ValueError("out must have g's shape")
+    if out.data_ptr() != g.data_ptr() and _overlap(out, g):
+        raise ValueError("out shares a part of g's memory: workgroups would write what others have yet to read")
     a, b, c = _polynomial(coefficients)
     if not g.numel():
         return out
@@ -173,7 +181,7 @@ def muon_step(params, grads, buffers, lr, momentum=0.95, nesterov=True, weight_d
     include/ecc_train.h).
 
     params, grads, buffers: sequences of one length; entry i of each is [rows, cols] or a stack [batch, rows, cols] of
-    matrices (layers of one shape), contiguous; buffers are float32.  scale: factor of the update, by default
+    matrices (layers of one shape), contiguous, without memory in common; buffers are float32.  scale: factor of the update, by default
     sqrt(max(1, rows / cols)).  Every argument is checked before anything is changed.
     """
     params, grads, buffers = list(params), list(grads), list(buffers)
@@ -188,6 +196,9 @@ def muon_step(params, grads, buffers, lr, momentum=0.95, nesterov=True, weight_d
         sizes = _matrix_sizes(p, "param")
         if g.shape != p.shape or m.shape != p.shape:
             raise ValueError(f"param {list(p.shape)}, grad {list(g.shape)} and buffer {list(m.shape)} must agree")
+        for t, other, names in ((p, g, "param and grad"), (p, m, "param and buffer"), (g, m, "grad and buffer")):
+            if _overlap(t, other):
+                raise ValueError(f"{names} share memory")
         calls.append((p, _matrix_dtype(p, "param"), g, _matrix_dtype(g, "grad"), m, sizes,
                       _orth_bytes(sizes) if p.numel() else 0))
     for p, pdtype, g, gdtype, m, sizes, nbytes in calls:

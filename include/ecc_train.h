@@ -117,7 +117,7 @@ size_t ecc_norm_workspace_bytes(int64_t batch, int64_t voxels, int64_t channels,
  * (dtype), each on its own: X = g / (|g|_F + eps), then `steps` times
  *   A = X X^T,  X <- a X + (b A + c A A) X
  * (with X^T in place of X where rows > cols), written to out (dtype, g's
- * shape; may be g itself).  The singular vectors stay, the singular values are
+ * shape; g itself, or memory that does not overlap it).  The singular vectors stay, the singular values are
  * driven towards 1 by the polynomial a s + b s^3 + c s^5.
  * The norm is summed in float64.  Products take operands of 22 significant bits
  * (pairs of float16) and sum in float32; where the short side is at most 64, or
@@ -137,7 +137,8 @@ int ecc_orthogonalize(const void* g, int dtype, int64_t batch, int64_t rows, int
  *   buffer <- momentum buffer + (1 - momentum) grad               (float32)
  *   u = nesterov ? momentum buffer + (1 - momentum) grad : buffer
  *   param <- (1 - lr weight_decay) param - lr scale orthogonalize(u)
- * param: pdtype, grad: gdtype, buffer: float32, all [batch][rows][cols].
+ * param: pdtype, grad: gdtype, buffer: float32, all [batch][rows][cols]; none
+ * overlaps another.
  * Refused with ECC_E_VALUE besides the above: lr, momentum, weight_decay or
  * scale not finite.
  */

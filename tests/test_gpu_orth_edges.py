@@ -32,3 +32,24 @@ def test_out_is_seen_by_autograd():
         E.orthogonalize(g, out=g)
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             loss.backward()
+
+
+def test_shared_memory_is_refused():
+    """Before anything is launched, and only where memory is shared in part."""
+    banner("orth overlap")
+    flat = torch.randn(30 * 40 + 40, device="cuda")
+    g, later = flat[:1200].view(30, 40), flat[40:].view(30, 40)
+    before = flat.clone()
+    for a, b in ((g, later), (later, g)):
+        with pytest.raises(ValueError, match="memory"):
+            E.orthogonalize(a, out=b)
+    p, m = torch.randn(30, 40, device="cuda"), torch.zeros(30, 40, device="cuda")
+    for args in ((g, later, m), (p, g, later), (g, p, later), (p, g, g), (p, p, m)):
+        with pytest.raises(ValueError, match="share memory"):
+            E.muon_step(*([t] for t in args), lr=0.1)
+    torch.cuda.synchronize()
+    assert torch.equal(flat, before) and not m.any()
+    want = E.orthogonalize(g.clone())
+    one, two = torch.stack([g, g]).unbind()       # neighbours in memory
+    assert torch.equal(E.orthogonalize(one, out=two), want)
+    assert torch.equal(E.orthogonalize(g, out=g), want)

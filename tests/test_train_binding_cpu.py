@@ -21,3 +21,14 @@ def test_forward_mode_is_refused(dual, grad):
         for enabled in (True, False):
             with torch.set_grad_enabled(enabled), pytest.raises(NotImplementedError, match="forward-mode"):
                 _torch.norm(*args, *plan)
+
+
+def test_overlap():
+    """Byte ranges that meet, over types and views that start inside each other."""
+    from euler_characteristic_curves_amd.train import _overlap
+    t = torch.zeros(100)
+    half = torch.zeros(100, dtype=torch.float16)
+    for a, b, want in ((t, t, True), (t[:50], t[50:], False), (t[:51], t[50:], True), (t[50:], t[:51], True),
+                       (t[10:20], t, True), (t, t[99:], True), (t, half, False), (t[:0], t, False),
+                       (half[:10], half.view(torch.float32)[4:], True), (half[:10], half.view(torch.float32)[5:], False)):
+        assert _overlap(a, b) is want
