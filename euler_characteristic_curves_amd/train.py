@@ -143,6 +143,14 @@ def _polynomial(coefficients):
     return float(a), float(b), float(c)
 
 
+def _whole(steps):
+    """steps as an int that fits the C argument; one that does not stays out of range there."""
+    n = int(steps)
+    if isinstance(steps, bool) or n != steps:
+        raise TypeError(f"steps must be a whole number (got {steps!r})")
+    return max(-1, min(n, 2 ** 31 - 1))
+
+
 def orthogonalize(g, steps=5, eps=1e-7, coefficients=_COEFFICIENTS, out=None):
     """The Newton-Schulz iterate of a matrix, or of each matrix of a stack (see ecc_orthogonalize in
     include/ecc_train.h): g with its singular values driven towards 1.  Not differentiable.
@@ -163,6 +171,7 @@ def orthogonalize(g, steps=5, eps=1e-7, coefficients=_COEFFICIENTS, out=None):
     if out.data_ptr() != g.data_ptr() and _overlap(out, g):
         raise ValueError("out shares a part of g's memory: workgroups would write what others have yet to read")
     a, b, c = _polynomial(coefficients)
+    steps = _whole(steps)
     if not g.numel():
         return out
     with _on_device(g):
@@ -170,7 +179,7 @@ def orthogonalize(g, steps=5, eps=1e-7, coefficients=_COEFFICIENTS, out=None):
         if given:  # a backward pass that saved it is to notice
             torch.autograd.graph.increment_version(out)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=g.device)
-        check(lib.ecc_orthogonalize(_ptr(g), dtype, *sizes, int(steps), float(eps), a, b, c, _ptr(out), _ptr(ws), nbytes,
+        check(lib.ecc_orthogonalize(_ptr(g), dtype, *sizes, steps, float(eps), a, b, c, _ptr(out), _ptr(ws), nbytes,
                                     _stream(g).cuda_stream), "ecc_orthogonalize")
     return out
 
@@ -188,6 +197,7 @@ def muon_step(params, grads, buffers, lr, momentum=0.95, nesterov=True, weight_d
     if not len(params) == len(grads) == len(buffers):
         raise ValueError(f"{len(params)} params, {len(grads)} grads, {len(buffers)} buffers")
     a, b, c = _polynomial(coefficients)
+    steps = _whole(steps)
     calls = []
     for p, g, m in zip(params, grads, buffers):
         _dev_tensor(p, "param")
@@ -208,7 +218,7 @@ def muon_step(params, grads, buffers, lr, momentum=0.95, nesterov=True, weight_d
         with _on_device(p):
             ws = torch.empty(nbytes, dtype=torch.uint8, device=p.device)
             check(lib.ecc_muon_step(_ptr(p), pdtype, _ptr(g), gdtype, _ptr(m), *sizes, float(lr), float(momentum),
-                                    1 if nesterov else 0, float(weight_decay), s, int(steps), float(eps), a, b, c,
+                                    1 if nesterov else 0, float(weight_decay), s, steps, float(eps), a, b, c,
                                     _ptr(ws), nbytes, _stream(p).cuda_stream), "ecc_muon_step")
         torch.autograd.graph.increment_version(p)
         torch.autograd.graph.increment_version(m)

@@ -53,3 +53,18 @@ def test_shared_memory_is_refused():
     one, two = torch.stack([g, g]).unbind()       # neighbours in memory
     assert torch.equal(E.orthogonalize(one, out=two), want)
     assert torch.equal(E.orthogonalize(g, out=g), want)
+
+
+def test_steps_are_a_whole_number():
+    """A fraction is refused, and so is a number that a 32-bit argument would cut."""
+    banner("orth steps")
+    g, b = gradient((20, 30), seed=1).cuda(), torch.zeros(20, 30, device="cuda")
+    p = g.clone()
+    for steps, exc in ((5.7, TypeError), (True, TypeError), ("5", TypeError), (None, TypeError), (2 ** 32 + 5, E.EccError),
+                       (-2 ** 32 + 5, E.EccError)):
+        with pytest.raises(exc):
+            E.orthogonalize(g, steps=steps)
+        with pytest.raises(exc):
+            E.muon_step([p], [g], [b], lr=0.1, steps=steps)
+    torch.cuda.synchronize()
+    assert torch.equal(p, g) and not b.any()

@@ -32,3 +32,13 @@ def test_overlap():
                        (t[10:20], t, True), (t, t[99:], True), (t, half, False), (t[:0], t, False),
                        (half[:10], half.view(torch.float32)[4:], True), (half[:10], half.view(torch.float32)[5:], False)):
         assert _overlap(a, b) is want
+
+
+def test_whole_steps():
+    from euler_characteristic_curves_amd.train import _whole
+    assert _whole(5) == 5 and _whole(5.0) == 5
+    for big in (2 ** 31, 2 ** 32 + 5, 10 ** 30):
+        assert _whole(big) == 2 ** 31 - 1 and _whole(-big) == -1
+    for bad in (5.7, True, "5", None):
+        with pytest.raises(TypeError):
+            _whole(bad)
