@@ -97,6 +97,7 @@ struct Norm : torch::autograd::Function<Norm> {
     const variable_list saved = ctx->get_saved_variables();
     variable_list in(5), out(6);
     bool any = false;
+    // strided inputs are copied again here: the copy of the forward pass would hold their memory twice until now
     for (int i = 0, edge = 0; i < 5; ++i) {
       in[i] = dense(saved[i]);
       if (!in[i].defined() || !ctx->needs_input_grad(edge++)) continue;  // absent inputs have no edge

@@ -86,7 +86,7 @@ def _grid_dtype(grid):
     raise TypeError(f"grid dtype {grid.dtype} not supported (uint8 or float32)")
 
 
-def _dev_tensor(t, name, dtype=None, device=None):
+def _dev_tensor(t, name, dtype=None, device=None, strided=False):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -95,7 +95,7 @@ def _dev_tensor(t, name, dtype=None, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if not t.is_contiguous():
+    if not strided and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
 

@@ -37,12 +37,13 @@ _NULL_CONTEXT = _NullContext()
 
 
 class _NormPlan:
-    """What a norm call needs besides its tensors, checked."""
+    """What a norm call needs besides its tensors, checked.  Strided tensors are made contiguous where the kernels are
+    called, once."""
 
     __slots__ = ("sizes", "dtype", "pdtype", "act", "nbytes")
 
     def __init__(self, x, groups, weight, bias, act, readout=None, offset=None, read=False):
-        _dev_tensor(x, "x")
+        _dev_tensor(x, "x", strided=True)
         if x.dtype not in _DTYPES:
             raise TypeError(f"x dtype {x.dtype} not supported (float32, float16 or bfloat16)")
         if x.dim() < 3:
@@ -61,7 +62,7 @@ class _NormPlan:
         for t, name, n in ((weight, "weight", C), (bias, "bias", C), (readout, "readout", C), (offset, "offset", 1)):
             if t is None:
                 continue
-            _dev_tensor(t, name, None, x.device)
+            _dev_tensor(t, name, None, x.device, strided=True)
             if t.dim() != 1 or t.numel() != n:
                 raise ValueError(f"{name} must be [{n}] (got {list(t.shape)})")
             if t.dtype != torch.float32 and t.dtype != x.dtype:
@@ -80,14 +81,8 @@ class _NormPlan:
                 raise EccError(_lib.ECC_E_SHAPE, "group norm: " + lib.ecc_last_error().decode(errors="replace"))
 
 
-def _contiguous(t):
-    return t if t is None or t.is_contiguous() else t.contiguous()
-
-
 def _norm(x, groups, weight, bias, readout, offset, act, eps, read):
-    # the checks look at what the kernels will read; the node keeps the caller's own tensors
-    plan = _NormPlan(_contiguous(x), groups, _contiguous(weight), _contiguous(bias), act, _contiguous(readout),
-                     _contiguous(offset), read)
+    plan = _NormPlan(x, groups, weight, bias, act, readout, offset, read)
     return _torch.norm(x, weight, bias, readout, offset, plan.sizes, plan.dtype, plan.pdtype, plan.act, plan.nbytes,
                        float(eps), read)
 

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import euler_characteristic_curves_amd as E
+from euler_characteristic_curves_amd._lib import lib
 from tests.gpu_util import banner, need_gpu
 from tests.norm_bounds import act_and_slope
 
@@ -137,3 +138,22 @@ def test_arguments_beyond_float32(act, readout):
     assert flat[0] == float("inf") and flat[1] == 0.0 and torch.equal(flat[2:], torch.zeros(48))
     (gb,) = torch.autograd.grad(out, [leaves[2]], grad.cuda())
     assert float(gb) == 1.0
+
+
+@pytest.mark.parametrize("readout", [False, True], ids=["norm", "readout"])
+def test_a_strided_input_is_copied_once(readout):
+    """Channels-first features in memory: what a forward call allocates is the copy that the kernels read, the result
+    and less than a megabyte of scratch."""
+    banner("norm copies", readout)
+    x = torch.randn(2, 64, 256, 256, device="cuda").permute(0, 2, 3, 1)
+    r = torch.ones(64, device="cuda")
+
+    def call():
+        return E.group_norm_readout(x, 8, None, None, r) if readout else E.group_norm_act(x, 8)
+
+    call()
+    before = torch.cuda.memory_stats()["allocated_bytes.all.allocated"]
+    out = call()
+    spent = torch.cuda.memory_stats()["allocated_bytes.all.allocated"] - before
+    scratch = lib.ecc_norm_workspace_bytes(2, 256 * 256, 64, 8)
+    assert spent <= x.numel() * 4 + out.numel() * 4 + scratch + (1 << 20)
