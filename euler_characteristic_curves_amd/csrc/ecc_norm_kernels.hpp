@@ -770,7 +770,7 @@ hipError_t with_cols(int V, int K, F f) {
 // that the join reads.
 inline void norm_fold(const NormArgs& a, double*& part, int& NB, int64_t cols, int64_t prow, int64_t NV,
                       hipStream_t stream) {
-  if (NB <= kNormFolded || (int64_t)NB * (a.C / a.G) * NV * (int64_t)sizeof(double) <= 128 * 1024) return;
+  if (!norm_folded(NB) || (int64_t)NB * (a.C / a.G) * NV * (int64_t)sizeof(double) <= 128 * 1024) return;
   const int per = (NB + kNormFolded - 1) / kNormFolded, rows = (NB + per - 1) / per;
   double* out = part + a.B * (NB + 1) * prow;
   hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)((cols + 255) / 256), (unsigned)rows, (unsigned)a.B), dim3(kJT), 0,
@@ -822,7 +822,7 @@ hipError_t norm_launch_bwd(const NormArgs& a, hipStream_t stream) {
   const int64_t prow = (int64_t)norm_row(a.C);
   double* part = reinterpret_cast<double*>(a.ws);
   double* chan = part + (int64_t)a.B * g.NB * prow;
-  float* coef = reinterpret_cast<float*>(chan + (1 + kNormFolded) * a.B * prow);
+  float* coef = reinterpret_cast<float*>(chan + (1 + norm_folded(g.NB)) * a.B * prow);
   const dim3 grid((unsigned)g.NB, (unsigned)a.B, (unsigned)g.chunks), block(kNT), join((unsigned)a.G, (unsigned)a.B);
   const dim3 last((unsigned)g.NB, a.gx ? (unsigned)a.B + 1 : 1u, a.gx ? (unsigned)g.chunks : 1u);
   return with_cols<T>(V, K, [&](auto v, auto k) {

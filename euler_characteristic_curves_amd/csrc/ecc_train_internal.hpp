@@ -50,15 +50,18 @@ inline int64_t norm_blocks(int64_t B, int64_t S, int64_t C, int64_t total) {
   return nb < 1 ? 1 : nb;
 }
 
-// Rows per sample that many partial rows are folded to before they are joined.
+// Rows per sample that more partial rows than that can be folded to before they
+// are joined.
 constexpr int kNormFolded = 32;
+inline int64_t norm_folded(int64_t blocks) { return blocks > kNormFolded ? kNormFolded : 0; }
 
 // Workspace: [partials: B x blocks rows | sums per sample: B rows | folded
-// partials: B x kNormFolded rows | 2 floats per group and sample]; a row is 3
+// partials: B x norm_folded rows | 2 floats per group and sample]; a row is 3
 // float64 per channel and one more.
 inline size_t norm_row(int64_t C) { return (size_t)(3 * C + 1); }
 inline size_t norm_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G) {
-  const size_t rows = (size_t)B * (size_t)(norm_blocks(B, S, C, kNormSums) + 1 + kNormFolded);
+  const int64_t blocks = norm_blocks(B, S, C, kNormSums);
+  const size_t rows = (size_t)B * (size_t)(blocks + 1 + norm_folded(blocks));
   return rows * norm_row(C) * sizeof(double) + (size_t)B * (size_t)G * 2 * sizeof(float) + 256;
 }
 

@@ -9,6 +9,7 @@ import euler_characteristic_curves_amd as E
 from euler_characteristic_curves_amd._lib import lib
 from tests.gpu_util import banner, need_gpu
 from tests.norm_bounds import act_and_slope
+from tests.test_gpu_norm import check_all, make
 
 pytestmark = pytest.mark.gpu
 F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
@@ -157,3 +158,13 @@ def test_a_strided_input_is_copied_once(readout):
     spent = torch.cuda.memory_stats()["allocated_bytes.all.allocated"] - before
     scratch = lib.ecc_norm_workspace_bytes(2, 256 * 256, 64, 8)
     assert spent <= x.numel() * 4 + out.numel() * 4 + scratch + (1 << 20)
+
+
+@pytest.mark.parametrize("readout", [False, True], ids=["norm", "readout"])
+@pytest.mark.parametrize("shape,groups", [((300, 3, 3, 48), 6), ((33, 9000, 16), 4), ((2000, 1, 8), 8), ((64, 40, 520), 20)],
+                         ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else None)
+def test_large_batches(shape, groups, readout):
+    """Workspaces without folded rows, one workgroup a sample and several."""
+    banner("norm batches", shape, groups, readout)
+    x, p, grad = make(shape, BF16, seed=21, readout=readout)
+    check_all(x, groups, p, grad, "silu")

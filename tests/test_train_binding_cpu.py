@@ -42,3 +42,16 @@ def test_whole_steps():
     for bad in (5.7, True, "5", None):
         with pytest.raises(TypeError):
             _whole(bad)
+
+
+def test_norm_workspace_of_large_batches():
+    """Rows for folded partial sums are there only where a sample has more partial rows than it is folded to: a batch
+    of small samples takes a fraction of its features, not several times them."""
+    from euler_characteristic_curves_amd._lib import lib
+    for batch, voxels, channels, groups in ((1024, 64, 512, 32), (32768, 1, 64, 8), (64, 64 * 64, 320, 32), (256, 1024, 64, 8)):
+        need = lib.ecc_norm_workspace_bytes(batch, voxels, channels, groups)
+        # two rows a sample where one workgroup sums it, and no more than 1024 + batch where several do
+        rows = batch + max(batch, 1024 + batch)
+        assert need <= rows * (3 * channels + 1) * 8 + batch * groups * 8 + 256
+    # 40 workgroups a sample: folded to 32
+    assert lib.ecc_norm_workspace_bytes(1, 40 * 8192, 1, 1) >= (40 + 1 + 32) * 4 * 8
