@@ -8,6 +8,8 @@ import torch
 
 import euler_characteristic_curves_amd as E
 from tests.gpu_util import banner, need_gpu
+from tests.orth_bounds import HALF
+from tests.orth_products import STACKS, orthogonal_on_device
 from tests.test_gpu_orth import gradient
 
 pytestmark = pytest.mark.gpu
@@ -68,3 +70,35 @@ def test_steps_are_a_whole_number():
             E.muon_step([p], [g], [b], lr=0.1, steps=steps)
     torch.cuda.synchronize()
     assert torch.equal(p, g) and not b.any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", STACKS, ids=lambda s: "x".join(map(str, s)))
+def test_every_way_products_are_shared_out(shape, dtype):
+    """Accuracy of the first, a middle and the last matrix, and the same bits when run again."""
+    banner("orth products", shape, dtype)
+    g = gradient(shape, dtype, seed=sum(shape)).cuda()
+    out = E.orthogonalize(g)
+    for _ in range(4):
+        assert torch.equal(E.orthogonalize(g), out)
+    for i in sorted({0, shape[0] // 2, shape[0] - 1}):
+        want, bound = orthogonal_on_device(g[i])
+        size = float(want.square().sum().sqrt())
+        total = bound + HALF[dtype] * size + 1e-7 * HALF[dtype] * want.numel() ** 0.5
+        err = float((out[i].double() - want).square().sum().sqrt())
+        assert err <= total, (i, err, total)
+
+
+@pytest.mark.parametrize("shape", [(1, 1409, 1411), (4, 1411, 1000), (32, 260, 257), (6, 1537, 769)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_muon_step_on_shared_products(shape):
+    """The update of the parameter in the last product of every kind of workgroup."""
+    banner("muon products", shape)
+    g = gradient(shape, seed=5).cuda()
+    p = torch.randn(shape, generator=torch.Generator().manual_seed(6)).cuda()
+    new, buf = p.clone(), torch.zeros_like(p)
+    E.muon_step([new], [g], [buf], lr=0.5, momentum=0.0, nesterov=False, weight_decay=0.125, scale=1.0)
+    assert torch.equal(buf, g)
+    # one fused multiply-add from the product that orthogonalize rounds to float32
+    want = p.double() * (1 - 0.5 * 0.125) - 0.5 * E.orthogonalize(g).double()
+    assert ((new.double() - want).abs() <= 2.0 ** -23 * (p.double().abs() + want.abs() + 1)).all()
