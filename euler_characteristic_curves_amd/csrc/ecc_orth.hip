@@ -9,11 +9,17 @@
 //
 // Arithmetic.  gfx950's float32 matrix instructions run at a sixteenth of the
 // float16 ones, so every operand is held as a pair of float16 numbers, x 2^s =
-// hi + lo, 22 bits and a sign together, and a product is three float16 matrix
-// products, hi hi' + hi lo' + lo hi', summed in float32 (the dropped lo lo' is
-// below 2^-24).  The exponent s comes from a bound of the matrix's entries, so
-// that nothing overflows and lo stays above float16's smallest number: per
-// matrix and step for X, per call for A and P.
+// hi + 2^-11 lo, 22 bits and a sign together, and a product is three float16
+// matrix products, hi hi' + 2^-11 (hi lo' + lo hi'), its two parts summed in
+// float32 apart (the dropped lo lo' is below 2^-24).  The exponent s comes from
+// a bound of the matrix's entries, so that nothing overflows: per matrix and
+// step for X, per call for A and P.  lo has a scale of its own so that it
+// reaches as far down as hi does: a pair keeps its 22 bits to 2^-27 of the bound
+// and ends at 2^-50, and rows and columns have float32's accuracy of their own
+// norm down to 1e-5 of the largest.  (With lo in hi's scale, which saves
+// nothing but the second sum, a pair ended at 2^-39: a row at 1e-5 of the others
+// was off by 4e-5 to 4e-4 of itself, one at 1e-7 by 0.4 to 5 %; 4096 x 4096 took
+// 3.97 ms, 4.01 so.)
 //
 // What bounds the products: the matrix unit, whose cycles the clock makes
 // dearer under load.  4096 x 4096 (3.87 ms) runs at 1.06e15 float16 operations a second
@@ -128,7 +134,7 @@ __device__ __forceinline__ float pair_scale(float bound) {
 
 __device__ __forceinline__ void split(float v, f16& hi, f16& lo) {
   hi = (f16)v;
-  lo = (f16)(v - (float)hi);
+  lo = (f16)((v - (float)hi) * kPairStep);
 }
 
 // X and X^T as pairs from a 64 x 64 tile of the input, and the scales of the
@@ -337,7 +343,7 @@ __device__ __forceinline__ void epilogue(const Product& p, int batch, int ti, in
       const f16x4 gh = *reinterpret_cast<const f16x4*>(gp), gl = *reinterpret_cast<const f16x4*>(gp + 32);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        u[r] = fmaf(p.o.b * p.sp / p.sa, (float)gh[r] + (float)gl[r], u[r]);
+        u[r] = fmaf(p.o.b * p.sp / p.sa, fmaf((float)gl[r], 1.0f / kPairStep, (float)gh[r]), u[r]);
         if (i + r == j) u[r] += p.o.a * p.sp;
       }
     }
@@ -386,7 +392,8 @@ __device__ __forceinline__ f16x8 fragment(const f16* lds, int row, int chunk) {
 
 // The first products' fragments are read, then one more with every product.
 template <int T>
-__device__ __forceinline__ void multiply_step(const f16* la, const f16* lb, f32x16 (&acc)[kFrag<T>][kFrag<T>]) {
+__device__ __forceinline__ void multiply_step(const f16* la, const f16* lb, f32x16 (&acc)[kFrag<T>][kFrag<T>],
+                                              f32x16 (&low)[kFrag<T>][kFrag<T>]) {
   constexpr int F = kFrag<T>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int ra = (wave >> 2) * T + (wave >> 1 & 1) * (T / 2) + (lane & 31), rb = (wave & 1) * (T / 2) + (lane & 31);
@@ -416,12 +423,12 @@ __device__ __forceinline__ void multiply_step(const f16* la, const f16* lb, f32x
     for (int i = 0; i < F; ++i)
 #pragma unroll
       for (int j = 0; j < F; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah[s][i], bl[s][j], acc[i][j], 0, 0, 0);
+        low[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah[s][i], bl[s][j], low[i][j], 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
       for (int j = 0; j < F; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(al[s][i], bh[s][j], acc[i][j], 0, 0, 0);
+        low[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(al[s][i], bh[s][j], low[i][j], 0, 0, 0);
   }
   __builtin_amdgcn_sched_group_barrier(0x100, 2 * F, 0);
 #pragma unroll
@@ -463,13 +470,13 @@ __global__ __launch_bounds__(kNT * R, T == 128 && S == 4 ? 1 : 2) void product_k
   const f16* Ap = p.A + batch * p.sA + (int64_t)ti * T * 64;
   const f16* Bp = p.B + batch * p.sB + (int64_t)tj * T * 64;
   const uint32_t offA = in_step<T * R, 4 * R>(), offB = in_step<T, 4 * R>();
-  f32x16 acc[F][F];
+  f32x16 acc[F][F], low[F][F];
 #pragma unroll
   for (int i = 0; i < F; ++i)
 #pragma unroll
     for (int j = 0; j < F; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = low[i][j][r] = 0.0f;
   const auto load = [&](int k, f16* la, f16* lb) {
     if (k < k1) {
       load_step<T * R, 4 * R>(Ap + k * p.rowsA * 64, offA, la);
@@ -488,7 +495,7 @@ __global__ __launch_bounds__(kNT * R, T == 128 && S == 4 ? 1 : 2) void product_k
     else
       wait_step<T, R, 0>();
     load(k + S - 1, na, nb);
-    multiply_step<T>(la, lb, acc);
+    multiply_step<T>(la, lb, acc, low);
   };
   load(k0, a0, b0);
   if constexpr (S == 2) {
@@ -513,6 +520,12 @@ __global__ __launch_bounds__(kNT * R, T == 128 && S == 4 ? 1 : 2) void product_k
       step(k + 3, a3, b3, a2, b2);
     }
   }
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+#pragma unroll
+    for (int j = 0; j < F; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(low[i][j][r], 1.0f / kPairStep, acc[i][j][r]);
   const int half = threadIdx.x / kNT;
   if (rest >= 0 && p.splits > 1) {
     float* out = p.part + ((int64_t)rest * R + half) * (T * T) + threadIdx.x % kNT * 4;

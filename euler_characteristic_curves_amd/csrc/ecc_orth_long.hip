@@ -217,7 +217,7 @@ __global__ __launch_bounds__(kNT) void long_square_kernel(Square p) {
     }
     if (p.pair) {
       const float v = (float)(s * p.scale);
-      const f16 hi = (f16)v, lo = (f16)(v - (float)hi);
+      const f16 hi = (f16)v, lo = (f16)((v - (float)hi) * kPairStep);
       f16* out = p.pair + off * 2;
       const int64_t at = ((col >> 5) * p.m + row) * 64 + (col & 31), to = ((row >> 5) * p.m + col) * 64 + (row & 31);
       out[at] = hi;

@@ -99,6 +99,9 @@ struct OrthArgs {
 // sa, sp.  False where they leave [-16, 16] or are not finite.
 bool orth_bounds(OrthArgs& o);
 
+// What the lower half of a pair is multiplied by (ecc_orth.hip).
+constexpr float kPairStep = 2048.0f;
+
 inline int64_t orth_pad(int64_t n) { return n <= 64 ? 64 : (n + 127) / 128 * 128; }
 
 // How a product of `batch` matrices of `rows` x `cols` (padded) results is

@@ -123,8 +123,10 @@ size_t ecc_norm_workspace_bytes(int64_t batch, int64_t voxels, int64_t channels,
  * (pairs of float16) and sum in float32; where the short side is at most 64, or
  * small beside the long one, and the steps let an error of X X^T grow by less
  * than 2^26, X X^T is carried through the steps in float64 instead and the long
- * side passed twice only.  Either way the result is that of float32 arithmetic,
- * rounded once to dtype.
+ * side passed twice only.  Either way the result has the error of float32
+ * arithmetic, rounded once to dtype, in every row and column down to 1e-5 of the
+ * largest; the pairs' last bit leaves an error of up to 1e-10 of the largest in
+ * smaller ones.  (Short sides up to 64 that are carried have no such limit.)
  * Refused with ECC_E_VALUE: steps outside [1, ECC_MAX_NS_STEPS], eps < 0, a
  * coefficient that is not finite, and coefficients under which a singular
  * value in [0, 1] leaves [-16, 16] within the steps.

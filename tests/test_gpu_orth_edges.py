@@ -102,3 +102,42 @@ def test_muon_step_on_shared_products(shape):
     # one fused multiply-add from the product that orthogonalize rounds to float32
     want = p.double() * (1 - 0.5 * 0.125) - 0.5 * E.orthogonalize(g).double()
     assert ((new.double() - want).abs() <= 2.0 ** -23 * (p.double().abs() + want.abs() + 1)).all()
+
+
+GRADED = [(130, 200), (200, 130), (512, 700), (1409, 1411), (100, 700), (512, 6000), (6000, 130), (40, 900), (64, 66)]
+
+
+def iterate(g, steps=5):
+    """The iteration in g's own type."""
+    if g.shape[0] > g.shape[1]:
+        return iterate(g.T.contiguous(), steps).T
+    a, b, c = 3.4445, -4.7750, 2.0315
+    x = (g / (g.double().square().sum().sqrt() + 1e-7)).to(g.dtype)
+    for _ in range(steps):
+        gram = x @ x.T.contiguous()
+        x = a * x + (b * gram + c * gram @ gram) @ x
+    return x
+
+
+@pytest.mark.parametrize("shape", GRADED, ids=lambda s: "x".join(map(str, s)))
+def test_graded_rows_and_columns(shape):
+    """Rows and columns far below the others have the error of float32 arithmetic, down to the floor that a pair's lowest
+    bit sets.
+
+    Operands of 22 bits for 24 are 4 times as coarse; 8 allows for a row's error being one draw of many.  A pair ends at
+    2^-50 of its matrix's bound (half a step of float16's smallest number, 2^-25, after the factor 2^11, over 2^14):
+    sqrt(n) such errors in a row, which the five steps multiply by 3.4445 each and add to, 525 in all, and twice that for
+    those of A and P.
+    """
+    banner("orth graded", shape)
+    g = torch.randn(shape, generator=torch.Generator().manual_seed(8))
+    for i, s in {3: 1e-3, 11: 1e-5, 17: 1e-7, 23: 1e-9}.items():
+        g[i] *= s
+        g[:, i + 1] *= s
+    g = g.cuda()
+    out, plain, want = E.orthogonalize(g).double(), iterate(g).double(), iterate(g.double())
+    floor = 3 * 525 * max(shape) ** 0.5 * 2.0 ** -50
+    for dim in (0, 1):
+        err, yard = ((t - want).square().sum(dim=dim).sqrt() for t in (out, plain))
+        worst = (err / (8 * yard + floor)).max()
+        assert worst <= 1, (dim, float(worst))
