@@ -46,7 +46,7 @@ struct NormGeom {
   int NB;      // workgroups per sample
   int L;       // lanes per row
   int nv;      // vectors per row
-  int chunks;  // column chunks of 64 vectors (rows of more than 4 x 64 vectors)
+  int chunks;  // column chunks of 64 vectors (rows of more than kMostK x 64)
   int runs;    // of kRun turns, of the workgroup that has most (passes that sum)
 };
 
@@ -191,14 +191,13 @@ __global__ __launch_bounds__(kNT) void norm_stats_kernel(NormGeom g, const T* x,
   Cols<V, K> col(g);
   const T* xs = x + (int64_t)blockIdx.y * g.S * g.C;
   constexpr int U = kUnroll<K>;
-  Vec<T, V> about[K];
-#pragma unroll
-  for (int k = 0; k < K; ++k) load_vec(xs + col.c[k], about[k]);
   int64_t r = col.template first<U>(g.S);
   for (int run = 0; run < g.runs; ++run) {
     float piv[K][V], s1[K][V], s2[K][V];
+    Vec<T, V> about[K];  // read again each run: the compiler would keep them as float64
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      load_vec(xs + col.c[k], about[k]);
       Vec<T, V> v = {};
       if (r < g.S) load_vec(xs + r * g.C + col.c[k], v);
 #pragma unroll
@@ -704,6 +703,15 @@ __global__ __launch_bounds__(kJT) void norm_join_bwd_kernel(NormArgs p, const do
   }
 }
 
+// Vectors a lane takes at most.  With four of 8 elements each, what a lane keeps
+// per channel fills the registers and leaves one or two waves a SIMD: forward
+// and training passes of 64 million bfloat16 values took 187 and 476 us with
+// 384 channels, 85 and 236 with two vectors, whose lanes are used to 75 % for 94;
+// with 1280 channels 208 and 553, in chunks of columns 104 and 282.  Four of 4
+// leave three waves, and the read-out needs a row in one wave.
+template <class T>
+constexpr int kMostK = sizeof(T) == 2 ? 2 : 4;
+
 // Lanes and vectors per row: the fewest vectors per lane that keep within 5 %
 // of the best use of the lanes (rows of nv vectors on floor(64 / L) L lanes).
 template <class T>
@@ -718,12 +726,12 @@ NormGeom norm_geom(const NormArgs& a, int& V, int& K) {
   g.chunks = 1;
   K = 1;
   g.L = 64;
-  if (g.nv > 4 * 64) {
+  if (g.nv > kMostK<T> * 64) {
     g.chunks = (g.nv + 63) / 64;
     return g;
   }
   double best = 0.0;
-  for (int k = 1; k <= (V == 1 ? 1 : 4); k *= 2) {
+  for (int k = 1; k <= (V == 1 ? 1 : kMostK<T>); k *= 2) {
     const int L = (g.nv + k - 1) / k;
     if (L > 64) continue;
     const double use = (double)(g.nv * (64 / L)) / (64.0 * k);
@@ -759,8 +767,9 @@ hipError_t with_cols(int V, int K, F f) {
   using std::integral_constant;
   if (V == 1) return f(integral_constant<int, 1>(), integral_constant<int, 1>());
   if (K == 1) return f(integral_constant<int, VF>(), integral_constant<int, 1>());
-  if (K == 2) return f(integral_constant<int, VF>(), integral_constant<int, 2>());
-  return f(integral_constant<int, VF>(), integral_constant<int, 4>());
+  if constexpr (kMostK<T> == 4)
+    if (K == 4) return f(integral_constant<int, VF>(), integral_constant<int, 4>());
+  return f(integral_constant<int, VF>(), integral_constant<int, 2>());
 }
 
 }  // namespace

@@ -36,11 +36,12 @@ struct NormArgs {
 // Workgroups per sample of a pass over the features, `total` in a launch.  Each
 // has at least 4096 elements, or 8192 where it leaves partial sums, which the
 // next pass has to read (256 x 256 x 64 float32 forward: 18.9 us, 20.3 with
-// 4096).  Passes that hold sums or both gradients need 80
-// to 127 registers, so that 4 workgroups a CU are resident, and leave a partial
-// row each: 1024 (2 x 128^3 x 64, bfloat16: 803 us a training pass, 838 with
-// 2048).  The forward's second pass fits 8 a CU: 2048 (read-out of 256^3 x 32:
-// 226 us, 250 with 1024).
+// 4096).  Passes that hold sums or both gradients leave a partial row each and
+// have some 4 workgroups a CU resident: 1024 (2 x 128^3 x 64, bfloat16: 803 us a
+// training pass, 838 with 2048).  (They need 54 to 130 registers with one vector
+// a lane, 4 to 8 workgroups a CU, 76 to 168 with two, 3 to 6, and float32 with four
+// 130 to 251, 2 or 3.)  The forward's second pass fits 6 to 8 a CU with one
+// vector: 2048 (read-out of 256^3 x 32: 226 us, 250 with 1024).
 constexpr int64_t kNormSums = 1024, kNormApply = 2048;
 inline int64_t norm_blocks(int64_t B, int64_t S, int64_t C, int64_t total) {
   const int64_t least = total == kNormSums ? 8192 : 4096;

@@ -168,3 +168,15 @@ def test_large_batches(shape, groups, readout):
     banner("norm batches", shape, groups, readout)
     x, p, grad = make(shape, BF16, seed=21, readout=readout)
     check_all(x, groups, p, grad, "silu")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("C", [384, 640, 1000, 1024, 1025, 1280, 2047])
+def test_wide_rows_of_16_bits(C, dtype):
+    """Two vectors a lane at most; beyond 1024 channels, chunks of columns."""
+    banner("norm 16-bit rows", C, dtype)
+    for readout in (False, True):
+        if readout and C > 1024:
+            continue
+        x, p, grad = make((2, 41, C), dtype, seed=C, readout=readout)
+        check_all(x, 1 if C % 2 else 4, p, grad, "silu")
