@@ -295,6 +295,8 @@ int ecc_muon_step(void* param, int pdtype, const void* grad, int gdtype, float* 
   o.nesterov = nesterov != 0;
   o.keep = (float)(1.0 - lr * weight_decay);
   o.rate = (float)(lr * scale);
+  if (!isfinite(o.momentum) || !isfinite(o.blend) || !isfinite(o.keep) || !isfinite(o.rate))
+    return fail(ECC_E_VALUE, "momentum, 1 - lr weight_decay and lr scale must be finite in float32");
   o.steps = steps;
   o.eps = eps;
   o.a = a;

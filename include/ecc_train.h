@@ -142,7 +142,7 @@ int ecc_orthogonalize(const void* g, int dtype, int64_t batch, int64_t rows, int
  * param: pdtype, grad: gdtype, buffer: float32, all [batch][rows][cols]; none
  * overlaps another.
  * Refused with ECC_E_VALUE besides the above: lr, momentum, weight_decay or
- * scale not finite.
+ * scale not finite, or momentum, 1 - lr weight_decay or lr scale beyond float32.
  */
 int ecc_muon_step(void* param, int pdtype, const void* grad, int gdtype, float* buffer, int64_t batch, int64_t rows,
                   int64_t cols, double lr, double momentum, int nesterov, double weight_decay, double scale,

@@ -55,3 +55,15 @@ def test_norm_workspace_of_large_batches():
         assert need <= rows * (3 * channels + 1) * 8 + batch * groups * 8 + 256
     # 40 workgroups a sample: folded to 32
     assert lib.ecc_norm_workspace_bytes(1, 40 * 8192, 1, 1) >= (40 + 1 + 32) * 4 * 8
+
+
+def test_factors_of_the_momentum_step_beyond_float32():
+    """Finite arguments whose products the kernels could only have as infinity are refused, not applied."""
+    from euler_characteristic_curves_amd import _lib
+    from tests.test_train_cpu import muon
+    for bad in (dict(momentum=1e39), dict(momentum=-1e300), dict(lr=1e20, scale=1e20), dict(lr=1e20, decay=-1e20),
+                dict(lr=-1e39)):
+        assert muon(_lib, **bad) == _lib.ECC_E_VALUE, bad
+        assert b"float32" in _lib.lib.ecc_last_error()
+    # in range, and refused for the workspace only
+    assert muon(_lib, lr=1e30, scale=1e-30, decay=1e-30, ws=None) == _lib.ECC_E_WORKSPACE
