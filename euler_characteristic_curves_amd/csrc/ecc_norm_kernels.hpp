@@ -14,10 +14,10 @@
 // Every pass is a stream over the features and bound by HBM (or by the memory
 // side cache when the features fit it); the statistics force two passes each
 // way, so forward reads x twice and backward reads x and dy twice.  2 x 128^3 x
-// 64 in bfloat16, a training pass: 0.81 ms, 8 times 537 MB at 5.3 TB/s (a copy
-// of 1 GB: 5.0).  The read-out of 256^3 x 32: 1.08 ms, 5 times 1.07 GB; its
-// passes with the activation are bound by issue as well, 11 to 14 instructions
-// an element beside two transcendental ones.  Mapping:
+// 64 in bfloat16, a training pass: 0.83 ms, 8 times 537 MB at 5.2 TB/s (a copy
+// of 1 GB: 5.0).  The read-out of 256^3 x 32: 1.12 to 1.17 ms, 5 times 1.07 GB;
+// its passes with the activation are bound by issue as well, 13 to 16
+// instructions an element beside two transcendental ones.  Mapping:
 // a row of C channels is taken by L lanes of one wave, K vectors of V = 16
 // bytes each, so a lane keeps its V K channels for the whole pass and holds
 // their scale, shift and sums in registers; a wave has floor(64 / L) rows in

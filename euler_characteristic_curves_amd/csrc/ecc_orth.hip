@@ -21,12 +21,13 @@
 // was off by 4e-5 to 4e-4 of itself, one at 1e-7 by 0.4 to 5 %; 4096 x 4096 took
 // 3.97 ms, 4.01 so.)
 //
-// What bounds the products: the matrix unit, whose cycles the clock makes
-// dearer under load.  4096 x 4096 (3.87 ms) runs at 1.06e15 float16 operations a second
-// (a library's product of that size in float16: 1.16e15), the unit busy half
-// the cycles at 1.9 GHz; short sums, the pipeline's start and the launches.
-// Matrices up to 64 across, and long ones, take other ways (orth_is_thin,
-// orth_is_long).
+// What bounds the products of large matrices: the clock, which falls from 2.4 to
+// 1.73 GHz under them, and the waits of a step, for its loads and the other
+// waves, 23 % of the waves' cycles.  4096 x 4096 takes 4.0 ms, 1.02e15 float16
+// operations a second (a library's product of that size in float16: 1.16e15);
+// the matrix unit is busy 60 (X X^T) to 63 % (P X) of the cycles that are left.
+// Of smaller ones: short sums, the pipeline's start and the launches.  Matrices
+// up to 64 across, and long ones, take other ways (orth_is_thin, orth_is_long).
 //
 // Layout.  A pair matrix keeps blocks of 32 columns one after the other, in
 // each its rows of 32 hi and 32 lo, 128 bytes: what a tile loads per step of

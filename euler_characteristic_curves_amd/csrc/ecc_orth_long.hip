@@ -13,7 +13,7 @@
 // What bounds it: A_0, the float64 matrix rate (512 x 16384: 83 to 87 us, 4.8e9
 // operations, 55e12 a second; a library's 4096^3 product in float64 68e12);
 // the 14 products of the short side, their launches and L2's latency, 5 to 9 us
-// each.  In all 325 us of a momentum step of 512 x 16384, 483 by the direct way.
+// each.  In all 330 us of a momentum step of 512 x 16384, 483 by the direct way.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
