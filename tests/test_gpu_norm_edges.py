@@ -180,3 +180,30 @@ def test_wide_rows_of_16_bits(C, dtype):
             continue
         x, p, grad = make((2, 41, C), dtype, seed=C, readout=readout)
         check_all(x, 1 if C % 2 else 4, p, grad, "silu")
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=["f32", "f16", "bf16"])
+def test_nan_passes_every_activation(dtype, act):
+    """One NaN makes its group's values, field and gradients NaN, and no others; the clamps of the activations do not
+    swallow it."""
+    banner("norm nan", dtype, act)
+    x, p, grad = make((3, 5, 7, 16), dtype, seed=6, readout=True)
+    x[1, 2, 3, 5] = float("nan")          # sample 1, group 1 of 4
+    hit = torch.zeros(3, 35, 4, 4, dtype=torch.bool)
+    hit[1, :, 1] = True
+    leaves = [x.cuda().requires_grad_(), *(v.cuda().requires_grad_() for v in p.values())]
+    y = E.group_norm_act(leaves[0], 4, leaves[1], leaves[2], act=act)
+    (gx,) = torch.autograd.grad(y, leaves[:1], torch.ones_like(y))
+    for t in (y.detach(), gx):
+        assert torch.equal(torch.isnan(t).reshape(hit.shape).cpu(), hit)
+    f = E.group_norm_readout(leaves[0], 4, *leaves[1:], act=act)
+    assert torch.equal(torch.isnan(f).reshape(3, 35).cpu(), hit.any(dim=3).any(dim=2))
+    grads = torch.autograd.grad(f, leaves, grad.cuda())
+    assert torch.equal(torch.isnan(grads[0]).reshape(hit.shape).cpu(), hit)
+    channels = hit.any(dim=1).any(dim=0).reshape(16)
+    for name, g in zip(p, grads[1:4]):
+        # the bias's gradient has no x in it where there is no activation
+        want = torch.zeros(16, dtype=torch.bool) if act == "none" and name == "bias" else channels
+        assert torch.equal(torch.isnan(g).cpu(), want), name
+    assert torch.isfinite(grads[4]).all()
