@@ -553,7 +553,7 @@ __global__ __launch_bounds__(kNT) void norm_grad_kernel(NormGeom g, NormArgs p, 
       const int c = col.c[k] + j;
       const int64_t gr = (int64_t)blockIdx.y * p.G + (unsigned)c / (unsigned)D;
       c1[k][j] = coef[2 * gr + 1];
-      c0[k][j] = fmaf(p.stats[kStat * gr + 2], c1[k][j], -coef[2 * gr]);
+      c0[k][j] = -coef[2 * gr];
       ar[k][j] = READ ? af.a[k][j] * load_param(p.readout, p.pdtype, c, 0.0f) : af.a[k][j];
     }
   const int64_t base = (int64_t)blockIdx.y * g.S * g.C;
@@ -644,8 +644,14 @@ __global__ __launch_bounds__(kJT) void norm_join_kernel(NormArgs p, const double
   if (threadIdx.x == 0) group_stats(s1, s2, (double)p.S * (double)D, pivot, p.eps, p.stats + (b * p.G + gr) * kStat);
 }
 
+// s - by, where `by` is a correction: an infinite gradient makes it infinite or
+// NaN, and s already what it is.
+__device__ __forceinline__ double less(double s, double by) { return isfinite(by) ? s - by : s; }
+
 // Joins the partial rows of one sample and group: channel sums with A2 scaled
-// by rstd, and the group's coefficients rstd m1 and rstd^2 m2 (backward).
+// by rstd, and the group's coefficients rstd m1 and rstd^2 m2 (backward).  The
+// passes before and after take x less the mean as float32 has it; the rest of
+// the mean is taken off A2, and off rstd m1 with the factor that x has there.
 template <bool READ>
 __global__ __launch_bounds__(kJT) void norm_join_bwd_kernel(NormArgs p, const double* part, int NB, int D,
                                                             int64_t prow, double* chan, float* coef) {
@@ -655,7 +661,7 @@ __global__ __launch_bounds__(kJT) void norm_join_bwd_kernel(NormArgs p, const do
   const int W = D < kJT ? D : kJT, parts = kJT / W;
   const int at = threadIdx.x % W, pt = threadIdx.x / W;
   const float* st = p.stats + (b * p.G + gr) * kStat;
-  const double rstd = (double)st[1], rest = (double)st[2];  // A2 was summed about st[0]
+  const double rstd = (double)st[1], rest = (double)st[2];
   double m1 = 0.0, m2 = 0.0;
   for (int64_t c0 = 0; c0 < D; c0 += W) {
     const int64_t c = gr * D + c0 + at;
@@ -679,7 +685,7 @@ __global__ __launch_bounds__(kJT) void norm_join_bwd_kernel(NormArgs p, const do
     if (threadIdx.x < W && c0 + at < D) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) s[i] = lds[i * kJT + at];
-      s[1] = (s[1] - rest * s[0]) * rstd;
+      s[1] = less(s[1], rest * s[0]) * rstd;
 #pragma unroll
       for (int i = 0; i < NV; ++i) chan[b * prow + c * NV + i] = s[i];
       double w = (double)load_param(p.weight, p.pdtype, c, 1.0f);
@@ -691,9 +697,9 @@ __global__ __launch_bounds__(kJT) void norm_join_bwd_kernel(NormArgs p, const do
   m1 = block_sum(m1, lds);
   m2 = block_sum(m2, lds);
   if (threadIdx.x == 0) {
-    const double n = (double)p.S * (double)D;
-    coef[2 * (b * p.G + gr)] = (float)(rstd * (m1 / n));
-    coef[2 * (b * p.G + gr) + 1] = (float)(rstd * rstd * (m2 / n));
+    const double n = (double)p.S * (double)D, c1 = rstd * rstd * (m2 / n);
+    coef[2 * (b * p.G + gr)] = (float)less(rstd * (m1 / n), rest * c1);
+    coef[2 * (b * p.G + gr) + 1] = (float)c1;
   }
   if (READ && gr == 0) {
     double t = 0.0;

@@ -185,8 +185,8 @@ def muon_step(params, grads, buffers, lr, momentum=0.95, nesterov=True, weight_d
     include/ecc_train.h).
 
     params, grads, buffers: sequences of one length; entry i of each is [rows, cols] or a stack [batch, rows, cols] of
-    matrices (layers of one shape), contiguous, without memory in common; buffers are float32.  scale: factor of the update, by default
-    sqrt(max(1, rows / cols)).  Every argument is checked before anything is changed.
+    matrices (layers of one shape), contiguous, without memory in common; buffers are float32.  scale: factor of the
+    update, by default sqrt(max(1, rows / cols)).  Every argument is checked before anything is changed.
     """
     params, grads, buffers = list(params), list(grads), list(buffers)
     if not len(params) == len(grads) == len(buffers):

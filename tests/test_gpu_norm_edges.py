@@ -9,7 +9,7 @@ import euler_characteristic_curves_amd as E
 from euler_characteristic_curves_amd._lib import lib
 from tests.gpu_util import banner, need_gpu
 from tests.norm_bounds import act_and_slope
-from tests.test_gpu_norm import check_all, make
+from tests.test_gpu_norm import call, check_all, make
 
 pytestmark = pytest.mark.gpu
 F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
@@ -207,3 +207,25 @@ def test_nan_passes_every_activation(dtype, act):
         want = torch.zeros(16, dtype=torch.bool) if act == "none" and name == "bias" else channels
         assert torch.equal(torch.isnan(g).cpu(), want), name
     assert torch.isfinite(grads[4]).all()
+
+
+@pytest.mark.parametrize("readout", [False, True], ids=["norm", "readout"])
+@pytest.mark.parametrize("dtype", [F32, F16], ids=["f32", "f16"])
+def test_infinite_gradient(dtype, readout):
+    """An infinite upstream gradient, as a scaled loss that overflows gives, makes its channels' gradients infinite with
+    the sign of their factors, and not NaN; others stay finite."""
+    banner("norm infinite gradient", dtype, readout)
+    x, p, grad = make((2, 9, 11, 16), dtype, seed=14, readout=readout)
+    where = (1, 4, 5) if readout else (1, 4, 5, 6)
+    grad[where] = float("inf")
+    leaves = [x.cuda().requires_grad_(), *(v.cuda().requires_grad_() for v in p.values())]
+    out = call(leaves[0], 4, dict(zip(p, leaves[1:])), "none")
+    gw, gb = torch.autograd.grad(out, leaves[1:3], grad.cuda())
+    v = x.double().reshape(2, 99, 4, 4)
+    xhat = (v - v.mean(dim=(1, 3), keepdim=True)).reshape(x.shape)[1, 4, 5]
+    factor = p["readout"].double() if readout else torch.ones(16, dtype=torch.float64)
+    hit = torch.ones(16, dtype=torch.bool) if readout else torch.arange(16) == 6
+    for g, f in ((gw, factor * xhat), (gb, factor)):
+        g = g.double().cpu()
+        assert torch.equal(g[hit], torch.sign(f[hit]) * float("inf"))
+        assert torch.isfinite(g[~hit]).all()
