@@ -15,7 +15,7 @@
 // side cache when the features fit it); the statistics force two passes each
 // way, so forward reads x twice and backward reads x and dy twice.  2 x 128^3 x
 // 64 in bfloat16, a training pass: 0.83 ms, 8 times 537 MB at 5.2 TB/s (a copy
-// of 1 GB: 5.0).  The read-out of 256^3 x 32: 1.12 to 1.17 ms, 5 times 1.07 GB;
+// of 1 GB: 5.0).  The read-out of 256^3 x 32: 1.12 to 1.16 ms, 5 times 1.07 GB;
 // its passes with the activation are bound by issue as well, 13 to 16
 // instructions an element beside two transcendental ones.  Mapping:
 // a row of C channels is taken by L lanes of one wave, K vectors of V = 16
