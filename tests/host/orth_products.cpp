@@ -1,10 +1,8 @@
-// How the products of an orthogonalisation are shared out, one line each:
-//   batch rows cols way product tile pair deep splits rest-of-whole
-// for the matrices given on the command line as batch,rows,cols[,steps].
-// (Host code of ecc_train_internal.hpp and the bounds of ecc_train_api.cpp's
-// default coefficients.)
+// How the products of an orthogonalisation are shared out, one line for each
+// stack given on the command line as batch,rows,cols:
+//   batch,rows,cols way product:tile,pair,deep,splits,whole,rest ...
+// (the sharing rule of ecc_train_internal.hpp, compiled for the host).
 #include <cstdio>
-#include <cstdlib>
 
 #include "ecc_train_internal.hpp"
 
