@@ -2,8 +2,9 @@
 
 The compute path is libecc_mi355.so (hand-written HIP for gfx950, C ABI in
 include/ecc.h and include/ecc_train.h); ``euler_characteristic_curves_amd.ecc``
-(the curves) and ``euler_characteristic_curves_amd.train`` (operators that train
-a network through them) are its thin PyTorch binding.  The binding is imported lazily so that ``workloads`` (seeded
+(the curves), ``euler_characteristic_curves_amd.train`` (operators that train
+a network through them) and ``euler_characteristic_curves_amd.block`` (those of a
+residual block) are its thin PyTorch binding.  The binding is imported lazily so that ``workloads`` (seeded
 synthetic inputs) can be used without the built library; any attempt to use
 an ECC entry point without the library raises ImportError.
 """
@@ -21,7 +22,9 @@ _API = (
 
 _TRAIN_API = ("group_norm_act", "group_norm_readout", "orthogonalize", "muon_step")
 
-__all__ = list(_API + _TRAIN_API)
+_BLOCK_API = ("residual_norm", "rms_norm")
+
+__all__ = list(_API + _TRAIN_API + _BLOCK_API)
 
 
 def __getattr__(name):
@@ -29,6 +32,8 @@ def __getattr__(name):
         from . import ecc as _module
     elif name in _TRAIN_API:
         from . import train as _module
+    elif name in _BLOCK_API:
+        from . import block as _module
     else:
         raise AttributeError(name)
     globals()[name] = value = getattr(_module, name)  # found without this call from now on

@@ -56,6 +56,7 @@ ECC_MAX_NS_STEPS = 64
 TRAIN_EXPORTS = (
     "ecc_norm_fwd", "ecc_norm_bwd", "ecc_norm_readout_fwd", "ecc_norm_readout_bwd", "ecc_norm_workspace_bytes",
     "ecc_orthogonalize", "ecc_muon_step", "ecc_orth_workspace_bytes",
+    "ecc_residual_norm_fwd", "ecc_residual_norm_bwd", "ecc_residual_norm_workspace_bytes",
 )
 
 
@@ -125,6 +126,12 @@ def _load():
     lib.ecc_muon_step.restype = I
     lib.ecc_orth_workspace_bytes.argtypes = [I64, I64, I64]
     lib.ecc_orth_workspace_bytes.restype = SZ
+    lib.ecc_residual_norm_fwd.argtypes = [P, I, P, I, I64, I64, I64, P, I, P, P, I, I, F, F, P, P, P, P]
+    lib.ecc_residual_norm_fwd.restype = I
+    lib.ecc_residual_norm_bwd.argtypes = [P, I, P, I, I64, I64, I64, P, I, P, P, I, I, F, P, P, P, P, P, P, P, P, P, SZ, P]
+    lib.ecc_residual_norm_bwd.restype = I
+    lib.ecc_residual_norm_workspace_bytes.argtypes = [I64, I64, I64, I]
+    lib.ecc_residual_norm_workspace_bytes.restype = SZ
     lib.ecc_status_string.argtypes = [I]
     lib.ecc_status_string.restype = ctypes.c_char_p
     lib.ecc_last_error.argtypes = []

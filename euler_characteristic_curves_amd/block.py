@@ -1,0 +1,39 @@
+"""Thin PyTorch binding of the operators of a residual block (include/ecc_train.h).
+
+Features are channels last, ``[batch, *space, channels]`` or, for curves and other sequences, ``[batch, steps,
+channels]``.  Every function takes tensors that live on a ROCm device and calls the C entry points on the current torch
+stream; argument checks and autograd nodes are in csrc/ecc_torch_block.cpp, all arithmetic is in the HIP kernels.
+Scratch comes from torch's allocator per call, so calls may run on any stream and be captured into a graph.  Strided
+tensors are copied once.  Forward-mode derivatives are refused, and gradients of gradients raise an error.
+"""
+
+from . import _lib  # noqa: F401  (loads the library that the binding needs)
+from . import _torch
+from ._lib import EccError
+
+__all__ = ["residual_norm", "rms_norm", "EccError"]
+
+
+def residual_norm(x, branch, gate=None, weight=None, branch_weight=None, norm_branch=True, scale=1.0, eps=1e-6):
+    """What stands between two blocks of a residual network, in one pass: the norm after a block, its gate, the residual
+    sum and the norm before the next block.
+
+        y = scale * x + gate * n(branch) * branch_weight,   z = n(y) * weight,   n(v) = v / sqrt(mean(v^2) + eps)
+
+    with the means over the channels of one position.  x: the residual stream, float32, float16 or bfloat16 [batch,
+    *space, channels]; branch: the block's output, of x's shape and type, or 16-bit beside a float32 x; gate: [channels],
+    or [batch, channels] for a gate per sample; gate, weight and branch_weight are float32 or branch's dtype, all alike,
+    and 1 where they are None.  norm_branch=False leaves n(branch) out of y.
+
+    Returns (y, z), y like x and z like branch.  Differentiable in the five tensors (see include/ecc_train.h).
+    """
+    return _torch.residual_norm(x, branch, gate, weight, branch_weight, scale, eps, norm_branch)
+
+
+def rms_norm(x, weight=None, eps=1e-6, dtype=None):
+    """The norm before the first block: x / sqrt(mean(x^2) + eps) * weight over the channels, [batch, *space, channels].
+
+    weight: [channels], float32 or the result's dtype, or None (1); dtype: of the result, x's by default; a float32 x may
+    have a 16-bit result.  Differentiable in x and weight.
+    """
+    return _torch.rms_norm(x, weight, eps, dtype)

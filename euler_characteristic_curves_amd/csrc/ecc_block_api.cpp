@@ -1,0 +1,124 @@
+// C ABI of a residual block's operators (include/ecc_train.h): argument
+// validation, error reporting, dispatch.
+
+#include "../../include/ecc_train.h"
+
+#include <hip/hip_runtime.h>
+#include <math.h>
+
+#include "../../include/ecc.h"
+#include "ecc_block_internal.hpp"
+#include "ecc_check.hpp"
+
+namespace {
+
+using ecc::check_eps;
+using ecc::check_workspace;
+using ecc::fail;
+using ecc::hip_status;
+using ecc::is_dtype;
+
+int check_residual_shape(int64_t batch, int64_t inner, int64_t channels, bool sample_gates) {
+  if (batch < 1 || inner < 1 || channels < 1)
+    return fail(ECC_E_SHAPE, "batch, inner and channels must be >= 1 (got inner=%lld channels=%lld)", inner, channels);
+  if (channels > ECC_MAX_CHANNELS) return fail(ECC_E_SHAPE, "channels=%lld exceeds %lld", channels, ECC_MAX_CHANNELS);
+  if (inner > ECC_MAX_VOXELS / channels || batch > ECC_MAX_VOXELS / (inner * channels))
+    return fail(ECC_E_SHAPE, "more than 2^40 elements");
+  if (sample_gates && batch > ECC_MAX_NORM_BATCH)
+    return fail(ECC_E_SHAPE, "batch=%lld with gates of their own exceeds %lld", batch, ECC_MAX_NORM_BATCH);
+  return ECC_OK;
+}
+
+// Checks shared by both directions, and the part of the arguments they share.
+int check_residual(ecc::ResArgs& a, const void* x, int xdtype, const void* branch, int dtype, int64_t batch, int64_t inner,
+                   int64_t channels, const void* gate, int per_sample, const void* weight, const void* branch_weight,
+                   int pdtype, int norm_branch, float scale) {
+  ecc::set_error("");
+  if (!x) return fail(ECC_E_NULL, "x is NULL");
+  if (!is_dtype(dtype)) return fail(ECC_E_DTYPE, "dtype %lld is not one of ECC_T_*", dtype);
+  if (xdtype != ECC_T_F32 && xdtype != dtype)
+    return fail(ECC_E_DTYPE, "xdtype %lld is neither ECC_T_F32 nor dtype (%lld)", xdtype, dtype);
+  if (pdtype != ECC_T_F32 && pdtype != dtype)
+    return fail(ECC_E_DTYPE, "pdtype %lld is neither ECC_T_F32 nor dtype (%lld)", pdtype, dtype);
+  const int st = check_residual_shape(batch, inner, channels, gate && per_sample);
+  if (st != ECC_OK) return st;
+  if (!branch && (gate || branch_weight || norm_branch))
+    return fail(ECC_E_NULL, "branch is NULL, but its gate or its norm is given");
+  if (!norm_branch && branch_weight) return fail(ECC_E_VALUE, "branch_weight is given without norm_branch");
+  if (!isfinite(scale)) return fail(ECC_E_VALUE, "scale must be finite");
+  a = ecc::ResArgs{};
+  a.x = x;
+  a.branch = branch;
+  a.xdtype = xdtype;
+  a.dtype = dtype;
+  a.batch = batch;
+  a.inner = inner;
+  a.channels = channels;
+  a.gate = gate;
+  a.gate_stride = gate && per_sample ? channels : 0;
+  a.weight = weight;
+  a.branch_weight = branch_weight;
+  a.pdtype = pdtype;
+  a.norm_branch = norm_branch != 0;
+  a.scale = scale;
+  return ECC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ecc_residual_norm_workspace_bytes(int64_t batch, int64_t inner, int64_t channels, int gate_per_sample) {
+  if (check_residual_shape(batch, inner, channels, gate_per_sample != 0) != ECC_OK) return 0;
+  return ecc::res_workspace_bytes(batch, inner, channels, gate_per_sample != 0);
+}
+
+int ecc_residual_norm_fwd(const void* x, int xdtype, const void* branch, int dtype, int64_t batch, int64_t inner,
+                          int64_t channels, const void* gate, int gate_per_sample, const void* weight,
+                          const void* branch_weight, int pdtype, int norm_branch, float scale, float eps, void* y, void* z,
+                          float* stats, void* stream) {
+  ecc::ResArgs a;
+  int st = check_residual(a, x, xdtype, branch, dtype, batch, inner, channels, gate, gate_per_sample, weight, branch_weight,
+                          pdtype, norm_branch, scale);
+  if (st != ECC_OK) return st;
+  if (!z) return fail(ECC_E_NULL, "z is NULL");
+  if (branch && !y) return fail(ECC_E_NULL, "y is NULL");
+  st = check_eps(eps);
+  if (st != ECC_OK) return st;
+  a.eps = eps;
+  a.y = y;
+  a.z = z;
+  a.stats = stats;
+  return hip_status(ecc::launch_residual_fwd(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int ecc_residual_norm_bwd(const void* x, int xdtype, const void* branch, int dtype, int64_t batch, int64_t inner,
+                          int64_t channels, const void* gate, int gate_per_sample, const void* weight,
+                          const void* branch_weight, int pdtype, int norm_branch, float scale, const float* stats,
+                          const void* grad_y, const void* grad_z, void* grad_x, void* grad_branch, void* grad_gate,
+                          void* grad_weight, void* grad_branch_weight, void* ws, size_t ws_bytes, void* stream) {
+  ecc::ResArgs a;
+  int st = check_residual(a, x, xdtype, branch, dtype, batch, inner, channels, gate, gate_per_sample, weight, branch_weight,
+                          pdtype, norm_branch, scale);
+  if (st != ECC_OK) return st;
+  if (!stats) return fail(ECC_E_NULL, "stats is NULL");
+  if (!grad_y && !grad_z) return fail(ECC_E_NULL, "grad_y and grad_z are both NULL");
+  if (!grad_x && !grad_branch && !grad_gate && !grad_weight && !grad_branch_weight)
+    return fail(ECC_E_NULL, "every gradient is NULL");
+  if ((grad_branch && !branch) || (grad_gate && !gate) || (grad_weight && !weight) || (grad_branch_weight && !branch_weight))
+    return fail(ECC_E_NULL, "a gradient of an argument that is NULL is wanted");
+  st = check_workspace(ws, ws_bytes, ecc::res_workspace_bytes(batch, inner, channels, a.gate_stride != 0));
+  if (st != ECC_OK) return st;
+  a.stats = const_cast<float*>(stats);
+  a.gy = grad_y;
+  a.gz = grad_z;
+  a.gx = grad_x;
+  a.gbranch = grad_branch;
+  a.ggate = grad_gate;
+  a.gweight = grad_weight;
+  a.gbranch_weight = grad_branch_weight;
+  a.ws = ws;
+  return hip_status(ecc::launch_residual_bwd(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

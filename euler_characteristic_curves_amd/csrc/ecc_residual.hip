@@ -1,0 +1,386 @@
+// The norms before and after a block, fused with its gate and the residual
+// scale (contract: include/ecc_train.h).
+//
+// With r(v) = 1 / sqrt(mean v^2 + eps) over a row of channels,
+//   n = branch r(branch) branch_weight   (or the branch itself),
+//   y = scale x + gate n,   z = y r(y) weight.
+// Backwards, with hat(v) = v r(v),
+//   dy += r(y) (dz weight - hat(y) mean(dz weight hat(y))),   dx = scale dy,
+//   dn = dy gate,   dgate = sum dy n,   dweight = sum dz hat(y),
+//   dbranch = r(branch) (dn branch_weight - hat(branch) mean(dn branch_weight hat(branch))),
+//   dbranch_weight = sum dn hat(branch).
+//
+// A row stays in the registers of the lanes that share it, from its one load to
+// its one store: the forward pass moves four streams, the backward pass six,
+// which is the least there is.  y is formed again from x in the backward pass:
+// x and y would cost the same to read, and y is rounded.  Squares are summed in
+// float64, so that no row of finite values overflows or underflows; it costs a
+// few cycles of 64 lanes against some 50 of memory.  The remaining sums along a
+// row are float32 over 16 elements a lane and then a tree.  Sums over rows: 16
+// rows of a thread in float32, then those, then the workgroup's rows by halves,
+// then all workgroups in float64, always in the same order.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "ecc_act.hpp"
+#include "ecc_block_internal.hpp"
+#include "ecc_train_internal.hpp"
+
+namespace ecc {
+namespace {
+
+constexpr int kRun = 16;  // rows of a thread that are summed before their sum joins the others
+
+struct ResGeom {
+  int L, slots;  // lanes of a row, rows of a workgroup at a time
+  int64_t samples, rows;  // rows of a sample
+  int64_t blocks;         // workgroups of a sample
+};
+
+// Where this lane's vectors begin, and how many of the first elements belong to
+// the vector before: the last one of a row is moved back to end with the row.
+template <int V, int K>
+struct Columns {
+  int64_t at[K];
+  int skip[K];  // V: the lane has no such vector
+  __device__ __forceinline__ Columns(int lane, int L, int64_t C) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int64_t c = ((int64_t)k * L + lane) * V;
+      at[k] = c + V <= C ? c : (C > V ? C - V : 0);
+      skip[k] = c < C ? (int)(c - at[k]) : V;
+    }
+  }
+};
+
+// Elements of a row, or of the parameters; those that another vector has are 0.
+template <int V, int K, class T>
+__device__ __forceinline__ void load_row(const T* p, const Columns<V, K>& col, bool active, float (&r)[K][V]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    Vec<T, V> v = {};
+    if (active && col.skip[k] < V) load_vec(p + col.at[k], v);
+#pragma unroll
+    for (int j = 0; j < V; ++j) r[k][j] = V > 1 && j < col.skip[k] ? 0.0f : (float)v.v[j];
+  }
+}
+template <int V, int K, class T>
+__device__ __forceinline__ void store_row(T* p, const Columns<V, K>& col, const float (&r)[K][V]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    Vec<T, V> v;
+#pragma unroll
+    for (int j = 0; j < V; ++j) v.v[j] = (T)r[k][j];
+    if (col.skip[k] == 0) {
+      store_vec(p + col.at[k], v);
+    } else if (col.skip[k] < V) {
+#pragma unroll
+      for (int j = 1; j < V; ++j)
+        if (j >= col.skip[k]) p[col.at[k] + j] = v.v[j];
+    }
+  }
+}
+template <int V, int K>
+__device__ __forceinline__ void load_params(const void* p, int pdtype, int64_t off, const Columns<V, K>& col,
+                                            float (&r)[K][V]) {
+  const auto take = [&](auto type) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      Vec<decltype(type), V> v = {};
+      if (col.skip[k] < V) load_vec(reinterpret_cast<const decltype(type)*>(p) + off + col.at[k], v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) r[k][j] = V > 1 && j < col.skip[k] ? 0.0f : (float)v.v[j];
+    }
+  };
+  if (!p) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) r[k][j] = j < col.skip[k] ? 0.0f : 1.0f;
+  } else if (pdtype == kTF32) {
+    take(float{});
+  } else if (pdtype == kTF16) {
+    take(f16{});
+  } else {
+    take(bf16{});
+  }
+}
+
+// Sum over the lanes of a row.  Every thread of the workgroup calls it where a
+// row has more than a wave.
+template <class T>
+__device__ __forceinline__ T row_sum(T v, int L, T* lds) {
+  const int within = L < 64 ? L : 64;
+  for (int d = 1; d < within; d *= 2) v += __shfl_xor(v, d);
+  if (L > 64) {
+    const int waves = L / 64, wave = threadIdx.x >> 6, first = wave / waves * waves;
+    __syncthreads();  // the sums before are read
+    if ((threadIdx.x & 63) == 0) lds[wave] = v;
+    __syncthreads();
+    v = lds[first];
+    for (int w = 1; w < waves; ++w) v += lds[first + w];
+  }
+  return v;
+}
+
+// Squares of float32 numbers and their sums fit float64 with room to spare.
+template <int V, int K>
+__device__ __forceinline__ float inverse_rms(const float (&r)[K][V], int L, int64_t C, float eps, double* lds) {
+  double s = 0.0;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j) s = fma((double)r[k][j], (double)r[k][j], s);
+  s = row_sum(s, L, lds);
+  return (float)(1.0 / sqrt(s / (double)C + (double)eps));
+}
+
+template <class XT, class BT, int V, int K>
+__global__ __launch_bounds__(512) void residual_fwd_kernel(ResArgs a, ResGeom g) {
+  __shared__ double lds[8];
+  const int lane = threadIdx.x & (g.L - 1), slot = threadIdx.x / g.L;
+  const int64_t sample = blockIdx.x / g.blocks, block = blockIdx.x - sample * g.blocks, C = a.channels;
+  const Columns<V, K> col(lane, g.L, C);
+  float gate[K][V], weight[K][V], after[K][V];
+  load_params(a.gate, a.pdtype, sample * a.gate_stride, col, gate);
+  load_params(a.weight, a.pdtype, 0, col, weight);
+  load_params(a.branch_weight, a.pdtype, 0, col, after);
+  for (int64_t first = block * g.slots; first < g.rows; first += g.blocks * g.slots) {
+    const bool active = first + slot < g.rows;
+    const int64_t row = sample * g.rows + first + slot;
+    float x[K][V], b[K][V];
+    load_row(reinterpret_cast<const XT*>(a.x) + row * C, col, active, x);
+    float rb = 1.0f;
+    if (a.branch) {
+      load_row(reinterpret_cast<const BT*>(a.branch) + row * C, col, active, b);
+      if (a.norm_branch) rb = inverse_rms(b, g.L, C, a.eps, lds);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[k][j] = fmaf(a.scale, x[k][j], gate[k][j] * (b[k][j] * rb * after[k][j]));
+      if (active) store_row(reinterpret_cast<XT*>(a.y) + row * C, col, x);
+    }
+    const float ry = inverse_rms(x, g.L, C, a.eps, lds);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[k][j] = x[k][j] * ry * weight[k][j];
+    if (active) {
+      store_row(reinterpret_cast<BT*>(a.z) + row * C, col, x);
+      if (a.stats && lane == 0) {
+        a.stats[row * 2] = rb;
+        a.stats[row * 2 + 1] = ry;
+      }
+    }
+  }
+}
+
+template <class XT, class BT, int V, int K>
+__global__ __launch_bounds__(512) void residual_bwd_kernel(ResArgs a, ResGeom g, float* part) {
+  extern __shared__ float shared[];  // the sums of half the slots, where a workgroup has more than one
+  __shared__ float lds[8];
+  const int lane = threadIdx.x & (g.L - 1), slot = threadIdx.x / g.L;
+  const int64_t sample = blockIdx.x / g.blocks, block = blockIdx.x - sample * g.blocks, C = a.channels;
+  const Columns<V, K> col(lane, g.L, C);
+  float gate[K][V], weight[K][V], after[K][V];
+  load_params(a.gate, a.pdtype, sample * a.gate_stride, col, gate);
+  load_params(a.weight, a.pdtype, 0, col, weight);
+  load_params(a.branch_weight, a.pdtype, 0, col, after);
+  float run[3][K][V] = {}, total[3][K][V] = {};  // of the gate, the weight, the branch's weight
+  const float inv = 1.0f / (float)C;
+  int turns = 0;
+  for (int64_t first = block * g.slots; first < g.rows; first += g.blocks * g.slots) {
+    const bool active = first + slot < g.rows;
+    const int64_t row = sample * g.rows + first + slot;
+    float x[K][V], b[K][V], dy[K][V], dz[K][V];
+    load_row(reinterpret_cast<const XT*>(a.x) + row * C, col, active, x);
+    load_row(reinterpret_cast<const BT*>(a.branch) + row * C, col, active && a.branch, b);
+    load_row(reinterpret_cast<const XT*>(a.gy) + row * C, col, active && a.gy, dy);
+    load_row(reinterpret_cast<const BT*>(a.gz) + row * C, col, active && a.gz, dz);
+    const float rb = active ? a.stats[row * 2] : 0.0f, ry = active ? a.stats[row * 2 + 1] : 0.0f;
+    // b: the branch's hat, or the branch itself; x: y's hat; dz: its gradient
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (a.branch) {
+          b[k][j] *= rb;
+          x[k][j] = fmaf(a.scale, x[k][j], gate[k][j] * (b[k][j] * after[k][j]));
+        }
+        x[k][j] *= ry;
+        if (active && a.gz) run[1][k][j] = fmaf(dz[k][j], x[k][j], run[1][k][j]);
+        dz[k][j] *= weight[k][j];
+        s = fmaf(dz[k][j], x[k][j], s);
+      }
+    if (a.gz) s = row_sum(s, g.L, lds) * inv;  // without it nothing of z, infinite or not, reaches a gradient
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (a.gz) dy[k][j] = fmaf(ry, fmaf(-x[k][j], s, dz[k][j]), dy[k][j]);
+        x[k][j] = a.branch ? a.scale * dy[k][j] : dy[k][j];
+        if (active) run[0][k][j] = fmaf(dy[k][j], b[k][j] * after[k][j], run[0][k][j]);
+        dy[k][j] *= gate[k][j];
+        if (active) run[2][k][j] = fmaf(dy[k][j], b[k][j], run[2][k][j]);
+        dy[k][j] *= after[k][j];
+        t = fmaf(dy[k][j], b[k][j], t);
+      }
+    if (a.gx && active) store_row(reinterpret_cast<XT*>(a.gx) + row * C, col, x);
+    if (a.norm_branch) {
+      t = row_sum(t, g.L, lds) * inv;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) dy[k][j] = rb * fmaf(-b[k][j], t, dy[k][j]);
+    }
+    if (a.gbranch && active) store_row(reinterpret_cast<BT*>(a.gbranch) + row * C, col, dy);
+    if (++turns == kRun) {
+      turns = 0;
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            total[q][k][j] += run[q][k][j];
+            run[q][k][j] = 0.0f;
+          }
+    }
+  }
+  if (!part) return;
+  part += (int64_t)blockIdx.x * 3 * C;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) total[q][k][j] += run[q][k][j];
+    // the slots' rows, by halves
+    for (int d = g.slots / 2; d > 0; d /= 2) {
+      __syncthreads();
+      if (slot >= d && slot < 2 * d) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int j = 0; j < V; ++j) shared[(k * V + j) * (d * g.L) + (slot - d) * g.L + lane] = total[q][k][j];
+      }
+      __syncthreads();
+      if (slot < d) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int j = 0; j < V; ++j) total[q][k][j] += shared[(k * V + j) * (d * g.L) + slot * g.L + lane];
+      }
+    }
+    if (slot == 0) store_row(part + q * C, col, total[q]);
+  }
+}
+
+// Joins the partial rows of a quantity: blockIdx.z 0 the gate (for every sample,
+// blockIdx.y), 1 and 2 the weights.  64 rows at a time, 16 columns.
+constexpr int kJoin = 1024;
+__global__ __launch_bounds__(kJoin) void residual_join_kernel(ResArgs a, ResGeom g, const float* part) {
+  __shared__ double lds[kJoin / 16][17];
+  const int q = blockIdx.z, c = threadIdx.x & 15, r = threadIdx.x >> 4;
+  void* out = q == 0 ? a.ggate : q == 1 ? a.gweight : a.gbranch_weight;
+  const bool each = q == 0 && a.gate_stride;
+  const int64_t C = a.channels, col = (int64_t)blockIdx.x * 16 + c;
+  if (!out) return;
+  for (int64_t sample = blockIdx.y; sample < (each ? g.samples : 1); sample += gridDim.y) {
+    const int64_t from = each ? sample * g.blocks : 0, rows = each ? g.blocks : g.samples * g.blocks;
+    double s = 0.0;
+    if (col < C) {
+#pragma unroll 4
+      for (int64_t i = r; i < rows; i += kJoin / 16) s += (double)part[((from + i) * 3 + q) * C + col];
+    }
+    lds[r][c] = s;
+    __syncthreads();
+    for (int d = kJoin / 32; d > 0; d /= 2) {
+      if (r < d) lds[r][c] += lds[r + d][c];
+      __syncthreads();
+    }
+    if (r == 0 && col < C) store_param(out, a.pdtype, sample * a.gate_stride * (q == 0) + col, (float)lds[0][c]);
+    __syncthreads();
+  }
+}
+
+template <class F>
+hipError_t with_types(int xdtype, int dtype, F f) {
+  if (dtype == 0) return f(float{}, float{});
+  if (dtype == 1) return xdtype == 0 ? f(float{}, f16{}) : f(f16{}, f16{});
+  return xdtype == 0 ? f(float{}, bf16{}) : f(bf16{}, bf16{});
+}
+
+// f(V, K) of a row's shape.
+template <bool HALF, class F>
+hipError_t with_shape(const RowShape& s, F f) {
+  using std::integral_constant;
+  if (s.V == 1) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+  if constexpr (HALF) {
+    if (s.K == 1) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+    return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
+  } else {
+    if (s.K == 1) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+    if (s.K == 2) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
+    if (s.K == 3) return f(integral_constant<int, 4>{}, integral_constant<int, 3>{});
+    return f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+  }
+}
+
+ResGeom geometry(const ResArgs& a, const RowShape& s, int64_t total) {
+  ResGeom g{};
+  g.L = s.L;
+  g.slots = s.threads / s.L;
+  g.samples = a.gate_stride ? a.batch : 1;
+  g.rows = a.gate_stride ? a.inner : a.batch * a.inner;
+  g.blocks = res_blocks(g.samples, g.rows, g.slots, total);
+  return g;
+}
+
+}  // namespace
+
+hipError_t launch_residual_fwd(const ResArgs& a, hipStream_t stream) {
+  return with_types(a.xdtype, a.dtype, [&](auto xt, auto bt) {
+    using XT = decltype(xt);
+    using BT = decltype(bt);
+    constexpr bool half = sizeof(XT) == 2;
+    const RowShape s = res_shape(a.channels, half);
+    const ResGeom g = geometry(a, s, kResApply);
+    return with_shape<half>(s, [&](auto v, auto k) {
+      hipLaunchKernelGGL((residual_fwd_kernel<XT, BT, v.value, k.value>), dim3((unsigned)(g.samples * g.blocks)),
+                         dim3(s.threads), 0, stream, a, g);
+      return hipGetLastError();
+    });
+  });
+}
+
+hipError_t launch_residual_bwd(const ResArgs& a, hipStream_t stream) {
+  return with_types(a.xdtype, a.dtype, [&](auto xt, auto bt) {
+    using XT = decltype(xt);
+    using BT = decltype(bt);
+    constexpr bool half = sizeof(XT) == 2;
+    const RowShape s = res_shape(a.channels, half);
+    const ResGeom g = geometry(a, s, kResSums);
+    const bool sums = a.ggate || a.gweight || a.gbranch_weight;
+    float* part = sums ? reinterpret_cast<float*>(a.ws) : nullptr;
+    return with_shape<half>(s, [&](auto v, auto k) {
+      const size_t lds = g.slots > 1 ? (size_t)(s.threads / 2) * v.value * k.value * sizeof(float) : 0;
+      hipLaunchKernelGGL((residual_bwd_kernel<XT, BT, v.value, k.value>), dim3((unsigned)(g.samples * g.blocks)),
+                         dim3(s.threads), lds, stream, a, g, part);
+      if (sums) {
+        const int64_t each = a.gate_stride && a.ggate ? a.batch : 1;
+        hipLaunchKernelGGL(residual_join_kernel,
+                           dim3((unsigned)((a.channels + 15) / 16), (unsigned)(each < 1024 ? each : 1024), 3), dim3(kJoin), 0,
+                           stream, a, g, part);
+      }
+      return hipGetLastError();
+    });
+  });
+}
+
+}  // namespace ecc

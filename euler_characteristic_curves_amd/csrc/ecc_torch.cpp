@@ -6,26 +6,11 @@
 // tensors become pointers, and scratch comes from torch's allocator per call,
 // on the current stream.
 
-#include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
-#include <c10/core/DeviceGuard.h>
-#include <torch/csrc/autograd/custom_function.h>
-#include <torch/csrc/autograd/functions/basic_ops.h>
-#include <torch/csrc/utils/pybind.h>
-
-#include <optional>
-#include <string>
-#include <vector>
-
-#include "../../include/ecc.h"
-#include "../../include/ecc_train.h"
+#include "ecc_torch.hpp"
 
 namespace {
 
-using torch::autograd::AutogradContext;
-using torch::autograd::variable_list;
-using Optional = std::optional<at::Tensor>;
+using namespace ecc_torch;
 
 // What a call needs besides its tensors.
 struct Plan {
@@ -33,22 +18,6 @@ struct Plan {
   double eps;
   bool read;
 };
-
-const void* ptr(const at::Tensor& t) { return t.defined() ? t.const_data_ptr() : nullptr; }
-void* out_ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
-at::Tensor dense(const at::Tensor& t) { return t.defined() ? t.contiguous() : t; }
-at::Tensor dense(const Optional& t) { return t ? t->contiguous() : at::Tensor(); }
-void* stream_of(const at::Tensor& t) { return c10::hip::getCurrentHIPStreamMasqueradingAsCUDA(t.get_device()).stream(); }
-
-void check(int status, const char* what) {
-  if (status == ECC_OK) return;
-  const std::string detail = ecc_last_error();
-  pybind11::gil_scoped_acquire gil;  // backward runs on the engine's thread
-  const auto error = pybind11::module_::import("euler_characteristic_curves_amd._lib").attr("EccError");
-  const auto value = error(status, std::string(what) + ": " + ecc_status_string(status) + " (" + detail + ")");
-  PyErr_SetObject(error.ptr(), value.ptr());
-  throw pybind11::error_already_set();
-}
 
 // x and the parameters are contiguous, absent ones undefined.
 at::Tensor run_forward(const Plan& p, const at::Tensor& x, const at::Tensor& w, const at::Tensor& b, const at::Tensor& r,
@@ -120,15 +89,7 @@ struct Norm : torch::autograd::Function<Norm> {
                            out_ptr(out[1]), out_ptr(out[2]), ws.data_ptr(), bytes, stream_of(x)),
               "ecc_norm_bwd");
     }
-    if (again && any) {  // a gradient of these gradients is an error, not zero
-      const auto error = std::make_shared<torch::autograd::DelayedError>(
-          "group norm's backward pass is differentiable once only", (int64_t)out.size());
-      variable_list leaves(out.size());
-      for (size_t i = 0; i < out.size(); ++i)
-        if (out[i].defined()) leaves[i] = out[i].detach().requires_grad_();
-      at::AutoGradMode on(true);
-      return (*error)(std::move(leaves));
-    }
+    if (again && any) return once_only(out, "group norm");
     return out;
   }
 };
@@ -137,9 +98,7 @@ at::Tensor norm(const at::Tensor& x, const Optional& w, const Optional& b, const
                 const std::vector<int64_t>& sizes, int64_t dtype, int64_t pdtype, int64_t act, int64_t bytes, double eps,
                 bool read) {
   const pybind11::gil_scoped_release nogil;
-  // a dual tensor need not require a gradient, and autograd modes do not turn it off
-  const auto dual = [](const Optional& t) { return t && t->_fw_grad(/*level=*/0).defined(); };
-  TORCH_CHECK_NOT_IMPLEMENTED(!dual(x) && !dual(w) && !dual(b) && !dual(r) && !dual(o),
+  TORCH_CHECK_NOT_IMPLEMENTED(!is_dual(x) && !is_dual(w) && !is_dual(b) && !is_dual(r) && !is_dual(o),
                               "group norm has no forward-mode derivative");
   const Plan p{sizes[0], sizes[1], sizes[2], sizes[3], dtype, pdtype, act, bytes, eps, read};
   const auto wants = [](const Optional& t) { return t && t->requires_grad(); };
@@ -150,4 +109,7 @@ at::Tensor norm(const at::Tensor& x, const Optional& w, const Optional& b, const
 
 }  // namespace
 
-PYBIND11_MODULE(_torch, m) { m.def("norm", &norm); }
+PYBIND11_MODULE(_torch, m) {
+  m.def("norm", &norm);
+  ecc_torch::define_block(m);
+}

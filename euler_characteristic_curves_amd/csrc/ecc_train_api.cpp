@@ -5,39 +5,20 @@
 
 #include <hip/hip_runtime.h>
 #include <math.h>
-#include <stdio.h>
 
 #include "../../include/ecc.h"
 #include "ecc_act.hpp"
+#include "ecc_check.hpp"
 #include "ecc_internal.hpp"
 #include "ecc_train_internal.hpp"
 
 namespace {
 
-int fail(int status, const char* fmt, long long a = 0, long long b = 0) {
-  char msg[256];
-  snprintf(msg, sizeof(msg), fmt, a, b);
-  ecc::set_error(msg);
-  return status;
-}
-
-int hip_status(hipError_t e) {
-  if (e == hipSuccess) return ECC_OK;
-  char msg[256];
-  snprintf(msg, sizeof(msg), "HIP error: %s", hipGetErrorString(e));
-  ecc::set_error(msg);
-  return ECC_E_HIP;
-}
-
-bool is_dtype(int d) { return d == ECC_T_F32 || d == ECC_T_F16 || d == ECC_T_BF16; }
-
-int check_workspace(const void* ws, size_t ws_bytes, size_t need) {
-  if (!ws) return fail(ECC_E_WORKSPACE, "workspace is NULL");
-  if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(ECC_E_WORKSPACE, "workspace is not 256-byte aligned");
-  if (ws_bytes < need)
-    return fail(ECC_E_WORKSPACE, "workspace has %lld bytes, needs %lld", (long long)ws_bytes, (long long)need);
-  return ECC_OK;
-}
+using ecc::check_eps;
+using ecc::check_workspace;
+using ecc::fail;
+using ecc::hip_status;
+using ecc::is_dtype;
 
 int check_norm_shape(int64_t B, int64_t S, int64_t C, int64_t G) {
   if (B < 1 || S < 1 || C < 1)
@@ -76,11 +57,6 @@ int check_norm(ecc::NormArgs& a, const void* x, int dtype, int64_t B, int64_t S,
   a.act = act;
   a.stats = const_cast<float*>(stats);
   a.ws = ws;
-  return ECC_OK;
-}
-
-int check_eps(float eps) {
-  if (!(eps >= 0.0f) || !isfinite(eps)) return fail(ECC_E_VALUE, "eps must be finite and >= 0");
   return ECC_OK;
 }
 

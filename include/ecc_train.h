@@ -2,7 +2,9 @@
  * ecc_train.h -- C ABI of the operators in libecc_mi355.so that train a
  * network through the curves: group norm with an activation over
  * channels-last features, the same norm read out to the scalar grid a curve
- * takes, Newton-Schulz orthogonalisation, and the momentum update built on it.
+ * takes, Newton-Schulz orthogonalisation, and the momentum update built on it;
+ * and those of a residual block over curves or other channels-last features:
+ * the norms around a block with its gate and residual scale.
  *
  * Conventions are those of ecc.h (device pointers owned by the caller, work
  * enqueued on `stream`, status codes, ecc_last_error), except the workspace:
@@ -150,6 +152,48 @@ int ecc_muon_step(void* param, int pdtype, const void* grad, int gdtype, float* 
 
 /* Workspace bytes of the two calls above (0 for invalid sizes). */
 size_t ecc_orth_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+
+/*
+ * The norms after a block and before the next one, with the block's gate and
+ * the residual scale between them.  A row is one position of one sample, of
+ * `channels` (<= ECC_MAX_CHANNELS) numbers; there are batch x inner of them.
+ *   x       device, xdtype elements, [batch][inner][channels]: the residual stream
+ *   branch  device, dtype elements, of x's shape: the block's output; NULL for
+ *           the norm alone, z of x (gate, branch_weight and norm_branch are
+ *           then NULL and 0, and scale is not used)
+ *   gate    pdtype elements, [channels], or [batch][channels] where
+ *           gate_per_sample (batch <= ECC_MAX_NORM_BATCH); NULL stands for 1
+ *   weight, branch_weight  pdtype elements, [channels]; NULL stands for 1
+ *   xdtype  ECC_T_F32 or dtype; pdtype: ECC_T_F32 or dtype
+ * With n(v) = v / sqrt(mean v^2 + eps) over a row,
+ *   y = scale x + gate n(branch) branch_weight   (xdtype; with branch in place
+ *       of n(branch) unless norm_branch),
+ *   z = n(y) weight                              (dtype; y as it was before rounding).
+ * stats: float32 [batch][inner][2], the factors 1 / sqrt(..) of both norms for
+ * the backward pass, or NULL.  No output overlaps an input.  One launch, no
+ * workspace.
+ * Squares are summed in float64, everything else is float32, rounded once.
+ */
+int ecc_residual_norm_fwd(const void* x, int xdtype, const void* branch, int dtype, int64_t batch, int64_t inner,
+                          int64_t channels, const void* gate, int gate_per_sample, const void* weight,
+                          const void* branch_weight, int pdtype, int norm_branch, float scale, float eps, void* y, void* z,
+                          float* stats, void* stream);
+
+/*
+ * Its backward pass.  grad_y (xdtype), grad_z (dtype): either may be NULL (0).
+ * grad_x (xdtype), grad_branch (dtype), grad_gate, grad_weight and
+ * grad_branch_weight (pdtype, of their arguments' shapes) are OVERWRITTEN; each
+ * may be NULL (not wanted), but not all of them.  One launch, two where a
+ * parameter's gradient is wanted.
+ */
+int ecc_residual_norm_bwd(const void* x, int xdtype, const void* branch, int dtype, int64_t batch, int64_t inner,
+                          int64_t channels, const void* gate, int gate_per_sample, const void* weight,
+                          const void* branch_weight, int pdtype, int norm_branch, float scale, const float* stats,
+                          const void* grad_y, const void* grad_z, void* grad_x, void* grad_branch, void* grad_gate,
+                          void* grad_weight, void* grad_branch_weight, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of the backward pass (0 for invalid sizes). */
+size_t ecc_residual_norm_workspace_bytes(int64_t batch, int64_t inner, int64_t channels, int gate_per_sample);
 
 #ifdef __cplusplus
 }
