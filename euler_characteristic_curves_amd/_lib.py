@@ -57,6 +57,8 @@ TRAIN_EXPORTS = (
     "ecc_norm_fwd", "ecc_norm_bwd", "ecc_norm_readout_fwd", "ecc_norm_readout_bwd", "ecc_norm_workspace_bytes",
     "ecc_orthogonalize", "ecc_muon_step", "ecc_orth_workspace_bytes",
     "ecc_residual_norm_fwd", "ecc_residual_norm_bwd", "ecc_residual_norm_workspace_bytes",
+    "ecc_gated_recurrence_fwd", "ecc_gated_recurrence_bwd", "ecc_gated_recurrence_workspace_bytes",
+    "ecc_gated_recurrence_saved_bytes",
 )
 
 
@@ -132,6 +134,13 @@ def _load():
     lib.ecc_residual_norm_bwd.restype = I
     lib.ecc_residual_norm_workspace_bytes.argtypes = [I64, I64, I64, I]
     lib.ecc_residual_norm_workspace_bytes.restype = SZ
+    lib.ecc_gated_recurrence_fwd.argtypes = [P, P, I, I64, I64, I64, P, P, P, P, P, P, SZ, P]
+    lib.ecc_gated_recurrence_fwd.restype = I
+    lib.ecc_gated_recurrence_bwd.argtypes = [P, P, I, I64, I64, I64, P, P, P, P, P, P, P, P, SZ, P]
+    lib.ecc_gated_recurrence_bwd.restype = I
+    for sizes in (lib.ecc_gated_recurrence_workspace_bytes, lib.ecc_gated_recurrence_saved_bytes):
+        sizes.argtypes = [I64, I64, I64, I]
+        sizes.restype = SZ
     lib.ecc_status_string.argtypes = [I]
     lib.ecc_status_string.restype = ctypes.c_char_p
     lib.ecc_last_error.argtypes = []

@@ -11,7 +11,7 @@ from . import _lib  # noqa: F401  (loads the library that the binding needs)
 from . import _torch
 from ._lib import EccError
 
-__all__ = ["residual_norm", "rms_norm", "EccError"]
+__all__ = ["residual_norm", "rms_norm", "gated_recurrence", "EccError"]
 
 
 def residual_norm(x, branch, gate=None, weight=None, branch_weight=None, norm_branch=True, scale=1.0, eps=1e-6):
@@ -37,3 +37,18 @@ def rms_norm(x, weight=None, eps=1e-6, dtype=None):
     have a 16-bit result.  Differentiable in x and weight.
     """
     return _torch.rms_norm(x, weight, eps, dtype)
+
+
+def gated_recurrence(x, gate, state=None, lengths=None):
+    """A gated linear recurrence along the steps of a sequence, such as the thresholds of a curve:
+
+        h_t = k_t h_(t-1) + (1 - k_t) x_t,   k_t = 1 / (1 + exp(-gate_t)),   h_(-1) = state
+
+    x, gate: float32, float16 or bfloat16 [batch, steps, channels] of one type; state: float32 [batch, channels], or None
+    (0); lengths: int64 [batch] on the device, how many steps each sequence has (all of them where None): what x and gate
+    hold behind them is not read, and h is 0 there.
+
+    Returns (h, last): h like x, and the float32 state after every sequence's last step, [batch, channels], which a next
+    call takes as its state.  Differentiable in x, gate and state (see include/ecc_train.h).
+    """
+    return _torch.gated_recurrence(x, gate, state, lengths)

@@ -7,6 +7,7 @@
 #include <math.h>
 
 #include "../../include/ecc.h"
+#include "ecc_act.hpp"
 #include "ecc_block_internal.hpp"
 #include "ecc_check.hpp"
 
@@ -64,6 +65,35 @@ int check_residual(ecc::ResArgs& a, const void* x, int xdtype, const void* branc
   return ECC_OK;
 }
 
+int check_recurrence_shape(int64_t batch, int64_t steps, int64_t channels, int dtype) {
+  if (!is_dtype(dtype)) return fail(ECC_E_DTYPE, "dtype %lld is not one of ECC_T_*", dtype);
+  if (batch < 1 || steps < 1 || channels < 1)
+    return fail(ECC_E_SHAPE, "batch, steps and channels must be >= 1 (got steps=%lld channels=%lld)", steps, channels);
+  if (batch > ECC_MAX_VOXELS || steps > ECC_MAX_VOXELS / channels || batch > ECC_MAX_VOXELS / (steps * channels))
+    return fail(ECC_E_SHAPE, "more than 2^40 elements");
+  const ecc::RecShape s = ecc::rec_shape(batch, steps, channels, dtype != ECC_T_F32);
+  if (s.blocks * s.segments > INT32_MAX / batch) return fail(ECC_E_SHAPE, "batch=%lld is too large for one launch", batch);
+  return ECC_OK;
+}
+
+int check_recurrence(ecc::RecArgs& a, const void* x, const void* gate, int dtype, int64_t batch, int64_t steps,
+                     int64_t channels, const int64_t* lengths, void* ws, size_t ws_bytes) {
+  ecc::set_error("");
+  if (!x) return fail(ECC_E_NULL, "x is NULL");
+  if (!gate) return fail(ECC_E_NULL, "gate is NULL");
+  const int st = check_recurrence_shape(batch, steps, channels, dtype);
+  if (st != ECC_OK) return st;
+  a = ecc::RecArgs{};
+  a.x = x;
+  a.gate = gate;
+  a.batch = batch;
+  a.steps = steps;
+  a.channels = channels;
+  a.lengths = lengths;
+  a.ws = ws;
+  return check_workspace(ws, ws_bytes, ecc::rec_workspace_bytes(batch, steps, channels, dtype != ECC_T_F32));
+}
+
 }  // namespace
 
 extern "C" {
@@ -119,6 +149,55 @@ int ecc_residual_norm_bwd(const void* x, int xdtype, const void* branch, int dty
   a.gbranch_weight = grad_branch_weight;
   a.ws = ws;
   return hip_status(ecc::launch_residual_bwd(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t ecc_gated_recurrence_workspace_bytes(int64_t batch, int64_t steps, int64_t channels, int dtype) {
+  if (check_recurrence_shape(batch, steps, channels, dtype) != ECC_OK) return 0;
+  return ecc::rec_workspace_bytes(batch, steps, channels, dtype != ECC_T_F32);
+}
+
+size_t ecc_gated_recurrence_saved_bytes(int64_t batch, int64_t steps, int64_t channels, int dtype) {
+  if (check_recurrence_shape(batch, steps, channels, dtype) != ECC_OK) return 0;
+  return (size_t)(batch * ecc::rec_shape(batch, steps, channels, dtype != ECC_T_F32).tiles * channels) * sizeof(float);
+}
+
+int ecc_gated_recurrence_fwd(const void* x, const void* gate, int dtype, int64_t batch, int64_t steps, int64_t channels,
+                             const float* state, const int64_t* lengths, void* h, float* last, float* saved, void* ws,
+                             size_t ws_bytes, void* stream) {
+  ecc::RecArgs a;
+  const int st = check_recurrence(a, x, gate, dtype, batch, steps, channels, lengths, ws, ws_bytes);
+  if (st != ECC_OK) return st;
+  if (!h) return fail(ECC_E_NULL, "h is NULL");
+  if (!last) return fail(ECC_E_NULL, "last is NULL");
+  a.state = state;
+  a.h = h;
+  a.last = last;
+  a.saved = saved;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (dtype == ECC_T_F32) return hip_status(ecc::launch_recurrence_fwd<float>(a, s));
+  if (dtype == ECC_T_F16) return hip_status(ecc::launch_recurrence_fwd<ecc::f16>(a, s));
+  return hip_status(ecc::launch_recurrence_fwd<ecc::bf16>(a, s));
+}
+
+int ecc_gated_recurrence_bwd(const void* x, const void* gate, int dtype, int64_t batch, int64_t steps, int64_t channels,
+                             const int64_t* lengths, const float* saved, const void* grad_h, const float* grad_last,
+                             void* grad_x, void* grad_gate, float* grad_state, void* ws, size_t ws_bytes, void* stream) {
+  ecc::RecArgs a;
+  const int st = check_recurrence(a, x, gate, dtype, batch, steps, channels, lengths, ws, ws_bytes);
+  if (st != ECC_OK) return st;
+  if (!saved) return fail(ECC_E_NULL, "saved is NULL");
+  if (!grad_h && !grad_last) return fail(ECC_E_NULL, "grad_h and grad_last are both NULL");
+  if (!grad_x && !grad_gate && !grad_state) return fail(ECC_E_NULL, "every gradient is NULL");
+  a.saved = const_cast<float*>(saved);
+  a.gh = grad_h;
+  a.glast = grad_last;
+  a.gx = grad_x;
+  a.ggate = grad_gate;
+  a.gstate = grad_state;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (dtype == ECC_T_F32) return hip_status(ecc::launch_recurrence_bwd<float>(a, s));
+  if (dtype == ECC_T_F16) return hip_status(ecc::launch_recurrence_bwd<ecc::f16>(a, s));
+  return hip_status(ecc::launch_recurrence_bwd<ecc::bf16>(a, s));
 }
 
 }  // extern "C"

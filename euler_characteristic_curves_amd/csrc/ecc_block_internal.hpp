@@ -91,4 +91,63 @@ inline size_t res_workspace_bytes(int64_t batch, int64_t inner, int64_t channels
 hipError_t launch_residual_fwd(const ResArgs& a, hipStream_t stream);
 hipError_t launch_residual_bwd(const ResArgs& a, hipStream_t stream);
 
+// -------------------------------------------------------- gated recurrence
+struct RecArgs {
+  const void* x;
+  const void* gate;
+  int64_t batch, steps, channels;
+  const float* state;       // null: 0
+  const int64_t* lengths;   // null: all steps
+  void* h;
+  float* last;
+  float* saved;       // [batch][tiles][channels]: the state before every tile; null: not kept
+  const void* gh;     // null: 0
+  const float* glast;  // null: 0
+  void *gx, *ggate;
+  float* gstate;      // null: not wanted
+  void* ws;
+};
+
+// A workgroup of 256 threads has L lanes of V channels and G = 256 / L groups of
+// them, each with R steps of a tile, and takes `per` tiles one after the other.
+struct RecShape {
+  int V, R, L, G;
+  int64_t blocks;       // workgroups across the channels
+  int64_t tiles, per, segments;
+};
+inline RecShape rec_shape(int64_t batch, int64_t steps, int64_t channels, bool half) {
+  RecShape s{};
+  s.V = channels >= 2 ? 2 : 1;
+  s.R = steps <= 4 ? 1 : (half ? 16 : 8);
+  // lanes that leave few idle ones over the channels, wide where two are alike
+  int64_t least = INT64_MAX;
+  for (int L = 64; L >= 8; L /= 2) {
+    const int64_t across = (int64_t)L * s.V, blocks = (channels + across - 1) / across;
+    if (blocks * across < least) {
+      least = blocks * across;
+      s.L = L;
+      s.blocks = blocks;
+    }
+  }
+  s.G = 256 / s.L;
+  const int64_t tile = (int64_t)s.G * s.R, base = batch * s.blocks;
+  s.tiles = (steps + tile - 1) / tile;
+  // with a workgroup for every CU a sequence is taken whole; with fewer, its
+  // parts are summed up in a pass of their own and then run side by side
+  const int64_t want = base >= 256 ? 1 : (1024 + base - 1) / base;
+  s.per = (s.tiles + want - 1) / want;
+  s.segments = (s.tiles + s.per - 1) / s.per;
+  return s;
+}
+// Workspace: 3 float32 per channel for every part.
+inline size_t rec_workspace_bytes(int64_t batch, int64_t steps, int64_t channels, bool half) {
+  const RecShape s = rec_shape(batch, steps, channels, half);
+  return s.segments > 1 ? (size_t)(batch * s.segments * 3 * channels) * sizeof(float) + 256 : 256;
+}
+
+template <class T>
+hipError_t launch_recurrence_fwd(const RecArgs& a, hipStream_t stream);
+template <class T>
+hipError_t launch_recurrence_bwd(const RecArgs& a, hipStream_t stream);
+
 }  // namespace ecc

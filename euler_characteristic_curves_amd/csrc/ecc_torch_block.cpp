@@ -193,6 +193,108 @@ variable_list residual_norm(const at::Tensor& x, const Optional& b, const Option
   return residual_forward(p, dense(x), dense(b), dense(g), dense(w), dense(bw), nullptr);
 }
 
+// -------------------------------------------------------- gated recurrence
+struct RecPlan {
+  int64_t batch, steps, channels, dtype;
+};
+
+// Tensors are contiguous, absent ones undefined.
+variable_list recurrence_forward(const RecPlan& p, const at::Tensor& x, const at::Tensor& f, const at::Tensor& s,
+                                 const at::Tensor& n, at::Tensor* keep) {
+  const c10::DeviceGuard guard(x.device());
+  const auto f32 = x.options().dtype(at::kFloat).requires_grad(false);
+  at::Tensor h = result_like(x), last = at::empty({p.batch, p.channels}, f32);
+  if (!x.numel()) {
+    if (s.defined())
+      last.copy_(s);
+    else
+      last.zero_();
+    return {h, last};
+  }
+  const int64_t bytes = ecc_gated_recurrence_workspace_bytes(p.batch, p.steps, p.channels, (int)p.dtype);
+  const int64_t saved = ecc_gated_recurrence_saved_bytes(p.batch, p.steps, p.channels, (int)p.dtype);
+  if (keep) *keep = at::empty({saved / 4}, f32);
+  at::Tensor ws = bytes_like(x, bytes);
+  check(ecc_gated_recurrence_fwd(ptr(x), ptr(f), (int)p.dtype, p.batch, p.steps, p.channels,
+                                 s.defined() ? s.const_data_ptr<float>() : nullptr,
+                                 n.defined() ? n.const_data_ptr<int64_t>() : nullptr, h.data_ptr(), last.data_ptr<float>(),
+                                 keep ? keep->data_ptr<float>() : nullptr, ws.data_ptr(), bytes, stream_of(x)),
+        "ecc_gated_recurrence_fwd");
+  return {h, last};
+}
+
+struct Recurrence : torch::autograd::Function<Recurrence> {
+  static variable_list forward(AutogradContext* ctx, const at::Tensor& x, const at::Tensor& f, const Optional& s,
+                               const Optional& n, const RecPlan& p) {
+    at::Tensor keep;
+    variable_list out = recurrence_forward(p, dense(x), dense(f), dense(s), dense(n), &keep);
+    ctx->set_materialize_grads(false);
+    ctx->save_for_backward({x, f, s.value_or(at::Tensor()), n.value_or(at::Tensor()), keep});
+    ctx->saved_data["plan"] = std::vector<int64_t>{p.batch, p.steps, p.channels, p.dtype};
+    return out;
+  }
+
+  static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+    const std::vector<int64_t> p = ctx->saved_data["plan"].toIntVector();
+    const bool again = at::GradMode::is_enabled();
+    at::AutoGradMode off(false);
+    const variable_list saved = ctx->get_saved_variables();
+    if (capturing())
+      for (const at::Tensor& t : saved) refuse_foreign_capture(t);
+    variable_list in(3), wanted(3), out(5);
+    for (int i = 0; i < 3; ++i) in[i] = dense(saved[i]);
+    const at::Tensor &x = in[0], n = dense(saved[3]), gh = dense(grads[0]), gl = dense(grads[1]);
+    const c10::DeviceGuard guard(x.device());
+    const bool nothing = !x.numel() || (!gh.defined() && !gl.defined());
+    const bool any = gradients(ctx, in, wanted, nothing);
+    if (nothing && wanted[2].defined() && gl.defined()) wanted[2].copy_(gl);  // no steps: the state is the last one
+    if (any && !nothing) {
+      const int64_t bytes = ecc_gated_recurrence_workspace_bytes(p[0], p[1], p[2], (int)p[3]);
+      at::Tensor ws = bytes_like(x, bytes);
+      check(ecc_gated_recurrence_bwd(ptr(x), ptr(in[1]), (int)p[3], p[0], p[1], p[2],
+                                     n.defined() ? n.const_data_ptr<int64_t>() : nullptr, saved[4].const_data_ptr<float>(),
+                                     ptr(gh), gl.defined() ? gl.const_data_ptr<float>() : nullptr, out_ptr(wanted[0]),
+                                     out_ptr(wanted[1]), wanted[2].defined() ? wanted[2].data_ptr<float>() : nullptr,
+                                     ws.data_ptr(), bytes, stream_of(x)),
+            "ecc_gated_recurrence_bwd");
+    }
+    for (int i = 0; i < 3; ++i) out[i] = wanted[i];
+    if (again && any) return once_only(out, "gated recurrence");
+    return out;
+  }
+};
+
+std::tuple<at::Tensor, at::Tensor> gated_recurrence(const at::Tensor& x, const at::Tensor& f, const Optional& s,
+                                                    const Optional& n) {
+  const pybind11::gil_scoped_release nogil;
+  features(x, "x");
+  TORCH_CHECK_VALUE(x.dim() == 3, "x must be [batch, steps, channels] (got ", x.sizes(), ")");
+  TORCH_CHECK_VALUE(x.size(2) >= 1, "x has no channels");
+  const c10::Device where = x.device();
+  on_device(f, "gate", &where);
+  TORCH_CHECK_TYPE(f.scalar_type() == x.scalar_type(), "gate must be ", x.scalar_type(), " (got ", f.scalar_type(), ")");
+  TORCH_CHECK_VALUE(f.sizes() == x.sizes(), "gate must have x's shape ", x.sizes(), " (got ", f.sizes(), ")");
+  const RecPlan p{x.size(0), x.size(1), x.size(2), type_of(x.scalar_type())};
+  if (s) {
+    on_device(*s, "state", &where);
+    TORCH_CHECK_TYPE(s->scalar_type() == at::kFloat, "state must be torch.float32 (got ", s->scalar_type(), ")");
+    TORCH_CHECK_VALUE(s->dim() == 2 && s->size(0) == p.batch && s->size(1) == p.channels, "state must be [", p.batch, ", ",
+                      p.channels, "] (got ", s->sizes(), ")");
+  }
+  if (n) {
+    on_device(*n, "lengths", &where);
+    TORCH_CHECK_TYPE(n->scalar_type() == at::kLong, "lengths must be torch.int64 (got ", n->scalar_type(), ")");
+    TORCH_CHECK_VALUE(n->dim() == 1 && n->size(0) == p.batch, "lengths must be [", p.batch, "] (got ", n->sizes(), ")");
+  }
+  TORCH_CHECK_NOT_IMPLEMENTED(!is_dual(x) && !is_dual(f) && !is_dual(s), "gated recurrence has no forward-mode derivative");
+  variable_list out;
+  if (at::GradMode::is_enabled() && (x.requires_grad() || f.requires_grad() || wants(s)))
+    out = Recurrence::apply(x, f, s, n, p);
+  else
+    out = recurrence_forward(p, dense(x), dense(f), dense(s), dense(n), nullptr);
+  return {out[0], out[1]};
+}
+
 }  // namespace
 
 void define_block(pybind11::module_& m) {
@@ -201,6 +303,7 @@ void define_block(pybind11::module_& m) {
     const variable_list out = residual_norm(x, b, g, w, bw, scale, eps, norm_branch, std::nullopt);
     return std::make_tuple(out[0], out[1]);
   });
+  m.def("gated_recurrence", &gated_recurrence);
   m.def("rms_norm", [](const at::Tensor& x, const Optional& w, double eps, const std::optional<at::ScalarType>& dtype) {
     return residual_norm(x, std::nullopt, std::nullopt, w, std::nullopt, 1.0, eps, false, dtype)[0];
   });

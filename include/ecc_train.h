@@ -4,7 +4,8 @@
  * channels-last features, the same norm read out to the scalar grid a curve
  * takes, Newton-Schulz orthogonalisation, and the momentum update built on it;
  * and those of a residual block over curves or other channels-last features:
- * the norms around a block with its gate and residual scale.
+ * the norms around a block with its gate and residual scale, and a gated
+ * linear recurrence along the steps of a sequence.
  *
  * Conventions are those of ecc.h (device pointers owned by the caller, work
  * enqueued on `stream`, status codes, ecc_last_error), except the workspace:
@@ -194,6 +195,41 @@ int ecc_residual_norm_bwd(const void* x, int xdtype, const void* branch, int dty
 
 /* Workspace bytes of the backward pass (0 for invalid sizes). */
 size_t ecc_residual_norm_workspace_bytes(int64_t batch, int64_t inner, int64_t channels, int gate_per_sample);
+
+/*
+ * The gated linear recurrence along a sequence's steps (the thresholds of a
+ * curve, say): with k_t = 1 / (1 + exp(-gate_t)),
+ *   h_t = k_t h_(t-1) + (1 - k_t) x_t,  h_(-1) = state, for every channel.
+ *   x, gate  device, dtype elements, [batch][steps][channels]
+ *   state    device float32 [batch][channels]; NULL stands for 0
+ *   lengths  device int64 [batch], or NULL: sequence b has the steps before
+ *            lengths[b] (taken as 0 below it and as `steps` beyond them); x and
+ *            gate behind them are not read, h there is 0
+ *   h        dtype, x's shape
+ *   last     float32 [batch][channels]: the state after the last step (the
+ *            initial one where there is none), to be carried to a next call
+ *   saved    float32, ecc_gated_recurrence_saved_bytes: states that the backward
+ *            pass starts from; NULL where there will be none
+ * No output overlaps an input.  States are float32.  One launch, two where batch x channels is small
+ * beside the card and the sequence is cut into parts.
+ */
+int ecc_gated_recurrence_fwd(const void* x, const void* gate, int dtype, int64_t batch, int64_t steps, int64_t channels,
+                             const float* state, const int64_t* lengths, void* h, float* last, float* saved, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/*
+ * Its backward pass.  grad_h (dtype; not read behind a sequence's length) and
+ * grad_last (float32): either may be NULL (0).  grad_x, grad_gate (dtype; 0
+ * behind a sequence's length) and grad_state (float32) are OVERWRITTEN; each may
+ * be NULL (not wanted), but not all of them.
+ */
+int ecc_gated_recurrence_bwd(const void* x, const void* gate, int dtype, int64_t batch, int64_t steps, int64_t channels,
+                             const int64_t* lengths, const float* saved, const void* grad_h, const float* grad_last,
+                             void* grad_x, void* grad_gate, float* grad_state, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of the two calls above, and the bytes of `saved` (0 for invalid sizes). */
+size_t ecc_gated_recurrence_workspace_bytes(int64_t batch, int64_t steps, int64_t channels, int dtype);
+size_t ecc_gated_recurrence_saved_bytes(int64_t batch, int64_t steps, int64_t channels, int dtype);
 
 #ifdef __cplusplus
 }

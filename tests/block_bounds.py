@@ -97,3 +97,56 @@ def residual(x, branch, gate=None, weight=None, branch_weight=None, norm_branch=
         db_ = rb * inner_ + 3 * E * db.abs()
     out["branch"] = (db.reshape(shape), rounded(db, db_, branch.dtype).reshape(shape))
     return out
+
+
+def recurrence(x, gate, state=None, lengths=None, gh=None, glast=None):
+    """{name: (value, bound)} of gated_recurrence and, with gh or glast, of every gradient.
+
+    m, the smaller of k and 1 - k, is off by (3 |gate| + 8) E relative: half a step of the exponent's two factors, |gate| E
+    each and doubled by the sum 1 + e at most half, and a step or half of one for the exponential, the sum, the reciprocal
+    and the product.  A step adds that share of what m multiplies, |x| + |h| at most, and roundings of the state: its own,
+    those of the run that it is part of and of the joins, 8 E together.  Errors pass on as states do, by k; magnitudes H
+    of states are those of the sums of absolute values."""
+    xd, f = x.detach().double().cpu(), gate.detach().double().cpu()
+    B, T, C = xd.shape
+    n = torch.full((B,), T) if lengths is None else lengths.cpu().clamp(0, T)
+    inside = (torch.arange(T)[None] < n[:, None])[..., None]
+    xd, f = torch.where(inside, xd, 0.0), torch.where(inside, f, 0.0)
+    k, blend = torch.where(inside, torch.sigmoid(f), 1.0), torch.where(inside, torch.sigmoid(-f), 0.0)
+    m = torch.minimum(k, blend)
+    rel = (3 * f.abs() + 8) * E
+    h = torch.zeros(B, C, dtype=torch.float64) if state is None else state.detach().double().cpu()
+    H, err = h.abs(), torch.zeros_like(h)
+    before, before_, out, out_ = (torch.empty_like(xd) for _ in range(4))
+    for t in range(T):
+        before[:, t], before_[:, t] = h, err
+        local = (rel[:, t] + 2 * E) * m[:, t] * (xd[:, t].abs() + H)
+        h = k[:, t] * h + blend[:, t] * xd[:, t]
+        H = k[:, t] * H + blend[:, t] * xd[:, t].abs()
+        err = k[:, t] * err + local + 8 * E * H + 2.0 ** -126
+        out[:, t], out_[:, t] = h, err
+    res = {"h": (torch.where(inside, out, 0.0), torch.where(inside, rounded(out, out_, x.dtype), 0.0) + 1e-300),
+           "last": (h, err + 1e-300)}
+    if gh is None and glast is None:
+        return res
+    d = torch.zeros_like(xd) if gh is None else torch.where(inside, gh.detach().double().cpu(), 0.0)
+    e = torch.zeros(B, C, dtype=torch.float64) if glast is None else glast.detach().double().cpu()
+    G, e_ = e.abs(), torch.zeros_like(e)
+    D, D_ = torch.empty_like(xd), torch.empty_like(xd)
+    for t in range(T - 1, -1, -1):
+        G = d[:, t].abs() + G
+        D[:, t] = d[:, t] + e
+        D_[:, t] = e_ + 2 * E * G
+        local = (rel[:, t] + 2 * E) * m[:, t] * G + 8 * E * k[:, t] * G
+        e, G = k[:, t] * D[:, t], k[:, t] * G
+        e_ = k[:, t] * D_[:, t] + local + 2.0 ** -126
+    dx = blend * D
+    dx_ = blend * D_ + (rel + 2 * E) * m * D.abs() + 2 * E * dx.abs()
+    diff, kb = before - xd, k * blend
+    df = D * diff * kb
+    df_ = kb * diff.abs() * D_ + kb * D.abs() * (before_ + E * diff.abs()) + df.abs() * (2 * rel + 6 * E)
+    for name, v, b in (("x", dx, dx_), ("gate", df, df_)):
+        res[name] = (torch.where(inside, v, 0.0), torch.where(inside, rounded(v, b, x.dtype), 0.0) + 1e-300)
+    if state is not None:
+        res["state"] = (e, e_ + 1e-300)
+    return res
