@@ -22,7 +22,7 @@ _API = (
 
 _TRAIN_API = ("group_norm_act", "group_norm_readout", "orthogonalize", "muon_step")
 
-_BLOCK_API = ("residual_norm", "rms_norm", "gated_recurrence")
+_BLOCK_API = ("residual_norm", "rms_norm", "gated_linear", "gated_recurrence")
 
 __all__ = list(_API + _TRAIN_API + _BLOCK_API)
 

@@ -7,11 +7,11 @@ Scratch comes from torch's allocator per call, so calls may run on any stream an
 tensors are copied once.  Forward-mode derivatives are refused, and gradients of gradients raise an error.
 """
 
-from . import _lib  # noqa: F401  (loads the library that the binding needs)
 from . import _torch
 from ._lib import EccError
+from .train import _ACTS
 
-__all__ = ["residual_norm", "rms_norm", "gated_recurrence", "EccError"]
+__all__ = ["residual_norm", "rms_norm", "gated_linear", "gated_recurrence", "EccError"]
 
 
 def residual_norm(x, branch, gate=None, weight=None, branch_weight=None, norm_branch=True, scale=1.0, eps=1e-6):
@@ -37,6 +37,21 @@ def rms_norm(x, weight=None, eps=1e-6, dtype=None):
     have a 16-bit result.  Differentiable in x and weight.
     """
     return _torch.rms_norm(x, weight, eps, dtype)
+
+
+def gated_linear(x, w_gate, w_up, b_gate=None, b_up=None, act="silu"):
+    """Both projections of a gated feed-forward block, the activation and their product:
+
+        h = act(x @ w_gate.T + b_gate) * (x @ w_up.T + b_up)
+
+    x: float32, float16 or bfloat16 [*space, channels]; w_gate, w_up: [hidden, channels]; b_gate, b_up: [hidden] or None;
+    all of x's type; act: "none", "relu", "silu" or "gelu".  Returns [*space, hidden], like x.  Sums are float32; the
+    backward pass forms the projections again, so that nothing but the arguments is kept.  Differentiable in all five
+    tensors (see include/ecc_train.h).
+    """
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)} (got {act!r})")
+    return _torch.gated_linear(x, w_gate, w_up, b_gate, b_up, _ACTS[act])
 
 
 def gated_recurrence(x, gate, state=None, lengths=None):

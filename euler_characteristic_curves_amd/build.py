@@ -23,7 +23,8 @@ LIB = os.path.join(PKG, "libecc_mi355.so")
 
 SOURCES = ["ecc_api.cpp", "ecc_hard.hip", "ecc_soft.hip", "ecc_soft_grad.hip", "ecc_height.hip", "ecc_static.hip",
            "ecc_train_api.cpp", "ecc_norm_f32.hip", "ecc_norm_f16.hip", "ecc_norm_bf16.hip", "ecc_orth.hip", "ecc_orth_long.hip",
-           "ecc_orth_thin_f32.hip", "ecc_orth_thin_f16.hip", "ecc_orth_thin_bf16.hip", "ecc_block_api.cpp", "ecc_residual.hip", "ecc_recurrence.hip"]
+           "ecc_orth_thin_f32.hip", "ecc_orth_thin_f16.hip", "ecc_orth_thin_bf16.hip", "ecc_block_api.cpp",
+           "ecc_residual.hip", "ecc_recurrence.hip", "ecc_glu_f32.hip", "ecc_glu_f16.hip", "ecc_glu_bf16.hip"]
 RATE_SOURCE = "ecc_sigmoid_rate.hip"
 RATE_LIB = os.path.join(PKG, "libecc_sigmoid_rate.so")
 TORCH_SOURCES = ["ecc_torch.cpp", "ecc_torch_block.cpp"]

@@ -94,6 +94,41 @@ int check_recurrence(ecc::RecArgs& a, const void* x, const void* gate, int dtype
   return check_workspace(ws, ws_bytes, ecc::rec_workspace_bytes(batch, steps, channels, dtype != ECC_T_F32));
 }
 
+int check_glu_shape(int64_t rows, int64_t channels, int64_t hidden, int dtype) {
+  if (!is_dtype(dtype)) return fail(ECC_E_DTYPE, "dtype %lld is not one of ECC_T_*", dtype);
+  if (rows < 1 || channels < 1 || hidden < 1)
+    return fail(ECC_E_SHAPE, "rows, channels and hidden must be >= 1 (got channels=%lld hidden=%lld)", channels, hidden);
+  if (channels > ECC_MAX_MATRIX || hidden > ECC_MAX_MATRIX)
+    return fail(ECC_E_SHAPE, "weights of %lld x %lld exceed the limit per side", hidden, channels);
+  const int64_t wide = channels > hidden ? channels : hidden;
+  if (rows > ECC_MAX_VOXELS / wide) return fail(ECC_E_SHAPE, "more than 2^40 elements");
+  // tiles of 64 rows in one launch
+  if ((rows + 63) / 64 > INT32_MAX / ((wide + 63) / 64)) return fail(ECC_E_SHAPE, "rows=%lld are too many for one launch", rows);
+  return ECC_OK;
+}
+
+int check_glu(ecc::GluArgs& a, const void* x, int dtype, int64_t rows, int64_t channels, int64_t hidden, const void* w_gate,
+              const void* w_up, const void* b_gate, const void* b_up, int act) {
+  ecc::set_error("");
+  if (!x) return fail(ECC_E_NULL, "x is NULL");
+  if (!w_gate) return fail(ECC_E_NULL, "w_gate is NULL");
+  if (!w_up) return fail(ECC_E_NULL, "w_up is NULL");
+  if (act < ECC_ACT_NONE || act > ECC_ACT_GELU) return fail(ECC_E_ACT, "act %lld is not one of ECC_ACT_*", act);
+  const int st = check_glu_shape(rows, channels, hidden, dtype);
+  if (st != ECC_OK) return st;
+  a = ecc::GluArgs{};
+  a.x = x;
+  a.wg = w_gate;
+  a.wu = w_up;
+  a.bg = b_gate;
+  a.bu = b_up;
+  a.act = act;
+  a.rows = rows;
+  a.channels = channels;
+  a.hidden = hidden;
+  return ECC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -198,6 +233,51 @@ int ecc_gated_recurrence_bwd(const void* x, const void* gate, int dtype, int64_t
   if (dtype == ECC_T_F32) return hip_status(ecc::launch_recurrence_bwd<float>(a, s));
   if (dtype == ECC_T_F16) return hip_status(ecc::launch_recurrence_bwd<ecc::f16>(a, s));
   return hip_status(ecc::launch_recurrence_bwd<ecc::bf16>(a, s));
+}
+
+size_t ecc_gated_linear_workspace_bytes(int64_t rows, int64_t channels, int64_t hidden, int dtype) {
+  if (check_glu_shape(rows, channels, hidden, dtype) != ECC_OK) return 0;
+  return ecc::glu_plan(rows, channels, hidden, dtype == ECC_T_F32 ? 4 : 2).bytes;
+}
+
+int ecc_gated_linear_fwd(const void* x, int dtype, int64_t rows, int64_t channels, int64_t hidden, const void* w_gate,
+                         const void* w_up, const void* b_gate, const void* b_up, int act, void* h, void* stream) {
+  ecc::GluArgs a;
+  const int st = check_glu(a, x, dtype, rows, channels, hidden, w_gate, w_up, b_gate, b_up, act);
+  if (st != ECC_OK) return st;
+  if (!h) return fail(ECC_E_NULL, "h is NULL");
+  a.h = h;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (dtype == ECC_T_F32) return hip_status(ecc::launch_glu_fwd<float>(a, s));
+  if (dtype == ECC_T_F16) return hip_status(ecc::launch_glu_fwd<ecc::f16>(a, s));
+  return hip_status(ecc::launch_glu_fwd<ecc::bf16>(a, s));
+}
+
+int ecc_gated_linear_bwd(const void* x, int dtype, int64_t rows, int64_t channels, int64_t hidden, const void* w_gate,
+                         const void* w_up, const void* b_gate, const void* b_up, int act, const void* grad_h, void* grad_x,
+                         void* grad_w_gate, void* grad_w_up, void* grad_b_gate, void* grad_b_up, void* ws, size_t ws_bytes,
+                         void* stream) {
+  ecc::GluArgs a;
+  int st = check_glu(a, x, dtype, rows, channels, hidden, w_gate, w_up, b_gate, b_up, act);
+  if (st != ECC_OK) return st;
+  if (!grad_h) return fail(ECC_E_NULL, "grad_h is NULL");
+  if (!grad_x && !grad_w_gate && !grad_w_up && !grad_b_gate && !grad_b_up)
+    return fail(ECC_E_NULL, "every gradient is NULL");
+  if ((grad_b_gate && !b_gate) || (grad_b_up && !b_up))
+    return fail(ECC_E_NULL, "a gradient of an argument that is NULL is wanted");
+  st = check_workspace(ws, ws_bytes, ecc::glu_plan(rows, channels, hidden, dtype == ECC_T_F32 ? 4 : 2).bytes);
+  if (st != ECC_OK) return st;
+  a.gh = grad_h;
+  a.gx = grad_x;
+  a.gwg = grad_w_gate;
+  a.gwu = grad_w_up;
+  a.gbg = grad_b_gate;
+  a.gbu = grad_b_up;
+  a.ws = ws;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (dtype == ECC_T_F32) return hip_status(ecc::launch_glu_bwd<float>(a, s));
+  if (dtype == ECC_T_F16) return hip_status(ecc::launch_glu_bwd<ecc::f16>(a, s));
+  return hip_status(ecc::launch_glu_bwd<ecc::bf16>(a, s));
 }
 
 }  // extern "C"

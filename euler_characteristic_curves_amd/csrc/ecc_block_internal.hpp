@@ -150,4 +150,87 @@ hipError_t launch_recurrence_fwd(const RecArgs& a, hipStream_t stream);
 template <class T>
 hipError_t launch_recurrence_bwd(const RecArgs& a, hipStream_t stream);
 
+// ------------------------------------------- gated pair of projections
+struct GluArgs {
+  const void* x;          // [rows][channels]
+  const void *wg, *wu;    // [hidden][channels]
+  const void *bg, *bu;    // [hidden], null: 0
+  int act;
+  int64_t rows, channels, hidden;
+  void* h;                // [rows][hidden]
+  const void* gh;         // [rows][hidden]
+  void *gx, *gwg, *gwu, *gbg, *gbu;  // each may be null
+  void* ws;
+};
+
+// A product's workgroups: tiles of 64 FM x 64 FN results, each shared by
+// `splits` workgroups along the summed axis.
+struct GluShare {
+  int FM, FN;
+  int64_t tiles_m, tiles_n;
+  int splits;
+};
+// Rows that one float32 sum runs over, at most.
+constexpr int64_t kGluRun = 16384;
+// m x n results of sums over k; `both` counts the matrices of the launch.  Large
+// tiles where there are enough of them (or of their shares) for the card.
+inline GluShare glu_share(int64_t m, int64_t n, int64_t k, int both, int step, bool can_split) {
+  GluShare s{};
+  const auto tiles = [&](int fm, int fn) { return ((m + 64 * fm - 1) / (64 * fm)) * ((n + 64 * fn - 1) / (64 * fn)) * both; };
+  const int64_t steps = (k + step - 1) / step;
+  const int64_t shares = can_split ? (steps / 16 > 1 ? steps / 16 : 1) : 1;
+  const bool large = tiles(4, 2) * (shares < 64 ? shares : 64) >= 192 && m > 128;
+  s.FM = large ? 4 : 1;
+  s.FN = 2;
+  s.tiles_m = (m + 64 * s.FM - 1) / (64 * s.FM);
+  s.tiles_n = (n + 64 * s.FN - 1) / (64 * s.FN);
+  int64_t splits = 1;
+  if (can_split) {
+    const int64_t all = s.tiles_m * s.tiles_n * both, most = steps / 8 > 1 ? steps / 8 : 1;
+    splits = all < 512 ? 512 / all : 1;
+    splits = splits < most ? splits : most;
+    const int64_t least = (k + kGluRun - 1) / kGluRun;
+    splits = splits > least ? splits : least;
+  }
+  s.splits = (int)splits;
+  return s;
+}
+inline size_t glu_part_bytes(const GluShare& s, int both) {
+  return s.splits > 1 ? (size_t)(s.tiles_m * s.tiles_n * both * s.splits) * (size_t)(64 * s.FM * 64 * s.FN) * sizeof(float) : 0;
+}
+
+// Workspace of the backward pass: the gradients of both projections (rows of
+// 2 x pitch elements), partial sums of the bias gradients, shares of products.
+struct GluPlan {
+  int64_t pitch;  // elements from the gate's gradients to the other's
+  GluShare gates, input, weight;
+  size_t at_bias, at_part, bytes;
+};
+inline GluPlan glu_plan(int64_t rows, int64_t channels, int64_t hidden, int elem) {
+  GluPlan p{};
+  const int step = 64 / elem;  // elements of a step along the summed axis
+  p.pitch = (hidden + 63) / 64 * 64;
+  p.gates = glu_share(rows, 2 * hidden, channels, 1, step, false);
+  p.gates.tiles_n = (hidden + 63) / 64;  // 64 of both projections a tile
+  p.input = glu_share(rows, channels, 2 * hidden, 1, step, true);
+  p.weight = glu_share(hidden, channels, rows, 2, step, true);
+  size_t at = (size_t)rows * 2 * p.pitch * elem;
+  const auto take = [&at](size_t bytes) {
+    at = (at + 255) & ~(size_t)255;
+    const size_t here = at;
+    at += bytes;
+    return here;
+  };
+  p.at_bias = take((size_t)p.gates.tiles_m * 2 * p.pitch * sizeof(float));
+  const size_t a = glu_part_bytes(p.input, 1), b = glu_part_bytes(p.weight, 2);
+  p.at_part = take(a > b ? a : b);
+  p.bytes = (at + 255) & ~(size_t)255;
+  return p;
+}
+
+template <class T>
+hipError_t launch_glu_fwd(const GluArgs& a, hipStream_t stream);
+template <class T>
+hipError_t launch_glu_bwd(const GluArgs& a, hipStream_t stream);
+
 }  // namespace ecc

@@ -1,0 +1,468 @@
+// The gated pair of projections of a feed-forward block (contract:
+// include/ecc_train.h), included by one source per element type.
+//
+//   a = x Wg^T + bg,  b = x Wu^T + bu,  h = act(a) b.
+// Backwards, from a and b formed anew,
+//   da = dh b act'(a),  db = dh act(a),
+//   dx = da Wg + db Wu,  dWg = da^T x,  dWu = db^T x,  dbg = sum da,  dbu = sum db.
+//
+// All of it is products of matrices on the matrix unit: tiles of 64 FM x 64 FN
+// results a workgroup of four waves, steps of 64 bytes along the summed axis
+// through LDS, float32 sums.  A tile of the forward product holds the same 64
+// hidden units of both projections, so activation and product are its epilogue;
+// the backward one's is da and db, rounded once to the element type (they are
+// the next products' operands) and written to the workspace.
+//
+// Operands of two kinds: those that lie along the summed axis, and those that
+// lie across it (the weights in dx, both operands in dW).  The second are kept
+// in LDS as they lie and turned on the way to the registers, by the transposing
+// read where elements have 16 bits.
+
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "ecc_act.hpp"
+#include "ecc_block_internal.hpp"
+
+namespace ecc {
+namespace {
+
+constexpr int kNT = 256;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+enum Kind { kForward, kGates, kInput, kWeight };
+constexpr bool is_dual(int kind) { return kind == kForward || kind == kGates; }
+// Whether the operands lie along the summed axis.
+constexpr bool a_along(int kind) { return kind != kWeight; }
+constexpr bool b_along(int kind) { return is_dual(kind); }
+
+template <class T>
+constexpr int kPer = 16 / (int)sizeof(T);  // elements of a 16-byte chunk
+template <class T>
+constexpr int kStep = 64 / (int)sizeof(T);  // elements of a step along the summed axis
+
+// One product.
+template <class T>
+struct Product {
+  const T* A;
+  int64_t pitchA, stepA;  // stepA: from one matrix, or part of the sum, to the next
+  const T* B[2];
+  int64_t pitchB;
+  int64_t M, N, K;  // N: hidden units of one projection in a dual product; K of one part of the sum
+  int parts;        // parts of the sum, A + i stepA with B[i]
+  int splits;
+  int64_t tiles_m, tiles_n;
+  float* part;
+  GluArgs a;
+  int64_t pitch;   // of the workspace's gradients
+  T* dab;
+  float* bias;     // partial sums of da and db, null: not wanted
+  T* out[2];
+  int64_t pitch_out;
+};
+
+// ---------------------------------------------------------------- loading
+// Rows (of the operand, across the sum) of a tile in LDS.  Along: rows of 64
+// bytes, four chunks, permuted so that 16 neighbouring rows at one chunk meet
+// every bank once.  Across: a row of ROWS elements for every step of the sum,
+// chunks permuted so that the rows that one read serves lie in different banks.
+template <class T, bool ALONG, int ROWS>
+struct Tile {
+  static constexpr int kChunks = ROWS / 64;                       // a thread
+  static constexpr int kLine = ROWS * (int)sizeof(T) / 16;        // chunks of a line, across
+  __device__ static __forceinline__ int permuted(int line, int chunk) {
+    if (ALONG) return chunk ^ (line >> 2 & 3);
+    if (sizeof(T) == 4) return chunk ^ (line >> 2 & 1) * 8;
+    return kLine == 8 ? chunk ^ (line >> 1 & 1) * 4 : chunk ^ (line & 3) * 4;
+  }
+  // Line (row along, summed index across) and chunk of this thread's chunk i.
+  __device__ static __forceinline__ void mine(int i, int& line, int& chunk) {
+    const int q = i * kNT + threadIdx.x, per = ALONG ? 4 : kLine;
+    line = q / per;
+    chunk = permuted(line, q % per);
+  }
+  // A chunk from anywhere, with zeros behind `n` rows and `end` along the sum.
+  __device__ static __forceinline__ u32x4 fetch(const T* p, int64_t pitch, int64_t row0, int64_t n, int64_t k0, int64_t end,
+                                                int i) {
+    int line, chunk;
+    mine(i, line, chunk);
+    const int64_t row = ALONG ? row0 + line : row0 + chunk * kPer<T>, k = ALONG ? k0 + chunk * kPer<T> : k0 + line;
+    const int64_t left = ALONG ? (row < n ? end - k : 0) : (k < end ? n - row : 0);
+    Vec<T, kPer<T>> v = {};
+    if (left > 0) {
+      const T* at = ALONG ? p + row * pitch + k : p + k * pitch + row;
+      if (left >= kPer<T>) {
+        load_vec(at, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPer<T> - 1; ++j)
+          if (j < left) v.v[j] = at[j];
+      }
+    }
+    u32x4 r;
+    __builtin_memcpy(&r, &v, 16);
+    return r;
+  }
+};
+
+// ---------------------------------------------------------------- fragments
+template <class T>
+struct Fragment {
+  u32x4 v;
+};
+
+// 32 rows from row0 on, chunks 2 s and 2 s + 1 of the step (lanes 32 and up have the second).
+template <class T, bool ALONG, int ROWS>
+__device__ __forceinline__ Fragment<T> read_fragment(const char* lds, int row0, int s) {
+  const int lane = threadIdx.x & 63, high = lane >> 5;
+  Fragment<T> f;
+  if constexpr (ALONG) {
+    const int row = row0 + (lane & 31);
+    f.v = *reinterpret_cast<const u32x4*>(lds + row * 64 + (Tile<T, ALONG, ROWS>::permuted(row, s * 2 + high) << 4));
+  } else if constexpr (sizeof(T) == 4) {
+    const int col = row0 + (lane & 31);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = s * 8 + high * 4 + j;
+      f.v[j] = *reinterpret_cast<const uint32_t*>(lds + k * (ROWS * 4) + (Tile<T, ALONG, ROWS>::permuted(k, col >> 2) << 4) +
+                                                  (col & 3) * 4);
+    }
+  } else {
+    // 16 lanes read 4 lines of 16 elements, and each gets a column of them
+    const int i = lane & 15, col = row0 + (lane & 16) + (i & 3) * 4;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int k = s * 16 + high * 8 + j * 4 + (i >> 2);
+      const char* at = lds + k * (ROWS * 2) + (Tile<T, ALONG, ROWS>::permuted(k, col >> 3) << 4) + (col & 7) * 2;
+      const s16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) s16x4*)reinterpret_cast<const s16x4*>(at));
+      __builtin_memcpy(reinterpret_cast<char*>(&f.v) + j * 8, &r, 8);
+    }
+  }
+  return f;
+}
+
+__device__ __forceinline__ f32x16 multiply(const Fragment<f16>& a, const Fragment<f16>& b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a.v), __builtin_bit_cast(f16x8, b.v), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 multiply(const Fragment<bf16>& a, const Fragment<bf16>& b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a.v), __builtin_bit_cast(bf16x8, b.v), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 multiply(const Fragment<float>& a, const Fragment<float>& b, f32x16 c) {
+  const f32x4 u = __builtin_bit_cast(f32x4, a.v), v = __builtin_bit_cast(f32x4, b.v);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(u[j], v[j], c, 0, 0, 0);
+  return c;
+}
+
+// Row within a fragment of its result r.
+__device__ __forceinline__ int result_row(int r) { return (r >> 2) * 8 + (threadIdx.x >> 5 & 1) * 4 + (r & 3); }
+
+// ---------------------------------------------------------------- epilogues
+template <class F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  if (act == kActSilu)
+    f(std::integral_constant<int, kActSilu>{});
+  else if (act == kActGelu)
+    f(std::integral_constant<int, kActGelu>{});
+  else if (act == kActRelu)
+    f(std::integral_constant<int, kActRelu>{});
+  else
+    f(std::integral_constant<int, kActNone>{});
+}
+
+// A workgroup's results: acc[i][j] is the fragment of rows wm FM 32 + 32 i.
+template <class T, int KIND, int FM, int FN>
+__device__ __forceinline__ void epilogue(const Product<T>& p, int z, int64_t tm, int64_t tn, f32x16 (&acc)[FM][FN], float* lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const int64_t row0 = tm * 64 * FM + wm * FM * 32;
+  if constexpr (is_dual(KIND)) {
+    const int64_t unit = tn * 64 + wn * 32 + (lane & 31);
+    const bool in = unit < p.N;
+    const float bg = in && p.a.bg ? (float)reinterpret_cast<const T*>(p.a.bg)[unit] : 0.0f;
+    const float bu = in && p.a.bu ? (float)reinterpret_cast<const T*>(p.a.bu)[unit] : 0.0f;
+    float sum_a = 0.0f, sum_b = 0.0f;
+    with_act(p.a.act, [&](auto act) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int64_t row = row0 + i * 32 + result_row(r);
+          if (!in || row >= p.M) continue;
+          const float a = acc[i][0][r] + bg, b = acc[i][1][r] + bu;
+          if constexpr (KIND == kForward) {
+            reinterpret_cast<T*>(p.a.h)[row * p.N + unit] = (T)(act_value<act.value>(a) * b);
+          } else {
+            const float g = (float)reinterpret_cast<const T*>(p.a.gh)[row * p.N + unit];
+            float y;
+            const float slope = act_slope<act.value>(a, y);
+            const float da = g * b * slope, db = g * y;
+            T* out = p.dab + row * 2 * p.pitch + unit;
+            out[0] = (T)da;
+            out[p.pitch] = (T)db;
+            sum_a += da;
+            sum_b += db;
+          }
+        }
+    });
+    if constexpr (KIND == kGates) {
+      if (!p.bias) return;
+      sum_a += __shfl_xor(sum_a, 32);
+      sum_b += __shfl_xor(sum_b, 32);
+      __syncthreads();  // the stages are free
+      if (wm == 1 && lane < 32) {
+        lds[wn * 32 + lane] = sum_a;
+        lds[64 + wn * 32 + lane] = sum_b;
+      }
+      __syncthreads();
+      if (wm == 0 && lane < 32 && in) {
+        float* out = p.bias + tm * 2 * p.pitch + unit;
+        out[0] = sum_a + lds[wn * 32 + lane];
+        out[p.pitch] = sum_b + lds[64 + wn * 32 + lane];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int64_t col = tn * 64 * FN + wn * FN * 32 + j * 32 + (lane & 31);
+      if (col >= p.N) continue;
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int64_t row = row0 + i * 32 + result_row(r);
+          if (row < p.M) p.out[z][row * p.pitch_out + col] = (T)acc[i][j][r];
+        }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- products
+template <class T, int KIND, int FM, int FN>
+__global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
+  constexpr int TM = 64 * FM, TN = 64 * FN, kA = TM * 64, kB = TN * 64;
+  using TileA = Tile<T, a_along(KIND), TM>;
+  using TileB = Tile<T, b_along(KIND), TN>;
+  __shared__ __align__(16) char lds[2][kA + kB];
+  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  int64_t id = blockIdx.x;
+  const int split = (int)(id % p.splits);
+  id /= p.splits;
+  const int64_t tn = id % p.tiles_n;
+  id /= p.tiles_n;
+  const int64_t tm = id % p.tiles_m;
+  const int z = KIND == kWeight ? (int)(id / p.tiles_m) : 0;
+  if (KIND == kWeight && !p.out[z]) return;  // not wanted
+  // steps of every part of the sum; this workgroup's are [from, to) of all of them
+  const int64_t each = (p.K + kStep<T> - 1) / kStep<T>, all = each * p.parts;
+  const int64_t share = (all + p.splits - 1) / p.splits, from = split * share;
+  const int64_t to = from + share < all ? from + share : all;
+  f32x16 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  u32x4 ra[TileA::kChunks], rb[TileB::kChunks];
+  const auto fetch = [&](int64_t s) {
+    const int part = KIND == kInput && s >= each ? 1 : 0;
+    const int64_t k0 = (s - part * each) * kStep<T>;
+    const T* A = p.A + (KIND == kWeight ? z : part) * p.stepA;
+#pragma unroll
+    for (int i = 0; i < TileA::kChunks; ++i) ra[i] = TileA::fetch(A, p.pitchA, tm * TM, p.M, k0, p.K, i);
+#pragma unroll
+    for (int i = 0; i < TileB::kChunks; ++i) {
+      if constexpr (is_dual(KIND))  // 64 rows of either projection: chunk i is one of rows 64 i to 64 i + 63
+        rb[i] = Tile<T, true, TN>::fetch(p.B[i] - i * 64 * p.pitchB, p.pitchB, tn * 64, p.N + i * 64, k0, p.K, i);
+      else
+        rb[i] = TileB::fetch(p.B[KIND == kInput ? part : 0], p.pitchB, tn * TN, p.N, k0, p.K, i);
+    }
+  };
+  const auto put = [&](char* to_lds) {
+#pragma unroll
+    for (int i = 0; i < TileA::kChunks; ++i) *reinterpret_cast<u32x4*>(to_lds + (i * kNT + threadIdx.x) * 16) = ra[i];
+#pragma unroll
+    for (int i = 0; i < TileB::kChunks; ++i) *reinterpret_cast<u32x4*>(to_lds + kA + (i * kNT + threadIdx.x) * 16) = rb[i];
+  };
+  if (from < to) {
+    fetch(from);
+    put(lds[0]);
+  }
+  __syncthreads();
+  for (int64_t s = from; s < to; ++s) {
+    const char* here = lds[(s - from) & 1];
+    if (s + 1 < to) fetch(s + 1);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      Fragment<T> a[FM], b[FN];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) a[i] = read_fragment<T, a_along(KIND), TM>(here, wm * FM * 32 + i * 32, c);
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        b[j] = read_fragment<T, b_along(KIND), TN>(here + kA, is_dual(KIND) ? j * 64 + wn * 32 : wn * FN * 32 + j * 32, c);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = multiply(a[i], b[j], acc[i][j]);
+    }
+    if (s + 1 < to) put(lds[(s + 1 - from) & 1]);
+    __syncthreads();
+  }
+  if (p.splits > 1) {
+    float* out = p.part + ((int64_t)blockIdx.x * kNT + threadIdx.x) * (FM * FN * 16);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f32x4 v;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = acc[i][j][q * 4 + r];
+          *reinterpret_cast<f32x4*>(out + (i * FN + j) * 16 + q * 4) = v;
+        }
+    return;
+  }
+  epilogue<T, KIND, FM, FN>(p, z, tm, tn, acc, reinterpret_cast<float*>(&lds[0][0]));
+}
+
+// Joins the shares of a tile, in order.  One fragment of four waves a workgroup.
+template <class T, int KIND, int FM, int FN>
+__global__ __launch_bounds__(kNT) void glu_join_kernel(Product<T> p) {
+  int64_t id = blockIdx.x;
+  if (!p.out[id / (p.tiles_n * p.tiles_m)]) return;
+  const int i = blockIdx.y / FN, j = blockIdx.y % FN;
+  const float* in = p.part + ((id * p.splits) * kNT + threadIdx.x) * (FM * FN * 16) + (i * FN + j) * 16;
+  float v[16] = {};
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const f32x4 u = *reinterpret_cast<const f32x4*>(in + (int64_t)s * kNT * (FM * FN * 16) + q * 4);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[q * 4 + r] += u[r];
+    }
+  }
+  const int64_t tn = id % p.tiles_n;
+  id /= p.tiles_n;
+  const int64_t tm = id % p.tiles_m;
+  const int z = (int)(id / p.tiles_m);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const int64_t col = tn * 64 * FN + wn * FN * 32 + j * 32 + (lane & 31);
+  if (col >= p.N) return;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int64_t row = tm * 64 * FM + wm * FM * 32 + i * 32 + result_row(r);
+    if (row < p.M) p.out[z][row * p.pitch_out + col] = (T)v[r];
+  }
+}
+
+// Bias gradients from the tiles' sums, in float64.  64 units a workgroup.
+template <class T>
+__global__ __launch_bounds__(kNT) void glu_bias_kernel(Product<T> p) {
+  __shared__ double lds[4][64];
+  const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
+  const int64_t unit = (int64_t)blockIdx.x * 64 + c;
+  T* out = reinterpret_cast<T*>(blockIdx.y == 0 ? p.a.gbg : p.a.gbu);
+  if (!out) return;
+  double s = 0.0;
+  if (unit < p.N)
+    for (int64_t t = r; t < p.tiles_m; t += 4) s += (double)p.bias[(t * 2 + blockIdx.y) * p.pitch + unit];
+  lds[r][c] = s;
+  __syncthreads();
+  if (r == 0 && unit < p.N) out[unit] = (T)(float)((lds[0][c] + lds[1][c]) + (lds[2][c] + lds[3][c]));
+}
+
+// ---------------------------------------------------------------- launches
+template <class T, int KIND, int FM>
+hipError_t launch_tiles(Product<T> p, hipStream_t stream) {
+  const int both = KIND == kWeight ? 2 : 1;
+  const int64_t tiles = p.tiles_m * p.tiles_n * both;
+  hipLaunchKernelGGL((glu_kernel<T, KIND, FM, 2>), dim3((unsigned)(tiles * p.splits)), dim3(kNT), 0, stream, p);
+  if constexpr (!is_dual(KIND)) {
+    if (p.splits > 1)
+      hipLaunchKernelGGL((glu_join_kernel<T, KIND, FM, 2>), dim3((unsigned)tiles, FM * 2), dim3(kNT), 0, stream, p);
+  }
+  return hipGetLastError();
+}
+template <class T, int KIND>
+hipError_t launch_product(Product<T> p, const GluShare& s, hipStream_t stream) {
+  p.splits = s.splits;
+  p.tiles_m = s.tiles_m;
+  p.tiles_n = s.tiles_n;
+  return s.FM == 4 ? launch_tiles<T, KIND, 4>(p, stream) : launch_tiles<T, KIND, 1>(p, stream);
+}
+
+template <class T>
+Product<T> projections(const GluArgs& a) {
+  Product<T> p{};
+  p.A = reinterpret_cast<const T*>(a.x);
+  p.pitchA = p.pitchB = p.K = a.channels;
+  p.B[0] = reinterpret_cast<const T*>(a.wg);
+  p.B[1] = reinterpret_cast<const T*>(a.wu);
+  p.M = a.rows;
+  p.N = a.hidden;
+  p.parts = 1;
+  p.a = a;
+  return p;
+}
+
+}  // namespace
+
+template <class T>
+hipError_t launch_glu_fwd(const GluArgs& a, hipStream_t stream) {
+  return launch_product<T, kForward>(projections<T>(a), glu_plan(a.rows, a.channels, a.hidden, sizeof(T)).gates, stream);
+}
+
+template <class T>
+hipError_t launch_glu_bwd(const GluArgs& a, hipStream_t stream) {
+  const GluPlan plan = glu_plan(a.rows, a.channels, a.hidden, sizeof(T));
+  char* ws = reinterpret_cast<char*>(a.ws);
+  Product<T> p = projections<T>(a);
+  p.pitch = plan.pitch;
+  p.dab = reinterpret_cast<T*>(ws);
+  p.bias = a.gbg || a.gbu ? reinterpret_cast<float*>(ws + plan.at_bias) : nullptr;
+  p.part = reinterpret_cast<float*>(ws + plan.at_part);
+  hipError_t st = launch_product<T, kGates>(p, plan.gates, stream);
+  if (st != hipSuccess) return st;
+  if (p.bias) {
+    p.tiles_m = plan.gates.tiles_m;
+    hipLaunchKernelGGL(glu_bias_kernel<T>, dim3((unsigned)((a.hidden + 63) / 64), 2), dim3(kNT), 0, stream, p);
+  }
+  p.A = p.dab;
+  p.pitchA = 2 * plan.pitch;
+  p.stepA = plan.pitch;
+  if (a.gx) {
+    p.N = a.channels;
+    p.K = a.hidden;
+    p.parts = 2;
+    p.out[0] = reinterpret_cast<T*>(a.gx);
+    p.pitch_out = a.channels;
+    st = launch_product<T, kInput>(p, plan.input, stream);
+    if (st != hipSuccess) return st;
+  }
+  if (a.gwg || a.gwu) {
+    p.M = a.hidden;
+    p.N = a.channels;
+    p.K = a.rows;
+    p.parts = 1;
+    p.B[0] = reinterpret_cast<const T*>(a.x);
+    p.out[0] = reinterpret_cast<T*>(a.gwg);
+    p.out[1] = reinterpret_cast<T*>(a.gwu);
+    p.pitch_out = a.channels;
+    st = launch_product<T, kWeight>(p, plan.weight, stream);
+  }
+  return st != hipSuccess ? st : hipGetLastError();
+}
+
+}  // namespace ecc

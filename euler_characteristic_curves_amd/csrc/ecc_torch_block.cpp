@@ -193,6 +193,95 @@ variable_list residual_norm(const at::Tensor& x, const Optional& b, const Option
   return residual_forward(p, dense(x), dense(b), dense(g), dense(w), dense(bw), nullptr);
 }
 
+// ------------------------------------------- gated pair of projections
+struct GluPlan {
+  int64_t rows, channels, hidden, dtype, act;
+};
+
+// Tensors are contiguous, absent ones undefined.
+at::Tensor glu_forward(const GluPlan& p, const at::Tensor& x, const at::Tensor& wg, const at::Tensor& wu, const at::Tensor& bg,
+                       const at::Tensor& bu) {
+  const c10::DeviceGuard guard(x.device());
+  std::vector<int64_t> sizes = x.sizes().vec();
+  sizes.back() = p.hidden;
+  at::Tensor h = at::empty(sizes, x.options().requires_grad(false));
+  if (h.numel())
+    check(ecc_gated_linear_fwd(ptr(x), (int)p.dtype, p.rows, p.channels, p.hidden, ptr(wg), ptr(wu), ptr(bg), ptr(bu),
+                               (int)p.act, h.data_ptr(), stream_of(x)),
+          "ecc_gated_linear_fwd");
+  return h;
+}
+
+struct Glu : torch::autograd::Function<Glu> {
+  static at::Tensor forward(AutogradContext* ctx, const at::Tensor& x, const at::Tensor& wg, const at::Tensor& wu,
+                            const Optional& bg, const Optional& bu, const GluPlan& p) {
+    at::Tensor h = glu_forward(p, dense(x), dense(wg), dense(wu), dense(bg), dense(bu));
+    ctx->save_for_backward({x, wg, wu, bg.value_or(at::Tensor()), bu.value_or(at::Tensor())});
+    ctx->saved_data["plan"] = std::vector<int64_t>{p.rows, p.channels, p.hidden, p.dtype, p.act};
+    return h;
+  }
+
+  static variable_list backward(AutogradContext* ctx, const variable_list& grads) {
+    const std::vector<int64_t> p = ctx->saved_data["plan"].toIntVector();
+    const bool again = at::GradMode::is_enabled();
+    at::AutoGradMode off(false);
+    const variable_list saved = ctx->get_saved_variables();
+    if (capturing())
+      for (const at::Tensor& t : saved) refuse_foreign_capture(t);
+    variable_list in(5), wanted(5), out(6);
+    for (int i = 0; i < 5; ++i) in[i] = dense(saved[i]);
+    const at::Tensor &x = in[0], g = dense(grads[0]);
+    const c10::DeviceGuard guard(x.device());
+    const bool any = gradients(ctx, in, wanted, !p[0]);
+    if (any && p[0]) {
+      const int64_t bytes = ecc_gated_linear_workspace_bytes(p[0], p[1], p[2], (int)p[3]);
+      at::Tensor ws = bytes_like(x, bytes);
+      check(ecc_gated_linear_bwd(ptr(x), (int)p[3], p[0], p[1], p[2], ptr(in[1]), ptr(in[2]), ptr(in[3]), ptr(in[4]),
+                                 (int)p[4], ptr(g), out_ptr(wanted[0]), out_ptr(wanted[1]), out_ptr(wanted[2]),
+                                 out_ptr(wanted[3]), out_ptr(wanted[4]), ws.data_ptr(), bytes, stream_of(x)),
+            "ecc_gated_linear_bwd");
+    }
+    for (int i = 0; i < 5; ++i) out[i] = wanted[i];
+    if (again && any) return once_only(out, "gated linear");
+    return out;
+  }
+};
+
+at::Tensor gated_linear(const at::Tensor& x, const at::Tensor& wg, const at::Tensor& wu, const Optional& bg,
+                        const Optional& bu, int64_t act) {
+  const pybind11::gil_scoped_release nogil;
+  features(x, "x");
+  TORCH_CHECK_VALUE(x.dim() >= 1, "x must be [*space, channels]");
+  const c10::Device where = x.device();
+  GluPlan p{};
+  p.channels = x.size(-1);
+  TORCH_CHECK_VALUE(p.channels >= 1, "x has no channels");
+  p.rows = x.numel() / p.channels;
+  p.dtype = type_of(x.scalar_type());
+  p.act = act;
+  const auto like = [&](const Optional& t, const char* name, int64_t dim) {
+    if (!t) return;
+    on_device(*t, name, &where);
+    TORCH_CHECK_TYPE(t->scalar_type() == x.scalar_type(), name, " must be ", x.scalar_type(), " (got ", t->scalar_type(), ")");
+    TORCH_CHECK_VALUE(t->dim() == dim, name, " must be ", dim == 2 ? "[hidden, channels]" : "[hidden]", " (got ", t->sizes(), ")");
+  };
+  like(wg, "w_gate", 2);
+  like(wu, "w_up", 2);
+  like(bg, "b_gate", 1);
+  like(bu, "b_up", 1);
+  p.hidden = wg.size(0);
+  TORCH_CHECK_VALUE(p.hidden >= 1 && wg.size(1) == p.channels, "w_gate must be [hidden, ", p.channels, "] (got ", wg.sizes(), ")");
+  TORCH_CHECK_VALUE(wu.sizes() == wg.sizes(), "w_up must have w_gate's shape ", wg.sizes(), " (got ", wu.sizes(), ")");
+  vector(bg, "b_gate", p.hidden);
+  vector(bu, "b_up", p.hidden);
+  TORCH_CHECK_NOT_IMPLEMENTED(!is_dual(x) && !is_dual(wg) && !is_dual(wu) && !is_dual(bg) && !is_dual(bu),
+                              "gated linear has no forward-mode derivative");
+  if (at::GradMode::is_enabled() &&
+      (x.requires_grad() || wg.requires_grad() || wu.requires_grad() || wants(bg) || wants(bu)))
+    return Glu::apply(x, wg, wu, bg, bu, p);
+  return glu_forward(p, dense(x), dense(wg), dense(wu), dense(bg), dense(bu));
+}
+
 // -------------------------------------------------------- gated recurrence
 struct RecPlan {
   int64_t batch, steps, channels, dtype;
@@ -303,6 +392,7 @@ void define_block(pybind11::module_& m) {
     const variable_list out = residual_norm(x, b, g, w, bw, scale, eps, norm_branch, std::nullopt);
     return std::make_tuple(out[0], out[1]);
   });
+  m.def("gated_linear", &gated_linear);
   m.def("gated_recurrence", &gated_recurrence);
   m.def("rms_norm", [](const at::Tensor& x, const Optional& w, double eps, const std::optional<at::ScalarType>& dtype) {
     return residual_norm(x, std::nullopt, std::nullopt, w, std::nullopt, 1.0, eps, false, dtype)[0];

@@ -4,8 +4,9 @@
  * channels-last features, the same norm read out to the scalar grid a curve
  * takes, Newton-Schulz orthogonalisation, and the momentum update built on it;
  * and those of a residual block over curves or other channels-last features:
- * the norms around a block with its gate and residual scale, and a gated
- * linear recurrence along the steps of a sequence.
+ * the norms around a block with its gate and residual scale, the gated pair of
+ * projections of a feed-forward block, and a gated linear recurrence along the
+ * steps of a sequence.
  *
  * Conventions are those of ecc.h (device pointers owned by the caller, work
  * enqueued on `stream`, status codes, ecc_last_error), except the workspace:
@@ -230,6 +231,37 @@ int ecc_gated_recurrence_bwd(const void* x, const void* gate, int dtype, int64_t
 /* Workspace bytes of the two calls above, and the bytes of `saved` (0 for invalid sizes). */
 size_t ecc_gated_recurrence_workspace_bytes(int64_t batch, int64_t steps, int64_t channels, int dtype);
 size_t ecc_gated_recurrence_saved_bytes(int64_t batch, int64_t steps, int64_t channels, int dtype);
+
+/*
+ * The gated pair of projections of a feed-forward block:
+ *   h = act(x w_gate^T + b_gate) (x w_up^T + b_up)
+ *   x             device, dtype elements, [rows][channels]
+ *   w_gate, w_up  dtype, [hidden][channels]
+ *   b_gate, b_up  dtype, [hidden]; each may be NULL (0)
+ *   act           of the first projection, ECC_ACT_*
+ *   h             dtype, [rows][hidden]; overlaps no input
+ * channels, hidden <= ECC_MAX_MATRIX.  Sums are float32, h is rounded once.  One
+ * launch, no workspace.
+ */
+int ecc_gated_linear_fwd(const void* x, int dtype, int64_t rows, int64_t channels, int64_t hidden, const void* w_gate,
+                         const void* w_up, const void* b_gate, const void* b_up, int act, void* h, void* stream);
+
+/*
+ * Its backward pass from grad_h = dL/dh (dtype, [rows][hidden]); the two
+ * projections are formed again.  With a and b the projections,
+ *   da = grad_h b act'(a), db = grad_h act(a)   (act'(0) = 0 for relu), each
+ *   rounded once to dtype, as operands of
+ *   grad_x = da w_gate + db w_up, grad_w_gate = da^T x, grad_w_up = db^T x;
+ *   grad_b_gate = sum da, grad_b_up = sum db, of the values before that rounding.
+ * All of dtype and OVERWRITTEN; each may be NULL (not wanted), but not all.
+ */
+int ecc_gated_linear_bwd(const void* x, int dtype, int64_t rows, int64_t channels, int64_t hidden, const void* w_gate,
+                         const void* w_up, const void* b_gate, const void* b_up, int act, const void* grad_h, void* grad_x,
+                         void* grad_w_gate, void* grad_w_up, void* grad_b_gate, void* grad_b_up, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* Workspace bytes of the backward pass (0 for invalid sizes). */
+size_t ecc_gated_linear_workspace_bytes(int64_t rows, int64_t channels, int64_t hidden, int dtype);
 
 #ifdef __cplusplus
 }

@@ -6,7 +6,7 @@ The bounds count roundings to first order; E = 2^-24 is float32's half step.
 
 import torch
 
-from tests.norm_bounds import E, _vec
+from tests.norm_bounds import E, _vec, act_and_slope
 from tests.norm_bounds import rounded as _rounded
 
 
@@ -150,3 +150,46 @@ def recurrence(x, gate, state=None, lengths=None, gh=None, glast=None):
     if state is not None:
         res["state"] = (e, e_ + 1e-300)
     return res
+
+
+def gated_linear(x, w_gate, w_up, b_gate=None, b_up=None, act="silu", gh=None):
+    """{name: (value, bound)} of gated_linear and, with gh, of every gradient.
+
+    A sum of n products in float32 has at most n roundings of partial sums and, from float32 elements, one of every
+    product: n + 1 roundings of the sum of magnitudes.  The gradients of the projections are rounded to the element type
+    before they are multiplied; the biases' are not, and are summed over at most 64 rows a lane, two waves and the tiles
+    in float64: 68 roundings."""
+    dt = x.dtype if x.dtype != torch.float64 else torch.float32
+    xd = x.detach().double().cpu().reshape(-1, x.shape[-1])
+    wg, wu = w_gate.detach().double().cpu(), w_up.detach().double().cpu()
+    (n, C), F = xd.shape, wg.shape[0]
+    bg, bu = _vec(b_gate, F, 0.0), _vec(b_up, F, 0.0)
+
+    def project(w, b):
+        return xd @ w.T + b, (C + 1) * E * (xd.abs() @ w.abs().T + b.abs())
+
+    (a, a_), (b, b_) = project(wg, bg), project(wu, bu)
+    y, sl = act_and_slope(a, act)
+    y_ = 1.2 * a_ + 2.0 ** -20 * a.abs()
+    h = y * b
+    h_ = y.abs() * b_ + b.abs() * y_ + y_ * b_ + E * h.abs()
+    shape = (*x.shape[:-1], F)
+    out = {"h": (h.reshape(shape), rounded(h, h_, dt).reshape(shape))}
+    if gh is None:
+        return out
+    g = gh.detach().double().cpu().reshape(n, F)
+    sl_ = (a.abs() <= a_).double() if act == "relu" else a_ + 2.0 ** -20 * (1 + a.abs())
+    da, db = g * b * sl, g * y
+    da_ = g.abs() * (b.abs() * sl_ + sl.abs() * b_ + b_ * sl_) + 3 * E * da.abs()
+    db_ = g.abs() * y_ + 2 * E * db.abs()
+    for name, v, b in (("b_gate", da, da_), ("b_up", db, db_)):
+        s, s_ = v.sum(0), (b + 68 * E * v.abs()).sum(0)
+        out[name] = (s, rounded(s, s_, dt))
+    ra, rb = rounded(da, da_, dt), rounded(db, db_, dt)
+    dx = da @ wg + db @ wu
+    dx_ = ra @ wg.abs() + rb @ wu.abs() + (2 * F + 1) * E * (da.abs() @ wg.abs() + db.abs() @ wu.abs())
+    out["x"] = (dx.reshape(x.shape), rounded(dx, dx_, dt).reshape(x.shape))
+    for name, v, r in (("w_gate", da, ra), ("w_up", db, rb)):
+        s, s_ = v.T @ xd, r.T @ xd.abs() + (n + 1) * E * (v.abs().T @ xd.abs())
+        out[name] = (s, rounded(s, s_, dt))
+    return out

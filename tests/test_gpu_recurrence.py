@@ -3,6 +3,7 @@ types, lengths from one step to many tiles and parts, odd channel counts, ragged
 
 import pytest
 import torch
+import torch.autograd.forward_ad as fa
 
 import euler_characteristic_curves_amd as E
 from tests.block_bounds import recurrence
@@ -278,3 +279,22 @@ def test_refusals():
     (g,) = torch.autograd.grad(h.sum(), [x], create_graph=True)
     with pytest.raises(RuntimeError, match="once"):
         g.sum().backward()
+
+
+def test_duals_and_changed_inputs():
+    """Tangents are refused, not dropped, and an input written after the call is noticed by its backward pass."""
+    banner("recurrence duals")
+    x = torch.zeros(2, 3, 4, device="cuda")
+    args = [x, torch.zeros_like(x), torch.zeros(2, 4, device="cuda", requires_grad=True)]
+    for i in range(len(args)):
+        with fa.dual_level(), pytest.raises(NotImplementedError, match="forward-mode"):
+            kept = args[i]
+            args[i] = fa.make_dual(kept.detach(), torch.ones_like(kept))
+            try:
+                E.gated_recurrence(*args)
+            finally:
+                args[i] = kept
+    out = E.gated_recurrence(*args)
+    x.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        (out[0] if isinstance(out, tuple) else out).sum().backward()

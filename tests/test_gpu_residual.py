@@ -4,6 +4,7 @@ graphs."""
 
 import pytest
 import torch
+import torch.autograd.forward_ad as fa
 
 import euler_characteristic_curves_amd as E
 from tests.block_bounds import residual
@@ -309,3 +310,23 @@ def test_refusals():
     (g,) = torch.autograd.grad(z.sum(), [x], create_graph=True)
     with pytest.raises(RuntimeError, match="once"):
         g.sum().backward()
+
+
+def test_duals_and_changed_inputs():
+    """Tangents are refused, not dropped, and an input written after the call is noticed by its backward pass."""
+    banner("residual duals")
+    x = torch.zeros(2, 3, 8, device="cuda")
+    w = torch.ones(8, device="cuda", requires_grad=True)
+    args = [x, torch.zeros_like(x), w, w, w]
+    for i in range(len(args)):
+        with fa.dual_level(), pytest.raises(NotImplementedError, match="forward-mode"):
+            kept = args[i]
+            args[i] = fa.make_dual(kept.detach(), torch.ones_like(kept))
+            try:
+                E.residual_norm(*args)
+            finally:
+                args[i] = kept
+    out = E.residual_norm(*args)
+    x.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        (out[0] if isinstance(out, tuple) else out).sum().backward()
