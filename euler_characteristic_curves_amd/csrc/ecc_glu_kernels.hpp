@@ -112,7 +112,37 @@ struct Tile {
     __builtin_memcpy(&r, &v, 16);
     return r;
   }
+  // Bytes from the tile's first element of a step to this thread's chunk i, of
+  // lines and chunks that are there (what those behind them would be is not used).
+  __device__ static __forceinline__ uint32_t offset(int64_t pitch, int64_t row0, int64_t n, int i) {
+    int line, chunk;
+    mine(i, line, chunk);
+    if (ALONG)
+      line = line < n - row0 ? line : (int)(n - row0 - 1);
+    else
+      chunk = chunk < (n - row0) / kPer<T> ? chunk : (int)((n - row0) / kPer<T>) - 1;
+    return (uint32_t)((int64_t)line * pitch * (int64_t)sizeof(T)) + chunk * 16;
+  }
 };
+
+// This thread's chunks of a step, straight to LDS.
+template <int N>
+__device__ __forceinline__ void load_chunks(const void* step, const uint32_t (&offset)[N], char* lds) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const char* base = reinterpret_cast<const char*>(step);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + offset[i]),
+                                     (__attribute__((address_space(3))) void*)(lds + (i * kNT + wave * 64) * 16), 16, 0, 0);
+}
+
+// Waits for all but the newest VM loads of this wave and for what it has read
+// of LDS, then for the other waves.
+template <int VM>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt((VM & 15) | 0x0070 | ((VM >> 4) << 14));  // the same, known to the compiler
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
+}
 
 // ---------------------------------------------------------------- fragments
 template <class T>
@@ -248,12 +278,35 @@ __device__ __forceinline__ void epilogue(const Product<T>& p, int z, int64_t tm,
 
 // ---------------------------------------------------------------- products
 template <class T, int KIND, int FM, int FN>
+__device__ __forceinline__ void multiply_step(const char* la, const char* lb, f32x16 (&acc)[FM][FN]) {
+  constexpr int TM = 64 * FM, TN = 64 * FN;
+  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    Fragment<T> a[FM], b[FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) a[i] = read_fragment<T, a_along(KIND), TM>(la, wm * FM * 32 + i * 32, c);
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      b[j] = read_fragment<T, b_along(KIND), TN>(lb, is_dual(KIND) ? j * 64 + wn * 32 : wn * FN * 32 + j * 32, c);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = multiply(a[i], b[j], acc[i][j]);
+  }
+}
+
+// ALIGNED: operands and their rows begin at multiples of 16 bytes.  Whole steps
+// then go straight to LDS, two of them on their way while a third is used; what
+// is left of each part of the sum comes last, through registers.  Otherwise
+// every step goes through registers, one ahead.
+template <class T, int KIND, int FM, int FN, bool ALIGNED>
 __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
   constexpr int TM = 64 * FM, TN = 64 * FN, kA = TM * 64, kB = TN * 64;
   using TileA = Tile<T, a_along(KIND), TM>;
   using TileB = Tile<T, b_along(KIND), TN>;
-  __shared__ __align__(16) char lds[2][kA + kB];
-  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  // arrays of their own, so that a read of one is known not to wait for another's loads
+  __shared__ __align__(16) char a0[kA], b0[kB], a1[kA], b1[kB], a2[ALIGNED ? kA : 16], b2[ALIGNED ? kB : 16];
   int64_t id = blockIdx.x;
   const int split = (int)(id % p.splits);
   id /= p.splits;
@@ -262,10 +315,23 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
   const int64_t tm = id % p.tiles_m;
   const int z = KIND == kWeight ? (int)(id / p.tiles_m) : 0;
   if (KIND == kWeight && !p.out[z]) return;  // not wanted
-  // steps of every part of the sum; this workgroup's are [from, to) of all of them
-  const int64_t each = (p.K + kStep<T> - 1) / kStep<T>, all = each * p.parts;
+  // steps of the sum: the whole ones of every part, then what is left of each;
+  // this workgroup's are [from, to)
+  const int64_t whole = ALIGNED ? p.K / kStep<T> : (p.K + kStep<T> - 1) / kStep<T>;
+  const int64_t all = (p.K + kStep<T> - 1) / kStep<T> * p.parts, direct = whole * p.parts;
   const int64_t share = (all + p.splits - 1) / p.splits, from = split * share;
   const int64_t to = from + share < all ? from + share : all;
+  const auto place = [&](int64_t s, int& part, int64_t& k0) {
+    part = 0;
+    if (ALIGNED && s >= direct) {
+      part = (int)(s - direct);
+      k0 = whole * kStep<T>;
+    } else {
+      if (KIND == kInput && s >= whole) part = 1;
+      k0 = (s - part * whole) * kStep<T>;
+    }
+  };
+  const auto base_a = [&](int part) { return p.A + (KIND == kWeight ? z : part) * p.stepA; };
   f32x16 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -275,48 +341,92 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
   u32x4 ra[TileA::kChunks], rb[TileB::kChunks];
   const auto fetch = [&](int64_t s) {
-    const int part = KIND == kInput && s >= each ? 1 : 0;
-    const int64_t k0 = (s - part * each) * kStep<T>;
-    const T* A = p.A + (KIND == kWeight ? z : part) * p.stepA;
+    int part;
+    int64_t k0;
+    place(s, part, k0);
 #pragma unroll
-    for (int i = 0; i < TileA::kChunks; ++i) ra[i] = TileA::fetch(A, p.pitchA, tm * TM, p.M, k0, p.K, i);
+    for (int i = 0; i < TileA::kChunks; ++i) ra[i] = TileA::fetch(base_a(part), p.pitchA, tm * TM, p.M, k0, p.K, i);
 #pragma unroll
     for (int i = 0; i < TileB::kChunks; ++i) {
       if constexpr (is_dual(KIND))  // 64 rows of either projection: chunk i is one of rows 64 i to 64 i + 63
-        rb[i] = Tile<T, true, TN>::fetch(p.B[i] - i * 64 * p.pitchB, p.pitchB, tn * 64, p.N + i * 64, k0, p.K, i);
+        rb[i] = TileB::fetch(p.B[i] - i * 64 * p.pitchB, p.pitchB, tn * 64, p.N + i * 64, k0, p.K, i);
       else
         rb[i] = TileB::fetch(p.B[KIND == kInput ? part : 0], p.pitchB, tn * TN, p.N, k0, p.K, i);
     }
   };
-  const auto put = [&](char* to_lds) {
+  const auto put = [&](char* la, char* lb) {
 #pragma unroll
-    for (int i = 0; i < TileA::kChunks; ++i) *reinterpret_cast<u32x4*>(to_lds + (i * kNT + threadIdx.x) * 16) = ra[i];
+    for (int i = 0; i < TileA::kChunks; ++i) *reinterpret_cast<u32x4*>(la + (i * kNT + threadIdx.x) * 16) = ra[i];
 #pragma unroll
-    for (int i = 0; i < TileB::kChunks; ++i) *reinterpret_cast<u32x4*>(to_lds + kA + (i * kNT + threadIdx.x) * 16) = rb[i];
+    for (int i = 0; i < TileB::kChunks; ++i) *reinterpret_cast<u32x4*>(lb + (i * kNT + threadIdx.x) * 16) = rb[i];
   };
-  if (from < to) {
-    fetch(from);
-    put(lds[0]);
-  }
-  __syncthreads();
-  for (int64_t s = from; s < to; ++s) {
-    const char* here = lds[(s - from) & 1];
-    if (s + 1 < to) fetch(s + 1);
+  if constexpr (ALIGNED) {
+    uint32_t offA[TileA::kChunks], offB[TileB::kChunks];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      Fragment<T> a[FM], b[FN];
+    for (int i = 0; i < TileA::kChunks; ++i) offA[i] = TileA::offset(p.pitchA, tm * TM, KIND == kWeight ? p.pitch : p.M, i);
 #pragma unroll
-      for (int i = 0; i < FM; ++i) a[i] = read_fragment<T, a_along(KIND), TM>(here, wm * FM * 32 + i * 32, c);
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-        b[j] = read_fragment<T, b_along(KIND), TN>(here + kA, is_dual(KIND) ? j * 64 + wn * 32 : wn * FN * 32 + j * 32, c);
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = multiply(a[i], b[j], acc[i][j]);
+    for (int i = 0; i < TileB::kChunks; ++i) {
+      if constexpr (is_dual(KIND))
+        offB[i] = Tile<T, true, 64>::offset(p.pitchB, tn * 64, p.N, 0);
+      else
+        offB[i] = TileB::offset(p.pitchB, tn * TN, p.N, i);
     }
-    if (s + 1 < to) put(lds[(s + 1 - from) & 1]);
+    const auto load = [&](int64_t s, char* la, char* lb) {
+      if (s >= to) return;
+      if (s >= direct) {
+        fetch(s);
+        put(la, lb);
+        return;
+      }
+      int part;
+      int64_t k0;
+      place(s, part, k0);
+      const T* A = base_a(part);
+      load_chunks(a_along(KIND) ? A + tm * TM * p.pitchA + k0 : A + k0 * p.pitchA + tm * TM, offA, la);
+      if constexpr (is_dual(KIND)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t one[1] = {offB[i]};
+          load_chunks(p.B[i] + tn * 64 * p.pitchB + k0, one, lb + i * 64 * 64);
+        }
+      } else {
+        load_chunks(p.B[KIND == kInput ? part : 0] + k0 * p.pitchB + tn * TN, offB, lb);
+      }
+    };
+    const int64_t last = to < direct ? to : direct;  // of those that go straight to LDS
+    const auto step = [&](int64_t s, char* la, char* lb, char* na, char* nb) {
+      if (s >= to) return;
+      if (s + 1 < last)
+        wait_loads<FM + FN>();
+      else
+        wait_loads<0>();
+      load(s + 2, na, nb);
+      multiply_step<T, KIND, FM, FN>(la, lb, acc);
+    };
+    load(from, a0, b0);
+    load(from + 1, a1, b1);
+    for (int64_t s = from; s < to; s += 3) {
+      step(s, a0, b0, a2, b2);
+      step(s + 1, a1, b1, a0, b0);
+      step(s + 2, a2, b2, a1, b1);
+    }
+  } else {
+    if (from < to) {
+      fetch(from);
+      put(a0, b0);
+    }
     __syncthreads();
+    const auto step = [&](int64_t s, char* la, char* lb, char* na, char* nb) {
+      if (s >= to) return;
+      if (s + 1 < to) fetch(s + 1);
+      multiply_step<T, KIND, FM, FN>(la, lb, acc);
+      if (s + 1 < to) put(na, nb);
+      __syncthreads();
+    };
+    for (int64_t s = from; s < to; s += 2) {
+      step(s, a0, b0, a1, b1);
+      step(s + 1, a1, b1, a0, b0);
+    }
   }
   if (p.splits > 1) {
     float* out = p.part + ((int64_t)blockIdx.x * kNT + threadIdx.x) * (FM * FN * 16);
@@ -333,7 +443,7 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
         }
     return;
   }
-  epilogue<T, KIND, FM, FN>(p, z, tm, tn, acc, reinterpret_cast<float*>(&lds[0][0]));
+  epilogue<T, KIND, FM, FN>(p, z, tm, tn, acc, reinterpret_cast<float*>(a0));
 }
 
 // Joins the shares of a tile, in order.  One fragment of four waves a workgroup.
@@ -367,28 +477,47 @@ __global__ __launch_bounds__(kNT) void glu_join_kernel(Product<T> p) {
   }
 }
 
-// Bias gradients from the tiles' sums, in float64.  64 units a workgroup.
+// Bias gradients from the tiles' sums, in float64.  16 units a workgroup.
+constexpr int kJoin = 1024;
 template <class T>
-__global__ __launch_bounds__(kNT) void glu_bias_kernel(Product<T> p) {
-  __shared__ double lds[4][64];
-  const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
-  const int64_t unit = (int64_t)blockIdx.x * 64 + c;
+__global__ __launch_bounds__(kJoin) void glu_bias_kernel(Product<T> p) {
+  __shared__ double lds[kJoin / 16][17];
+  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int64_t unit = (int64_t)blockIdx.x * 16 + c;
   T* out = reinterpret_cast<T*>(blockIdx.y == 0 ? p.a.gbg : p.a.gbu);
   if (!out) return;
   double s = 0.0;
-  if (unit < p.N)
-    for (int64_t t = r; t < p.tiles_m; t += 4) s += (double)p.bias[(t * 2 + blockIdx.y) * p.pitch + unit];
+  if (unit < p.N) {
+#pragma unroll 4
+    for (int64_t t = r; t < p.tiles_m; t += kJoin / 16) s += (double)p.bias[(t * 2 + blockIdx.y) * p.pitch + unit];
+  }
   lds[r][c] = s;
   __syncthreads();
-  if (r == 0 && unit < p.N) out[unit] = (T)(float)((lds[0][c] + lds[1][c]) + (lds[2][c] + lds[3][c]));
+  for (int d = kJoin / 32; d > 0; d /= 2) {
+    if (r < d) lds[r][c] += lds[r + d][c];
+    __syncthreads();
+  }
+  if (r == 0 && unit < p.N) out[unit] = (T)(float)lds[0][c];
 }
 
 // ---------------------------------------------------------------- launches
+template <class T>
+bool is_aligned(const Product<T>& p) {
+  const auto ok = [](const void* q, int64_t pitch) {
+    return reinterpret_cast<uintptr_t>(q) % 16 == 0 && pitch % kPer<T> == 0;
+  };
+  return ok(p.A, p.pitchA) && ok(p.B[0], p.pitchB) && ok(p.B[1], p.pitchB);
+}
+
 template <class T, int KIND, int FM>
 hipError_t launch_tiles(Product<T> p, hipStream_t stream) {
   const int both = KIND == kWeight ? 2 : 1;
   const int64_t tiles = p.tiles_m * p.tiles_n * both;
-  hipLaunchKernelGGL((glu_kernel<T, KIND, FM, 2>), dim3((unsigned)(tiles * p.splits)), dim3(kNT), 0, stream, p);
+  const dim3 grid((unsigned)(tiles * p.splits)), block(kNT);
+  if (is_aligned(p))
+    hipLaunchKernelGGL((glu_kernel<T, KIND, FM, 2, true>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((glu_kernel<T, KIND, FM, 2, false>), grid, block, 0, stream, p);
   if constexpr (!is_dual(KIND)) {
     if (p.splits > 1)
       hipLaunchKernelGGL((glu_join_kernel<T, KIND, FM, 2>), dim3((unsigned)tiles, FM * 2), dim3(kNT), 0, stream, p);
@@ -437,7 +566,7 @@ hipError_t launch_glu_bwd(const GluArgs& a, hipStream_t stream) {
   if (st != hipSuccess) return st;
   if (p.bias) {
     p.tiles_m = plan.gates.tiles_m;
-    hipLaunchKernelGGL(glu_bias_kernel<T>, dim3((unsigned)((a.hidden + 63) / 64), 2), dim3(kNT), 0, stream, p);
+    hipLaunchKernelGGL(glu_bias_kernel<T>, dim3((unsigned)((a.hidden + 15) / 16), 2), dim3(kJoin), 0, stream, p);
   }
   p.A = p.dab;
   p.pitchA = 2 * plan.pitch;
@@ -456,7 +585,7 @@ hipError_t launch_glu_bwd(const GluArgs& a, hipStream_t stream) {
     p.N = a.channels;
     p.K = a.rows;
     p.parts = 1;
-    p.B[0] = reinterpret_cast<const T*>(a.x);
+    p.B[0] = p.B[1] = reinterpret_cast<const T*>(a.x);
     p.out[0] = reinterpret_cast<T*>(a.gwg);
     p.out[1] = reinterpret_cast<T*>(a.gwu);
     p.pitch_out = a.channels;
