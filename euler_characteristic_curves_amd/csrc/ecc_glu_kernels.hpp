@@ -194,86 +194,230 @@ __device__ __forceinline__ f32x16 multiply(const Fragment<float>& a, const Fragm
   return c;
 }
 
-// Row within a fragment of its result r.
-__device__ __forceinline__ int result_row(int r) { return (r >> 2) * 8 + (threadIdx.x >> 5 & 1) * 4 + (r & 3); }
+// A fragment's result r of a lane: row lane % 32 of the operand with M rows,
+// and this one of the other.
+__device__ __forceinline__ int result_col(int r) { return (r >> 2) * 8 + (threadIdx.x >> 5 & 1) * 4 + (r & 3); }
 
 // ---------------------------------------------------------------- epilogues
-template <class F>
-__device__ __forceinline__ void with_act(int act, F f) {
-  if (act == kActSilu)
-    f(std::integral_constant<int, kActSilu>{});
-  else if (act == kActGelu)
-    f(std::integral_constant<int, kActGelu>{});
-  else if (act == kActRelu)
-    f(std::integral_constant<int, kActRelu>{});
-  else
-    f(std::integral_constant<int, kActNone>{});
+// A fragment's 32 x 32 results pass through LDS, so that memory sees whole
+// chunks of rows: 4 KB of its own for every wave, whose accesses keep their
+// order.  Chunks of a row are permuted as they are in the tiles.
+constexpr int kStage = 4096;
+template <class T>
+struct Stage {
+  static constexpr int kLine = 32 * (int)sizeof(T), kChunks = kLine / 16, kTurns = 32 * kChunks / 64;
+  char* lds;
+  __device__ __forceinline__ char* at(int row, int chunk) const {
+    return lds + row * kLine + ((sizeof(T) == 2 ? chunk ^ (row >> 2 & 3) : chunk ^ (row >> 1 & 7)) << 4);
+  }
+  __device__ __forceinline__ char* mine(int q) const {  // results 4 q to 4 q + 3
+    const int lane = threadIdx.x & 63, byte = (q * 8 + (lane >> 5) * 4) * (int)sizeof(T);
+    return at(lane & 31, byte >> 4) + (byte & 15);
+  }
+  __device__ __forceinline__ void put(const float (&v)[16]) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      Vec<T, 4> u;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) u.v[r] = (T)v[q * 4 + r];
+      __builtin_memcpy(__builtin_assume_aligned(mine(q), sizeof(u)), &u, sizeof(u));
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  __device__ __forceinline__ void get(float (&v)[16]) const {
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      Vec<T, 4> u;
+      __builtin_memcpy(&u, __builtin_assume_aligned(mine(q), sizeof(u)), sizeof(u));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[q * 4 + r] = (float)u.v[r];
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  // To and from memory: rows and columns that are left from p on.  p is the same
+  // for all lanes, and 32 rows of any pitch fit 32 bits.
+  __device__ __forceinline__ static uint32_t offset(int row, int col, int64_t pitch) {
+    return (uint32_t)row * (uint32_t)(pitch * (int64_t)sizeof(T)) + (uint32_t)(col * (int)sizeof(T));
+  }
+  __device__ __forceinline__ void store(T* p, int64_t pitch, int64_t rows, int64_t cols) const {
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+      const int id = i * 64 + (threadIdx.x & 63), row = id / kChunks, chunk = id % kChunks, col = chunk * kPer<T>;
+      Vec<T, kPer<T>> u;
+      __builtin_memcpy(&u, __builtin_assume_aligned(at(row, chunk), 16), 16);
+      if (row >= rows || col >= cols) continue;
+      T* out = reinterpret_cast<T*>(reinterpret_cast<char*>(p) + offset(row, col, pitch));
+      if (col + kPer<T> <= cols) {
+        store_vec(out, u);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPer<T> - 1; ++j)
+          if (col + j < cols) out[j] = u.v[j];
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  __device__ __forceinline__ static void load(const T* p, int64_t pitch, int64_t rows, int64_t cols, u32x4 (&u)[kTurns]) {
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+      const int id = i * 64 + (threadIdx.x & 63), row = id / kChunks, col = id % kChunks * kPer<T>;
+      u[i] = u32x4{};
+      if (row >= rows || col >= cols) continue;
+      const char* in = reinterpret_cast<const char*>(p) + offset(row, col, pitch);
+      if (col + kPer<T> <= cols) {
+        __builtin_memcpy(&u[i], in, 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPer<T> - 1; ++j)
+          if (col + j < cols) {
+            if constexpr (sizeof(T) == 4)
+              u[i][j] = reinterpret_cast<const uint32_t*>(in)[j];
+            else
+              u[i][j / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(in)[j] << (j % 2 * 16);
+          }
+      }
+    }
+  }
+  __device__ __forceinline__ void place(const u32x4 (&u)[kTurns]) const {
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+      const int id = i * 64 + (threadIdx.x & 63);
+      *reinterpret_cast<u32x4*>(at(id / kChunks, id % kChunks)) = u[i];
+    }
+  }
+};
+
+// Sums of 16 values a lane over the 32 rows of all waves' fragments: lanes 0 to
+// 31 get one each.  lds: the wave's.
+__device__ __forceinline__ float sum_rows(const float (&v)[16], float* lds) {
+  const int lane = threadIdx.x & 63;
+  // [row][column], columns turned by the row
+#pragma unroll
+  for (int r = 0; r < 16; ++r) lds[(lane & 31) * 32 + ((result_col(r) + lane) & 31)] = v[r];
+  __builtin_amdgcn_wave_barrier();
+  float s = 0.0f;
+#pragma unroll 8
+  for (int i = 0; i < 32; ++i) s += lds[i * 32 + ((lane + i) & 31)];
+  __builtin_amdgcn_wave_barrier();
+  return s;
 }
 
 // A workgroup's results: acc[i][j] is the fragment of rows wm FM 32 + 32 i.
-template <class T, int KIND, int FM, int FN>
-__device__ __forceinline__ void epilogue(const Product<T>& p, int z, int64_t tm, int64_t tn, f32x16 (&acc)[FM][FN], float* lds) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+// lds: kStage bytes for this wave; shared: 128 floats for all of them.
+template <class T, int KIND, int FM, int FN, int ACT>
+__device__ __forceinline__ void epilogue(const Product<T>& p, int z, int64_t tm, int64_t tn, f32x16 (&acc)[FM][FN], char* lds,
+                                         float* shared) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
   const int64_t row0 = tm * 64 * FM + wm * FM * 32;
+  const Stage<T> stage{lds};
   if constexpr (is_dual(KIND)) {
-    const int64_t unit = tn * 64 + wn * 32 + (lane & 31);
-    const bool in = unit < p.N;
-    const float bg = in && p.a.bg ? (float)reinterpret_cast<const T*>(p.a.bg)[unit] : 0.0f;
-    const float bu = in && p.a.bu ? (float)reinterpret_cast<const T*>(p.a.bu)[unit] : 0.0f;
-    float sum_a = 0.0f, sum_b = 0.0f;
-    with_act(p.a.act, [&](auto act) {
+    const int64_t unit0 = tn * 64 + wn * 32, cols = p.N - unit0;
+    // the tile's biases, of both projections
+    if (threadIdx.x < 128) {
+      const T* bias = reinterpret_cast<const T*>(threadIdx.x < 64 ? p.a.bg : p.a.bu);
+      const int64_t unit = tn * 64 + (threadIdx.x & 63);
+      shared[threadIdx.x] = bias && unit < p.N ? (float)bias[unit] : 0.0f;
+    }
+    __syncthreads();
+    const f32x4* bg = reinterpret_cast<const f32x4*>(shared + wn * 32 + (lane >> 5) * 4);
+    if constexpr (KIND == kForward) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
+      for (int i = 0; i < FM; ++i) {
+        float v[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int64_t row = row0 + i * 32 + result_row(r);
-          if (!in || row >= p.M) continue;
-          const float a = acc[i][0][r] + bg, b = acc[i][1][r] + bu;
-          if constexpr (KIND == kForward) {
-            reinterpret_cast<T*>(p.a.h)[row * p.N + unit] = (T)(act_value<act.value>(a) * b);
-          } else {
-            const float g = (float)reinterpret_cast<const T*>(p.a.gh)[row * p.N + unit];
-            float y;
-            const float slope = act_slope<act.value>(a, y);
-            const float da = g * b * slope, db = g * y;
-            T* out = p.dab + row * 2 * p.pitch + unit;
-            out[0] = (T)da;
-            out[p.pitch] = (T)db;
-            sum_a += da;
-            sum_b += db;
-          }
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 ug = bg[q * 2], uu = bg[16 + q * 2];
+#pragma unroll
+          for (int r = q * 4; r < q * 4 + 4; ++r)
+            v[r] = act_value<ACT>(acc[i][0][r] + ug[r & 3]) * (acc[i][1][r] + uu[r & 3]);
         }
-    });
-    if constexpr (KIND == kGates) {
+        stage.put(v);
+        const int64_t row = row0 + i * 32;
+        stage.store(reinterpret_cast<T*>(p.a.h) + row * p.N + unit0, p.N, p.M - row, cols);
+      }
+    } else {
+      const T* gh = reinterpret_cast<const T*>(p.a.gh);
+      u32x4 next[Stage<T>::kTurns];
+      Stage<T>::load(gh + row0 * p.N + unit0, p.N, p.M - row0, cols, next);
+      // sums over the fragments; rows that are not there have no gradient, but
+      // may have infinite projections
+      float sum_a[16] = {}, sum_b[16] = {};
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int64_t row = row0 + i * 32;
+        const bool in = row + (lane & 31) < p.M;
+        float g[16], da[16];
+        stage.place(next);
+        stage.get(g);
+        if (i + 1 < FM) Stage<T>::load(gh + (row + 32) * p.N + unit0, p.N, p.M - row - 32, cols, next);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 ug = bg[q * 2], uu = bg[16 + q * 2];
+#pragma unroll
+          for (int r = q * 4; r < q * 4 + 4; ++r) {
+            float y;
+            const float b = acc[i][1][r] + uu[r & 3], slope = act_slope<ACT>(acc[i][0][r] + ug[r & 3], y);
+            da[r] = g[r] * b * slope;
+            g[r] *= y;
+            sum_a[r] += in ? da[r] : 0.0f;
+            sum_b[r] += in ? g[r] : 0.0f;
+          }
+          __builtin_amdgcn_sched_barrier(0);  // all at once would not fit the registers
+        }
+        T* out = p.dab + row * 2 * p.pitch + unit0;
+        stage.put(da);
+        stage.store(out, 2 * p.pitch, p.M - row, cols);
+        stage.put(g);
+        stage.store(out + p.pitch, 2 * p.pitch, p.M - row, cols);
+      }
       if (!p.bias) return;
-      sum_a += __shfl_xor(sum_a, 32);
-      sum_b += __shfl_xor(sum_b, 32);
-      __syncthreads();  // the stages are free
+      const float a = sum_rows(sum_a, reinterpret_cast<float*>(lds)), b = sum_rows(sum_b, reinterpret_cast<float*>(lds));
+      __syncthreads();  // the biases are read
       if (wm == 1 && lane < 32) {
-        lds[wn * 32 + lane] = sum_a;
-        lds[64 + wn * 32 + lane] = sum_b;
+        shared[wn * 32 + lane] = a;
+        shared[64 + wn * 32 + lane] = b;
       }
       __syncthreads();
-      if (wm == 0 && lane < 32 && in) {
-        float* out = p.bias + tm * 2 * p.pitch + unit;
-        out[0] = sum_a + lds[wn * 32 + lane];
-        out[p.pitch] = sum_b + lds[64 + wn * 32 + lane];
+      if (wm == 0 && lane < cols && lane < 32) {
+        float* out = p.bias + tm * 2 * p.pitch + unit0 + lane;
+        out[0] = a + shared[wn * 32 + lane];
+        out[p.pitch] = b + shared[64 + wn * 32 + lane];
       }
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int64_t col = tn * 64 * FN + wn * FN * 32 + j * 32 + (lane & 31);
-      if (col >= p.N) continue;
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
+      for (int j = 0; j < FN; ++j) {
+        const int64_t row = row0 + i * 32, col = tn * 64 * FN + wn * FN * 32 + j * 32;
+        float v[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int64_t row = row0 + i * 32 + result_row(r);
-          if (row < p.M) p.out[z][row * p.pitch_out + col] = (T)acc[i][j][r];
-        }
-    }
+        for (int r = 0; r < 16; ++r) v[r] = acc[i][j][r];
+        stage.put(v);
+        stage.store(p.out[z] + row * p.pitch_out + col, p.pitch_out, p.M - row, p.N - col);
+      }
   }
+}
+
+// Which tile a workgroup takes.  Workgroups are dealt out to the eight dies in
+// turn, so that each gets a run of neighbours: eight tiles along M for every one
+// along N, whose operands its cache then holds.  `shares` of all tiles come one
+// after the other.
+struct TileId {
+  int64_t tm, tn, share;  // tm counts the rows of all matrices
+};
+__device__ __forceinline__ TileId tile_of(int64_t id, int64_t rows, int64_t cols, int64_t shares) {
+  const int64_t all = rows * cols * shares, die = id & 7, each = all >> 3, more = all & 7;
+  id = die * each + (die < more ? die : more) + (id >> 3);
+  TileId t;
+  t.share = id / (rows * cols);
+  id -= t.share * (rows * cols);
+  const int64_t group = id / (8 * cols), in = id - group * 8 * cols;
+  const int64_t high = rows - group * 8 < 8 ? rows - group * 8 : 8;
+  t.tn = in / high;
+  t.tm = group * 8 + (in - t.tn * high);
+  return t;
 }
 
 // ---------------------------------------------------------------- products
@@ -292,7 +436,7 @@ __device__ __forceinline__ void multiply_step(const char* la, const char* lb, f3
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) acc[i][j] = multiply(a[i], b[j], acc[i][j]);
+      for (int j = 0; j < FN; ++j) acc[i][j] = multiply(b[j], a[i], acc[i][j]);
   }
 }
 
@@ -300,20 +444,16 @@ __device__ __forceinline__ void multiply_step(const char* la, const char* lb, f3
 // then go straight to LDS, two of them on their way while a third is used; what
 // is left of each part of the sum comes last, through registers.  Otherwise
 // every step goes through registers, one ahead.
-template <class T, int KIND, int FM, int FN, bool ALIGNED>
+template <class T, int KIND, int FM, int FN, bool ALIGNED, int ACT>
 __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
   constexpr int TM = 64 * FM, TN = 64 * FN, kA = TM * 64, kB = TN * 64;
   using TileA = Tile<T, a_along(KIND), TM>;
   using TileB = Tile<T, b_along(KIND), TN>;
   // arrays of their own, so that a read of one is known not to wait for another's loads
   __shared__ __align__(16) char a0[kA], b0[kB], a1[kA], b1[kB], a2[ALIGNED ? kA : 16], b2[ALIGNED ? kB : 16];
-  int64_t id = blockIdx.x;
-  const int split = (int)(id % p.splits);
-  id /= p.splits;
-  const int64_t tn = id % p.tiles_n;
-  id /= p.tiles_n;
-  const int64_t tm = id % p.tiles_m;
-  const int z = KIND == kWeight ? (int)(id / p.tiles_m) : 0;
+  const TileId id = tile_of(blockIdx.x, p.tiles_m * (KIND == kWeight ? 2 : 1), p.tiles_n, p.splits);
+  const int z = KIND == kWeight && id.tm >= p.tiles_m ? 1 : 0;
+  const int64_t tm = id.tm - z * p.tiles_m, tn = id.tn, split = id.share;
   if (KIND == kWeight && !p.out[z]) return;  // not wanted
   // steps of the sum: the whole ones of every part, then what is left of each;
   // this workgroup's are [from, to)
@@ -429,7 +569,8 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
     }
   }
   if (p.splits > 1) {
-    float* out = p.part + ((int64_t)blockIdx.x * kNT + threadIdx.x) * (FM * FN * 16);
+    const int64_t tile = id.tm * p.tiles_n + tn;
+    float* out = p.part + ((tile * p.splits + split) * kNT + threadIdx.x) * (FM * FN * 16);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -443,12 +584,15 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
         }
     return;
   }
-  epilogue<T, KIND, FM, FN>(p, z, tm, tn, acc, reinterpret_cast<float*>(a0));
+  if (ALIGNED) wait_loads<0>();  // the stages are free
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  epilogue<T, KIND, FM, FN, ACT>(p, z, tm, tn, acc, (wave & 2 ? b1 : b0) + (wave & 1) * kStage, reinterpret_cast<float*>(a0));
 }
 
 // Joins the shares of a tile, in order.  One fragment of four waves a workgroup.
 template <class T, int KIND, int FM, int FN>
 __global__ __launch_bounds__(kNT) void glu_join_kernel(Product<T> p) {
+  __shared__ __align__(16) char lds[4 * kStage];
   int64_t id = blockIdx.x;
   if (!p.out[id / (p.tiles_n * p.tiles_m)]) return;
   const int i = blockIdx.y / FN, j = blockIdx.y % FN;
@@ -467,14 +611,11 @@ __global__ __launch_bounds__(kNT) void glu_join_kernel(Product<T> p) {
   id /= p.tiles_n;
   const int64_t tm = id % p.tiles_m;
   const int z = (int)(id / p.tiles_m);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
-  const int64_t col = tn * 64 * FN + wn * FN * 32 + j * 32 + (lane & 31);
-  if (col >= p.N) return;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int64_t row = tm * 64 * FM + wm * FM * 32 + i * 32 + result_row(r);
-    if (row < p.M) p.out[z][row * p.pitch_out + col] = (T)v[r];
-  }
+  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const int64_t row = tm * 64 * FM + wm * FM * 32 + i * 32, col = tn * 64 * FN + wn * FN * 32 + j * 32;
+  const Stage<T> stage{lds + wave * kStage};
+  stage.put(v);
+  stage.store(p.out[z] + row * p.pitch_out + col, p.pitch_out, p.M - row, p.N - col);
 }
 
 // Bias gradients from the tiles' sums, in float64.  16 units a workgroup.
@@ -514,10 +655,24 @@ hipError_t launch_tiles(Product<T> p, hipStream_t stream) {
   const int both = KIND == kWeight ? 2 : 1;
   const int64_t tiles = p.tiles_m * p.tiles_n * both;
   const dim3 grid((unsigned)(tiles * p.splits)), block(kNT);
-  if (is_aligned(p))
-    hipLaunchKernelGGL((glu_kernel<T, KIND, FM, 2, true>), grid, block, 0, stream, p);
-  else
-    hipLaunchKernelGGL((glu_kernel<T, KIND, FM, 2, false>), grid, block, 0, stream, p);
+  const auto launch = [&](auto act) {
+    if (is_aligned(p))
+      hipLaunchKernelGGL((glu_kernel<T, KIND, FM, 2, true, act.value>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((glu_kernel<T, KIND, FM, 2, false, act.value>), grid, block, 0, stream, p);
+  };
+  using std::integral_constant;
+  if (!is_dual(KIND) || p.a.act == kActNone)
+    launch(integral_constant<int, kActNone>{});
+  else if constexpr (is_dual(KIND)) {
+    // (chosen in the kernel, the activation costs it more registers than there are)
+    if (p.a.act == kActRelu)
+      launch(integral_constant<int, kActRelu>{});
+    else if (p.a.act == kActSilu)
+      launch(integral_constant<int, kActSilu>{});
+    else
+      launch(integral_constant<int, kActGelu>{});
+  }
   if constexpr (!is_dual(KIND)) {
     if (p.splits > 1)
       hipLaunchKernelGGL((glu_join_kernel<T, KIND, FM, 2>), dim3((unsigned)tiles, FM * 2), dim3(kNT), 0, stream, p);
