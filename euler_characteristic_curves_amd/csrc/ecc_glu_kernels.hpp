@@ -125,22 +125,27 @@ struct Tile {
   }
 };
 
-// This thread's chunks of a step, straight to LDS.
+// This thread's chunks of a step, straight to LDS: the base is the same for all
+// lanes, and so is where a wave's 64 chunks go.  In assembly, because the compiler
+// would wait for all such loads before it reads what one of them may have
+// written, as it cannot tell which are complete; the waits are wait_loads.  (m0
+// is not the compiler's to keep anything in.)
 template <int N>
 __device__ __forceinline__ void load_chunks(const void* step, const uint32_t (&offset)[N], char* lds) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const char* base = reinterpret_cast<const char*>(step);
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds + wave * 1024;
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + offset[i]),
-                                     (__attribute__((address_space(3))) void*)(lds + (i * kNT + wave * 64) * 16), 16, 0, 0);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(to + i * (kNT * 16)), "v"(offset[i]), "s"(step)
+                 : "memory");
 }
 
 // Waits for all but the newest VM loads of this wave and for what it has read
 // of LDS, then for the other waves.
 template <int VM>
 __device__ __forceinline__ void wait_loads() {
-  __builtin_amdgcn_s_waitcnt((VM & 15) | 0x0070 | ((VM >> 4) << 14));  // the same, known to the compiler
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
 }
 
@@ -405,19 +410,18 @@ __device__ __forceinline__ void epilogue(const Product<T>& p, int z, int64_t tm,
 // along N, whose operands its cache then holds.  `shares` of all tiles come one
 // after the other.
 struct TileId {
-  int64_t tm, tn, share;  // tm counts the rows of all matrices
+  int tm, tn, share;  // tm counts the rows of all matrices
 };
-__device__ __forceinline__ TileId tile_of(int64_t id, int64_t rows, int64_t cols, int64_t shares) {
-  const int64_t all = rows * cols * shares, die = id & 7, each = all >> 3, more = all & 7;
-  id = die * each + (die < more ? die : more) + (id >> 3);
-  TileId t;
-  t.share = id / (rows * cols);
-  id -= t.share * (rows * cols);
-  const int64_t group = id / (8 * cols), in = id - group * 8 * cols;
-  const int64_t high = rows - group * 8 < 8 ? rows - group * 8 : 8;
-  t.tn = in / high;
-  t.tm = group * 8 + (in - t.tn * high);
-  return t;
+__device__ __forceinline__ TileId tile_of(uint32_t rows, uint32_t cols, uint32_t shares) {
+  const uint32_t all = rows * cols * shares, die = blockIdx.x & 7, each = all >> 3, more = all & 7;
+  uint32_t id = die * each + (die < more ? die : more) + (blockIdx.x >> 3);
+  const uint32_t share = id / (rows * cols);
+  id -= share * (rows * cols);
+  const uint32_t group = id / (8 * cols), in = id - group * 8 * cols, high = rows - group * 8 < 8 ? rows - group * 8 : 8;
+  const uint32_t tn = in / high;
+  // (divisions leave the scalar registers, where loads want their bases)
+  return TileId{__builtin_amdgcn_readfirstlane(group * 8 + (in - tn * high)), __builtin_amdgcn_readfirstlane(tn),
+                __builtin_amdgcn_readfirstlane(share)};
 }
 
 // ---------------------------------------------------------------- products
@@ -425,18 +429,41 @@ template <class T, int KIND, int FM, int FN>
 __device__ __forceinline__ void multiply_step(const char* la, const char* lb, f32x16 (&acc)[FM][FN]) {
   constexpr int TM = 64 * FM, TN = 64 * FN;
   const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  Fragment<T> a[2][FM], b[2][FN];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    Fragment<T> a[FM], b[FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) a[i] = read_fragment<T, a_along(KIND), TM>(la, wm * FM * 32 + i * 32, c);
 #pragma unroll
     for (int j = 0; j < FN; ++j)
-      b[j] = read_fragment<T, b_along(KIND), TN>(lb, is_dual(KIND) ? j * 64 + wn * 32 : wn * FN * 32 + j * 32, c);
+      b[c][j] = read_fragment<T, b_along(KIND), TN>(lb, is_dual(KIND) ? j * 64 + wn * 32 : wn * FN * 32 + j * 32, c);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) a[c][i] = read_fragment<T, a_along(KIND), TM>(la, wm * FM * 32 + i * 32, c);
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) acc[i][j] = multiply(b[j], a[i], acc[i][j]);
+      for (int j = 0; j < FN; ++j) acc[i][j] = multiply(b[c][j], a[c][i], acc[i][j]);
+  // the first half's reads, then the others' between the first half's products
+  constexpr int kTurned = sizeof(T) == 4 ? 4 : 2;
+  constexpr int kReads = FM * (a_along(KIND) ? 1 : kTurned) + FN * (b_along(KIND) ? 1 : kTurned);
+  constexpr int kProducts = FM * FN * (sizeof(T) == 4 ? 4 : 1);
+  __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+  if constexpr (kReads <= kProducts) {
+#pragma unroll
+    for (int i = 0; i < kReads; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 2 * kProducts - kReads, 0);
+  } else {
+    constexpr int kEach = (kReads + kProducts - 1) / kProducts;
+#pragma unroll
+    for (int i = 0; i < kProducts; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, kProducts, 0);
   }
 }
 
@@ -451,24 +478,24 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
   using TileB = Tile<T, b_along(KIND), TN>;
   // arrays of their own, so that a read of one is known not to wait for another's loads
   __shared__ __align__(16) char a0[kA], b0[kB], a1[kA], b1[kB], a2[ALIGNED ? kA : 16], b2[ALIGNED ? kB : 16];
-  const TileId id = tile_of(blockIdx.x, p.tiles_m * (KIND == kWeight ? 2 : 1), p.tiles_n, p.splits);
-  const int z = KIND == kWeight && id.tm >= p.tiles_m ? 1 : 0;
-  const int64_t tm = id.tm - z * p.tiles_m, tn = id.tn, split = id.share;
+  const TileId id = tile_of((uint32_t)p.tiles_m * (KIND == kWeight ? 2 : 1), (uint32_t)p.tiles_n, (uint32_t)p.splits);
+  const int z = KIND == kWeight && id.tm >= p.tiles_m ? 1 : 0, split = id.share;
+  const int64_t tm = id.tm - z * p.tiles_m, tn = id.tn;
   if (KIND == kWeight && !p.out[z]) return;  // not wanted
   // steps of the sum: the whole ones of every part, then what is left of each;
   // this workgroup's are [from, to)
-  const int64_t whole = ALIGNED ? p.K / kStep<T> : (p.K + kStep<T> - 1) / kStep<T>;
-  const int64_t all = (p.K + kStep<T> - 1) / kStep<T> * p.parts, direct = whole * p.parts;
-  const int64_t share = (all + p.splits - 1) / p.splits, from = split * share;
-  const int64_t to = from + share < all ? from + share : all;
-  const auto place = [&](int64_t s, int& part, int64_t& k0) {
+  const int left = (int)(p.K % kStep<T>), whole = (int)(p.K / kStep<T>) + (!ALIGNED && left ? 1 : 0);
+  const int direct = whole * p.parts, all = ALIGNED && left ? direct + p.parts : direct;
+  const int share = __builtin_amdgcn_readfirstlane((all + p.splits - 1) / p.splits), from = split * share;
+  const int to = from + share < all ? from + share : all;
+  const auto place = [&](int s, int& part, int64_t& k0) {
     part = 0;
     if (ALIGNED && s >= direct) {
-      part = (int)(s - direct);
-      k0 = whole * kStep<T>;
+      part = s - direct;
+      k0 = (int64_t)whole * kStep<T>;
     } else {
       if (KIND == kInput && s >= whole) part = 1;
-      k0 = (s - part * whole) * kStep<T>;
+      k0 = (int64_t)(s - part * whole) * kStep<T>;
     }
   };
   const auto base_a = [&](int part) { return p.A + (KIND == kWeight ? z : part) * p.stepA; };
@@ -480,7 +507,7 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
   u32x4 ra[TileA::kChunks], rb[TileB::kChunks];
-  const auto fetch = [&](int64_t s) {
+  const auto fetch = [&](int s) {
     int part;
     int64_t k0;
     place(s, part, k0);
@@ -511,13 +538,8 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
       else
         offB[i] = TileB::offset(p.pitchB, tn * TN, p.N, i);
     }
-    const auto load = [&](int64_t s, char* la, char* lb) {
-      if (s >= to) return;
-      if (s >= direct) {
-        fetch(s);
-        put(la, lb);
-        return;
-      }
+    const int last = to < direct ? to : direct;  // of those that go straight to LDS
+    const auto load = [&](int s, char* la, char* lb) {
       int part;
       int64_t k0;
       place(s, part, k0);
@@ -533,22 +555,28 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
         load_chunks(p.B[KIND == kInput ? part : 0] + k0 * p.pitchB + tn * TN, offB, lb);
       }
     };
-    const int64_t last = to < direct ? to : direct;  // of those that go straight to LDS
-    const auto step = [&](int64_t s, char* la, char* lb, char* na, char* nb) {
-      if (s >= to) return;
+    const auto step = [&](int s, char* la, char* lb, char* na, char* nb) {
+      if (s >= last) return;
       if (s + 1 < last)
         wait_loads<FM + FN>();
       else
         wait_loads<0>();
-      load(s + 2, na, nb);
+      if (s + 2 < last) load(s + 2, na, nb);
       multiply_step<T, KIND, FM, FN>(la, lb, acc);
     };
-    load(from, a0, b0);
-    load(from + 1, a1, b1);
-    for (int64_t s = from; s < to; s += 3) {
+    if (from < last) load(from, a0, b0);
+    if (from + 1 < last) load(from + 1, a1, b1);
+    for (int s = from; s < last; s += 3) {
       step(s, a0, b0, a2, b2);
       step(s + 1, a1, b1, a0, b0);
       step(s + 2, a2, b2, a1, b1);
+    }
+    for (int s = from > direct ? from : direct; s < to; ++s) {
+      __syncthreads();
+      fetch(s);
+      put(a0, b0);
+      __syncthreads();
+      multiply_step<T, KIND, FM, FN>(a0, b0, acc);
     }
   } else {
     if (from < to) {
@@ -556,14 +584,14 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
       put(a0, b0);
     }
     __syncthreads();
-    const auto step = [&](int64_t s, char* la, char* lb, char* na, char* nb) {
+    const auto step = [&](int s, char* la, char* lb, char* na, char* nb) {
       if (s >= to) return;
       if (s + 1 < to) fetch(s + 1);
       multiply_step<T, KIND, FM, FN>(la, lb, acc);
       if (s + 1 < to) put(na, nb);
       __syncthreads();
     };
-    for (int64_t s = from; s < to; s += 2) {
+    for (int s = from; s < to; s += 2) {
       step(s, a0, b0, a1, b1);
       step(s + 1, a1, b1, a0, b0);
     }
