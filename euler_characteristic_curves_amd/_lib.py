@@ -139,12 +139,13 @@ def _load():
     lib.ecc_gated_recurrence_fwd.restype = I
     lib.ecc_gated_recurrence_bwd.argtypes = [P, P, I, I64, I64, I64, P, P, P, P, P, P, P, P, SZ, P]
     lib.ecc_gated_recurrence_bwd.restype = I
-    lib.ecc_gated_linear_fwd.argtypes = [P, I, I64, I64, I64, P, P, P, P, I, P, P]
+    lib.ecc_gated_linear_fwd.argtypes = [P, I, I64, I64, I64, P, P, P, P, I, P, P, SZ, P]
     lib.ecc_gated_linear_fwd.restype = I
     lib.ecc_gated_linear_bwd.argtypes = [P, I, I64, I64, I64, P, P, P, P, I, P, P, P, P, P, P, P, SZ, P]
     lib.ecc_gated_linear_bwd.restype = I
-    for sizes in (lib.ecc_gated_recurrence_workspace_bytes, lib.ecc_gated_recurrence_saved_bytes,
-                  lib.ecc_gated_linear_workspace_bytes):
+    lib.ecc_gated_linear_workspace_bytes.argtypes = [I64, I64, I64, I, I]
+    lib.ecc_gated_linear_workspace_bytes.restype = SZ
+    for sizes in (lib.ecc_gated_recurrence_workspace_bytes, lib.ecc_gated_recurrence_saved_bytes):
         sizes.argtypes = [I64, I64, I64, I]
         sizes.restype = SZ
     lib.ecc_status_string.argtypes = [I]

@@ -235,18 +235,23 @@ int ecc_gated_recurrence_bwd(const void* x, const void* gate, int dtype, int64_t
   return hip_status(ecc::launch_recurrence_bwd<ecc::bf16>(a, s));
 }
 
-size_t ecc_gated_linear_workspace_bytes(int64_t rows, int64_t channels, int64_t hidden, int dtype) {
+size_t ecc_gated_linear_workspace_bytes(int64_t rows, int64_t channels, int64_t hidden, int dtype, int backward) {
   if (check_glu_shape(rows, channels, hidden, dtype) != ECC_OK) return 0;
-  return ecc::glu_plan(rows, channels, hidden, dtype == ECC_T_F32 ? 4 : 2).bytes;
+  return ecc::glu_plan(rows, channels, hidden, dtype == ECC_T_F32 ? 4 : 2, backward != 0).bytes;
 }
 
 int ecc_gated_linear_fwd(const void* x, int dtype, int64_t rows, int64_t channels, int64_t hidden, const void* w_gate,
-                         const void* w_up, const void* b_gate, const void* b_up, int act, void* h, void* stream) {
+                         const void* w_up, const void* b_gate, const void* b_up, int act, void* h, void* ws, size_t ws_bytes,
+                         void* stream) {
   ecc::GluArgs a;
-  const int st = check_glu(a, x, dtype, rows, channels, hidden, w_gate, w_up, b_gate, b_up, act);
+  int st = check_glu(a, x, dtype, rows, channels, hidden, w_gate, w_up, b_gate, b_up, act);
   if (st != ECC_OK) return st;
   if (!h) return fail(ECC_E_NULL, "h is NULL");
+  const ecc::GluPlan plan = ecc::glu_plan(rows, channels, hidden, dtype == ECC_T_F32 ? 4 : 2, false);
+  if (plan.packed) st = check_workspace(ws, ws_bytes, plan.bytes);
+  if (st != ECC_OK) return st;
   a.h = h;
+  a.ws = ws;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (dtype == ECC_T_F32) return hip_status(ecc::launch_glu_fwd<float>(a, s));
   if (dtype == ECC_T_F16) return hip_status(ecc::launch_glu_fwd<ecc::f16>(a, s));
@@ -265,7 +270,7 @@ int ecc_gated_linear_bwd(const void* x, int dtype, int64_t rows, int64_t channel
     return fail(ECC_E_NULL, "every gradient is NULL");
   if ((grad_b_gate && !b_gate) || (grad_b_up && !b_up))
     return fail(ECC_E_NULL, "a gradient of an argument that is NULL is wanted");
-  st = check_workspace(ws, ws_bytes, ecc::glu_plan(rows, channels, hidden, dtype == ECC_T_F32 ? 4 : 2).bytes);
+  st = check_workspace(ws, ws_bytes, ecc::glu_plan(rows, channels, hidden, dtype == ECC_T_F32 ? 4 : 2, true).bytes);
   if (st != ECC_OK) return st;
   a.gh = grad_h;
   a.gx = grad_x;

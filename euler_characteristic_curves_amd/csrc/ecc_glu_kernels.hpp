@@ -536,7 +536,7 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
       if constexpr (is_dual(KIND))
         offB[i] = Tile<T, true, 64>::offset(p.pitchB, tn * 64, p.N, 0);
       else
-        offB[i] = TileB::offset(p.pitchB, tn * TN, p.N, i);
+        offB[i] = TileB::offset(p.pitchB, tn * TN, b_along(KIND) ? p.N : p.pitchB, i);
     }
     const int last = to < direct ? to : direct;  // of those that go straight to LDS
     const auto load = [&](int s, char* la, char* lb) {
@@ -598,7 +598,7 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
   }
   if (p.splits > 1) {
     const int64_t tile = id.tm * p.tiles_n + tn;
-    float* out = p.part + ((tile * p.splits + split) * kNT + threadIdx.x) * (FM * FN * 16);
+    float* out = p.part + (tile * p.splits + split) * (kNT * FM * FN * 16) + threadIdx.x * 4;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -608,7 +608,7 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
           f32x4 v;
 #pragma unroll
           for (int r = 0; r < 4; ++r) v[r] = acc[i][j][q * 4 + r];
-          *reinterpret_cast<f32x4*>(out + (i * FN + j) * 16 + q * 4) = v;
+          *reinterpret_cast<f32x4*>(out + ((i * FN + j) * 4 + q) * (kNT * 4)) = v;
         }
     return;
   }
@@ -617,37 +617,47 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
   epilogue<T, KIND, FM, FN, ACT>(p, z, tm, tn, acc, (wave & 2 ? b1 : b0) + (wave & 1) * kStage, reinterpret_cast<float*>(a0));
 }
 
-// Joins the shares of a tile, in order.  One fragment of four waves a workgroup.
+constexpr int kJoin = 1024;
+
+// Joins the shares of a tile, each of four groups of threads every fourth one,
+// in order.  A workgroup has one fragment of each of the four waves.
 template <class T, int KIND, int FM, int FN>
-__global__ __launch_bounds__(kNT) void glu_join_kernel(Product<T> p) {
-  __shared__ __align__(16) char lds[4 * kStage];
-  int64_t id = blockIdx.x;
-  if (!p.out[id / (p.tiles_n * p.tiles_m)]) return;
-  const int i = blockIdx.y / FN, j = blockIdx.y % FN;
-  const float* in = p.part + ((id * p.splits) * kNT + threadIdx.x) * (FM * FN * 16) + (i * FN + j) * 16;
-  float v[16] = {};
+__global__ __launch_bounds__(kJoin) void glu_join_kernel(Product<T> p) {
+  __shared__ f32x4 lds[3][4][kNT];
+  __shared__ __align__(16) char staged[4 * kStage];
+  const int64_t tile = blockIdx.x;
+  const int z = (int)(tile / (p.tiles_n * p.tiles_m));
+  if (!p.out[z]) return;
+  const int j = blockIdx.y % FN, i = blockIdx.y / FN;
+  const int thread = threadIdx.x & (kNT - 1), group = threadIdx.x / kNT;
+  constexpr int64_t next = (int64_t)kNT * (FM * FN * 16);  // from one share to the next
+  const float* in = p.part + tile * p.splits * next + (i * FN + j) * (kNT * 16) + thread * 4;
+  f32x4 v[4] = {};
 #pragma unroll 4
-  for (int s = 0; s < p.splits; ++s) {
+  for (int s = group; s < p.splits; s += 4)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const f32x4 u = *reinterpret_cast<const f32x4*>(in + (int64_t)s * kNT * (FM * FN * 16) + q * 4);
+    for (int q = 0; q < 4; ++q) v[q] += *reinterpret_cast<const f32x4*>(in + s * next + q * (kNT * 4));
+  if (group)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[q * 4 + r] += u[r];
-    }
+    for (int q = 0; q < 4; ++q) lds[group - 1][q][thread] = v[q];
+  __syncthreads();
+  if (group) return;
+  float u[16];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    for (int g = 0; g < 3; ++g) v[q] += lds[g][q][thread];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) u[q * 4 + r] = v[q][r];
   }
-  const int64_t tn = id % p.tiles_n;
-  id /= p.tiles_n;
-  const int64_t tm = id % p.tiles_m;
-  const int z = (int)(id / p.tiles_m);
-  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const int64_t tn = tile % p.tiles_n, tm = tile / p.tiles_n - z * p.tiles_m;
+  const int wave = __builtin_amdgcn_readfirstlane(thread >> 6), wm = wave >> 1, wn = wave & 1;
   const int64_t row = tm * 64 * FM + wm * FM * 32 + i * 32, col = tn * 64 * FN + wn * FN * 32 + j * 32;
-  const Stage<T> stage{lds + wave * kStage};
-  stage.put(v);
+  const Stage<T> stage{staged + wave * kStage};
+  stage.put(u);
   stage.store(p.out[z] + row * p.pitch_out + col, p.pitch_out, p.M - row, p.N - col);
 }
 
 // Bias gradients from the tiles' sums, in float64.  16 units a workgroup.
-constexpr int kJoin = 1024;
 template <class T>
 __global__ __launch_bounds__(kJoin) void glu_bias_kernel(Product<T> p) {
   __shared__ double lds[kJoin / 16][17];
@@ -667,6 +677,129 @@ __global__ __launch_bounds__(kJoin) void glu_bias_kernel(Product<T> p) {
     __syncthreads();
   }
   if (r == 0 && unit < p.N) out[unit] = (T)(float)lds[0][c];
+}
+
+// ---------------------------------------------------------------- few rows
+__device__ __forceinline__ f32x4 multiply16(const Fragment<f16>& a, const Fragment<f16>& b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a.v), __builtin_bit_cast(f16x8, b.v), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 multiply16(const Fragment<bf16>& a, const Fragment<bf16>& b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.v), __builtin_bit_cast(bf16x8, b.v), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 multiply16(const Fragment<float>& a, const Fragment<float>& b, f32x4 c) {
+  const f32x4 u = __builtin_bit_cast(f32x4, a.v), v = __builtin_bit_cast(f32x4, b.v);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(u[j], v[j], c, 0, 0, 0);
+  return c;
+}
+
+// Up to 16 RB rows: bound by the weights' one way from memory.  A workgroup has
+// 16 hidden units of both projections, its eight waves every eighth step of the
+// sum each, whose operands go straight to the registers; everything is on its
+// way at once.  (1 x 1024 to 2816, bfloat16, 11.5 MB: 9.8 us in tiles.)
+constexpr int kFewThreads = 512;
+template <class T, int RB>
+__global__ __launch_bounds__(kFewThreads) void glu_few_kernel(Product<T> p) {
+  constexpr int kWaves = kFewThreads / 64, kAhead = RB == 1 ? 4 : 2;
+  __shared__ f32x4 lds[kWaves][2][RB][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, line = lane & 15, chunk = lane >> 4;
+  const int64_t unit0 = (int64_t)blockIdx.x * 16, unit = unit0 + line < p.N ? unit0 + line : p.N - 1;
+  const T* w[2] = {p.B[0] + unit * p.pitchB, p.B[1] + unit * p.pitchB};
+  const auto fetch = [&](const T* at, int64_t k) {
+    Fragment<T> f;
+    if (k + kPer<T> <= p.K) {
+      __builtin_memcpy(&f.v, at + k, 16);
+    } else {  // zeros behind the end
+      Vec<T, kPer<T>> v = {};
+#pragma unroll
+      for (int j = 0; j < kPer<T> - 1; ++j)
+        if (k + j < p.K) v.v[j] = at[k + j];
+      __builtin_memcpy(&f.v, &v, 16);
+    }
+    return f;
+  };
+  f32x4 acc[2][RB];
+#pragma unroll
+  for (int z = 0; z < 2; ++z)
+#pragma unroll
+    for (int i = 0; i < RB; ++i) acc[z][i] = f32x4{};
+  const int64_t steps = (p.K + kStep<T> - 1) / kStep<T>;
+  for (int64_t s0 = wave; s0 < steps; s0 += kWaves * kAhead) {
+    Fragment<T> a[kAhead][2], b[kAhead][RB];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t k = (s0 + u * kWaves) * kStep<T> + chunk * kPer<T>;
+#pragma unroll
+      for (int z = 0; z < 2; ++z) a[u][z] = fetch(w[z], k);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        const int64_t row = i * 16 + line;
+        b[u][i] = fetch(p.A + (row < p.M ? row : p.M - 1) * p.pitchA, k);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int i = 0; i < RB; ++i) acc[z][i] = multiply16(a[u][z], b[u][i], acc[z][i]);
+  }
+#pragma unroll
+  for (int z = 0; z < 2; ++z)
+#pragma unroll
+    for (int i = 0; i < RB; ++i) lds[wave][z][i][lane] = acc[z][i];
+  __syncthreads();
+  // a thread for every result: unit and row within the 16 x 16 block
+  const float* all = reinterpret_cast<const float*>(lds);
+  for (int id = threadIdx.x; id < RB * 256; id += kFewThreads) {
+    const int i = id >> 8, u = id & 15, r = id >> 4 & 15;
+    const int64_t row = i * 16 + r, at = unit0 + u;
+    if (row >= p.M || at >= p.N) continue;
+    float v[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const void* bias = z ? p.a.bu : p.a.bg;
+      float s = 0.0f;
+#pragma unroll
+      for (int g = 0; g < kWaves; ++g) s += all[(((g * 2 + z) * RB + i) * 64 + (u >> 2) * 16 + r) * 4 + (u & 3)];
+      v[z] = s + (bias ? (float)reinterpret_cast<const T*>(bias)[at] : 0.0f);
+    }
+    float y = v[0];
+    if (p.a.act == kActRelu) y = act_value<kActRelu>(y);
+    if (p.a.act == kActSilu) y = act_value<kActSilu>(y);
+    if (p.a.act == kActGelu) y = act_value<kActGelu>(y);
+    reinterpret_cast<T*>(p.a.h)[row * p.N + at] = (T)(y * v[1]);
+  }
+}
+
+// --------------------------------------------------------------- packing
+// x and the weights with rows of `wide` elements, zeros at the end of each.
+template <class T>
+__global__ __launch_bounds__(kNT) void glu_pack_kernel(GluArgs a, T* x, T* wg, T* wu, int64_t wide) {
+  const int64_t chunks = wide / kPer<T>, all = (a.rows + 2 * a.hidden) * chunks;
+  for (int64_t id = (int64_t)blockIdx.x * kNT + threadIdx.x; id < all; id += (int64_t)gridDim.x * kNT) {
+    int64_t row = id / chunks;
+    const int64_t k = (id - row * chunks) * kPer<T>;
+    const T* in = reinterpret_cast<const T*>(a.x);
+    T* out = x;
+    if (row >= a.rows) {
+      row -= a.rows;
+      const bool up = row >= a.hidden;
+      if (up) row -= a.hidden;
+      in = reinterpret_cast<const T*>(up ? a.wu : a.wg);
+      out = up ? wu : wg;
+    }
+    in += row * a.channels + k;
+    Vec<T, kPer<T>> v = {};
+    if (k + kPer<T> <= a.channels) {
+      load_vec(in, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer<T> - 1; ++j)
+        if (k + j < a.channels) v.v[j] = in[j];
+    }
+    store_vec(out + row * wide + k, v);
+  }
 }
 
 // ---------------------------------------------------------------- launches
@@ -703,7 +836,7 @@ hipError_t launch_tiles(Product<T> p, hipStream_t stream) {
   }
   if constexpr (!is_dual(KIND)) {
     if (p.splits > 1)
-      hipLaunchKernelGGL((glu_join_kernel<T, KIND, FM, 2>), dim3((unsigned)tiles, FM * 2), dim3(kNT), 0, stream, p);
+      hipLaunchKernelGGL((glu_join_kernel<T, KIND, FM, 2>), dim3((unsigned)tiles, FM * 2), dim3(kJoin), 0, stream, p);
   }
   return hipGetLastError();
 }
@@ -715,8 +848,9 @@ hipError_t launch_product(Product<T> p, const GluShare& s, hipStream_t stream) {
   return s.FM == 4 ? launch_tiles<T, KIND, 4>(p, stream) : launch_tiles<T, KIND, 1>(p, stream);
 }
 
+// The projections' product, of packed operands if there are any.
 template <class T>
-Product<T> projections(const GluArgs& a) {
+Product<T> projections(const GluArgs& a, const GluPlan& plan, hipStream_t stream) {
   Product<T> p{};
   p.A = reinterpret_cast<const T*>(a.x);
   p.pitchA = p.pitchB = p.K = a.channels;
@@ -726,6 +860,18 @@ Product<T> projections(const GluArgs& a) {
   p.N = a.hidden;
   p.parts = 1;
   p.a = a;
+  if (plan.packed) {
+    char* ws = reinterpret_cast<char*>(a.ws);
+    T *x = reinterpret_cast<T*>(ws + plan.at_x), *wg = reinterpret_cast<T*>(ws + plan.at_wg),
+      *wu = reinterpret_cast<T*>(ws + plan.at_wu);
+    const int64_t blocks = ((a.rows + 2 * a.hidden) * (plan.wide / kPer<T>) + kNT - 1) / kNT;
+    hipLaunchKernelGGL(glu_pack_kernel<T>, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(kNT), 0, stream, a, x, wg,
+                       wu, plan.wide);
+    p.A = x;
+    p.B[0] = wg;
+    p.B[1] = wu;
+    p.pitchA = p.pitchB = p.K = plan.wide;
+  }
   return p;
 }
 
@@ -733,16 +879,27 @@ Product<T> projections(const GluArgs& a) {
 
 template <class T>
 hipError_t launch_glu_fwd(const GluArgs& a, hipStream_t stream) {
-  return launch_product<T, kForward>(projections<T>(a), glu_plan(a.rows, a.channels, a.hidden, sizeof(T)).gates, stream);
+  const GluPlan plan = glu_plan(a.rows, a.channels, a.hidden, sizeof(T), false);
+  const Product<T> p = projections<T>(a, plan, stream);
+  if (a.rows > kGluFew) return launch_product<T, kForward>(p, plan.gates, stream);
+  const dim3 grid((unsigned)((a.hidden + 15) / 16)), block(kFewThreads);
+  if (a.rows <= 16)
+    hipLaunchKernelGGL((glu_few_kernel<T, 1>), grid, block, 0, stream, p);
+  else if (a.rows <= 32)
+    hipLaunchKernelGGL((glu_few_kernel<T, 2>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((glu_few_kernel<T, 4>), grid, block, 0, stream, p);
+  return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch_glu_bwd(const GluArgs& a, hipStream_t stream) {
-  const GluPlan plan = glu_plan(a.rows, a.channels, a.hidden, sizeof(T));
+  const GluPlan plan = glu_plan(a.rows, a.channels, a.hidden, sizeof(T), true);
   char* ws = reinterpret_cast<char*>(a.ws);
-  Product<T> p = projections<T>(a);
+  Product<T> p = projections<T>(a, plan, stream);
+  const T* x = p.A;
   p.pitch = plan.pitch;
-  p.dab = reinterpret_cast<T*>(ws);
+  p.dab = reinterpret_cast<T*>(ws + plan.at_dab);
   p.bias = a.gbg || a.gbu ? reinterpret_cast<float*>(ws + plan.at_bias) : nullptr;
   p.part = reinterpret_cast<float*>(ws + plan.at_part);
   hipError_t st = launch_product<T, kGates>(p, plan.gates, stream);
@@ -768,7 +925,7 @@ hipError_t launch_glu_bwd(const GluArgs& a, hipStream_t stream) {
     p.N = a.channels;
     p.K = a.rows;
     p.parts = 1;
-    p.B[0] = p.B[1] = reinterpret_cast<const T*>(a.x);
+    p.B[0] = p.B[1] = x;
     p.out[0] = reinterpret_cast<T*>(a.gwg);
     p.out[1] = reinterpret_cast<T*>(a.gwu);
     p.pitch_out = a.channels;

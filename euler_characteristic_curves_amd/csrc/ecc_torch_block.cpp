@@ -205,10 +205,13 @@ at::Tensor glu_forward(const GluPlan& p, const at::Tensor& x, const at::Tensor& 
   std::vector<int64_t> sizes = x.sizes().vec();
   sizes.back() = p.hidden;
   at::Tensor h = at::empty(sizes, x.options().requires_grad(false));
-  if (h.numel())
-    check(ecc_gated_linear_fwd(ptr(x), (int)p.dtype, p.rows, p.channels, p.hidden, ptr(wg), ptr(wu), ptr(bg), ptr(bu),
-                               (int)p.act, h.data_ptr(), stream_of(x)),
-          "ecc_gated_linear_fwd");
+  if (!h.numel()) return h;
+  const int64_t bytes = ecc_gated_linear_workspace_bytes(p.rows, p.channels, p.hidden, (int)p.dtype, 0);
+  at::Tensor ws;
+  if (bytes > 256) ws = bytes_like(x, bytes);  // no workspace otherwise
+  check(ecc_gated_linear_fwd(ptr(x), (int)p.dtype, p.rows, p.channels, p.hidden, ptr(wg), ptr(wu), ptr(bg), ptr(bu),
+                             (int)p.act, h.data_ptr(), out_ptr(ws), ws.defined() ? bytes : 0, stream_of(x)),
+        "ecc_gated_linear_fwd");
   return h;
 }
 
@@ -234,7 +237,7 @@ struct Glu : torch::autograd::Function<Glu> {
     const c10::DeviceGuard guard(x.device());
     const bool any = gradients(ctx, in, wanted, !p[0]);
     if (any && p[0]) {
-      const int64_t bytes = ecc_gated_linear_workspace_bytes(p[0], p[1], p[2], (int)p[3]);
+      const int64_t bytes = ecc_gated_linear_workspace_bytes(p[0], p[1], p[2], (int)p[3], 1);
       at::Tensor ws = bytes_like(x, bytes);
       check(ecc_gated_linear_bwd(ptr(x), (int)p[3], p[0], p[1], p[2], ptr(in[1]), ptr(in[2]), ptr(in[3]), ptr(in[4]),
                                  (int)p[4], ptr(g), out_ptr(wanted[0]), out_ptr(wanted[1]), out_ptr(wanted[2]),

@@ -241,10 +241,12 @@ size_t ecc_gated_recurrence_saved_bytes(int64_t batch, int64_t steps, int64_t ch
  *   act           of the first projection, ECC_ACT_*
  *   h             dtype, [rows][hidden]; overlaps no input
  * channels, hidden <= ECC_MAX_MATRIX.  Sums are float32, h is rounded once.  One
- * launch, no workspace.
+ * launch; one more, and a workspace, only where rows > 64 and x's rows are not
+ * whole 16-byte chunks (ws may be NULL otherwise).
  */
 int ecc_gated_linear_fwd(const void* x, int dtype, int64_t rows, int64_t channels, int64_t hidden, const void* w_gate,
-                         const void* w_up, const void* b_gate, const void* b_up, int act, void* h, void* stream);
+                         const void* w_up, const void* b_gate, const void* b_up, int act, void* h, void* ws, size_t ws_bytes,
+                         void* stream);
 
 /*
  * Its backward pass from grad_h = dL/dh (dtype, [rows][hidden]); the two
@@ -260,8 +262,8 @@ int ecc_gated_linear_bwd(const void* x, int dtype, int64_t rows, int64_t channel
                          void* grad_w_gate, void* grad_w_up, void* grad_b_gate, void* grad_b_up, void* ws, size_t ws_bytes,
                          void* stream);
 
-/* Workspace bytes of the backward pass (0 for invalid sizes). */
-size_t ecc_gated_linear_workspace_bytes(int64_t rows, int64_t channels, int64_t hidden, int dtype);
+/* Workspace bytes of either call (0 for invalid sizes). */
+size_t ecc_gated_linear_workspace_bytes(int64_t rows, int64_t channels, int64_t hidden, int dtype, int backward);
 
 #ifdef __cplusplus
 }

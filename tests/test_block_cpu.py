@@ -64,11 +64,11 @@ def test_residual_workspace(L):
     assert f(1, 1 << 28, 1024, 0) <= (1 << 28) // 256 * 3 * 1024 * 4 + 256
 
 
-def glu_fwd(L, x=FAKE, d=0, R=9, C=8, H=10, wg=FAKE, wu=FAKE, act=2, h=FAKE, ws=None, wsb=None):
-    return L.lib.ecc_gated_linear_fwd(x, d, R, C, H, wg, wu, None, None, act, h, None)
+def glu_fwd(L, x=FAKE, d=0, R=90, C=9, H=10, wg=FAKE, wu=FAKE, act=2, h=FAKE, ws=FAKE, wsb=1 << 40):
+    return L.lib.ecc_gated_linear_fwd(x, d, R, C, H, wg, wu, None, None, act, h, ws, wsb, None)
 
 
-def glu_bwd(L, x=FAKE, d=0, R=9, C=8, H=10, wg=FAKE, wu=FAKE, act=2, h=FAKE, g=(FAKE, FAKE, FAKE, None, None), ws=FAKE,
+def glu_bwd(L, x=FAKE, d=0, R=90, C=9, H=10, wg=FAKE, wu=FAKE, act=2, h=FAKE, g=(FAKE, FAKE, FAKE, None, None), ws=FAKE,
             wsb=1 << 40):
     return L.lib.ecc_gated_linear_bwd(x, d, R, C, H, wg, wu, None, None, act, h, *g, ws, wsb, None)
 
@@ -83,17 +83,23 @@ def test_gated_linear_argument_errors(L, call):
     if call is glu_bwd:
         assert call(L, g=(None,) * 5) == L.ECC_E_NULL
         assert call(L, g=(FAKE,) * 4 + (None,)) == L.ECC_E_NULL  # of a bias that is not there
-        assert call(L, ws=None) == L.ECC_E_WORKSPACE
-        assert call(L, wsb=L.lib.ecc_gated_linear_workspace_bytes(9, 8, 10, 0) - 1) == L.ECC_E_WORKSPACE
+    assert call(L, ws=None) == L.ECC_E_WORKSPACE
+    need = L.lib.ecc_gated_linear_workspace_bytes(90, 9, 10, 0, int(call is glu_bwd))
+    assert call(L, wsb=need - 1) == L.ECC_E_WORKSPACE
 
 
 def test_gated_linear_workspace(L):
-    f = L.lib.ecc_gated_linear_workspace_bytes
+    def f(*a):
+        return L.lib.ecc_gated_linear_workspace_bytes(*a, 1)
+
     assert f(0, 8, 8, 0) == f(1, 0, 8, 0) == f(1, 8, 0, 0) == f(1, 8, 8, 3) == 0
     # both projections' gradients, and at most as much again and some shares
     for rows, c, h, e in ((1 << 16, 64, 160, 2), (1 << 14, 1024, 2816, 2), (4000, 333, 877, 0)):
         size = rows * 2 * (h + 63) * (2 if e else 4)
         assert rows * 2 * h * (2 if e else 4) <= f(rows, c, h, e) <= 2 * size + 512 * 256 * 128 * 4
+    # forward: nothing, or copies of the operands
+    for R, C, want in ((64, 9, 256), (1 << 20, 1024, 256), (65, 9, (65 + 20) * 16 * 4 + 3 * 256)):
+        assert L.lib.ecc_gated_linear_workspace_bytes(R, C, 10, 0, 0) <= want
 
 
 def rec_fwd(L, x=FAKE, f=FAKE, d=0, B=2, T=9, C=8, n=None, h=FAKE, last=FAKE, ws=FAKE, wsb=1 << 40):
