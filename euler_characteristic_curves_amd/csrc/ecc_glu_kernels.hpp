@@ -125,21 +125,29 @@ struct Tile {
   }
 };
 
-// This thread's chunks of a step, straight to LDS: the base is the same for all
-// lanes, and so is where a wave's 64 chunks go.  In assembly, because the compiler
-// would wait for all such loads before it reads what one of them may have
-// written, as it cannot tell which are complete; the waits are wait_loads.  (m0
-// is not the compiler's to keep anything in.)
-template <int N>
-__device__ __forceinline__ void load_chunks(const void* step, const uint32_t (&offset)[N], char* lds) {
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds + wave * 1024;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :
-                 : "s"(to + i * (kNT * 16)), "v"(offset[i]), "s"(step)
-                 : "memory");
+// One of this thread's chunks of step s, straight to LDS, if s is before `last`:
+// the base is the same for all lanes, and so is where a wave's 64 chunks go.  In
+// assembly, because the compiler would wait for all such loads before it reads
+// what one of them may have written, as it cannot tell which are complete; the
+// waits are wait_loads.  (m0 is not the compiler's to keep anything in.)
+__device__ __forceinline__ void load_chunk(const void* step, uint32_t offset, uint32_t lds, int s, int last) {
+  // (uniform values do not always stay in scalar registers)
+  const uint64_t at = (uint64_t)step;
+  const uint64_t base = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at) |
+                        (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)) << 32;
+  s = __builtin_amdgcn_readfirstlane(s);
+  last = __builtin_amdgcn_readfirstlane(last);
+  asm volatile(
+      "s_cmp_ge_i32 %3, %4\n\ts_cbranch_scc1 .Lnot_wanted%=\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2\n.Lnot_wanted%=:"
+      :
+      : "s"(lds), "v"(offset), "s"(base), "s"(s), "s"(last)
+      : "memory", "scc");
+}
+// Where this wave's part of a tile begins in LDS.
+__device__ __forceinline__ uint32_t wave_lds(char* lds) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds +
+         __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
 }
 
 // Waits for all but the newest VM loads of this wave and for what it has read
@@ -425,45 +433,36 @@ __device__ __forceinline__ TileId tile_of(uint32_t rows, uint32_t cols, uint32_t
 }
 
 // ---------------------------------------------------------------- products
-template <class T, int KIND, int FM, int FN>
-__device__ __forceinline__ void multiply_step(const char* la, const char* lb, f32x16 (&acc)[FM][FN]) {
+// A step from LDS.  The second half's reads stand between the first half's
+// products, and so do loads of a later step, `load(i)` with i below FM + FN, one
+// with every second product: issued together, before the first read, they kept
+// the wave from it for as long as the memory unit took to accept them.
+template <class T, int KIND, int FM, int FN, class Load>
+__device__ __forceinline__ void multiply_step(const char* la, const char* lb, f32x16 (&acc)[FM][FN], Load load) {
   constexpr int TM = 64 * FM, TN = 64 * FN;
   const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
   Fragment<T> a[2][FM], b[2][FN];
+  const auto read = [&](int c, int n) {  // fragment n of half c
+    if (n < FN)
+      b[c][n] = read_fragment<T, b_along(KIND), TN>(lb, is_dual(KIND) ? n * 64 + wn * 32 : wn * FN * 32 + n * 32, c);
+    else
+      a[c][n - FN] = read_fragment<T, a_along(KIND), TM>(la, wm * FM * 32 + (n - FN) * 32, c);
+  };
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
+  for (int n = 0; n < FM + FN; ++n) read(0, n);
+  constexpr int kProducts = FM * FN, kAll = FM + FN;
+  int reads = 0, loads = 0;
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-      b[c][j] = read_fragment<T, b_along(KIND), TN>(lb, is_dual(KIND) ? j * 64 + wn * 32 : wn * FN * 32 + j * 32, c);
+  for (int n = 0; n < 2 * kProducts; ++n) {
+    const int c = n / kProducts, i = n % kProducts / FN, j = n % FN;
+    acc[i][j] = multiply(b[c][j], a[c][i], acc[i][j]);
+    // (n + 1) kAll / kProducts reads by now, and half as many loads
 #pragma unroll
-    for (int i = 0; i < FM; ++i) a[c][i] = read_fragment<T, a_along(KIND), TM>(la, wm * FM * 32 + i * 32, c);
-  }
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) acc[i][j] = multiply(b[c][j], a[c][i], acc[i][j]);
-  // the first half's reads, then the others' between the first half's products
-  constexpr int kTurned = sizeof(T) == 4 ? 4 : 2;
-  constexpr int kReads = FM * (a_along(KIND) ? 1 : kTurned) + FN * (b_along(KIND) ? 1 : kTurned);
-  constexpr int kProducts = FM * FN * (sizeof(T) == 4 ? 4 : 1);
-  __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
-  if constexpr (kReads <= kProducts) {
-#pragma unroll
-    for (int i = 0; i < kReads; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    for (int k = 0; k < kAll; ++k) {
+      if (reads < kAll && reads * kProducts < (n + 1) * kAll) read(1, reads++);
+      if (loads < kAll && loads * 2 * kProducts < (n + 1) * kAll) load(loads++);
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, 2 * kProducts - kReads, 0);
-  } else {
-    constexpr int kEach = (kReads + kProducts - 1) / kProducts;
-#pragma unroll
-    for (int i = 0; i < kProducts; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x008, kProducts, 0);
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -539,33 +538,50 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
         offB[i] = TileB::offset(p.pitchB, tn * TN, b_along(KIND) ? p.N : p.pitchB, i);
     }
     const int last = to < direct ? to : direct;  // of those that go straight to LDS
-    const auto load = [&](int s, char* la, char* lb) {
+    const T *const first0 = p.B[0], *const first1 = p.B[1];
+    // a step's first elements of A, and of B (of both projections)
+    struct Bases {
+      const T *a, *b0, *b1;
+    };
+    const auto bases = [&](int s) {
       int part;
       int64_t k0;
       place(s, part, k0);
       const T* A = base_a(part);
-      load_chunks(a_along(KIND) ? A + tm * TM * p.pitchA + k0 : A + k0 * p.pitchA + tm * TM, offA, la);
+      Bases r;
+      r.a = a_along(KIND) ? A + tm * TM * p.pitchA + k0 : A + k0 * p.pitchA + tm * TM;
       if constexpr (is_dual(KIND)) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t one[1] = {offB[i]};
-          load_chunks(p.B[i] + tn * 64 * p.pitchB + k0, one, lb + i * 64 * 64);
-        }
+        r.b0 = first0 + tn * 64 * p.pitchB + k0;
+        r.b1 = first1 + tn * 64 * p.pitchB + k0;
       } else {
-        load_chunks(p.B[KIND == kInput ? part : 0] + k0 * p.pitchB + tn * TN, offB, lb);
+        const T* B = first0;
+        if (KIND == kInput && part) B = first1;
+        r.b0 = r.b1 = B + k0 * p.pitchB + tn * TN;
       }
+      return r;
+    };
+    const auto load = [&](const Bases& r, int s, char* la, char* lb, int i) {  // chunk i, A's first
+      if (i < FM)
+        load_chunk(r.a, offA[i], wave_lds(la) + i * (kNT * 16), s, last);
+      else
+        load_chunk(is_dual(KIND) && i > FM ? r.b1 : r.b0, offB[i - FM], wave_lds(lb) + (i - FM) * (kNT * 16), s, last);
+    };
+    const auto load_all = [&](int s, char* la, char* lb) {
+      const Bases r = bases(s);
+#pragma unroll
+      for (int i = 0; i < FM + FN; ++i) load(r, s, la, lb, i);
     };
     const auto step = [&](int s, char* la, char* lb, char* na, char* nb) {
       if (s >= last) return;
+      const Bases r = bases(s + 2);
       if (s + 1 < last)
         wait_loads<FM + FN>();
       else
         wait_loads<0>();
-      if (s + 2 < last) load(s + 2, na, nb);
-      multiply_step<T, KIND, FM, FN>(la, lb, acc);
+      multiply_step<T, KIND, FM, FN>(la, lb, acc, [&](int i) { load(r, s + 2, na, nb, i); });
     };
-    if (from < last) load(from, a0, b0);
-    if (from + 1 < last) load(from + 1, a1, b1);
+    load_all(from, a0, b0);
+    load_all(from + 1, a1, b1);
     for (int s = from; s < last; s += 3) {
       step(s, a0, b0, a2, b2);
       step(s + 1, a1, b1, a0, b0);
@@ -576,7 +592,7 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
       fetch(s);
       put(a0, b0);
       __syncthreads();
-      multiply_step<T, KIND, FM, FN>(a0, b0, acc);
+      multiply_step<T, KIND, FM, FN>(a0, b0, acc, [](int) {});
     }
   } else {
     if (from < to) {
@@ -587,7 +603,7 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
     const auto step = [&](int s, char* la, char* lb, char* na, char* nb) {
       if (s >= to) return;
       if (s + 1 < to) fetch(s + 1);
-      multiply_step<T, KIND, FM, FN>(la, lb, acc);
+      multiply_step<T, KIND, FM, FN>(la, lb, acc, [](int) {});
       if (s + 1 < to) put(na, nb);
       __syncthreads();
     };
