@@ -52,6 +52,7 @@ ECC_MAX_READOUT_CHANNELS = 1024
 ECC_MAX_NORM_BATCH = 32768
 ECC_MAX_MATRIX = 32768
 ECC_MAX_NS_STEPS = 64
+ECC_MAX_RECURRENCE_CHANNELS = 1048576
 
 TRAIN_EXPORTS = (
     "ecc_norm_fwd", "ecc_norm_bwd", "ecc_norm_readout_fwd", "ecc_norm_readout_bwd", "ecc_norm_workspace_bytes",

@@ -9,7 +9,7 @@
 // Steps from a sequence's length on keep the state (k = 1) and have no input.
 //
 // What is kept of a gate is m, the smaller of k and 1 - k with the gate's sign:
-// a step is then h + m (x - h), or x + |m| (h - x), exact where a state lasts
+// a step is then h + m (x - h), or x - |m| (x - h), exact where a state lasts
 // for thousands of steps as well as where it is replaced.  A run of steps maps h
 // to A h + B; its A is kept twice, as the product of the k and as c = 1 - A, and
 // whichever of the two is small is used, for the same reason.  (Products of
@@ -22,8 +22,8 @@
 // backward pass does so in both directions at once: its forward states start
 // from those that the forward pass kept before every tile.  A sequence is one
 // workgroup's work if there are enough of them, three streams forward and five
-// backward; if not, a pass of its own finds the (A, c, B) of its parts, and
-// reads two streams once more.
+// backward; if not, a pass of its own finds the (A, c, B) of its parts, which
+// reads two streams once more, and a small one the states between them.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -39,27 +39,34 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The smaller of k and 1 - k, with the gate's sign.  The exponent's rounding
-// leaves |gate| 2^-24 relative.
-__device__ __forceinline__ float small_gate(float f) {
+// The smaller of k and 1 - k, with the gate's sign, and k.  The exponent's
+// rounding leaves |gate| 2^-24 relative.
+__device__ __forceinline__ float small_gate(float f, float& k) {
   const float e = __builtin_amdgcn_exp2f(-1.44269502f * fabsf(f));
-  return copysignf(e * __builtin_amdgcn_rcpf(1.0f + e), f);
+  const float r = __builtin_amdgcn_rcpf(1.0f + e), m = e * r;
+  k = __float_as_int(f) < 0 ? m : r;
+  return copysignf(m, f);
 }
 __device__ __forceinline__ bool keeps(float m) { return (__float_as_uint(m) >> 31) == 0; }
 
-// k h + (1 - k) x
-__device__ __forceinline__ float step(float h, float x, float m) {
-  const bool up = keeps(m);
-  const float base = up ? h : x, other = up ? x : h;
-  return fmaf(fabsf(m), other - base, base);
-}
-// k d
-__device__ __forceinline__ float kept(float d, float m) { return keeps(m) ? fmaf(-m, d, d) : -m * d; }
+// k h + (1 - k) x: h + m (x - h), or x - |m| (x - h)
+__device__ __forceinline__ float step(float h, float x, float m) { return fmaf(m, x - h, keeps(m) ? h : x); }
+// k d, and (1 - k) d
+__device__ __forceinline__ float kept(float d, float m) { return fmaf(-m, d, keeps(m) ? d : 0.0f); }
+__device__ __forceinline__ float taken(float d, float m) { return fmaf(m, d, keeps(m) ? 0.0f : d); }
 
 // What a run of steps does to a state: h -> A h + B, c = 1 - A.
 struct Run {
   float A, c, B;
 };
+// One step more, whose x is taken separately.  c is the sum of what the steps
+// take away where all of them keep more than half; where one does not, A is
+// below a half and exact enough for both.
+__device__ __forceinline__ void lengthen(Run& r, float m, float k) {
+  r.A *= k;
+  r.c = fmaf(fabsf(m), 1.0f - r.c, r.c);
+}
+__device__ __forceinline__ void settle(Run& r) { r.c = r.A < 0.5f ? 1.0f - r.A : r.c; }
 __device__ __forceinline__ float keep(const Run& r, float h) { return r.c < 0.5f ? fmaf(-r.c, h, h) : r.A * h; }
 __device__ __forceinline__ float apply(const Run& r, float h) { return r.B + keep(r, h); }
 __device__ __forceinline__ Run then(const Run& first, const Run& r) {
@@ -75,11 +82,13 @@ template <int V>
 __device__ __forceinline__ Place place(const RecArgs& a, const RecShape& s) {
   Place p;
   const int lane = threadIdx.x & (s.L - 1);
-  const int64_t block = blockIdx.x % s.blocks, rest = blockIdx.x / s.blocks;
-  p.seg = rest % s.segments;
-  p.b = rest / s.segments;
+  const uint32_t blocks = (uint32_t)s.blocks, segments = (uint32_t)s.segments;
+  const uint32_t rest = blockIdx.x / blocks, b = rest / segments;
+  // (divisions leave the scalar registers, where loads want their bases)
+  p.seg = __builtin_amdgcn_readfirstlane(rest - b * segments);
+  p.b = __builtin_amdgcn_readfirstlane(b);
   p.g = threadIdx.x / s.L;
-  const int64_t c = (block * s.L + lane) * V;
+  const int64_t c = ((int64_t)(blockIdx.x - rest * blocks) * s.L + lane) * V;
   p.active = c < a.channels;
   // the last lane's channels end with the row; what two lanes have, both write alike
   p.c = c + V <= a.channels ? c : a.channels - V;
@@ -87,27 +96,58 @@ __device__ __forceinline__ Place place(const RecArgs& a, const RecShape& s) {
 }
 __device__ __forceinline__ int64_t length_of(const RecArgs& a, int64_t b) {
   if (!a.lengths) return a.steps;
-  const int64_t n = a.lengths[b];
-  return n < 0 ? 0 : (n < a.steps ? n : a.steps);
+  int64_t n = a.lengths[b];
+  n = n < 0 ? 0 : (n < a.steps ? n : a.steps);
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)n) |
+                   (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)n >> 32)) << 32);
 }
 
-// R steps from t on; what lies at or behind `end` is not read.
+// R steps of a tile.  `whole`: all of the workgroup's lie before the end; what
+// lies at or behind it is not read otherwise.  p: the tile's first step, the same
+// for all lanes, so that a load has a scalar base and one offset.
 template <class T, int V, int R>
-__device__ __forceinline__ void load_steps(const T* p, const Place& at, int64_t t, int64_t end, int64_t C,
-                                           Vec<T, V> (&r)[R]) {
+__device__ __forceinline__ void load_steps(const T* p, uint32_t offset, int64_t left, bool whole, int64_t C, Vec<T, V> (&r)[R]) {
+  const char* base = reinterpret_cast<const char*>(p);
+  if (whole) {
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    r[i] = Vec<T, V>{};
-    if (at.active && t + i < end) load_vec(p + (t + i) * C, r[i]);
+    for (int i = 0; i < R; ++i) load_vec(reinterpret_cast<const T*>(base + (int64_t)i * C * (int64_t)sizeof(T) + offset), r[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      r[i] = Vec<T, V>{};
+      if (i < left) load_vec(reinterpret_cast<const T*>(base + (int64_t)i * C * (int64_t)sizeof(T) + offset), r[i]);
+    }
   }
 }
 template <class T, int V, int R>
-__device__ __forceinline__ void gates_of(const Vec<T, V> (&f)[R], int64_t t, int64_t end, float (&m)[R][V]) {
+__device__ __forceinline__ void store_steps(T* p, uint32_t offset, int64_t left, bool whole, int64_t C, const Vec<T, V> (&r)[R]) {
+  char* base = reinterpret_cast<char*>(p);
 #pragma unroll
   for (int i = 0; i < R; ++i)
-#pragma unroll
-    for (int v = 0; v < V; ++v) m[i][v] = t + i < end ? small_gate((float)f[i].v[v]) : 0.0f;
+    if (whole || i < left) store_vec(reinterpret_cast<T*>(base + (int64_t)i * C * (int64_t)sizeof(T) + offset), r[i]);
 }
+
+// Tiles that begin before a sequence's end.
+template <int R>
+__device__ __forceinline__ int64_t live_tiles(const RecShape& s, int64_t len, int64_t first, int64_t last) {
+  const int64_t live = (len + s.G * R - 1) / (s.G * R);
+  return live < first ? first : (live < last ? live : last);
+}
+
+// A tile's place: how many of this thread's steps lie before the sequence's end
+// and before the row's, and whether all of the workgroup's do.
+template <int R>
+struct Tile {
+  int64_t left, rows;
+  bool whole, full;
+  __device__ __forceinline__ Tile(const RecArgs& a, const RecShape& s, int64_t tile, int g, int64_t len) {
+    const int64_t t = (tile * s.G + g) * R, end = (tile + 1) * s.G * R;
+    left = len - t;
+    rows = a.steps - t;
+    whole = end <= len;
+    full = end <= a.steps;
+  }
+};
 
 // Runs of the groups in LDS, [number][group][lane].
 template <int V>
@@ -123,34 +163,60 @@ struct Shared {
   __device__ __forceinline__ Run get(int g, int v) { return Run{ref(0, g, v), ref(1, g, v), ref(2, g, v)}; }
 };
 
-// State before this workgroup's part from `start`: the parts before it, in the
-// order in which they apply (BACK: from the last one on), shared out over the groups.
-template <int V, bool BACK>
-__device__ __forceinline__ void join_parts(const RecArgs& a, const RecShape& s, const Place& at, Shared<V> sh,
-                                           float (&state)[V]) {
-  const int64_t n = BACK ? s.segments - 1 - at.seg : at.seg;
-  if (n == 0) return;
-  const int64_t each = (n + s.G - 1) / s.G, from = at.g * each, to = from + each < n ? from + each : n;
-  const float* parts = reinterpret_cast<const float*>(a.ws) + at.b * s.segments * 3 * a.channels + at.c;
-  Run mine[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) mine[v] = Run{1.0f, 0.0f, 0.0f};
-  if (at.active) {
+// The state before every part, from the parts' (A, c, B) and the first state
+// (BACK: the gradient after every part, from the last one on).  64 groups of
+// threads share the parts of a sequence, 16 channels a workgroup.
+constexpr int kJoin = 1024, kJoinGroups = kJoin / 16;
+template <bool BACK>
+__global__ __launch_bounds__(kJoin) void recurrence_starts_kernel(RecArgs a, RecShape s) {
+  __shared__ float lds[3][kJoinGroups][16];
+  const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
+  const int64_t across = (a.channels + 15) / 16, b = blockIdx.x / across, c = (blockIdx.x - b * across) * 16 + lane;
+  const int64_t n = s.segments, C = a.channels;
+  const bool active = c < C;
+  const int64_t each = (n + kJoinGroups - 1) / kJoinGroups, from = group * each, to = from + each < n ? from + each : n;
+  const float* parts = reinterpret_cast<const float*>(a.ws) + b * n * 3 * C + c;
+  float* starts = reinterpret_cast<float*>(a.ws) + a.batch * n * 3 * C + b * n * C + c;
+  const auto part = [&](int64_t i) {
+    const float* p = parts + (BACK ? n - 1 - i : i) * 3 * C;
+    return Run{p[0], p[C], p[2 * C]};
+  };
+  Run mine{1.0f, 0.0f, 0.0f};
+  if (active) {
 #pragma unroll 4
-    for (int64_t i = from; i < to; ++i) {
-      const float* p = parts + (BACK ? s.segments - 1 - i : i) * 3 * a.channels;
-#pragma unroll
-      for (int v = 0; v < V; ++v) mine[v] = then(mine[v], Run{p[v], p[a.channels + v], p[2 * a.channels + v]});
-    }
+    for (int64_t i = from; i < to; ++i) mine = then(mine, part(i));
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) sh.put(at.g, v, mine[v]);
+  lds[0][group][lane] = mine.A;
+  lds[1][group][lane] = mine.c;
+  lds[2][group][lane] = mine.B;
+  const float* first = BACK ? a.glast : a.state;
+  float state = active && first ? first[b * C + c] : 0.0f;
   __syncthreads();
-  for (int g = 0; g < s.G; ++g)
-#pragma unroll
-    for (int v = 0; v < V; ++v) state[v] = apply(sh.get(g, v), state[v]);
-  __syncthreads();
+  if (!active) return;
+  for (int g = 0; g < group; ++g) state = apply(Run{lds[0][g][lane], lds[1][g][lane], lds[2][g][lane]}, state);
+#pragma unroll 4
+  for (int64_t i = from; i < to; ++i) {
+    starts[(BACK ? n - 1 - i : i) * C] = state;
+    state = apply(part(i), state);
+  }
 }
+
+// The first state of this workgroup's part.
+template <int V>
+__device__ __forceinline__ void first_state(const RecArgs& a, const RecShape& s, const Place& at, const float* first,
+                                            float (&state)[V]) {
+  const float* p = first ? first + at.b * a.channels : nullptr;
+  if (s.segments > 1)
+    p = reinterpret_cast<const float*>(a.ws) + (a.batch * 3 + at.b) * s.segments * a.channels + at.seg * a.channels;
+#pragma unroll
+  for (int v = 0; v < V; ++v) state[v] = p ? p[at.c + v] : 0.0f;
+}
+
+// What a tile takes from memory.
+template <class T, int V, int R, bool GRAD>
+struct Raw {
+  Vec<T, V> f[R], x[R], d[GRAD ? R : 1];
+};
 
 // (A, c, B) of every part: of the states, or (BACK) of the gradients.
 template <class T, int V, int R, bool BACK>
@@ -158,29 +224,33 @@ __global__ __launch_bounds__(kThreads) void recurrence_parts_kernel(RecArgs a, R
   __shared__ float lds[3 * kThreads * V];
   const Place at = place<V>(a, s);
   Shared<V> sh{lds, s.L, s.G, (int)(threadIdx.x & (s.L - 1))};
-  const int64_t len = length_of(a, at.b), C = a.channels, off = at.b * a.steps * C + at.c;
-  const T* second = reinterpret_cast<const T*>(BACK ? a.gh : a.x);
+  const int64_t len = length_of(a, at.b), C = a.channels, stride = (int64_t)s.G * R * C, row = at.b * a.steps * C;
+  const uint32_t offset = (uint32_t)(((int64_t)at.g * R * C + at.c) * (int64_t)sizeof(T));
+  const T *gate = reinterpret_cast<const T*>(a.gate) + row, *second = reinterpret_cast<const T*>(BACK ? a.gh : a.x) + row;
+  const bool there = BACK ? a.gh != nullptr : true;
   Run all[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) all[v] = Run{1.0f, 0.0f, 0.0f};
-  const int64_t first = at.seg * s.per, last = first + s.per < s.tiles ? first + s.per : s.tiles;
+  const int64_t first = at.seg * s.per;
+  const int64_t last = live_tiles<R>(s, len, first, first + s.per < s.tiles ? first + s.per : s.tiles);
   for (int64_t i = 0; i < last - first; ++i) {
-    const int64_t tile = BACK ? last - 1 - i : first + i, t = (tile * s.G + at.g) * R;
+    const int64_t tile = BACK ? last - 1 - i : first + i;
+    const Tile<R> in(a, s, tile, at.g, len);
     Vec<T, V> f[R], x[R];
-    float m[R][V];
-    load_steps<T, V, R>(reinterpret_cast<const T*>(a.gate) + off, at, t, len, C, f);
-    load_steps<T, V, R>(second + off, at, t, second ? len : 0, C, x);
-    gates_of<T, V, R>(f, t, len, m);
+    load_steps<T, V, R>(gate + tile * stride, offset, in.left, in.whole, C, f);
+    load_steps<T, V, R>(second + tile * stride, offset, there ? in.left : 0, in.whole && there, C, x);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       Run r{1.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         const int q = BACK ? R - 1 - j : j;
-        r.A = step(r.A, 0.0f, m[q][v]);
-        r.c = step(r.c, 1.0f, m[q][v]);
-        r.B = BACK ? kept(r.B + (float)x[q].v[v], m[q][v]) : step(r.B, (float)x[q].v[v], m[q][v]);
+        float k, m = small_gate((float)f[q].v[v], k);
+        if (!in.whole && q >= in.left) m = 0.0f, k = 1.0f;
+        lengthen(r, m, k);
+        r.B = BACK ? kept(r.B + (float)x[q].v[v], m) : step(r.B, (float)x[q].v[v], m);
       }
+      settle(r);
       sh.put(at.g, v, r);
     }
     __syncthreads();
@@ -205,34 +275,44 @@ __global__ __launch_bounds__(kThreads) void recurrence_fwd_kernel(RecArgs a, Rec
   __shared__ float lds[3 * kThreads * V];
   const Place at = place<V>(a, s);
   Shared<V> sh{lds, s.L, s.G, (int)(threadIdx.x & (s.L - 1))};
-  const int64_t len = length_of(a, at.b), C = a.channels, off = at.b * a.steps * C + at.c;
+  const int64_t len = length_of(a, at.b), C = a.channels, stride = (int64_t)s.G * R * C, row = at.b * a.steps * C;
+  const uint32_t offset = (uint32_t)(((int64_t)at.g * R * C + at.c) * (int64_t)sizeof(T));
+  const T *gate = reinterpret_cast<const T*>(a.gate) + row, *xs = reinterpret_cast<const T*>(a.x) + row;
+  T* hs = reinterpret_cast<T*>(a.h) + row;
   float state[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) state[v] = a.state && at.active ? a.state[at.b * C + at.c + v] : 0.0f;
-  join_parts<V, false>(a, s, at, sh, state);
-  const int64_t first = at.seg * s.per, last = first + s.per < s.tiles ? first + s.per : s.tiles;
+  const int64_t first = at.seg * s.per, end = first + s.per < s.tiles ? first + s.per : s.tiles;
+  const int64_t last = live_tiles<R>(s, len, first, end);
+  Raw<T, V, R, false> now;
+  const auto load = [&](int64_t tile, Raw<T, V, R, false>& r) {
+    const Tile<R> in(a, s, tile, at.g, len);
+    load_steps<T, V, R>(gate + tile * stride, offset, in.left, in.whole, C, r.f);
+    load_steps<T, V, R>(xs + tile * stride, offset, in.left, in.whole, C, r.x);
+  };
+  if (first < last) load(first, now);
+  first_state(a, s, at, a.state, state);
   for (int64_t tile = first; tile < last; ++tile) {
-    const int64_t t = (tile * s.G + at.g) * R;
-    Vec<T, V> f[R], x[R];
+    const Tile<R> in(a, s, tile, at.g, len);
     float m[R][V], h[V];
-    load_steps<T, V, R>(reinterpret_cast<const T*>(a.gate) + off, at, t, len, C, f);
-    load_steps<T, V, R>(reinterpret_cast<const T*>(a.x) + off, at, t, len, C, x);
     if (a.saved && at.g == 0 && at.active) {
 #pragma unroll
       for (int v = 0; v < V; ++v) a.saved[(at.b * s.tiles + tile) * C + at.c + v] = state[v];
     }
-    gates_of<T, V, R>(f, t, len, m);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       Run r{1.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        r.A = step(r.A, 0.0f, m[i][v]);
-        r.c = step(r.c, 1.0f, m[i][v]);
-        r.B = step(r.B, (float)x[i].v[v], m[i][v]);
+        float k;
+        m[i][v] = small_gate((float)now.f[i].v[v], k);
+        if (!in.whole && i >= in.left) m[i][v] = 0.0f, k = 1.0f;
+        lengthen(r, m[i][v], k);
+        r.B = step(r.B, (float)now.x[i].v[v], m[i][v]);
       }
+      settle(r);
       sh.put(at.g, v, r);
     }
+    Raw<T, V, R, false> next;  // on its way while this tile is finished
+    if (tile + 1 < last) load(tile + 1, next);
     __syncthreads();
     for (int g = 0; g < s.G; ++g)
 #pragma unroll
@@ -241,17 +321,21 @@ __global__ __launch_bounds__(kThreads) void recurrence_fwd_kernel(RecArgs a, Rec
         state[v] = apply(sh.get(g, v), state[v]);
       }
     __syncthreads();
-    T* out = reinterpret_cast<T*>(a.h) + off;
+    Vec<T, V> y[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      Vec<T, V> y;
+    for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        h[v] = step(h[v], (float)x[i].v[v], m[i][v]);
-        y.v[v] = (T)(t + i < len ? h[v] : 0.0f);
+        h[v] = step(h[v], (float)now.x[i].v[v], m[i][v]);
+        y[i].v[v] = (T)(in.whole || i < in.left ? h[v] : 0.0f);
       }
-      if (at.active && t + i < a.steps) store_vec(out + (t + i) * C, y);
-    }
+    if (at.active) store_steps<T, V, R>(hs + tile * stride, offset, in.rows, in.full, C, y);
+    now = next;
+  }
+  const Vec<T, V> zeros[R] = {};
+  for (int64_t tile = last; tile < end && at.active; ++tile) {
+    const Tile<R> in(a, s, tile, at.g, len);
+    store_steps<T, V, R>(hs + tile * stride, offset, in.rows, in.full, C, zeros);
   }
   if (at.seg == s.segments - 1 && at.g == 0 && at.active) {
 #pragma unroll
@@ -260,40 +344,53 @@ __global__ __launch_bounds__(kThreads) void recurrence_fwd_kernel(RecArgs a, Rec
 }
 
 template <class T, int V, int R>
-__global__ __launch_bounds__(kThreads) void recurrence_bwd_kernel(RecArgs a, RecShape s) {
+__global__ __launch_bounds__(kThreads, 2) void recurrence_bwd_kernel(RecArgs a, RecShape s) {
   __shared__ float lds[4 * kThreads * V];  // (A, c, B) of the states, B of the gradients
   const Place at = place<V>(a, s);
   Shared<V> sh{lds, s.L, s.G, (int)(threadIdx.x & (s.L - 1))};
-  const int64_t len = length_of(a, at.b), C = a.channels, off = at.b * a.steps * C + at.c;
+  const int64_t len = length_of(a, at.b), C = a.channels, stride = (int64_t)s.G * R * C, row = at.b * a.steps * C;
+  const uint32_t offset = (uint32_t)(((int64_t)at.g * R * C + at.c) * (int64_t)sizeof(T));
+  const T *gate = reinterpret_cast<const T*>(a.gate) + row, *xs = reinterpret_cast<const T*>(a.x) + row;
+  const T* gh = reinterpret_cast<const T*>(a.gh) + row;
   float grad[V];  // of the state after the tile, through later steps
+  const int64_t first = at.seg * s.per, end = first + s.per < s.tiles ? first + s.per : s.tiles;
+  const int64_t last = live_tiles<R>(s, len, first, end);
+  Raw<T, V, R, true> now;
+  float start[V];
+  const auto load = [&](int64_t tile, Raw<T, V, R, true>& r, float(&h)[V]) {
+    const Tile<R> in(a, s, tile, at.g, len);
+    load_steps<T, V, R>(gate + tile * stride, offset, in.left, in.whole, C, r.f);
+    load_steps<T, V, R>(xs + tile * stride, offset, in.left, in.whole, C, r.x);
+    load_steps<T, V, R>(gh + tile * stride, offset, a.gh ? in.left : 0, in.whole && a.gh, C, r.d);
 #pragma unroll
-  for (int v = 0; v < V; ++v) grad[v] = a.glast && at.active ? a.glast[at.b * C + at.c + v] : 0.0f;
-  join_parts<V, true>(a, s, at, sh, grad);
-  const int64_t first = at.seg * s.per, last = first + s.per < s.tiles ? first + s.per : s.tiles;
+    for (int v = 0; v < V; ++v) h[v] = a.saved[(at.b * s.tiles + tile) * C + at.c + v];
+  };
+  if (first < last) load(last - 1, now, start);
+  first_state(a, s, at, a.glast, grad);
   for (int64_t tile = last - 1; tile >= first; --tile) {
-    const int64_t t = (tile * s.G + at.g) * R;
-    Vec<T, V> f[R], x[R], d[R];
-    float m[R][V], diff[R][V], h[V], e[V];
-    load_steps<T, V, R>(reinterpret_cast<const T*>(a.gate) + off, at, t, len, C, f);
-    load_steps<T, V, R>(reinterpret_cast<const T*>(a.x) + off, at, t, len, C, x);
-    load_steps<T, V, R>(reinterpret_cast<const T*>(a.gh) + off, at, t, a.gh ? len : 0, C, d);
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = at.active ? a.saved[(at.b * s.tiles + tile) * C + at.c + v] : 0.0f;
-    gates_of<T, V, R>(f, t, len, m);
+    const Tile<R> in(a, s, tile, at.g, len);
+    float m[R][V], h[V], e[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       Run r{1.0f, 0.0f, 0.0f};
       float back = 0.0f;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        r.A = step(r.A, 0.0f, m[i][v]);
-        r.c = step(r.c, 1.0f, m[i][v]);
-        r.B = step(r.B, (float)x[i].v[v], m[i][v]);
-        back = kept(back + (float)d[R - 1 - i].v[v], m[R - 1 - i][v]);
+        float k;
+        m[i][v] = small_gate((float)now.f[i].v[v], k);
+        if (!in.whole && i >= in.left) m[i][v] = 0.0f, k = 1.0f;
+        lengthen(r, m[i][v], k);
+        r.B = step(r.B, (float)now.x[i].v[v], m[i][v]);
       }
+#pragma unroll
+      for (int i = R - 1; i >= 0; --i) back = kept(back + (float)now.d[i].v[v], m[i][v]);
+      settle(r);
       sh.put(at.g, v, r);
       sh.ref(3, at.g, v) = back;
+      h[v] = start[v];
     }
+    Raw<T, V, R, true> next;  // on its way while this tile is finished
+    if (tile > first) load(tile - 1, next, start);
     __syncthreads();
     for (int g = 0; g < at.g; ++g)
 #pragma unroll
@@ -307,33 +404,37 @@ __global__ __launch_bounds__(kThreads) void recurrence_bwd_kernel(RecArgs a, Rec
         grad[v] = apply(r, grad[v]);
       }
     __syncthreads();
+    float diff[R][V];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float xv = (float)x[i].v[v];
+        const float xv = (float)now.x[i].v[v];
         diff[i][v] = h[v] - xv;
         h[v] = step(h[v], xv, m[i][v]);
       }
-    T* gx = reinterpret_cast<T*>(a.gx) + off;
-    T* gf = reinterpret_cast<T*>(a.ggate) + off;
+    Vec<T, V> ox[R], of[R];
 #pragma unroll
-    for (int i = R - 1; i >= 0; --i) {
-      Vec<T, V> ox, of;
+    for (int i = R - 1; i >= 0; --i)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float D = (float)d[i].v[v] + e[v], small = fabsf(m[i][v]);
-        const float minor = small * D, major = fmaf(-small, D, D);
-        const bool up = keeps(m[i][v]), in = t + i < len;
-        e[v] = up ? major : minor;
-        ox.v[v] = (T)(in ? (up ? minor : major) : 0.0f);
-        of.v[v] = (T)(in ? diff[i][v] * (minor - small * minor) : 0.0f);
+        const float D = (float)now.d[i].v[v] + e[v], small = fabsf(m[i][v]);
+        const bool is = in.whole || i < in.left;
+        e[v] = kept(D, m[i][v]);
+        ox[i].v[v] = (T)(is ? taken(D, m[i][v]) : 0.0f);
+        of[i].v[v] = (T)(is ? diff[i][v] * D * fmaf(-small, small, small) : 0.0f);
       }
-      if (at.active && t + i < a.steps) {
-        if (a.gx) store_vec(gx + (t + i) * C, ox);
-        if (a.ggate) store_vec(gf + (t + i) * C, of);
-      }
+    if (at.active) {
+      if (a.gx) store_steps<T, V, R>(reinterpret_cast<T*>(a.gx) + row + tile * stride, offset, in.rows, in.full, C, ox);
+      if (a.ggate) store_steps<T, V, R>(reinterpret_cast<T*>(a.ggate) + row + tile * stride, offset, in.rows, in.full, C, of);
     }
+    now = next;
+  }
+  const Vec<T, V> zeros[R] = {};
+  for (int64_t tile = last; tile < end && at.active; ++tile) {
+    const Tile<R> in(a, s, tile, at.g, len);
+    if (a.gx) store_steps<T, V, R>(reinterpret_cast<T*>(a.gx) + row + tile * stride, offset, in.rows, in.full, C, zeros);
+    if (a.ggate) store_steps<T, V, R>(reinterpret_cast<T*>(a.ggate) + row + tile * stride, offset, in.rows, in.full, C, zeros);
   }
   if (a.gstate && at.seg == 0 && at.g == 0 && at.active) {
 #pragma unroll
@@ -360,7 +461,11 @@ hipError_t launch_recurrence_fwd(const RecArgs& a, hipStream_t stream) {
   const RecShape s = rec_shape(a.batch, a.steps, a.channels, sizeof(T) == 2);
   return with_shape<T>(s, [&](auto v, auto r) {
     const dim3 grid((unsigned)(a.batch * s.segments * s.blocks)), block(kThreads);
-    if (s.segments > 1) hipLaunchKernelGGL((recurrence_parts_kernel<T, v.value, r.value, false>), grid, block, 0, stream, a, s);
+    if (s.segments > 1) {
+      hipLaunchKernelGGL((recurrence_parts_kernel<T, v.value, r.value, false>), grid, block, 0, stream, a, s);
+      hipLaunchKernelGGL(recurrence_starts_kernel<false>, dim3((unsigned)(a.batch * ((a.channels + 15) / 16))), dim3(kJoin), 0,
+                         stream, a, s);
+    }
     hipLaunchKernelGGL((recurrence_fwd_kernel<T, v.value, r.value>), grid, block, 0, stream, a, s);
     return hipGetLastError();
   });
@@ -371,7 +476,11 @@ hipError_t launch_recurrence_bwd(const RecArgs& a, hipStream_t stream) {
   const RecShape s = rec_shape(a.batch, a.steps, a.channels, sizeof(T) == 2);
   return with_shape<T>(s, [&](auto v, auto r) {
     const dim3 grid((unsigned)(a.batch * s.segments * s.blocks)), block(kThreads);
-    if (s.segments > 1) hipLaunchKernelGGL((recurrence_parts_kernel<T, v.value, r.value, true>), grid, block, 0, stream, a, s);
+    if (s.segments > 1) {
+      hipLaunchKernelGGL((recurrence_parts_kernel<T, v.value, r.value, true>), grid, block, 0, stream, a, s);
+      hipLaunchKernelGGL(recurrence_starts_kernel<true>, dim3((unsigned)(a.batch * ((a.channels + 15) / 16))), dim3(kJoin), 0,
+                         stream, a, s);
+    }
     hipLaunchKernelGGL((recurrence_bwd_kernel<T, v.value, r.value>), grid, block, 0, stream, a, s);
     return hipGetLastError();
   });

@@ -51,6 +51,7 @@ extern "C" {
 #define ECC_MAX_NORM_BATCH 32768
 #define ECC_MAX_MATRIX 32768           /* rows and columns of one matrix      */
 #define ECC_MAX_NS_STEPS 64
+#define ECC_MAX_RECURRENCE_CHANNELS 1048576
 
 /*
  * Group norm with an activation, channels last.
@@ -201,7 +202,8 @@ size_t ecc_residual_norm_workspace_bytes(int64_t batch, int64_t inner, int64_t c
  * The gated linear recurrence along a sequence's steps (the thresholds of a
  * curve, say): with k_t = 1 / (1 + exp(-gate_t)),
  *   h_t = k_t h_(t-1) + (1 - k_t) x_t,  h_(-1) = state, for every channel.
- *   x, gate  device, dtype elements, [batch][steps][channels]
+ *   x, gate  device, dtype elements, [batch][steps][channels];
+ *            channels <= ECC_MAX_RECURRENCE_CHANNELS
  *   state    device float32 [batch][channels]; NULL stands for 0
  *   lengths  device int64 [batch], or NULL: sequence b has the steps before
  *            lengths[b] (taken as 0 below it and as `steps` beyond them); x and
@@ -211,7 +213,7 @@ size_t ecc_residual_norm_workspace_bytes(int64_t batch, int64_t inner, int64_t c
  *            initial one where there is none), to be carried to a next call
  *   saved    float32, ecc_gated_recurrence_saved_bytes: states that the backward
  *            pass starts from; NULL where there will be none
- * No output overlaps an input.  States are float32.  One launch, two where batch x channels is small
+ * No output overlaps an input.  States are float32.  One launch, three where batch x channels is small
  * beside the card and the sequence is cut into parts.
  */
 int ecc_gated_recurrence_fwd(const void* x, const void* gate, int dtype, int64_t batch, int64_t steps, int64_t channels,

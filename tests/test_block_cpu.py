@@ -114,7 +114,7 @@ def rec_bwd(L, x=FAKE, f=FAKE, d=0, B=2, T=9, C=8, n=None, saved=FAKE, gh=FAKE, 
 def test_recurrence_argument_errors(L, call):
     assert call(L, x=None) == L.ECC_E_NULL and call(L, f=None) == L.ECC_E_NULL
     assert call(L, d=3) == L.ECC_E_DTYPE
-    for bad in (dict(B=0), dict(T=0), dict(C=0), dict(T=1 << 40), dict(B=1 << 32, T=1, C=1), dict(B=1 << 62)):
+    for bad in (dict(B=0), dict(T=0), dict(C=0), dict(T=1 << 40), dict(C=(1 << 20) + 1), dict(B=1 << 32, T=1, C=1), dict(B=1 << 62)):
         assert call(L, **bad) == L.ECC_E_SHAPE, bad
     assert call(L, ws=None) == L.ECC_E_WORKSPACE
     need = L.lib.ecc_gated_recurrence_workspace_bytes(1, 100000, 8, 0)
@@ -131,9 +131,9 @@ def test_recurrence_sizes(L):
     assert ws(0, 1, 1, 0) == saved(1, 0, 1, 0) == saved(1, 1, 1, 3) == 0
     for B, T, C, d in ((64, 256, 1024, 2), (1, 65536, 96, 0), (12, 8192, 201, 1), (64, 1, 1024, 2), (3, 7, 1, 0)):
         assert saved(B, T, C, d) % (B * C * 4) == 0 and saved(B, T, C, d) >= B * C * 4
-        # small beside the features: a state for 32 steps or more, three numbers for every part
+        # small beside the features: a state for 32 steps or more, four numbers for every part
         if T >= 64:
-            assert saved(B, T, C, d) <= B * C * 4 * (T // 32 + 1) and ws(B, T, C, d) <= 3 * saved(B, T, C, d) + 256
+            assert saved(B, T, C, d) <= B * C * 4 * (T // 32 + 1) and ws(B, T, C, d) <= 4 * saved(B, T, C, d) + 256
 
 
 def test_binding_refusals():
