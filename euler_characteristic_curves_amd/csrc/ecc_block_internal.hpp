@@ -35,15 +35,19 @@ struct ResArgs {
 struct RowShape {
   int V, K, L, threads;
 };
-inline RowShape res_shape(int64_t channels, bool half) {
+inline RowShape res_shape(int64_t channels, bool half, bool backward) {
   RowShape best{};
-  const int vec = half ? 8 : 4, most = half ? 2 : 4;  // 16 elements a lane at most: the backward pass holds ten of each
+  const int vec = half ? 8 : 4;
   if (channels < vec) {
     best.V = best.K = 1;
     for (best.L = 1; best.L < channels; best.L *= 2) {
     }
   } else {
     const int64_t vectors = (channels + vec - 1) / vec;
+    // 16 elements a lane at most, 8 in the backward pass, which holds ten numbers
+    // of each, unless a row would need more than 512 lanes
+    int most = 16 / vec;
+    if (backward && vectors <= 512 * (8 / vec)) most = 8 / vec;
     int64_t least = INT64_MAX;
     for (int K = 1; K <= most; ++K) {
       int64_t L = 1;
@@ -80,7 +84,7 @@ inline size_t res_workspace_bytes(int64_t batch, int64_t inner, int64_t channels
   const int64_t samples = sample_gates ? batch : 1, rows = sample_gates ? inner : batch * inner;
   size_t most = 0;
   for (int half = 0; half < 2; ++half) {
-    const RowShape s = res_shape(channels, half);
+    const RowShape s = res_shape(channels, half, true);
     const size_t bytes = (size_t)samples * (size_t)res_blocks(samples, rows, s.threads / s.L, kResSums) *
                          (size_t)(3 * channels) * sizeof(float);
     most = bytes > most ? bytes : most;

@@ -56,16 +56,22 @@ struct Columns {
   }
 };
 
-// Elements of a row, or of the parameters; those that another vector has are 0.
+// Elements of a row as they lie, and as numbers, or of the parameters; those
+// that another vector has are 0.
 template <int V, int K, class T>
-__device__ __forceinline__ void load_row(const T* p, const Columns<V, K>& col, bool active, float (&r)[K][V]) {
+__device__ __forceinline__ void load_raw(const T* p, const Columns<V, K>& col, bool active, Vec<T, V> (&r)[K]) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    Vec<T, V> v = {};
-    if (active && col.skip[k] < V) load_vec(p + col.at[k], v);
-#pragma unroll
-    for (int j = 0; j < V; ++j) r[k][j] = V > 1 && j < col.skip[k] ? 0.0f : (float)v.v[j];
+    r[k] = Vec<T, V>{};
+    if (active && col.skip[k] < V) load_vec(p + col.at[k], r[k]);
   }
+}
+template <int V, int K, class T>
+__device__ __forceinline__ void unpack(const Vec<T, V> (&v)[K], const Columns<V, K>& col, float (&r)[K][V]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j) r[k][j] = V > 1 && j < col.skip[k] ? 0.0f : (float)v[k].v[j];
 }
 template <int V, int K, class T>
 __device__ __forceinline__ void store_row(T* p, const Columns<V, K>& col, const float (&r)[K][V]) {
@@ -148,14 +154,25 @@ __global__ __launch_bounds__(512) void residual_fwd_kernel(ResArgs a, ResGeom g)
   load_params(a.gate, a.pdtype, sample * a.gate_stride, col, gate);
   load_params(a.weight, a.pdtype, 0, col, weight);
   load_params(a.branch_weight, a.pdtype, 0, col, after);
-  for (int64_t first = block * g.slots; first < g.rows; first += g.blocks * g.slots) {
+  const int64_t turn = g.blocks * g.slots;
+  Vec<XT, V> nx[K];
+  Vec<BT, V> nb[K];
+  const auto load = [&](int64_t first) {  // the rows of a turn
+    const bool active = first + slot < g.rows;
+    const int64_t at = (sample * g.rows + first + slot) * C;
+    load_raw(reinterpret_cast<const XT*>(a.x) + at, col, active, nx);
+    load_raw(reinterpret_cast<const BT*>(a.branch) + at, col, active && a.branch, nb);
+  };
+  load(block * g.slots);
+  for (int64_t first = block * g.slots; first < g.rows; first += turn) {
     const bool active = first + slot < g.rows;
     const int64_t row = sample * g.rows + first + slot;
     float x[K][V], b[K][V];
-    load_row(reinterpret_cast<const XT*>(a.x) + row * C, col, active, x);
+    unpack(nx, col, x);
+    unpack(nb, col, b);
+    load(first + turn);  // on their way while these are finished
     float rb = 1.0f;
     if (a.branch) {
-      load_row(reinterpret_cast<const BT*>(a.branch) + row * C, col, active, b);
       if (a.norm_branch) rb = inverse_rms(b, g.L, C, a.eps, lds);
 #pragma unroll
       for (int k = 0; k < K; ++k)
@@ -180,7 +197,7 @@ __global__ __launch_bounds__(512) void residual_fwd_kernel(ResArgs a, ResGeom g)
 
 template <class XT, class BT, int V, int K>
 __global__ __launch_bounds__(512) void residual_bwd_kernel(ResArgs a, ResGeom g, float* part) {
-  extern __shared__ float shared[];  // the sums of half the slots, where a workgroup has more than one
+  extern __shared__ float shared[];  // sums of runs, then of half the slots
   __shared__ float lds[8];
   const int lane = threadIdx.x & (g.L - 1), slot = threadIdx.x / g.L;
   const int64_t sample = blockIdx.x / g.blocks, block = blockIdx.x - sample * g.blocks, C = a.channels;
@@ -189,18 +206,41 @@ __global__ __launch_bounds__(512) void residual_bwd_kernel(ResArgs a, ResGeom g,
   load_params(a.gate, a.pdtype, sample * a.gate_stride, col, gate);
   load_params(a.weight, a.pdtype, 0, col, weight);
   load_params(a.branch_weight, a.pdtype, 0, col, after);
-  float run[3][K][V] = {}, total[3][K][V] = {};  // of the gate, the weight, the branch's weight
+  // sums over a run of rows, of the gate, the weight and the branch's weight; the
+  // sums of runs are in LDS: in registers they did not fit (16384 x 1024, float32
+  // stream: 105 us)
+  float run[3][K][V] = {};
+  const auto total = [&](int q, int k, int j) -> float& {
+    return shared[((q * K + k) * V + j) * blockDim.x + threadIdx.x];
+  };
   const float inv = 1.0f / (float)C;
   int turns = 0;
-  for (int64_t first = block * g.slots; first < g.rows; first += g.blocks * g.slots) {
+  bool runs = false;
+  const int64_t turn = g.blocks * g.slots;
+  Vec<XT, V> nx[K], ny[K];
+  Vec<BT, V> nb[K], nz[K];
+  float nrb, nry;
+  const auto load = [&](int64_t first) {  // the rows of a turn
+    const bool active = first + slot < g.rows;
+    const int64_t row = sample * g.rows + first + slot, at = row * C;
+    load_raw(reinterpret_cast<const XT*>(a.x) + at, col, active, nx);
+    load_raw(reinterpret_cast<const BT*>(a.branch) + at, col, active && a.branch, nb);
+    load_raw(reinterpret_cast<const XT*>(a.gy) + at, col, active && a.gy, ny);
+    load_raw(reinterpret_cast<const BT*>(a.gz) + at, col, active && a.gz, nz);
+    nrb = active ? a.stats[row * 2] : 0.0f;
+    nry = active ? a.stats[row * 2 + 1] : 0.0f;
+  };
+  load(block * g.slots);
+  for (int64_t first = block * g.slots; first < g.rows; first += turn) {
     const bool active = first + slot < g.rows;
     const int64_t row = sample * g.rows + first + slot;
     float x[K][V], b[K][V], dy[K][V], dz[K][V];
-    load_row(reinterpret_cast<const XT*>(a.x) + row * C, col, active, x);
-    load_row(reinterpret_cast<const BT*>(a.branch) + row * C, col, active && a.branch, b);
-    load_row(reinterpret_cast<const XT*>(a.gy) + row * C, col, active && a.gy, dy);
-    load_row(reinterpret_cast<const BT*>(a.gz) + row * C, col, active && a.gz, dz);
-    const float rb = active ? a.stats[row * 2] : 0.0f, ry = active ? a.stats[row * 2 + 1] : 0.0f;
+    unpack(nx, col, x);
+    unpack(nb, col, b);
+    unpack(ny, col, dy);
+    unpack(nz, col, dz);
+    const float rb = nrb, ry = nry;
+    load(first + turn);  // on their way while these are finished
     // b: the branch's hat, or the branch itself; x: y's hat; dz: its gradient
     float s = 0.0f;
 #pragma unroll
@@ -247,19 +287,24 @@ __global__ __launch_bounds__(512) void residual_bwd_kernel(ResArgs a, ResGeom g,
         for (int k = 0; k < K; ++k)
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            total[q][k][j] += run[q][k][j];
+            total(q, k, j) = (runs ? total(q, k, j) : 0.0f) + run[q][k][j];
             run[q][k][j] = 0.0f;
           }
+      runs = true;
     }
   }
   if (!part) return;
   part += (int64_t)blockIdx.x * 3 * C;
+  if (runs) {
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) run[q][k][j] += total(q, k, j);
+  }
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int j = 0; j < V; ++j) total[q][k][j] += run[q][k][j];
     // the slots' rows, by halves
     for (int d = g.slots / 2; d > 0; d /= 2) {
       __syncthreads();
@@ -267,17 +312,17 @@ __global__ __launch_bounds__(512) void residual_bwd_kernel(ResArgs a, ResGeom g,
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-          for (int j = 0; j < V; ++j) shared[(k * V + j) * (d * g.L) + (slot - d) * g.L + lane] = total[q][k][j];
+          for (int j = 0; j < V; ++j) shared[(k * V + j) * (d * g.L) + (slot - d) * g.L + lane] = run[q][k][j];
       }
       __syncthreads();
       if (slot < d) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-          for (int j = 0; j < V; ++j) total[q][k][j] += shared[(k * V + j) * (d * g.L) + slot * g.L + lane];
+          for (int j = 0; j < V; ++j) run[q][k][j] += shared[(k * V + j) * (d * g.L) + slot * g.L + lane];
       }
     }
-    if (slot == 0) store_row(part + q * C, col, total[q]);
+    if (slot == 0) store_row(part + q * C, col, run[q]);
   }
 }
 
@@ -349,7 +394,7 @@ hipError_t launch_residual_fwd(const ResArgs& a, hipStream_t stream) {
     using XT = decltype(xt);
     using BT = decltype(bt);
     constexpr bool half = sizeof(XT) == 2;
-    const RowShape s = res_shape(a.channels, half);
+    const RowShape s = res_shape(a.channels, half, false);
     const ResGeom g = geometry(a, s, kResApply);
     return with_shape<half>(s, [&](auto v, auto k) {
       hipLaunchKernelGGL((residual_fwd_kernel<XT, BT, v.value, k.value>), dim3((unsigned)(g.samples * g.blocks)),
@@ -364,12 +409,14 @@ hipError_t launch_residual_bwd(const ResArgs& a, hipStream_t stream) {
     using XT = decltype(xt);
     using BT = decltype(bt);
     constexpr bool half = sizeof(XT) == 2;
-    const RowShape s = res_shape(a.channels, half);
+    const RowShape s = res_shape(a.channels, half, true);
     const ResGeom g = geometry(a, s, kResSums);
     const bool sums = a.ggate || a.gweight || a.gbranch_weight;
     float* part = sums ? reinterpret_cast<float*>(a.ws) : nullptr;
     return with_shape<half>(s, [&](auto v, auto k) {
-      const size_t lds = g.slots > 1 ? (size_t)(s.threads / 2) * v.value * k.value * sizeof(float) : 0;
+      // of runs, where there are any, or of half the slots
+      const bool runs = g.rows > g.blocks * g.slots * (kRun - 1);
+      const size_t lds = (size_t)(runs ? 3 * s.threads : s.threads / 2) * v.value * k.value * sizeof(float);
       hipLaunchKernelGGL((residual_bwd_kernel<XT, BT, v.value, k.value>), dim3((unsigned)(g.samples * g.blocks)),
                          dim3(s.threads), lds, stream, a, g, part);
       if (sums) {
