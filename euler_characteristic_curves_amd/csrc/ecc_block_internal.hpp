@@ -216,6 +216,7 @@ constexpr int64_t kGluFew = 64;
 struct GluPlan {
   bool packed;
   int64_t wide;   // elements of a packed row
+  int64_t walkers;  // workgroups that share the rows of a narrow product, or 0
   int64_t pitch;  // elements from the gate's gradients to the other's
   GluShare gates, input, weight;
   size_t at_x, at_wg, at_wu, at_dab, at_bias, at_part, bytes;
@@ -240,6 +241,16 @@ inline GluPlan glu_plan(int64_t rows, int64_t channels, int64_t hidden, int elem
   // 877, float32, forward and backward: 174 us so)
   p.packed = channels * elem % 16 != 0 && rows > kGluFew;
   p.wide = (channels + step - 1) / step * step;
+  // sums of up to four steps: a workgroup keeps its weights and walks over the
+  // rows, 64 at a time, 64 times at most (its sums of the bias gradients are
+  // float32).  About three workgroups a CU, a multiple of eight to each of the 64
+  // units, so that those of one tile of rows run on one die.
+  const int64_t row_tiles = (rows + 63) / 64, units = (hidden + 63) / 64;
+  if (p.wide <= 4 * step && row_tiles >= 64) {
+    p.walkers = (768 + units - 1) / units;
+    if (p.walkers * 64 < row_tiles) p.walkers = (row_tiles + 63) / 64;
+    p.walkers = (p.walkers + 7) / 8 * 8;
+  }
   if (p.packed) {
     p.at_x = take((size_t)(rows * p.wide) * elem);
     p.at_wg = take((size_t)(hidden * p.wide) * elem);
@@ -247,7 +258,8 @@ inline GluPlan glu_plan(int64_t rows, int64_t channels, int64_t hidden, int elem
   }
   if (backward) {
     p.at_dab = take((size_t)rows * 2 * p.pitch * elem);
-    p.at_bias = take((size_t)p.gates.tiles_m * 2 * p.pitch * sizeof(float));
+    const int64_t sums = p.walkers > p.gates.tiles_m ? p.walkers : p.gates.tiles_m;
+    p.at_bias = take((size_t)sums * 2 * p.pitch * sizeof(float));
     const size_t a = glu_part_bytes(p.input, 1), b = glu_part_bytes(p.weight, 2);
     p.at_part = take(a > b ? a : b);
   }

@@ -257,16 +257,22 @@ struct Stage {
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
       const int id = i * 64 + (threadIdx.x & 63), row = id / kChunks, chunk = id % kChunks, col = chunk * kPer<T>;
-      Vec<T, kPer<T>> u;
-      __builtin_memcpy(&u, __builtin_assume_aligned(at(row, chunk), 16), 16);
+      const u32x4 u = *reinterpret_cast<const u32x4*>(at(row, chunk));
       if (row >= rows || col >= cols) continue;
-      T* out = reinterpret_cast<T*>(reinterpret_cast<char*>(p) + offset(row, col, pitch));
+      char* out = reinterpret_cast<char*>(p) + offset(row, col, pitch);
       if (col + kPer<T> <= cols) {
-        store_vec(out, u);
+        // (one store of any alignment: of elements, the compiler makes three)
+        typedef u32x4 u32x4_any __attribute__((aligned(2)));
+        *reinterpret_cast<u32x4_any*>(out) = u;
       } else {
 #pragma unroll
         for (int j = 0; j < kPer<T> - 1; ++j)
-          if (col + j < cols) out[j] = u.v[j];
+          if (col + j < cols) {
+            if constexpr (sizeof(T) == 4)
+              reinterpret_cast<uint32_t*>(out)[j] = u[j];
+            else
+              reinterpret_cast<uint16_t*>(out)[j] = (uint16_t)(u[j / 2] >> (j % 2 * 16));
+          }
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -316,6 +322,84 @@ __device__ __forceinline__ float sum_rows(const float (&v)[16], float* lds) {
   return s;
 }
 
+// A tile's biases, of both projections, to `shared`.
+template <class T>
+__device__ __forceinline__ void load_biases(const Product<T>& p, int64_t tn, float* shared) {
+  if (threadIdx.x < 128) {
+    const T* bias = reinterpret_cast<const T*>(threadIdx.x < 64 ? p.a.bg : p.a.bu);
+    const int64_t unit = tn * 64 + (threadIdx.x & 63);
+    shared[threadIdx.x] = bias && unit < p.N ? (float)bias[unit] : 0.0f;
+  }
+}
+
+// The results of a fragment of both projections, from row and unit0 on.
+template <class T, int ACT>
+__device__ __forceinline__ void forward_fragment(const Product<T>& p, const Stage<T>& stage, const f32x4* bias, const f32x16& a,
+                                                 const f32x16& b, int64_t row, int64_t unit0) {
+  float v[16];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const f32x4 ug = bias[q * 2], uu = bias[16 + q * 2];
+#pragma unroll
+    for (int r = q * 4; r < q * 4 + 4; ++r) v[r] = act_value<ACT>(a[r] + ug[r & 3]) * (b[r] + uu[r & 3]);
+  }
+  stage.put(v);
+  stage.store(reinterpret_cast<T*>(p.a.h) + row * p.N + unit0, p.N, p.M - row, p.N - unit0);
+}
+
+// Its gradients: `gh` has the result's.  Sums are over the fragments; rows that
+// are not there have no gradient, but may have infinite projections.
+template <class T, int ACT, class Between>
+__device__ __forceinline__ void gates_fragment(const Product<T>& p, const Stage<T>& stage, const f32x4* bias, const f32x16& a,
+                                               const f32x16& b, int64_t row, int64_t unit0,
+                                               u32x4 (&gh)[Stage<T>::kTurns], float (&sum_a)[16], float (&sum_b)[16],
+                                               Between between) {
+  const bool in = row + (threadIdx.x & 31) < p.M;
+  float g[16], da[16];
+  stage.place(gh);
+  stage.get(g);
+  between();  // gh is free
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const f32x4 ug = bias[q * 2], uu = bias[16 + q * 2];
+#pragma unroll
+    for (int r = q * 4; r < q * 4 + 4; ++r) {
+      float y;
+      const float u = b[r] + uu[r & 3], slope = act_slope<ACT>(a[r] + ug[r & 3], y);
+      da[r] = g[r] * u * slope;
+      g[r] *= y;
+      sum_a[r] += in ? da[r] : 0.0f;
+      sum_b[r] += in ? g[r] : 0.0f;
+    }
+    __builtin_amdgcn_sched_barrier(0);  // all at once would not fit the registers
+  }
+  T* out = p.dab + row * 2 * p.pitch + unit0;
+  stage.put(da);
+  stage.store(out, 2 * p.pitch, p.M - row, p.N - unit0);
+  stage.put(g);
+  stage.store(out + p.pitch, 2 * p.pitch, p.M - row, p.N - unit0);
+}
+
+// A workgroup's sums over rows, to partial row `part`.  lds: 4 KB for this wave.
+template <class T>
+__device__ __forceinline__ void store_bias_sums(const Product<T>& p, int64_t part, int64_t tn, const float (&sum_a)[16],
+                                                const float (&sum_b)[16], char* lds, float* shared) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
+  const int64_t unit0 = tn * 64 + wn * 32;
+  const float a = sum_rows(sum_a, reinterpret_cast<float*>(lds)), b = sum_rows(sum_b, reinterpret_cast<float*>(lds));
+  __syncthreads();  // the biases are read
+  if (wm == 1 && lane < 32) {
+    shared[wn * 32 + lane] = a;
+    shared[64 + wn * 32 + lane] = b;
+  }
+  __syncthreads();
+  if (wm == 0 && lane < p.N - unit0 && lane < 32) {
+    float* out = p.bias + part * 2 * p.pitch + unit0 + lane;
+    out[0] = a + shared[wn * 32 + lane];
+    out[p.pitch] = b + shared[64 + wn * 32 + lane];
+  }
+}
+
 // A workgroup's results: acc[i][j] is the fragment of rows wm FM 32 + 32 i.
 // lds: kStage bytes for this wave; shared: 128 floats for all of them.
 template <class T, int KIND, int FM, int FN, int ACT>
@@ -325,78 +409,26 @@ __device__ __forceinline__ void epilogue(const Product<T>& p, int z, int64_t tm,
   const int64_t row0 = tm * 64 * FM + wm * FM * 32;
   const Stage<T> stage{lds};
   if constexpr (is_dual(KIND)) {
-    const int64_t unit0 = tn * 64 + wn * 32, cols = p.N - unit0;
-    // the tile's biases, of both projections
-    if (threadIdx.x < 128) {
-      const T* bias = reinterpret_cast<const T*>(threadIdx.x < 64 ? p.a.bg : p.a.bu);
-      const int64_t unit = tn * 64 + (threadIdx.x & 63);
-      shared[threadIdx.x] = bias && unit < p.N ? (float)bias[unit] : 0.0f;
-    }
+    const int64_t unit0 = tn * 64 + wn * 32;
+    load_biases(p, tn, shared);
     __syncthreads();
-    const f32x4* bg = reinterpret_cast<const f32x4*>(shared + wn * 32 + (lane >> 5) * 4);
+    const f32x4* bias = reinterpret_cast<const f32x4*>(shared + wn * 32 + (lane >> 5) * 4);
     if constexpr (KIND == kForward) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        float v[16];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x4 ug = bg[q * 2], uu = bg[16 + q * 2];
-#pragma unroll
-          for (int r = q * 4; r < q * 4 + 4; ++r)
-            v[r] = act_value<ACT>(acc[i][0][r] + ug[r & 3]) * (acc[i][1][r] + uu[r & 3]);
-        }
-        stage.put(v);
-        const int64_t row = row0 + i * 32;
-        stage.store(reinterpret_cast<T*>(p.a.h) + row * p.N + unit0, p.N, p.M - row, cols);
-      }
+      for (int i = 0; i < FM; ++i) forward_fragment<T, ACT>(p, stage, bias, acc[i][0], acc[i][1], row0 + i * 32, unit0);
     } else {
       const T* gh = reinterpret_cast<const T*>(p.a.gh);
       u32x4 next[Stage<T>::kTurns];
-      Stage<T>::load(gh + row0 * p.N + unit0, p.N, p.M - row0, cols, next);
-      // sums over the fragments; rows that are not there have no gradient, but
-      // may have infinite projections
+      Stage<T>::load(gh + row0 * p.N + unit0, p.N, p.M - row0, p.N - unit0, next);
       float sum_a[16] = {}, sum_b[16] = {};
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int64_t row = row0 + i * 32;
-        const bool in = row + (lane & 31) < p.M;
-        float g[16], da[16];
-        stage.place(next);
-        stage.get(g);
-        if (i + 1 < FM) Stage<T>::load(gh + (row + 32) * p.N + unit0, p.N, p.M - row - 32, cols, next);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x4 ug = bg[q * 2], uu = bg[16 + q * 2];
-#pragma unroll
-          for (int r = q * 4; r < q * 4 + 4; ++r) {
-            float y;
-            const float b = acc[i][1][r] + uu[r & 3], slope = act_slope<ACT>(acc[i][0][r] + ug[r & 3], y);
-            da[r] = g[r] * b * slope;
-            g[r] *= y;
-            sum_a[r] += in ? da[r] : 0.0f;
-            sum_b[r] += in ? g[r] : 0.0f;
-          }
-          __builtin_amdgcn_sched_barrier(0);  // all at once would not fit the registers
-        }
-        T* out = p.dab + row * 2 * p.pitch + unit0;
-        stage.put(da);
-        stage.store(out, 2 * p.pitch, p.M - row, cols);
-        stage.put(g);
-        stage.store(out + p.pitch, 2 * p.pitch, p.M - row, cols);
+        gates_fragment<T, ACT>(p, stage, bias, acc[i][0], acc[i][1], row, unit0, next, sum_a, sum_b, [&] {
+          if (i + 1 < FM) Stage<T>::load(gh + (row + 32) * p.N + unit0, p.N, p.M - row - 32, p.N - unit0, next);
+        });
       }
-      if (!p.bias) return;
-      const float a = sum_rows(sum_a, reinterpret_cast<float*>(lds)), b = sum_rows(sum_b, reinterpret_cast<float*>(lds));
-      __syncthreads();  // the biases are read
-      if (wm == 1 && lane < 32) {
-        shared[wn * 32 + lane] = a;
-        shared[64 + wn * 32 + lane] = b;
-      }
-      __syncthreads();
-      if (wm == 0 && lane < cols && lane < 32) {
-        float* out = p.bias + tm * 2 * p.pitch + unit0 + lane;
-        out[0] = a + shared[wn * 32 + lane];
-        out[p.pitch] = b + shared[64 + wn * 32 + lane];
-      }
+      if (p.bias) store_bias_sums(p, tm, tn, sum_a, sum_b, lds, shared);
     }
   } else {
 #pragma unroll
@@ -633,6 +665,95 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
   epilogue<T, KIND, FM, FN, ACT>(p, z, tm, tn, acc, (wave & 2 ? b1 : b0) + (wave & 1) * kStage, reinterpret_cast<float*>(a0));
 }
 
+// Narrow sums, of up to four steps: a workgroup keeps the weights of its 64 units
+// in LDS and walks over the rows, 64 at a time, two turns' rows and a turn's
+// gradients on their way (2 x 64^3 x 64 to 160, float16, in tiles: 107 us forward,
+// 306 us for the gates' gradients).
+template <class T>
+struct Narrow {
+  static constexpr int kW = 128 * 64, kX = 64 * 64, kOut = 4 * 32 * 32 * (int)sizeof(T);  // bytes of a step, of the stages
+  static size_t bytes(int steps) { return (size_t)steps * (kW + 3 * kX) + kOut + 128 * sizeof(float); }
+};
+template <class T, int KIND, int ACT>
+__global__ __launch_bounds__(kNT, 2) void glu_narrow_kernel(Product<T> p, int walkers, int steps) {
+  extern __shared__ __align__(16) char lds[];
+  using N = Narrow<T>;
+  char* const w = lds;
+  char* const x = lds + steps * N::kW;
+  char* const out = x + 3 * steps * N::kX;
+  float* const shared = reinterpret_cast<float*>(out + N::kOut);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
+  const uint32_t tiles_n = (uint32_t)p.tiles_n, k = blockIdx.x >> 3, far = k / tiles_n;
+  const int64_t tn = __builtin_amdgcn_readfirstlane(k - far * tiles_n);
+  const int walker = __builtin_amdgcn_readfirstlane((blockIdx.x & 7) + 8 * far);
+  const int64_t tiles_m = (p.M + 63) / 64, unit0 = tn * 64 + wn * 32;
+  // zeros where a row ends within a step: no load writes them
+  for (int i = threadIdx.x; i < steps * (N::kW + 3 * N::kX) / 16; i += kNT) reinterpret_cast<u32x4*>(lds)[i] = u32x4{};
+  load_biases(p, tn, shared);
+  __syncthreads();
+  int line, chunk;
+  Tile<T, true, 64>::mine(0, line, chunk);
+  const auto fetch = [&](const T* base, int row, char* to, int s) {  // this thread's chunk of step s
+    if (s * kStep<T> + chunk * kPer<T> < p.K)
+      load_chunk(base + s * kStep<T>, (uint32_t)((int64_t)row * p.pitchA * (int64_t)sizeof(T)) + chunk * 16, wave_lds(to), 0, 1);
+  };
+  for (int s = 0; s < steps; ++s) {
+    const int64_t left = p.N - tn * 64;
+    const int row = line < left ? line : (int)left - 1;
+    fetch(p.B[0] + tn * 64 * p.pitchB, row, w + s * N::kW, s);
+    fetch(p.B[1] + tn * 64 * p.pitchB, row, w + s * N::kW + N::kW / 2, s);
+  }
+  const auto fetch_rows = [&](int64_t tm, char* to) {
+    const int64_t left = p.M - tm * 64;
+    const int row = line < left ? line : (int)left - 1;
+    for (int s = 0; s < steps; ++s) fetch(p.A + tm * 64 * p.pitchA, row, to + s * N::kX, s);
+  };
+  constexpr int kTurns = Stage<T>::kTurns;
+  u32x4 next[kTurns] = {};
+  const auto fetch_gradients = [&](int64_t tm) {
+    const int64_t row = tm * 64 + wm * 32;
+    Stage<T>::load(reinterpret_cast<const T*>(p.a.gh) + row * p.N + unit0, p.N, p.M - row, p.N - unit0, next);
+  };
+  if (walker < tiles_m) {
+    fetch_rows(walker, x);
+    if (walker + walkers < tiles_m) fetch_rows(walker + walkers, x + steps * N::kX);
+    if constexpr (KIND == kGates) fetch_gradients(walker);
+  }
+  const Stage<T> stage{out + wave * (N::kOut / 4)};
+  const f32x4* bias = reinterpret_cast<const f32x4*>(shared + wn * 32 + (lane >> 5) * 4);
+  float sum_a[16] = {}, sum_b[16] = {};
+  // What a wave whose units are all there issues in a turn after its rows' loads,
+  // which two turns later are complete when so much is left: stores, the
+  // gradients' loads, and one of the rows' in between.
+  constexpr int kAfter = 2 * (KIND == kGates ? 3 * kTurns : kTurns) + 1;
+  const bool counted = unit0 + 32 <= p.N;
+  int turn = 0;
+  for (int64_t tm = walker; tm < tiles_m; tm += walkers) {
+    if (counted && tm != walker && tm + walkers < tiles_m)
+      wait_loads<kAfter>();
+    else
+      wait_loads<0>();
+    const int ahead = turn == 0 ? 2 : turn - 1;
+    if (tm + 2 * walkers < tiles_m) fetch_rows(tm + 2 * walkers, x + ahead * steps * N::kX);
+    f32x16 acc[1][2] = {};
+    for (int s = 0; s < steps; ++s)
+      multiply_step<T, KIND, 1, 2>(x + (turn * steps + s) * N::kX, w + s * N::kW, acc, [](int) {});
+    turn = turn == 2 ? 0 : turn + 1;
+    const int64_t row = tm * 64 + wm * 32;
+    if constexpr (KIND == kForward)
+      forward_fragment<T, ACT>(p, stage, bias, acc[0][0], acc[0][1], row, unit0);
+    else
+      gates_fragment<T, ACT>(p, stage, bias, acc[0][0], acc[0][1], row, unit0, next, sum_a, sum_b, [&] {
+        if (tm + walkers < tiles_m) fetch_gradients(tm + walkers);
+      });
+  }
+  if constexpr (KIND == kGates) {
+    if (!p.bias) return;
+    wait_loads<0>();
+    store_bias_sums(p, walker, tn, sum_a, sum_b, lds + wave * kStage, shared);
+  }
+}
+
 constexpr int kJoin = 1024;
 
 // Joins the shares of a tile, each of four groups of threads every fourth one,
@@ -864,6 +985,27 @@ hipError_t launch_product(Product<T> p, const GluShare& s, hipStream_t stream) {
   return s.FM == 4 ? launch_tiles<T, KIND, 4>(p, stream) : launch_tiles<T, KIND, 1>(p, stream);
 }
 
+// Both projections; `sums`: partial rows of the bias gradients.
+template <class T, int KIND>
+hipError_t launch_projections(Product<T> p, const GluPlan& plan, hipStream_t stream, int64_t* sums = nullptr) {
+  if (sums) *sums = plan.gates.tiles_m;
+  if (!plan.walkers || !is_aligned(p)) return launch_product<T, KIND>(p, plan.gates, stream);
+  if (sums) *sums = plan.walkers;
+  p.tiles_n = plan.gates.tiles_n;
+  const int steps = (int)((p.K + kStep<T> - 1) / kStep<T>);
+  const dim3 grid((unsigned)(plan.walkers * p.tiles_n)), block(kNT);
+  const auto launch = [&](auto act) {
+    hipLaunchKernelGGL((glu_narrow_kernel<T, KIND, act.value>), grid, block, Narrow<T>::bytes(steps), stream, p,
+                       (int)plan.walkers, steps);
+    return hipGetLastError();
+  };
+  using std::integral_constant;
+  if (p.a.act == kActRelu) return launch(integral_constant<int, kActRelu>{});
+  if (p.a.act == kActSilu) return launch(integral_constant<int, kActSilu>{});
+  if (p.a.act == kActGelu) return launch(integral_constant<int, kActGelu>{});
+  return launch(integral_constant<int, kActNone>{});
+}
+
 // The projections' product, of packed operands if there are any.
 template <class T>
 Product<T> projections(const GluArgs& a, const GluPlan& plan, hipStream_t stream) {
@@ -897,7 +1039,7 @@ template <class T>
 hipError_t launch_glu_fwd(const GluArgs& a, hipStream_t stream) {
   const GluPlan plan = glu_plan(a.rows, a.channels, a.hidden, sizeof(T), false);
   const Product<T> p = projections<T>(a, plan, stream);
-  if (a.rows > kGluFew) return launch_product<T, kForward>(p, plan.gates, stream);
+  if (a.rows > kGluFew) return launch_projections<T, kForward>(p, plan, stream);
   const dim3 grid((unsigned)((a.hidden + 15) / 16)), block(kFewThreads);
   if (a.rows <= 16)
     hipLaunchKernelGGL((glu_few_kernel<T, 1>), grid, block, 0, stream, p);
@@ -918,10 +1060,9 @@ hipError_t launch_glu_bwd(const GluArgs& a, hipStream_t stream) {
   p.dab = reinterpret_cast<T*>(ws + plan.at_dab);
   p.bias = a.gbg || a.gbu ? reinterpret_cast<float*>(ws + plan.at_bias) : nullptr;
   p.part = reinterpret_cast<float*>(ws + plan.at_part);
-  hipError_t st = launch_product<T, kGates>(p, plan.gates, stream);
+  hipError_t st = launch_projections<T, kGates>(p, plan, stream, &p.tiles_m);
   if (st != hipSuccess) return st;
   if (p.bias) {
-    p.tiles_m = plan.gates.tiles_m;
     hipLaunchKernelGGL(glu_bias_kernel<T>, dim3((unsigned)((a.hidden + 15) / 16), 2), dim3(kJoin), 0, stream, p);
   }
   p.A = p.dab;

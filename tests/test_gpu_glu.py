@@ -82,6 +82,36 @@ def test_large(shape, hidden, dtype):
     check_all(*make(shape, hidden, dtype, seed=6), "gelu")
 
 
+# sums of up to four steps over many rows: rows that end within a step or a chunk, units within a tile, several turns of a
+# workgroup
+NARROW = [((4097, 8), 70), ((5000, 40), 33), ((4200, 64), 64), ((4133, 100), 130), ((9000, 17), 5), ((4300, 128), 16),
+          ((4160, 16), 6400), ((64, 65, 48), 1)]
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("shape,hidden", NARROW, ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else str(v))
+def test_narrow(shape, hidden, act, dtype):
+    banner("glu narrow", shape, hidden, act, dtype)
+    check_all(*make(shape, hidden, dtype, act == "silu", seed=13), act)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_narrow_keeps_nan_in_its_row(dtype):
+    """What lies behind a row's end belongs to the next row."""
+    banner("glu narrow nan", dtype)
+    t, gh = make((4200, 40), 24, dtype, seed=14)
+    t["x"][7, 0] = float("nan")
+    t["x"][4199, 39] = float("inf")
+    d = {k: v.cuda().requires_grad_() for k, v in t.items()}
+    h = call(d, "silu")
+    ok = torch.ones(4200, dtype=torch.bool)
+    ok[[7, 4199]] = False
+    assert torch.equal(torch.isfinite(h).all(dim=1).cpu(), ok)
+    (gx,) = torch.autograd.grad(h, [d["x"]], gh.cuda())
+    assert torch.isfinite(gx.cpu()[ok]).all()
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 8, 9, 16, 17, 32, 33])
 def test_few_rows(rows, dtype):
