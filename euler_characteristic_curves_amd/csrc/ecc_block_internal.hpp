@@ -209,12 +209,16 @@ inline size_t glu_part_bytes(const GluShare& s, int both) {
 // Up to so many rows the weights are read once, straight to registers.
 constexpr int64_t kGluFew = 64;
 
+// Up to so many rows the projections' 16-bit gradients are kept in two parts.
+constexpr int64_t kGluPairs = 512;
+
 // Workspace: x and both weights with rows of whole steps, where theirs are not
 // whole 16-byte chunks (`packed`); in the backward pass the gradients of both
 // projections (rows of 2 x pitch elements), partial sums of the bias gradients
 // and shares of products.
 struct GluPlan {
   bool packed;
+  bool pairs;     // 16-bit gradients of the projections in two parts
   int64_t wide;   // elements of a packed row
   int64_t walkers;  // workgroups that share the rows of a narrow product, or 0
   int64_t pitch;  // elements from the gate's gradients to the other's
@@ -225,10 +229,15 @@ inline GluPlan glu_plan(int64_t rows, int64_t channels, int64_t hidden, int elem
   GluPlan p{};
   const int step = 64 / elem;  // elements of a step along the summed axis
   p.pitch = (hidden + 63) / 64 * 64;
+  p.pairs = elem == 2 && rows <= kGluPairs;
   p.gates = glu_share(rows, 2 * hidden, channels, 1, step, false);
+  if (p.pairs && backward) {  // (only the small tiles have registers for both parts)
+    p.gates.FM = 1;
+    p.gates.tiles_m = (rows + 63) / 64;
+  }
   p.gates.tiles_n = (hidden + 63) / 64;  // 64 of both projections a tile
-  p.input = glu_share(rows, channels, 2 * hidden, 1, step, true);
-  p.weight = glu_share(hidden, channels, rows, 2, step, true);
+  p.input = glu_share(rows, channels, (p.pairs ? 4 : 2) * hidden, 1, step, true);
+  p.weight = glu_share(hidden, channels, (p.pairs ? 2 : 1) * rows, 2, step, true);
   size_t at = 0;
   const auto take = [&at](size_t bytes) {
     at = (at + 255) & ~(size_t)255;
@@ -257,7 +266,7 @@ inline GluPlan glu_plan(int64_t rows, int64_t channels, int64_t hidden, int elem
     p.at_wu = take((size_t)(hidden * p.wide) * elem);
   }
   if (backward) {
-    p.at_dab = take((size_t)rows * 2 * p.pitch * elem);
+    p.at_dab = take((size_t)rows * (p.pairs ? 4 : 2) * p.pitch * elem);
     const int64_t sums = p.walkers > p.gates.tiles_m ? p.walkers : p.gates.tiles_m;
     p.at_bias = take((size_t)sums * 2 * p.pitch * sizeof(float));
     const size_t a = glu_part_bytes(p.input, 1), b = glu_part_bytes(p.weight, 2);

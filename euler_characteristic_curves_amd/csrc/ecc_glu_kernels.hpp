@@ -11,7 +11,10 @@
 // through LDS, float32 sums.  A tile of the forward product holds the same 64
 // hidden units of both projections, so activation and product are its epilogue;
 // the backward one's is da and db, rounded once to the element type (they are
-// the next products' operands) and written to the workspace.
+// the next products' operands: the error is that of the results' own rounding,
+// 1.41 times it in all) and written to the workspace.  With few rows sums do not
+// even such errors out, and the products are bound by the weights' way to memory:
+// there what the rounding leaves is kept and multiplied too.
 //
 // Operands of two kinds: those that lie along the summed axis, and those that
 // lie across it (the weights in dx, both operands in dW).  The second are kept
@@ -58,13 +61,14 @@ struct Product {
   const T* B[2];
   int64_t pitchB;
   int64_t M, N, K;  // N: hidden units of one projection in a dual product; K of one part of the sum
-  int parts;        // parts of the sum, A + i stepA with B[i]
+  int parts;        // parts of the sum: in dx A + i stepA with B[i % 2], in dW A + (z + 2 i) stepA
   int splits;
   int64_t tiles_m, tiles_n;
   float* part;
   GluArgs a;
   int64_t pitch;   // of the workspace's gradients
   T* dab;
+  bool pairs;      // what rounding leaves of these gradients is kept too, 2 pitch further on
   float* bias;     // partial sums of da and db, null: not wanted
   T* out[2];
   int64_t pitch_out;
@@ -348,8 +352,9 @@ __device__ __forceinline__ void forward_fragment(const Product<T>& p, const Stag
 }
 
 // Its gradients: `gh` has the result's.  Sums are over the fragments; rows that
-// are not there have no gradient, but may have infinite projections.
-template <class T, int ACT, class Between>
+// are not there have no gradient, but may have infinite projections.  PAIRS:
+// whether there may be few rows.
+template <class T, int ACT, bool PAIRS, class Between>
 __device__ __forceinline__ void gates_fragment(const Product<T>& p, const Stage<T>& stage, const f32x4* bias, const f32x16& a,
                                                const f32x16& b, int64_t row, int64_t unit0,
                                                u32x4 (&gh)[Stage<T>::kTurns], float (&sum_a)[16], float (&sum_b)[16],
@@ -368,16 +373,32 @@ __device__ __forceinline__ void gates_fragment(const Product<T>& p, const Stage<
       const float u = b[r] + uu[r & 3], slope = act_slope<ACT>(a[r] + ug[r & 3], y);
       da[r] = g[r] * u * slope;
       g[r] *= y;
+      // both parts come from this number: a product rounded straight to 16 bits
+      // for one of them alone is a step off where it lies between two
+      if constexpr (PAIRS) asm("" : "+v"(da[r]), "+v"(g[r]));
       sum_a[r] += in ? da[r] : 0.0f;
       sum_b[r] += in ? g[r] : 0.0f;
     }
     __builtin_amdgcn_sched_barrier(0);  // all at once would not fit the registers
   }
-  T* out = p.dab + row * 2 * p.pitch + unit0;
+  const bool pairs = PAIRS && p.pairs;
+  const int64_t line = (pairs ? 4 : 2) * p.pitch;
+  T* out = p.dab + row * line + unit0;
   stage.put(da);
-  stage.store(out, 2 * p.pitch, p.M - row, p.N - unit0);
+  stage.store(out, line, p.M - row, p.N - unit0);
   stage.put(g);
-  stage.store(out + p.pitch, 2 * p.pitch, p.M - row, p.N - unit0);
+  stage.store(out + p.pitch, line, p.M - row, p.N - unit0);
+  if (pairs) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      da[r] -= (float)(T)da[r];
+      g[r] -= (float)(T)g[r];
+    }
+    stage.put(da);
+    stage.store(out + 2 * p.pitch, line, p.M - row, p.N - unit0);
+    stage.put(g);
+    stage.store(out + 3 * p.pitch, line, p.M - row, p.N - unit0);
+  }
 }
 
 // A workgroup's sums over rows, to partial row `part`.  lds: 4 KB for this wave.
@@ -424,7 +445,7 @@ __device__ __forceinline__ void epilogue(const Product<T>& p, int z, int64_t tm,
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int64_t row = row0 + i * 32;
-        gates_fragment<T, ACT>(p, stage, bias, acc[i][0], acc[i][1], row, unit0, next, sum_a, sum_b, [&] {
+        gates_fragment<T, ACT, FM == 1>(p, stage, bias, acc[i][0], acc[i][1], row, unit0, next, sum_a, sum_b, [&] {
           if (i + 1 < FM) Stage<T>::load(gh + (row + 32) * p.N + unit0, p.N, p.M - row - 32, p.N - unit0, next);
         });
       }
@@ -525,11 +546,11 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
       part = s - direct;
       k0 = (int64_t)whole * kStep<T>;
     } else {
-      if (KIND == kInput && s >= whole) part = 1;
+      if (!is_dual(KIND)) part = (s >= whole) + (s >= 2 * whole) + (s >= 3 * whole);
       k0 = (int64_t)(s - part * whole) * kStep<T>;
     }
   };
-  const auto base_a = [&](int part) { return p.A + (KIND == kWeight ? z : part) * p.stepA; };
+  const auto base_a = [&](int part) { return p.A + (KIND == kWeight ? z + 2 * part : part) * p.stepA; };
   f32x16 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -549,7 +570,7 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
       if constexpr (is_dual(KIND))  // 64 rows of either projection: chunk i is one of rows 64 i to 64 i + 63
         rb[i] = TileB::fetch(p.B[i] - i * 64 * p.pitchB, p.pitchB, tn * 64, p.N + i * 64, k0, p.K, i);
       else
-        rb[i] = TileB::fetch(p.B[KIND == kInput ? part : 0], p.pitchB, tn * TN, p.N, k0, p.K, i);
+        rb[i] = TileB::fetch(p.B[KIND == kInput ? part & 1 : 0], p.pitchB, tn * TN, p.N, k0, p.K, i);
     }
   };
   const auto put = [&](char* la, char* lb) {
@@ -587,7 +608,7 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
         r.b1 = first1 + tn * 64 * p.pitchB + k0;
       } else {
         const T* B = first0;
-        if (KIND == kInput && part) B = first1;
+        if (KIND == kInput && part & 1) B = first1;
         r.b0 = r.b1 = B + k0 * p.pitchB + tn * TN;
       }
       return r;
@@ -743,7 +764,7 @@ __global__ __launch_bounds__(kNT, 2) void glu_narrow_kernel(Product<T> p, int wa
     if constexpr (KIND == kForward)
       forward_fragment<T, ACT>(p, stage, bias, acc[0][0], acc[0][1], row, unit0);
     else
-      gates_fragment<T, ACT>(p, stage, bias, acc[0][0], acc[0][1], row, unit0, next, sum_a, sum_b, [&] {
+      gates_fragment<T, ACT, false>(p, stage, bias, acc[0][0], acc[0][1], row, unit0, next, sum_a, sum_b, [&] {
         if (tm + walkers < tiles_m) fetch_gradients(tm + walkers);
       });
   }
@@ -1058,6 +1079,7 @@ hipError_t launch_glu_bwd(const GluArgs& a, hipStream_t stream) {
   const T* x = p.A;
   p.pitch = plan.pitch;
   p.dab = reinterpret_cast<T*>(ws + plan.at_dab);
+  p.pairs = plan.pairs;
   p.bias = a.gbg || a.gbu ? reinterpret_cast<float*>(ws + plan.at_bias) : nullptr;
   p.part = reinterpret_cast<float*>(ws + plan.at_part);
   hipError_t st = launch_projections<T, kGates>(p, plan, stream, &p.tiles_m);
@@ -1066,12 +1088,12 @@ hipError_t launch_glu_bwd(const GluArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(glu_bias_kernel<T>, dim3((unsigned)((a.hidden + 15) / 16), 2), dim3(kJoin), 0, stream, p);
   }
   p.A = p.dab;
-  p.pitchA = 2 * plan.pitch;
+  p.pitchA = (plan.pairs ? 4 : 2) * plan.pitch;
   p.stepA = plan.pitch;
   if (a.gx) {
     p.N = a.channels;
     p.K = a.hidden;
-    p.parts = 2;
+    p.parts = plan.pairs ? 4 : 2;
     p.out[0] = reinterpret_cast<T*>(a.gx);
     p.pitch_out = a.channels;
     st = launch_product<T, kInput>(p, plan.input, stream);
@@ -1081,7 +1103,7 @@ hipError_t launch_glu_bwd(const GluArgs& a, hipStream_t stream) {
     p.M = a.hidden;
     p.N = a.channels;
     p.K = a.rows;
-    p.parts = 1;
+    p.parts = plan.pairs ? 2 : 1;
     p.B[0] = p.B[1] = x;
     p.out[0] = reinterpret_cast<T*>(a.gwg);
     p.out[1] = reinterpret_cast<T*>(a.gwu);

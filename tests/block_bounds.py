@@ -6,7 +6,7 @@ The bounds count roundings to first order; E = 2^-24 is float32's half step.
 
 import torch
 
-from tests.norm_bounds import E, _vec, act_and_slope
+from tests.norm_bounds import HALF, TINY, E, _vec, act_and_slope
 from tests.norm_bounds import rounded as _rounded
 
 
@@ -157,7 +157,7 @@ def gated_linear(x, w_gate, w_up, b_gate=None, b_up=None, act="silu", gh=None):
 
     A sum of n products in float32 has at most n roundings of partial sums and, from float32 elements, one of every
     product: n + 1 roundings of the sum of magnitudes.  The gradients of the projections are rounded to the element type
-    before they are multiplied; the biases' are not, and are summed over at most 64 rows a lane, two waves and the tiles
+    before they are multiplied (up to 512 rows in two parts); the biases' are not, and are summed over at most 64 rows a lane, two waves and the tiles
     in float64: 68 roundings."""
     dt = x.dtype if x.dtype != torch.float64 else torch.float32
     xd = x.detach().double().cpu().reshape(-1, x.shape[-1])
@@ -185,7 +185,10 @@ def gated_linear(x, w_gate, w_up, b_gate=None, b_up=None, act="silu", gh=None):
     for name, v, b in (("b_gate", da, da_), ("b_up", db, db_)):
         s, s_ = v.sum(0), (b + 68 * E * v.abs()).sum(0)
         out[name] = (s, rounded(s, s_, dt))
-    ra, rb = rounded(da, da_, dt), rounded(db, db_, dt)
+    if dt != torch.float32 and n <= 512:  # in two parts: the second one's rounding is a half step of a half step
+        ra, rb = (v_ + HALF[dt] ** 2 * v.abs() + TINY[dt] for v, v_ in ((da, da_), (db, db_)))
+    else:
+        ra, rb = rounded(da, da_, dt), rounded(db, db_, dt)
     dx = da @ wg + db @ wu
     dx_ = ra @ wg.abs() + rb @ wu.abs() + (2 * F + 1) * E * (da.abs() @ wg.abs() + db.abs() @ wu.abs())
     out["x"] = (dx.reshape(x.shape), rounded(dx, dx_, dt).reshape(x.shape))

@@ -60,7 +60,7 @@ def test_residual_workspace(L):
     assert f(0, 1, 8, 0) == f(1, 0, 8, 0) == f(1, 1, 0, 0) == f(1, 1, 8193, 0) == f(32769, 1, 8, 1) == 0
     assert f(32769, 1, 8, 0) > 0
     # partial rows: bounded by the launch, and by a 256th of the rows where these are many
-    assert f(1, 1 << 20, 1024, 0) <= 1024 * 3 * 1024 * 4 + 256
+    assert f(1, 1 << 18, 1024, 0) <= 1024 * 3 * 1024 * 4 + 256
     assert f(1, 1 << 28, 1024, 0) <= (1 << 28) // 256 * 3 * 1024 * 4 + 256
 
 
