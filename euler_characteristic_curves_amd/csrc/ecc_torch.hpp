@@ -24,8 +24,13 @@ using Optional = std::optional<at::Tensor>;
 
 inline const void* ptr(const at::Tensor& t) { return t.defined() ? t.const_data_ptr() : nullptr; }
 inline void* out_ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
-inline at::Tensor dense(const at::Tensor& t) { return t.defined() ? t.contiguous() : t; }
-inline at::Tensor dense(const Optional& t) { return t ? t->contiguous() : at::Tensor(); }
+// What a kernel reads: contiguous, and not the negative of what lies in memory,
+// as the imaginary part of a conjugate is.
+inline at::Tensor dense(const at::Tensor& t) {
+  if (!t.defined()) return t;
+  return t.is_neg() ? t.resolve_neg().contiguous() : t.contiguous();
+}
+inline at::Tensor dense(const Optional& t) { return t ? dense(*t) : at::Tensor(); }
 inline void* stream_of(const at::Tensor& t) {
   return c10::hip::getCurrentHIPStreamMasqueradingAsCUDA(t.get_device()).stream();
 }

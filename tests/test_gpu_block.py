@@ -207,3 +207,63 @@ def test_projections_beyond_32_bits(rows, c, hidden):
     (gs,) = torch.autograd.grad(hs, [last], hs.detach())
     # (sums may be shared out differently)
     assert torch.allclose(gx[-n:].float(), gs.float(), rtol=2.0 ** -6, atol=1e-3)
+
+
+def conjugate_part(t):
+    """t as the imaginary part of a conjugate: in memory it lies negated."""
+    out = torch.complex(torch.zeros_like(t), -t).conj().imag
+    assert out.is_neg()
+    return out
+
+
+def test_lazily_negated():
+    banner("block negated")
+    gen = torch.Generator().manual_seed(6)
+    t = {k: torch.randn(*s, generator=gen).cuda() for k, s in (
+        ("x", (2, 7, 12)), ("b", (2, 7, 12)), ("w", (12,)), ("wg", (9, 12)), ("wu", (9, 12)), ("s", (2, 12)))}
+    gy, gh = torch.randn(2, 7, 12, generator=gen).cuda(), torch.randn(2, 7, 9, generator=gen).cuda()
+
+    def run(t, gy, gh):
+        t = {k: v.detach().requires_grad_() for k, v in t.items()}
+        out = [*E.residual_norm(t["x"], t["b"], t["w"], t["w"]), *E.gated_recurrence(t["x"], t["b"], t["s"]),
+               E.gated_linear(t["x"], t["wg"], t["wu"]), E.rms_norm(t["x"], t["w"]),
+               E.group_norm_act(t["x"], 3, t["w"], t["w"])]
+        leaves = list(t.values())
+        grads = [*torch.autograd.grad(out[:2], [leaves[0], leaves[1], leaves[2]], [gy, gy]),
+                 *torch.autograd.grad(out[2], [leaves[0], leaves[1], leaves[5]], gy),
+                 *torch.autograd.grad(out[4], [leaves[0], leaves[3], leaves[4]], gh)]
+        return [o.detach() for o in out] + grads
+
+    want = run(t, gy, gh)
+    got = run({k: conjugate_part(v) for k, v in t.items()}, conjugate_part(gy), conjugate_part(gh))
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("which", ["norm", "recurrence", "linear"])
+def test_capture_beside_an_eager_graph_is_refused(which):
+    """A captured backward pass of leaves that an eager graph holds would have the leaves' stream wait for the capturing
+    one.  It is refused before, and the leaves can be captured once that graph is gone."""
+    banner("block capture", which)
+    gen = torch.Generator().manual_seed(7)
+    x, w = torch.randn(2, 7, 12, generator=gen).cuda().requires_grad_(), torch.randn(12, 12, generator=gen).cuda()
+    call = {"norm": lambda: E.rms_norm(x, w[0]), "recurrence": lambda: E.gated_recurrence(x, x)[0],
+            "linear": lambda: E.gated_linear(x, w, w)}[which]
+    g = torch.ones(2, 7, 12, device="cuda")
+    held = call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+        with pytest.raises(RuntimeError, match="free that graph first"):
+            torch.autograd.grad(out, [x], g)
+    (want,) = torch.autograd.grad(held, [x], g)
+    want = want.clone()
+    del held, out
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        (got,) = torch.autograd.grad(call(), [x], g)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
