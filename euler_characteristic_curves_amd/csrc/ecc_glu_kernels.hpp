@@ -20,6 +20,14 @@
 // lie across it (the weights in dx, both operands in dW).  The second are kept
 // in LDS as they lie and turned on the way to the registers, by the transposing
 // read where elements have 16 bits.
+//
+// Large products are bound by the matrix unit at the clock that the power
+// leaves: 16384 x 1024 to 2816, bfloat16, forward 200 us (9.4e14 operations a
+// second), gradients of the projections 232 us, dx 194 us, dW 201 us and 15 for
+// its join.  1999 x 333 to 877, float32: 28 to 35 us each (6.7e13 to 8.3e13 of
+// 1.5e14: 448 to 504 workgroups, two to some compute units and one to others).
+// 2^19 x 64 to 160, float16: 80, 131, 103 and 113 us, bound by the bytes of the
+// results and of da and db, 2.9 to 4.4 TB/s.
 
 #pragma once
 

@@ -19,6 +19,11 @@
 // row are float32 over 16 elements a lane and then a tree.  Sums over rows: 16
 // rows of a thread in float32, then those, then the workgroup's rows by halves,
 // then all workgroups in float64, always in the same order.
+//
+// Both passes are bound by memory (a copy of 1.07 GB: 5.1 TB/s).  16384 rows of
+// 1024 bfloat16 beside a float32 stream: forward 46 us, 4.4 TB/s; backward 74 us,
+// 4.1 TB/s, and 6 for the join of the sums.  1.8e6 rows of 64 bfloat16: 222 us
+// and 305 us, 4.1 and 4.5 TB/s.  One row of 1024: 5.5 us, a launch.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
