@@ -213,8 +213,10 @@ size_t ecc_residual_norm_workspace_bytes(int64_t batch, int64_t inner, int64_t c
  *            initial one where there is none), to be carried to a next call
  *   saved    float32, ecc_gated_recurrence_saved_bytes: states that the backward
  *            pass starts from; NULL where there will be none
- * No output overlaps an input.  States are float32.  One launch, three where batch x channels is small
- * beside the card and the sequence is cut into parts.
+ * No output overlaps an input.  States are float32.  A step is formed from
+ * x_t - h_(t-1): where that is beyond float32, an infinite x or state among
+ * others, h is not finite from there on.  One launch, three where batch x
+ * channels is small beside the card and the sequence is cut into parts.
  */
 int ecc_gated_recurrence_fwd(const void* x, const void* gate, int dtype, int64_t batch, int64_t steps, int64_t channels,
                              const float* state, const int64_t* lengths, void* h, float* last, float* saved, void* ws,
@@ -254,7 +256,8 @@ int ecc_gated_linear_fwd(const void* x, int dtype, int64_t rows, int64_t channel
  * Its backward pass from grad_h = dL/dh (dtype, [rows][hidden]); the two
  * projections are formed again.  With a and b the projections,
  *   da = grad_h b act'(a), db = grad_h act(a)   (act'(0) = 0 for relu), each
- *   rounded once to dtype (up to 512 rows in two parts, with twice its bits), as operands of
+ *   rounded once to dtype (up to 512 rows in two parts, with twice its bits), as
+ *   operands of
  *   grad_x = da w_gate + db w_up, grad_w_gate = da^T x, grad_w_up = db^T x;
  *   grad_b_gate = sum da, grad_b_up = sum db, of the values before that rounding.
  * All of dtype and OVERWRITTEN; each may be NULL (not wanted), but not all.

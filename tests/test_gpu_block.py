@@ -267,3 +267,18 @@ def test_capture_beside_an_eager_graph_is_refused(which):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("steps", [9, 700])
+def test_infinite_input_of_the_recurrence(steps):
+    banner("recurrence infinite", steps)
+    gen = torch.Generator().manual_seed(8)
+    x, gate = (torch.randn(2, steps, 5, generator=gen).cuda() for _ in range(2))
+    want, _ = E.gated_recurrence(x, gate)
+    x[1, 4, 3] = float("inf")
+    h, last = E.gated_recurrence(x, gate)
+    # x - h is infinite: infinity or, where the gate takes x and gives back a part of the difference, NaN
+    assert not torch.isfinite(h[1, 4:, 3]).any() and not torch.isfinite(last[1, 3])
+    keep = torch.ones_like(h, dtype=torch.bool)
+    keep[1, 4:, 3] = False
+    assert torch.equal(h[keep], want[keep])
