@@ -212,16 +212,13 @@ inline size_t glu_part_bytes(const GluShare& s, int both) {
 // Up to so many rows the weights are read once, straight to registers.
 constexpr int64_t kGluFew = 64;
 
-// Up to so many rows the projections' 16-bit gradients are kept in two parts.
-constexpr int64_t kGluPairs = 512;
-
 // Workspace: x and both weights with rows of whole steps, where theirs are not
 // whole 16-byte chunks (`packed`); in the backward pass the gradients of both
-// projections (rows of 2 x pitch elements), partial sums of the bias gradients
-// and shares of products.
+// projections (rows of 2 x pitch elements, of 4 where they have 16 bits and are
+// kept in two parts), partial sums of the bias gradients and shares of products.
 struct GluPlan {
   bool packed;
-  bool pairs;     // 16-bit gradients of the projections in two parts
+  bool pairs;     // gradients of the projections in two parts
   int64_t wide;   // elements of a packed row
   int64_t walkers;  // workgroups that share the rows of a narrow product, or 0
   int64_t pitch;  // elements from the gate's gradients to the other's
@@ -232,12 +229,8 @@ inline GluPlan glu_plan(int64_t rows, int64_t channels, int64_t hidden, int elem
   GluPlan p{};
   const int step = 64 / elem;  // elements of a step along the summed axis
   p.pitch = (hidden + 63) / 64 * 64;
-  p.pairs = elem == 2 && rows <= kGluPairs;
+  p.pairs = elem == 2;
   p.gates = glu_share(rows, 2 * hidden, channels, 1, step, false);
-  if (p.pairs && backward) {  // (only the small tiles have registers for both parts)
-    p.gates.FM = 1;
-    p.gates.tiles_m = (rows + 63) / 64;
-  }
   p.gates.tiles_n = (hidden + 63) / 64;  // 64 of both projections a tile
   p.input = glu_share(rows, channels, (p.pairs ? 4 : 2) * hidden, 1, step, true);
   p.weight = glu_share(hidden, channels, (p.pairs ? 2 : 1) * rows, 2, step, true);

@@ -10,11 +10,12 @@
 // results a workgroup of four waves, steps of 64 bytes along the summed axis
 // through LDS, float32 sums.  A tile of the forward product holds the same 64
 // hidden units of both projections, so activation and product are its epilogue;
-// the backward one's is da and db, rounded once to the element type (they are
-// the next products' operands: the error is that of the results' own rounding,
-// 1.41 times it in all) and written to the workspace.  With few rows sums do not
-// even such errors out, and the products are bound by the weights' way to memory:
-// there what the rounding leaves is kept and multiplied too.
+// the backward one's is da and db, written to the workspace as the next products'
+// operands.  Of 16 bits they are kept in two parts, the number rounded and what
+// that leaves, and both are multiplied: with the first alone dx and dW were 1.41
+// times as far off as their own rounding (1.6 times in single elements), however
+// many terms a sum has, as relative errors of the terms pass on to it.  It makes
+// dx and dW twice the products.
 //
 // Operands of two kinds: those that lie along the summed axis, and those that
 // lie across it (the weights in dx, both operands in dW).  The second are kept
@@ -60,6 +61,8 @@ template <class T>
 constexpr int kPer = 16 / (int)sizeof(T);  // elements of a 16-byte chunk
 template <class T>
 constexpr int kStep = 64 / (int)sizeof(T);  // elements of a step along the summed axis
+template <class T>
+constexpr bool kPairs = sizeof(T) == 2;  // da and db in two parts, the second 2 pitch further on
 
 // One product.
 template <class T>
@@ -76,7 +79,6 @@ struct Product {
   GluArgs a;
   int64_t pitch;   // of the workspace's gradients
   T* dab;
-  bool pairs;      // what rounding leaves of these gradients is kept too, 2 pitch further on
   float* bias;     // partial sums of da and db, null: not wanted
   T* out[2];
   int64_t pitch_out;
@@ -360,9 +362,8 @@ __device__ __forceinline__ void forward_fragment(const Product<T>& p, const Stag
 }
 
 // Its gradients: `gh` has the result's.  Sums are over the fragments; rows that
-// are not there have no gradient, but may have infinite projections.  PAIRS:
-// whether there may be few rows.
-template <class T, int ACT, bool PAIRS, class Between>
+// are not there have no gradient, but may have infinite projections.
+template <class T, int ACT, class Between>
 __device__ __forceinline__ void gates_fragment(const Product<T>& p, const Stage<T>& stage, const f32x4* bias, const f32x16& a,
                                                const f32x16& b, int64_t row, int64_t unit0,
                                                u32x4 (&gh)[Stage<T>::kTurns], float (&sum_a)[16], float (&sum_b)[16],
@@ -383,20 +384,19 @@ __device__ __forceinline__ void gates_fragment(const Product<T>& p, const Stage<
       g[r] *= y;
       // both parts come from this number: a product rounded straight to 16 bits
       // for one of them alone is a step off where it lies between two
-      if constexpr (PAIRS) asm("" : "+v"(da[r]), "+v"(g[r]));
+      if constexpr (kPairs<T>) asm("" : "+v"(da[r]), "+v"(g[r]));
       sum_a[r] += in ? da[r] : 0.0f;
       sum_b[r] += in ? g[r] : 0.0f;
     }
     __builtin_amdgcn_sched_barrier(0);  // all at once would not fit the registers
   }
-  const bool pairs = PAIRS && p.pairs;
-  const int64_t line = (pairs ? 4 : 2) * p.pitch;
+  const int64_t line = (kPairs<T> ? 4 : 2) * p.pitch;
   T* out = p.dab + row * line + unit0;
   stage.put(da);
   stage.store(out, line, p.M - row, p.N - unit0);
   stage.put(g);
   stage.store(out + p.pitch, line, p.M - row, p.N - unit0);
-  if (pairs) {
+  if constexpr (kPairs<T>) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       da[r] -= (float)(T)da[r];
@@ -453,7 +453,7 @@ __device__ __forceinline__ void epilogue(const Product<T>& p, int z, int64_t tm,
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int64_t row = row0 + i * 32;
-        gates_fragment<T, ACT, FM == 1>(p, stage, bias, acc[i][0], acc[i][1], row, unit0, next, sum_a, sum_b, [&] {
+        gates_fragment<T, ACT>(p, stage, bias, acc[i][0], acc[i][1], row, unit0, next, sum_a, sum_b, [&] {
           if (i + 1 < FM) Stage<T>::load(gh + (row + 32) * p.N + unit0, p.N, p.M - row - 32, p.N - unit0, next);
         });
       }
@@ -754,7 +754,7 @@ __global__ __launch_bounds__(kNT, 2) void glu_narrow_kernel(Product<T> p, int wa
   // What a wave whose units are all there issues in a turn after its rows' loads,
   // which two turns later are complete when so much is left: stores, the
   // gradients' loads, and one of the rows' in between.
-  constexpr int kAfter = 2 * (KIND == kGates ? 3 * kTurns : kTurns) + 1;
+  constexpr int kAfter = 2 * (KIND == kGates ? (kPairs<T> ? 5 : 3) * kTurns : kTurns) + 1;
   const bool counted = unit0 + 32 <= p.N;
   int turn = 0;
   for (int64_t tm = walker; tm < tiles_m; tm += walkers) {
@@ -772,7 +772,7 @@ __global__ __launch_bounds__(kNT, 2) void glu_narrow_kernel(Product<T> p, int wa
     if constexpr (KIND == kForward)
       forward_fragment<T, ACT>(p, stage, bias, acc[0][0], acc[0][1], row, unit0);
     else
-      gates_fragment<T, ACT, false>(p, stage, bias, acc[0][0], acc[0][1], row, unit0, next, sum_a, sum_b, [&] {
+      gates_fragment<T, ACT>(p, stage, bias, acc[0][0], acc[0][1], row, unit0, next, sum_a, sum_b, [&] {
         if (tm + walkers < tiles_m) fetch_gradients(tm + walkers);
       });
   }
@@ -1087,7 +1087,6 @@ hipError_t launch_glu_bwd(const GluArgs& a, hipStream_t stream) {
   const T* x = p.A;
   p.pitch = plan.pitch;
   p.dab = reinterpret_cast<T*>(ws + plan.at_dab);
-  p.pairs = plan.pairs;
   p.bias = a.gbg || a.gbu ? reinterpret_cast<float*>(ws + plan.at_bias) : nullptr;
   p.part = reinterpret_cast<float*>(ws + plan.at_part);
   hipError_t st = launch_projections<T, kGates>(p, plan, stream, &p.tiles_m);

@@ -255,8 +255,8 @@ int ecc_gated_linear_fwd(const void* x, int dtype, int64_t rows, int64_t channel
 /*
  * Its backward pass from grad_h = dL/dh (dtype, [rows][hidden]); the two
  * projections are formed again.  With a and b the projections,
- *   da = grad_h b act'(a), db = grad_h act(a)   (act'(0) = 0 for relu), each
- *   rounded once to dtype (up to 512 rows in two parts, with twice its bits), as
+ *   da = grad_h b act'(a), db = grad_h act(a)   (act'(0) = 0 for relu), float32,
+ *   or where dtype has 16 bits two numbers of dtype, with twice its bits, as
  *   operands of
  *   grad_x = da w_gate + db w_up, grad_w_gate = da^T x, grad_w_up = db^T x;
  *   grad_b_gate = sum da, grad_b_up = sum db, of the values before that rounding.

@@ -1,0 +1,96 @@
+"""The gradients of the projections between gated_linear's products, in 16 bits: what dx and dW lose by them is far below
+the results' own rounding at every size."""
+
+import pytest
+import torch
+
+import euler_characteristic_curves_amd as E
+from tests.block_bounds import gated_linear
+from tests.gpu_util import banner, need_gpu
+from tests.norm_bounds import HALF, TINY, _vec, act_and_slope, rounded, worst
+from tests.norm_bounds import E as STEP
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+NAMES = ("x", "w_gate", "w_up", "b_gate", "b_up")
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def make(rows, C, F, dtype, scale=1.0, bias=True, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    t = {"x": rnd(rows, C), "w_gate": rnd(F, C) / C ** 0.5, "w_up": rnd(F, C) / C ** 0.5}
+    if bias:
+        t.update(b_gate=0.3 * rnd(F), b_up=0.3 * rnd(F))
+    # of one sign mostly, so that sums over rows are of the size of their terms
+    gh = (scale * (0.25 + torch.rand(rows, F, generator=gen))).to(dtype)
+    return {k: v.to(dtype) for k, v in t.items()}, gh
+
+
+def gradients(t, gh, act):
+    d = {k: v.cuda().requires_grad_() for k, v in t.items()}
+    out = E.gated_linear(*(d.get(k) for k in NAMES), act=act)
+    return dict(zip(d, torch.autograd.grad(out, list(d.values()), gh.cuda())))
+
+
+def bounds(t, gh, act):
+    """{name: (value, bound)} of dx and both dW: da and db in two parts, the second one's rounding a half step of a half
+    step.  The rest is as in block_bounds.gated_linear."""
+    dt = gh.dtype
+    xd, wg, wu = (t[k].double() for k in ("x", "w_gate", "w_up"))
+    (n, C), F = xd.shape, wg.shape[0]
+    bg, bu = _vec(t.get("b_gate"), F, 0.0), _vec(t.get("b_up"), F, 0.0)
+    a, b = xd @ wg.T + bg, xd @ wu.T + bu
+    a_, b_ = ((C + 1) * STEP * (xd.abs() @ w.abs().T + v.abs()) for w, v in ((wg, bg), (wu, bu)))
+    y, sl = act_and_slope(a, act)
+    y_ = 1.2 * a_ + 2.0 ** -20 * a.abs()
+    sl_ = a_ + 2.0 ** -20 * (1 + a.abs())
+    g = gh.double()
+    da, db = g * b * sl, g * y
+    da_ = g.abs() * (b.abs() * sl_ + sl.abs() * b_ + b_ * sl_) + 3 * STEP * da.abs()
+    db_ = g.abs() * y_ + 2 * STEP * db.abs()
+    ra, rb = (v_ + HALF[dt] ** 2 * v.abs() + TINY[dt] for v, v_ in ((da, da_), (db, db_)))
+    # parts are products of their own: twice as many terms
+    dx = da @ wg + db @ wu
+    dx_ = ra @ wg.abs() + rb @ wu.abs() + (4 * F + 1) * STEP * (da.abs() @ wg.abs() + db.abs() @ wu.abs())
+    out = {"x": (dx, rounded(dx, dx_, dt))}
+    for name, v, r in (("w_gate", da, ra), ("w_up", db, rb)):
+        s, s_ = v.T @ xd, r.T @ xd.abs() + (2 * n + 1) * STEP * (v.abs().T @ xd.abs())
+        out[name] = (s, rounded(s, s_, dt))
+    return out
+
+
+# up to 512 rows and beyond, in small tiles and large, narrow sums, sums in shares
+SHAPES = [(512, 48, 24), (513, 48, 24), (600, 33, 17), (2050, 136, 24), (5000, 64, 40), (4100, 40, 9), (3000, 72, 1610)]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_two_parts_at_every_size(shape, act, dtype):
+    banner("glu parts", shape, act, dtype)
+    t, gh = make(*shape, dtype, bias=act == "silu", seed=sum(shape))
+    want, got = bounds(t, gh, act), gradients(t, gh, act)
+    for name in want:
+        ratio = worst(got[name], want[name])
+        assert ratio <= 1, (name, ratio)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("shape", [(700, 64, 96), (4500, 64, 160), (2048, 512, 1408)], ids=lambda s: "x".join(map(str, s)))
+def test_error_is_the_results_own_rounding(shape, dtype):
+    """Root mean squares: the second part leaves HALF of a rounding, the float32 sums some sqrt(n) 2^-24 of the terms,
+    2e-5 of HALF / sqrt 3 = 2.8e-4 at most; both in quadrature are below a hundredth of the rounding."""
+    banner("glu rounding", shape, dtype)
+    t, gh = make(*shape, dtype, seed=1)
+    gh = (gh - 0.75).to(dtype)
+    want, got = gated_linear(**t, gh=gh), gradients(t, gh, "silu")
+    for name in ("x", "w_gate", "w_up"):
+        exact = want[name][0]
+        own = (exact.to(dtype).double() - exact).norm()
+        err = (got[name].double().cpu() - exact).norm()
+        assert err <= 1.02 * own, (name, float(err / own))
