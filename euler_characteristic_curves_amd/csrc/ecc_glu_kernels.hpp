@@ -62,7 +62,15 @@ constexpr int kPer = 16 / (int)sizeof(T);  // elements of a 16-byte chunk
 template <class T>
 constexpr int kStep = 64 / (int)sizeof(T);  // elements of a step along the summed axis
 template <class T>
-constexpr bool kPairs = sizeof(T) == 2;  // da and db in two parts, the second 2 pitch further on
+constexpr bool kPairs = sizeof(T) == 2;  // da and db in two parts: what rounding leaves, 2 pitch further on what it rounds to
+// float16 has the mantissa but not the range: da is 2^4 (second + 2^-11 first) of
+// its parts, so that numbers up to 2^20 are there, and steps of 2^-31 (of parts
+// that are simply added 65504, and 2^-24: a loss that is scaled for training in
+// float16 went beyond the one, 5000 rows of gradients of 2^-22 had dW off by 57
+// times its rounding for the other).
+template <class T>
+constexpr bool kScaled = std::is_same<T, f16>::value;
+constexpr float kPartScale = 0x1p-4f, kRestScale = 0x1p11f;
 
 // One product.
 template <class T>
@@ -72,7 +80,7 @@ struct Product {
   const T* B[2];
   int64_t pitchB;
   int64_t M, N, K;  // N: hidden units of one projection in a dual product; K of one part of the sum
-  int parts;        // parts of the sum: in dx A + i stepA with B[i % 2], in dW A + (z + 2 i) stepA
+  int parts;        // parts of the sum, rests first: in dx A + i stepA with B[i % 2], in dW A + (z + 2 i) stepA
   int splits;
   int64_t tiles_m, tiles_n;
   float* part;
@@ -391,21 +399,30 @@ __device__ __forceinline__ void gates_fragment(const Product<T>& p, const Stage<
     __builtin_amdgcn_sched_barrier(0);  // all at once would not fit the registers
   }
   const int64_t line = (kPairs<T> ? 4 : 2) * p.pitch;
-  T* out = p.dab + row * line + unit0;
+  T* rest = p.dab + row * line + unit0;
+  T* out = rest + (kPairs<T> ? 2 : 0) * p.pitch;
+  if constexpr (kScaled<T>) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      da[r] *= kPartScale;
+      g[r] *= kPartScale;
+    }
+  }
   stage.put(da);
   stage.store(out, line, p.M - row, p.N - unit0);
   stage.put(g);
   stage.store(out + p.pitch, line, p.M - row, p.N - unit0);
   if constexpr (kPairs<T>) {
+    constexpr float scale = kScaled<T> ? kRestScale : 1.0f;
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      da[r] -= (float)(T)da[r];
-      g[r] -= (float)(T)g[r];
+      da[r] = (da[r] - (float)(T)da[r]) * scale;
+      g[r] = (g[r] - (float)(T)g[r]) * scale;
     }
     stage.put(da);
-    stage.store(out + 2 * p.pitch, line, p.M - row, p.N - unit0);
+    stage.store(rest, line, p.M - row, p.N - unit0);
     stage.put(g);
-    stage.store(out + 3 * p.pitch, line, p.M - row, p.N - unit0);
+    stage.store(rest + p.pitch, line, p.M - row, p.N - unit0);
   }
 }
 
@@ -467,7 +484,7 @@ __device__ __forceinline__ void epilogue(const Product<T>& p, int z, int64_t tm,
         const int64_t row = row0 + i * 32, col = tn * 64 * FN + wn * FN * 32 + j * 32;
         float v[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) v[r] = acc[i][j][r];
+        for (int r = 0; r < 16; ++r) v[r] = kScaled<T> ? acc[i][j][r] * (1.0f / kPartScale) : acc[i][j][r];
         stage.put(v);
         stage.store(p.out[z] + row * p.pitch_out + col, p.pitch_out, p.M - row, p.N - col);
       }
@@ -542,13 +559,14 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
   const int z = KIND == kWeight && id.tm >= p.tiles_m ? 1 : 0, split = id.share;
   const int64_t tm = id.tm - z * p.tiles_m, tn = id.tn;
   if (KIND == kWeight && !p.out[z]) return;  // not wanted
-  // steps of the sum: the whole ones of every part, then what is left of each;
-  // this workgroup's are [from, to)
+  // steps of the sum: the whole ones of every part, then what is left of each; in
+  // two groups where the rests have a scale of their own
+  constexpr int kGroups = kScaled<T> && !is_dual(KIND) ? 2 : 1;
   const int left = (int)(p.K % kStep<T>), whole = (int)(p.K / kStep<T>) + (!ALIGNED && left ? 1 : 0);
-  const int direct = whole * p.parts, all = ALIGNED && left ? direct + p.parts : direct;
-  const int share = __builtin_amdgcn_readfirstlane((all + p.splits - 1) / p.splits), from = split * share;
-  const int to = from + share < all ? from + share : all;
-  const auto place = [&](int s, int& part, int64_t& k0) {
+  const int parts = p.parts / kGroups, direct = whole * parts, all = ALIGNED && left ? direct + parts : direct;
+  const int share = __builtin_amdgcn_readfirstlane((all * kGroups + p.splits - 1) / p.splits);
+  int group = 0;
+  const auto place = [&](int s, int& part, int64_t& k0) {  // step s of the group
     part = 0;
     if (ALIGNED && s >= direct) {
       part = s - direct;
@@ -557,6 +575,7 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
       if (!is_dual(KIND)) part = (s >= whole) + (s >= 2 * whole) + (s >= 3 * whole);
       k0 = (int64_t)(s - part * whole) * kStep<T>;
     }
+    part += group * parts;
   };
   const auto base_a = [&](int part) { return p.A + (KIND == kWeight ? z + 2 * part : part) * p.stepA; };
   f32x16 acc[FM][FN];
@@ -587,8 +606,8 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
 #pragma unroll
     for (int i = 0; i < TileB::kChunks; ++i) *reinterpret_cast<u32x4*>(lb + (i * kNT + threadIdx.x) * 16) = rb[i];
   };
+  uint32_t offA[TileA::kChunks], offB[TileB::kChunks];
   if constexpr (ALIGNED) {
-    uint32_t offA[TileA::kChunks], offB[TileB::kChunks];
 #pragma unroll
     for (int i = 0; i < TileA::kChunks; ++i) offA[i] = TileA::offset(p.pitchA, tm * TM, KIND == kWeight ? p.pitch : p.M, i);
 #pragma unroll
@@ -598,79 +617,96 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
       else
         offB[i] = TileB::offset(p.pitchB, tn * TN, b_along(KIND) ? p.N : p.pitchB, i);
     }
-    const int last = to < direct ? to : direct;  // of those that go straight to LDS
-    const T *const first0 = p.B[0], *const first1 = p.B[1];
-    // a step's first elements of A, and of B (of both projections)
-    struct Bases {
-      const T *a, *b0, *b1;
-    };
-    const auto bases = [&](int s) {
-      int part;
-      int64_t k0;
-      place(s, part, k0);
-      const T* A = base_a(part);
-      Bases r;
-      r.a = a_along(KIND) ? A + tm * TM * p.pitchA + k0 : A + k0 * p.pitchA + tm * TM;
-      if constexpr (is_dual(KIND)) {
-        r.b0 = first0 + tn * 64 * p.pitchB + k0;
-        r.b1 = first1 + tn * 64 * p.pitchB + k0;
-      } else {
-        const T* B = first0;
-        if (KIND == kInput && part & 1) B = first1;
-        r.b0 = r.b1 = B + k0 * p.pitchB + tn * TN;
-      }
-      return r;
-    };
-    const auto load = [&](const Bases& r, int s, char* la, char* lb, int i) {  // chunk i, A's first
-      if (i < FM)
-        load_chunk(r.a, offA[i], wave_lds(la) + i * (kNT * 16), s, last);
-      else
-        load_chunk(is_dual(KIND) && i > FM ? r.b1 : r.b0, offB[i - FM], wave_lds(lb) + (i - FM) * (kNT * 16), s, last);
-    };
-    const auto load_all = [&](int s, char* la, char* lb) {
-      const Bases r = bases(s);
+  }
+#pragma unroll 1
+  for (; group < kGroups; ++group) {
+    // this workgroup's steps are [from, to)
+    const auto within = [&](int s) { return s < 0 ? 0 : (s < all ? s : all); };
+    const int from = within(split * share - group * all), to = within((split + 1) * share - group * all);
+    if constexpr (ALIGNED) {
+      const int last = to < direct ? to : direct;  // of those that go straight to LDS
+      const T *const first0 = p.B[0], *const first1 = p.B[1];
+      // a step's first elements of A, and of B (of both projections)
+      struct Bases {
+        const T *a, *b0, *b1;
+      };
+      const auto bases = [&](int s) {
+        int part;
+        int64_t k0;
+        place(s, part, k0);
+        const T* A = base_a(part);
+        Bases r;
+        r.a = a_along(KIND) ? A + tm * TM * p.pitchA + k0 : A + k0 * p.pitchA + tm * TM;
+        if constexpr (is_dual(KIND)) {
+          r.b0 = first0 + tn * 64 * p.pitchB + k0;
+          r.b1 = first1 + tn * 64 * p.pitchB + k0;
+        } else {
+          const T* B = first0;
+          if (KIND == kInput && part & 1) B = first1;
+          r.b0 = r.b1 = B + k0 * p.pitchB + tn * TN;
+        }
+        return r;
+      };
+      const auto load = [&](const Bases& r, int s, char* la, char* lb, int i) {  // chunk i, A's first
+        if (i < FM)
+          load_chunk(r.a, offA[i], wave_lds(la) + i * (kNT * 16), s, last);
+        else
+          load_chunk(is_dual(KIND) && i > FM ? r.b1 : r.b0, offB[i - FM], wave_lds(lb) + (i - FM) * (kNT * 16), s, last);
+      };
+      const auto load_all = [&](int s, char* la, char* lb) {
+        const Bases r = bases(s);
 #pragma unroll
-      for (int i = 0; i < FM + FN; ++i) load(r, s, la, lb, i);
-    };
-    const auto step = [&](int s, char* la, char* lb, char* na, char* nb) {
-      if (s >= last) return;
-      const Bases r = bases(s + 2);
-      if (s + 1 < last)
-        wait_loads<FM + FN>();
-      else
-        wait_loads<0>();
-      multiply_step<T, KIND, FM, FN>(la, lb, acc, [&](int i) { load(r, s + 2, na, nb, i); });
-    };
-    load_all(from, a0, b0);
-    load_all(from + 1, a1, b1);
-    for (int s = from; s < last; s += 3) {
-      step(s, a0, b0, a2, b2);
-      step(s + 1, a1, b1, a0, b0);
-      step(s + 2, a2, b2, a1, b1);
-    }
-    for (int s = from > direct ? from : direct; s < to; ++s) {
+        for (int i = 0; i < FM + FN; ++i) load(r, s, la, lb, i);
+      };
+      const auto step = [&](int s, char* la, char* lb, char* na, char* nb) {
+        if (s >= last) return;
+        const Bases r = bases(s + 2);
+        if (s + 1 < last)
+          wait_loads<FM + FN>();
+        else
+          wait_loads<0>();
+        multiply_step<T, KIND, FM, FN>(la, lb, acc, [&](int i) { load(r, s + 2, na, nb, i); });
+      };
+      load_all(from, a0, b0);
+      load_all(from + 1, a1, b1);
+      for (int s = from; s < last; s += 3) {
+        step(s, a0, b0, a2, b2);
+        step(s + 1, a1, b1, a0, b0);
+        step(s + 2, a2, b2, a1, b1);
+      }
+      for (int s = from > direct ? from : direct; s < to; ++s) {
+        __syncthreads();
+        fetch(s);
+        put(a0, b0);
+        __syncthreads();
+        multiply_step<T, KIND, FM, FN>(a0, b0, acc, [](int) {});
+      }
+    } else {
+      if (from < to) {
+        fetch(from);
+        put(a0, b0);
+      }
       __syncthreads();
-      fetch(s);
-      put(a0, b0);
-      __syncthreads();
-      multiply_step<T, KIND, FM, FN>(a0, b0, acc, [](int) {});
+      const auto step = [&](int s, char* la, char* lb, char* na, char* nb) {
+        if (s >= to) return;
+        if (s + 1 < to) fetch(s + 1);
+        multiply_step<T, KIND, FM, FN>(la, lb, acc, [](int) {});
+        if (s + 1 < to) put(na, nb);
+        __syncthreads();
+      };
+      for (int s = from; s < to; s += 2) {
+        step(s, a0, b0, a1, b1);
+        step(s + 1, a1, b1, a0, b0);
+      }
     }
-  } else {
-    if (from < to) {
-      fetch(from);
-      put(a0, b0);
-    }
-    __syncthreads();
-    const auto step = [&](int s, char* la, char* lb, char* na, char* nb) {
-      if (s >= to) return;
-      if (s + 1 < to) fetch(s + 1);
-      multiply_step<T, KIND, FM, FN>(la, lb, acc, [](int) {});
-      if (s + 1 < to) put(na, nb);
-      __syncthreads();
-    };
-    for (int s = from; s < to; s += 2) {
-      step(s, a0, b0, a1, b1);
-      step(s + 1, a1, b1, a0, b0);
+    if (group + 1 < kGroups) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][j][r] *= 1.0f / kRestScale;
+      __syncthreads();  // the stages are free
     }
   }
   if (p.splits > 1) {
@@ -813,7 +849,7 @@ __global__ __launch_bounds__(kJoin) void glu_join_kernel(Product<T> p) {
   for (int q = 0; q < 4; ++q) {
     for (int g = 0; g < 3; ++g) v[q] += lds[g][q][thread];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) u[q * 4 + r] = v[q][r];
+    for (int r = 0; r < 4; ++r) u[q * 4 + r] = kScaled<T> ? v[q][r] * (1.0f / kPartScale) : v[q][r];
   }
   const int64_t tn = tile % p.tiles_n, tm = tile / p.tiles_n - z * p.tiles_m;
   const int wave = __builtin_amdgcn_readfirstlane(thread >> 6), wm = wave >> 1, wn = wave & 1;

@@ -260,6 +260,7 @@ int ecc_gated_linear_fwd(const void* x, int dtype, int64_t rows, int64_t channel
  *   operands of
  *   grad_x = da w_gate + db w_up, grad_w_gate = da^T x, grad_w_up = db^T x;
  *   grad_b_gate = sum da, grad_b_up = sum db, of the values before that rounding.
+ * In float16 da and db may be up to 2^20, and are kept to 2^-32 at least.
  * All of dtype and OVERWRITTEN; each may be NULL (not wanted), but not all.
  */
 int ecc_gated_linear_bwd(const void* x, int dtype, int64_t rows, int64_t channels, int64_t hidden, const void* w_gate,

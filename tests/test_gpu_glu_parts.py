@@ -1,5 +1,5 @@
 """The gradients of the projections between gated_linear's products, in 16 bits: what dx and dW lose by them is far below
-the results' own rounding at every size."""
+the results' own rounding at every size, and float16's range does not end where the results' does not."""
 
 import pytest
 import torch
@@ -7,7 +7,7 @@ import torch
 import euler_characteristic_curves_amd as E
 from tests.block_bounds import gated_linear
 from tests.gpu_util import banner, need_gpu
-from tests.norm_bounds import HALF, TINY, _vec, act_and_slope, rounded, worst
+from tests.norm_bounds import HALF, _vec, act_and_slope, rounded, worst
 from tests.norm_bounds import E as STEP
 
 pytestmark = pytest.mark.gpu
@@ -39,7 +39,8 @@ def gradients(t, gh, act):
 
 def bounds(t, gh, act):
     """{name: (value, bound)} of dx and both dW: da and db in two parts, the second one's rounding a half step of a half
-    step.  The rest is as in block_bounds.gated_linear."""
+    step, and below float16's range 2^-32 (the second part is kept 2^7 times as large).  The rest is as in
+    block_bounds.gated_linear."""
     dt = gh.dtype
     xd, wg, wu = (t[k].double() for k in ("x", "w_gate", "w_up"))
     (n, C), F = xd.shape, wg.shape[0]
@@ -53,7 +54,8 @@ def bounds(t, gh, act):
     da, db = g * b * sl, g * y
     da_ = g.abs() * (b.abs() * sl_ + sl.abs() * b_ + b_ * sl_) + 3 * STEP * da.abs()
     db_ = g.abs() * y_ + 2 * STEP * db.abs()
-    ra, rb = (v_ + HALF[dt] ** 2 * v.abs() + TINY[dt] for v, v_ in ((da, da_), (db, db_)))
+    tiny = 2.0 ** -32 if dt == F16 else 2.0 ** -126
+    ra, rb = (v_ + HALF[dt] ** 2 * v.abs() + tiny for v, v_ in ((da, da_), (db, db_)))
     # parts are products of their own: twice as many terms
     dx = da @ wg + db @ wu
     dx_ = ra @ wg.abs() + rb @ wu.abs() + (4 * F + 1) * STEP * (da.abs() @ wg.abs() + db.abs() @ wu.abs())
@@ -94,3 +96,21 @@ def test_error_is_the_results_own_rounding(shape, dtype):
         own = (exact.to(dtype).double() - exact).norm()
         err = (got[name].double().cpu() - exact).norm()
         assert err <= 1.02 * own, (name, float(err / own))
+
+
+@pytest.mark.parametrize("act", ["silu", "none"])
+@pytest.mark.parametrize("shape", [(1, 64, 160), (300, 64, 160), (5000, 64, 160), (2100, 520, 160)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("scale", [2.0 ** -22, 2.0 ** -16, 2.0 ** 14], ids=["tiny", "small", "large"])
+def test_range_of_float16(scale, shape, act):
+    """Gradients as a scaled loss has them and as one without scaling has: da and db pass float16's largest number, or
+    are a few of its smallest steps, where dx and dW are numbers of their own."""
+    banner("glu range", scale, shape, act)
+    t, gh = make(*shape, F16, scale, bias=False, seed=2)
+    want, got = bounds(t, gh, act), gradients(t, gh, act)
+    for name in want:
+        v, b = want[name]
+        there = v.abs() < 65000  # (the others round to infinity, or may)
+        assert there.any()
+        ratio = worst(got[name].cpu()[there], (v[there], b[there]))
+        assert ratio <= 1, (name, ratio)
