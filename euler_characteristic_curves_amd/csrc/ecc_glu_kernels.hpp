@@ -369,6 +369,13 @@ __device__ __forceinline__ void forward_fragment(const Product<T>& p, const Stag
   stage.store(reinterpret_cast<T*>(p.a.h) + row * p.N + unit0, p.N, p.M - row, p.N - unit0);
 }
 
+// What rounding leaves: nothing of an infinity or a NaN, which the number itself passes on.
+template <class T>
+__device__ __forceinline__ float rest_of(float v) {
+  const float first = (float)(T)v;
+  return fabsf(first) < __builtin_inff() ? (v - first) * (kScaled<T> ? kRestScale : 1.0f) : 0.0f;
+}
+
 // Its gradients: `gh` has the result's.  Sums are over the fragments; rows that
 // are not there have no gradient, but may have infinite projections.
 template <class T, int ACT, class Between>
@@ -413,11 +420,10 @@ __device__ __forceinline__ void gates_fragment(const Product<T>& p, const Stage<
   stage.put(g);
   stage.store(out + p.pitch, line, p.M - row, p.N - unit0);
   if constexpr (kPairs<T>) {
-    constexpr float scale = kScaled<T> ? kRestScale : 1.0f;
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      da[r] = (da[r] - (float)(T)da[r]) * scale;
-      g[r] = (g[r] - (float)(T)g[r]) * scale;
+      da[r] = rest_of<T>(da[r]);
+      g[r] = rest_of<T>(g[r]);
     }
     stage.put(da);
     stage.store(rest, line, p.M - row, p.N - unit0);

@@ -114,3 +114,21 @@ def test_range_of_float16(scale, shape, act):
         assert there.any()
         ratio = worst(got[name].cpu()[there], (v[there], b[there]))
         assert ratio <= 1, (name, ratio)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("rows", [40, 700])
+def test_infinite_gradient(rows, dtype):
+    """An infinite gradient is infinite in both parts of nothing: where weights have one sign, so has the result."""
+    banner("glu infinite gradient", rows, dtype)
+    t, gh = make(rows, 24, 16, dtype, bias=False, seed=3)
+    t["x"], t["w_gate"], t["w_up"] = (v.abs() + 0.1 for v in (t["x"], t["w_gate"], t["w_up"]))
+    gh[7, 5] = float("inf")
+    got = {k: v.cpu() for k, v in gradients(t, gh, "none").items()}
+    assert (got["x"][7] == float("inf")).all()
+    for k in ("w_gate", "w_up"):
+        assert (got[k][5] == float("inf")).all()
+        rest = [i for i in range(16) if i != 5]
+        assert torch.isfinite(got[k][rest]).all()
+    rest = [i for i in range(rows) if i != 7]
+    assert torch.isfinite(got["x"][rest]).all()
