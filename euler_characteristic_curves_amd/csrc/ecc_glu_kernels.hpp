@@ -376,13 +376,13 @@ __device__ __forceinline__ float rest_of(float v) {
   return fabsf(first) < __builtin_inff() ? (v - first) * (kScaled<T> ? kRestScale : 1.0f) : 0.0f;
 }
 
-// Its gradients: `gh` has the result's.  Sums are over the fragments; rows that
-// are not there have no gradient, but may have infinite projections.
-template <class T, int ACT, class Between>
+// Its gradients: `gh` has the result's.  sums(q, in, da, db) adds numbers 4 q to
+// 4 q + 3 to the sums over rows; rows that are not there (`in`) have no gradient,
+// but may have infinite projections.
+template <class T, int ACT, class Sums, class Between>
 __device__ __forceinline__ void gates_fragment(const Product<T>& p, const Stage<T>& stage, const f32x4* bias, const f32x16& a,
                                                const f32x16& b, int64_t row, int64_t unit0,
-                                               u32x4 (&gh)[Stage<T>::kTurns], float (&sum_a)[16], float (&sum_b)[16],
-                                               Between between) {
+                                               u32x4 (&gh)[Stage<T>::kTurns], Sums sums, Between between) {
   const bool in = row + (threadIdx.x & 31) < p.M;
   float g[16], da[16];
   stage.place(gh);
@@ -400,33 +400,36 @@ __device__ __forceinline__ void gates_fragment(const Product<T>& p, const Stage<
       // both parts come from this number: a product rounded straight to 16 bits
       // for one of them alone is a step off where it lies between two
       if constexpr (kPairs<T>) asm("" : "+v"(da[r]), "+v"(g[r]));
-      sum_a[r] += in ? da[r] : 0.0f;
-      sum_b[r] += in ? g[r] : 0.0f;
+    }
+    sums(q, in, da, g);
+    if constexpr (kScaled<T>) {
+#pragma unroll
+      for (int r = q * 4; r < q * 4 + 4; ++r) {
+        da[r] *= kPartScale;
+        g[r] *= kPartScale;
+      }
     }
     __builtin_amdgcn_sched_barrier(0);  // all at once would not fit the registers
   }
   const int64_t line = (kPairs<T> ? 4 : 2) * p.pitch;
   T* rest = p.dab + row * line + unit0;
   T* out = rest + (kPairs<T> ? 2 : 0) * p.pitch;
-  if constexpr (kScaled<T>) {
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      da[r] *= kPartScale;
-      g[r] *= kPartScale;
-    }
-  }
   stage.put(da);
   stage.store(out, line, p.M - row, p.N - unit0);
   stage.put(g);
   stage.store(out + p.pitch, line, p.M - row, p.N - unit0);
   if constexpr (kPairs<T>) {
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
+      asm("" : "+v"(da[r]), "+v"(g[r]));  // (rounded again: kept, the first parts do not fit the registers)
       da[r] = rest_of<T>(da[r]);
-      g[r] = rest_of<T>(g[r]);
     }
     stage.put(da);
     stage.store(rest, line, p.M - row, p.N - unit0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) g[r] = rest_of<T>(g[r]);
     stage.put(g);
     stage.store(rest + p.pitch, line, p.M - row, p.N - unit0);
   }
@@ -453,10 +456,11 @@ __device__ __forceinline__ void store_bias_sums(const Product<T>& p, int64_t par
 }
 
 // A workgroup's results: acc[i][j] is the fragment of rows wm FM 32 + 32 i.
-// lds: kStage bytes for this wave; shared: 128 floats for all of them.
+// lds: kStage bytes for this wave; shared: 128 floats for all of them; sums_a,
+// sums_b: 16 floats a thread, where FM > 1.
 template <class T, int KIND, int FM, int FN, int ACT>
 __device__ __forceinline__ void epilogue(const Product<T>& p, int z, int64_t tm, int64_t tn, f32x16 (&acc)[FM][FN], char* lds,
-                                         float* shared) {
+                                         float* shared, f32x4* sums_a, f32x4* sums_b) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
   const int64_t row0 = tm * 64 * FM + wm * FM * 32;
   const Stage<T> stage{lds};
@@ -472,15 +476,43 @@ __device__ __forceinline__ void epilogue(const Product<T>& p, int z, int64_t tm,
       const T* gh = reinterpret_cast<const T*>(p.a.gh);
       u32x4 next[Stage<T>::kTurns];
       Stage<T>::load(gh + row0 * p.N + unit0, p.N, p.M - row0, p.N - unit0, next);
-      float sum_a[16] = {}, sum_b[16] = {};
+      // sums of several fragments are in LDS: in registers they did not fit (46 of
+      // a lane's went to memory and back, 78 with float16)
+      float sum_a[16], sum_b[16];
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int64_t row = row0 + i * 32;
-        gates_fragment<T, ACT>(p, stage, bias, acc[i][0], acc[i][1], row, unit0, next, sum_a, sum_b, [&] {
+        const auto sums = [&](int q, bool in, const float(&da)[16], const float(&db)[16]) {
+          if (!p.bias) return;
+          f32x4 va = {}, vb = {};
+          const int at = q * kNT + threadIdx.x;
+          if (i > 0) va = sums_a[at], vb = sums_b[at];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            va[r] += in ? da[q * 4 + r] : 0.0f;
+            vb[r] += in ? db[q * 4 + r] : 0.0f;
+          }
+          if constexpr (FM > 1) {
+            sums_a[at] = va, sums_b[at] = vb;
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum_a[q * 4 + r] = va[r], sum_b[q * 4 + r] = vb[r];
+          }
+        };
+        gates_fragment<T, ACT>(p, stage, bias, acc[i][0], acc[i][1], row, unit0, next, sums, [&] {
           if (i + 1 < FM) Stage<T>::load(gh + (row + 32) * p.N + unit0, p.N, p.M - row - 32, p.N - unit0, next);
         });
       }
-      if (p.bias) store_bias_sums(p, tm, tn, sum_a, sum_b, lds, shared);
+      if (!p.bias) return;
+      if constexpr (FM > 1) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 va = sums_a[q * kNT + threadIdx.x], vb = sums_b[q * kNT + threadIdx.x];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sum_a[q * 4 + r] = va[r], sum_b[q * 4 + r] = vb[r];
+        }
+      }
+      store_bias_sums(p, tm, tn, sum_a, sum_b, lds, shared);
     }
   } else {
 #pragma unroll
@@ -560,7 +592,7 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
   using TileA = Tile<T, a_along(KIND), TM>;
   using TileB = Tile<T, b_along(KIND), TN>;
   // arrays of their own, so that a read of one is known not to wait for another's loads
-  __shared__ __align__(16) char a0[kA], b0[kB], a1[kA], b1[kB], a2[ALIGNED ? kA : 16], b2[ALIGNED ? kB : 16];
+  __shared__ __align__(16) char a0[kA], b0[kB], a1[kA], b1[kB], a2[ALIGNED ? kA : 512], b2[ALIGNED ? kB : 16];
   const TileId id = tile_of((uint32_t)p.tiles_m * (KIND == kWeight ? 2 : 1), (uint32_t)p.tiles_n, (uint32_t)p.splits);
   const int z = KIND == kWeight && id.tm >= p.tiles_m ? 1 : 0, split = id.share;
   const int64_t tm = id.tm - z * p.tiles_m, tn = id.tn;
@@ -733,7 +765,8 @@ __global__ __launch_bounds__(kNT, 2) void glu_kernel(Product<T> p) {
   }
   if (ALIGNED) wait_loads<0>();  // the stages are free
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  epilogue<T, KIND, FM, FN, ACT>(p, z, tm, tn, acc, (wave & 2 ? b1 : b0) + (wave & 1) * kStage, reinterpret_cast<float*>(a0));
+  epilogue<T, KIND, FM, FN, ACT>(p, z, tm, tn, acc, (wave & 2 ? b1 : b0) + (wave & 1) * kStage, reinterpret_cast<float*>(a2),
+                                     reinterpret_cast<f32x4*>(a0), reinterpret_cast<f32x4*>(a1));
 }
 
 // Narrow sums, of up to four steps: a workgroup keeps the weights of its 64 units
@@ -814,9 +847,18 @@ __global__ __launch_bounds__(kNT, 2) void glu_narrow_kernel(Product<T> p, int wa
     if constexpr (KIND == kForward)
       forward_fragment<T, ACT>(p, stage, bias, acc[0][0], acc[0][1], row, unit0);
     else
-      gates_fragment<T, ACT>(p, stage, bias, acc[0][0], acc[0][1], row, unit0, next, sum_a, sum_b, [&] {
-        if (tm + walkers < tiles_m) fetch_gradients(tm + walkers);
-      });
+      gates_fragment<T, ACT>(
+          p, stage, bias, acc[0][0], acc[0][1], row, unit0, next,
+          [&](int q, bool in, const float(&da)[16], const float(&db)[16]) {
+#pragma unroll
+            for (int r = q * 4; r < q * 4 + 4; ++r) {
+              sum_a[r] += in ? da[r] : 0.0f;
+              sum_b[r] += in ? db[r] : 0.0f;
+            }
+          },
+          [&] {
+            if (tm + walkers < tiles_m) fetch_gradients(tm + walkers);
+          });
   }
   if constexpr (KIND == kGates) {
     if (!p.bias) return;
