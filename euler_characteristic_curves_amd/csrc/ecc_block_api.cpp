@@ -73,8 +73,7 @@ int check_recurrence_shape(int64_t batch, int64_t steps, int64_t channels, int d
     return fail(ECC_E_SHAPE, "more than 2^40 elements");
   if (channels > ECC_MAX_RECURRENCE_CHANNELS)
     return fail(ECC_E_SHAPE, "channels=%lld exceeds %lld", channels, ECC_MAX_RECURRENCE_CHANNELS);
-  const ecc::RecShape s = ecc::rec_shape(batch, steps, channels, dtype != ECC_T_F32);
-  if (s.blocks * s.segments > INT32_MAX / batch) return fail(ECC_E_SHAPE, "batch=%lld is too large for one launch", batch);
+  if (batch > INT32_MAX) return fail(ECC_E_SHAPE, "batch=%lld exceeds 2^31 - 1", batch);
   return ECC_OK;
 }
 

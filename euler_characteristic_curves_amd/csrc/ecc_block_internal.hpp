@@ -149,6 +149,9 @@ inline RecShape rec_shape(int64_t batch, int64_t steps, int64_t channels, bool h
   s.segments = (s.tiles + s.per - 1) / s.per;
   return s;
 }
+// Sequences of one launch: HIP counts its threads in 32 bits.  (Parts are for
+// fewer than 256 workgroups.)
+inline int64_t rec_run(const RecShape& s) { return s.segments > 1 ? INT64_MAX : UINT32_MAX / 256 / s.blocks; }
 // Workspace: 3 float32 per channel for every part, and its first state.
 inline size_t rec_workspace_bytes(int64_t batch, int64_t steps, int64_t channels, bool half) {
   const RecShape s = rec_shape(batch, steps, channels, half);

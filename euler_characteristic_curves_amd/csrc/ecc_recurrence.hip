@@ -460,35 +460,71 @@ hipError_t with_shape(const RecShape& s, F f) {
   return steps(integral_constant<int, 2>{});
 }
 
+// launch(args) for as many sequences at a time as a launch may have threads for,
+// which are counted in 32 bits.  A batch of that size has no parts.
+template <class T, class F>
+hipError_t in_runs(const RecArgs& a, const RecShape& s, F launch) {
+  const int64_t most = rec_run(s);
+  const auto move = [](auto& p, int64_t n) { p = p ? p + n : p; };
+  const auto move_features = [](auto& p, int64_t n) {
+    using V = std::remove_reference_t<decltype(p)>;
+    p = p ? (V)((uintptr_t)p + (uintptr_t)n * sizeof(T)) : p;
+  };
+  for (int64_t b = 0; b < a.batch; b += most) {
+    RecArgs r = a;
+    r.batch = a.batch - b < most ? a.batch - b : most;
+    const int64_t features = b * a.steps * a.channels;
+    move_features(r.x, features);
+    move_features(r.gate, features);
+    move_features(r.h, features);
+    move_features(r.gh, features);
+    move_features(r.gx, features);
+    move_features(r.ggate, features);
+    move(r.state, b * a.channels);
+    move(r.lengths, b);
+    move(r.last, b * a.channels);
+    move(r.saved, b * s.tiles * a.channels);
+    move(r.glast, b * a.channels);
+    move(r.gstate, b * a.channels);
+    const hipError_t st = launch(r);
+    if (st != hipSuccess) return st;
+  }
+  return hipSuccess;
+}
+
 }  // namespace
 
 template <class T>
-hipError_t launch_recurrence_fwd(const RecArgs& a, hipStream_t stream) {
-  const RecShape s = rec_shape(a.batch, a.steps, a.channels, sizeof(T) == 2);
+hipError_t launch_recurrence_fwd(const RecArgs& all, hipStream_t stream) {
+  const RecShape s = rec_shape(all.batch, all.steps, all.channels, sizeof(T) == 2);
   return with_shape<T>(s, [&](auto v, auto r) {
-    const dim3 grid((unsigned)(a.batch * s.segments * s.blocks)), block(kThreads);
-    if (s.segments > 1) {
-      hipLaunchKernelGGL((recurrence_parts_kernel<T, v.value, r.value, false>), grid, block, 0, stream, a, s);
-      hipLaunchKernelGGL(recurrence_starts_kernel<false>, dim3((unsigned)(a.batch * ((a.channels + 15) / 16))), dim3(kJoin), 0,
-                         stream, a, s);
-    }
-    hipLaunchKernelGGL((recurrence_fwd_kernel<T, v.value, r.value>), grid, block, 0, stream, a, s);
-    return hipGetLastError();
+    return in_runs<T>(all, s, [&](const RecArgs& a) {
+      const dim3 grid((unsigned)(a.batch * s.segments * s.blocks)), block(kThreads);
+      if (s.segments > 1) {
+        hipLaunchKernelGGL((recurrence_parts_kernel<T, v.value, r.value, false>), grid, block, 0, stream, a, s);
+        hipLaunchKernelGGL(recurrence_starts_kernel<false>, dim3((unsigned)(a.batch * ((a.channels + 15) / 16))), dim3(kJoin), 0,
+                           stream, a, s);
+      }
+      hipLaunchKernelGGL((recurrence_fwd_kernel<T, v.value, r.value>), grid, block, 0, stream, a, s);
+      return hipGetLastError();
+    });
   });
 }
 
 template <class T>
-hipError_t launch_recurrence_bwd(const RecArgs& a, hipStream_t stream) {
-  const RecShape s = rec_shape(a.batch, a.steps, a.channels, sizeof(T) == 2);
+hipError_t launch_recurrence_bwd(const RecArgs& all, hipStream_t stream) {
+  const RecShape s = rec_shape(all.batch, all.steps, all.channels, sizeof(T) == 2);
   return with_shape<T>(s, [&](auto v, auto r) {
-    const dim3 grid((unsigned)(a.batch * s.segments * s.blocks)), block(kThreads);
-    if (s.segments > 1) {
-      hipLaunchKernelGGL((recurrence_parts_kernel<T, v.value, r.value, true>), grid, block, 0, stream, a, s);
-      hipLaunchKernelGGL(recurrence_starts_kernel<true>, dim3((unsigned)(a.batch * ((a.channels + 15) / 16))), dim3(kJoin), 0,
-                         stream, a, s);
-    }
-    hipLaunchKernelGGL((recurrence_bwd_kernel<T, v.value, r.value>), grid, block, 0, stream, a, s);
-    return hipGetLastError();
+    return in_runs<T>(all, s, [&](const RecArgs& a) {
+      const dim3 grid((unsigned)(a.batch * s.segments * s.blocks)), block(kThreads);
+      if (s.segments > 1) {
+        hipLaunchKernelGGL((recurrence_parts_kernel<T, v.value, r.value, true>), grid, block, 0, stream, a, s);
+        hipLaunchKernelGGL(recurrence_starts_kernel<true>, dim3((unsigned)(a.batch * ((a.channels + 15) / 16))), dim3(kJoin), 0,
+                           stream, a, s);
+      }
+      hipLaunchKernelGGL((recurrence_bwd_kernel<T, v.value, r.value>), grid, block, 0, stream, a, s);
+      return hipGetLastError();
+    });
   });
 }
 

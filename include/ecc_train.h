@@ -203,7 +203,7 @@ size_t ecc_residual_norm_workspace_bytes(int64_t batch, int64_t inner, int64_t c
  * curve, say): with k_t = 1 / (1 + exp(-gate_t)),
  *   h_t = k_t h_(t-1) + (1 - k_t) x_t,  h_(-1) = state, for every channel.
  *   x, gate  device, dtype elements, [batch][steps][channels];
- *            channels <= ECC_MAX_RECURRENCE_CHANNELS
+ *            channels <= ECC_MAX_RECURRENCE_CHANNELS, batch < 2^31
  *   state    device float32 [batch][channels]; NULL stands for 0
  *   lengths  device int64 [batch], or NULL: sequence b has the steps before
  *            lengths[b] (taken as 0 below it and as `steps` beyond them); x and
@@ -216,7 +216,8 @@ size_t ecc_residual_norm_workspace_bytes(int64_t batch, int64_t inner, int64_t c
  * No output overlaps an input.  States are float32.  A step is formed from
  * x_t - h_(t-1): where that is beyond float32, an infinite x or state among
  * others, h is not finite from there on.  One launch, three where batch x
- * channels is small beside the card and the sequence is cut into parts.
+ * channels is small beside the card and the sequence is cut into parts, and one
+ * for every 2^24 - 1 sequences where there are more.
  */
 int ecc_gated_recurrence_fwd(const void* x, const void* gate, int dtype, int64_t batch, int64_t steps, int64_t channels,
                              const float* state, const int64_t* lengths, void* h, float* last, float* saved, void* ws,
