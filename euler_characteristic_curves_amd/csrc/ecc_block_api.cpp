@@ -95,7 +95,7 @@ int check_recurrence(ecc::RecArgs& a, const void* x, const void* gate, int dtype
   return check_workspace(ws, ws_bytes, ecc::rec_workspace_bytes(batch, steps, channels, dtype != ECC_T_F32));
 }
 
-int check_glu_shape(int64_t rows, int64_t channels, int64_t hidden, int dtype) {
+int check_glu_shape(int64_t rows, int64_t channels, int64_t hidden, int dtype, bool backward, bool aligned) {
   if (!is_dtype(dtype)) return fail(ECC_E_DTYPE, "dtype %lld is not one of ECC_T_*", dtype);
   if (rows < 1 || channels < 1 || hidden < 1)
     return fail(ECC_E_SHAPE, "rows, channels and hidden must be >= 1 (got channels=%lld hidden=%lld)", channels, hidden);
@@ -103,19 +103,20 @@ int check_glu_shape(int64_t rows, int64_t channels, int64_t hidden, int dtype) {
     return fail(ECC_E_SHAPE, "weights of %lld x %lld exceed the limit per side", hidden, channels);
   const int64_t wide = channels > hidden ? channels : hidden;
   if (rows > ECC_MAX_VOXELS / wide) return fail(ECC_E_SHAPE, "more than 2^40 elements");
-  // tiles of 64 rows in one launch
-  if ((rows + 63) / 64 > INT32_MAX / ((wide + 63) / 64)) return fail(ECC_E_SHAPE, "rows=%lld are too many for one launch", rows);
+  const ecc::GluPlan plan = ecc::glu_plan(rows, channels, hidden, dtype == ECC_T_F32 ? 4 : 2, backward);
+  if (!ecc::glu_launches(plan, backward, aligned)) return fail(ECC_E_SHAPE, "rows=%lld are too many for one launch", rows);
   return ECC_OK;
 }
 
 int check_glu(ecc::GluArgs& a, const void* x, int dtype, int64_t rows, int64_t channels, int64_t hidden, const void* w_gate,
-              const void* w_up, const void* b_gate, const void* b_up, int act) {
+              const void* w_up, const void* b_gate, const void* b_up, int act, bool backward) {
   ecc::set_error("");
   if (!x) return fail(ECC_E_NULL, "x is NULL");
   if (!w_gate) return fail(ECC_E_NULL, "w_gate is NULL");
   if (!w_up) return fail(ECC_E_NULL, "w_up is NULL");
   if (act < ECC_ACT_NONE || act > ECC_ACT_GELU) return fail(ECC_E_ACT, "act %lld is not one of ECC_ACT_*", act);
-  const int st = check_glu_shape(rows, channels, hidden, dtype);
+  const auto at16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  const int st = check_glu_shape(rows, channels, hidden, dtype, backward, at16(x) && at16(w_gate) && at16(w_up));
   if (st != ECC_OK) return st;
   a = ecc::GluArgs{};
   a.x = x;
@@ -237,7 +238,7 @@ int ecc_gated_recurrence_bwd(const void* x, const void* gate, int dtype, int64_t
 }
 
 size_t ecc_gated_linear_workspace_bytes(int64_t rows, int64_t channels, int64_t hidden, int dtype, int backward) {
-  if (check_glu_shape(rows, channels, hidden, dtype) != ECC_OK) return 0;
+  if (check_glu_shape(rows, channels, hidden, dtype, backward != 0, true) != ECC_OK) return 0;
   return ecc::glu_plan(rows, channels, hidden, dtype == ECC_T_F32 ? 4 : 2, backward != 0).bytes;
 }
 
@@ -245,7 +246,7 @@ int ecc_gated_linear_fwd(const void* x, int dtype, int64_t rows, int64_t channel
                          const void* w_up, const void* b_gate, const void* b_up, int act, void* h, void* ws, size_t ws_bytes,
                          void* stream) {
   ecc::GluArgs a;
-  int st = check_glu(a, x, dtype, rows, channels, hidden, w_gate, w_up, b_gate, b_up, act);
+  int st = check_glu(a, x, dtype, rows, channels, hidden, w_gate, w_up, b_gate, b_up, act, false);
   if (st != ECC_OK) return st;
   if (!h) return fail(ECC_E_NULL, "h is NULL");
   const ecc::GluPlan plan = ecc::glu_plan(rows, channels, hidden, dtype == ECC_T_F32 ? 4 : 2, false);
@@ -264,7 +265,7 @@ int ecc_gated_linear_bwd(const void* x, int dtype, int64_t rows, int64_t channel
                          void* grad_w_gate, void* grad_w_up, void* grad_b_gate, void* grad_b_up, void* ws, size_t ws_bytes,
                          void* stream) {
   ecc::GluArgs a;
-  int st = check_glu(a, x, dtype, rows, channels, hidden, w_gate, w_up, b_gate, b_up, act);
+  int st = check_glu(a, x, dtype, rows, channels, hidden, w_gate, w_up, b_gate, b_up, act, true);
   if (st != ECC_OK) return st;
   if (!grad_h) return fail(ECC_E_NULL, "grad_h is NULL");
   if (!grad_x && !grad_w_gate && !grad_w_up && !grad_b_gate && !grad_b_up)

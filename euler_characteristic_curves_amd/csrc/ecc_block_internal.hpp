@@ -276,6 +276,19 @@ inline GluPlan glu_plan(int64_t rows, int64_t channels, int64_t hidden, int elem
   return p;
 }
 
+// Whether every launch of a pass has fewer than 2^32 threads, as HIP counts them
+// in 32 bits: tiles and their shares in workgroups of 256, joins in 1024.
+// `aligned`: x and the weights are (their rows are where they are packed).
+inline bool glu_launches(const GluPlan& p, bool backward, bool aligned) {
+  const auto fits = [](int64_t blocks, int64_t threads) { return blocks <= (int64_t)(UINT32_MAX / threads); };
+  const auto product = [&](const GluShare& s, int both) {
+    const int64_t tiles = s.tiles_m * s.tiles_n * both;
+    return fits(tiles, s.splits > 1 ? 1024 : 256) && fits(tiles * s.splits, 256);
+  };
+  if (p.walkers && (aligned || p.packed) ? !fits(p.walkers * p.gates.tiles_n, 256) : !product(p.gates, 1)) return false;
+  return !backward || (product(p.input, 1) && product(p.weight, 2));
+}
+
 template <class T>
 hipError_t launch_glu_fwd(const GluArgs& a, hipStream_t stream);
 template <class T>

@@ -21,3 +21,20 @@ def test_batches_of_the_recurrence(L):
         assert f(1 << 31, 1, 1, 2) == 0
     call = L.lib.ecc_gated_recurrence_fwd
     assert call(FAKE, FAKE, 2, 1 << 31, 1, 1, None, None, FAKE, FAKE, None, FAKE, 1 << 40, None) == L.ECC_E_SHAPE
+
+
+def test_rows_of_the_projections(L):
+    """Rows that one launch has threads for, 2^24 - 1 workgroups of 256, are taken, others refused: the forward pass of
+    narrow sums, 64 turns of 64 rows a workgroup, the gradients, tiles of 256 rows."""
+    f = L.lib.ecc_gated_linear_workspace_bytes
+    for rows, C, F, d, backward, ok in ((1 << 34, 8, 8, 2, 0, True), ((1 << 36) - (1 << 16), 8, 8, 2, 0, True),
+                                        (1 << 36, 8, 8, 2, 0, False), ((1 << 32) - 512, 8, 8, 2, 1, True),
+                                        ((1 << 32) + 1, 8, 8, 2, 1, False), (1 << 23, 1024, 16384, 2, 0, True),
+                                        (1 << 25, 256, 32768, 2, 0, False), (1 << 23, 1024, 2816, 2, 1, True)):
+        assert (f(rows, C, F, d, backward) > 0) == ok, (rows, C, F, d, backward)
+    args = (FAKE, 2, 1 << 36, 8, 8, FAKE, FAKE, None, None, 2)
+    assert L.lib.ecc_gated_linear_fwd(*args, FAKE, FAKE, 1 << 62, None) == L.ECC_E_SHAPE
+    # beside an operand that is not aligned, tiles of 256 rows
+    odd = ctypes.c_void_p(0x1002)
+    assert L.lib.ecc_gated_linear_fwd(FAKE, 2, 1 << 34, 8, 8, odd, FAKE, None, None, 2, FAKE, FAKE, 1 << 62, None) == L.ECC_E_SHAPE
+    assert L.lib.ecc_gated_linear_bwd(*args, FAKE, *([FAKE] * 3), None, None, FAKE, 1 << 62, None) == L.ECC_E_SHAPE
