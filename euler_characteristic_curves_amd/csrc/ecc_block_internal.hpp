@@ -183,26 +183,27 @@ struct GluShare {
   int64_t tiles_m, tiles_n;
   int splits;
 };
-// Rows that one float32 sum runs over, at most.
+// Rows that one float32 sum of dW runs over, at most.  (dx's sums, like the
+// projections', end with a matrix's side.)
 constexpr int64_t kGluRun = 16384;
 // m x n results of sums over k; `both` counts the matrices of the launch.  Large
-// tiles where there are enough of them (or of their shares) for the card.
-inline GluShare glu_share(int64_t m, int64_t n, int64_t k, int both, int step, bool can_split) {
+// tiles where there are enough of them (or of their shares) for the card.  least:
+// shares of a sum, 0 where it cannot be shared.
+inline GluShare glu_share(int64_t m, int64_t n, int64_t k, int both, int step, int64_t least) {
   GluShare s{};
   const auto tiles = [&](int fm, int fn) { return ((m + 64 * fm - 1) / (64 * fm)) * ((n + 64 * fn - 1) / (64 * fn)) * both; };
   const int64_t steps = (k + step - 1) / step;
-  const int64_t shares = can_split ? (steps / 16 > 1 ? steps / 16 : 1) : 1;
+  const int64_t shares = least ? (steps / 16 > 1 ? steps / 16 : 1) : 1;
   const bool large = tiles(4, 2) * (shares < 64 ? shares : 64) >= 192 && m > 128;
   s.FM = large ? 4 : 1;
   s.FN = 2;
   s.tiles_m = (m + 64 * s.FM - 1) / (64 * s.FM);
   s.tiles_n = (n + 64 * s.FN - 1) / (64 * s.FN);
   int64_t splits = 1;
-  if (can_split) {
+  if (least) {
     const int64_t all = s.tiles_m * s.tiles_n * both, most = steps / 8 > 1 ? steps / 8 : 1;
     splits = all < 512 ? 512 / all : 1;
     splits = splits < most ? splits : most;
-    const int64_t least = (k + kGluRun - 1) / kGluRun;
     splits = splits > least ? splits : least;
   }
   s.splits = (int)splits;
@@ -233,10 +234,10 @@ inline GluPlan glu_plan(int64_t rows, int64_t channels, int64_t hidden, int elem
   const int step = 64 / elem;  // elements of a step along the summed axis
   p.pitch = (hidden + 63) / 64 * 64;
   p.pairs = elem == 2;
-  p.gates = glu_share(rows, 2 * hidden, channels, 1, step, false);
+  p.gates = glu_share(rows, 2 * hidden, channels, 1, step, 0);
   p.gates.tiles_n = (hidden + 63) / 64;  // 64 of both projections a tile
-  p.input = glu_share(rows, channels, (p.pairs ? 4 : 2) * hidden, 1, step, true);
-  p.weight = glu_share(hidden, channels, (p.pairs ? 2 : 1) * rows, 2, step, true);
+  p.input = glu_share(rows, channels, (p.pairs ? 4 : 2) * hidden, 1, step, 1);
+  p.weight = glu_share(hidden, channels, (p.pairs ? 2 : 1) * rows, 2, step, (rows + kGluRun - 1) / kGluRun);
   size_t at = 0;
   const auto take = [&at](size_t bytes) {
     at = (at + 255) & ~(size_t)255;

@@ -38,3 +38,14 @@ def test_rows_of_the_projections(L):
     odd = ctypes.c_void_p(0x1002)
     assert L.lib.ecc_gated_linear_fwd(FAKE, 2, 1 << 34, 8, 8, odd, FAKE, None, None, 2, FAKE, FAKE, 1 << 62, None) == L.ECC_E_SHAPE
     assert L.lib.ecc_gated_linear_bwd(*args, FAKE, *([FAKE] * 3), None, None, FAKE, 1 << 62, None) == L.ECC_E_SHAPE
+
+
+def test_workspace_of_wide_gradients(L):
+    """dx's sums are not shared out where there are tiles enough, however many units they run over: the workspace holds
+    the projections' gradients (8 bytes a unit and row in 16 bits, 8 in float32) and little beside."""
+    f = L.lib.ecc_gated_linear_workspace_bytes
+    for d in (0, 2):
+        for hidden in (8192, 8193, 12000, 28672):
+            rows, C = 131072, 4096
+            room = rows * 8 * (hidden + 63)
+            assert f(rows, C, hidden, d, 1) <= room + 2 * hidden * C * 4 * 9 + (1 << 24), (d, hidden)
