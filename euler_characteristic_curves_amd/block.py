@@ -5,6 +5,7 @@ channels]``.  Every function takes tensors that live on a ROCm device and calls 
 stream; argument checks and autograd nodes are in csrc/ecc_torch_block.cpp, all arithmetic is in the HIP kernels.
 Scratch comes from torch's allocator per call, so calls may run on any stream and be captured into a graph.  Strided
 tensors are copied once.  Forward-mode derivatives are refused, and gradients of gradients raise an error.
+A backward pass is not captured while a graph made on the default stream holds a leaf whose gradient it forms.
 """
 
 from . import _torch

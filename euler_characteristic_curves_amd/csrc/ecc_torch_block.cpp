@@ -43,20 +43,25 @@ void vector(const Optional& t, const char* name, int64_t n) {
   TORCH_CHECK_VALUE(!t || (t->dim() == 1 && t->size(0) == n), name, " must be [", n, "] (got ", t->sizes(), ")");
 }
 
-// A leaf's gradient accumulator belongs to the stream it was made on, and lives
-// as long as any graph that reaches the leaf.  A captured backward pass would
-// make that stream wait for the capturing one, which ends the process.
-void refuse_foreign_capture(const at::Tensor& t) {
-  if (!t.defined() || !t.requires_grad() || !t.is_leaf()) return;
-  const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
-  if (!node) return;
-  const auto made = node->stream();
-  const c10::Stream here = c10::hip::getCurrentHIPStreamMasqueradingAsCUDA(t.get_device()).unwrap();
-  TORCH_CHECK(!made || *made == here,
-              "a backward pass is captured while an eager graph of the same leaves is alive: free that graph first");
-}
 bool capturing() {
   return c10::hip::currentStreamCaptureStatusMayInitCtx() != c10::hip::CaptureStatus::None;
+}
+// A leaf's gradient accumulator belongs to the stream it was made on, and lives
+// as long as any graph that reaches the leaf.  A captured backward pass makes
+// that stream wait for the capturing one: another stream joins the capture by
+// it, the default one cannot, which ends the process.  `in`: a node's first
+// inputs; what no gradient is wanted of has no say.  Absent inputs have no edge.
+void refuse_foreign_capture(AutogradContext* ctx, const variable_list& in, size_t count) {
+  if (!capturing()) return;
+  for (size_t i = 0, edge = 0; i < count; ++i) {
+    const at::Tensor& t = in[i];
+    if (!t.defined() || !ctx->needs_input_grad(edge++) || !t.requires_grad() || !t.is_leaf()) continue;
+    const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
+    if (!node) continue;
+    const auto made = node->stream();
+    TORCH_CHECK(!made || *made != c10::hip::getDefaultHIPStreamMasqueradingAsCUDA(t.get_device()).unwrap(),
+                "a backward pass is captured while an eager graph of the same leaves is alive: free that graph first");
+  }
 }
 
 at::Tensor bytes_like(const at::Tensor& x, int64_t bytes) {
@@ -122,8 +127,7 @@ struct Residual : torch::autograd::Function<Residual> {
     at::AutoGradMode off(false);
     const variable_list saved = ctx->get_saved_variables();
     variable_list in(5), out(6);
-    if (capturing())
-      for (const at::Tensor& t : saved) refuse_foreign_capture(t);
+    refuse_foreign_capture(ctx, saved, 5);
     for (int i = 0; i < 5; ++i) in[i] = dense(saved[i]);
     variable_list wanted(5);
     const at::Tensor& x = in[0];
@@ -229,8 +233,7 @@ struct Glu : torch::autograd::Function<Glu> {
     const bool again = at::GradMode::is_enabled();
     at::AutoGradMode off(false);
     const variable_list saved = ctx->get_saved_variables();
-    if (capturing())
-      for (const at::Tensor& t : saved) refuse_foreign_capture(t);
+    refuse_foreign_capture(ctx, saved, 5);
     variable_list in(5), wanted(5), out(6);
     for (int i = 0; i < 5; ++i) in[i] = dense(saved[i]);
     const at::Tensor &x = in[0], g = dense(grads[0]);
@@ -331,8 +334,7 @@ struct Recurrence : torch::autograd::Function<Recurrence> {
     const bool again = at::GradMode::is_enabled();
     at::AutoGradMode off(false);
     const variable_list saved = ctx->get_saved_variables();
-    if (capturing())
-      for (const at::Tensor& t : saved) refuse_foreign_capture(t);
+    refuse_foreign_capture(ctx, saved, 3);
     variable_list in(3), wanted(3), out(5);
     for (int i = 0; i < 3; ++i) in[i] = dense(saved[i]);
     const at::Tensor &x = in[0], n = dense(saved[3]), gh = dense(grads[0]), gl = dense(grads[1]);
