@@ -4,8 +4,8 @@ Features are channels last, ``[batch, *space, channels]`` or, for curves and oth
 channels]``.  Every function takes tensors that live on a ROCm device and calls the C entry points on the current torch
 stream; argument checks and autograd nodes are in csrc/ecc_torch_block.cpp, all arithmetic is in the HIP kernels.
 Scratch comes from torch's allocator per call, so calls may run on any stream and be captured into a graph.  Strided
-tensors are copied once.  Forward-mode derivatives are refused, and gradients of gradients raise an error.
-A backward pass is not captured while a graph made on the default stream holds a leaf whose gradient it forms.
+tensors are copied once.  Forward-mode derivatives and torch.jit.trace are refused, and gradients of gradients raise an
+error.  A backward pass is not captured while a graph made on the default stream holds a leaf whose gradient it forms.
 """
 
 from . import _torch

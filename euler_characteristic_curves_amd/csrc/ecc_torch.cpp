@@ -97,6 +97,7 @@ struct Norm : torch::autograd::Function<Norm> {
 at::Tensor norm(const at::Tensor& x, const Optional& w, const Optional& b, const Optional& r, const Optional& o,
                 const std::vector<int64_t>& sizes, int64_t dtype, int64_t pdtype, int64_t act, int64_t bytes, double eps,
                 bool read) {
+  refuse_tracing("group norm");
   const pybind11::gil_scoped_release nogil;
   TORCH_CHECK_NOT_IMPLEMENTED(!is_dual(x) && !is_dual(w) && !is_dual(b) && !is_dual(r) && !is_dual(o),
                               "group norm has no forward-mode derivative");

@@ -7,6 +7,7 @@
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/jit/frontend/tracer.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <optional>
@@ -47,6 +48,12 @@ inline void check(int status, const char* what) {
 
 // A dual tensor need not require a gradient, and autograd modes do not turn it off.
 inline bool is_dual(const Optional& t) { return t && t->_fw_grad(/*level=*/0).defined(); }
+
+// A traced call would leave its results' allocation in the graph, and nothing
+// that writes them.
+inline void refuse_tracing(const char* what) {
+  TORCH_CHECK_NOT_IMPLEMENTED(!torch::jit::tracer::isTracing(), what, " cannot be traced");
+}
 
 // A gradient of these gradients is an error, not zero.
 inline variable_list once_only(const variable_list& out, const char* what) {

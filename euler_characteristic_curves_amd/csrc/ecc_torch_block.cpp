@@ -153,6 +153,7 @@ struct Residual : torch::autograd::Function<Residual> {
 
 variable_list residual_norm(const at::Tensor& x, const Optional& b, const Optional& g, const Optional& w, const Optional& bw,
                             double scale, double eps, bool norm_branch, const std::optional<at::ScalarType>& ztype) {
+  refuse_tracing("residual norm");
   const pybind11::gil_scoped_release nogil;
   features(x, "x");
   TORCH_CHECK_VALUE(x.dim() >= 2, "x must be [batch, *space, channels] (got ", x.sizes(), ")");
@@ -255,6 +256,7 @@ struct Glu : torch::autograd::Function<Glu> {
 
 at::Tensor gated_linear(const at::Tensor& x, const at::Tensor& wg, const at::Tensor& wu, const Optional& bg,
                         const Optional& bu, int64_t act) {
+  refuse_tracing("gated linear");
   const pybind11::gil_scoped_release nogil;
   features(x, "x");
   TORCH_CHECK_VALUE(x.dim() >= 1, "x must be [*space, channels]");
@@ -360,6 +362,7 @@ struct Recurrence : torch::autograd::Function<Recurrence> {
 
 std::tuple<at::Tensor, at::Tensor> gated_recurrence(const at::Tensor& x, const at::Tensor& f, const Optional& s,
                                                     const Optional& n) {
+  refuse_tracing("gated recurrence");
   const pybind11::gil_scoped_release nogil;
   features(x, "x");
   TORCH_CHECK_VALUE(x.dim() == 3, "x must be [batch, steps, channels] (got ", x.sizes(), ")");

@@ -5,7 +5,7 @@ tensors that live on a ROCm device, checks them, and calls the C entry points
 on the current torch stream (the norms through their autograd nodes in
 csrc/ecc_torch.cpp).  All arithmetic happens in the HIP kernels.
 Scratch comes from torch's allocator per call, so calls may run on any stream
-and be captured into a graph.
+and be captured into a graph.  torch.jit.trace is refused by the norms.
 """
 
 import torch
