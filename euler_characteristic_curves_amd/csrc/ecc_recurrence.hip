@@ -73,7 +73,10 @@ __device__ __forceinline__ void lengthen(Run& r, float m, float k) {
   r.c = fmaf(fabsf(m), 1.0f - r.c, r.c);
 }
 __device__ __forceinline__ void settle(Run& r) { r.c = r.A < 0.5f ? 1.0f - r.A : r.c; }
-__device__ __forceinline__ float keep(const Run& r, float h) { return r.c < 0.5f ? fmaf(-r.c, h, h) : r.A * h; }
+// (Where nothing is taken, an infinity too stays what it is.)
+__device__ __forceinline__ float keep(const Run& r, float h) {
+  return r.c < 0.5f ? fmaf(-r.c, r.c == 0.0f ? 0.0f : h, h) : r.A * h;
+}
 __device__ __forceinline__ float apply(const Run& r, float h) { return r.B + keep(r, h); }
 __device__ __forceinline__ Run then(const Run& first, const Run& r) {
   return Run{first.A * r.A, r.c + keep(r, first.c), apply(r, first.B)};
@@ -252,9 +255,11 @@ __global__ __launch_bounds__(kThreads) void recurrence_parts_kernel(RecArgs a, R
       for (int j = 0; j < R; ++j) {
         const int q = BACK ? R - 1 - j : j;
         float k, m = small_gate((float)f[q].v[v], k);
-        if (!in.whole && q >= in.left) m = 0.0f, k = 1.0f;
+        const bool none = !in.whole && q >= in.left;
+        if (none) m = 0.0f, k = 1.0f;
         lengthen(r, m, k);
-        r.B = BACK ? kept(r.B + (float)x[q].v[v], m) : step(r.B, (float)x[q].v[v], m);
+        const float B = BACK ? kept(r.B + (float)x[q].v[v], m) : step(r.B, (float)x[q].v[v], m);
+        r.B = none ? r.B : B;
       }
       settle(r);
       sh.put(at.g, v, r);
@@ -310,9 +315,11 @@ __global__ __launch_bounds__(kThreads) void recurrence_fwd_kernel(RecArgs a, Rec
       for (int i = 0; i < R; ++i) {
         float k;
         m[i][v] = small_gate((float)now.f[i].v[v], k);
-        if (!in.whole && i >= in.left) m[i][v] = 0.0f, k = 1.0f;
+        const bool none = !in.whole && i >= in.left;
+        if (none) m[i][v] = 0.0f, k = 1.0f;
         lengthen(r, m[i][v], k);
-        r.B = step(r.B, (float)now.x[i].v[v], m[i][v]);
+        const float B = step(r.B, (float)now.x[i].v[v], m[i][v]);
+        r.B = none ? r.B : B;
       }
       settle(r);
       sh.put(at.g, v, r);
@@ -426,7 +433,7 @@ __global__ __launch_bounds__(kThreads, 2) void recurrence_bwd_kernel(RecArgs a, 
       for (int v = 0; v < V; ++v) {
         const float D = (float)now.d[i].v[v] + e[v], small = fabsf(m[i][v]);
         const bool is = in.whole || i < in.left;
-        e[v] = kept(D, m[i][v]);
+        e[v] = is ? kept(D, m[i][v]) : D;
         ox[i].v[v] = (T)(is ? taken(D, m[i][v]) : 0.0f);
         of[i].v[v] = (T)(is ? diff[i][v] * D * fmaf(-small, small, small) : 0.0f);
       }

@@ -207,7 +207,8 @@ size_t ecc_residual_norm_workspace_bytes(int64_t batch, int64_t inner, int64_t c
  *   state    device float32 [batch][channels]; NULL stands for 0
  *   lengths  device int64 [batch], or NULL: sequence b has the steps before
  *            lengths[b] (taken as 0 below it and as `steps` beyond them); x and
- *            gate behind them are not read, h there is 0
+ *            gate behind them are not read, h there is 0, and the state, infinite
+ *            or not, stays as it is
  *   h        dtype, x's shape
  *   last     float32 [batch][channels]: the state after the last step (the
  *            initial one where there is none), to be carried to a next call
