@@ -61,6 +61,21 @@ __device__ __forceinline__ float step(float h, float x, float m) { return fmaf(m
 __device__ __forceinline__ float kept(float d, float m) { return fmaf(-m, d, keeps(m) ? d : 0.0f); }
 __device__ __forceinline__ float taken(float d, float m) { return fmaf(m, d, keeps(m) ? 0.0f : d); }
 
+// What follows finds anew what it needs of v.  (Kept from one pass over the steps
+// to the next, whether each keeps more than half, whether it is there and where it
+// lies take more registers than there are, 196 scalar ones in the backward pass.)
+template <class N>
+__device__ __forceinline__ void anew(N& v) {
+  asm("" : "+v"(v));
+}
+template <int R, int V>
+__device__ __forceinline__ void anew(float (&m)[R][V]) {
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int v = 0; v < V; ++v) anew(m[i][v]);
+}
+
 // What a run of steps does to a state: h -> A h + B, c = 1 - A.
 struct Run {
   float A, c, B;
@@ -113,27 +128,33 @@ __device__ __forceinline__ int64_t length_of(const RecArgs& a, int64_t b) {
 
 // R steps of a tile.  `whole`: all of the workgroup's lie before the end; what
 // lies at or behind it is not read otherwise.  p: the tile's first step, the same
-// for all lanes, so that a load has a scalar base and one offset.
+// for all lanes, so that a stream has one scalar base; offset and pitch are in
+// bytes and fit 32 bits.
 template <class T, int V, int R>
-__device__ __forceinline__ void load_steps(const T* p, uint32_t offset, int64_t left, bool whole, int64_t C, Vec<T, V> (&r)[R]) {
+__device__ __forceinline__ void load_steps(const T* p, uint32_t offset, int left, bool whole, uint32_t pitch,
+                                           Vec<T, V> (&r)[R]) {
   const char* base = reinterpret_cast<const char*>(p);
+  anew(offset);
   if (whole) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) load_vec(reinterpret_cast<const T*>(base + (int64_t)i * C * (int64_t)sizeof(T) + offset), r[i]);
+    for (int i = 0; i < R; ++i) load_vec(reinterpret_cast<const T*>(base + (offset + i * pitch)), r[i]);
   } else {
+    anew(left);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       r[i] = Vec<T, V>{};
-      if (i < left) load_vec(reinterpret_cast<const T*>(base + (int64_t)i * C * (int64_t)sizeof(T) + offset), r[i]);
+      if (i < left) load_vec(reinterpret_cast<const T*>(base + (offset + i * pitch)), r[i]);
     }
   }
 }
 template <class T, int V, int R>
-__device__ __forceinline__ void store_steps(T* p, uint32_t offset, int64_t left, bool whole, int64_t C, const Vec<T, V> (&r)[R]) {
+__device__ __forceinline__ void store_steps(T* p, uint32_t offset, int left, bool whole, uint32_t pitch,
+                                            const Vec<T, V> (&r)[R]) {
   char* base = reinterpret_cast<char*>(p);
+  anew(offset);
 #pragma unroll
   for (int i = 0; i < R; ++i)
-    if (whole || i < left) store_vec(reinterpret_cast<T*>(base + (int64_t)i * C * (int64_t)sizeof(T) + offset), r[i]);
+    if (whole || i < left) store_vec(reinterpret_cast<T*>(base + (offset + i * pitch)), r[i]);
 }
 
 // Tiles that begin before a sequence's end.
@@ -147,12 +168,13 @@ __device__ __forceinline__ int64_t live_tiles(const RecShape& s, int64_t len, in
 // and before the row's, and whether all of the workgroup's do.
 template <int R>
 struct Tile {
-  int64_t left, rows;
+  int left, rows;
   bool whole, full;
   __device__ __forceinline__ Tile(const RecArgs& a, const RecShape& s, int64_t tile, int g, int64_t len) {
     const int64_t t = (tile * s.G + g) * R, end = (tile + 1) * s.G * R;
-    left = len - t;
-    rows = a.steps - t;
+    const auto of_mine = [&](int64_t n) { return (int)(n < 0 ? 0 : n < R ? n : R); };
+    left = of_mine(len - t);
+    rows = of_mine(a.steps - t);
     whole = end <= len;
     full = end <= a.steps;
   }
@@ -234,7 +256,7 @@ __global__ __launch_bounds__(kThreads) void recurrence_parts_kernel(RecArgs a, R
   const Place at = place<V>(a, s);
   Shared<V> sh{lds, s.L, s.G, (int)(threadIdx.x & (s.L - 1))};
   const int64_t len = length_of(a, at.b), C = a.channels, stride = (int64_t)s.G * R * C, row = at.b * a.steps * C;
-  const uint32_t offset = (uint32_t)(((int64_t)at.g * R * C + at.c) * (int64_t)sizeof(T));
+  const uint32_t pitch = (uint32_t)(C * (int64_t)sizeof(T)), offset = at.g * R * pitch + (uint32_t)(at.c * (int64_t)sizeof(T));
   const T *gate = reinterpret_cast<const T*>(a.gate) + row, *second = reinterpret_cast<const T*>(BACK ? a.gh : a.x) + row;
   const bool there = BACK ? a.gh != nullptr : true;
   Run all[V];
@@ -246,8 +268,8 @@ __global__ __launch_bounds__(kThreads) void recurrence_parts_kernel(RecArgs a, R
     const int64_t tile = BACK ? last - 1 - i : first + i;
     const Tile<R> in(a, s, tile, at.g, len);
     Vec<T, V> f[R], x[R];
-    load_steps<T, V, R>(gate + tile * stride, offset, in.left, in.whole, C, f);
-    load_steps<T, V, R>(second + tile * stride, offset, there ? in.left : 0, in.whole && there, C, x);
+    load_steps<T, V, R>(gate + tile * stride, offset, in.left, in.whole, pitch, f);
+    load_steps<T, V, R>(second + tile * stride, offset, there ? in.left : 0, in.whole && there, pitch, x);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       Run r{1.0f, 0.0f, 0.0f};
@@ -265,9 +287,11 @@ __global__ __launch_bounds__(kThreads) void recurrence_parts_kernel(RecArgs a, R
       sh.put(at.g, v, r);
     }
     __syncthreads();
-    for (int j = 0; j < s.G; ++j)
+    for (int four = 0; four < s.G; four += 4)
 #pragma unroll
-      for (int v = 0; v < V; ++v) all[v] = then(all[v], sh.get(BACK ? s.G - 1 - j : j, v));
+      for (int j = four; j < four + 4; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) all[v] = then(all[v], sh.get(BACK ? s.G - 1 - j : j, v));
     __syncthreads();
   }
   if (at.g == 0 && at.active) {
@@ -287,7 +311,7 @@ __global__ __launch_bounds__(kThreads) void recurrence_fwd_kernel(RecArgs a, Rec
   const Place at = place<V>(a, s);
   Shared<V> sh{lds, s.L, s.G, (int)(threadIdx.x & (s.L - 1))};
   const int64_t len = length_of(a, at.b), C = a.channels, stride = (int64_t)s.G * R * C, row = at.b * a.steps * C;
-  const uint32_t offset = (uint32_t)(((int64_t)at.g * R * C + at.c) * (int64_t)sizeof(T));
+  const uint32_t pitch = (uint32_t)(C * (int64_t)sizeof(T)), offset = at.g * R * pitch + (uint32_t)(at.c * (int64_t)sizeof(T));
   const T *gate = reinterpret_cast<const T*>(a.gate) + row, *xs = reinterpret_cast<const T*>(a.x) + row;
   T* hs = reinterpret_cast<T*>(a.h) + row;
   float state[V];
@@ -296,13 +320,13 @@ __global__ __launch_bounds__(kThreads) void recurrence_fwd_kernel(RecArgs a, Rec
   Raw<T, V, R, false> now;
   const auto load = [&](int64_t tile, Raw<T, V, R, false>& r) {
     const Tile<R> in(a, s, tile, at.g, len);
-    load_steps<T, V, R>(gate + tile * stride, offset, in.left, in.whole, C, r.f);
-    load_steps<T, V, R>(xs + tile * stride, offset, in.left, in.whole, C, r.x);
+    load_steps<T, V, R>(gate + tile * stride, offset, in.left, in.whole, pitch, r.f);
+    load_steps<T, V, R>(xs + tile * stride, offset, in.left, in.whole, pitch, r.x);
   };
   if (first < last) load(first, now);
   first_state(a, s, at, a.state, state);
   for (int64_t tile = first; tile < last; ++tile) {
-    const Tile<R> in(a, s, tile, at.g, len);
+    Tile<R> in(a, s, tile, at.g, len);
     float m[R][V], h[V];
     if (a.saved && at.g == 0 && at.active) {
 #pragma unroll
@@ -327,13 +351,17 @@ __global__ __launch_bounds__(kThreads) void recurrence_fwd_kernel(RecArgs a, Rec
     Raw<T, V, R, false> next;  // on its way while this tile is finished
     if (tile + 1 < last) load(tile + 1, next);
     __syncthreads();
-    for (int g = 0; g < s.G; ++g)
+    for (int four = 0; four < s.G; four += 4)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (g == at.g) h[v] = state[v];
-        state[v] = apply(sh.get(g, v), state[v]);
-      }
+      for (int g = four; g < four + 4; ++g)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (g == at.g) h[v] = state[v];
+          state[v] = apply(sh.get(g, v), state[v]);
+        }
     __syncthreads();
+    anew(m);
+    anew(in.left);
     Vec<T, V> y[R];
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -342,13 +370,13 @@ __global__ __launch_bounds__(kThreads) void recurrence_fwd_kernel(RecArgs a, Rec
         h[v] = step(h[v], (float)now.x[i].v[v], m[i][v]);
         y[i].v[v] = (T)(in.whole || i < in.left ? h[v] : 0.0f);
       }
-    if (at.active) store_steps<T, V, R>(hs + tile * stride, offset, in.rows, in.full, C, y);
+    if (at.active) store_steps<T, V, R>(hs + tile * stride, offset, in.rows, in.full, pitch, y);
     now = next;
   }
   const Vec<T, V> zeros[R] = {};
   for (int64_t tile = last; tile < end && at.active; ++tile) {
     const Tile<R> in(a, s, tile, at.g, len);
-    store_steps<T, V, R>(hs + tile * stride, offset, in.rows, in.full, C, zeros);
+    store_steps<T, V, R>(hs + tile * stride, offset, in.rows, in.full, pitch, zeros);
   }
   if (at.seg == s.segments - 1 && at.g == 0 && at.active) {
 #pragma unroll
@@ -362,7 +390,7 @@ __global__ __launch_bounds__(kThreads, 2) void recurrence_bwd_kernel(RecArgs a, 
   const Place at = place<V>(a, s);
   Shared<V> sh{lds, s.L, s.G, (int)(threadIdx.x & (s.L - 1))};
   const int64_t len = length_of(a, at.b), C = a.channels, stride = (int64_t)s.G * R * C, row = at.b * a.steps * C;
-  const uint32_t offset = (uint32_t)(((int64_t)at.g * R * C + at.c) * (int64_t)sizeof(T));
+  const uint32_t pitch = (uint32_t)(C * (int64_t)sizeof(T)), offset = at.g * R * pitch + (uint32_t)(at.c * (int64_t)sizeof(T));
   const T *gate = reinterpret_cast<const T*>(a.gate) + row, *xs = reinterpret_cast<const T*>(a.x) + row;
   const T* gh = reinterpret_cast<const T*>(a.gh) + row;
   float grad[V];  // of the state after the tile, through later steps
@@ -372,16 +400,16 @@ __global__ __launch_bounds__(kThreads, 2) void recurrence_bwd_kernel(RecArgs a, 
   float start[V];
   const auto load = [&](int64_t tile, Raw<T, V, R, true>& r, float(&h)[V]) {
     const Tile<R> in(a, s, tile, at.g, len);
-    load_steps<T, V, R>(gate + tile * stride, offset, in.left, in.whole, C, r.f);
-    load_steps<T, V, R>(xs + tile * stride, offset, in.left, in.whole, C, r.x);
-    load_steps<T, V, R>(gh + tile * stride, offset, a.gh ? in.left : 0, in.whole && a.gh, C, r.d);
+    load_steps<T, V, R>(gate + tile * stride, offset, in.left, in.whole, pitch, r.f);
+    load_steps<T, V, R>(xs + tile * stride, offset, in.left, in.whole, pitch, r.x);
+    load_steps<T, V, R>(gh + tile * stride, offset, a.gh ? in.left : 0, in.whole && a.gh, pitch, r.d);
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = a.saved[(at.b * s.tiles + tile) * C + at.c + v];
   };
   if (first < last) load(last - 1, now, start);
   first_state(a, s, at, a.glast, grad);
   for (int64_t tile = last - 1; tile >= first; --tile) {
-    const Tile<R> in(a, s, tile, at.g, len);
+    Tile<R> in(a, s, tile, at.g, len);
     float m[R][V], h[V], e[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -396,7 +424,10 @@ __global__ __launch_bounds__(kThreads, 2) void recurrence_bwd_kernel(RecArgs a, 
         r.B = step(r.B, (float)now.x[i].v[v], m[i][v]);
       }
 #pragma unroll
-      for (int i = R - 1; i >= 0; --i) back = kept(back + (float)now.d[i].v[v], m[i][v]);
+      for (int i = R - 1; i >= 0; --i) {
+        anew(m[i][v]);
+        back = kept(back + (float)now.d[i].v[v], m[i][v]);
+      }
       settle(r);
       sh.put(at.g, v, r);
       sh.ref(3, at.g, v) = back;
@@ -405,18 +436,24 @@ __global__ __launch_bounds__(kThreads, 2) void recurrence_bwd_kernel(RecArgs a, 
     Raw<T, V, R, true> next;  // on its way while this tile is finished
     if (tile > first) load(tile - 1, next, start);
     __syncthreads();
+#pragma unroll 1  // (several at a time take more scalar registers than there are)
     for (int g = 0; g < at.g; ++g)
 #pragma unroll
       for (int v = 0; v < V; ++v) h[v] = apply(sh.get(g, v), h[v]);
-    for (int g = s.G - 1; g >= 0; --g)
+#pragma unroll 1
+    for (int two = s.G - 2; two >= 0; two -= 2)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (g == at.g) e[v] = grad[v];
-        Run r = sh.get(g, v);
-        r.B = sh.ref(3, g, v);
-        grad[v] = apply(r, grad[v]);
-      }
+      for (int j = 1; j >= 0; --j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int g = two + j;
+          if (g == at.g) e[v] = grad[v];
+          Run r = sh.get(g, v);
+          r.B = sh.ref(3, g, v);
+          grad[v] = apply(r, grad[v]);
+        }
     __syncthreads();
+    anew(m);
     float diff[R][V];
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -426,6 +463,8 @@ __global__ __launch_bounds__(kThreads, 2) void recurrence_bwd_kernel(RecArgs a, 
         diff[i][v] = h[v] - xv;
         h[v] = step(h[v], xv, m[i][v]);
       }
+    anew(m);
+    anew(in.left);
     Vec<T, V> ox[R], of[R];
 #pragma unroll
     for (int i = R - 1; i >= 0; --i)
@@ -438,16 +477,17 @@ __global__ __launch_bounds__(kThreads, 2) void recurrence_bwd_kernel(RecArgs a, 
         of[i].v[v] = (T)(is ? diff[i][v] * D * fmaf(-small, small, small) : 0.0f);
       }
     if (at.active) {
-      if (a.gx) store_steps<T, V, R>(reinterpret_cast<T*>(a.gx) + row + tile * stride, offset, in.rows, in.full, C, ox);
-      if (a.ggate) store_steps<T, V, R>(reinterpret_cast<T*>(a.ggate) + row + tile * stride, offset, in.rows, in.full, C, of);
+      if (a.gx) store_steps<T, V, R>(reinterpret_cast<T*>(a.gx) + row + tile * stride, offset, in.rows, in.full, pitch, ox);
+      anew(in.rows);
+      if (a.ggate) store_steps<T, V, R>(reinterpret_cast<T*>(a.ggate) + row + tile * stride, offset, in.rows, in.full, pitch, of);
     }
     now = next;
   }
   const Vec<T, V> zeros[R] = {};
   for (int64_t tile = last; tile < end && at.active; ++tile) {
     const Tile<R> in(a, s, tile, at.g, len);
-    if (a.gx) store_steps<T, V, R>(reinterpret_cast<T*>(a.gx) + row + tile * stride, offset, in.rows, in.full, C, zeros);
-    if (a.ggate) store_steps<T, V, R>(reinterpret_cast<T*>(a.ggate) + row + tile * stride, offset, in.rows, in.full, C, zeros);
+    if (a.gx) store_steps<T, V, R>(reinterpret_cast<T*>(a.gx) + row + tile * stride, offset, in.rows, in.full, pitch, zeros);
+    if (a.ggate) store_steps<T, V, R>(reinterpret_cast<T*>(a.ggate) + row + tile * stride, offset, in.rows, in.full, pitch, zeros);
   }
   if (a.gstate && at.seg == 0 && at.g == 0 && at.active) {
 #pragma unroll
