@@ -61,6 +61,15 @@ struct Columns {
   }
 };
 
+// (Asked anew each time: kept, the answers for every element take more scalar
+// registers than there are.)
+template <int V, int K>
+__device__ __forceinline__ int skip_of(const Columns<V, K>& col, int k) {
+  int skip = col.skip[k];
+  asm("" : "+v"(skip));
+  return skip;
+}
+
 // Elements of a row as they lie, and as numbers, or of the parameters; those
 // that another vector has are 0.
 template <int V, int K, class T>
@@ -74,9 +83,11 @@ __device__ __forceinline__ void load_raw(const T* p, const Columns<V, K>& col, b
 template <int V, int K, class T>
 __device__ __forceinline__ void unpack(const Vec<T, V> (&v)[K], const Columns<V, K>& col, float (&r)[K][V]) {
 #pragma unroll
-  for (int k = 0; k < K; ++k)
+  for (int k = 0; k < K; ++k) {
+    const int skip = skip_of(col, k);
 #pragma unroll
-    for (int j = 0; j < V; ++j) r[k][j] = V > 1 && j < col.skip[k] ? 0.0f : (float)v[k].v[j];
+    for (int j = 0; j < V; ++j) r[k][j] = V > 1 && j < skip ? 0.0f : (float)v[k].v[j];
+  }
 }
 template <int V, int K, class T>
 __device__ __forceinline__ void store_row(T* p, const Columns<V, K>& col, const float (&r)[K][V]) {
@@ -85,12 +96,13 @@ __device__ __forceinline__ void store_row(T* p, const Columns<V, K>& col, const 
     Vec<T, V> v;
 #pragma unroll
     for (int j = 0; j < V; ++j) v.v[j] = (T)r[k][j];
-    if (col.skip[k] == 0) {
+    const int skip = skip_of(col, k);
+    if (skip == 0) {
       store_vec(p + col.at[k], v);
-    } else if (col.skip[k] < V) {
+    } else if (skip < V) {
 #pragma unroll
       for (int j = 1; j < V; ++j)
-        if (j >= col.skip[k]) p[col.at[k] + j] = v.v[j];
+        if (j >= skip) p[col.at[k] + j] = v.v[j];
     }
   }
 }
@@ -225,27 +237,34 @@ __global__ __launch_bounds__(512) void residual_bwd_kernel(ResArgs a, ResGeom g,
   Vec<XT, V> nx[K], ny[K];
   Vec<BT, V> nb[K], nz[K];
   float nrb, nry;
+  // Of 16 elements a lane, as rows beyond 4096 have, the next turn's do not fit the
+  // registers beside this one's (64 to 113 of a lane's went to memory and back:
+  // 4096 rows of 8192 float32 373 us, 248 so); 16-bit ones do but for grad_z (200
+  // us so, 213 with none ahead, 188 with 3 of a lane's in memory).
+  constexpr bool kFits = V * K < 16, kAhead = kFits || sizeof(XT) == 2;
   const auto load = [&](int64_t first) {  // the rows of a turn
     const bool active = first + slot < g.rows;
     const int64_t row = sample * g.rows + first + slot, at = row * C;
     load_raw(reinterpret_cast<const XT*>(a.x) + at, col, active, nx);
     load_raw(reinterpret_cast<const BT*>(a.branch) + at, col, active && a.branch, nb);
     load_raw(reinterpret_cast<const XT*>(a.gy) + at, col, active && a.gy, ny);
-    load_raw(reinterpret_cast<const BT*>(a.gz) + at, col, active && a.gz, nz);
+    if (kFits || !kAhead) load_raw(reinterpret_cast<const BT*>(a.gz) + at, col, active && a.gz, nz);
     nrb = active ? a.stats[row * 2] : 0.0f;
     nry = active ? a.stats[row * 2 + 1] : 0.0f;
   };
-  load(block * g.slots);
+  if (kAhead) load(block * g.slots);
   for (int64_t first = block * g.slots; first < g.rows; first += turn) {
     const bool active = first + slot < g.rows;
     const int64_t row = sample * g.rows + first + slot;
     float x[K][V], b[K][V], dy[K][V], dz[K][V];
+    if (!kAhead) load(first);
+    if (!kFits && kAhead) load_raw(reinterpret_cast<const BT*>(a.gz) + row * C, col, active && a.gz, nz);
     unpack(nx, col, x);
     unpack(nb, col, b);
     unpack(ny, col, dy);
     unpack(nz, col, dz);
     const float rb = nrb, ry = nry;
-    load(first + turn);  // on their way while these are finished
+    if (kAhead) load(first + turn);  // on their way while these are finished
     // b: the branch's hat, or the branch itself; x: y's hat; dz: its gradient
     float s = 0.0f;
 #pragma unroll

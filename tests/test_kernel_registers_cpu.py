@@ -25,7 +25,7 @@ def kernels():
     return found
 
 
-@pytest.mark.parametrize("part", ["glu_", "recurrence_"])
+@pytest.mark.parametrize("part", ["glu_", "recurrence_", "residual_"])
 def test_no_kernel_keeps_registers_in_memory(part):
     mine = {n: k for n, k in kernels().items() if part in n}
     assert mine
