@@ -49,3 +49,17 @@ def test_workspace_of_wide_gradients(L):
             rows, C = 131072, 4096
             room = rows * 8 * (hidden + 63)
             assert f(rows, C, hidden, d, 1) <= room + 2 * hidden * C * 4 * 9 + (1 << 24), (d, hidden)
+
+
+def test_tiles_of_the_recurrence(L):
+    """The sizes of tests/test_gpu_recurrence_tiles.py have several tiles a part, or parts for more than 64 groups."""
+    from tests.test_gpu_recurrence_tiles import SHAPES
+
+    for B, T, C in SHAPES:
+        for d in (0, 1):
+            tiles = L.lib.ecc_gated_recurrence_saved_bytes(B, T, C, d) // (B * C * 4)
+            parts = max((L.lib.ecc_gated_recurrence_workspace_bytes(B, T, C, d) - 256) // (B * C * 16), 1)
+            if B == 1:
+                assert parts > 64, (B, T, C, d, tiles, parts)
+            else:
+                assert tiles > parts and (parts > 1) == (T == 4000), (B, T, C, d, tiles, parts)

@@ -9,6 +9,8 @@ from tests.block_bounds import gated_linear
 from tests.gpu_util import banner, need_gpu
 from tests.norm_bounds import HALF, _vec, act_and_slope, rounded, worst
 from tests.norm_bounds import E as STEP
+from tests.test_gpu_glu import check_all
+from tests.test_gpu_glu import make as make_all
 
 pytestmark = pytest.mark.gpu
 F16, BF16 = torch.float16, torch.bfloat16
@@ -132,3 +134,12 @@ def test_infinite_gradient(rows, dtype):
         assert torch.isfinite(got[k][rest]).all()
     rest = [i for i in range(rows) if i != 7]
     assert torch.isfinite(got["x"][rest]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, F16, BF16], ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("act", ["none", "relu", "silu"])
+@pytest.mark.parametrize("bias", [True, False], ids=["bias", "plain"])
+def test_every_activation_in_large_tiles(bias, act, dtype):
+    banner("glu large", act, bias, dtype)
+    for C in (72, 70):   # whole chunks, and rows that are packed
+        check_all(*make_all((2050, C), 1610, dtype, bias, seed=7), act)
