@@ -23,12 +23,12 @@
 // read where elements have 16 bits.
 //
 // Large products are bound by the matrix unit at the clock that the power
-// leaves: 16384 x 1024 to 2816, bfloat16, forward 200 us (9.4e14 operations a
-// second), gradients of the projections 232 us, dx 194 us, dW 201 us and 15 for
-// its join.  1999 x 333 to 877, float32: 28 to 35 us each (6.7e13 to 8.3e13 of
-// 1.5e14: 448 to 504 workgroups, two to some compute units and one to others).
-// 2^19 x 64 to 160, float16: 80, 131, 103 and 113 us, bound by the bytes of the
-// results and of da and db, 2.9 to 4.4 TB/s.
+// leaves: 16384 x 1024 to 2816, bfloat16, forward 198 us (9.5e14 operations a
+// second), gradients of the projections 256 us, the two parts of dx 392 us, of dW
+// 429 us and 14 for its join.  1999 x 333 to 877, float32: 29 to 35 us each
+// (6.7e13 to 8.1e13 of 1.5e14: 448 to 504 workgroups, two to some compute units
+// and one to others).  2^19 x 64 to 160, float16: 80, 211, 219 and 203 us, bound by
+// the bytes of the results and of da and db's two parts, 2.9 to 4 TB/s.
 
 #pragma once
 

@@ -26,10 +26,10 @@
 // reads two streams once more, and a small one the states between them.
 //
 // Bound by memory and, in a tile, by the wait for the joined runs.  64 x 256 x
-// 1024 bfloat16: forward 30 us, 3.3 TB/s, backward 45 us, 3.7 TB/s.  12 x 8192 x
-// 201 float16: parts 26 us each way, forward 33, backward 62 (rows of 402 bytes
+// 1024 bfloat16: forward 27 us, 3.7 TB/s, backward 44 us, 3.8 TB/s.  12 x 8192 x
+// 201 float16: parts 26 us each way, forward 30, backward 62 (rows of 402 bytes
 // begin inside a line).  1 x 65536 x 96 float32: parts 14 us, states between
-// them 6, forward 18.  One step of 64 x 1024: 4.6 us, a launch.
+// them 6, forward 18.  One step of 64 x 1024: 4.4 us, a launch.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

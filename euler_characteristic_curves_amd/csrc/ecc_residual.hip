@@ -14,11 +14,13 @@
 // its one store: the forward pass moves four streams, the backward pass six,
 // which is the least there is.  y is formed again from x in the backward pass:
 // x and y would cost the same to read, and y is rounded.  Squares are summed in
-// float64, so that no row of finite values overflows or underflows; it costs a
-// few cycles of 64 lanes against some 50 of memory.  The remaining sums along a
-// row are float32 over 16 elements a lane and then a tree.  Sums over rows: 16
-// rows of a thread in float32, then those, then the workgroup's rows by halves,
-// then all workgroups in float64, always in the same order.
+// float64, so that no sum over finite values overflows or underflows; it costs a
+// few cycles of 64 lanes against some 50 of memory.  (r itself is float32: beyond
+// an rms of 2^126 it has fewer bits, below 2^-128 with eps = 0 it is infinite.)
+// The remaining sums along a row are float32 over 16 elements a lane and then a
+// tree.  Sums over rows: 16 rows of a thread in float32, then those, up to 16 of
+// them, then the workgroup's rows by halves, then all workgroups in float64, always
+// in the same order.
 //
 // Both passes are bound by memory (a copy of 1.07 GB: 5.1 TB/s).  16384 rows of
 // 1024 bfloat16 beside a float32 stream: forward 46 us, 4.4 TB/s; backward 74 us,

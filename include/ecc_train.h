@@ -175,7 +175,9 @@ size_t ecc_orth_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
  * stats: float32 [batch][inner][2], the factors 1 / sqrt(..) of both norms for
  * the backward pass, or NULL.  No output overlaps an input.  One launch, no
  * workspace.
- * Squares are summed in float64, everything else is float32, rounded once.
+ * Squares are summed in float64, everything else is float32, rounded once (so
+ * are the factors: beyond a root mean square of 2^126 they have fewer bits, below
+ * 2^-128 with eps = 0 they are infinite).
  */
 int ecc_residual_norm_fwd(const void* x, int xdtype, const void* branch, int dtype, int64_t batch, int64_t inner,
                           int64_t channels, const void* gate, int gate_per_sample, const void* weight,
